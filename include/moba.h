@@ -428,6 +428,105 @@ int moba_decode_fwd_ws(const void *q, const void *k_cache, const void *v_cache,
                        int32_t *idx, int B, int H, int S_max, int D, int block_size, int topk,
                        void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Rotary positions of q and k, applied before pooling, gate and attention (the
+ * pages leave positions outside the method; "When a MoBA reproduction will not
+ * run" section 3.3 asks where they enter).  The first rot_dim values of every
+ * head are rotated in pairs, the rest is copied.  With angle = positions[t] *
+ * freqs[i], held as exactly as 64 bits hold it at any position,
+ *   out[a] = magnitude * (x[a] cos - x[b] sin)
+ *   out[b] = magnitude * (x[b] cos + x[a] sin)
+ * for pair i: (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved.
+ * moba_rope_bwd is the gradient: the transposed rotation of the output's
+ * gradient (the same with -sin).
+ *   q, q_out  : [tokens][Hq][D] bf16 (device), a token's heads dense, tokens
+ *               *_stride elements apart (0: Hq * D); 16-byte aligned, strides
+ *               multiples of 8
+ *   k, k_out  : the same with Hk heads; NULL with Hk = 0
+ *   positions : [tokens] int32 (device), any sign
+ *   freqs     : [rot_dim / 2] double (device), radians per position, as
+ *               moba_rope_frequencies fills it or any other table
+ *   rot_dim   : a multiple of 16, at most D; D is 64 or 128
+ * An output may be its own input (same pointer and stride); any other overlap
+ * is MOBA_ERR_INVALID_ARG.  Values are rounded once, to bf16.
+ */
+int moba_rope(const void *q, const void *k, void *q_out, void *k_out, const int32_t *positions,
+              const double *freqs, int tokens, int Hq, int Hk, int D, int rot_dim, int interleaved,
+              float magnitude, long long q_stride, long long k_stride, long long q_out_stride,
+              long long k_out_stride, void *stream);
+int moba_rope_bwd(const void *dq_out, const void *dk_out, void *dq, void *dk,
+                  const int32_t *positions, const double *freqs, int tokens, int Hq, int Hk, int D,
+                  int rot_dim, int interleaved, float magnitude, long long dq_out_stride,
+                  long long dk_out_stride, long long dq_stride, long long dk_stride, void *stream);
+
+/*
+ * Fills freqs (HOST, rot_dim / 2 doubles): base^(-2i / rot_dim), scaled for
+ * contexts longer than the original one by
+ *   MOBA_ROPE_PLAIN   nothing;
+ *   MOBA_ROPE_LINEAR  1 / factor on every pair (positions interpolated);
+ *   MOBA_ROPE_BASE    a larger base, base * factor^(rot_dim / (rot_dim - 2)):
+ *                     the slowest pair ends up interpolated by factor;
+ *   MOBA_ROPE_BANDS   1 / factor on pairs that make at most slow_turns turns in
+ *                     original_length positions, nothing on those that make at
+ *                     least fast_turns, a linear ramp over the turns between.
+ */
+enum { MOBA_ROPE_PLAIN = 0, MOBA_ROPE_LINEAR = 1, MOBA_ROPE_BASE = 2, MOBA_ROPE_BANDS = 3 };
+int moba_rope_frequencies(double *freqs, int rot_dim, double base, int scaling, double factor,
+                          double original_length, double slow_turns, double fast_turns);
+
+/*
+ * Paged cache.  One layer's cache is three pools of pages of page_size tokens:
+ *   k_pages, v_pages : [num_pages][Hkv][page_size][D] bf16 (device); a page's
+ *                      tokens of one head are one dense run, since heads
+ *                      select blocks independently
+ *   kbar_pages       : [num_pages][Hkv][D] fp32 (device), the pooled key of a
+ *                      block in the slot of the block's LAST page: that page is
+ *                      written last, so sequences that share a block's earlier
+ *                      pages do not share the slot until the block is complete.
+ *                      NULL where no block is ever selected (caches of
+ *                      full-attention layers).
+ * Token p of sequence b lies in page page_table[b][p / page_size] (DEVICE
+ * int32 [num_seqs][max_pages]) at offset p % page_size.  page_size is a power
+ * of two from 16 up, block_size a multiple of 64 and of page_size.  Entries of
+ * the table behind a sequence's last token are not read.
+ * A call adds or attends cu_new[b + 1] - cu_new[b] new tokens of each sequence
+ * (cu_new: DEVICE int32 [num_seqs + 1], rows of the packed tensors; at most
+ * max_new each, 0 allowed), the last ones of its cache_lens[b] tokens
+ * (DEVICE int32, with the new ones).  Rows from cu_new[num_seqs] to total are
+ * padding: neither read nor written.
+ * Lengths and pages are checked on the device: a sequence whose offsets or
+ * length are inconsistent (new tokens below 0 or above max_new or the length,
+ * rows outside [0, total), more tokens than max_pages hold) or that needs a
+ * page outside [0, num_pages) records MOBA_ERR_INVALID_ARG in the device
+ * status word; nothing outside the given arrays is read or written, and the
+ * other sequences are computed.
+ *
+ * moba_paged_append writes the new tokens' k and v ([total][Hkv][D] bf16) to
+ * their pages and pools every block that they complete (options: pooling)
+ * from the keys as stored.  A pooled key depends on the block's keys alone,
+ * not on how the appends were cut.  Tokens of a refused sequence, and tokens on
+ * pages outside the pool, are not written.  Pages that are written must not be
+ * shared with another sequence of the call.
+ */
+int moba_paged_append(const void *k, const void *v, void *k_pages, void *v_pages,
+                      float *kbar_pages, const int32_t *page_table, const int32_t *cu_new,
+                      const int32_t *cache_lens, int num_seqs, int total, int max_new, int Hkv,
+                      int D, int num_pages, int page_size, int max_pages, int block_size,
+                      const moba_options_t *options, void *stream);
+
+/*
+ * Copies whole pages, page src[i] to page dst[i] (DEVICE int32 [n]), in every
+ * one of `layers` layers (pools [layers][num_pages]...): the last, partly
+ * filled page of a forked sequence, or a pool's live pages when it is
+ * compacted.  kbar_pages may be NULL.  A pair whose source or destination lies
+ * outside [0, num_pages), whose destination is another pair's destination too,
+ * or whose source is a pair's destination, copies nothing and records
+ * MOBA_ERR_INVALID_ARG in the device status word; the other pairs are copied.
+ */
+int moba_page_copy(void *k_pages, void *v_pages, float *kbar_pages, const int32_t *src,
+                   const int32_t *dst, int n, int layers, int num_pages, int Hkv, int D,
+                   int page_size, void *stream);
+
 /* Where the timeout reported by the calling thread's last moba_get_status
  * happened: out4 = {barrier shared-memory address, parity, block index, thread
  * index}. */

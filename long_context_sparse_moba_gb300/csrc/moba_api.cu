@@ -9,8 +9,6 @@
 #include "moba.h"
 #include "moba_internal.cuh"
 
-#define MOBA_EXPORT extern "C" __attribute__((visibility("default")))
-
 namespace moba {
 
 // [0] status word; [1..4] where the first timeout happened (barrier shared
@@ -325,6 +323,8 @@ static int cuda_status(cudaError_t e) {
     g_last_cuda_error = e;
     return MOBA_ERR_CUDA;
 }
+
+int cuda_result(cudaError_t e) { return cuda_status(e); }
 
 static bool misaligned(const void *p) { return reinterpret_cast<uintptr_t>(p) & 15; }
 

@@ -13,6 +13,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#define MOBA_EXPORT extern "C" __attribute__((visibility("default")))
+
 namespace moba {
 
 constexpr int kMaxPastSlots = 31;      // topk - 1 limit when gating is needed
@@ -155,6 +157,11 @@ cudaError_t launch_attn_current(const Plan &p, const Workspace &ws, const __nv_b
 
 // count of kernels this library has launched (for the benchmark's launch tally)
 void note_launches(int n);
+
+// MOBA_OK, or MOBA_ERR_CUDA with the error kept for moba_last_cuda_error
+int cuda_result(cudaError_t e);
+
+inline bool misaligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) & 15; }
 
 // streaming multiprocessors of the current device (cached per device)
 int sm_count();

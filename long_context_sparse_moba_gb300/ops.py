@@ -7,6 +7,7 @@ fails, a ``RuntimeError`` is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -25,6 +26,7 @@ MOBA_ERR_TIMEOUT = 5
 _lib = None
 
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_F, _DB, _LL = ctypes.c_float, ctypes.c_double, ctypes.c_longlong
 _SIGNATURES = {
     "moba_num_blocks": (_I, [_I, _I]),
     "moba_status_string": (ctypes.c_char_p, [_I]),
@@ -68,6 +70,13 @@ _SIGNATURES = {
                                      _P, _SZ, _P]),
     "moba_attn_bwd_ex": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P,
                               _P, _SZ, _P]),
+    "moba_rope": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _LL, _LL, _LL, _LL, _P]),
+    "moba_rope_bwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _LL, _LL, _LL, _LL,
+                           _P]),
+    "moba_rope_frequencies": (_I, [_P, _I, _DB, _I, _DB, _DB, _DB, _DB]),
+    "moba_paged_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                               _P, _P]),
+    "moba_page_copy": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "moba_attn_bwd_varlen_ex": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I,
                                      _I, _I, _I, _P, _P, _SZ, _P]),
 }
@@ -493,3 +502,200 @@ def debug_timeout_info():
     buf = (ctypes.c_int * 4)()
     lib().moba_debug_timeout_info(ctypes.cast(buf, ctypes.c_void_p))
     return tuple(buf)
+
+
+# ---------------------------------------------------------------------------
+# rotary positions and the paged cache
+# ---------------------------------------------------------------------------
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_BASE = 2
+ROPE_BANDS = 3
+
+_NULL = contextlib.nullcontext()
+
+
+@contextlib.contextmanager
+def _switched(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _on(device, stream):
+    """A context in which the tensors' device is current and ``stream`` (if one
+    is given) too, so that results and scratch are allocated where they are used."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _NULL
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream must be on {device}")
+    return _switched(device, stream)
+
+
+def _same_device(like, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{n} must be on {like.device}")
+
+
+def _heads(t, name):
+    """(tokens, H, D, elements between tokens) of t [..., H, D] bf16: a token's
+    heads dense, all tokens one stride apart."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() < 2:
+        raise ValueError(f"{name} must be a CUDA torch.bfloat16 tensor [..., H, D]")
+    H, D = t.shape[-2:]
+    if t.is_contiguous():
+        return t.numel() // max(1, H * D), H, D, H * D
+    stride, size, tokens = None, 1, 1
+    if (D > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
+        raise ValueError(f"{name}: a token's heads must be dense")
+    for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        tokens *= n
+        if n == 1:
+            continue
+        if stride is None:
+            stride = s
+        elif s != stride * size:
+            raise ValueError(f"{name}: tokens must be one stride apart")
+        size *= n
+    if stride is not None and stride < H * D:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return tokens, H, D, stride if stride is not None else H * D
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling=ROPE_PLAIN, factor: float = 1.0,
+                     original_length: float = 0.0, slow_turns: float = 1.0,
+                     fast_turns: float = 4.0, device="cuda"):
+    """Radians per position of each pair of ``rot_dim`` rotated values: float64
+    [rot_dim / 2] on ``device``; the scalings are those of moba_rope_frequencies
+    (``ROPE_PLAIN``, ``ROPE_LINEAR``, ``ROPE_BASE``, ``ROPE_BANDS``)."""
+    f = torch.empty(max(0, int(rot_dim)) // 2, dtype=torch.float64)
+    _check(lib().moba_rope_frequencies(_ptr(f) if f.numel() else None, int(rot_dim), base, scaling,
+                                       factor, original_length, slow_turns, fast_turns),
+           "moba_rope_frequencies")
+    return f.to(device)
+
+
+def _rope(fn, what, q, k, positions, freqs, interleaved, magnitude, q_out, k_out, stream):
+    T, Hq, D, qs = _heads(q, "q")
+    Hk, ks, kos = 0, 0, 0
+    _need(positions, torch.int32, "positions")
+    _need(freqs, torch.float64, "freqs")
+    if positions.numel() != T:
+        raise ValueError(f"positions must hold one position for each of the {T} tokens")
+    if k is not None:
+        Tk, Hk, Dk, ks = _heads(k, "k")
+        if Tk != T or Dk != D:
+            raise ValueError("k must have the tokens and the head dimension of q")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _same_device(q, k=k, positions=positions, freqs=freqs, q_out=q_out, k_out=k_out)
+    with _on(q.device, stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        elif k is not None and k_out.shape != k.shape:
+            raise ValueError("k_out must have the shape of k")
+        qos = _heads(q_out, "q_out")[3]
+        if k is not None:
+            kos = _heads(k_out, "k_out")[3]
+        rc = fn(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(positions), _ptr(freqs), T, Hq,
+                Hk, D, 2 * freqs.numel(), int(bool(interleaved)), magnitude, qs, ks, qos, kos,
+                _stream(stream))
+    _check(rc, what)
+    return q_out, k_out
+
+
+def rope(q, k, positions, freqs, interleaved: bool = False, magnitude: float = 1.0, q_out=None,
+         k_out=None, stream=None):
+    """Rotary positions: q [..., Hq, D] and k [..., Hk, D] bf16 (k may be None)
+    with the first ``2 * len(freqs)`` values of each head rotated by
+    ``positions[t] * freqs`` -> (q_out, k_out).  positions int32, one per token;
+    freqs float64 (:func:`rope_frequencies`).  Pairs are (i, i + half), or
+    (2i, 2i + 1) when ``interleaved``.  The tokens of an operand may be a stride
+    apart (slices of one projection); q_out / k_out may be q / k (in place)."""
+    return _rope(lib().moba_rope, "moba_rope", q, k, positions, freqs, interleaved, magnitude,
+                 q_out, k_out, stream)
+
+
+def rope_bwd(dq_out, dk_out, positions, freqs, interleaved: bool = False, magnitude: float = 1.0,
+             dq=None, dk=None, stream=None):
+    """The gradient of :func:`rope`: gradients of its outputs -> (dq, dk)."""
+    return _rope(lib().moba_rope_bwd, "moba_rope_bwd", dq_out, dk_out, positions, freqs,
+                 interleaved, magnitude, dq, dk, stream)
+
+
+def _paged(k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens):
+    """Checks one layer's pools and the sequences' tables; the sizes a call passes on."""
+    _need(k_pages, torch.bfloat16, "k_pages")
+    _need(v_pages, torch.bfloat16, "v_pages")
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, D]")
+    P, Hkv, ps, D = k_pages.shape
+    if kbar_pages is not None:
+        _need(kbar_pages, torch.float32, "kbar_pages")
+        if kbar_pages.shape != (P, Hkv, D):
+            raise ValueError("kbar_pages must be [num_pages, Hkv, D]")
+    _need(page_table, torch.int32, "page_table")
+    _need(cu_new, torch.int32, "cu_new")
+    _need(cache_lens, torch.int32, "cache_lens")
+    n = cache_lens.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != n or cu_new.numel() != n + 1:
+        raise ValueError("page_table must be [num_seqs, max_pages], cu_new [num_seqs + 1] and "
+                         "cache_lens [num_seqs]")
+    _same_device(k_pages, v_pages=v_pages, kbar_pages=kbar_pages, page_table=page_table,
+                 cu_new=cu_new, cache_lens=cache_lens)
+    return P, Hkv, ps, D, n, page_table.shape[1]
+
+
+def paged_append(k, v, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens, max_new: int,
+                 block_size: int, pooling=POOL_MEAN, stream=None):
+    """Writes the new tokens' k, v [total, Hkv, D] bf16 to the pages of their
+    sequences (the last ``cu_new[b + 1] - cu_new[b]`` of ``cache_lens[b]`` tokens) and
+    the pooled keys of the blocks that they complete to ``kbar_pages`` (None: the
+    cache keeps none)."""
+    P, Hkv, ps, D, n, mp = _paged(k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens)
+    _need(k, torch.bfloat16, "k")
+    _need(v, torch.bfloat16, "v")
+    if k.dim() != 3 or k.shape[1:] != (Hkv, D) or v.shape != k.shape:
+        raise ValueError("k and v must be [total, Hkv, D] of the pages")
+    _same_device(k_pages, k=k, v=v)
+    o, _keep = _options(pooling=pooling)
+    with _on(k.device, stream):
+        rc = lib().moba_paged_append(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages),
+                                     _ptr(kbar_pages), _ptr(page_table), _ptr(cu_new),
+                                     _ptr(cache_lens), n, k.shape[0], max_new, Hkv, D, P, ps, mp,
+                                     block_size, ctypes.byref(o), _stream(stream))
+    _check(rc, "moba_paged_append")
+
+
+def page_copy(k_pages, v_pages, kbar_pages, src, dst, stream=None):
+    """Copies pages ``src[i]`` to ``dst[i]`` (int32) of the pools [num_pages, Hkv,
+    page_size, D] (kbar_pages [num_pages, Hkv, D] or None), or of every layer of
+    pools with a leading layer dimension."""
+    _need(k_pages, torch.bfloat16, "k_pages")
+    _need(v_pages, torch.bfloat16, "v_pages")
+    if k_pages.dim() not in (4, 5) or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [(layers,) num_pages, Hkv, page_size, D]")
+    P, Hkv, ps, D = k_pages.shape[-4:]
+    if kbar_pages is not None:
+        _need(kbar_pages, torch.float32, "kbar_pages")
+        if kbar_pages.shape != (*k_pages.shape[:-2], D):
+            raise ValueError("kbar_pages must be [(layers,) num_pages, Hkv, D]")
+    _need(src, torch.int32, "src")
+    _need(dst, torch.int32, "dst")
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must have the same length")
+    _same_device(k_pages, v_pages=v_pages, kbar_pages=kbar_pages, src=src, dst=dst)
+    with _on(k_pages.device, stream):
+        rc = lib().moba_page_copy(_ptr(k_pages), _ptr(v_pages), _ptr(kbar_pages), _ptr(src),
+                                  _ptr(dst), src.numel(),
+                                  k_pages.shape[0] if k_pages.dim() == 5 else 1, P, Hkv, D, ps,
+                                  _stream(stream))
+    _check(rc, "moba_page_copy")
