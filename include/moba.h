@@ -515,6 +515,40 @@ int moba_paged_append(const void *k, const void *v, void *k_pages, void *v_pages
                       const moba_options_t *options, void *stream);
 
 /*
+ * Attention of the new tokens over the paged cache (their own k, v appended
+ * before): for a token at position p of its sequence and a query head h, the
+ * selection rule of the forward (the own block p / block_size, up to p, and
+ * the top (topk - 1) complete past blocks by <q, kbar>), softmax attention over
+ * those keys with the kv head h / (Hq / Hkv).  The new token of a decode step is
+ * a chunk of one.  topk of at least the blocks of max_pages pages gives full
+ * causal attention and reads no kbar.
+ * The selection orders the scores as 64-bit arithmetic on the given q and kbar
+ * does (fp32 scores decide where they are far enough apart, a 64-bit re-score
+ * elsewhere); ties go to the lower block, a NaN score counts as -inf.
+ *   q, out : [total][Hq][D] bf16 (device);  lse : [total][Hq] fp32, natural log
+ *   idx    : [total][Hq][topk] int32 or NULL: the selection, ascending, the own
+ *            block last, -1 padded
+ *   Hq a multiple of Hkv, at most 64 query heads to a kv head; topk - 1 at most
+ *   31 unless topk covers every block
+ * Rows of a refused sequence (that lie in [0, total)) get zero outputs, -inf
+ * lse and -1 idx; a row that meets a page outside the pool gets zero outputs
+ * and -inf lse.
+ * workspace: device scratch, 256-byte aligned, at least
+ * moba_paged_attn_workspace_size bytes, used by nothing else until the call's
+ * work has finished; NULL: stream-ordered scratch of the call's own.  It needs
+ * no initialisation.
+ */
+int moba_paged_attn(const void *q, const void *k_pages, const void *v_pages,
+                    const float *kbar_pages, const int32_t *page_table, const int32_t *cu_new,
+                    const int32_t *cache_lens, void *out, float *lse, int32_t *idx, int num_seqs,
+                    int total, int max_new, int Hq, int Hkv, int D, int num_pages, int page_size,
+                    int max_pages, int block_size, int topk, void *workspace,
+                    size_t workspace_bytes, void *stream);
+size_t moba_paged_attn_workspace_size(int num_seqs, int total, int max_new, int Hq, int Hkv,
+                                      int D, int page_size, int max_pages, int block_size,
+                                      int topk);
+
+/*
  * Copies whole pages, page src[i] to page dst[i] (DEVICE int32 [n]), in every
  * one of `layers` layers (pools [layers][num_pages]...): the last, partly
  * filled page of a forked sequence, or a pool's live pages when it is

@@ -1,0 +1,76 @@
+// moba_paged_attn.cuh -- what the kernels of the attention over a paged cache
+// share: the call's arguments, its entries (a tile of a sequence's query rows on
+// one kv head) and the scratch.
+#pragma once
+
+#include "moba_paged.cuh"
+
+namespace moba {
+namespace paged {
+
+constexpr int kTile = 64;        // keys per tile
+constexpr int kMaxRows = 64;     // query rows of an entry at most
+constexpr int kMaxBlocks = 65536;  // blocks of a sequence where blocks are selected
+
+struct Attn {
+    Cache c;
+    const __nv_bfloat16 *q, *k, *v;
+    const float *kbar;
+    __nv_bfloat16 *out;
+    float *lse;
+    int32_t *idx;  // or nullptr
+    int Hq, G, D, topk, km1;
+    bool dense;     // topk covers every block
+    int rows;       // rows of an entry at most: 16, 32 or 64
+    int tt, tps;    // tokens of an entry at most (rows / G), entries of a sequence and kv head
+    int n_ent;      // (sequence * tps + tile) * Hkv + kv head
+    int tpb;        // key tiles per block
+    int ctas;       // of the attention kernel
+    int ucap;       // union blocks of an entry at most
+    float scale_log2;
+    int *status;
+    // scratch
+    int *tiles;                 // [n_ent] key tiles of an entry (selection only)
+    int *ublk;                  // [n_ent][ucap] blocks that some row of the entry selected, ascending
+    unsigned long long *umask;  // [n_ent][ucap] which rows did
+    int *c_first, *c_last;      // [n_ent] first and last CTA that worked on the entry
+    float *part_o;              // [ctas][2][rows][D] partial sums of exp2(s - m) v
+    float2 *part_ml;            // [ctas][2][rows] their m and sum of exp2(s - m); a sum below 0: bad page
+};
+
+struct Entry {
+    int b, hk;
+    int t0, nt;    // tokens [t0, t0 + nt) of the sequence's new ones
+    int row0;      // packed row of token t0
+    int pos0;      // position of token t0
+    int state;     // kSeqOk (then nt > 0), kSeqBad (rows to clear, if any), or kSeqEmpty
+};
+
+__device__ __forceinline__ Entry get_entry(const Attn &a, int e) {
+    Entry x;
+    x.hk = e % a.c.Hkv;
+    const int t = e / a.c.Hkv;
+    x.b = t / a.tps;
+    x.t0 = (t - x.b * a.tps) * a.tt;
+    Seq s;
+    x.state = a.c.seq(x.b, s);
+    x.nt = max(0, min(a.tt, s.n - x.t0));
+    x.row0 = s.row0 + x.t0;
+    x.pos0 = s.len - s.n + x.t0;
+    // a refused sequence is recorded by its first entry, with rows or without
+    if (x.nt == 0 && !(x.state == kSeqBad && x.t0 == 0)) x.state = kSeqEmpty;
+    return x;
+}
+
+// key tiles that an entry visits
+__device__ __forceinline__ int get_tiles(const Attn &a, int e) {
+    if (!a.dense) return a.tiles[e];
+    const Entry x = get_entry(a, e);
+    return x.state == kSeqOk ? (x.pos0 + x.nt - 1) / kTile + 1 : 0;
+}
+
+cudaError_t launch_gate(const Attn &a, cudaStream_t st);
+cudaError_t launch_rows(const Attn &a, cudaStream_t st);
+
+}  // namespace paged
+}  // namespace moba

@@ -76,6 +76,9 @@ _SIGNATURES = {
     "moba_rope_frequencies": (_I, [_P, _I, _DB, _I, _DB, _DB, _DB, _DB]),
     "moba_paged_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                _P, _P]),
+    "moba_paged_attn": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
+                             _I, _I, _I, _P, _SZ, _P]),
+    "moba_paged_attn_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I]),
     "moba_page_copy": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "moba_attn_bwd_varlen_ex": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I,
                                      _I, _I, _I, _P, _P, _SZ, _P]),
@@ -673,6 +676,48 @@ def paged_append(k, v, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_l
                                      _ptr(cache_lens), n, k.shape[0], max_new, Hkv, D, P, ps, mp,
                                      block_size, ctypes.byref(o), _stream(stream))
     _check(rc, "moba_paged_append")
+
+
+def paged_attn_workspace_size(num_seqs, total, max_new, Hq, Hkv, D, page_size, max_pages,
+                              block_size, topk) -> int:
+    """Bytes of device scratch :func:`paged_attn` needs (0: sizes it refuses)."""
+    return int(lib().moba_paged_attn_workspace_size(num_seqs, total, max_new, Hq, Hkv, D, page_size,
+                                                    max_pages, block_size, topk))
+
+
+def paged_attn(q, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens, max_new: int,
+               block_size: int, topk: int, out=None, lse=None, idx=None, with_idx: bool = False,
+               workspace=None, stream=None):
+    """Attention of the new tokens q [total, Hq, D] bf16 (already appended, see
+    :func:`paged_append`) over the paged cache -> (out [total, Hq, D] bf16, lse
+    [total, Hq] fp32, idx [total, Hq, topk] int32 or None): MoBA over the own
+    block and the best topk - 1 past blocks of each query head, or full causal
+    attention when topk covers the blocks of every page table row.  ``workspace`` is a uint8
+    CUDA tensor of at least :func:`paged_attn_workspace_size` bytes, or None."""
+    P, Hkv, ps, D, n, mp = _paged(k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens)
+    _need(q, torch.bfloat16, "q")
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError("q must be [total, Hq, D] with the pages' head dimension")
+    total, Hq = q.shape[:2]
+    workspace = _ws(workspace)
+    _same_device(k_pages, q=q, workspace=workspace)
+    with _on(q.device, stream):
+        out = _out(out, q.shape, torch.bfloat16, q, "out")
+        lse = _out(lse, (total, Hq), torch.float32, q, "lse")
+        if with_idx or idx is not None:
+            idx = _out(idx, (total, Hq, topk), torch.int32, q, "idx")
+        if workspace is None:
+            workspace = torch.empty(
+                lib().moba_paged_attn_workspace_size(n, total, max_new, Hq, Hkv, D, ps, mp,
+                                                     block_size, topk),
+                dtype=torch.uint8, device=q.device)
+        rc = lib().moba_paged_attn(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kbar_pages),
+                                   _ptr(page_table), _ptr(cu_new), _ptr(cache_lens), _ptr(out),
+                                   _ptr(lse), _ptr(idx), n, total, max_new, Hq, Hkv, D, P, ps, mp,
+                                   block_size, topk, _ptr(workspace), workspace.numel(),
+                                   _stream(stream))
+    _check(rc, "moba_paged_attn")
+    return out, lse, idx
 
 
 def page_copy(k_pages, v_pages, kbar_pages, src, dst, stream=None):
