@@ -1001,6 +1001,20 @@ bool make_tma_3d(CUtensorMap *m, const void *ptr, int total, int H, int D, int r
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [rows][D] bf16 viewed as a 2-D tensor; box = 64 dims x `box` rows, 128-byte swizzle.
+bool make_tma_rows(CUtensorMap *m, const void *ptr, long long rows, int D, int box) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+    cuuint32_t boxes[2] = {64, (cuuint32_t)box};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, boxes,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int tc_tile_rows() { return tc::kRows; }
 
 static tc::Args make_tc_args(const Plan &p, const Workspace &ws, const __nv_bfloat16 *q,

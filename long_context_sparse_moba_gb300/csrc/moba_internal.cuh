@@ -184,6 +184,8 @@ cudaError_t launch_attn_current_mma(const Plan &p, const Workspace &ws, const __
 int tc_tile_rows();
 // [total][H][D] bf16 as a 3-D TMA tensor (D, H, total), box 64 x 1 x rows, 128B swizzle
 bool make_tma_3d(CUtensorMap *m, const void *ptr, int total, int H, int D, int rows);
+// [rows][D] bf16 as a 2-D TMA tensor, box 64 x `box` rows, 128B swizzle
+bool make_tma_rows(CUtensorMap *m, const void *ptr, long long rows, int D, int box);
 // kbar (fp32) -> hi = bf16(kbar), lo = bf16(kbar - hi)
 cudaError_t launch_kbar_split(const Plan &p, const float *kbar, __nv_bfloat16 *hi,
                               __nv_bfloat16 *lo, float *norm, cudaStream_t st);

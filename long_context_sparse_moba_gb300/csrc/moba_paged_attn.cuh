@@ -3,6 +3,8 @@
 // one kv head) and the scratch.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "moba_paged.cuh"
 
 namespace moba {
@@ -10,6 +12,7 @@ namespace paged {
 
 constexpr int kTile = 64;        // keys per tile
 constexpr int kMaxRows = 64;     // query rows of an entry at most
+constexpr int kJobRows = 256;    // query rows of a job of the tcgen05 kernel
 constexpr int kMaxBlocks = 65536;  // blocks of a sequence where blocks are selected
 
 struct Attn {
@@ -30,12 +33,30 @@ struct Attn {
     float scale_log2;
     int *status;
     // scratch
-    int *tiles;                 // [n_ent] key tiles of an entry (selection only)
+    // (selection only) key tiles of an entry; with lists, its union blocks + 1,
+    // or 0: the entry met a page outside the pool
+    int *tiles;                 // [n_ent]
     int *ublk;                  // [n_ent][ucap] blocks that some row of the entry selected, ascending
     unsigned long long *umask;  // [n_ent][ucap] which rows did
     int *c_first, *c_last;      // [n_ent] first and last CTA that worked on the entry
     float *part_o;              // [ctas][2][rows][D] partial sums of exp2(s - m) v
     float2 *part_ml;            // [ctas][2][rows] their m and sum of exp2(s - m); a sum below 0: bad page
+    // ---- chunks of many rows (the tcgen05 kernel): jobs of up to 256 rows ----
+    bool chunk;
+    int n_max;                  // blocks of a sequence at most
+    int w_cap;                  // 256-row tiles of all sequences on one kv head, at most
+    long long job_cap, list_cap;
+    int *own_off;               // [num_seqs + 1] 256-row tiles before each sequence
+    long long *unit_off;        // [w_cap + 1] key tiles before each row tile (all blocks)
+    int *counts;                // [num_seqs][n_max][Hkv] rows that selected the block
+    int *list_off;              // [num_seqs * n_max * Hkv + 1]
+    int2 *jobs;                 // [job_cap] list, first entry
+    int *n_jobs;                // [1]
+    int *list;                  // rows of each list: (token * G + head) << 5 | slot
+    int *ubase;                 // [n_ent][ucap] where the entry's rows start in the block's list
+    __half *part_h;             // [Hkv][total * G][km1 + 1][D] normalised partial outputs
+    float4 *part_s;             // [Hkv][total * G][km1 + 1] log2-sum-exp, scale of each 64 columns,
+                                // and 1 (0: a page outside the pool)
 };
 
 struct Entry {
@@ -71,6 +92,9 @@ __device__ __forceinline__ int get_tiles(const Attn &a, int e) {
 
 cudaError_t launch_gate(const Attn &a, cudaStream_t st);
 cudaError_t launch_rows(const Attn &a, cudaStream_t st);
+// chunks of many rows: row tiles, lists and jobs; then the attention and the merge
+cudaError_t launch_plan(const Attn &a, cudaStream_t st);
+cudaError_t launch_chunk(const Attn &a, cudaStream_t st);
 
 }  // namespace paged
 }  // namespace moba

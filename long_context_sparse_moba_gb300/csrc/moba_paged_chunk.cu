@@ -1,0 +1,1027 @@
+// moba_paged_chunk.cu -- attention of chunks of many query rows over a paged
+// cache on the sm_103a tensor cores (tcgen05.mma, accumulators in tensor memory,
+// K/V pages staged by TMA).
+//
+// Pages: "When a MoBA reproduction will not run" (mhpq.cn/news/582794) section
+// 3.3 (the selected blocks of all queries batched before the attention) and
+// "MOBA mixture of block attention for server-side long context"
+// (hncyxsy.com/news/197418) section 3 (own block forced, causal inside it).
+//
+// A row is a (new token, query head of a kv head's group); the rows of one kv
+// head are numbered token * G + head, so that a job's 256 rows share its keys
+// whatever the group size.  Jobs:
+//   with selection: (1) up to 256 rows that selected one past block of one kv
+//     head, from its list; (2) up to 256 consecutive rows with the keys of
+//     their own blocks.  Each writes, for a row and slot, a normalised partial
+//     output and its log2-sum-exp; the merge kernel joins a row's slots.
+//     Partials are fp16 with a power-of-two scale per row and 64 columns: half
+//     the bytes of fp32, and 2^-11 of a value is a fraction of the rounding of
+//     the result (bf16 partials would double its error);
+//   all blocks: 256 consecutive rows with every key up to them.  The key tiles
+//     of all jobs form one sequence that is cut into equal runs, one per CTA; a
+//     job that falls into several runs leaves fp32 partial sums.
+//
+// Persistent, one CTA per SM, 12 warps:
+//   warp 0   K pages by TMA (one lane), warp 10 V pages, into rings of tiles;
+//   warp 1   allocates TMEM; one lane issues, for the two 128-row tiles g of a
+//            job, PV_0(j-1), S_0(j), PV_1(j-1), S_1(j): one tile's MMAs run
+//            while the other tile's softmax works;
+//   warps 2..9  softmax: thread r owns row r of its tile.  The offset mu is
+//            raised, to a whole number, only when the maximum exceeds it by more
+//            than 8, so that a rescale is by an exact power of two and rare.
+//            They gather the next job's query rows as soon as the MMAs have
+//            released Q, and write the results;
+//   warp 11  one lane hands job descriptors to the others, three ahead.
+// Keys that no row of a job sees (behind its last row, possibly never written)
+// are zeroed in the V tile before its product; in K their scores are masked.
+// Every mbarrier wait is bounded: one that runs out sets MOBA_ERR_TIMEOUT in the
+// status word and an abort flag that makes every role leave; copies and MMAs
+// in flight are awaited before the CTA frees its tensor memory.
+#include <atomic>
+
+#include "moba_paged_attn.cuh"
+#include "moba_ptx.cuh"
+
+namespace moba {
+namespace paged {
+namespace {
+
+using namespace ptx;
+
+constexpr int kM = 128;          // rows per Q tile
+constexpr int kG = 2;            // Q tiles per job
+constexpr int kThreads = 384;
+constexpr int kTmemCols = 512;
+constexpr int kJobs = 3;         // descriptors in flight
+constexpr int kBadSlots = 8;
+
+struct Job {
+    int valid;
+    int own;         // consecutive rows (else a list)
+    int b, hk;
+    int nrows;
+    int rbase;       // first row, or first entry of the list
+    int key0;        // position of key tile 0
+    int key_end;     // keys from here on are seen by no row
+    int lo, nt;      // first key tile of this job's part, and how many
+    int te[kG];      // tiles of the part that Q tile g visits
+    int pdelta;      // own: position of a row = its token + pdelta
+    int whole;       // all blocks: the part is the whole job
+    int slot;        // all blocks: partial slot
+    int pad;
+};
+
+struct ChunkArgs {
+    Attn a;
+    int psh;         // log2(page size)
+    long long wait_limit;
+};
+
+template <int D, int N>
+struct Smem {
+    static constexpr int NB = D / 64;                    // 64-dim boxes per row
+    static constexpr int kStages = N == 128 ? 2 : 4;
+    static constexpr uint32_t kQBox = kM * 128;
+    static constexpr uint32_t kKVBox = N * 128;
+    static constexpr uint32_t kTileBytes = NB * kKVBox;
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kK = kQ + kG * NB * kQBox;
+    static constexpr uint32_t kV = kK + kStages * kTileBytes;
+    static constexpr uint32_t kStage = kV + kStages * kTileBytes;  // 4 KB per softmax warp
+    static constexpr uint32_t kEnd = kStage + 4 * kG * 4096;
+    static constexpr int kBarQ = 0, kBarQE = kBarQ + kG, kBarKF = kBarQE + kG,
+                         kBarKE = kBarKF + kStages, kBarVF = kBarKE + kStages,
+                         kBarVE = kBarVF + kStages, kBarS = kBarVE + kStages, kBarP = kBarS + kG,
+                         kBarPV = kBarP + kG, kBarDrain = kBarPV + kG,
+                         kBarJF = kBarDrain + 1, kBarJE = kBarJF + kJobs, kNumBars = kBarJE + kJobs;
+    static constexpr uint32_t kSlot = kNumBars * 8;      // TMEM address, abort flag
+    static constexpr uint32_t kBad = kSlot + 8;
+    static constexpr uint32_t kJob = (kBad + 4 * kBadSlots + 15) & ~15u;
+    static constexpr uint32_t kMisc = kJob + kJobs * sizeof(Job);
+    static constexpr uint32_t kNeed = kEnd + 1008 + kMisc;
+    static_assert(kNeed <= 227 * 1024, "shared memory per CTA");
+    static constexpr uint32_t kRequest = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
+};
+
+// The part [lo, lo + nt) of the key tiles of 256-row tile x of sequence b on kv head hk.
+template <int N>
+__device__ __forceinline__ void own_job(const Attn &a, const Seq &s, int b, int hk, int x, Job &J) {
+    const int r0 = x * kJobRows;
+    J.valid = 1;
+    J.own = 1;
+    J.b = b;
+    J.hk = hk;
+    J.nrows = min(kJobRows, s.n * a.G - r0);
+    J.rbase = s.row0 * a.G + r0;
+    J.pdelta = s.len - s.n - s.row0;
+    const int pf = s.len - s.n + r0 / a.G, pl = s.len - s.n + (r0 + J.nrows - 1) / a.G;
+    J.key0 = a.dense ? 0 : pf / a.c.bs * a.c.bs;
+    J.key_end = pl + 1;
+    J.lo = 0;
+    J.nt = (pl - J.key0) / N + 1;
+    J.whole = 1;
+    J.slot = 0;
+    J.pad = 0;
+}
+
+// Q tile g's share of the part's tiles: those up to its last row.
+template <int N>
+__device__ __forceinline__ void job_ends(const Attn &a, Job &J) {
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+        if (J.nrows <= g * kM) {
+            J.te[g] = 0;
+        } else if (!J.own) {
+            J.te[g] = J.nt;
+        } else {
+            const int last = (J.rbase + min(J.nrows, (g + 1) * kM) - 1) / a.G + J.pdelta;
+            J.te[g] = min(max((last - J.key0) / N + 1 - J.lo, 0), J.nt);
+        }
+    }
+}
+
+template <int D, int N, bool DENSE>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                 const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ ChunkArgs ca) {
+    using L = Smem<D, N>;
+    constexpr int ST = L::kStages;
+    const Attn &a = ca.a;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = saddr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t misc = base - raw >= L::kMisc ? raw : base + L::kEnd;
+    uint8_t *gmisc = smem_raw + (misc - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sQ = base + L::kQ, sK = base + L::kK, sV = base + L::kV;
+    auto bar = [&](int i) -> uint32_t { return misc + 8u * (uint32_t)i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gmisc + L::kSlot);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gmisc + L::kSlot + 4);
+    volatile int *bad_job = reinterpret_cast<volatile int *>(gmisc + L::kBad);
+    Job *ring = reinterpret_cast<Job *>(gmisc + L::kJob);
+    Ctl ctl{abort_flag, a.status, ca.wait_limit};
+
+    if (tid == 0) {
+        for (int g = 0; g < kG; ++g) {
+            mbar_init(bar(L::kBarQ + g), kM);  // an asynchronous arrival per gathering thread
+            mbar_init(bar(L::kBarQE + g), 1);
+            mbar_init(bar(L::kBarS + g), 1);
+            mbar_init(bar(L::kBarP + g), 4);
+            mbar_init(bar(L::kBarPV + g), 1);
+        }
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(bar(L::kBarKF + s), 1);
+            mbar_init(bar(L::kBarKE + s), 1);
+            mbar_init(bar(L::kBarVF + s), 1);
+            mbar_init(bar(L::kBarVE + s), 1);
+        }
+        for (int s = 0; s < kJobs; ++s) {
+            mbar_init(bar(L::kBarJF + s), 1);
+            mbar_init(bar(L::kBarJE + s), 4 * kG + 3);  // softmax warps, producers, MMA lane
+        }
+        mbar_init(bar(L::kBarDrain), 1);
+        for (int i = 0; i < kBadSlots; ++i) bad_job[i] = 0;
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         saddr(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 11) {
+        // ================= job descriptors =================
+        if (lane == 0) {
+            int n = 0;
+            auto hand = [&](const Job &J) -> bool {
+                const int s = n % kJobs;
+                if (n >= kJobs && !wait_bar(bar(L::kBarJE + s), (n / kJobs - 1) & 1, ctl)) return false;
+                ring[s] = J;
+                mbar_arrive(bar(L::kBarJF + s));
+                ++n;
+                return true;
+            };
+            bool go = true;
+            Job J;
+            Seq sq;
+            const int tiles = __ldg(a.own_off + a.c.num_seqs);
+            if (DENSE) {
+                const long long total = a.unit_off[tiles];
+                const long long runs = total < (long long)gridDim.x ? total : (long long)gridDim.x;
+                if ((long long)blockIdx.x < runs) {
+                    long long u = total * blockIdx.x / runs;
+                    const long long u1 = total * (blockIdx.x + 1) / runs;
+                    int w = 0, hi = tiles - 1;  // largest row tile that starts at or before u
+                    while (w < hi) {
+                        const int mid = (w + hi + 1) >> 1;
+                        if (a.unit_off[mid] <= u) w = mid; else hi = mid - 1;
+                    }
+                    while (go && u < u1) {
+                        const int b = upper_index(a.own_off, a.c.num_seqs, w);
+                        a.c.seq(b, sq);
+                        own_job<N>(a, sq, b, 0, w - __ldg(a.own_off + b), J);
+                        const int T = J.nt;
+                        for (; go && u < u1 && u < a.unit_off[w + 1];) {
+                            const long long in = u - a.unit_off[w];
+                            J.hk = (int)(in / T);
+                            J.lo = (int)(in - (long long)J.hk * T);
+                            J.nt = (int)min((long long)(T - J.lo), u1 - u);
+                            J.whole = J.nt == T;
+                            J.slot = blockIdx.x * 2 + (J.lo == 0 ? 1 : 0);
+                            job_ends<N>(a, J);
+                            const size_t e = (size_t)w * a.c.Hkv + J.hk;
+                            if (J.lo == 0) a.c_first[e] = blockIdx.x;
+                            if (J.lo + J.nt == T) a.c_last[e] = blockIdx.x;
+                            go = hand(J);
+                            u += J.nt;
+                        }
+                        ++w;
+                    }
+                }
+            } else {
+                const int listed = a.km1 > 0 ? *a.n_jobs : 0;
+                const long long all = listed + (long long)tiles * a.c.Hkv;
+                for (long long q = blockIdx.x; go && q < all; q += gridDim.x) {
+                    if (q < listed) {
+                        const int2 d = a.jobs[q];
+                        const int lb = a.list_off[d.x];
+                        J.valid = 1;
+                        J.own = 0;
+                        J.hk = d.x % a.c.Hkv;
+                        J.b = d.x / a.c.Hkv / a.n_max;
+                        J.nrows = min(kJobRows, a.list_off[d.x + 1] - lb - d.y);
+                        J.rbase = lb + d.y;
+                        J.key0 = (d.x / a.c.Hkv % a.n_max) * a.c.bs;
+                        J.key_end = J.key0 + a.c.bs;
+                        J.lo = 0;
+                        J.nt = a.c.bs / N;
+                        J.pdelta = 0;
+                        J.whole = 1;
+                        J.slot = 0;
+                        J.pad = 0;
+                    } else {
+                        const int w = (int)((q - listed) / a.c.Hkv);
+                        const int b = upper_index(a.own_off, a.c.num_seqs, w);
+                        a.c.seq(b, sq);
+                        own_job<N>(a, sq, b, (int)((q - listed) % a.c.Hkv), w - __ldg(a.own_off + b), J);
+                    }
+                    job_ends<N>(a, J);
+                    go = hand(J);
+                }
+            }
+            J.valid = 0;
+            if (go) hand(J);
+        }
+        __syncwarp();
+    } else if (warp == 0 || warp == 10) {
+        // ================= K pages (warp 0), V pages (warp 10) =================
+        if (lane == 0) {
+            const bool is_k = warp == 0;
+            const int bfull = is_k ? L::kBarKF : L::kBarVF, bempty = is_k ? L::kBarKE : L::kBarVE;
+            const uint32_t tiles = is_k ? sK : sV;
+            const CUtensorMap *map = is_k ? &tmap_k : &tmap_v;
+            const int ps = a.c.ps, box = min(ps, N);
+            int pend[ST];
+            for (int s = 0; s < ST; ++s) pend[s] = -1;
+            int t = 0;
+            for (int n = 0;; ++n) {
+                const int js = n % kJobs;
+                if (!wait_bar(bar(L::kBarJF + js), (n / kJobs) & 1, ctl)) break;
+                const Job J = ring[js];
+                mbar_arrive(bar(L::kBarJE + js));
+                if (!J.valid) break;
+                const int *table = a.c.table + (size_t)J.b * a.c.max_pages;
+                bool ok = true;
+                for (int j = 0; j < J.nt; ++j, ++t) {
+                    const int s = t % ST;
+                    if (t >= ST && !wait_bar(bar(bempty + s), (t / ST - 1) & 1, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    pend[s] = -1;
+                    const int p0 = J.key0 + (J.lo + j) * N;
+                    const int nv = min(N, J.key_end - p0);  // keys that some row sees
+                    const int boxes = (nv + box - 1) / box;
+                    mbar_expect_tx(bar(bfull + s), (uint32_t)(boxes * box) * 128u * L::NB);
+                    for (int i = 0; i < boxes; ++i) {
+                        const int p = p0 + i * box;
+                        int page = __ldg(table + (p >> ca.psh));
+                        if ((unsigned)page >= (unsigned)a.c.num_pages) {
+                            page = 0;  // some memory of the pool; the job's results are dropped
+                            if (is_k) {
+                                bad_job[n % kBadSlots] = n + 1;
+                                __threadfence_block();
+                            }
+                        }
+                        const int row = (page * a.c.Hkv + J.hk) * ps + (p & (ps - 1));
+#pragma unroll
+                        for (int x = 0; x < L::NB; ++x)
+                            asm volatile(
+                                "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::"
+                                "bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                                    tiles + s * L::kTileBytes + x * L::kKVBox + (uint32_t)(i * box) * 128u),
+                                "l"(reinterpret_cast<uint64_t>(map)), "r"(bar(bfull + s)), "r"(x * 64),
+                                "r"(row)
+                                : "memory");
+                    }
+                    pend[s] = t;
+                }
+                if (!ok) break;
+            }
+            if (*abort_flag)
+                for (int s = 0; s < ST; ++s)
+                    if (pend[s] >= 0) drain_bar(bar(bfull + s), (pend[s] / ST) & 1, ca.wait_limit);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================= MMA issuer =================
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_bf16(kM, N, 0);
+            constexpr uint32_t idesc_o = idesc_bf16(kM, D, 1);
+            int t = 0;
+            int gt[kG] = {0, 0};  // S tiles of each Q tile so far
+            bool ok = true;
+            for (int n = 0; ok; ++n) {
+                const int js = n % kJobs;
+                if (!wait_poll(bar(L::kBarJF + js), (n / kJobs) & 1, ctl)) break;
+                const Job J = ring[js];
+                mbar_arrive(bar(L::kBarJE + js));
+                if (!J.valid) break;
+                // a Q tile without tiles in this job is released at once
+#pragma unroll
+                for (int g = 0; g < kG; ++g)
+                    if (ok && J.te[g] == 0) {
+                        ok = wait_poll(bar(L::kBarQ + g), n & 1, ctl);
+                        if (ok) mbar_arrive(bar(L::kBarQE + g));
+                    }
+                for (int j = 0; ok && j <= J.nt; ++j) {
+                    const int tk = t + j, s = tk % ST, tp = tk - 1, sp = (tp + ST) % ST, jp = j - 1;
+                    if (j < J.nt) {
+                        if (!wait_poll(bar(L::kBarKF + s), (tk / ST) & 1, ctl)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    if (jp >= 0 && !wait_poll(bar(L::kBarVF + sp), (tp / ST) & 1, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t kb = sK + s * L::kTileBytes, vb = sV + sp * L::kTileBytes;
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) {
+                        const uint32_t tS = tmem + g * 256, tO = tS + 128;
+                        if (ok && jp >= 0 && jp < J.te[g]) {
+                            // O_g += P_g V, P_g in the first columns of S_g (the warps
+                            // make a job's first P after they have read the last job's O)
+                            if (!wait_poll(bar(L::kBarP + g), (gt[g] + jp) & 1, ctl)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 0; k < N / 16; ++k)
+                                tc_mma_ta(tO, tS + k * 8, sdesc(vb + k * 2048, L::kKVBox, 1024), idesc_o,
+                                          (jp > 0 || k > 0) ? 1u : 0u);
+                            if (jp == J.te[g] - 1) tc_commit(bar(L::kBarPV + g));
+                        }
+                        if (ok && j < J.nt && j < J.te[g]) {
+                            if (j == 0) {
+                                if (!wait_poll(bar(L::kBarQ + g), n & 1, ctl)) {
+                                    ok = false;
+                                    break;
+                                }
+                                fence_proxy_async();
+                                tc_fence_after();
+                            }
+                            const uint32_t qb = sQ + g * L::NB * L::kQBox;
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = (uint32_t)(k % 4) * 32;
+                                tc_mma(tS, sdesc(qb + (k / 4) * L::kQBox + off, 16, 1024),
+                                       sdesc(kb + (k / 4) * L::kKVBox + off, 16, 1024), idesc_s, k > 0);
+                            }
+                            tc_commit(bar(L::kBarS + g));
+                            if (j == J.te[g] - 1) tc_commit(bar(L::kBarQE + g));
+                        }
+                    }
+                    if (!ok) break;
+                    if (j < J.nt) tc_commit(bar(L::kBarKE + s));
+                    if (jp >= 0) tc_commit(bar(L::kBarVE + sp));
+                }
+                t += J.nt;
+#pragma unroll
+                for (int g = 0; g < kG; ++g) gt[g] += J.te[g];
+            }
+            tc_commit(bar(L::kBarDrain));
+            drain_bar(bar(L::kBarDrain), 0, ca.wait_limit);
+        }
+        __syncwarp();
+    } else {
+        // ================= softmax (warps 2..9) =================
+        const int g = (warp - 2) >> 2, quarter = warp & 3;
+        const int jrow = g * kM + quarter * 32 + lane;  // row inside the job
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + lane_off + g * 256, tO = tS + 128;
+        const uint32_t sQg = sQ + g * L::NB * L::kQBox;
+        const uint32_t stg = base + L::kStage + (uint32_t)(warp - 2) * 4096u;
+        const int S = a.km1 + 1;
+        // this thread's row of a job: row << 5 | slot
+        auto entry_of = [&](const Job &J) -> int {
+            if (jrow >= J.nrows) return -1;
+            return J.own ? (J.rbase + jrow) << 5 | a.km1 : __ldg(a.list + J.rbase + jrow);
+        };
+        auto q_row = [&](int hk, int entry) -> size_t {
+            const int row = entry >> 5;
+            return (size_t)(row / a.G) * a.Hq + hk * a.G + row % a.G;
+        };
+        // the warp's 32 query rows into shared memory; zeros where there is no row
+        auto gather = [&](int hk, int entry) {
+            const unsigned long long mine =
+                entry >= 0 ? reinterpret_cast<unsigned long long>(a.q + q_row(hk, entry) * D) : 0ull;
+            const int ch = lane & 7;
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+                const int r = it * 4 + (lane >> 3);
+                const unsigned long long p = __shfl_sync(0xffffffffu, mine, r);
+                const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(p) + ch * 8;
+                const uint32_t dst =
+                    sQg + (uint32_t)(quarter * 32 + r) * 128 + ((uint32_t)(ch ^ (r & 7)) << 4);
+#pragma unroll
+                for (int x = 0; x < L::NB; ++x)
+                    cp_async16(dst + x * L::kQBox, p ? (const void *)(src + x * 64) : (const void *)a.q,
+                               p != 0);
+            }
+            cp_async_arrive_noinc(bar(L::kBarQ + g));
+        };
+        auto take = [&](int n, Job &J) -> bool {
+            const int js = n % kJobs;
+            if (!__all_sync(0xffffffffu, wait_bar(bar(L::kBarJF + js), (n / kJobs) & 1, ctl))) return false;
+            J = ring[js];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kBarJE + js));
+            return true;
+        };
+        int gt = 0, gj = 0, t = 0, n = 0;
+        Job J;
+        bool ok = take(0, J);
+        int entry = -1;
+        if (ok && J.valid) {
+            entry = entry_of(J);
+            gather(J.hk, entry);
+        }
+        while (ok && J.valid) {
+            const int ntile = g == 0 ? J.te[0] : J.te[1];
+            // positions that this row sees: [lo, hi]
+            int lo = 0, hi = J.key_end - 1;
+            if (J.own) {
+                hi = (entry >> 5) / a.G + J.pdelta;
+                if (!DENSE) lo = hi / a.c.bs * a.c.bs;
+            }
+            int lo_max = lo, hi_min = hi;
+            if (J.own) {  // over the Q tile's rows: consecutive, so the last and the first one
+                const int first = (J.rbase + g * kM) / a.G + J.pdelta;
+                const int last = (J.rbase + min(J.nrows, (g + 1) * kM) - 1) / a.G + J.pdelta;
+                hi_min = first;
+                lo_max = DENSE ? 0 : last / a.c.bs * a.c.bs;
+            }
+            float m_run = -INFINITY, l_run = 0.f;
+            const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+            for (int j = 0; j < ntile; ++j) {
+                if (!__all_sync(0xffffffffu, wait_bar(bar(L::kBarS + g), (gt + j) & 1, ctl))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int key0 = J.key0 + (J.lo + j) * N;
+                const bool mask = key0 + N - 1 > hi_min || key0 < lo_max || key0 + N > J.key_end;
+#pragma unroll 1
+                for (int h2 = 0; h2 < N / 64; ++h2) {
+                    uint32_t sr[2][32];
+                    tc_ld32(tS + 64 * h2, sr[0]);
+                    tc_ld32(tS + 64 * h2 + 32, sr[1]);
+                    tc_wait_ld();
+                    if (mask) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) {
+                            const int p = key0 + 64 * h2 + c;
+                            if (p > hi || p < lo) sr[c >> 5][c & 31] = 0xff800000u;
+                        }
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2)
+                        mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(sr[c >> 5][c & 31]),
+                                                 __uint_as_float(sr[c >> 5][(c & 31) + 1]));
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                    const bool raise = mt > m_run + 8.f;
+                    const float m_new = raise ? ceilf(mt) : m_run;
+                    if (__any_sync(0xffffffffu, raise && (j > 0 || h2 > 0))) {
+                        const float alpha = raise ? pow2_whole(m_run - m_new) : 1.f;
+                        if (j > 0) {
+#pragma unroll
+                            for (int c0 = 0; c0 < D; c0 += 16) {
+                                uint32_t o[16];
+                                tc_ld16(tO + c0, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int c = 0; c < 16; ++c)
+                                    o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                                tc_st16(tO + c0, o);
+                            }
+                        }
+                        if (h2 > 0) {  // the first half's P was made with the old offset
+                            tc_wait_st();
+#pragma unroll
+                            for (int c0 = 0; c0 < 32; c0 += 16) {
+                                uint32_t pw[16];
+                                tc_ld16(tS + c0, pw);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) {
+                                    const float2 f =
+                                        __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&pw[c]));
+                                    __nv_bfloat162 bb = __floats2bfloat162_rn(f.x * alpha, f.y * alpha);
+                                    pw[c] = *reinterpret_cast<uint32_t *>(&bb);
+                                }
+                                tc_st16(tS + c0, pw);
+                            }
+                        }
+                    }
+                    if (raise) {
+                        l_run *= pow2_whole(m_run - m_new);
+                        m_run = m_new;
+                    }
+                    const float mu = m_run == -INFINITY ? 0.f : m_run;
+                    const float2 nmu2 = make_float2(-mu, -mu);
+                    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float2 x = ffma2(make_float2(__uint_as_float(sr[(2 * c) >> 5][(2 * c) & 31]),
+                                                           __uint_as_float(sr[(2 * c + 1) >> 5][(2 * c + 1) & 31])),
+                                               sc2, nmu2);
+                        const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        ls[c & 1] = fadd2(ls[c & 1], pp);
+                        __nv_bfloat162 bb = __floats2bfloat162_rn(pp.x, pp.y);
+                        pk[c] = *reinterpret_cast<uint32_t *>(&bb);
+                    }
+                    tc_st32(tS + 32 * h2, pk);
+                    l_run += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
+                }
+                if (key0 + N > J.key_end) {
+                    // keys that no row sees: zeros in V (both Q tiles' warps write
+                    // the same zeros, each before its own product)
+                    const int tv = t + j;
+                    if (!__all_sync(0xffffffffu, wait_bar(bar(L::kBarVF + tv % ST), (tv / ST) & 1, ctl))) {
+                        ok = false;
+                        break;
+                    }
+                    const int nv = J.key_end - key0;
+                    const int rows = N - nv, per = rows * 8;
+                    for (int i = quarter * 32 + lane; i < per * L::NB; i += kM)
+                        st_shared_v4(sV + (tv % ST) * L::kTileBytes + (i / per) * L::kKVBox + nv * 128 +
+                                         (i % per) * 16,
+                                     0, 0, 0, 0);
+                    fence_proxy_async();
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::kBarP + g));
+            }
+            if (!ok) break;
+            gt += ntile;
+            t += J.nt;
+            // the next job's rows, as soon as this job's S MMAs have read Q
+            Job NJ;
+            if (!take(n + 1, NJ)) {
+                ok = false;
+                break;
+            }
+            int next_entry = -1;
+            if (NJ.valid) {
+                next_entry = entry_of(NJ);
+                if (!__all_sync(0xffffffffu, wait_bar(bar(L::kBarQE + g), n & 1, ctl))) {
+                    ok = false;
+                    break;
+                }
+                gather(NJ.hk, next_entry);
+            }
+            // ---------------- results ----------------
+            const bool bad = bad_job[n % kBadSlots] == n + 1;
+            if (bad && lane == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+            if (ntile > 0) {
+                if (!__all_sync(0xffffffffu, wait_bar(bar(L::kBarPV + g), gj & 1, ctl))) {
+                    ok = false;
+                    break;
+                }
+                ++gj;
+                tc_fence_after();
+                const float inv = 1.f / l_run;
+                const float lse2 = m_run + __log2f(l_run);
+                if (!DENSE || J.whole) {
+                    // 64 columns a pass, 128 bytes of each row: fp16 with a scale, or the bf16 result
+                    const size_t at = DENSE ? q_row(J.hk, max(entry, 0))
+                                            : ((size_t)J.hk * a.c.total * a.G + (max(entry, 0) >> 5)) * S +
+                                                  (max(entry, 0) & 31);
+                    uint16_t *dst0 = DENSE ? reinterpret_cast<uint16_t *>(a.out) : reinterpret_cast<uint16_t *>(a.part_h);
+                    const unsigned long long mine =
+                        entry >= 0 ? reinterpret_cast<unsigned long long>(dst0 + at * D) : 0ull;
+                    float back[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 64) {
+                        uint32_t o[2][32];
+                        tc_ld32(tO + c0, o[0]);
+                        tc_ld32(tO + c0 + 32, o[1]);
+                        tc_wait_ld();
+                        float f = inv;
+                        if (!DENSE) {
+                            float mx = 0.f;
+#pragma unroll
+                            for (int c = 0; c < 64; ++c)
+                                mx = fmaxf(mx, fabsf(__uint_as_float(o[c >> 5][c & 31]) * inv));
+                            // the largest value into [2^14, 2^15)
+                            const int ex = min(max((__float_as_int(mx) >> 23) & 255, 15), 254);
+                            f = inv * __int_as_float((268 - ex) << 23);
+                            back[c0 / 64] = __int_as_float((ex - 14) << 23);
+                        }
+#pragma unroll
+                        for (int ch = 0; ch < 8; ++ch) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int c = ch * 8 + 2 * e;
+                                const float x = __uint_as_float(o[c >> 5][c & 31]);
+                                const float y = __uint_as_float(o[(c + 1) >> 5][(c + 1) & 31]);
+                                if (DENSE) {
+                                    __nv_bfloat162 bb = __floats2bfloat162_rn(x * f, y * f);
+                                    w[e] = bad ? 0u : *reinterpret_cast<uint32_t *>(&bb);
+                                } else {
+                                    __half2 hh = __floats2half2_rn(x * f, y * f);
+                                    w[e] = *reinterpret_cast<uint32_t *>(&hh);
+                                }
+                            }
+                            st_shared_v4(stg + lane * 128 + ((uint32_t)(ch ^ (lane & 7)) << 4), w[0], w[1],
+                                         w[2], w[3]);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int it = 0; it < 8; ++it) {
+                            const int r = it * 4 + (lane >> 3), ch = lane & 7;
+                            const unsigned long long d = __shfl_sync(0xffffffffu, mine, r);
+                            const uint4 val = ld_shared_v4(stg + r * 128 + ((uint32_t)(ch ^ (r & 7)) << 4));
+                            if (d)
+                                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(d) + c0 + ch * 8) = val;
+                        }
+                        __syncwarp();
+                    }
+                    if (entry >= 0) {
+                        if (DENSE) a.lse[at] = bad ? -INFINITY : lse2 * 0.69314718055994530942f;
+                        else a.part_s[at] = make_float4(lse2, back[0], back[1], bad ? 0.f : 1.f);
+                    }
+                } else {
+                    // fp32 partial sums, 32 columns a pass
+                    float *prow = a.part_o + ((size_t)J.slot * kJobRows + g * kM + quarter * 32) * D;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tc_ld32(tO + c0, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int ch = 0; ch < 8; ++ch)
+                            st_shared_v4(stg + lane * 128 + ((uint32_t)(ch ^ (lane & 7)) << 4), o[4 * ch],
+                                         o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
+                        __syncwarp();
+#pragma unroll
+                        for (int it = 0; it < 8; ++it) {
+                            const int r = it * 4 + (lane >> 3), ch = lane & 7;
+                            const uint4 val = ld_shared_v4(stg + r * 128 + ((uint32_t)(ch ^ (r & 7)) << 4));
+                            if (g * kM + quarter * 32 + r < J.nrows)
+                                *reinterpret_cast<uint4 *>(prow + (size_t)r * D + c0 + ch * 4) = val;
+                        }
+                        __syncwarp();
+                    }
+                    if (entry >= 0)
+                        a.part_ml[(size_t)J.slot * kJobRows + jrow] = make_float2(m_run, bad ? -1.f : l_run);
+                }
+                // O may be overwritten
+                tc_fence_before();
+            } else if (DENSE && entry >= 0) {
+                // rows that see nothing of this part
+                a.part_ml[(size_t)J.slot * kJobRows + jrow] = make_float2(-INFINITY, bad ? -1.f : 0.f);
+            }
+            ++n;
+            J = NJ;
+            entry = next_entry;
+        }
+        cp_async_wait_all();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols)
+                     : "memory");
+    }
+}
+
+// ----------------------------------------------------------------------------
+// row tiles, list offsets and jobs (one CTA), and the lists
+// ----------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+
+// inclusive sum over the CTA's threads
+__device__ __forceinline__ long long block_scan(long long v, long long *warps, long long &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    __syncthreads();
+    if (lane == 31) warps[warp] = v;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w == warp) v += total;
+        total += warps[w];
+    }
+    return v;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
+    __shared__ long long warps[kPlanThreads / 32];
+    const int tid = threadIdx.x;
+    long long total;
+    // 256-row tiles of each sequence; refused ones have none, and clear rows
+    long long run = 0;
+    for (int b0 = 0; b0 < a.c.num_seqs; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        Seq s;
+        const int state = b < a.c.num_seqs ? a.c.seq(b, s) : (int)kSeqEmpty;
+        if (state == kSeqBad) {
+            atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+            for (size_t i = (size_t)s.row0 * a.Hq; i < (size_t)(s.row0 + s.n) * a.Hq; ++i) {
+                a.lse[i] = -INFINITY;
+                for (int d = 0; d < a.D; d += 8)
+                    *reinterpret_cast<uint4 *>(a.out + i * a.D + d) = make_uint4(0, 0, 0, 0);
+            }
+        }
+        const long long mine = state == kSeqOk ? ((long long)s.n * a.G + kJobRows - 1) / kJobRows : 0;
+        const long long inc = block_scan(mine, warps, total);
+        if (b < a.c.num_seqs) a.own_off[b + 1] = (int)min(run + inc, (long long)a.w_cap);
+        run += total;
+    }
+    if (tid == 0) a.own_off[0] = 0;
+    __threadfence_block();
+    __syncthreads();
+    const int tiles = (int)min(run, (long long)a.w_cap);
+    if (a.dense) {
+        run = 0;
+        for (int w0 = 0; w0 < tiles; w0 += kPlanThreads) {
+            const int w = w0 + tid;
+            long long mine = 0;
+            if (w < tiles) {
+                int b = 0, hi = a.c.num_seqs - 1;
+                while (b < hi) {
+                    const int mid = (b + hi + 1) >> 1;
+                    if (a.own_off[mid] <= w) b = mid; else hi = mid - 1;
+                }
+                Seq s;
+                a.c.seq(b, s);
+                Job J;
+                own_job<N>(a, s, b, 0, w - a.own_off[b], J);
+                mine = (long long)J.nt * a.c.Hkv;
+            }
+            const long long inc = block_scan(mine, warps, total);
+            if (w < tiles) a.unit_off[w + 1] = run + inc;
+            run += total;
+        }
+        if (tid == 0) a.unit_off[0] = 0;
+        return;
+    }
+    if (a.km1 == 0) return;
+    // offsets of the lists, and a job for every 256 rows of one
+    const long long lists = (long long)a.c.num_seqs * a.n_max * a.c.Hkv;
+    const long long per = (lists + kPlanThreads - 1) / kPlanThreads;
+    const long long l0 = min(per * tid, lists), l1 = min(l0 + per, lists);
+    long long rows = 0, jobs = 0;
+    for (long long l = l0; l < l1; ++l) {
+        const int n = a.counts[l];
+        rows += n;
+        jobs += (n + kJobRows - 1) / kJobRows;
+    }
+    long long row = block_scan(rows, warps, total) - rows;
+    const long long all_rows = total;
+    long long job = block_scan(jobs, warps, total) - jobs;
+    for (long long l = l0; l < l1; ++l) {
+        const int n = a.counts[l];
+        a.list_off[l] = (int)min(row, a.list_cap);
+        for (int s = 0; s < n; s += kJobRows, ++job)
+            if (job < a.job_cap) a.jobs[job] = make_int2((int)l, s);
+        row += n;
+    }
+    // (more rows than the tensors hold: only from offsets that overlap, refused ones among them)
+    if (tid == 0) {
+        a.list_off[lists] = (int)min(all_rows, a.list_cap);
+        *a.n_jobs = (int)min(total, a.job_cap);
+    }
+}
+
+// An entry's rows into the lists of the blocks that they selected; a row's
+// slots are its past blocks in ascending order.
+__global__ void __launch_bounds__(kMaxRows) scatter_kernel(Attn a) {
+    const int e = blockIdx.x, r = threadIdx.x;
+    const int n = a.tiles[e] - 1;
+    if (n <= 0) return;
+    const Entry x = get_entry(a, e);
+    if (r >= x.nt * a.G) return;
+    const int row = (x.row0 + r / a.G) * a.G + r % a.G;
+    int slot = 0;
+    for (int i = 0; i < n; ++i) {
+        const unsigned long long mask = a.umask[(size_t)e * a.ucap + i];
+        if (!((mask >> r) & 1)) continue;
+        const size_t l = ((size_t)x.b * a.n_max + a.ublk[(size_t)e * a.ucap + i]) * a.c.Hkv + x.hk;
+        const long long at = (long long)a.list_off[l] + a.ubase[(size_t)e * a.ucap + i] +
+                             __popcll(mask & ((1ull << r) - 1));
+        if (at < a.list_cap) a.list[at] = row << 5 | slot;
+        ++slot;
+    }
+}
+
+// ----------------------------------------------------------------------------
+// merges
+// ----------------------------------------------------------------------------
+// A row's slots (its past blocks and its own), weighted by their sums: a warp a
+// row, the rows of an entry to a CTA.
+template <int D>
+__global__ void __launch_bounds__(128) merge_slots_kernel(Attn a) {
+    constexpr int V = D / 32;
+    const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Entry x = get_entry(a, e);
+    if (x.state != kSeqOk) return;  // cleared before
+    const bool none = a.tiles[e] == 0;
+    const int S = a.km1 + 1;
+    for (int r = warp; r < x.nt * a.G; r += 4) {
+        const size_t at = (size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G;
+        const size_t p0 = ((size_t)x.hk * a.c.total * a.G + (size_t)(x.row0 + r / a.G) * a.G + r % a.G) * S;
+        const int n = min(a.km1, (x.pos0 + r / a.G) / a.c.bs);
+        // lane s < n: slot s, lane n: the own block's
+        float4 mine = make_float4(-INFINITY, 0.f, 0.f, 1.f);
+        if (!none && lane <= n) mine = a.part_s[p0 + (lane < n ? lane : a.km1)];
+        float M = mine.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const bool bad = none || __any_sync(0xffffffffu, mine.w == 0.f);
+        const float w = fast_exp2(mine.x - M);
+        float W = lane <= n ? w : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+        const float inv = 1.f / W;
+        const float f0 = w * inv * mine.y, f1 = w * inv * mine.z;
+        float acc[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        if (!bad)
+            for (int s = 0; s <= n; ++s) {
+                const float g0 = __shfl_sync(0xffffffffu, f0, s), g1 = __shfl_sync(0xffffffffu, f1, s);
+                const float f = lane * V < 64 ? g0 : g1;
+                const __half2 *src = reinterpret_cast<const __half2 *>(
+                    a.part_h + (p0 + (s < n ? s : a.km1)) * D + lane * V);
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) {
+                    const float2 h = __half22float2(src[k]);
+                    acc[2 * k] = fmaf(h.x, f, acc[2 * k]);
+                    acc[2 * k + 1] = fmaf(h.y, f, acc[2 * k + 1]);
+                }
+            }
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            __nv_bfloat162 bb = __floats2bfloat162_rn(acc[k], acc[k + 1]);
+            *reinterpret_cast<uint32_t *>(a.out + at * D + lane * V + k) =
+                bad ? 0u : *reinterpret_cast<uint32_t *>(&bb);
+        }
+        if (lane == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(W)) * 0.69314718055994530942f;
+    }
+}
+
+// The fp32 partial sums of row tiles that several CTAs worked on.
+template <int D>
+__global__ void __launch_bounds__(128) merge_runs_kernel(Attn a) {
+    constexpr int V = D / 32;
+    const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = e / a.c.Hkv, hk = e % a.c.Hkv;
+    if (w >= a.own_off[a.c.num_seqs]) return;
+    const int first = a.c_first[e], last = a.c_last[e];
+    if (first == last) return;
+    const int b = upper_index(a.own_off, a.c.num_seqs, w);
+    Seq s;
+    a.c.seq(b, s);
+    const int r0 = (w - a.own_off[b]) * kJobRows, nrows = min(kJobRows, s.n * a.G - r0);
+    for (int r = blockIdx.y * 4 + warp; r < nrows; r += gridDim.y * 4) {
+        const int row = s.row0 * a.G + r0 + r;
+        const size_t at = (size_t)(row / a.G) * a.Hq + hk * a.G + row % a.G;
+        float M = -INFINITY;
+        bool bad = false;
+        for (int c = first + lane; c <= last; c += 32) {
+            const float2 ml = a.part_ml[(size_t)(2 * c + (c == first)) * kJobRows + r];
+            bad |= ml.y < 0.f;
+            M = fmaxf(M, ml.x);
+        }
+        bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float acc[V], sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        if (!bad)
+            for (int c = first; c <= last; ++c) {
+                const size_t p = (size_t)(2 * c + (c == first)) * kJobRows + r;
+                const float2 ml = a.part_ml[p];
+                if (ml.y == 0.f) continue;
+                const float f = fast_exp2(ml.x - M);
+                sum = fmaf(ml.y, f, sum);
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[k] = fmaf(a.part_o[p * D + lane * V + k], f, acc[k]);
+            }
+        const float inv = 1.f / sum;
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            __nv_bfloat162 bb = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
+            *reinterpret_cast<uint32_t *>(a.out + at * D + lane * V + k) =
+                bad ? 0u : *reinterpret_cast<uint32_t *>(&bb);
+        }
+        if (lane == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(sum)) * 0.69314718055994530942f;
+    }
+}
+
+// ----------------------------------------------------------------------------
+// host side
+// ----------------------------------------------------------------------------
+template <int D, int N, bool DENSE>
+cudaError_t launch(const Attn &a, cudaStream_t st) {
+    CUtensorMap mk, mv;
+    const long long rows = (long long)a.c.num_pages * a.c.Hkv * a.c.ps;
+    const int box = a.c.ps < N ? a.c.ps : N;
+    if (!make_tma_rows(&mk, a.k, rows, D, box) || !make_tma_rows(&mv, a.v, rows, D, box))
+        return cudaErrorInvalidValue;
+    const int bytes = (int)Smem<D, N>::kRequest;
+    auto kern = chunk_kernel<D, N, DENSE>;
+    // every warp role must be resident: refuse a build whose registers do not allow it
+    static std::atomic<int> fits{0};
+    if (fits.load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes fa;
+        const cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+        if (e != cudaSuccess) return e;
+        fits.store(fa.maxThreadsPerBlock >= kThreads ? 1 : -1, std::memory_order_relaxed);
+    }
+    if (fits.load(std::memory_order_relaxed) < 0) return cudaErrorInvalidConfiguration;
+    cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (rc != cudaSuccess) return rc;
+    ChunkArgs ca;
+    ca.a = a;
+    ca.psh = __builtin_ctz((unsigned)a.c.ps);
+    ca.wait_limit = kDefaultWaitLimit;
+    kern<<<a.ctas, kThreads, bytes, st>>>(mk, mv, ca);
+    rc = cudaGetLastError();
+    if (rc != cudaSuccess) return rc;
+    if (DENSE) merge_runs_kernel<D><<<dim3(a.w_cap * a.c.Hkv, 4), 128, 0, st>>>(a);
+    else merge_slots_kernel<D><<<a.n_ent, 128, 0, st>>>(a);
+    note_launches(2);
+    return cudaGetLastError();
+}
+
+// keys per tile: 128, or 64 where blocks are no multiple of 128
+bool wide(const Attn &a) { return a.dense || a.c.bs % 128 == 0; }
+
+}  // namespace
+
+cudaError_t launch_plan(const Attn &a, cudaStream_t st) {
+    if (wide(a)) plan_kernel<128><<<1, kPlanThreads, 0, st>>>(a);
+    else plan_kernel<64><<<1, kPlanThreads, 0, st>>>(a);
+    cudaError_t rc = cudaGetLastError();
+    note_launches(1);
+    if (rc != cudaSuccess || a.km1 == 0) return rc;
+    scatter_kernel<<<a.n_ent, kMaxRows, 0, st>>>(a);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_chunk(const Attn &a, cudaStream_t st) {
+    if (a.dense) return a.D == 64 ? launch<64, 128, true>(a, st) : launch<128, 128, true>(a, st);
+    if (wide(a)) return a.D == 64 ? launch<64, 128, false>(a, st) : launch<128, 128, false>(a, st);
+    return a.D == 64 ? launch<64, 64, false>(a, st) : launch<128, 64, false>(a, st);
+}
+
+}  // namespace paged
+}  // namespace moba

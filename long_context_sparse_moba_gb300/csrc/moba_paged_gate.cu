@@ -16,7 +16,9 @@
 // tie) are decided by a warp with 64-bit scores of the blocks within 3 E of the
 // boundary, so that the selection is the one of 64-bit arithmetic.
 // Then the blocks that any row selected are listed, each with the rows that
-// did: the attention kernel reads a block once for all rows of the entry.
+// did: the attention kernel reads a block once for all rows of the entry.  For
+// chunks of many rows the own blocks stay out of it, and each block's count of
+// rows over all entries is taken, for lists of the rows that selected it.
 #include "moba_mma.cuh"
 #include "moba_paged_attn.cuh"
 #include "moba_select.cuh"
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
         }
         if (!bad) {
             for (int i = 0; i < n; ++i) atomicOr(bits + (mine[i] >> 5), 1u << (mine[i] & 31));
-            atomicOr(bits + (ci >> 5), 1u << (ci & 31));
+            if (!a.chunk) atomicOr(bits + (ci >> 5), 1u << (ci & 31));
         }
         if (a.idx) {
             int32_t *dst = a.idx + ((size_t)(x.row0 + tid / G) * a.Hq + x.hk * G + tid % G) * a.topk;
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
     __syncthreads();
     if (row_ok) {
         const int n = min(km1, ci);
-        for (int i = 0; i <= n; ++i) {
+        for (int i = 0; i < n + (a.chunk ? 0 : 1); ++i) {
             const int c = i < n ? sel[tid * 32 + i] : ci;
             const int at = rank[c >> 5] + __popc(bits[c >> 5] & ((1u << (c & 31)) - 1u));
             atomicOr(mask + at, 1ull << tid);
@@ -343,7 +345,16 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
         }
     }
     for (int i = tid; i < count; i += kThreads) umask[i] = mask[i];
-    if (tid == 0) a.tiles[e] = (count - 1) * a.tpb + (pos_last - c_own * bs) / kTile + 1;
+    if (!a.chunk) {
+        if (tid == 0) a.tiles[e] = (count - 1) * a.tpb + (pos_last - c_own * bs) / kTile + 1;
+        return;
+    }
+    // this entry's place in the list of each block that its rows selected
+    if (tid == 0) a.tiles[e] = count + 1;
+    __syncthreads();
+    for (int i = tid; i < count; i += kThreads)
+        a.ubase[(size_t)e * a.ucap + i] =
+            atomicAdd(a.counts + ((size_t)x.b * a.n_max + ublk[i]) * a.c.Hkv + x.hk, __popcll(mask[i]));
 }
 
 // The selection where topk covers every block: all of them.

@@ -406,14 +406,35 @@ size_t scratch(Attn *a, void *base) {
         return p;
     };
     const size_t n = a->n_ent;
-    a->c_first = static_cast<int *>(take(4 * n));
-    a->c_last = static_cast<int *>(take(4 * n));
-    a->part_ml = static_cast<float2 *>(take(sizeof(float2) * 2 * a->ctas * a->rows));
-    a->part_o = static_cast<float *>(take(sizeof(float) * 2 * a->ctas * a->rows * a->D));
+    // entries, CTAs and rows that share partial sums
+    const size_t ents = a->chunk ? (size_t)a->w_cap * a->c.Hkv : n;
+    const size_t parts = 2 * (size_t)a->ctas * (a->chunk ? kJobRows : a->rows);
+    if (a->dense || !a->chunk) {
+        a->c_first = static_cast<int *>(take(4 * ents));
+        a->c_last = static_cast<int *>(take(4 * ents));
+        a->part_ml = static_cast<float2 *>(take(sizeof(float2) * parts));
+        a->part_o = static_cast<float *>(take(sizeof(float) * parts * a->D));
+    }
     if (!a->dense) {
         a->tiles = static_cast<int *>(take(4 * n));
         a->ublk = static_cast<int *>(take(4 * n * a->ucap));
         a->umask = static_cast<unsigned long long *>(take(8 * n * a->ucap));
+    }
+    if (a->chunk) {
+        a->own_off = static_cast<int *>(take(4 * ((size_t)a->c.num_seqs + 1)));
+        a->unit_off = static_cast<long long *>(take(8 * ((size_t)a->w_cap + 1)));
+    }
+    if (a->chunk && !a->dense) {
+        const size_t lists = (size_t)a->c.num_seqs * a->n_max * a->c.Hkv;
+        const size_t slots = (size_t)a->c.total * a->Hq * (a->km1 + 1);
+        a->counts = static_cast<int *>(take(4 * lists));
+        a->list_off = static_cast<int *>(take(4 * (lists + 1)));
+        a->jobs = static_cast<int2 *>(take(8 * (size_t)a->job_cap));
+        a->n_jobs = static_cast<int *>(take(4));
+        a->list = static_cast<int *>(take(4 * (size_t)a->list_cap));
+        a->ubase = static_cast<int *>(take(4 * n * a->ucap));
+        a->part_h = static_cast<__half *>(take(sizeof(__half) * slots * a->D));
+        a->part_s = static_cast<float4 *>(take(sizeof(float4) * slots));
     }
     return off;
 }
@@ -440,8 +461,22 @@ int make_attn(Attn *a, int Hq, int D, int topk) {
     a->n_ent = (int)n_ent;
     a->tpb = bs / kTile;
     a->ctas = sm_count();
-    const long long ucap = (long long)a->rows * (a->km1 + 1);
-    a->ucap = a->dense ? 0 : (int)(ucap < n_max ? ucap : n_max);
+    a->n_max = (int)(n_max < (1 << 30) ? n_max : 1 << 30);
+    // more rows than an entry holds go to the tcgen05 kernel, where row numbers
+    // (token, head of the group) and lists are 32-bit
+    const long long lists = a->dense ? 0 : (long long)a->c.num_seqs * n_max * a->c.Hkv;
+    a->list_cap = (long long)a->c.total * Hq * a->km1;
+    a->chunk = rows > kMaxRows && (long long)a->c.total * a->G < (1ll << 26) &&
+               lists < (1ll << 30) && a->list_cap < (1ll << 31);
+    if (a->chunk) {
+        const long long w0 = (long long)a->c.num_seqs * ((rows + kJobRows - 1) / kJobRows);
+        const long long w1 = (long long)a->c.total * a->G / kJobRows + a->c.num_seqs;
+        a->w_cap = (int)(w0 < w1 ? w0 : w1);
+        a->job_cap = a->list_cap / kJobRows + (lists < a->list_cap ? lists : a->list_cap) + 1;
+        if ((long long)a->w_cap * a->c.Hkv >= (1ll << 30)) return MOBA_ERR_UNSUPPORTED;
+    }
+    const long long ucap = (long long)a->rows * (a->km1 + (a->chunk ? 0 : 1));
+    a->ucap = a->dense ? 0 : (int)(ucap < n_max ? (ucap > 0 ? ucap : 1) : n_max);
     a->scale_log2 = (float)(1.4426950408889634 / __builtin_sqrt((double)D));
     return MOBA_OK;
 }
@@ -504,8 +539,12 @@ MOBA_EXPORT int moba_paged_attn(const void *q, const void *k_pages, const void *
         workspace = own;
     }
     scratch(&a, workspace);
-    cudaError_t e = launch_gate(a, st);
-    if (e == cudaSuccess) e = launch_rows(a, st);
+    cudaError_t e = cudaSuccess;
+    if (a.chunk && !a.dense)
+        e = cudaMemsetAsync(a.counts, 0, 4 * (size_t)num_seqs * a.n_max * Hkv, st);
+    if (e == cudaSuccess) e = launch_gate(a, st);
+    if (e == cudaSuccess && a.chunk) e = launch_plan(a, st);
+    if (e == cudaSuccess) e = a.chunk ? launch_chunk(a, st) : launch_rows(a, st);
     if (own) {
         const cudaError_t f = cudaFreeAsync(own, st);
         if (e == cudaSuccess) e = f;

@@ -284,3 +284,34 @@ def test_offsets_beyond_32_bits():
     got = attend(c, q, [5], [n], block, 3, with_idx=True)
     assert ops.get_status() == ops.MOBA_OK
     compare(got, expect(q, ks, vs, c, [5], [n], block, 3))
+
+
+@pytest.mark.parametrize("topk", [1, 3, 40])
+def test_bad_sequences_in_long_chunks(topk):
+    nq, lens = [200, 90, 150, 400], [300, 1000, 150, 900]
+    c, ks, vs = filled(lens, 2, 64, 16, 64, seed=12)
+    q = normal(2, 840, 4, 64)
+    want = expect(q, ks, vs, c, nq, lens, 64, topk)
+    cu = [0, 200, 290, 440, 840]
+    good = torch.ones(840, dtype=torch.bool, device="cuda")
+    good[200:440] = False
+    out, lse, idx = ops.paged_attn(q, c.k, c.v, c.kbar, c.table, i32(cu), i32([300, 89, c.mp * 16 + 1, 900]), 400, 64,
+                                   topk, with_idx=True)
+    assert ops.get_status() == ops.MOBA_ERR_INVALID_ARG
+    compare((out[good], lse[good], idx[good]), [t[good] for t in want])
+    assert (out[~good] == 0).all() and (lse[~good] == -float("inf")).all() and (idx[~good] == -1).all()
+    # offsets that decrease, overlap, leave the rows, or give more than max_new
+    for wrong in ([0, 400, 0, 400, 0], [0, 200, 290, 440, 841], [-1, 200, 290, 440, 840], [0, 401, 401, 401, 840]):
+        ops.paged_attn(q, c.k, c.v, c.kbar, c.table, i32(wrong), i32([900] * 4), 400, 64, topk)
+        assert ops.get_status() == ops.MOBA_ERR_INVALID_ARG
+    # a page outside the pool: the newest tokens' page of the last sequence
+    table = c.table.clone()
+    table[3, 899 // 16] = c.P
+    out, lse, _ = ops.paged_attn(q, c.k, c.v, c.kbar, table, i32(cu), i32(lens), 400, 64, topk)
+    assert ops.get_status() == ops.MOBA_ERR_INVALID_ARG
+    assert (out[836:] == 0).all() and (lse[836:] == -float("inf")).all()
+    compare((out[:440], lse[:440], None), [t[:440] for t in want])
+    # the context stays usable
+    got = ops.paged_attn(q, c.k, c.v, c.kbar, c.table, i32(cu), i32(lens), 400, 64, topk, with_idx=True)
+    assert ops.get_status() == ops.MOBA_OK
+    compare(got, want)
