@@ -741,6 +741,7 @@ constexpr int kPlanThreads = 1024;
 
 // inclusive sum over the CTA's threads
 __device__ __forceinline__ long long block_scan(long long v, long long *warps, long long &total) {
+    static_assert(kPlanThreads == 1024, "a warp scans the warps' sums");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -750,12 +751,15 @@ __device__ __forceinline__ long long block_scan(long long v, long long *warps, l
     __syncthreads();
     if (lane == 31) warps[warp] = v;
     __syncthreads();
-    total = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w == warp) v += total;
-        total += warps[w];
+    long long s = warps[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
     }
-    return v;
+    total = __shfl_sync(0xffffffffu, s, 31);
+    const long long before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+    return v + (warp > 0 ? before : 0);
 }
 
 template <int N>
@@ -839,21 +843,31 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
 }
 
 // An entry's rows into the lists of the blocks that they selected; a row's
-// slots are its past blocks in ascending order.
-__global__ void __launch_bounds__(kMaxRows) scatter_kernel(Attn a) {
+// slots are its past blocks in ascending order.  The entry's blocks are read
+// once, side by side, then each row walks them in shared memory.
+constexpr int kScatterThreads = 128;
+
+__global__ void __launch_bounds__(kScatterThreads) scatter_kernel(Attn a) {
+    extern __shared__ unsigned long long s_mask[];  // [ucap], then where each block's rows go, [ucap]
+    int *s_at = reinterpret_cast<int *>(s_mask + a.ucap);
     const int e = blockIdx.x, r = threadIdx.x;
     const int n = a.tiles[e] - 1;
     if (n <= 0) return;
     const Entry x = get_entry(a, e);
+    for (int i = r; i < n; i += kScatterThreads) {
+        s_mask[i] = a.umask[(size_t)e * a.ucap + i];
+        const size_t l = ((size_t)x.b * a.n_max + a.ublk[(size_t)e * a.ucap + i]) * a.c.Hkv + x.hk;
+        // (sums stay below the list capacity, or are refused below)
+        s_at[i] = (int)min((long long)a.list_off[l] + a.ubase[(size_t)e * a.ucap + i], a.list_cap);
+    }
+    __syncthreads();
     if (r >= x.nt * a.G) return;
     const int row = (x.row0 + r / a.G) * a.G + r % a.G;
     int slot = 0;
     for (int i = 0; i < n; ++i) {
-        const unsigned long long mask = a.umask[(size_t)e * a.ucap + i];
+        const unsigned long long mask = s_mask[i];
         if (!((mask >> r) & 1)) continue;
-        const size_t l = ((size_t)x.b * a.n_max + a.ublk[(size_t)e * a.ucap + i]) * a.c.Hkv + x.hk;
-        const long long at = (long long)a.list_off[l] + a.ubase[(size_t)e * a.ucap + i] +
-                             __popcll(mask & ((1ull << r) - 1));
+        const long long at = (long long)s_at[i] + __popcll(mask & ((1ull << r) - 1));
         if (at < a.list_cap) a.list[at] = row << 5 | slot;
         ++slot;
     }
@@ -862,56 +876,73 @@ __global__ void __launch_bounds__(kMaxRows) scatter_kernel(Attn a) {
 // ----------------------------------------------------------------------------
 // merges
 // ----------------------------------------------------------------------------
-// A row's slots (its past blocks and its own), weighted by their sums: a warp a
-// row, the rows of an entry to a CTA.
+// A row's slots (its past blocks and its own), weighted by their sums, the
+// weights taken relative to a running maximum: D / 8 lanes a row, 16 bytes of
+// each slot a lane, four slots in flight.  Bound: HBM and L2 (the partials).
+constexpr int kSlotThreads = 256;
+
 template <int D>
-__global__ void __launch_bounds__(128) merge_slots_kernel(Attn a) {
-    constexpr int V = D / 32;
-    const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kSlotThreads) merge_slots_kernel(Attn a) {
+    constexpr int GL = D / 8, U = 4;
+    const int e = blockIdx.x, gl = threadIdx.x % GL;
     const Entry x = get_entry(a, e);
     if (x.state != kSeqOk) return;  // cleared before
     const bool none = a.tiles[e] == 0;
     const int S = a.km1 + 1;
-    for (int r = warp; r < x.nt * a.G; r += 4) {
+    for (int r = threadIdx.x / GL; r < x.nt * a.G; r += kSlotThreads / GL) {
+        const int row = (x.row0 + r / a.G) * a.G + r % a.G;
         const size_t at = (size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G;
-        const size_t p0 = ((size_t)x.hk * a.c.total * a.G + (size_t)(x.row0 + r / a.G) * a.G + r % a.G) * S;
-        const int n = min(a.km1, (x.pos0 + r / a.G) / a.c.bs);
-        // lane s < n: slot s, lane n: the own block's
-        float4 mine = make_float4(-INFINITY, 0.f, 0.f, 1.f);
-        if (!none && lane <= n) mine = a.part_s[p0 + (lane < n ? lane : a.km1)];
-        float M = mine.x;
+        const size_t p0 = ((size_t)x.hk * a.c.total * a.G + row) * S;
+        const int n = none ? 0 : min(a.km1, (x.pos0 + r / a.G) / a.c.bs) + 1;  // slots, the own block's last
+        float M = -INFINITY, W = 0.f, acc[8];
+        bool bad = none;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const bool bad = none || __any_sync(0xffffffffu, mine.w == 0.f);
-        const float w = fast_exp2(mine.x - M);
-        float W = lane <= n ? w : 0.f;
+        for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+        for (int s0 = 0; s0 < n; s0 += U) {
+            float4 ps[U];
+            uint4 h[U];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
-        const float inv = 1.f / W;
-        const float f0 = w * inv * mine.y, f1 = w * inv * mine.z;
-        float acc[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = 0.f;
-        if (!bad)
-            for (int s = 0; s <= n; ++s) {
-                const float g0 = __shfl_sync(0xffffffffu, f0, s), g1 = __shfl_sync(0xffffffffu, f1, s);
-                const float f = lane * V < 64 ? g0 : g1;
-                const __half2 *src = reinterpret_cast<const __half2 *>(
-                    a.part_h + (p0 + (s < n ? s : a.km1)) * D + lane * V);
-#pragma unroll
-                for (int k = 0; k < V / 2; ++k) {
-                    const float2 h = __half22float2(src[k]);
-                    acc[2 * k] = fmaf(h.x, f, acc[2 * k]);
-                    acc[2 * k + 1] = fmaf(h.y, f, acc[2 * k + 1]);
+            for (int j = 0; j < U; ++j)
+                if (s0 + j < n) {
+                    const size_t p = p0 + (s0 + j < n - 1 ? s0 + j : a.km1);
+                    ps[j] = __ldg(a.part_s + p);
+                    h[j] = __ldcs(reinterpret_cast<const uint4 *>(a.part_h + p * D) + gl);
                 }
+            float mx = M;
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (s0 + j < n) mx = fmaxf(mx, ps[j].x);
+            if (mx > M) {
+                const float f = fast_exp2(M - mx);
+                W *= f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] *= f;
+                M = mx;
             }
 #pragma unroll
-        for (int k = 0; k < V; k += 2) {
-            __nv_bfloat162 bb = __floats2bfloat162_rn(acc[k], acc[k + 1]);
-            *reinterpret_cast<uint32_t *>(a.out + at * D + lane * V + k) =
-                bad ? 0u : *reinterpret_cast<uint32_t *>(&bb);
+            for (int j = 0; j < U; ++j)
+                if (s0 + j < n) {
+                    bad |= ps[j].w == 0.f;
+                    const float w = fast_exp2(ps[j].x - M);
+                    W += w;
+                    const float f = w * (gl < 8 ? ps[j].y : ps[j].z);
+                    const __half2 *h2 = reinterpret_cast<const __half2 *>(&h[j]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 v = __half22float2(h2[k]);
+                        acc[2 * k] = fmaf(v.x, f, acc[2 * k]);
+                        acc[2 * k + 1] = fmaf(v.y, f, acc[2 * k + 1]);
+                    }
+                }
         }
-        if (lane == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(W)) * 0.69314718055994530942f;
+        const float inv = 1.f / W;
+        uint4 o;
+        __nv_bfloat162 *o2 = reinterpret_cast<__nv_bfloat162 *>(&o);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o2[k] = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+        if (bad) o = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(a.out + at * D + gl * 8) = o;
+        if (gl == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(W)) * 0.69314718055994530942f;
     }
 }
 
@@ -995,8 +1026,8 @@ cudaError_t launch(const Attn &a, cudaStream_t st) {
     kern<<<a.ctas, kThreads, bytes, st>>>(mk, mv, ca);
     rc = cudaGetLastError();
     if (rc != cudaSuccess) return rc;
-    if (DENSE) merge_runs_kernel<D><<<dim3(a.w_cap * a.c.Hkv, 4), 128, 0, st>>>(a);
-    else merge_slots_kernel<D><<<a.n_ent, 128, 0, st>>>(a);
+    if (DENSE) merge_runs_kernel<D><<<dim3(a.w_cap * a.c.Hkv, 16), 128, 0, st>>>(a);
+    else merge_slots_kernel<D><<<a.n_ent, kSlotThreads, 0, st>>>(a);
     note_launches(2);
     return cudaGetLastError();
 }
@@ -1012,7 +1043,7 @@ cudaError_t launch_plan(const Attn &a, cudaStream_t st) {
     cudaError_t rc = cudaGetLastError();
     note_launches(1);
     if (rc != cudaSuccess || a.km1 == 0) return rc;
-    scatter_kernel<<<a.n_ent, kMaxRows, 0, st>>>(a);
+    scatter_kernel<<<a.n_ent, kScatterThreads, 12 * a.ucap, st>>>(a);
     note_launches(1);
     return cudaGetLastError();
 }

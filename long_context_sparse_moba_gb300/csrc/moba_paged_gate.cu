@@ -13,8 +13,9 @@
 // a term for pooled keys so small that lo underflows).  Where the last kept and
 // the first dropped score are more than 2 E apart the selection is settled;
 // the other rows (about one in a hundred on random keys, all of them when keys
-// tie) are decided by a warp with 64-bit scores of the blocks within 3 E of the
-// boundary, so that the selection is the one of 64-bit arithmetic.
+// tie) are decided by a warp with 64-bit scores, so that the selection is the
+// one of 64-bit arithmetic: scores of the topk best by fp32 where the next one
+// lies 2 E below the boundary, else of all blocks within 3 E of it.
 // Then the blocks that any row selected are listed, each with the rows that
 // did: the attention kernel reads a block once for all rows of the entry.  For
 // chunks of many rows the own blocks stay out of it, and each block's count of
@@ -36,7 +37,7 @@ constexpr int kScStride = kTile + 1;
 struct GateSmem {
     uint32_t hi, lo, sc, sel, bits, rank, mask, bytes;
 };
-__host__ __device__ inline GateSmem gate_smem(int D, int words, int ucap) {
+__host__ __device__ inline GateSmem gate_smem(int D, int words, int ucap, int km1) {
     GateSmem s;
     uint32_t o = 0;
     s.hi = o;
@@ -48,7 +49,7 @@ __host__ __device__ inline GateSmem gate_smem(int D, int words, int ucap) {
     s.sc = o;
     o += 4 * kMaxRows * kScStride;
     s.sel = o;
-    o += 4 * kMaxRows * 32;
+    o += 4 * kMaxRows * (km1 + 1);
     s.bits = o;
     o += 4 * words;
     s.rank = o;
@@ -104,15 +105,66 @@ __device__ __noinline__ int pick64(const Attn &a, int hk, const int *table, cons
     return who;
 }
 
+// The same among n given blocks, in any order.
+template <int D>
+__device__ __noinline__ int pick64_of(const Attn &a, int hk, const int *table, const __nv_bfloat16 *qr,
+                                      const int *ids, int n) {
+    const int lane = threadIdx.x & 31, ppb = a.c.bs / a.c.ps;
+    double best = -INFINITY;
+    int who = sel::kEmpty;
+    for (int i = 0; i < n; ++i) {
+        const int c = ids[i], page = __ldg(table + (c + 1) * ppb - 1);
+        if ((unsigned)page >= (unsigned)a.c.num_pages) continue;
+        const float *kb = a.kbar + ((size_t)page * a.c.Hkv + hk) * D;
+        double s = 0.0;
+#pragma unroll
+        for (int d = 0; d < D; d += 32)
+            s = fma((double)__bfloat162float(qr[d + lane]), (double)__ldg(kb + d + lane), s);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (s != s) s = -INFINITY;
+        const int at = __popc(__ballot_sync(
+            0xffffffffu, who != sel::kEmpty && (best > s || (best == s && who < c))));
+        const double pb = __shfl_up_sync(0xffffffffu, best, 1);
+        const int pw = __shfl_up_sync(0xffffffffu, who, 1);
+        if (lane > at) {
+            best = pb;
+            who = pw;
+        } else if (lane == at) {
+            best = s;
+            who = c;
+        }
+    }
+    return who;
+}
+
+// insert (x, c) into a descending list; an equal score keeps the lower block first
+template <int KCAP>
+__device__ __forceinline__ void merge_insert(float (&ts)[KCAP], int (&ti)[KCAP], float x, int c) {
+    bool ins = false;
+#pragma unroll
+    for (int s = 0; s < KCAP; ++s) {
+        if (ins || x > ts[s] || ti[s] == sel::kEmpty || (x == ts[s] && c < ti[s])) {
+            const float fs = ts[s];
+            const int fi = ti[s];
+            ts[s] = x;
+            ti[s] = c;
+            x = fs;
+            c = fi;
+            ins = true;
+        }
+    }
+}
+
 template <int D, int KCAP>
 __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
     constexpr int KS = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int s_bad, s_knmax, s_unsure, s_count, s_rows[kMaxRows];
+    __shared__ int s_bad, s_knmax, s_unsure, s_count, s_rows[kMaxRows], s_few[kMaxRows], s_page[kTile];
     __shared__ float s_floor[kMaxRows];
-    const GateSmem L = gate_smem(D, words, a.ucap);
+    const GateSmem L = gate_smem(D, words, a.ucap, a.km1);
     float *sc = reinterpret_cast<float *>(smem + L.sc);
-    int *sel = reinterpret_cast<int *>(smem + L.sel);  // [row][32]
+    int *sel = reinterpret_cast<int *>(smem + L.sel);  // [row][km1 + 1]
     unsigned *bits = reinterpret_cast<unsigned *>(smem + L.bits);
     int *rank = reinterpret_cast<int *>(smem + L.rank);
     unsigned long long *mask = reinterpret_cast<unsigned long long *>(smem + L.mask);
@@ -139,11 +191,13 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
     }
     for (int i = tid; i < words; i += kThreads) bits[i] = 0;
     __syncthreads();
-    const bool row_ok = tid < nrows;
-    const int ci = row_ok ? (x.pos0 + tid / G) / bs : 0;  // the row's own block
-    const __nv_bfloat16 *qrow =
-        a.q + ((size_t)(x.row0 + tid / G) * a.Hq + x.hk * G + tid % G) * D;
+    // two threads to a row, for half the scores of a tile each
+    const int row = tid >> 1, half = tid & 1;
+    const bool row_ok = row < nrows;
+    const int ci = row_ok ? (x.pos0 + row / G) / bs : 0;  // the row's own block
+    const __nv_bfloat16 *qrow = a.q + ((size_t)(x.row0 + row / G) * a.Hq + x.hk * G + row % G) * D;
     const bool scored = km1 > 0 && c_own > km1;
+    const int ss = km1 + 1;  // of a row's blocks in `sel`
     if (scored) {
         // this warp's 16 rows of q as MMA operands, and each row's norm
         uint32_t qa[KS][4];
@@ -160,10 +214,17 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
         }
         float q2 = 0.f;
         if (row_ok)
-            for (int d = 0; d < D; d += 2) {
-                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(qrow + d));
-                q2 = fmaf(f.x, f.x, fmaf(f.y, f.y, q2));
+#pragma unroll
+            for (int d = 0; d < D / 2; d += 8) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(qrow + half * (D / 2) + d));
+                const __nv_bfloat162 *p2 = reinterpret_cast<const __nv_bfloat162 *>(&u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = __bfloat1622float2(p2[i]);
+                    q2 = fmaf(f.x, f.x, fmaf(f.y, f.y, q2));
+                }
             }
+        q2 += __shfl_xor_sync(0xffffffffu, q2, 1);
         float ts[KCAP];
         int ti[KCAP];
 #pragma unroll
@@ -171,30 +232,39 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
             ts[i] = -INFINITY;
             ti[i] = sel::kEmpty;
         }
+        float worst = -INFINITY;
         const uint32_t s_hi = smem_u32(smem + L.hi), s_lo = smem_u32(smem + L.lo);
         for (int cb = 0; cb < c_own; cb += kTile) {
             // 64 pooled keys, four values a lane, split into hi + lo
             constexpr int LR = D / 4;  // lanes per pooled key
+            constexpr int NR = kTile / (kThreads / LR);
+            if (tid < kTile) {
+                const int page = cb + tid < c_own ? __ldg(table + (cb + tid + 1) * ppb - 1) : -1;
+                const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
+                s_page[tid] = ok ? page : -1;
+                if (cb + tid < c_own && !ok) s_bad = 1;
+            }
+            __syncthreads();
+            float4 f[NR];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int page = s_page[i * (kThreads / LR) + tid / LR];
+                f[i] = page < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                : __ldg(reinterpret_cast<const float4 *>(
+                                            a.kbar + ((size_t)page * a.c.Hkv + x.hk) * D) + tid % LR);
+            }
             float kn = 0.f;
-            for (int r = tid / LR; r < kTile; r += kThreads / LR) {
-                const int c = cb + r;
-                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c < c_own) {
-                    const int page = __ldg(table + (c + 1) * ppb - 1);
-                    if ((unsigned)page < (unsigned)a.c.num_pages)
-                        f = __ldg(reinterpret_cast<const float4 *>(
-                                      a.kbar + ((size_t)page * a.c.Hkv + x.hk) * D) + tid % LR);
-                    else
-                        s_bad = 1;
-                }
-                const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int r = i * (kThreads / LR) + tid / LR;
+                const float v[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
                 __nv_bfloat16 h[4], l[4];
                 float n2 = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[i] = __float2bfloat16(v[i]);
-                    l[i] = __float2bfloat16(v[i] - __bfloat162float(h[i]));
-                    n2 = fmaf(v[i], v[i], n2);
+                for (int k = 0; k < 4; ++k) {
+                    h[k] = __float2bfloat16(v[k]);
+                    l[k] = __float2bfloat16(v[k] - __bfloat162float(h[k]));
+                    n2 = fmaf(v[k], v[k], n2);
                 }
                 const uint32_t at = swz<D>(r, (tid % LR) >> 1) + (tid & 1) * 8;
                 *reinterpret_cast<uint2 *>(smem + L.hi + at) = *reinterpret_cast<uint2 *>(h);
@@ -236,24 +306,43 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
             }
             __syncthreads();
             if (row_ok) {
-                const int n = min(kTile, ci - cb);
-                for (int j = 0; j < n; ++j)
-                    sel::top_insert<KCAP>(ts, ti, km1 + 1, sc[tid * kScStride + j], cb + j);
+                const int n = min(kTile / 2 * (half + 1), ci - cb);
+                for (int k = kTile / 2 * half; k < n; ++k) {
+                    float y = sc[row * kScStride + k];
+                    if (y != y) y = -INFINITY;
+                    if (y > worst || ti[KCAP - 1] == sel::kEmpty) {
+                        sel::top_insert<KCAP>(ts, ti, KCAP, y, cb + k);
+                        worst = ts[KCAP - 1];
+                    }
+                }
             }
         }
-        if (row_ok && ci > km1) {
-            float kept = 0.f, dropped = 0.f;
+        // the other thread's list into the first one's
+#pragma unroll
+        for (int i = 0; i < KCAP; ++i) {
+            const float y = __shfl_xor_sync(0xffffffffu, ts[i], 1);
+            const int c = __shfl_xor_sync(0xffffffffu, ti[i], 1);
+            if (half == 0 && c != sel::kEmpty) merge_insert<KCAP>(ts, ti, y, c);
+        }
+        if (row_ok && half == 0 && ci > km1) {
+            float kept = 0.f, dropped = 0.f, next = 0.f;
+            bool none = false;  // there is no next one, or it is not held
 #pragma unroll
             for (int i = 0; i < KCAP; ++i) {
                 if (i == km1 - 1) kept = ts[i];
                 if (i == km1) dropped = ts[i];
-                if (i < km1) sel[tid * 32 + i] = ti[i];
+                if (i == km1 + 1) {
+                    next = ts[i];
+                    none = ti[i] == sel::kEmpty;
+                }
+                if (i <= km1) sel[row * ss + i] = ti[i];
             }
             const float err = sqrtf(q2) * fmaf(__int_as_float(s_knmax), 6.103515625e-5f, 1e-34f);
             if (!(kept - dropped > 2.f * err)) {
                 const int u = atomicAdd(&s_unsure, 1);
-                s_rows[u] = tid;
+                s_rows[u] = row;
                 s_floor[u] = kept - 3.f * err;
+                s_few[u] = km1 + 1 < KCAP && (none || next < kept - 2.f * err);
             }
         }
         __syncthreads();
@@ -263,19 +352,21 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
             const int r = s_rows[u];
             const int cr = (x.pos0 + r / G) / bs;
             const __nv_bfloat16 *qr = a.q + ((size_t)(x.row0 + r / G) * a.Hq + x.hk * G + r % G) * D;
-            int who = pick64<D>(a, x.hk, table, qr, cr, s_floor[u]);
+            int who = s_few[u] ? pick64_of<D>(a, x.hk, table, qr, sel + r * ss, min(ss, cr))
+                               : pick64<D>(a, x.hk, table, qr, cr, s_floor[u]);
             // should the bound not have left enough: from the lowest score on
             if (__any_sync(0xffffffffu, lane < km1 && who == sel::kEmpty))
                 who = pick64<D>(a, x.hk, table, qr, cr, -INFINITY);
-            if (lane < km1) sel[r * 32 + lane] = who;
+            __syncwarp();
+            if (lane < km1) sel[r * ss + lane] = who;
         }
         __syncthreads();
     }
     const bool bad = scored && s_bad;
     // each row's selection, ascending (a row with few past blocks takes them all)
-    if (row_ok) {
+    if (row_ok && half == 0) {
         const int n = min(km1, ci);
-        int *mine = sel + tid * 32;
+        int *mine = sel + row * ss;
         if (ci > km1) {
             for (int i = 1; i < n; ++i) {
                 const int v = mine[i];
@@ -291,7 +382,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
             if (!a.chunk) atomicOr(bits + (ci >> 5), 1u << (ci & 31));
         }
         if (a.idx) {
-            int32_t *dst = a.idx + ((size_t)(x.row0 + tid / G) * a.Hq + x.hk * G + tid % G) * a.topk;
+            int32_t *dst = a.idx + ((size_t)(x.row0 + row / G) * a.Hq + x.hk * G + row % G) * a.topk;
             for (int i = 0; i < a.topk; ++i) dst[i] = bad || i > n ? -1 : i < n ? mine[i] : ci;
         }
     }
@@ -325,12 +416,12 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
     const int count = s_count;
     for (int i = tid; i < count; i += kThreads) mask[i] = 0ull;
     __syncthreads();
-    if (row_ok) {
+    if (row_ok && half == 0) {
         const int n = min(km1, ci);
         for (int i = 0; i < n + (a.chunk ? 0 : 1); ++i) {
-            const int c = i < n ? sel[tid * 32 + i] : ci;
+            const int c = i < n ? sel[row * ss + i] : ci;
             const int at = rank[c >> 5] + __popc(bits[c >> 5] & ((1u << (c & 31)) - 1u));
-            atomicOr(mask + at, 1ull << tid);
+            atomicOr(mask + at, 1ull << row);
         }
     }
     __syncthreads();
@@ -373,7 +464,7 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(Attn a) {
 template <int D, int KCAP>
 cudaError_t launch(const Attn &a, cudaStream_t st) {
     const int words = (int)(((long long)a.c.max_pages * a.c.ps / a.c.bs) / 32 + 1);
-    const int bytes = (int)gate_smem(D, words, a.ucap).bytes;
+    const int bytes = (int)gate_smem(D, words, a.ucap, a.km1).bytes;
     const cudaError_t rc = cudaFuncSetAttribute(
         gate_kernel<D, KCAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (rc != cudaSuccess) return rc;
@@ -384,11 +475,10 @@ cudaError_t launch(const Attn &a, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_d(const Attn &a, cudaStream_t st) {
-    // one more than the kept ones: the first dropped score
-    if (a.km1 < 2) return launch<D, 2>(a, st);
-    if (a.km1 < 4) return launch<D, 4>(a, st);
-    if (a.km1 < 8) return launch<D, 8>(a, st);
-    if (a.km1 < 16) return launch<D, 16>(a, st);
+    // the kept ones, the first dropped one, and the next where there is room
+    if (a.km1 <= 2) return launch<D, 4>(a, st);
+    if (a.km1 <= 6) return launch<D, 8>(a, st);
+    if (a.km1 <= 14) return launch<D, 16>(a, st);
     return launch<D, 32>(a, st);
 }
 

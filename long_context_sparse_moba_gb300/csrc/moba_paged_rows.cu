@@ -12,57 +12,92 @@
 // equal runs, one per CTA, whatever the sequences' lengths; an entry that falls
 // into several runs leaves partial sums (at most two per CTA) that the merge
 // kernel joins.
-// Four warps: 16 * RW rows, 4 / RW warps side by side on a tile's keys, joined
-// through shared memory at the end of an entry.  Scores and outputs on
+// One warp brings the pages in by TMA, 128 KB or more in flight per SM: each of
+// its lanes looks up the pages of one of the next 32 tiles, then they issue in
+// turn.  CW warps attend: 16 rows each, RW of them side by side for the rows,
+// the KW = CW / RW sets of them taking the tiles of the run in turn (stages are a
+// multiple of KW, so a stage always belongs to the same set: a set that skipped
+// phases of a stage's barrier could take an old phase for its own); they join
+// through shared memory at the end of an entry's part.  Scores and outputs on
 // mma.sync; one pass with running maximum and sum in 32 bits; P is rounded to
 // bf16 for the second product, as the prefill kernels do.
+// Waits on mbarriers are bounded as in the other kernels; a warp that gives up
+// still joins the barrier of the part, where all warps agree to leave.
 #include "moba_mma.cuh"
 #include "moba_paged_attn.cuh"
+#include "moba_ptx.cuh"
 
 namespace moba {
 namespace paged {
 namespace {
 
-using namespace mma;
+using ptx::Ctl;
 
-constexpr int kThreads = 128;
-constexpr int kStages = 5;
+constexpr int kParts = 4;  // part descriptors in flight
 
-template <int D>
+struct Part {
+    int valid, e;
+    int n;            // tiles
+    int start, last;  // the part holds the entry's first, its last tile
+    int pad[3];
+};
+struct Info {         // of a tile, beside its stage
+    unsigned long long mask;
+    int key0, nv;     // first key, keys that some row sees
+    int bad, pad;
+};
+
+template <int D, int CW>
 struct RowsSmem {
-    static constexpr uint32_t kTileBytes = kTile * D * 2;         // K or V
-    static constexpr uint32_t kComb = kStages * 2 * kTileBytes;   // [64][D] fp32
-    static constexpr uint32_t kBytes = kComb + kMaxRows * D * 4;
+    static constexpr int NB = D / 64;
+    static constexpr int kStages = 4 * (128 / D);
+    static constexpr uint32_t kBox = kTile * 128;
+    static constexpr uint32_t kTileBytes = NB * kBox;                // K or V
+    static constexpr uint32_t kComb = kStages * 2 * kTileBytes;      // [CW * 16][D] fp32
+    static constexpr uint32_t kInfo = kComb + CW * 16 * D * 4;
+    static constexpr uint32_t kPart = kInfo + kStages * sizeof(Info);
+    static constexpr uint32_t kBars = kPart + kParts * sizeof(Part);  // full, empty, part full, part empty
+    static constexpr uint32_t kBytes = kBars + (2 * kStages + 2 * kParts) * 8 + 1024;
+    static_assert(kBytes + 2048 <= 227 * 1024, "shared memory per CTA");
 };
 
-// Where a run stands: tile i of entry e's T tiles.
-struct Cursor {
-    int e, i, T;
-    __device__ __forceinline__ void next(const Attn &a) {
-        if (++i < T) return;
-        i = 0;
-        do {
-            ++e;
-        } while (e < a.n_ent && (T = get_tiles(a, e)) == 0);
-    }
+struct RowsArgs {
+    Attn a;
+    int psh;  // log2(page size)
+    long long wait_limit;
 };
 
-template <int D, int RW>
-__global__ void __launch_bounds__(kThreads, 1) rows_kernel(Attn a) {
-    using S = RowsSmem<D>;
-    constexpr int KS = D / 16;
-    constexpr int KW = 4 / RW;         // warps along the keys
-    constexpr int KPW = kTile / KW;    // keys of a tile per warp
-    constexpr int ROWS = 16 * RW;
+template <int D, int RW, int CW>
+__global__ void __launch_bounds__(32 * (CW + 1), 1)
+    rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                const __grid_constant__ RowsArgs ra) {
+    using S = RowsSmem<D, CW>;
+    using mma::fast_exp2;
+    using mma::ldsm_x4;
+    using mma::ldsm_x4_t;
+    using mma::mma16816;
+    using mma::pack_bf16;
+    constexpr int KS = D / 16, KW = CW / RW, ST = S::kStages;
+    constexpr int kThreads = 32 * (CW + 1);
     constexpr int CH = D / 8;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_warp[4], s_base;
-    __shared__ int s_e0, s_bad[kStages];
-    __shared__ float s_m[kMaxRows], s_l[kMaxRows];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int cta = blockIdx.x;
-    const uint32_t s0 = smem_u32(smem);
+    const Attn &a = ra.a;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ long long s_warp[CW + 1], s_base;
+    __shared__ int s_e0, s_leave[CW], s_badw[CW];
+    __shared__ int s_abort;
+    __shared__ float s_m[CW * 16], s_l[CW * 16];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    const uint32_t raw = ptx::saddr(smem_raw);
+    const uint32_t s0 = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (s0 - raw);
     float *comb = reinterpret_cast<float *>(smem + S::kComb);
+    Info *info = reinterpret_cast<Info *>(smem + S::kInfo);
+    Part *parts = reinterpret_cast<Part *>(smem + S::kPart);
+    auto full = [&](int s) { return s0 + S::kBars + 8u * s; };
+    auto empty = [&](int s) { return s0 + S::kBars + 8u * (ST + s); };
+    auto pfull = [&](int s) { return s0 + S::kBars + 8u * (2 * ST + s); };
+    auto pempty = [&](int s) { return s0 + S::kBars + 8u * (2 * ST + kParts + s); };
+    Ctl ctl{&s_abort, a.status, ra.wait_limit};
 
     // ---- this CTA's run of the tiles of all entries ----
     const int per = (a.n_ent + kThreads - 1) / kThreads;
@@ -76,11 +111,22 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(Attn a) {
         if (lane >= o) inc += y;
     }
     if (lane == 31) s_warp[warp] = inc;
-    if (tid < kStages) s_bad[tid] = 0;
+    if (tid == 0) {
+        for (int s = 0; s < ST; ++s) {
+            ptx::mbar_init(full(s), 1);
+            ptx::mbar_init(empty(s), RW);
+        }
+        for (int s = 0; s < kParts; ++s) {
+            ptx::mbar_init(pfull(s), 1);
+            ptx::mbar_init(pempty(s), CW);
+        }
+        s_abort = 0;
+        ptx::fence_mbar_init();
+    }
     __syncthreads();
     long long before = inc - sum, total = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w <= CW; ++w) {
         if (w < warp) before += s_warp[w];
         total += s_warp[w];
     }
@@ -96,167 +142,271 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(Attn a) {
         s_base = p;
     }
     __syncthreads();
-    Cursor cur{s_e0, (int)(u0 - s_base), get_tiles(a, s_e0)};
-    Cursor ld = cur;
-    const int n = (int)(u1 - u0);
 
-    // first key and row mask of a tile
-    auto tile_of = [&](const Cursor &c, unsigned long long &mask) -> int {
-        if (a.dense) {
-            mask = ~0ull;
-            return c.i * kTile;
-        }
-        const int u = c.i / a.tpb;
-        mask = a.umask[(size_t)c.e * a.ucap + u];
-        return a.ublk[(size_t)c.e * a.ucap + u] * a.c.bs + (c.i - u * a.tpb) * kTile;
-    };
-    // copies of tile j of the run into its stage: keys behind the entry's last
-    // row are zeros, so that nothing unwritten meets the products
-    auto load = [&](int j) {
-        if (j < n) {
-            const Entry x = get_entry(a, ld.e);
-            unsigned long long mask;
-            const int key0 = tile_of(ld, mask), end = x.pos0 + x.nt;
-            const int *table = a.c.table + (size_t)x.b * a.c.max_pages;
-            const int st = j % kStages;
-            const uint32_t dk = s0 + st * 2 * S::kTileBytes, dv = dk + S::kTileBytes;
-#pragma unroll
-            for (int it = 0; it < kTile * CH / kThreads; ++it) {
-                const int r = (tid + it * kThreads) / CH, ch = tid % CH;
-                const int p = key0 + r;
-                bool ok = p < end;
-                size_t at = 0;
-                if (ok) {
-                    const int page = __ldg(table + p / a.c.ps);
-                    ok = (unsigned)page < (unsigned)a.c.num_pages;
-                    if (ok) at = (((size_t)page * a.c.Hkv + x.hk) * a.c.ps + p % a.c.ps) * D + ch * 8;
-                    else s_bad[st] = j + 1;
+    if (warp == CW) {
+        // ================= pages =================
+        const int n = (int)(u1 - u0), ps = a.c.ps, box = min(ps, kTile);
+        int e = s_e0, i = (int)(u0 - s_base);  // where the batch starts
+        int np = 0;                            // parts so far
+        bool go = true;
+        for (int t0 = 0; go && t0 < n; t0 += 32) {
+            // lane: tile t0 + lane of the run
+            const int t = t0 + lane;
+            int le = e, li = i + lane, T = 0;
+            if (t < n)
+                while (li >= (T = get_tiles(a, le))) {
+                    li -= T;
+                    ++le;
                 }
-                cp_async16(dk + swz<D>(r, ch), a.k + at, ok);
-                cp_async16(dv + swz<D>(r, ch), a.v + at, ok);
-            }
-            ld.next(a);
-        }
-        cp_async_commit();
-    };
+            Entry x;
+            Info f;
+            f.mask = ~0ull;
+            int pages[kTile / 16] = {0, 0, 0, 0};
+            f.bad = 0;
+            f.pad = 0;
+            f.key0 = f.nv = 0;
+            if (t < n) {
+                x = get_entry(a, le);
+                if (a.dense) {
+                    f.key0 = li * kTile;
+                } else {
+                    const int u = li / a.tpb;
+                    f.mask = a.umask[(size_t)le * a.ucap + u];
+                    f.key0 = a.ublk[(size_t)le * a.ucap + u] * a.c.bs + (li - u * a.tpb) * kTile;
+                }
+                f.nv = min(kTile, x.pos0 + x.nt - f.key0);
+                const int *table = a.c.table + (size_t)x.b * a.c.max_pages;
 #pragma unroll
-    for (int j = 0; j < kStages - 1; ++j) load(j);
+                for (int k = 0; k < kTile / 16; ++k)
+                    if (k * box < f.nv) {
+                        const int page = __ldg(table + ((f.key0 + k * box) >> ra.psh));
+                        const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
+                        f.bad |= !ok;
+                        // (some memory of the pool for a page outside it: its rows are dropped)
+                        pages[k] = ((ok ? page : 0) * a.c.Hkv + x.hk) * ps + ((f.key0 + k * box) & (ps - 1));
+                    }
+            }
+            const bool starts = t < n && (li == 0 || t == 0);
+            const unsigned ballot = __ballot_sync(0xffffffffu, starts);
+            const int pi = np + __popc(ballot & ((1u << lane) - 1u));
+            for (int k = 0; k < 32 && t0 + k < n; ++k) {
+                if (lane == k && go) {
+                    if (starts) {
+                        const int s = pi % kParts;
+                        if (pi >= kParts) go = ptx::wait_bar(pempty(s), (pi / kParts - 1) & 1, ctl);
+                        if (go) {
+                            Part p;
+                            p.valid = 1;
+                            p.e = le;
+                            p.n = min(T - li, n - t);
+                            p.start = li == 0;
+                            p.last = li + p.n == T;
+                            p.pad[0] = p.pad[1] = p.pad[2] = 0;
+                            parts[s] = p;
+                            ptx::mbar_arrive(pfull(s));
+                        }
+                    }
+                    const int st = t % ST;
+                    if (go && t >= ST) go = ptx::wait_bar(empty(st), (t / ST - 1) & 1, ctl);
+                    if (go) {
+                        info[st] = f;
+                        const int boxes = (f.nv + box - 1) / box;
+                        ptx::mbar_expect_tx(full(st), (uint32_t)(boxes * box) * 256u * S::NB);
+                        const uint32_t dk = s0 + st * 2 * S::kTileBytes;
+#pragma unroll
+                        for (int j = 0; j < kTile / 16; ++j)
+                            if (j < boxes) {
+#pragma unroll
+                                for (int v = 0; v < 2; ++v)
+#pragma unroll
+                                    for (int b = 0; b < S::NB; ++b)
+                                        asm volatile(
+                                            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::"
+                                            "complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                                                dk + v * S::kTileBytes + b * S::kBox +
+                                                (uint32_t)(j * box) * 128u),
+                                            "l"(reinterpret_cast<uint64_t>(v ? &tmap_v : &tmap_k)),
+                                            "r"(full(st)), "r"(b * 64), "r"(pages[j])
+                                            : "memory");
+                            }
+                    }
+                }
+                go = __shfl_sync(0xffffffffu, (int)go, k) != 0;
+            }
+            np += __popc(ballot);
+            // the tile behind the batch
+            const int last = min(31, n - 1 - t0);
+            e = __shfl_sync(0xffffffffu, le, last);
+            i = __shfl_sync(0xffffffffu, li, last) + 1;
+        }
+        if (go && lane == 0) {
+            const int s = np % kParts;
+            if (np < kParts || ptx::wait_bar(pempty(s), (np / kParts - 1) & 1, ctl)) {
+                parts[s].valid = 0;
+                ptx::mbar_arrive(pfull(s));
+            }
+        }
+        if (!go && lane == 0) {
+            // copies in flight land before the CTA ends: each stage's last phase
+            for (int s = 0; s < ST; ++s)
+                for (int ph = 0; ph < 2; ++ph) ptx::drain_bar(full(s), ph, ra.wait_limit / 8);
+        }
+        return;
+    }
 
+    // ================= attention =================
     const int rw = warp % RW, kw = warp / RW;
-    uint32_t qa[KS][4];
-    float o[D / 8][4], m[2], l[2];
-    int pos[2];
-    int start = cur.i;  // first tile of the entry in this run
-    bool bad = false, fresh = true;
-    Entry x;
-    for (int j = 0; j < n; ++j) {
-        cp_async_wait<kStages - 2>();
-        __syncthreads();
-        load(j + kStages - 1);
-        const int st = j % kStages;
-        bad |= s_bad[st] == j + 1;
-        if (fresh) {
-            fresh = false;
-            x = get_entry(a, cur.e);
-            start = cur.i;
+    const int row = rw * 16 + (lane >> 2);
+    int tbase = 0;
+    for (int np = 0;; ++np) {
+        const int s = np % kParts;
+        bool ok = __all_sync(0xffffffffu, ptx::wait_bar(pfull(s), (np / kParts) & 1, ctl));
+        Part part;
+        part.valid = 0;
+        if (ok) {
+            part = parts[s];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(pempty(s));
+        }
+        const bool leave = !ok || !part.valid;
+        uint32_t qa[KS][4];
+        float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        int pos[2] = {-1, -1};
+        bool bad = false;
+        Entry x;
+        x.nt = 0;
+        if (!leave) {
+            x = get_entry(a, part.e);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int r = rw * 16 + (lane >> 2) + 8 * h;
-                const bool ok = r < x.nt * a.G;
-                pos[h] = ok ? x.pos0 + r / a.G : -1;
+                const int r = row + 8 * h;
+                const bool live = r < x.nt * a.G;
+                pos[h] = live ? x.pos0 + r / a.G : -1;  // -1: no row, whose scores do not matter
                 const uint32_t *src = reinterpret_cast<const uint32_t *>(
                     a.q + ((size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G) * D) + (lane & 3);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    qa[ks][h] = ok ? __ldg(src + ks * 8) : 0u;
-                    qa[ks][h + 2] = ok ? __ldg(src + ks * 8 + 4) : 0u;
+                    qa[ks][h] = live ? __ldg(src + ks * 8) : 0u;
+                    qa[ks][h + 2] = live ? __ldg(src + ks * 8 + 4) : 0u;
                 }
-                m[h] = -INFINITY;
-                l[h] = 0.f;
             }
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
-        }
-        unsigned long long mask;
-        const int key0 = tile_of(cur, mask) + kw * KPW;
-        const uint32_t sk = s0 + st * 2 * S::kTileBytes, sv = sk + S::kTileBytes;
-        float s[KPW / 8][4];
+            static_assert(ST % KW == 0, "a stage belongs to one set of warps");
+            for (int t = tbase + (kw - tbase % KW + KW) % KW; t < tbase + part.n; t += KW) {
+                const int st = t % ST;
+                if (!__all_sync(0xffffffffu, ptx::wait_fast(full(st), (t / ST) & 1, ctl))) {
+                    ok = false;
+                    break;
+                }
+                const Info f = info[st];
+                const uint32_t sk = s0 + st * 2 * S::kTileBytes, sv = sk + S::kTileBytes;
+                bad |= f.bad != 0;
+                if (f.nv < kTile) {
+                    // keys that no row sees may never have been written: zeros in V
+                    for (int z = lane; z < (kTile - f.nv) * 8 * S::NB; z += 32) {
+                        const int b = z / ((kTile - f.nv) * 8), w = z % ((kTile - f.nv) * 8);
+                        ptx::st_shared_v4(sv + b * S::kBox + f.nv * 128 + w * 16, 0, 0, 0, 0);
+                    }
+                    ptx::fence_proxy_async();
+                    __syncwarp();
+                }
+                float sc[8][4];
 #pragma unroll
-        for (int i = 0; i < KPW / 8; ++i)
+                for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[i][k] = 0.f;
+                    for (int k = 0; k < 4; ++k) sc[j][k] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+                for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int np = 0; np < KPW / 16; ++np) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4(b0, b1, b2, b3,
-                        sk + swz<D>(kw * KPW + np * 16 + (lane & 7) + ((lane >> 4) << 3),
-                                    ks * 2 + ((lane >> 3) & 1)));
-                mma16816(s[2 * np], qa[ks], b0, b1);
-                mma16816(s[2 * np + 1], qa[ks], b2, b3);
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = j * 16 + (lane & 7) + ((lane >> 4) << 3);
+                        const int c = ks * 2 + ((lane >> 3) & 1);
+                        uint32_t b0, b1, b2, b3;
+                        ldsm_x4(b0, b1, b2, b3,
+                                sk + (c >> 3) * S::kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                        mma16816(sc[2 * j], qa[ks], b0, b1);
+                        mma16816(sc[2 * j + 1], qa[ks], b2, b3);
+                    }
+                // last key that each of the two rows sees
+                int see[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    see[h] = pos[h] < 0 ? 0x7fffffff : (f.mask >> (row + 8 * h)) & 1 ? pos[h] : -1;
+                float mx[2] = {-INFINITY, -INFINITY}, mu[2];
+                const bool open = f.key0 + kTile - 1 <= min(see[0], see[1]);
+                if (__all_sync(0xffffffffu, open)) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mx[k >> 1] = fmaxf(mx[k >> 1], sc[j][k]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int key = f.key0 + j * 8 + 2 * (lane & 3) + (k & 1);
+                            if (key > see[k >> 1]) sc[j][k] = -INFINITY;
+                            mx[k >> 1] = fmaxf(mx[k >> 1], sc[j][k]);
+                        }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * a.scale_log2;
+                }
+                if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float mn = fmaxf(m[h], mx[h]);
+                        const float r = fast_exp2(m[h] - (mn == -INFINITY ? 0.f : mn));
+                        m[h] = mn;
+                        l[h] *= r;
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j) {
+                            o[j][2 * h] *= r;
+                            o[j][2 * h + 1] *= r;
+                        }
+                    }
+                }
+                mu[0] = m[0] == -INFINITY ? 0.f : m[0];
+                mu[1] = m[1] == -INFINITY ? 0.f : m[1];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        sc[j][k] = fast_exp2(fmaf(sc[j][k], a.scale_log2, -mu[k >> 1]));
+                        l[k >> 1] += sc[j][k];
+                    }
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const uint32_t pa[4] = {pack_bf16(sc[2 * kk][0], sc[2 * kk][1]),
+                                            pack_bf16(sc[2 * kk][2], sc[2 * kk][3]),
+                                            pack_bf16(sc[2 * kk + 1][0], sc[2 * kk + 1][1]),
+                                            pack_bf16(sc[2 * kk + 1][2], sc[2 * kk + 1][3])};
+                    const int r = kk * 16 + (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+                    for (int dp = 0; dp < D / 16; ++dp) {
+                        const int c = dp * 2 + (lane >> 4);
+                        uint32_t b0, b1, b2, b3;
+                        ldsm_x4_t(b0, b1, b2, b3,
+                                  sv + (c >> 3) * S::kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                        mma16816(o[2 * dp], pa, b0, b1);
+                        mma16816(o[2 * dp + 1], pa, b2, b3);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(empty(st));
             }
-        float mx[2] = {-INFINITY, -INFINITY}, mu[2];
-        const int row = rw * 16 + (lane >> 2);
-        // last key that each of the two rows sees
-        const int see[2] = {(mask >> row) & 1 ? pos[0] : -1, (mask >> (row + 8)) & 1 ? pos[1] : -1};
-#pragma unroll
-        for (int i = 0; i < KPW / 8; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int key = key0 + i * 8 + 2 * (lane & 3) + (k & 1);
-                const float y = key > see[k >> 1] ? -INFINITY : s[i][k] * a.scale_log2;
-                s[i][k] = y;
-                mx[k >> 1] = fmaxf(mx[k >> 1], y);
-            }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-            const float mn = fmaxf(m[h], mx[h]);
-            mu[h] = mn == -INFINITY ? 0.f : mn;
-            const float f = fast_exp2(m[h] - mu[h]);
-            m[h] = mn;
-            l[h] *= f;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                o[i][2 * h] *= f;
-                o[i][2 * h + 1] *= f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < KPW / 8; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                s[i][k] = fast_exp2(s[i][k] - mu[k >> 1]);
-                l[k >> 1] += s[i][k];
-            }
-#pragma unroll
-        for (int kk = 0; kk < KPW / 16; ++kk) {
-            const uint32_t pa[4] = {pack_bf16(s[2 * kk][0], s[2 * kk][1]),
-                                    pack_bf16(s[2 * kk][2], s[2 * kk][3]),
-                                    pack_bf16(s[2 * kk + 1][0], s[2 * kk + 1][1]),
-                                    pack_bf16(s[2 * kk + 1][2], s[2 * kk + 1][3])};
-#pragma unroll
-            for (int dp = 0; dp < D / 16; ++dp) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4_t(b0, b1, b2, b3,
-                          sv + swz<D>(kw * KPW + kk * 16 + (lane & 7) + (((lane >> 3) & 1) << 3),
-                                      dp * 2 + (lane >> 4)));
-                mma16816(o[2 * dp], pa, b0, b1);
-                mma16816(o[2 * dp + 1], pa, b2, b3);
-            }
-        }
-        const bool end = cur.i == cur.T - 1;
-        if (end || j == n - 1) {
+            tbase += part.n;
             // ---- the entry's rows leave this run ----
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-                const int at = kw * ROWS + row + 8 * h;
+                const int at = warp * 16 + (lane >> 2) + 8 * h;
                 if ((lane & 3) == 0) {
                     s_m[at] = m[h];
                     s_l[at] = l[h];
@@ -266,60 +416,77 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(Attn a) {
                     *reinterpret_cast<float2 *>(comb + at * D + i * 8 + 2 * (lane & 3)) =
                         make_float2(o[i][2 * h], o[i][2 * h + 1]);
             }
-            bad = __syncthreads_or(bad);
-            const bool whole = end && start == 0;
-            const int slot = cta * 2 + (start == 0 ? 1 : 0);
-            if (tid == 0) {
-                if (start == 0) a.c_first[cur.e] = cta;
-                if (end) a.c_last[cur.e] = cta;
-                if (bad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-            }
-            for (int id = tid; id < x.nt * a.G * CH; id += kThreads) {
-                const int r = id / CH, d = id % CH * 8;
-                float M = -INFINITY, Lsum = 0.f, acc[8];
-#pragma unroll
-                for (int w = 0; w < KW; ++w) M = fmaxf(M, s_m[w * ROWS + r]);
-                const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-#pragma unroll
-                for (int w = 0; w < KW; ++w) {
-                    const float f = fast_exp2(s_m[w * ROWS + r] - ref);
-                    Lsum = fmaf(s_l[w * ROWS + r], f, Lsum);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        acc[k] = fmaf(comb[(w * ROWS + r) * D + d + k], f, acc[k]);
-                }
-                if (whole) {
-                    const size_t at = (size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G;
-                    const float inv = bad ? 0.f : 1.f / Lsum;
-                    uint4 w;
-                    uint32_t *pw = reinterpret_cast<uint32_t *>(&w);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        pw[k] = bad ? 0u : pack_bf16(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-                    *reinterpret_cast<uint4 *>(a.out + at * D + d) = w;
-                    if (d == 0)
-                        a.lse[at] = bad ? -INFINITY : (M + log2f(Lsum)) * 0.69314718055994530942f;
-                } else {
-                    float *dst = a.part_o + ((size_t)slot * ROWS + r) * D + d;
-                    *reinterpret_cast<float4 *>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                    *reinterpret_cast<float4 *>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
-                    if (d == 0) a.part_ml[(size_t)slot * ROWS + r] = make_float2(M, bad ? -1.f : Lsum);
-                }
-            }
-            bad = false;
-            fresh = true;
         }
-        cur.next(a);
+        if (lane == 0) {
+            s_leave[warp] = leave || !ok;
+            s_badw[warp] = bad;
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * CW) : "memory");
+        bool out = false;
+        bad = false;
+#pragma unroll
+        for (int w = 0; w < CW; ++w) {
+            out |= s_leave[w] != 0;
+            bad |= s_badw[w] != 0;
+        }
+        if (out) break;  // every warp of the attention alike
+        const bool whole = part.start && part.last;
+        const int slot = cta * 2 + (part.start ? 1 : 0);
+        if (tid == 0) {
+            if (part.start) a.c_first[part.e] = cta;
+            if (part.last) a.c_last[part.e] = cta;
+            if (bad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+        }
+        for (int id = tid; id < x.nt * a.G * CH; id += 32 * CW) {
+            const int r = id / CH, d = id % CH * 8;
+            float M = -INFINITY, Lsum = 0.f, acc[8];
+#pragma unroll
+            for (int w = 0; w < KW; ++w) M = fmaxf(M, s_m[(w * RW + r / 16) * 16 + r % 16]);
+            const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+                const int at = (w * RW + r / 16) * 16 + r % 16;
+                const float f = fast_exp2(s_m[at] - ref);
+                Lsum = fmaf(s_l[at], f, Lsum);
+#pragma unroll
+                for (int k = 0; k < 8; k += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(comb + at * D + d + k);
+                    acc[k] = fmaf(v.x, f, acc[k]);
+                    acc[k + 1] = fmaf(v.y, f, acc[k + 1]);
+                    acc[k + 2] = fmaf(v.z, f, acc[k + 2]);
+                    acc[k + 3] = fmaf(v.w, f, acc[k + 3]);
+                }
+            }
+            if (whole) {
+                const size_t at = (size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G;
+                const float inv = 1.f / Lsum;
+                uint4 w;
+                uint32_t *pw = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    pw[k] = bad ? 0u : pack_bf16(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+                *reinterpret_cast<uint4 *>(a.out + at * D + d) = w;
+                if (d == 0)
+                    a.lse[at] = bad ? -INFINITY : (M + log2f(Lsum)) * 0.69314718055994530942f;
+            } else {
+                float *dst = a.part_o + ((size_t)slot * a.rows + r) * D + d;
+                *reinterpret_cast<float4 *>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                *reinterpret_cast<float4 *>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+                if (d == 0) a.part_ml[(size_t)slot * a.rows + r] = make_float2(M, bad ? -1.f : Lsum);
+            }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * CW) : "memory");  // before the next part's sums
     }
-    cp_async_wait<0>();
 }
+
+constexpr int kMergeThreads = 128;
 
 // Joins the partial sums of the entries that several CTAs worked on, and clears
 // the rows of refused sequences.  A warp per row.
 template <int D>
-__global__ void __launch_bounds__(kThreads) merge_kernel(Attn a) {
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(Attn a) {
     const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Entry x = get_entry(a, e);
     if (x.state == kSeqEmpty) return;
@@ -332,7 +499,7 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(Attn a) {
         last = a.c_last[e];
         if (first == last) return;  // written by that CTA
     }
-    for (int r = warp; r < nrows; r += kThreads / 32) {
+    for (int r = warp; r < nrows; r += kMergeThreads / 32) {
         const size_t at = (size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G;
         float M = -INFINITY, L = 0.f;
         bool bad = none;
@@ -353,7 +520,7 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(Attn a) {
             for (int c = first; c <= last; ++c) {
                 const size_t p = (size_t)(2 * c + (c == first)) * a.rows + r;
                 const float2 ml = a.part_ml[p];
-                const float f = fast_exp2(ml.x - ref);
+                const float f = mma::fast_exp2(ml.x - ref);
                 L = fmaf(ml.y, f, L);
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)
@@ -363,28 +530,39 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(Attn a) {
 #pragma unroll
         for (int k = 0; k < D / 32; k += 2)
             *reinterpret_cast<uint32_t *>(a.out + at * D + lane * (D / 32) + k) =
-                bad ? 0u : pack_bf16(acc[k] * inv, acc[k + 1] * inv);
+                bad ? 0u : mma::pack_bf16(acc[k] * inv, acc[k + 1] * inv);
         if (lane == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
     }
 }
 
-template <int D, int RW>
+template <int D, int RW, int CW>
 cudaError_t launch(const Attn &a, cudaStream_t st) {
-    const int bytes = (int)RowsSmem<D>::kBytes;
-    cudaError_t rc = cudaFuncSetAttribute(rows_kernel<D, RW>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    CUtensorMap mk, mv;
+    const long long rows = (long long)a.c.num_pages * a.c.Hkv * a.c.ps;
+    const int box = a.c.ps < kTile ? a.c.ps : kTile;
+    if (!make_tma_rows(&mk, a.k, rows, D, box) || !make_tma_rows(&mv, a.v, rows, D, box))
+        return cudaErrorInvalidValue;
+    const int bytes = (int)RowsSmem<D, CW>::kBytes;
+    auto kern = rows_kernel<D, RW, CW>;
+    cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (rc != cudaSuccess) return rc;
-    rows_kernel<D, RW><<<a.ctas, kThreads, bytes, st>>>(a);
+    RowsArgs ra;
+    ra.a = a;
+    ra.psh = __builtin_ctz((unsigned)a.c.ps);
+    ra.wait_limit = kDefaultWaitLimit;
+    kern<<<a.ctas, 32 * (CW + 1), bytes, st>>>(mk, mv, ra);
     rc = cudaGetLastError();
     if (rc != cudaSuccess) return rc;
-    merge_kernel<D><<<a.n_ent, kThreads, 0, st>>>(a);
+    merge_kernel<D><<<a.n_ent, kMergeThreads, 0, st>>>(a);
     note_launches(2);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(const Attn &a, cudaStream_t st) {
-    return a.rows == 16 ? launch<D, 1>(a, st) : a.rows == 32 ? launch<D, 2>(a, st) : launch<D, 4>(a, st);
+    return a.rows == 16   ? launch<D, 1, 4>(a, st)
+           : a.rows == 32 ? launch<D, 2, 4>(a, st)
+                          : launch<D, 4, 8>(a, st);
 }
 
 }  // namespace

@@ -315,3 +315,12 @@ def test_bad_sequences_in_long_chunks(topk):
     got = ops.paged_attn(q, c.k, c.v, c.kbar, c.table, i32(cu), i32(lens), 400, 64, topk, with_idx=True)
     assert ops.get_status() == ops.MOBA_OK
     compare(got, want)
+
+
+@pytest.mark.parametrize("topk", [3, 1000])
+@pytest.mark.parametrize("n,hq,hkv,d,page,block", [(1, 8, 8, 128, 64, 512), (1, 16, 8, 64, 16, 64),
+                                                   (4, 32, 4, 128, 32, 128), (8, 24, 4, 64, 64, 128)])
+def test_steps_over_long_caches(n, hq, hkv, d, page, block, topk):
+    """Many key tiles to each of the GPU's SMs."""
+    lens = [20000, 15001, 9000, 17, 12345, 19999]
+    case([min(n, x) for x in lens], lens, hq, hkv, d, page, block, topk, seed=n + topk, with_idx=topk < 100)
