@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
         comp[e] = 0.f;
     }
     bool bad = false;
-    constexpr int U = 4;
+    constexpr int U = 8;
     for (int pb = t0 - (t0 - p0) % G + g; pb < c1; pb += U * G) {
         uint4 x[U];
         __nv_bfloat16 *dst[U];

@@ -1,6 +1,8 @@
 // moba_paged.cuh -- the paged cache as its kernels see it.
 #pragma once
 
+#include <atomic>
+
 #include "moba.h"
 #include "moba_internal.cuh"
 
@@ -41,6 +43,47 @@ struct Cache {
         return kSeqBad;
     }
 };
+
+// A kernel that follows another one of the same call: its CTAs may start while
+// that one drains, and each begins with after_previous(), which waits for all of
+// its results.  Every CTA of every kernel in such a row has to make that wait, so
+// that a kernel's end implies the end of all before it.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                         const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// the next kernel's CTAs may be brought in as this one's leave
+__device__ __forceinline__ void let_next() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The dynamic shared memory limit of kernel K, raised once per device.
+template <auto K>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t rc = cudaGetDevice(&dev);
+    if (rc != cudaSuccess) return rc;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    rc = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (rc == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return rc;
+}
 
 // Host checks shared by the entry points; fills c.
 int make_cache(Cache *c, const void *k_pages, const void *v_pages, const float *kbar_pages,

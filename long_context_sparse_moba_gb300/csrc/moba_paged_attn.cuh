@@ -38,7 +38,8 @@ struct Attn {
     int *tiles;                 // [n_ent]
     int *ublk;                  // [n_ent][ucap] blocks that some row of the entry selected, ascending
     unsigned long long *umask;  // [n_ent][ucap] which rows did
-    int *c_first, *c_last;      // [n_ent] first and last CTA that worked on the entry
+    int *c_open;                // [ctas] the entry that starts in the CTA's run and ends in another's, or -1
+    int *c_last;                // [n_ent] the CTA in whose run the entry ends
     float *part_o;              // [ctas][2][rows][D] partial sums of exp2(s - m) v
     float2 *part_ml;            // [ctas][2][rows] their m and sum of exp2(s - m); a sum below 0: bad page
     // ---- chunks of many rows (the tcgen05 kernel): jobs of up to 256 rows ----
@@ -91,10 +92,13 @@ __device__ __forceinline__ int get_tiles(const Attn &a, int e) {
 }
 
 cudaError_t launch_gate(const Attn &a, cudaStream_t st);
-cudaError_t launch_rows(const Attn &a, cudaStream_t st);
+// (after_gate: a kernel of this call is before it)
+cudaError_t launch_rows(const Attn &a, bool after_gate, cudaStream_t st);
 // chunks of many rows: row tiles, lists and jobs; then the attention and the merge
-cudaError_t launch_plan(const Attn &a, cudaStream_t st);
+cudaError_t launch_plan(const Attn &a, bool after_gate, cudaStream_t st);
 cudaError_t launch_chunk(const Attn &a, cudaStream_t st);
+// joins the partial sums of entries (row tiles of chunks) that fell into several runs
+cudaError_t launch_merge_runs(const Attn &a, cudaStream_t st);
 
 }  // namespace paged
 }  // namespace moba

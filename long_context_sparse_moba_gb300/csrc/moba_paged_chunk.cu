@@ -160,6 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *bad_job = reinterpret_cast<volatile int *>(gmisc + L::kBad);
     Job *ring = reinterpret_cast<Job *>(gmisc + L::kJob);
     Ctl ctl{abort_flag, a.status, ca.wait_limit};
+    after_previous();
+    let_next();
 
     if (tid == 0) {
         for (int g = 0; g < kG; ++g) {
@@ -213,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Seq sq;
             const int tiles = __ldg(a.own_off + a.c.num_seqs);
             if (DENSE) {
+                int open = -1;
                 const long long total = a.unit_off[tiles];
                 const long long runs = total < (long long)gridDim.x ? total : (long long)gridDim.x;
                 if ((long long)blockIdx.x < runs) {
@@ -236,15 +239,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             J.whole = J.nt == T;
                             J.slot = blockIdx.x * 2 + (J.lo == 0 ? 1 : 0);
                             job_ends<N>(a, J);
-                            const size_t e = (size_t)w * a.c.Hkv + J.hk;
-                            if (J.lo == 0) a.c_first[e] = blockIdx.x;
+                            const int e = w * a.c.Hkv + J.hk;
                             if (J.lo + J.nt == T) a.c_last[e] = blockIdx.x;
+                            else if (J.lo == 0) open = e;
                             go = hand(J);
                             u += J.nt;
                         }
                         ++w;
                     }
                 }
+                a.c_open[blockIdx.x] = open;
             } else {
                 const int listed = a.km1 > 0 ? *a.n_jobs : 0;
                 const long long all = listed + (long long)tiles * a.c.Hkv;
@@ -765,6 +769,8 @@ __device__ __forceinline__ long long block_scan(long long v, long long *warps, l
 template <int N>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
     __shared__ long long warps[kPlanThreads / 32];
+    after_previous();
+    let_next();
     const int tid = threadIdx.x;
     long long total;
     // 256-row tiles of each sequence; refused ones have none, and clear rows
@@ -850,6 +856,8 @@ constexpr int kScatterThreads = 128;
 __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(Attn a) {
     extern __shared__ unsigned long long s_mask[];  // [ucap], then where each block's rows go, [ucap]
     int *s_at = reinterpret_cast<int *>(s_mask + a.ucap);
+    after_previous();
+    let_next();
     const int e = blockIdx.x, r = threadIdx.x;
     const int n = a.tiles[e] - 1;
     if (n <= 0) return;
@@ -874,7 +882,7 @@ __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(Attn a) {
 }
 
 // ----------------------------------------------------------------------------
-// merges
+// merge
 // ----------------------------------------------------------------------------
 // A row's slots (its past blocks and its own), weighted by their sums, the
 // weights taken relative to a running maximum: D / 8 lanes a row, 16 bytes of
@@ -884,6 +892,7 @@ constexpr int kSlotThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kSlotThreads) merge_slots_kernel(Attn a) {
     constexpr int GL = D / 8, U = 4;
+    after_previous();
     const int e = blockIdx.x, gl = threadIdx.x % GL;
     const Entry x = get_entry(a, e);
     if (x.state != kSeqOk) return;  // cleared before
@@ -946,56 +955,6 @@ __global__ void __launch_bounds__(kSlotThreads) merge_slots_kernel(Attn a) {
     }
 }
 
-// The fp32 partial sums of row tiles that several CTAs worked on.
-template <int D>
-__global__ void __launch_bounds__(128) merge_runs_kernel(Attn a) {
-    constexpr int V = D / 32;
-    const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w = e / a.c.Hkv, hk = e % a.c.Hkv;
-    if (w >= a.own_off[a.c.num_seqs]) return;
-    const int first = a.c_first[e], last = a.c_last[e];
-    if (first == last) return;
-    const int b = upper_index(a.own_off, a.c.num_seqs, w);
-    Seq s;
-    a.c.seq(b, s);
-    const int r0 = (w - a.own_off[b]) * kJobRows, nrows = min(kJobRows, s.n * a.G - r0);
-    for (int r = blockIdx.y * 4 + warp; r < nrows; r += gridDim.y * 4) {
-        const int row = s.row0 * a.G + r0 + r;
-        const size_t at = (size_t)(row / a.G) * a.Hq + hk * a.G + row % a.G;
-        float M = -INFINITY;
-        bool bad = false;
-        for (int c = first + lane; c <= last; c += 32) {
-            const float2 ml = a.part_ml[(size_t)(2 * c + (c == first)) * kJobRows + r];
-            bad |= ml.y < 0.f;
-            M = fmaxf(M, ml.x);
-        }
-        bad = __any_sync(0xffffffffu, bad);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float acc[V], sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = 0.f;
-        if (!bad)
-            for (int c = first; c <= last; ++c) {
-                const size_t p = (size_t)(2 * c + (c == first)) * kJobRows + r;
-                const float2 ml = a.part_ml[p];
-                if (ml.y == 0.f) continue;
-                const float f = fast_exp2(ml.x - M);
-                sum = fmaf(ml.y, f, sum);
-#pragma unroll
-                for (int k = 0; k < V; ++k) acc[k] = fmaf(a.part_o[p * D + lane * V + k], f, acc[k]);
-            }
-        const float inv = 1.f / sum;
-#pragma unroll
-        for (int k = 0; k < V; k += 2) {
-            __nv_bfloat162 bb = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
-            *reinterpret_cast<uint32_t *>(a.out + at * D + lane * V + k) =
-                bad ? 0u : *reinterpret_cast<uint32_t *>(&bb);
-        }
-        if (lane == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(sum)) * 0.69314718055994530942f;
-    }
-}
-
 // ----------------------------------------------------------------------------
 // host side
 // ----------------------------------------------------------------------------
@@ -1007,29 +966,27 @@ cudaError_t launch(const Attn &a, cudaStream_t st) {
     if (!make_tma_rows(&mk, a.k, rows, D, box) || !make_tma_rows(&mv, a.v, rows, D, box))
         return cudaErrorInvalidValue;
     const int bytes = (int)Smem<D, N>::kRequest;
-    auto kern = chunk_kernel<D, N, DENSE>;
     // every warp role must be resident: refuse a build whose registers do not allow it
     static std::atomic<int> fits{0};
     if (fits.load(std::memory_order_relaxed) == 0) {
         cudaFuncAttributes fa;
-        const cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+        const cudaError_t e = cudaFuncGetAttributes(&fa, chunk_kernel<D, N, DENSE>);
         if (e != cudaSuccess) return e;
         fits.store(fa.maxThreadsPerBlock >= kThreads ? 1 : -1, std::memory_order_relaxed);
     }
     if (fits.load(std::memory_order_relaxed) < 0) return cudaErrorInvalidConfiguration;
-    cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t rc = allow_smem<chunk_kernel<D, N, DENSE>>(bytes);
     if (rc != cudaSuccess) return rc;
     ChunkArgs ca;
     ca.a = a;
     ca.psh = __builtin_ctz((unsigned)a.c.ps);
     ca.wait_limit = kDefaultWaitLimit;
-    kern<<<a.ctas, kThreads, bytes, st>>>(mk, mv, ca);
-    rc = cudaGetLastError();
+    rc = launch_after(chunk_kernel<D, N, DENSE>, a.ctas, kThreads, bytes, st, mk, mv, ca);
+    note_launches(1);
     if (rc != cudaSuccess) return rc;
-    if (DENSE) merge_runs_kernel<D><<<dim3(a.w_cap * a.c.Hkv, 16), 128, 0, st>>>(a);
-    else merge_slots_kernel<D><<<a.n_ent, kSlotThreads, 0, st>>>(a);
-    note_launches(2);
-    return cudaGetLastError();
+    if (DENSE) return launch_merge_runs(a, st);
+    note_launches(1);
+    return launch_after(merge_slots_kernel<D>, a.n_ent, kSlotThreads, 0, st, a);
 }
 
 // keys per tile: 128, or 64 where blocks are no multiple of 128
@@ -1037,15 +994,19 @@ bool wide(const Attn &a) { return a.dense || a.c.bs % 128 == 0; }
 
 }  // namespace
 
-cudaError_t launch_plan(const Attn &a, cudaStream_t st) {
-    if (wide(a)) plan_kernel<128><<<1, kPlanThreads, 0, st>>>(a);
-    else plan_kernel<64><<<1, kPlanThreads, 0, st>>>(a);
-    cudaError_t rc = cudaGetLastError();
+cudaError_t launch_plan(const Attn &a, bool after_gate, cudaStream_t st) {
+    cudaError_t rc;
+    const auto plan = wide(a) ? plan_kernel<128> : plan_kernel<64>;
+    if (after_gate) {
+        rc = launch_after(plan, 1, kPlanThreads, 0, st, a);
+    } else {
+        plan<<<1, kPlanThreads, 0, st>>>(a);
+        rc = cudaGetLastError();
+    }
     note_launches(1);
     if (rc != cudaSuccess || a.km1 == 0) return rc;
-    scatter_kernel<<<a.n_ent, kScatterThreads, 12 * a.ucap, st>>>(a);
     note_launches(1);
-    return cudaGetLastError();
+    return launch_after(scatter_kernel, a.n_ent, kScatterThreads, 12 * (size_t)a.ucap, st, a);
 }
 
 cudaError_t launch_chunk(const Attn &a, cudaStream_t st) {

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_bad, s_knmax, s_unsure, s_count, s_rows[kMaxRows], s_few[kMaxRows], s_page[kTile];
     __shared__ float s_floor[kMaxRows];
+    let_next();
     const GateSmem L = gate_smem(D, words, a.ucap, a.km1);
     float *sc = reinterpret_cast<float *>(smem + L.sc);
     int *sel = reinterpret_cast<int *>(smem + L.sel);  // [row][km1 + 1]
@@ -450,6 +451,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
 
 // The selection where topk covers every block: all of them.
 __global__ void __launch_bounds__(kThreads) fill_kernel(Attn a) {
+    let_next();
     const Entry x = get_entry(a, blockIdx.x);
     if (x.state == kSeqEmpty) return;
     const long long n = (long long)x.nt * a.G * a.topk;
@@ -465,8 +467,9 @@ template <int D, int KCAP>
 cudaError_t launch(const Attn &a, cudaStream_t st) {
     const int words = (int)(((long long)a.c.max_pages * a.c.ps / a.c.bs) / 32 + 1);
     const int bytes = (int)gate_smem(D, words, a.ucap, a.km1).bytes;
-    const cudaError_t rc = cudaFuncSetAttribute(
-        gate_kernel<D, KCAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    constexpr int kMost = kMaxRows * (kMaxPastSlots + 1);
+    const cudaError_t rc = allow_smem<gate_kernel<D, KCAP>>(
+        (int)gate_smem(D, kMaxBlocks / 32 + 1, kMost, kMaxPastSlots).bytes);
     if (rc != cudaSuccess) return rc;
     gate_kernel<D, KCAP><<<a.n_ent, kThreads, bytes, st>>>(a, words);
     note_launches(1);

@@ -67,6 +67,21 @@ struct RowsArgs {
     long long wait_limit;
 };
 
+// The rows of an entry without tiles: of a refused sequence, or one whose
+// selection met a page outside the pool.
+template <int D>
+__device__ __noinline__ void clear_entry(const Attn &a, int e) {
+    const Entry x = get_entry(a, e);
+    if (x.state == kSeqEmpty) return;
+    if (x.state == kSeqBad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+    for (int r = 0; r < x.nt * a.G; ++r) {
+        const size_t at = (size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G;
+        a.lse[at] = -INFINITY;
+        for (int d = 0; d < D; d += 8)
+            *reinterpret_cast<uint4 *>(a.out + at * D + d) = make_uint4(0, 0, 0, 0);
+    }
+}
+
 template <int D, int RW, int CW>
 __global__ void __launch_bounds__(32 * (CW + 1), 1)
     rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -103,7 +118,13 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
     const int per = (a.n_ent + kThreads - 1) / kThreads;
     const int lo = min(tid * per, a.n_ent), hi = min(lo + per, a.n_ent);
     long long sum = 0;
-    for (int e = lo; e < hi; ++e) sum += get_tiles(a, e);
+    after_previous();
+    let_next();
+    for (int e = lo; e < hi; ++e) {
+        const int T = get_tiles(a, e);
+        sum += T;
+        if (T == 0 && e % (int)gridDim.x == cta) clear_entry<D>(a, e);
+    }
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -132,7 +153,10 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
     }
     // at least one tile each, so that an entry's runs are those of adjacent CTAs
     const long long runs = total < (long long)gridDim.x ? total : (long long)gridDim.x;
-    if (cta >= runs) return;
+    if (cta >= runs) {
+        if (tid == 0) a.c_open[cta] = -1;
+        return;
+    }
     const long long u0 = total * cta / runs, u1 = total * (cta + 1) / runs;
     if (u0 >= before && u0 < before + sum) {
         int e = lo;
@@ -257,7 +281,7 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
     // ================= attention =================
     const int rw = warp % RW, kw = warp / RW;
     const int row = rw * 16 + (lane >> 2);
-    int tbase = 0;
+    int tbase = 0, open = -1;
     for (int np = 0;; ++np) {
         const int s = np % kParts;
         bool ok = __all_sync(0xffffffffu, ptx::wait_bar(pfull(s), (np / kParts) & 1, ctl));
@@ -433,7 +457,7 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
         const bool whole = part.start && part.last;
         const int slot = cta * 2 + (part.start ? 1 : 0);
         if (tid == 0) {
-            if (part.start) a.c_first[part.e] = cta;
+            if (part.start && !part.last) open = part.e;
             if (part.last) a.c_last[part.e] = cta;
             if (bad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
         }
@@ -479,96 +503,148 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * CW) : "memory");  // before the next part's sums
     }
+    if (tid == 0) a.c_open[cta] = open;
 }
 
-constexpr int kMergeThreads = 128;
+// Joins the partial sums of an entry (a row tile of a chunk) that starts in one
+// CTA's run and ends in another's.  Four rows to a CTA, four warps to a row:
+// each takes every fourth part, four in flight, and they join in shared memory.
+constexpr int kMergeThreads = 512;
 
-// Joins the partial sums of the entries that several CTAs worked on, and clears
-// the rows of refused sequences.  A warp per row.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(Attn a) {
-    const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Entry x = get_entry(a, e);
-    if (x.state == kSeqEmpty) return;
-    const int nrows = x.nt * a.G;
-    const bool none = x.state == kSeqBad || get_tiles(a, e) == 0;
-    if (x.state == kSeqBad && threadIdx.x == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-    int first = 0, last = 0;
-    if (!none) {
-        first = a.c_first[e];
-        last = a.c_last[e];
-        if (first == last) return;  // written by that CTA
+template <int D, bool CHUNK>
+__global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(Attn a) {
+    constexpr int V = D / 32, U = 4;
+    __shared__ float s_acc[16][D], s_m[16], s_l[16];
+    after_previous();
+    const int first = blockIdx.x, e = a.c_open[first];
+    if (e < 0) return;
+    const int last = min(a.c_last[e], (int)gridDim.x - 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp & 3;
+    const int r = blockIdx.y * 4 + (warp >> 2), R = CHUNK ? kJobRows : a.rows;
+    bool live;
+    size_t at;
+    if (CHUNK) {
+        const int w = e / a.c.Hkv, b = upper_index(a.own_off, a.c.num_seqs, w);
+        Seq s;
+        a.c.seq(b, s);
+        const int r0 = (w - a.own_off[b]) * kJobRows + r, row = s.row0 * a.G + r0;
+        live = r0 < s.n * a.G;
+        at = (size_t)(row / a.G) * a.Hq + e % a.c.Hkv * a.G + row % a.G;
+    } else {
+        const Entry x = get_entry(a, e);
+        live = r < x.nt * a.G;
+        at = (size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G;
     }
-    for (int r = warp; r < nrows; r += kMergeThreads / 32) {
-        const size_t at = (size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G;
-        float M = -INFINITY, L = 0.f;
-        bool bad = none;
-        if (!none)
-            for (int c = first + lane; c <= last; c += 32) {
-                const float2 ml = a.part_ml[(size_t)(2 * c + (c == first)) * a.rows + r];
-                bad |= ml.y < 0.f;
-                M = fmaxf(M, ml.x);
+    float M = -INFINITY, L = 0.f, acc[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+    bool bad = false;
+    if (live)
+        for (int c0 = first + part; c0 <= last; c0 += 4 * U) {
+            float2 ml[U];
+            float v[U][V];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int c = c0 + 4 * j;
+                ml[j] = make_float2(-INFINITY, 0.f);
+                if (c <= last) {
+                    const size_t p = (size_t)(2 * c + (c == first)) * R + r;
+                    ml[j] = a.part_ml[p];
+#pragma unroll
+                    for (int k = 0; k < V; k += 2)
+                        *reinterpret_cast<float2 *>(&v[j][k]) =
+                            *reinterpret_cast<const float2 *>(a.part_o + p * D + lane * V + k);
+                }
             }
-        bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float ref = M == -INFINITY ? 0.f : M;
-        float acc[D / 32];
+            for (int j = 0; j < U; ++j) {
+                bad |= ml[j].y < 0.f;
+                if (ml[j].y == 0.f) continue;  // no part, or one without a key for this row
+                const float mn = fmaxf(M, ml[j].x), ref = mn == -INFINITY ? 0.f : mn;
+                const float f = mma::fast_exp2(M - ref), g = mma::fast_exp2(ml[j].x - ref);
+                M = mn;
+                L = fmaf(ml[j].y, g, L * f);
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
-        if (!bad)
-            for (int c = first; c <= last; ++c) {
-                const size_t p = (size_t)(2 * c + (c == first)) * a.rows + r;
-                const float2 ml = a.part_ml[p];
-                const float f = mma::fast_exp2(ml.x - ref);
-                L = fmaf(ml.y, f, L);
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k)
-                    acc[k] = fmaf(a.part_o[p * D + lane * (D / 32) + k], f, acc[k]);
+                for (int k = 0; k < V; ++k) acc[k] = fmaf(v[j][k], g, acc[k] * f);
             }
-        const float inv = 1.f / L;
+        }
 #pragma unroll
-        for (int k = 0; k < D / 32; k += 2)
-            *reinterpret_cast<uint32_t *>(a.out + at * D + lane * (D / 32) + k) =
-                bad ? 0u : mma::pack_bf16(acc[k] * inv, acc[k + 1] * inv);
-        if (lane == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+    for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
+    if (lane == 0) {
+        s_m[warp] = M;
+        s_l[warp] = bad ? -1.f : L;
     }
+    __syncthreads();
+    if (!live || part) return;
+    M = -INFINITY;
+    L = 0.f;
+    bad = false;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        M = fmaxf(M, s_m[warp + w]);
+        bad |= s_l[warp + w] < 0.f;
+    }
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = mma::fast_exp2(s_m[warp + w] - ref);
+        L = fmaf(s_l[warp + w], f, L);
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(s_acc[warp + w][lane * V + k], f, acc[k]);
+    }
+    const float inv = 1.f / L;
+#pragma unroll
+    for (int k = 0; k < V; k += 2)
+        *reinterpret_cast<uint32_t *>(a.out + at * D + lane * V + k) =
+            bad ? 0u : mma::pack_bf16(acc[k] * inv, acc[k + 1] * inv);
+    if (lane == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
 }
 
 template <int D, int RW, int CW>
-cudaError_t launch(const Attn &a, cudaStream_t st) {
+cudaError_t launch(const Attn &a, bool after_gate, cudaStream_t st) {
     CUtensorMap mk, mv;
     const long long rows = (long long)a.c.num_pages * a.c.Hkv * a.c.ps;
     const int box = a.c.ps < kTile ? a.c.ps : kTile;
     if (!make_tma_rows(&mk, a.k, rows, D, box) || !make_tma_rows(&mv, a.v, rows, D, box))
         return cudaErrorInvalidValue;
     const int bytes = (int)RowsSmem<D, CW>::kBytes;
-    auto kern = rows_kernel<D, RW, CW>;
-    cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t rc = allow_smem<rows_kernel<D, RW, CW>>(bytes);
     if (rc != cudaSuccess) return rc;
     RowsArgs ra;
     ra.a = a;
     ra.psh = __builtin_ctz((unsigned)a.c.ps);
     ra.wait_limit = kDefaultWaitLimit;
-    kern<<<a.ctas, 32 * (CW + 1), bytes, st>>>(mk, mv, ra);
-    rc = cudaGetLastError();
-    if (rc != cudaSuccess) return rc;
-    merge_kernel<D><<<a.n_ent, kMergeThreads, 0, st>>>(a);
-    note_launches(2);
+    note_launches(1);
+    if (after_gate)
+        return launch_after(rows_kernel<D, RW, CW>, a.ctas, 32 * (CW + 1), bytes, st, mk, mv, ra);
+    rows_kernel<D, RW, CW><<<a.ctas, 32 * (CW + 1), bytes, st>>>(mk, mv, ra);
     return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_d(const Attn &a, cudaStream_t st) {
-    return a.rows == 16   ? launch<D, 1, 4>(a, st)
-           : a.rows == 32 ? launch<D, 2, 4>(a, st)
-                          : launch<D, 4, 8>(a, st);
+cudaError_t launch_d(const Attn &a, bool after_gate, cudaStream_t st) {
+    return a.rows == 16   ? launch<D, 1, 4>(a, after_gate, st)
+           : a.rows == 32 ? launch<D, 2, 4>(a, after_gate, st)
+                          : launch<D, 4, 8>(a, after_gate, st);
 }
 
 }  // namespace
 
-cudaError_t launch_rows(const Attn &a, cudaStream_t st) {
-    return a.D == 64 ? launch_d<64>(a, st) : launch_d<128>(a, st);
+cudaError_t launch_rows(const Attn &a, bool after_gate, cudaStream_t st) {
+    const cudaError_t rc = a.D == 64 ? launch_d<64>(a, after_gate, st) : launch_d<128>(a, after_gate, st);
+    return rc == cudaSuccess ? launch_merge_runs(a, st) : rc;
+}
+
+cudaError_t launch_merge_runs(const Attn &a, cudaStream_t st) {
+    const dim3 grid(a.ctas, (a.chunk ? kJobRows : a.rows) / 4);
+    note_launches(1);
+    if (a.D == 64)
+        return a.chunk ? launch_after(merge_runs_kernel<64, true>, grid, kMergeThreads, 0, st, a)
+                       : launch_after(merge_runs_kernel<64, false>, grid, kMergeThreads, 0, st, a);
+    return a.chunk ? launch_after(merge_runs_kernel<128, true>, grid, kMergeThreads, 0, st, a)
+                   : launch_after(merge_runs_kernel<128, false>, grid, kMergeThreads, 0, st, a);
 }
 
 // ----------------------------------------------------------------------------
@@ -588,7 +664,7 @@ size_t scratch(Attn *a, void *base) {
     const size_t ents = a->chunk ? (size_t)a->w_cap * a->c.Hkv : n;
     const size_t parts = 2 * (size_t)a->ctas * (a->chunk ? kJobRows : a->rows);
     if (a->dense || !a->chunk) {
-        a->c_first = static_cast<int *>(take(4 * ents));
+        a->c_open = static_cast<int *>(take(4 * (size_t)a->ctas));
         a->c_last = static_cast<int *>(take(4 * ents));
         a->part_ml = static_cast<float2 *>(take(sizeof(float2) * parts));
         a->part_o = static_cast<float *>(take(sizeof(float) * parts * a->D));
@@ -721,8 +797,9 @@ MOBA_EXPORT int moba_paged_attn(const void *q, const void *k_pages, const void *
     if (a.chunk && !a.dense)
         e = cudaMemsetAsync(a.counts, 0, 4 * (size_t)num_seqs * a.n_max * Hkv, st);
     if (e == cudaSuccess) e = launch_gate(a, st);
-    if (e == cudaSuccess && a.chunk) e = launch_plan(a, st);
-    if (e == cudaSuccess) e = a.chunk ? launch_chunk(a, st) : launch_rows(a, st);
+    const bool gated = !a.dense || a.idx;
+    if (e == cudaSuccess && a.chunk) e = launch_plan(a, gated, st);
+    if (e == cudaSuccess) e = a.chunk ? launch_chunk(a, st) : launch_rows(a, gated, st);
     if (own) {
         const cudaError_t f = cudaFreeAsync(own, st);
         if (e == cudaSuccess) e = f;

@@ -515,9 +515,6 @@ ROPE_LINEAR = 1
 ROPE_BASE = 2
 ROPE_BANDS = 3
 
-_NULL = contextlib.nullcontext()
-
-
 @contextlib.contextmanager
 def _switched(device, stream):
     with torch.cuda.device(device):
@@ -528,27 +525,56 @@ def _switched(device, stream):
                 yield
 
 
-def _on(device, stream):
-    """A context in which the tensors' device is current and ``stream`` (if one
-    is given) too, so that results and scratch are allocated where they are used."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return _NULL
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream must be on {device}")
-    return _switched(device, stream)
+# the current stream's handle: torch's own short way where it has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _same_device(like, **tensors):
-    for n, t in tensors.items():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{n} must be on {like.device}")
+def _call(device: int, stream, fn):
+    """fn(raw stream) with the tensors' device current, and ``stream`` too if one
+    is given, so that results and scratch are allocated where they are used."""
+    if stream is None and torch.cuda.current_device() == device:
+        return fn(_raw_stream(device))
+    if stream is not None and stream.device.index != device:
+        raise ValueError(f"stream must be on cuda:{device}")
+    with _switched(device, stream):
+        return fn(torch.cuda.current_stream().cuda_stream)
 
 
-def _heads(t, name):
+# The checks of these calls are on a decode step's latency path: a tensor's
+# device number says in one look that it is a CUDA tensor and on which device.
+def _is(t, dtype, device) -> bool:
+    return t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+
+
+def _tensor(t, dtype, device, name):
+    if not _is(t, dtype, device):
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor"
+                         + (f" on cuda:{device}" if device >= 0 else ""))
+
+
+def _device(t, name) -> int:
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return device
+
+
+def _result(t, shape, dtype, like, device, name):
+    """A result: a new tensor beside ``like``, or the caller's one, checked."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not _is(t, dtype, device) or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"on cuda:{device}")
+    return t
+
+
+def _heads(t, device, name):
     """(tokens, H, D, elements between tokens) of t [..., H, D] bf16: a token's
     heads dense, all tokens one stride apart."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() < 2:
-        raise ValueError(f"{name} must be a CUDA torch.bfloat16 tensor [..., H, D]")
+    if t.dtype is not torch.bfloat16 or t.get_device() != device or t.dim() < 2:
+        raise ValueError(f"{name} must be a torch.bfloat16 tensor [..., H, D] on cuda:{device}")
     H, D = t.shape[-2:]
     if t.is_contiguous():
         return t.numel() // max(1, H * D), H, D, H * D
@@ -583,36 +609,43 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling=ROPE_PLAIN, fa
 
 
 def _rope(fn, what, q, k, positions, freqs, interleaved, magnitude, q_out, k_out, stream):
-    T, Hq, D, qs = _heads(q, "q")
-    Hk, ks, kos = 0, 0, 0
-    _need(positions, torch.int32, "positions")
-    _need(freqs, torch.float64, "freqs")
+    device = _device(q, "q")
+    T, Hq, D, qs = _heads(q, device, "q")
+    _tensor(positions, torch.int32, device, "positions")
+    _tensor(freqs, torch.float64, device, "freqs")
     if positions.numel() != T:
         raise ValueError(f"positions must hold one position for each of the {T} tokens")
+    Hk = ks = 0
     if k is not None:
-        Tk, Hk, Dk, ks = _heads(k, "k")
+        Tk, Hk, Dk, ks = _heads(k, device, "k")
         if Tk != T or Dk != D:
             raise ValueError("k must have the tokens and the head dimension of q")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _same_device(q, k=k, positions=positions, freqs=freqs, q_out=q_out, k_out=k_out)
-    with _on(q.device, stream):
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape:
+
+    def run(st):
+        qo, ko, qos, kos, pk, pko = q_out, k_out, 0, 0, None, None
+        if qo is None:
+            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif qo.shape != q.shape:
             raise ValueError("q_out must have the shape of q")
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        elif k is not None and k_out.shape != k.shape:
-            raise ValueError("k_out must have the shape of k")
-        qos = _heads(q_out, "q_out")[3]
+        else:
+            qos = _heads(qo, device, "q_out")[3]
         if k is not None:
-            kos = _heads(k_out, "k_out")[3]
-        rc = fn(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(positions), _ptr(freqs), T, Hq,
-                Hk, D, 2 * freqs.numel(), int(bool(interleaved)), magnitude, qs, ks, qos, kos,
-                _stream(stream))
-    _check(rc, what)
-    return q_out, k_out
+            if ko is None:
+                ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            elif ko.shape != k.shape:
+                raise ValueError("k_out must have the shape of k")
+            else:
+                kos = _heads(ko, device, "k_out")[3]
+            pk, pko = k.data_ptr(), ko.data_ptr()
+        rc = fn(q.data_ptr(), pk, qo.data_ptr(), pko, positions.data_ptr(), freqs.data_ptr(), T, Hq,
+                Hk, D, 2 * freqs.numel(), 1 if interleaved else 0, magnitude, qs, ks, qos, kos, st)
+        if rc:
+            _check(rc, what)
+        return qo, ko
+
+    return _call(device, stream, run)
 
 
 def rope(q, k, positions, freqs, interleaved: bool = False, magnitude: float = 1.0, q_out=None,
@@ -634,27 +667,30 @@ def rope_bwd(dq_out, dk_out, positions, freqs, interleaved: bool = False, magnit
                  interleaved, magnitude, dq, dk, stream)
 
 
-def _paged(k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens):
+def _paged(device, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens):
     """Checks one layer's pools and the sequences' tables; the sizes a call passes on."""
-    _need(k_pages, torch.bfloat16, "k_pages")
-    _need(v_pages, torch.bfloat16, "v_pages")
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+    bf16, i32 = torch.bfloat16, torch.int32
+    _tensor(k_pages, bf16, device, "k_pages")
+    _tensor(v_pages, bf16, device, "v_pages")
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, D]")
-    P, Hkv, ps, D = k_pages.shape
+    P, Hkv, ps, D = shape
+    bar = None
     if kbar_pages is not None:
-        _need(kbar_pages, torch.float32, "kbar_pages")
+        _tensor(kbar_pages, torch.float32, device, "kbar_pages")
         if kbar_pages.shape != (P, Hkv, D):
             raise ValueError("kbar_pages must be [num_pages, Hkv, D]")
-    _need(page_table, torch.int32, "page_table")
-    _need(cu_new, torch.int32, "cu_new")
-    _need(cache_lens, torch.int32, "cache_lens")
+        bar = kbar_pages.data_ptr()
+    _tensor(page_table, i32, device, "page_table")
+    _tensor(cu_new, i32, device, "cu_new")
+    _tensor(cache_lens, i32, device, "cache_lens")
     n = cache_lens.numel()
-    if page_table.dim() != 2 or page_table.shape[0] != n or cu_new.numel() != n + 1:
+    table = page_table.shape
+    if len(table) != 2 or table[0] != n or cu_new.numel() != n + 1:
         raise ValueError("page_table must be [num_seqs, max_pages], cu_new [num_seqs + 1] and "
                          "cache_lens [num_seqs]")
-    _same_device(k_pages, v_pages=v_pages, kbar_pages=kbar_pages, page_table=page_table,
-                 cu_new=cu_new, cache_lens=cache_lens)
-    return P, Hkv, ps, D, n, page_table.shape[1]
+    return P, Hkv, ps, D, n, table[1], bar
 
 
 def paged_append(k, v, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens, max_new: int,
@@ -663,19 +699,21 @@ def paged_append(k, v, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_l
     sequences (the last ``cu_new[b + 1] - cu_new[b]`` of ``cache_lens[b]`` tokens) and
     the pooled keys of the blocks that they complete to ``kbar_pages`` (None: the
     cache keeps none)."""
-    P, Hkv, ps, D, n, mp = _paged(k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens)
-    _need(k, torch.bfloat16, "k")
-    _need(v, torch.bfloat16, "v")
-    if k.dim() != 3 or k.shape[1:] != (Hkv, D) or v.shape != k.shape:
+    device = _device(k_pages, "k_pages")
+    P, Hkv, ps, D, n, mp, bar = _paged(device, k_pages, v_pages, kbar_pages, page_table, cu_new,
+                                       cache_lens)
+    _tensor(k, torch.bfloat16, device, "k")
+    _tensor(v, torch.bfloat16, device, "v")
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != Hkv or shape[2] != D or v.shape != shape:
         raise ValueError("k and v must be [total, Hkv, D] of the pages")
-    _same_device(k_pages, k=k, v=v)
-    o, _keep = _options(pooling=pooling)
-    with _on(k.device, stream):
-        rc = lib().moba_paged_append(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages),
-                                     _ptr(kbar_pages), _ptr(page_table), _ptr(cu_new),
-                                     _ptr(cache_lens), n, k.shape[0], max_new, Hkv, D, P, ps, mp,
-                                     block_size, ctypes.byref(o), _stream(stream))
-    _check(rc, "moba_paged_append")
+    opt = ctypes.byref(_options(pooling=pooling)[0]) if pooling != POOL_MEAN else None
+    rc = _call(device, stream, lambda st: lib().moba_paged_append(
+        k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), bar,
+        page_table.data_ptr(), cu_new.data_ptr(), cache_lens.data_ptr(), n, shape[0], max_new, Hkv,
+        D, P, ps, mp, block_size, opt, st))
+    if rc:
+        _check(rc, "moba_paged_append")
 
 
 def paged_attn_workspace_size(num_seqs, total, max_new, Hq, Hkv, D, page_size, max_pages,
@@ -692,55 +730,67 @@ def paged_attn(q, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens, 
     :func:`paged_append`) over the paged cache -> (out [total, Hq, D] bf16, lse
     [total, Hq] fp32, idx [total, Hq, topk] int32 or None): MoBA over the own
     block and the best topk - 1 past blocks of each query head, or full causal
-    attention when topk covers the blocks of every page table row.  ``workspace`` is a uint8
-    CUDA tensor of at least :func:`paged_attn_workspace_size` bytes, or None."""
-    P, Hkv, ps, D, n, mp = _paged(k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens)
-    _need(q, torch.bfloat16, "q")
-    if q.dim() != 3 or q.shape[2] != D:
+    attention when topk covers the blocks of a page table row.  ``workspace`` is
+    a uint8 CUDA tensor of at least :func:`paged_attn_workspace_size` bytes, or
+    None (scratch from torch's allocator, on the call's stream)."""
+    device = _device(k_pages, "k_pages")
+    P, Hkv, ps, D, n, mp, bar = _paged(device, k_pages, v_pages, kbar_pages, page_table, cu_new,
+                                       cache_lens)
+    _tensor(q, torch.bfloat16, device, "q")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D:
         raise ValueError("q must be [total, Hq, D] with the pages' head dimension")
-    total, Hq = q.shape[:2]
-    workspace = _ws(workspace)
-    _same_device(k_pages, q=q, workspace=workspace)
-    with _on(q.device, stream):
-        out = _out(out, q.shape, torch.bfloat16, q, "out")
-        lse = _out(lse, (total, Hq), torch.float32, q, "lse")
+    total, Hq = shape[0], shape[1]
+    if workspace is not None:
+        _tensor(workspace, torch.uint8, device, "workspace")
+    size = 0 if workspace is not None else lib().moba_paged_attn_workspace_size(
+        n, total, max_new, Hq, Hkv, D, ps, mp, block_size, topk)
+
+    def run(st):
+        ws = workspace if workspace is not None else torch.empty(size, dtype=torch.uint8,
+                                                                 device=q.device)
+        o = _result(out, shape, torch.bfloat16, q, device, "out")
+        z = _result(lse, (total, Hq), torch.float32, q, device, "lse")
+        sel = None
         if with_idx or idx is not None:
-            idx = _out(idx, (total, Hq, topk), torch.int32, q, "idx")
-        if workspace is None:
-            workspace = torch.empty(
-                lib().moba_paged_attn_workspace_size(n, total, max_new, Hq, Hkv, D, ps, mp,
-                                                     block_size, topk),
-                dtype=torch.uint8, device=q.device)
-        rc = lib().moba_paged_attn(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kbar_pages),
-                                   _ptr(page_table), _ptr(cu_new), _ptr(cache_lens), _ptr(out),
-                                   _ptr(lse), _ptr(idx), n, total, max_new, Hq, Hkv, D, P, ps, mp,
-                                   block_size, topk, _ptr(workspace), workspace.numel(),
-                                   _stream(stream))
-    _check(rc, "moba_paged_attn")
-    return out, lse, idx
+            sel = _result(idx, (total, Hq, topk), torch.int32, q, device, "idx")
+        rc = lib().moba_paged_attn(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), bar, page_table.data_ptr(),
+            cu_new.data_ptr(), cache_lens.data_ptr(), o.data_ptr(), z.data_ptr(),
+            sel.data_ptr() if sel is not None else None, n, total, max_new, Hq, Hkv, D, P, ps, mp,
+            block_size, topk, ws.data_ptr(), ws.numel(), st)
+        if rc:
+            _check(rc, "moba_paged_attn")
+        return o, z, sel
+
+    return _call(device, stream, run)
 
 
 def page_copy(k_pages, v_pages, kbar_pages, src, dst, stream=None):
     """Copies pages ``src[i]`` to ``dst[i]`` (int32) of the pools [num_pages, Hkv,
     page_size, D] (kbar_pages [num_pages, Hkv, D] or None), or of every layer of
     pools with a leading layer dimension."""
-    _need(k_pages, torch.bfloat16, "k_pages")
-    _need(v_pages, torch.bfloat16, "v_pages")
-    if k_pages.dim() not in (4, 5) or v_pages.shape != k_pages.shape:
+    device = _device(k_pages, "k_pages")
+    _tensor(k_pages, torch.bfloat16, device, "k_pages")
+    _tensor(v_pages, torch.bfloat16, device, "v_pages")
+    shape = k_pages.shape
+    if len(shape) not in (4, 5) or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [(layers,) num_pages, Hkv, page_size, D]")
-    P, Hkv, ps, D = k_pages.shape[-4:]
+    P, Hkv, ps, D = shape[-4:]
+    bar = None
     if kbar_pages is not None:
-        _need(kbar_pages, torch.float32, "kbar_pages")
-        if kbar_pages.shape != (*k_pages.shape[:-2], D):
+        _tensor(kbar_pages, torch.float32, device, "kbar_pages")
+        if kbar_pages.shape != (*shape[:-2], D):
             raise ValueError("kbar_pages must be [(layers,) num_pages, Hkv, D]")
-    _need(src, torch.int32, "src")
-    _need(dst, torch.int32, "dst")
-    if src.numel() != dst.numel():
+        bar = kbar_pages.data_ptr()
+    _tensor(src, torch.int32, device, "src")
+    _tensor(dst, torch.int32, device, "dst")
+    n = src.numel()
+    if n != dst.numel():
         raise ValueError("src and dst must have the same length")
-    _same_device(k_pages, v_pages=v_pages, kbar_pages=kbar_pages, src=src, dst=dst)
-    with _on(k_pages.device, stream):
-        rc = lib().moba_page_copy(_ptr(k_pages), _ptr(v_pages), _ptr(kbar_pages), _ptr(src),
-                                  _ptr(dst), src.numel(),
-                                  k_pages.shape[0] if k_pages.dim() == 5 else 1, P, Hkv, D, ps,
-                                  _stream(stream))
-    _check(rc, "moba_page_copy")
+    layers = shape[0] if len(shape) == 5 else 1
+    rc = _call(device, stream, lambda st: lib().moba_page_copy(
+        k_pages.data_ptr(), v_pages.data_ptr(), bar, src.data_ptr(), dst.data_ptr(), n, layers, P,
+        Hkv, D, ps, st))
+    if rc:
+        _check(rc, "moba_page_copy")
