@@ -499,7 +499,8 @@ int moba_rope_frequencies(double *freqs, int rot_dim, double base, int scaling, 
  * rows outside [0, total), more tokens than max_pages hold) or that needs a
  * page outside [0, num_pages) records MOBA_ERR_INVALID_ARG in the device
  * status word; nothing outside the given arrays is read or written, and the
- * other sequences are computed.
+ * other sequences are computed (rows that two sequences claim, where offsets
+ * decrease, hold either one's results or neither's).
  *
  * moba_paged_append writes the new tokens' k and v ([total][Hkv][D] bf16) to
  * their pages and pools every block that they complete (options: pooling)

@@ -13,6 +13,7 @@ namespace paged {
 constexpr int kTile = 64;        // keys per tile
 constexpr int kMaxRows = 64;     // query rows of an entry at most
 constexpr int kJobRows = 256;    // query rows of a job of the tcgen05 kernel
+constexpr int kSelBad = -2;
 constexpr int kMaxBlocks = 65536;  // blocks of a sequence where blocks are selected
 
 struct Attn {
@@ -33,9 +34,7 @@ struct Attn {
     float scale_log2;
     int *status;
     // scratch
-    // (selection only) key tiles of an entry; with lists, its union blocks + 1,
-    // or 0: the entry met a page outside the pool
-    int *tiles;                 // [n_ent]
+    int *tiles;                 // [n_ent] key tiles of an entry (selection only)
     int *ublk;                  // [n_ent][ucap] blocks that some row of the entry selected, ascending
     unsigned long long *umask;  // [n_ent][ucap] which rows did
     int *c_open;                // [ctas] the entry that starts in the CTA's run and ends in another's, or -1
@@ -54,7 +53,8 @@ struct Attn {
     int2 *jobs;                 // [job_cap] list, first entry
     int *n_jobs;                // [1]
     int *list;                  // rows of each list: (token * G + head) << 5 | slot
-    int *ubase;                 // [n_ent][ucap] where the entry's rows start in the block's list
+    int2 *sel;                  // [Hkv][total * G][km1] a row's past blocks, ascending (-1: none, and
+                                // kSelBad: a page outside the pool), and its place in the block's list
     __half *part_h;             // [Hkv][total * G][km1 + 1][D] normalised partial outputs
     float4 *part_s;             // [Hkv][total * G][km1 + 1] log2-sum-exp, scale of each 64 columns,
                                 // and 1 (0: a page outside the pool)
@@ -92,6 +92,7 @@ __device__ __forceinline__ int get_tiles(const Attn &a, int e) {
 }
 
 cudaError_t launch_gate(const Attn &a, cudaStream_t st);
+cudaError_t launch_chunk_gate(const Attn &a, cudaStream_t st);
 // (after_gate: a kernel of this call is before it)
 cudaError_t launch_rows(const Attn &a, bool after_gate, cudaStream_t st);
 // chunks of many rows: row tiles, lists and jobs; then the attention and the merge

@@ -66,9 +66,10 @@ struct Job {
     int lo, nt;      // first key tile of this job's part, and how many
     int te[kG];      // tiles of the part that Q tile g visits
     int pdelta;      // own: position of a row = its token + pdelta
+    int rlo, rn;     // list: the sequence's rows [rlo, rlo + rn)
     int whole;       // all blocks: the part is the whole job
     int slot;        // all blocks: partial slot
-    int pad;
+    int pad[3];
 };
 
 struct ChunkArgs {
@@ -121,7 +122,7 @@ __device__ __forceinline__ void own_job(const Attn &a, const Seq &s, int b, int 
     J.nt = (pl - J.key0) / N + 1;
     J.whole = 1;
     J.slot = 0;
-    J.pad = 0;
+    J.rlo = J.rn = 0;
 }
 
 // Q tile g's share of the part's tiles: those up to its last row.
@@ -269,7 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         J.pdelta = 0;
                         J.whole = 1;
                         J.slot = 0;
-                        J.pad = 0;
+                        a.c.seq(J.b, sq);
+                        J.rlo = sq.row0 * a.G;
+                        J.rn = sq.n * a.G;
                     } else {
                         const int w = (int)((q - listed) / a.c.Hkv);
                         const int b = upper_index(a.own_off, a.c.num_seqs, w);
@@ -440,7 +443,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this thread's row of a job: row << 5 | slot
         auto entry_of = [&](const Job &J) -> int {
             if (jrow >= J.nrows) return -1;
-            return J.own ? (J.rbase + jrow) << 5 | a.km1 : __ldg(a.list + J.rbase + jrow);
+            if (J.own) return (J.rbase + jrow) << 5 | a.km1;
+            // (two sequences that claim the same rows, from offsets that decrease,
+            // spoil one another's lists: such an entry is no row)
+            const int e = __ldg(a.list + J.rbase + jrow);
+            return (unsigned)((e >> 5) - J.rlo) < (unsigned)J.rn && (e & 31) < a.km1 ? e : -1;
         };
         auto q_row = [&](int hk, int entry) -> size_t {
             const int row = entry >> 5;
@@ -848,36 +855,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
     }
 }
 
-// An entry's rows into the lists of the blocks that they selected; a row's
-// slots are its past blocks in ascending order.  The entry's blocks are read
-// once, side by side, then each row walks them in shared memory.
-constexpr int kScatterThreads = 128;
+// The rows into the lists of the blocks that they selected; a row's slots are
+// its past blocks in ascending order.
+constexpr int kScatterThreads = 256;
 
 __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(Attn a) {
-    extern __shared__ unsigned long long s_mask[];  // [ucap], then where each block's rows go, [ucap]
-    int *s_at = reinterpret_cast<int *>(s_mask + a.ucap);
     after_previous();
     let_next();
-    const int e = blockIdx.x, r = threadIdx.x;
-    const int n = a.tiles[e] - 1;
-    if (n <= 0) return;
-    const Entry x = get_entry(a, e);
-    for (int i = r; i < n; i += kScatterThreads) {
-        s_mask[i] = a.umask[(size_t)e * a.ucap + i];
-        const size_t l = ((size_t)x.b * a.n_max + a.ublk[(size_t)e * a.ucap + i]) * a.c.Hkv + x.hk;
-        // (sums stay below the list capacity, or are refused below)
-        s_at[i] = (int)min((long long)a.list_off[l] + a.ubase[(size_t)e * a.ucap + i], a.list_cap);
-    }
-    __syncthreads();
-    if (r >= x.nt * a.G) return;
-    const int row = (x.row0 + r / a.G) * a.G + r % a.G;
-    int slot = 0;
-    for (int i = 0; i < n; ++i) {
-        const unsigned long long mask = s_mask[i];
-        if (!((mask >> r) & 1)) continue;
-        const long long at = (long long)s_at[i] + __popcll(mask & ((1ull << r) - 1));
+    const int b = blockIdx.y;
+    Seq s;
+    if (a.c.seq(b, s) != kSeqOk) return;
+    const long long per = (long long)s.n * a.G * a.km1, all = per * a.c.Hkv;
+    for (long long i = (long long)blockIdx.x * kScatterThreads + threadIdx.x; i < all;
+         i += (long long)gridDim.x * kScatterThreads) {
+        const int hk = (int)(i / per), x = (int)(i - hk * per);
+        const int row = s.row0 * a.G + x / a.km1, slot = x % a.km1;
+        const int2 c = a.sel[((size_t)hk * a.c.total * a.G + row) * a.km1 + slot];
+        if (c.x < 0) continue;
+        const long long at = (long long)a.list_off[((size_t)b * a.n_max + c.x) * a.c.Hkv + hk] + c.y;
         if (at < a.list_cap) a.list[at] = row << 5 | slot;
-        ++slot;
     }
 }
 
@@ -891,18 +887,29 @@ constexpr int kSlotThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kSlotThreads) merge_slots_kernel(Attn a) {
-    constexpr int GL = D / 8, U = 4;
+    constexpr int GL = D / 8, U = 4, STEP = kSlotThreads / GL;
     after_previous();
     const int e = blockIdx.x, gl = threadIdx.x % GL;
     const Entry x = get_entry(a, e);
     if (x.state != kSeqOk) return;  // cleared before
-    const bool none = a.tiles[e] == 0;
-    const int S = a.km1 + 1;
-    for (int r = threadIdx.x / GL; r < x.nt * a.G; r += kSlotThreads / GL) {
-        const int row = (x.row0 + r / a.G) * a.G + r % a.G;
-        const size_t at = (size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G;
-        const size_t p0 = ((size_t)x.hk * a.c.total * a.G + row) * S;
-        const int n = none ? 0 : min(a.km1, (x.pos0 + r / a.G) / a.c.bs) + 1;  // slots, the own block's last
+    const int S = a.km1 + 1, G = a.G;
+    // (token, head) of the row, advanced without divisions; an entry's tokens lie
+    // in two blocks at most
+    int r = threadIdx.x / GL, t = r / G, g = r - t * G;
+    const int dt = STEP / G, dg = STEP - dt * G;
+    const int c0 = x.pos0 / a.c.bs, cut = (c0 + 1) * a.c.bs - x.pos0;
+    for (; r < x.nt * G; r += STEP) {
+        const int row = (x.row0 + t) * G + g;
+        const size_t at = (size_t)(x.row0 + t) * a.Hq + x.hk * G + g;
+        const size_t lin = (size_t)x.hk * a.c.total * G + row, p0 = lin * S;
+        const int n = min(a.km1, c0 + (t >= cut)) + 1;  // slots, the own block's last
+        const bool none = a.km1 > 0 && __ldg(&a.sel[lin * a.km1].x) == kSelBad;
+        t += dt;
+        g += dg;
+        if (g >= G) {
+            g -= G;
+            ++t;
+        }
         float M = -INFINITY, W = 0.f, acc[8];
         bool bad = none;
 #pragma unroll
@@ -1006,7 +1013,10 @@ cudaError_t launch_plan(const Attn &a, bool after_gate, cudaStream_t st) {
     note_launches(1);
     if (rc != cudaSuccess || a.km1 == 0) return rc;
     note_launches(1);
-    return launch_after(scatter_kernel, a.n_ent, kScatterThreads, 12 * (size_t)a.ucap, st, a);
+    const long long most = (long long)a.c.max_new * a.G * a.km1 * a.c.Hkv;
+    const long long ctas = (most + 4 * kScatterThreads - 1) / (4 * kScatterThreads);
+    const dim3 grid((unsigned)(ctas < 4096 ? ctas : 4096), a.c.num_seqs);
+    return launch_after(scatter_kernel, grid, kScatterThreads, 0, st, a);
 }
 
 cudaError_t launch_chunk(const Attn &a, cudaStream_t st) {

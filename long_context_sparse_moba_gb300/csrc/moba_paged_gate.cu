@@ -5,21 +5,26 @@
 // scores) and "MOBA mixture of block attention for server-side long context"
 // (hncyxsy.com/news/197418) section 3 (the own block forced).
 //
-// One CTA per entry (up to 64 query rows that share a kv head).  64 pooled keys
-// at a time are split into two bf16 terms (hi + lo) and scored on the tensor
-// cores, q being bf16 already; a thread per row keeps the topk best.
-// A score errs by at most 2^-16 |q||k| for the split and 256 roundings of at
-// most 2^-23 |q||k| for the sums, less than E = 2^-14 |q| max|k| together (plus
-// a term for pooled keys so small that lo underflows).  Where the last kept and
-// the first dropped score are more than 2 E apart the selection is settled;
-// the other rows (about one in a hundred on random keys, all of them when keys
-// tie) are decided by a warp with 64-bit scores, so that the selection is the
-// one of 64-bit arithmetic: scores of the topk best by fp32 where the next one
-// lies 2 E below the boundary, else of all blocks within 3 E of it.
-// Then the blocks that any row selected are listed, each with the rows that
-// did: the attention kernel reads a block once for all rows of the entry.  For
-// chunks of many rows the own blocks stay out of it, and each block's count of
-// rows over all entries is taken, for lists of the rows that selected it.
+// 64 pooled keys at a time are split into two bf16 terms (hi + lo) and scored on
+// the tensor cores, q being bf16 already.  A score errs by at most 2^-16 |q||k|
+// for the split and 256 roundings of at most 2^-23 |q||k| for the sums.  The
+// accumulators go straight into the selection: the four lanes of a row hold 16
+// scores each as integers in the scores' order, their low 7 bits replaced by the
+// score's place (another 2^-16 |q||k|), and each round of a maximum over the
+// lanes yields the next best; the topk + 1 best of the tiles before compete again.
+// (A list kept by insertion costs several times the instructions.)
+// Where the last kept and the first dropped score are more than 2 E apart, E =
+// 2^-13 |q| max|k| (plus a term for pooled keys so small that lo underflows), the
+// selection is settled; the other rows (two in a hundred on random keys, all of
+// them when keys tie) are decided by a warp with 64-bit scores, so that the
+// selection is the one of 64-bit arithmetic: scores of the topk best by fp32 where
+// the next one lies 2 E below the boundary, else of all blocks within 3 E of it.
+//
+// gate_kernel: one CTA per entry (up to 64 query rows that share a kv head); then
+// the blocks that any row selected are listed, each with the rows that did: the
+// attention kernel reads a block once for all rows of the entry.
+// chunk_gate_kernel: chunks of many rows, 128 rows to a CTA; a row takes its
+// place in the list of each block that it selected.
 #include "moba_mma.cuh"
 #include "moba_paged_attn.cuh"
 #include "moba_select.cuh"
@@ -31,11 +36,10 @@ namespace {
 using namespace mma;
 
 constexpr int kThreads = 128;
-constexpr int kScStride = kTile + 1;
 
 // dynamic shared memory of the gate, in order
 struct GateSmem {
-    uint32_t hi, lo, sc, sel, bits, rank, mask, bytes;
+    uint32_t hi, lo, sel, bits, rank, mask, bytes;
 };
 __host__ __device__ inline GateSmem gate_smem(int D, int words, int ucap, int km1) {
     GateSmem s;
@@ -46,8 +50,6 @@ __host__ __device__ inline GateSmem gate_smem(int D, int words, int ucap, int km
     o += kTile * D * 2;
     s.mask = o;
     o += 8 * ucap;
-    s.sc = o;
-    o += 4 * kMaxRows * kScStride;
     s.sel = o;
     o += 4 * kMaxRows * (km1 + 1);
     s.bits = o;
@@ -138,33 +140,242 @@ __device__ __noinline__ int pick64_of(const Attn &a, int hk, const int *table, c
     return who;
 }
 
-// insert (x, c) into a descending list; an equal score keeps the lower block first
-template <int KCAP>
-__device__ __forceinline__ void merge_insert(float (&ts)[KCAP], int (&ti)[KCAP], float x, int c) {
-    bool ins = false;
+// The best scores of a row so far, spread over the row's four lanes: rank r with
+// lane r % 4, place r / 4.  `key`: the score's bits in integer order, the low 7
+// bits cleared.
+constexpr int kNone = (int)0x80000000;
+template <int NS>
+struct Best {
+    int key[NS], blk[NS];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int s = 0; s < KCAP; ++s) {
-        if (ins || x > ts[s] || ti[s] == sel::kEmpty || (x == ts[s] && c < ti[s])) {
-            const float fs = ts[s];
-            const int fi = ti[s];
-            ts[s] = x;
-            ti[s] = c;
-            x = fs;
-            c = fi;
-            ins = true;
+        for (int i = 0; i < NS; ++i) {
+            key[i] = kNone;
+            blk[i] = sel::kEmpty;
         }
+    }
+    // the 16 scores of this lane (blocks cb + 8 j + 2 (lane % 4) + k, those from `own`
+    // on left out) against the ranks so far; `want` ranks are kept
+    __device__ __forceinline__ void rank(const float (&acc)[8][4], int h, int cb, int own, int want) {
+        const int lane = threadIdx.x & 31;
+        int v[16], old[NS];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int at = (j >> 1) * 8 + 2 * (lane & 3) + (j & 1);
+            const int x = __float_as_int(acc[j >> 1][2 * h + (j & 1)]);
+            // NaN as -inf; below zero the order of the bits is turned around
+            const int y = (x & 0x7fffffff) > 0x7f800000 ? (int)0x807fffff : x ^ ((x >> 31) & 0x7fffffff);
+            v[j] = cb + at < own ? ((y & ~127) | at) : kNone;
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            old[i] = blk[i];
+            key[i] = blk[i] == sel::kEmpty ? kNone : key[i] | (64 + 4 * i + (lane & 3));
+        }
+        int nkey[NS], nblk[NS];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            nkey[i] = kNone;
+            nblk[i] = sel::kEmpty;
+#pragma unroll 1
+            for (int l = 0; l < 4; ++l) {
+                if (4 * i + l >= want) break;
+                int m = key[0];
+#pragma unroll
+                for (int k = 1; k < NS; ++k) m = max(m, key[k]);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) m = max(m, v[j]);
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                // its block: of this tile, or of the rank that it had
+                const int id = m & 127, was = (id - 64) >> 2;
+                int b = old[0];
+#pragma unroll
+                for (int k = 1; k < NS; ++k) b = was == k ? old[k] : b;
+                b = __shfl_sync(0xffffffffu, b, (lane & 28) | (id & 3));
+                if (id < 64) b = cb + id;
+                if ((lane & 3) == l) {
+                    nkey[i] = m & ~127;
+                    nblk[i] = m == kNone ? sel::kEmpty : b;
+                }
+                if (m != kNone) {
+#pragma unroll
+                    for (int k = 0; k < NS; ++k) key[k] = key[k] == m ? kNone : key[k];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = v[j] == m ? kNone : v[j];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            key[i] = nkey[i];
+            blk[i] = nblk[i];
+        }
+    }
+    // the score and the block of a rank, to all four lanes
+    __device__ __forceinline__ float score(int r, int &b) const {
+        const int lane = threadIdx.x & 31;
+        int k = key[0];
+        b = blk[0];
+#pragma unroll
+        for (int i = 1; i < NS; ++i) {
+            k = (r >> 2) == i ? key[i] : k;
+            b = (r >> 2) == i ? blk[i] : b;
+        }
+        k = __shfl_sync(0xffffffffu, k, (lane & 28) | (r & 3));
+        b = __shfl_sync(0xffffffffu, b, (lane & 28) | (r & 3));
+        return b == sel::kEmpty ? -INFINITY : __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+    }
+};
+
+// Rows left to 64-bit scores.
+template <int ROWS>
+struct Unsure {
+    int n, row[ROWS], few[ROWS];
+    float from[ROWS];
+};
+
+// A row's ranks into sel[0 .. km1], and whether its selection is settled.  All
+// four lanes of a row (r < 0: of no row).
+template <int NS, int ROWS>
+__device__ __forceinline__ void decide(const Best<NS> &best, int r, int own, int km1, float q2,
+                                       float knmax, int *sel, Unsure<ROWS> &un) {
+    const int lane = threadIdx.x & 31;
+    int b;
+    const float kept = best.score(km1 - 1, b), dropped = best.score(km1, b);
+    const float next = best.score(km1 + 1, b);
+    if (r < 0 || own <= km1) return;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+        if (4 * i + (lane & 3) <= km1) sel[r * (km1 + 1) + 4 * i + (lane & 3)] = best.blk[i];
+    const float err = sqrtf(q2) * fmaf(knmax, 1.220703125e-4f, 1e-34f);
+    if ((lane & 3) == 0 && !(kept - dropped > 2.f * err)) {
+        const int u = atomicAdd(&un.n, 1);
+        un.row[u] = r;
+        un.from[u] = kept - 3.f * err;
+        un.few[u] = b == sel::kEmpty || next < kept - 2.f * err;  // (b: there is no next one)
     }
 }
 
-template <int D, int KCAP>
+// Pooled keys [cb, cb + 64) of a sequence, split into bf16 hi + lo tiles (zeros
+// from c_end on), and their largest norm into s_knmax.  Between two barriers.
+template <int D, int T>
+__device__ __forceinline__ void load_pooled(const Attn &a, int hk, const int *table, int cb, int c_end,
+                                            int *s_page, int *s_bad, int *s_knmax, uint8_t *hi,
+                                            uint8_t *lo) {
+    constexpr int LR = D / 4;  // lanes per pooled key, four values each
+    constexpr int NR = kTile / (T / LR);
+    const int tid = threadIdx.x, ppb = a.c.bs / a.c.ps;
+    if (tid < kTile) {
+        const int page = cb + tid < c_end ? __ldg(table + (cb + tid + 1) * ppb - 1) : -1;
+        const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
+        s_page[tid] = ok ? page : -1;
+        if (cb + tid < c_end && !ok) *s_bad = 1;
+    }
+    __syncthreads();
+    float4 f[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int page = s_page[i * (T / LR) + tid / LR];
+        f[i] = page < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                        : __ldg(reinterpret_cast<const float4 *>(
+                                    a.kbar + ((size_t)page * a.c.Hkv + hk) * D) + tid % LR);
+    }
+    float kn = 0.f;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int r = i * (T / LR) + tid / LR;
+        const float v[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
+        __nv_bfloat16 h[4], l[4];
+        float n2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = __float2bfloat16(v[k]);
+            l[k] = __float2bfloat16(v[k] - __bfloat162float(h[k]));
+            n2 = fmaf(v[k], v[k], n2);
+        }
+        const uint32_t at = swz<D>(r, (tid % LR) >> 1) + (tid & 1) * 8;
+        *reinterpret_cast<uint2 *>(hi + at) = *reinterpret_cast<uint2 *>(h);
+        *reinterpret_cast<uint2 *>(lo + at) = *reinterpret_cast<uint2 *>(l);
+#pragma unroll
+        for (int o = LR / 2; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+        kn = n2 > kn || n2 != n2 ? n2 : kn;
+    }
+    // a NaN norm has the largest bits of all
+    if (tid % LR == 0) atomicMax(s_knmax, __float_as_int(fabsf(sqrtf(kn))));
+}
+
+// Scores of this warp's 16 rows with the 64 pooled keys.
+template <int D>
+__device__ __forceinline__ void score_tile(const uint32_t (&qa)[D / 16][4], uint32_t s_hi,
+                                           uint32_t s_lo, float (&acc)[8][4]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+#pragma unroll
+    for (int term = 0; term < 2; ++term) {
+        const uint32_t base = term ? s_lo : s_hi;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int np = 0; np < 4; ++np) {
+                uint32_t b0, b1, b2, b3;
+                ldsm_x4(b0, b1, b2, b3,
+                        base + swz<D>(np * 16 + (lane & 7) + ((lane >> 4) << 3),
+                                      ks * 2 + ((lane >> 3) & 1)));
+                mma16816(acc[2 * np], qa[ks], b0, b1);
+                mma16816(acc[2 * np + 1], qa[ks], b2, b3);
+            }
+    }
+}
+
+// Two rows of q as MMA operands (nullptr: zeros) and their squared norms.
+template <int D>
+__device__ __forceinline__ void load_q(const __nv_bfloat16 *q0, const __nv_bfloat16 *q1,
+                                       uint32_t (&qa)[D / 16][4], float (&q2)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(h ? q1 : q0) + (threadIdx.x & 3);
+        const bool live = (h ? q1 : q0) != nullptr;
+        q2[h] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t u = live ? __ldg(src + ks * 8 + 4 * k) : 0u;
+                qa[ks][h + 2 * k] = u;
+                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
+                q2[h] = fmaf(f.x, f.x, fmaf(f.y, f.y, q2[h]));
+            }
+        q2[h] += __shfl_xor_sync(0xffffffffu, q2[h], 1);
+        q2[h] += __shfl_xor_sync(0xffffffffu, q2[h], 2);
+    }
+}
+
+// A row's selection by 64-bit scores into sel[0 .. km1); a warp.
+template <int D>
+__device__ __forceinline__ void settle(const Attn &a, int hk, const int *table, const __nv_bfloat16 *qr,
+                                       int own, int few, float from, int *sel) {
+    const int lane = threadIdx.x & 31, km1 = a.km1;
+    int who = few ? pick64_of<D>(a, hk, table, qr, sel, min(km1 + 1, own))
+                  : pick64<D>(a, hk, table, qr, own, from);
+    // should the bound not have left enough: from the lowest score on
+    if (__any_sync(0xffffffffu, lane < km1 && who == sel::kEmpty))
+        who = pick64<D>(a, hk, table, qr, own, -INFINITY);
+    __syncwarp();
+    if (lane < km1) sel[lane] = who;
+}
+
+template <int D, int NS>
 __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
     constexpr int KS = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int s_bad, s_knmax, s_unsure, s_count, s_rows[kMaxRows], s_few[kMaxRows], s_page[kTile];
-    __shared__ float s_floor[kMaxRows];
+    __shared__ int s_bad, s_knmax, s_count, s_page[kTile];
+    __shared__ Unsure<kMaxRows> s_un;
     let_next();
     const GateSmem L = gate_smem(D, words, a.ucap, a.km1);
-    float *sc = reinterpret_cast<float *>(smem + L.sc);
     int *sel = reinterpret_cast<int *>(smem + L.sel);  // [row][km1 + 1]
     unsigned *bits = reinterpret_cast<unsigned *>(smem + L.bits);
     int *rank = reinterpret_cast<int *>(smem + L.rank);
@@ -184,188 +395,60 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
     }
     const int pos_last = x.pos0 + x.nt - 1, c_own = pos_last / bs;
     const int *table = a.c.table + (size_t)x.b * a.c.max_pages;
-    const int ppb = bs / a.c.ps;
     if (tid == 0) {
         s_bad = 0;
         s_knmax = 0;
-        s_unsure = 0;
+        s_un.n = 0;
     }
     for (int i = tid; i < words; i += kThreads) bits[i] = 0;
     __syncthreads();
-    // two threads to a row, for half the scores of a tile each
-    const int row = tid >> 1, half = tid & 1;
-    const bool row_ok = row < nrows;
-    const int ci = row_ok ? (x.pos0 + row / G) / bs : 0;  // the row's own block
-    const __nv_bfloat16 *qrow = a.q + ((size_t)(x.row0 + row / G) * a.Hq + x.hk * G + row % G) * D;
     const bool scored = km1 > 0 && c_own > km1;
     const int ss = km1 + 1;  // of a row's blocks in `sel`
+    auto q_of = [&](int r) -> const __nv_bfloat16 * {
+        return a.q + ((size_t)(x.row0 + r / G) * a.Hq + x.hk * G + r % G) * D;
+    };
+    auto own_of = [&](int r) -> int { return (x.pos0 + r / G) / bs; };
     if (scored) {
         // this warp's 16 rows of q as MMA operands, and each row's norm
         uint32_t qa[KS][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = warp * 16 + (lane >> 2) + 8 * h;
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(
-                a.q + ((size_t)(x.row0 + r / G) * a.Hq + x.hk * G + r % G) * D) + (lane & 3);
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                qa[ks][h] = r < nrows ? __ldg(src + ks * 8) : 0u;
-                qa[ks][h + 2] = r < nrows ? __ldg(src + ks * 8 + 4) : 0u;
-            }
-        }
-        float q2 = 0.f;
-        if (row_ok)
-#pragma unroll
-            for (int d = 0; d < D / 2; d += 8) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(qrow + half * (D / 2) + d));
-                const __nv_bfloat162 *p2 = reinterpret_cast<const __nv_bfloat162 *>(&u);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = __bfloat1622float2(p2[i]);
-                    q2 = fmaf(f.x, f.x, fmaf(f.y, f.y, q2));
-                }
-            }
-        q2 += __shfl_xor_sync(0xffffffffu, q2, 1);
-        float ts[KCAP];
-        int ti[KCAP];
-#pragma unroll
-        for (int i = 0; i < KCAP; ++i) {
-            ts[i] = -INFINITY;
-            ti[i] = sel::kEmpty;
-        }
-        float worst = -INFINITY;
+        float q2[2];
+        const int rq = warp * 16 + (lane >> 2);
+        load_q<D>(rq < nrows ? q_of(rq) : nullptr, rq + 8 < nrows ? q_of(rq + 8) : nullptr, qa, q2);
+        const int ci[2] = {rq < nrows ? own_of(rq) : 0, rq + 8 < nrows ? own_of(rq + 8) : 0};
+        Best<NS> best[2];
+        best[0].clear();
+        best[1].clear();
         const uint32_t s_hi = smem_u32(smem + L.hi), s_lo = smem_u32(smem + L.lo);
         for (int cb = 0; cb < c_own; cb += kTile) {
-            // 64 pooled keys, four values a lane, split into hi + lo
-            constexpr int LR = D / 4;  // lanes per pooled key
-            constexpr int NR = kTile / (kThreads / LR);
-            if (tid < kTile) {
-                const int page = cb + tid < c_own ? __ldg(table + (cb + tid + 1) * ppb - 1) : -1;
-                const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
-                s_page[tid] = ok ? page : -1;
-                if (cb + tid < c_own && !ok) s_bad = 1;
-            }
+            __syncthreads();  // (the tile before has been read)
+            load_pooled<D, kThreads>(a, x.hk, table, cb, c_own, s_page, &s_bad, &s_knmax, smem + L.hi,
+                                     smem + L.lo);
             __syncthreads();
-            float4 f[NR];
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                const int page = s_page[i * (kThreads / LR) + tid / LR];
-                f[i] = page < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                : __ldg(reinterpret_cast<const float4 *>(
-                                            a.kbar + ((size_t)page * a.c.Hkv + x.hk) * D) + tid % LR);
-            }
-            float kn = 0.f;
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                const int r = i * (kThreads / LR) + tid / LR;
-                const float v[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
-                __nv_bfloat16 h[4], l[4];
-                float n2 = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    h[k] = __float2bfloat16(v[k]);
-                    l[k] = __float2bfloat16(v[k] - __bfloat162float(h[k]));
-                    n2 = fmaf(v[k], v[k], n2);
-                }
-                const uint32_t at = swz<D>(r, (tid % LR) >> 1) + (tid & 1) * 8;
-                *reinterpret_cast<uint2 *>(smem + L.hi + at) = *reinterpret_cast<uint2 *>(h);
-                *reinterpret_cast<uint2 *>(smem + L.lo + at) = *reinterpret_cast<uint2 *>(l);
-#pragma unroll
-                for (int o = LR / 2; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
-                kn = n2 > kn || n2 != n2 ? n2 : kn;
-            }
-            // a NaN norm has the largest bits of all
-            if (tid % LR == 0) atomicMax(&s_knmax, __float_as_int(fabsf(sqrtf(kn))));
-            __syncthreads();
-            float acc[8][4];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
             if (warp * 16 < nrows) {
+                float acc[8][4];
+                score_tile<D>(qa, s_hi, s_lo, acc);
 #pragma unroll
-                for (int term = 0; term < 2; ++term) {
-                    const uint32_t base = term ? s_lo : s_hi;
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                        for (int np = 0; np < 4; ++np) {
-                            uint32_t b0, b1, b2, b3;
-                            ldsm_x4(b0, b1, b2, b3,
-                                    base + swz<D>(np * 16 + (lane & 7) + ((lane >> 4) << 3),
-                                                  ks * 2 + ((lane >> 3) & 1)));
-                            mma16816(acc[2 * np], qa[ks], b0, b1);
-                            mma16816(acc[2 * np + 1], qa[ks], b2, b3);
-                        }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sc[(warp * 16 + (lane >> 2) + (i >> 1) * 8) * kScStride + j * 8 +
-                           2 * (lane & 3) + (i & 1)] = acc[j][i];
-            }
-            __syncthreads();
-            if (row_ok) {
-                const int n = min(kTile / 2 * (half + 1), ci - cb);
-                for (int k = kTile / 2 * half; k < n; ++k) {
-                    float y = sc[row * kScStride + k];
-                    if (y != y) y = -INFINITY;
-                    if (y > worst || ti[KCAP - 1] == sel::kEmpty) {
-                        sel::top_insert<KCAP>(ts, ti, KCAP, y, cb + k);
-                        worst = ts[KCAP - 1];
-                    }
-                }
+                for (int h = 0; h < 2; ++h) best[h].rank(acc, h, cb, ci[h], km1 + 2);
             }
         }
-        // the other thread's list into the first one's
+        if (warp * 16 < nrows)
 #pragma unroll
-        for (int i = 0; i < KCAP; ++i) {
-            const float y = __shfl_xor_sync(0xffffffffu, ts[i], 1);
-            const int c = __shfl_xor_sync(0xffffffffu, ti[i], 1);
-            if (half == 0 && c != sel::kEmpty) merge_insert<KCAP>(ts, ti, y, c);
-        }
-        if (row_ok && half == 0 && ci > km1) {
-            float kept = 0.f, dropped = 0.f, next = 0.f;
-            bool none = false;  // there is no next one, or it is not held
-#pragma unroll
-            for (int i = 0; i < KCAP; ++i) {
-                if (i == km1 - 1) kept = ts[i];
-                if (i == km1) dropped = ts[i];
-                if (i == km1 + 1) {
-                    next = ts[i];
-                    none = ti[i] == sel::kEmpty;
-                }
-                if (i <= km1) sel[row * ss + i] = ti[i];
-            }
-            const float err = sqrtf(q2) * fmaf(__int_as_float(s_knmax), 6.103515625e-5f, 1e-34f);
-            if (!(kept - dropped > 2.f * err)) {
-                const int u = atomicAdd(&s_unsure, 1);
-                s_rows[u] = row;
-                s_floor[u] = kept - 3.f * err;
-                s_few[u] = km1 + 1 < KCAP && (none || next < kept - 2.f * err);
-            }
-        }
+            for (int h = 0; h < 2; ++h)
+                decide(best[h], rq + 8 * h < nrows ? rq + 8 * h : -1, ci[h], km1, q2[h],
+                       __int_as_float(s_knmax), sel, s_un);
         __syncthreads();
-        // rows that the error bound leaves open: 64-bit scores of the blocks
-        // near the boundary, blocks ascending; lane i holds the i-th best
-        for (int u = warp; u < s_unsure; u += kThreads / 32) {
-            const int r = s_rows[u];
-            const int cr = (x.pos0 + r / G) / bs;
-            const __nv_bfloat16 *qr = a.q + ((size_t)(x.row0 + r / G) * a.Hq + x.hk * G + r % G) * D;
-            int who = s_few[u] ? pick64_of<D>(a, x.hk, table, qr, sel + r * ss, min(ss, cr))
-                               : pick64<D>(a, x.hk, table, qr, cr, s_floor[u]);
-            // should the bound not have left enough: from the lowest score on
-            if (__any_sync(0xffffffffu, lane < km1 && who == sel::kEmpty))
-                who = pick64<D>(a, x.hk, table, qr, cr, -INFINITY);
-            __syncwarp();
-            if (lane < km1) sel[r * ss + lane] = who;
+        // rows that the error bound leaves open: a warp each
+        for (int u = warp; u < s_un.n; u += kThreads / 32) {
+            const int r = s_un.row[u];
+            settle<D>(a, x.hk, table, q_of(r), own_of(r), s_un.few[u], s_un.from[u], sel + r * ss);
         }
         __syncthreads();
     }
     const bool bad = scored && s_bad;
     // each row's selection, ascending (a row with few past blocks takes them all)
-    if (row_ok && half == 0) {
+    const bool row_ok = tid < nrows;
+    const int row = tid, ci = row_ok ? own_of(row) : 0;
+    if (row_ok) {
         const int n = min(km1, ci);
         int *mine = sel + row * ss;
         if (ci > km1) {
@@ -380,7 +463,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
         }
         if (!bad) {
             for (int i = 0; i < n; ++i) atomicOr(bits + (mine[i] >> 5), 1u << (mine[i] & 31));
-            if (!a.chunk) atomicOr(bits + (ci >> 5), 1u << (ci & 31));
+            atomicOr(bits + (ci >> 5), 1u << (ci & 31));
         }
         if (a.idx) {
             int32_t *dst = a.idx + ((size_t)(x.row0 + row / G) * a.Hq + x.hk * G + row % G) * a.topk;
@@ -417,9 +500,9 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
     const int count = s_count;
     for (int i = tid; i < count; i += kThreads) mask[i] = 0ull;
     __syncthreads();
-    if (row_ok && half == 0) {
+    if (row_ok) {
         const int n = min(km1, ci);
-        for (int i = 0; i < n + (a.chunk ? 0 : 1); ++i) {
+        for (int i = 0; i <= n; ++i) {
             const int c = i < n ? sel[row * ss + i] : ci;
             const int at = rank[c >> 5] + __popc(bits[c >> 5] & ((1u << (c & 31)) - 1u));
             atomicOr(mask + at, 1ull << row);
@@ -437,16 +520,124 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
         }
     }
     for (int i = tid; i < count; i += kThreads) umask[i] = mask[i];
-    if (!a.chunk) {
-        if (tid == 0) a.tiles[e] = (count - 1) * a.tpb + (pos_last - c_own * bs) / kTile + 1;
+    if (tid == 0) a.tiles[e] = (count - 1) * a.tpb + (pos_last - c_own * bs) / kTile + 1;
+}
+
+// ----------------------------------------------------------------------------
+// chunks of many rows
+// ----------------------------------------------------------------------------
+constexpr int kChunkRows = 128, kChunkThreads = 256;
+
+__host__ __device__ constexpr int chunk_gate_smem(int D, int km1) {
+    return 2 * kTile * D * 2 + 4 * kChunkRows * (km1 + 1);
+}
+
+template <int D, int NS>
+__global__ void __launch_bounds__(kChunkThreads, NS <= 2 ? 2 : 1) chunk_gate_kernel(Attn a, int tps) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_bad, s_knmax, s_page[kTile];
+    __shared__ Unsure<kChunkRows> s_un;
+    uint8_t *const hi = smem, *const lo = smem + kTile * D * 2;
+    int *sel = reinterpret_cast<int *>(smem + 2 * kTile * D * 2);  // [row][km1 + 1]
+    let_next();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hk = blockIdx.x % a.c.Hkv, bt = blockIdx.x / a.c.Hkv;
+    const int b = bt / tps, r0 = (bt - b * tps) * kChunkRows;
+    const int bs = a.c.bs, km1 = a.km1, G = a.G, ss = km1 + 1;
+    Seq s;
+    const int state = a.c.seq(b, s);
+    const int nrows = min(kChunkRows, s.n * G - r0);
+    if (nrows <= 0 || state == kSeqEmpty) return;
+    const int row0 = s.row0 * G + r0;  // row = row0 + r: token row / G, head row % G
+    if (state == kSeqBad) {
+        if (a.idx)
+            for (int i = tid; i < nrows * a.topk; i += kChunkThreads) {
+                const int row = row0 + i / a.topk;
+                a.idx[((size_t)(row / G) * a.Hq + hk * G + row % G) * a.topk + i % a.topk] = -1;
+            }
         return;
     }
-    // this entry's place in the list of each block that its rows selected
-    if (tid == 0) a.tiles[e] = count + 1;
+    const int pdelta = s.len - s.n - s.row0;  // position of a row = its token + pdelta
+    const int c_own = ((row0 + nrows - 1) / G + pdelta) / bs;
+    const int *table = a.c.table + (size_t)b * a.c.max_pages;
+    if (tid == 0) {
+        s_bad = 0;
+        s_knmax = 0;
+        s_un.n = 0;
+    }
+    auto q_of = [&](int r) -> const __nv_bfloat16 * {
+        const int row = row0 + r;
+        return a.q + ((size_t)(row / G) * a.Hq + hk * G + row % G) * D;
+    };
+    auto own_of = [&](int r) -> int { return ((row0 + r) / G + pdelta) / bs; };
+    const bool scored = km1 > 0 && c_own > km1;
+    if (scored) {
+        uint32_t qa[D / 16][4];
+        float q2[2];
+        const int rq = warp * 16 + (lane >> 2);  // the quad's first row
+        load_q<D>(rq < nrows ? q_of(rq) : nullptr, rq + 8 < nrows ? q_of(rq + 8) : nullptr, qa, q2);
+        const int ci[2] = {rq < nrows ? own_of(rq) : 0, rq + 8 < nrows ? own_of(rq + 8) : 0};
+        Best<NS> best[2];
+        best[0].clear();
+        best[1].clear();
+        const uint32_t s_hi = smem_u32(hi), s_lo = smem_u32(lo);
+        for (int cb = 0; cb < c_own; cb += kTile) {
+            __syncthreads();  // (the tile before has been read)
+            load_pooled<D, kChunkThreads>(a, hk, table, cb, c_own, s_page, &s_bad, &s_knmax, hi, lo);
+            __syncthreads();
+            if (warp * 16 < nrows) {
+                float acc[8][4];
+                score_tile<D>(qa, s_hi, s_lo, acc);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) best[h].rank(acc, h, cb, ci[h], km1 + 2);
+            }
+        }
+        if (warp * 16 < nrows)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                decide(best[h], rq + 8 * h < nrows ? rq + 8 * h : -1, ci[h], km1, q2[h],
+                       __int_as_float(s_knmax), sel, s_un);
+        __syncthreads();
+        for (int u = warp; u < s_un.n; u += kChunkThreads / 32) {
+            const int r = s_un.row[u];
+            settle<D>(a, hk, table, q_of(r), own_of(r), s_un.few[u], s_un.from[u], sel + r * ss);
+        }
+    }
     __syncthreads();
-    for (int i = tid; i < count; i += kThreads)
-        a.ubase[(size_t)e * a.ucap + i] =
-            atomicAdd(a.counts + ((size_t)x.b * a.n_max + ublk[i]) * a.c.Hkv + x.hk, __popcll(mask[i]));
+    const bool bad = scored && s_bad;
+    if (bad && tid == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+    if (tid >= nrows) return;
+    // each row's selection, ascending, and its places in the blocks' lists
+    const int own = own_of(tid), n = min(km1, own), row = row0 + tid;
+    int *mine = sel + tid * ss;
+    if (own > km1) {
+        for (int i = 1; i < n; ++i) {
+            const int v = mine[i];
+            int j = i - 1;
+            for (; j >= 0 && mine[j] > v; --j) mine[j + 1] = mine[j];
+            mine[j + 1] = v;
+        }
+    } else {
+        for (int i = 0; i < n; ++i) mine[i] = i;
+    }
+    if (a.idx) {
+        int32_t *dst = a.idx + ((size_t)(row / G) * a.Hq + hk * G + row % G) * a.topk;
+        for (int i = 0; i < a.topk; ++i) dst[i] = bad || i > n ? -1 : i < n ? mine[i] : own;
+    }
+    int2 *out = a.sel + ((size_t)hk * a.c.total * G + row) * km1;
+    for (int i0 = 0; i0 < km1; i0 += 4) {
+        int c[4], at[4];  // (four in flight)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            c[j] = bad ? kSelBad : i0 + j < n ? mine[i0 + j] : -1;
+            at[j] = c[j] >= 0
+                        ? atomicAdd(a.counts + ((size_t)b * a.n_max + c[j]) * a.c.Hkv + hk, 1)
+                        : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i0 + j < km1) out[i0 + j] = make_int2(c[j], at[j]);
+    }
 }
 
 // The selection where topk covers every block: all of them.
@@ -463,26 +654,45 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(Attn a) {
     }
 }
 
-template <int D, int KCAP>
+template <int D, int NS>
 cudaError_t launch(const Attn &a, cudaStream_t st) {
     const int words = (int)(((long long)a.c.max_pages * a.c.ps / a.c.bs) / 32 + 1);
     const int bytes = (int)gate_smem(D, words, a.ucap, a.km1).bytes;
     constexpr int kMost = kMaxRows * (kMaxPastSlots + 1);
-    const cudaError_t rc = allow_smem<gate_kernel<D, KCAP>>(
+    const cudaError_t rc = allow_smem<gate_kernel<D, NS>>(
         (int)gate_smem(D, kMaxBlocks / 32 + 1, kMost, kMaxPastSlots).bytes);
     if (rc != cudaSuccess) return rc;
-    gate_kernel<D, KCAP><<<a.n_ent, kThreads, bytes, st>>>(a, words);
+    gate_kernel<D, NS><<<a.n_ent, kThreads, bytes, st>>>(a, words);
     note_launches(1);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(const Attn &a, cudaStream_t st) {
-    // the kept ones, the first dropped one, and the next where there is room
-    if (a.km1 <= 2) return launch<D, 4>(a, st);
-    if (a.km1 <= 6) return launch<D, 8>(a, st);
-    if (a.km1 <= 14) return launch<D, 16>(a, st);
-    return launch<D, 32>(a, st);
+    // ranks: the kept ones, the first dropped one and the next, four to a place
+    if (a.km1 <= 2) return launch<D, 1>(a, st);
+    if (a.km1 <= 6) return launch<D, 2>(a, st);
+    if (a.km1 <= 14) return launch<D, 4>(a, st);
+    return launch<D, 9>(a, st);
+}
+
+template <int D, int NS>
+cudaError_t launch_c(const Attn &a, cudaStream_t st) {
+    const cudaError_t rc = allow_smem<chunk_gate_kernel<D, NS>>(chunk_gate_smem(D, kMaxPastSlots));
+    if (rc != cudaSuccess) return rc;
+    const int tps = (int)(((long long)a.c.max_new * a.G + kChunkRows - 1) / kChunkRows);
+    chunk_gate_kernel<D, NS><<<a.c.num_seqs * tps * a.c.Hkv, kChunkThreads, chunk_gate_smem(D, a.km1),
+                               st>>>(a, tps);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_cd(const Attn &a, cudaStream_t st) {
+    if (a.km1 <= 2) return launch_c<D, 1>(a, st);
+    if (a.km1 <= 6) return launch_c<D, 2>(a, st);
+    if (a.km1 <= 14) return launch_c<D, 4>(a, st);
+    return launch_c<D, 9>(a, st);
 }
 
 }  // namespace
@@ -495,6 +705,10 @@ cudaError_t launch_gate(const Attn &a, cudaStream_t st) {
         return cudaGetLastError();
     }
     return a.D == 64 ? launch_d<64>(a, st) : launch_d<128>(a, st);
+}
+
+cudaError_t launch_chunk_gate(const Attn &a, cudaStream_t st) {
+    return a.D == 64 ? launch_cd<64>(a, st) : launch_cd<128>(a, st);
 }
 
 }  // namespace paged

@@ -507,9 +507,10 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
 }
 
 // Joins the partial sums of an entry (a row tile of a chunk) that starts in one
-// CTA's run and ends in another's.  Four rows to a CTA, four warps to a row:
-// each takes every fourth part, four in flight, and they join in shared memory.
-constexpr int kMergeThreads = 512;
+// CTA's run and ends in another's: 16 rows to a CTA.  Few parts: a warp a row.
+// Many (a long cache of few heads): four warps a row, every fourth part each,
+// joined in shared memory.  Four parts in flight.
+constexpr int kMergeThreads = 512, kMergeRows = 16, kFewParts = 8;
 
 template <int D, bool CHUNK>
 __global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(Attn a) {
@@ -519,87 +520,101 @@ __global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(Attn a) {
     const int first = blockIdx.x, e = a.c_open[first];
     if (e < 0) return;
     const int last = min(a.c_last[e], (int)gridDim.x - 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp & 3;
-    const int r = blockIdx.y * 4 + (warp >> 2), R = CHUNK ? kJobRows : a.rows;
-    bool live;
-    size_t at;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int R = CHUNK ? kJobRows : a.rows;
+    const int W = last - first < kFewParts ? 1 : 4;  // warps to a row
+    const int part = warp % W;
+    Entry x;
+    int row0 = 0, nrows, hk;
     if (CHUNK) {
         const int w = e / a.c.Hkv, b = upper_index(a.own_off, a.c.num_seqs, w);
         Seq s;
         a.c.seq(b, s);
-        const int r0 = (w - a.own_off[b]) * kJobRows + r, row = s.row0 * a.G + r0;
-        live = r0 < s.n * a.G;
-        at = (size_t)(row / a.G) * a.Hq + e % a.c.Hkv * a.G + row % a.G;
+        const int r0 = (w - a.own_off[b]) * kJobRows;
+        row0 = s.row0 * a.G + r0;
+        nrows = min(kJobRows, s.n * a.G - r0);
+        hk = e % a.c.Hkv;
     } else {
-        const Entry x = get_entry(a, e);
-        live = r < x.nt * a.G;
-        at = (size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G;
+        x = get_entry(a, e);
+        row0 = x.row0 * a.G;
+        nrows = x.nt * a.G;
+        hk = x.hk;
     }
-    float M = -INFINITY, L = 0.f, acc[V];
+    for (int pass = 0; pass < W; ++pass) {
+        const int r = blockIdx.y * kMergeRows + pass * (16 / W) + warp / W;
+        const bool live = r < nrows;
+        float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.f;
-    bool bad = false;
-    if (live)
-        for (int c0 = first + part; c0 <= last; c0 += 4 * U) {
-            float2 ml[U];
-            float v[U][V];
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        bool bad = false;
+        if (live)
+            for (int c0 = first + part; c0 <= last; c0 += W * U) {
+                float2 ml[U];
+                float v[U][V];
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int c = c0 + 4 * j;
-                ml[j] = make_float2(-INFINITY, 0.f);
-                if (c <= last) {
-                    const size_t p = (size_t)(2 * c + (c == first)) * R + r;
-                    ml[j] = a.part_ml[p];
+                for (int j = 0; j < U; ++j) {
+                    const int c = c0 + W * j;
+                    ml[j] = make_float2(-INFINITY, 0.f);
+                    if (c <= last) {
+                        const size_t p = (size_t)(2 * c + (c == first)) * R + r;
+                        ml[j] = a.part_ml[p];
 #pragma unroll
-                    for (int k = 0; k < V; k += 2)
-                        *reinterpret_cast<float2 *>(&v[j][k]) =
-                            *reinterpret_cast<const float2 *>(a.part_o + p * D + lane * V + k);
+                        for (int k = 0; k < V; k += 2)
+                            *reinterpret_cast<float2 *>(&v[j][k]) =
+                                *reinterpret_cast<const float2 *>(a.part_o + p * D + lane * V + k);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    bad |= ml[j].y < 0.f;
+                    if (ml[j].y == 0.f) continue;  // no part, or one without a key for this row
+                    const float mn = fmaxf(M, ml[j].x), ref = mn == -INFINITY ? 0.f : mn;
+                    const float f = mma::fast_exp2(M - ref), g = mma::fast_exp2(ml[j].x - ref);
+                    M = mn;
+                    L = fmaf(ml[j].y, g, L * f);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[k] = fmaf(v[j][k], g, acc[k] * f);
                 }
             }
+        if (W > 1) {
+            __syncthreads();  // (the pass before has been read)
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                bad |= ml[j].y < 0.f;
-                if (ml[j].y == 0.f) continue;  // no part, or one without a key for this row
-                const float mn = fmaxf(M, ml[j].x), ref = mn == -INFINITY ? 0.f : mn;
-                const float f = mma::fast_exp2(M - ref), g = mma::fast_exp2(ml[j].x - ref);
-                M = mn;
-                L = fmaf(ml[j].y, g, L * f);
+            for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
+            if (lane == 0) {
+                s_m[warp] = M;
+                s_l[warp] = bad ? -1.f : L;
+            }
+            __syncthreads();
+            if (!live || part) continue;
+            M = -INFINITY;
+            L = 0.f;
+            bad = false;
 #pragma unroll
-                for (int k = 0; k < V; ++k) acc[k] = fmaf(v[j][k], g, acc[k] * f);
+            for (int w = 0; w < 4; ++w) {
+                M = fmaxf(M, s_m[warp + w]);
+                bad |= s_l[warp + w] < 0.f;
+            }
+            const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float f = mma::fast_exp2(s_m[warp + w] - ref);
+                L = fmaf(s_l[warp + w], f, L);
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[k] = fmaf(s_acc[warp + w][lane * V + k], f, acc[k]);
             }
         }
+        if (!live) continue;
+        const int row = row0 + r;
+        const size_t at = (size_t)(row / a.G) * a.Hq + hk * a.G + row % a.G;
+        const float inv = 1.f / L;
 #pragma unroll
-    for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
-    if (lane == 0) {
-        s_m[warp] = M;
-        s_l[warp] = bad ? -1.f : L;
+        for (int k = 0; k < V; k += 2)
+            *reinterpret_cast<uint32_t *>(a.out + at * D + lane * V + k) =
+                bad ? 0u : mma::pack_bf16(acc[k] * inv, acc[k + 1] * inv);
+        if (lane == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
     }
-    __syncthreads();
-    if (!live || part) return;
-    M = -INFINITY;
-    L = 0.f;
-    bad = false;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        M = fmaxf(M, s_m[warp + w]);
-        bad |= s_l[warp + w] < 0.f;
-    }
-    const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float f = mma::fast_exp2(s_m[warp + w] - ref);
-        L = fmaf(s_l[warp + w], f, L);
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = fmaf(s_acc[warp + w][lane * V + k], f, acc[k]);
-    }
-    const float inv = 1.f / L;
-#pragma unroll
-    for (int k = 0; k < V; k += 2)
-        *reinterpret_cast<uint32_t *>(a.out + at * D + lane * V + k) =
-            bad ? 0u : mma::pack_bf16(acc[k] * inv, acc[k + 1] * inv);
-    if (lane == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
 }
 
 template <int D, int RW, int CW>
@@ -638,7 +653,7 @@ cudaError_t launch_rows(const Attn &a, bool after_gate, cudaStream_t st) {
 }
 
 cudaError_t launch_merge_runs(const Attn &a, cudaStream_t st) {
-    const dim3 grid(a.ctas, (a.chunk ? kJobRows : a.rows) / 4);
+    const dim3 grid(a.ctas, (a.chunk ? kJobRows : a.rows) / kMergeRows);
     note_launches(1);
     if (a.D == 64)
         return a.chunk ? launch_after(merge_runs_kernel<64, true>, grid, kMergeThreads, 0, st, a)
@@ -669,7 +684,7 @@ size_t scratch(Attn *a, void *base) {
         a->part_ml = static_cast<float2 *>(take(sizeof(float2) * parts));
         a->part_o = static_cast<float *>(take(sizeof(float) * parts * a->D));
     }
-    if (!a->dense) {
+    if (!a->dense && !a->chunk) {
         a->tiles = static_cast<int *>(take(4 * n));
         a->ublk = static_cast<int *>(take(4 * n * a->ucap));
         a->umask = static_cast<unsigned long long *>(take(8 * n * a->ucap));
@@ -686,7 +701,7 @@ size_t scratch(Attn *a, void *base) {
         a->jobs = static_cast<int2 *>(take(8 * (size_t)a->job_cap));
         a->n_jobs = static_cast<int *>(take(4));
         a->list = static_cast<int *>(take(4 * (size_t)a->list_cap));
-        a->ubase = static_cast<int *>(take(4 * n * a->ucap));
+        a->sel = static_cast<int2 *>(take(8 * (size_t)a->c.total * a->Hq * a->km1));
         a->part_h = static_cast<__half *>(take(sizeof(__half) * slots * a->D));
         a->part_s = static_cast<float4 *>(take(sizeof(float4) * slots));
     }
@@ -727,10 +742,12 @@ int make_attn(Attn *a, int Hq, int D, int topk) {
         const long long w1 = (long long)a->c.total * a->G / kJobRows + a->c.num_seqs;
         a->w_cap = (int)(w0 < w1 ? w0 : w1);
         a->job_cap = a->list_cap / kJobRows + (lists < a->list_cap ? lists : a->list_cap) + 1;
-        if ((long long)a->w_cap * a->c.Hkv >= (1ll << 30)) return MOBA_ERR_UNSUPPORTED;
+        if ((long long)a->w_cap * a->c.Hkv >= (1ll << 30) ||
+            (long long)a->c.num_seqs * (rows / 128 + 1) * a->c.Hkv >= (1ll << 31))
+            return MOBA_ERR_UNSUPPORTED;
     }
-    const long long ucap = (long long)a->rows * (a->km1 + (a->chunk ? 0 : 1));
-    a->ucap = a->dense ? 0 : (int)(ucap < n_max ? (ucap > 0 ? ucap : 1) : n_max);
+    const long long ucap = (long long)a->rows * (a->km1 + 1);
+    a->ucap = a->dense ? 0 : (int)(ucap < n_max ? ucap : n_max);
     a->scale_log2 = (float)(1.4426950408889634 / __builtin_sqrt((double)D));
     return MOBA_OK;
 }
@@ -796,7 +813,7 @@ MOBA_EXPORT int moba_paged_attn(const void *q, const void *k_pages, const void *
     cudaError_t e = cudaSuccess;
     if (a.chunk && !a.dense)
         e = cudaMemsetAsync(a.counts, 0, 4 * (size_t)num_seqs * a.n_max * Hkv, st);
-    if (e == cudaSuccess) e = launch_gate(a, st);
+    if (e == cudaSuccess) e = a.chunk && !a.dense ? launch_chunk_gate(a, st) : launch_gate(a, st);
     const bool gated = !a.dense || a.idx;
     if (e == cudaSuccess && a.chunk) e = launch_plan(a, gated, st);
     if (e == cudaSuccess) e = a.chunk ? launch_chunk(a, st) : launch_rows(a, gated, st);
