@@ -49,6 +49,7 @@ struct Attn {
     int *own_off;               // [num_seqs + 1] 256-row tiles before each sequence
     long long *unit_off;        // [w_cap + 1] key tiles before each row tile (all blocks)
     int *counts;                // [num_seqs][n_max][Hkv] rows that selected the block
+    int *next_job;              // [1] behind them: jobs handed out
     int *list_off;              // [num_seqs * n_max * Hkv + 1]
     int2 *jobs;                 // [job_cap] list, first entry
     int *n_jobs;                // [1]

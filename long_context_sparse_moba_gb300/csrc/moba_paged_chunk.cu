@@ -253,7 +253,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 const int listed = a.km1 > 0 ? *a.n_jobs : 0;
                 const long long all = listed + (long long)tiles * a.c.Hkv;
-                for (long long q = blockIdx.x; go && q < all; q += gridDim.x) {
+                // jobs differ in length: taken as CTAs become free (the next one's
+                // number is fetched while this one is looked up)
+                long long q = (long long)atomicAdd(a.next_job, 1);
+                while (go && q < all) {
+                    const long long after = (long long)atomicAdd(a.next_job, 1);
                     if (q < listed) {
                         const int2 d = a.jobs[q];
                         const int lb = a.list_off[d.x];
@@ -281,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     job_ends<N>(a, J);
                     go = hand(J);
+                    q = after;
                 }
             }
             J.valid = 0;
@@ -886,32 +891,23 @@ __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(Attn a) {
 constexpr int kSlotThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kSlotThreads) merge_slots_kernel(Attn a) {
-    constexpr int GL = D / 8, U = 4, STEP = kSlotThreads / GL;
+__global__ void __launch_bounds__(kSlotThreads, 4) merge_slots_kernel(Attn a, int per) {
+    constexpr int GL = D / 8, U = 4, ROWS = kSlotThreads / GL;
     after_previous();
-    const int e = blockIdx.x, gl = threadIdx.x % GL;
-    const Entry x = get_entry(a, e);
-    if (x.state != kSeqOk) return;  // cleared before
-    const int S = a.km1 + 1, G = a.G;
-    // (token, head) of the row, advanced without divisions; an entry's tokens lie
-    // in two blocks at most
-    int r = threadIdx.x / GL, t = r / G, g = r - t * G;
-    const int dt = STEP / G, dg = STEP - dt * G;
-    const int c0 = x.pos0 / a.c.bs, cut = (c0 + 1) * a.c.bs - x.pos0;
-    for (; r < x.nt * G; r += STEP) {
-        const int row = (x.row0 + t) * G + g;
-        const size_t at = (size_t)(x.row0 + t) * a.Hq + x.hk * G + g;
-        const size_t lin = (size_t)x.hk * a.c.total * G + row, p0 = lin * S;
-        const int n = min(a.km1, c0 + (t >= cut)) + 1;  // slots, the own block's last
-        const bool none = a.km1 > 0 && __ldg(&a.sel[lin * a.km1].x) == kSelBad;
-        t += dt;
-        g += dg;
-        if (g >= G) {
-            g -= G;
-            ++t;
-        }
+    const int gl = threadIdx.x % GL, S = a.km1 + 1, G = a.G;
+    // i: ROWS rows of a sequence on one kv head
+    for (int i = blockIdx.x; i < a.c.num_seqs * per * a.c.Hkv; i += gridDim.x) {
+        const int hk = i % a.c.Hkv, bt = i / a.c.Hkv, b = bt / per;
+        Seq s;
+        if (a.c.seq(b, s) != kSeqOk) continue;  // (refused ones are cleared by the plan)
+        const int r = (bt - b * per) * ROWS + threadIdx.x / GL, t = r / G;
+        if (t >= s.n) continue;
+        const int row = s.row0 * G + r;
+        const size_t at = (size_t)(s.row0 + t) * a.Hq + hk * G + (r - t * G);
+        const size_t lin = (size_t)hk * a.c.total * G + row, p0 = lin * S;
+        const int n = min(a.km1, (s.len - s.n + t) / a.c.bs) + 1;  // slots, the own block's last
+        bool bad = a.km1 > 0 && __ldg(&a.sel[lin * a.km1].x) == kSelBad;
         float M = -INFINITY, W = 0.f, acc[8];
-        bool bad = none;
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[k] = 0.f;
         for (int s0 = 0; s0 < n; s0 += U) {
@@ -993,7 +989,10 @@ cudaError_t launch(const Attn &a, cudaStream_t st) {
     if (rc != cudaSuccess) return rc;
     if (DENSE) return launch_merge_runs(a, st);
     note_launches(1);
-    return launch_after(merge_slots_kernel<D>, a.n_ent, kSlotThreads, 0, st, a);
+    constexpr int ROWS = kSlotThreads / (D / 8);
+    const int per = (int)(((long long)a.c.max_new * a.G + ROWS - 1) / ROWS);
+    const int most = a.c.num_seqs * per * a.c.Hkv, ctas = 4 * a.ctas;
+    return launch_after(merge_slots_kernel<D>, most < ctas ? most : ctas, kSlotThreads, 0, st, a, per);
 }
 
 // keys per tile: 128, or 64 where blocks are no multiple of 128

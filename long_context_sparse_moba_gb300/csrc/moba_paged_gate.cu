@@ -527,15 +527,16 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
 // chunks of many rows
 // ----------------------------------------------------------------------------
 constexpr int kChunkRows = 128, kChunkThreads = 256;
+constexpr int kPlaces = 1024;  // blocks whose rows are counted in shared memory
 
 __host__ __device__ constexpr int chunk_gate_smem(int D, int km1) {
-    return 2 * kTile * D * 2 + 4 * kChunkRows * (km1 + 1);
+    return 2 * kTile * D * 2 + 4 * kChunkRows * (2 * km1 + 1);
 }
 
 template <int D, int NS>
-__global__ void __launch_bounds__(kChunkThreads, NS <= 2 ? 2 : 1) chunk_gate_kernel(Attn a, int tps) {
+__global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : D == 64 ? 3 : 2) chunk_gate_kernel(Attn a, int tps) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int s_bad, s_knmax, s_page[kTile];
+    __shared__ int s_bad, s_knmax, s_page[kTile], s_place[kPlaces];
     __shared__ Unsure<kChunkRows> s_un;
     uint8_t *const hi = smem, *const lo = smem + kTile * D * 2;
     int *sel = reinterpret_cast<int *>(smem + 2 * kTile * D * 2);  // [row][km1 + 1]
@@ -606,9 +607,9 @@ __global__ void __launch_bounds__(kChunkThreads, NS <= 2 ? 2 : 1) chunk_gate_ker
     __syncthreads();
     const bool bad = scored && s_bad;
     if (bad && tid == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-    if (tid >= nrows) return;
-    // each row's selection, ascending, and its places in the blocks' lists
-    const int own = own_of(tid), n = min(km1, own), row = row0 + tid;
+    // each row's selection, ascending
+    const int own = tid < nrows ? own_of(tid) : 0, n = tid < nrows ? min(km1, own) : 0;
+    const int row = row0 + tid;
     int *mine = sel + tid * ss;
     if (own > km1) {
         for (int i = 1; i < n; ++i) {
@@ -620,23 +621,32 @@ __global__ void __launch_bounds__(kChunkThreads, NS <= 2 ? 2 : 1) chunk_gate_ker
     } else {
         for (int i = 0; i < n; ++i) mine[i] = i;
     }
-    if (a.idx) {
+    if (a.idx && tid < nrows) {
         int32_t *dst = a.idx + ((size_t)(row / G) * a.Hq + hk * G + row % G) * a.topk;
         for (int i = 0; i < a.topk; ++i) dst[i] = bad || i > n ? -1 : i < n ? mine[i] : own;
     }
+    // its places in the blocks' lists: counted in shared memory first, then one
+    // global addition per block and CTA (an addition per row and block waits a
+    // third of the kernel for the few hundred counters that all rows share)
+    int *counts = a.counts + (size_t)b * a.n_max * a.c.Hkv + hk;
     int2 *out = a.sel + ((size_t)hk * a.c.total * G + row) * km1;
-    for (int i0 = 0; i0 < km1; i0 += 4) {
-        int c[4], at[4];  // (four in flight)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            c[j] = bad ? kSelBad : i0 + j < n ? mine[i0 + j] : -1;
-            at[j] = c[j] >= 0
-                        ? atomicAdd(a.counts + ((size_t)b * a.n_max + c[j]) * a.c.Hkv + hk, 1)
-                        : 0;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (i0 + j < km1) out[i0 + j] = make_int2(c[j], at[j]);
+    const bool counted = c_own <= kPlaces;
+    int *at = sel + kChunkRows * ss + tid * km1;  // the row's places among this CTA's
+    if (counted) {
+        for (int c = tid; c < c_own; c += kChunkThreads) s_place[c] = 0;
+        __syncthreads();
+        if (!bad)
+            for (int i = 0; i < n; ++i) at[i] = atomicAdd(s_place + mine[i], 1);
+        __syncthreads();
+        for (int c = tid; c < c_own; c += kChunkThreads)
+            if (s_place[c]) s_place[c] = atomicAdd(counts + (size_t)c * a.c.Hkv, s_place[c]);
+        __syncthreads();
+    }
+    if (tid >= nrows) return;
+    for (int i = 0; i < km1; ++i) {
+        const int c = bad ? kSelBad : i < n ? mine[i] : -1;
+        const int place = c < 0 ? 0 : counted ? s_place[c] + at[i] : atomicAdd(counts + (size_t)c * a.c.Hkv, 1);
+        out[i] = make_int2(c, place);
     }
 }
 

@@ -507,10 +507,12 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
 }
 
 // Joins the partial sums of an entry (a row tile of a chunk) that starts in one
-// CTA's run and ends in another's: 16 rows to a CTA.  Few parts: a warp a row.
-// Many (a long cache of few heads): four warps a row, every fourth part each,
-// joined in shared memory.  Four parts in flight.
-constexpr int kMergeThreads = 512, kMergeRows = 16, kFewParts = 8;
+// CTA's run and ends in another's.  Few parts: a warp a row.  Many (a long cache
+// of few heads): four warps a row, every fourth part each, joined in shared
+// memory.  Four parts in flight.  A chunk's tile has 256 rows and seldom many
+// parts, so a CTA takes 64 of them and looks the tile up once.
+constexpr int kMergeThreads = 512, kFewParts = 8;
+__host__ __device__ constexpr int merge_rows(bool chunk) { return chunk ? 64 : 4; }  // of a CTA
 
 template <int D, bool CHUNK>
 __global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(Attn a) {
@@ -540,9 +542,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(Attn a) {
         nrows = x.nt * a.G;
         hk = x.hk;
     }
-    for (int pass = 0; pass < W; ++pass) {
-        const int r = blockIdx.y * kMergeRows + pass * (16 / W) + warp / W;
-        const bool live = r < nrows;
+    for (int r0 = 0; r0 < merge_rows(CHUNK); r0 += 16 / W) {
+        const int r = blockIdx.y * merge_rows(CHUNK) + r0 + warp / W;
+        const bool live = r < nrows && r0 + warp / W < merge_rows(CHUNK);
         float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[k] = 0.f;
@@ -653,7 +655,7 @@ cudaError_t launch_rows(const Attn &a, bool after_gate, cudaStream_t st) {
 }
 
 cudaError_t launch_merge_runs(const Attn &a, cudaStream_t st) {
-    const dim3 grid(a.ctas, (a.chunk ? kJobRows : a.rows) / kMergeRows);
+    const dim3 grid(a.ctas, (a.chunk ? kJobRows : a.rows) / merge_rows(a.chunk));
     note_launches(1);
     if (a.D == 64)
         return a.chunk ? launch_after(merge_runs_kernel<64, true>, grid, kMergeThreads, 0, st, a)
@@ -696,7 +698,8 @@ size_t scratch(Attn *a, void *base) {
     if (a->chunk && !a->dense) {
         const size_t lists = (size_t)a->c.num_seqs * a->n_max * a->c.Hkv;
         const size_t slots = (size_t)a->c.total * a->Hq * (a->km1 + 1);
-        a->counts = static_cast<int *>(take(4 * lists));
+        a->counts = static_cast<int *>(take(4 * (lists + 1)));
+        a->next_job = a->counts + lists;
         a->list_off = static_cast<int *>(take(4 * (lists + 1)));
         a->jobs = static_cast<int2 *>(take(8 * (size_t)a->job_cap));
         a->n_jobs = static_cast<int *>(take(4));
@@ -743,7 +746,7 @@ int make_attn(Attn *a, int Hq, int D, int topk) {
         a->w_cap = (int)(w0 < w1 ? w0 : w1);
         a->job_cap = a->list_cap / kJobRows + (lists < a->list_cap ? lists : a->list_cap) + 1;
         if ((long long)a->w_cap * a->c.Hkv >= (1ll << 30) ||
-            (long long)a->c.num_seqs * (rows / 128 + 1) * a->c.Hkv >= (1ll << 31))
+            (long long)a->c.num_seqs * (rows / 16 + 1) * a->c.Hkv >= (1ll << 31))
             return MOBA_ERR_UNSUPPORTED;
     }
     const long long ucap = (long long)a->rows * (a->km1 + 1);
@@ -812,7 +815,7 @@ MOBA_EXPORT int moba_paged_attn(const void *q, const void *k_pages, const void *
     scratch(&a, workspace);
     cudaError_t e = cudaSuccess;
     if (a.chunk && !a.dense)
-        e = cudaMemsetAsync(a.counts, 0, 4 * (size_t)num_seqs * a.n_max * Hkv, st);
+        e = cudaMemsetAsync(a.counts, 0, 4 * ((size_t)num_seqs * a.n_max * Hkv + 1), st);
     if (e == cudaSuccess) e = a.chunk && !a.dense ? launch_chunk_gate(a, st) : launch_gate(a, st);
     const bool gated = !a.dense || a.idx;
     if (e == cudaSuccess && a.chunk) e = launch_plan(a, gated, st);
