@@ -886,61 +886,65 @@ __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(Attn a) {
 // merge
 // ----------------------------------------------------------------------------
 // A row's slots (its past blocks and its own), weighted by their sums, the
-// weights taken relative to a running maximum: D / 8 lanes a row, 16 bytes of
-// each slot a lane, four slots in flight.  Bound: HBM and L2 (the partials).
+// weights taken relative to a running maximum: D / 16 lanes a row, 32 bytes of
+// each slot a lane, up to four slots in flight.  Bound: HBM and L2 (the partials),
+// then the issue of instructions, so a lane does much per row and index
+// arithmetic is kept to one division.
 constexpr int kSlotThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kSlotThreads, 4) merge_slots_kernel(Attn a, int per) {
-    constexpr int GL = D / 8, U = 4, ROWS = kSlotThreads / GL;
+__global__ void __launch_bounds__(kSlotThreads, 3) merge_slots_kernel(Attn a) {
+    constexpr int GL = D / 16, U = 4, ROWS = kSlotThreads / GL;
     after_previous();
-    const int gl = threadIdx.x % GL, S = a.km1 + 1, G = a.G;
-    // i: ROWS rows of a sequence on one kv head
-    for (int i = blockIdx.x; i < a.c.num_seqs * per * a.c.Hkv; i += gridDim.x) {
-        const int hk = i % a.c.Hkv, bt = i / a.c.Hkv, b = bt / per;
-        Seq s;
-        if (a.c.seq(b, s) != kSeqOk) continue;  // (refused ones are cleared by the plan)
-        const int r = (bt - b * per) * ROWS + threadIdx.x / GL, t = r / G;
-        if (t >= s.n) continue;
-        const int row = s.row0 * G + r;
-        const size_t at = (size_t)(s.row0 + t) * a.Hq + hk * G + (r - t * G);
-        const size_t lin = (size_t)hk * a.c.total * G + row, p0 = lin * S;
-        const int n = min(a.km1, (s.len - s.n + t) / a.c.bs) + 1;  // slots, the own block's last
+    const int hk = blockIdx.y, b = blockIdx.z, gl = threadIdx.x % GL, S = a.km1 + 1, G = a.G;
+    Seq s;
+    if (a.c.seq(b, s) != kSeqOk) return;  // (refused ones are cleared by the plan)
+    const int nrows = s.n * G, first = s.len - s.n, c_first = first / a.c.bs;
+    const size_t base = ((size_t)hk * a.c.total + s.row0) * G;
+    for (int r = blockIdx.x * ROWS + threadIdx.x / GL; r < nrows; r += gridDim.x * ROWS) {
+        const int t = r / G;
+        const size_t lin = base + r, p0 = lin * S;
+        // slots, the own block's last (past blocks are counted from the first token's)
+        int n = a.km1;
+        if (c_first < a.km1) n = min(a.km1, (first + t) / a.c.bs);
+        ++n;
         bool bad = a.km1 > 0 && __ldg(&a.sel[lin * a.km1].x) == kSelBad;
-        float M = -INFINITY, W = 0.f, acc[8];
+        float M = -INFINITY, W = 0.f, acc[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+        for (int k = 0; k < 16; ++k) acc[k] = 0.f;
         for (int s0 = 0; s0 < n; s0 += U) {
             float4 ps[U];
-            uint4 h[U];
+            uint4 h[U][2];
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 if (s0 + j < n) {
                     const size_t p = p0 + (s0 + j < n - 1 ? s0 + j : a.km1);
                     ps[j] = __ldg(a.part_s + p);
-                    h[j] = __ldcs(reinterpret_cast<const uint4 *>(a.part_h + p * D) + gl);
+                    const uint4 *src = reinterpret_cast<const uint4 *>(a.part_h + p * D) + 2 * gl;
+                    h[j][0] = __ldcs(src);
+                    h[j][1] = __ldcs(src + 1);
                 }
             float mx = M;
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 if (s0 + j < n) mx = fmaxf(mx, ps[j].x);
-            if (mx > M) {
+            if (s0 > 0 && mx > M) {
                 const float f = fast_exp2(M - mx);
                 W *= f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) acc[k] *= f;
-                M = mx;
+                for (int k = 0; k < 16; ++k) acc[k] *= f;
             }
+            M = mx;
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 if (s0 + j < n) {
                     bad |= ps[j].w == 0.f;
                     const float w = fast_exp2(ps[j].x - M);
                     W += w;
-                    const float f = w * (gl < 8 ? ps[j].y : ps[j].z);
-                    const __half2 *h2 = reinterpret_cast<const __half2 *>(&h[j]);
+                    const float f = w * (gl < 4 ? ps[j].y : ps[j].z);
+                    const __half2 *h2 = reinterpret_cast<const __half2 *>(h[j]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 8; ++k) {
                         const float2 v = __half22float2(h2[k]);
                         acc[2 * k] = fmaf(v.x, f, acc[2 * k]);
                         acc[2 * k + 1] = fmaf(v.y, f, acc[2 * k + 1]);
@@ -948,12 +952,16 @@ __global__ void __launch_bounds__(kSlotThreads, 4) merge_slots_kernel(Attn a, in
                 }
         }
         const float inv = 1.f / W;
-        uint4 o;
-        __nv_bfloat162 *o2 = reinterpret_cast<__nv_bfloat162 *>(&o);
+        uint4 o[2];
+        __nv_bfloat162 *o2 = reinterpret_cast<__nv_bfloat162 *>(o);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o2[k] = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-        if (bad) o = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(a.out + at * D + gl * 8) = o;
+        for (int k = 0; k < 8; ++k)
+            o2[k] = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+        if (bad) o[0] = o[1] = make_uint4(0, 0, 0, 0);
+        const size_t at = (size_t)(s.row0 + t) * a.Hq + hk * G + (r - t * G);
+        uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D) + 2 * gl;
+        dst[0] = o[0];
+        dst[1] = o[1];
         if (gl == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(W)) * 0.69314718055994530942f;
     }
 }
@@ -989,10 +997,11 @@ cudaError_t launch(const Attn &a, cudaStream_t st) {
     if (rc != cudaSuccess) return rc;
     if (DENSE) return launch_merge_runs(a, st);
     note_launches(1);
-    constexpr int ROWS = kSlotThreads / (D / 8);
-    const int per = (int)(((long long)a.c.max_new * a.G + ROWS - 1) / ROWS);
-    const int most = a.c.num_seqs * per * a.c.Hkv, ctas = 4 * a.ctas;
-    return launch_after(merge_slots_kernel<D>, most < ctas ? most : ctas, kSlotThreads, 0, st, a, per);
+    constexpr int ROWS = kSlotThreads / (D / 16);
+    const long long tiles = ((long long)a.c.max_new * a.G + ROWS - 1) / ROWS;
+    const long long fill = (3 * a.ctas + a.c.Hkv - 1) / a.c.Hkv;
+    const dim3 grid((unsigned)(tiles < fill ? tiles : fill), a.c.Hkv, a.c.num_seqs);
+    return launch_after(merge_slots_kernel<D>, grid, kSlotThreads, 0, st, a);
 }
 
 // keys per tile: 128, or 64 where blocks are no multiple of 128

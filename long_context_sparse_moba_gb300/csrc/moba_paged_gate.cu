@@ -273,33 +273,37 @@ __device__ __forceinline__ void load_pooled(const Attn &a, int hk, const int *ta
         if (cb + tid < c_end && !ok) *s_bad = 1;
     }
     __syncthreads();
-    float4 f[NR];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const int page = s_page[i * (T / LR) + tid / LR];
-        f[i] = page < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
-                        : __ldg(reinterpret_cast<const float4 *>(
-                                    a.kbar + ((size_t)page * a.c.Hkv + hk) * D) + tid % LR);
-    }
+    constexpr int HALF = NR > 4 ? NR / 2 : NR;  // loads in flight
     float kn = 0.f;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const int r = i * (T / LR) + tid / LR;
-        const float v[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
-        __nv_bfloat16 h[4], l[4];
-        float n2 = 0.f;
+    for (int i0 = 0; i0 < NR; i0 += HALF) {
+        float4 f[HALF];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            h[k] = __float2bfloat16(v[k]);
-            l[k] = __float2bfloat16(v[k] - __bfloat162float(h[k]));
-            n2 = fmaf(v[k], v[k], n2);
+        for (int i = 0; i < HALF; ++i) {
+            const int page = s_page[(i0 + i) * (T / LR) + tid / LR];
+            f[i] = page < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : __ldg(reinterpret_cast<const float4 *>(
+                                        a.kbar + ((size_t)page * a.c.Hkv + hk) * D) + tid % LR);
         }
-        const uint32_t at = swz<D>(r, (tid % LR) >> 1) + (tid & 1) * 8;
-        *reinterpret_cast<uint2 *>(hi + at) = *reinterpret_cast<uint2 *>(h);
-        *reinterpret_cast<uint2 *>(lo + at) = *reinterpret_cast<uint2 *>(l);
 #pragma unroll
-        for (int o = LR / 2; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
-        kn = n2 > kn || n2 != n2 ? n2 : kn;
+        for (int i = 0; i < HALF; ++i) {
+            const int r = (i0 + i) * (T / LR) + tid / LR;
+            const float v[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
+            __nv_bfloat16 h[4], l[4];
+            float n2 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                h[k] = __float2bfloat16(v[k]);
+                l[k] = __float2bfloat16(v[k] - __bfloat162float(h[k]));
+                n2 = fmaf(v[k], v[k], n2);
+            }
+            const uint32_t at = swz<D>(r, (tid % LR) >> 1) + (tid & 1) * 8;
+            *reinterpret_cast<uint2 *>(hi + at) = *reinterpret_cast<uint2 *>(h);
+            *reinterpret_cast<uint2 *>(lo + at) = *reinterpret_cast<uint2 *>(l);
+#pragma unroll
+            for (int o = LR / 2; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+            kn = n2 > kn || n2 != n2 ? n2 : kn;
+        }
     }
     // a NaN norm has the largest bits of all
     if (tid % LR == 0) atomicMax(s_knmax, __float_as_int(fabsf(sqrtf(kn))));
@@ -534,7 +538,7 @@ __host__ __device__ constexpr int chunk_gate_smem(int D, int km1) {
 }
 
 template <int D, int NS>
-__global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : D == 64 ? 3 : 2) chunk_gate_kernel(Attn a, int tps) {
+__global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kernel(Attn a, int tps) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_bad, s_knmax, s_page[kTile], s_place[kPlaces];
     __shared__ Unsure<kChunkRows> s_un;
@@ -573,10 +577,10 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : D == 64 ? 3 : 2) c
     auto own_of = [&](int r) -> int { return ((row0 + r) / G + pdelta) / bs; };
     const bool scored = km1 > 0 && c_own > km1;
     if (scored) {
-        uint32_t qa[D / 16][4];
-        float q2[2];
+        float q2[2] = {0.f, 0.f};
         const int rq = warp * 16 + (lane >> 2);  // the quad's first row
-        load_q<D>(rq < nrows ? q_of(rq) : nullptr, rq + 8 < nrows ? q_of(rq + 8) : nullptr, qa, q2);
+        const __nv_bfloat16 *q0 = rq < nrows ? q_of(rq) : nullptr;
+        const __nv_bfloat16 *q1 = rq + 8 < nrows ? q_of(rq + 8) : nullptr;
         const int ci[2] = {rq < nrows ? own_of(rq) : 0, rq + 8 < nrows ? own_of(rq + 8) : 0};
         Best<NS> best[2];
         best[0].clear();
@@ -588,7 +592,11 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : D == 64 ? 3 : 2) c
             __syncthreads();
             if (warp * 16 < nrows) {
                 float acc[8][4];
-                score_tile<D>(qa, s_hi, s_lo, acc);
+                {   // (q read again for each tile: its registers are free for the ranks)
+                    uint32_t qa[D / 16][4];
+                    load_q<D>(q0, q1, qa, q2);
+                    score_tile<D>(qa, s_hi, s_lo, acc);
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) best[h].rank(acc, h, cb, ci[h], km1 + 2);
             }
