@@ -46,16 +46,21 @@ int make_cache(Cache *c, const void *k_pages, const void *v_pages, const float *
 // ----------------------------------------------------------------------------
 // append
 // ----------------------------------------------------------------------------
-// One CTA per (block of a sequence that the new tokens touch, kv head, k or v):
-// it copies the block's new tokens to their pages (16 bytes a lane) and, for k,
+// A cluster of four CTAs per (block of a sequence that the new tokens touch, kv
+// head): it copies the block's new tokens to their pages (16 bytes a lane) and,
 // when the block is complete with them, sums the block's keys: the new ones as
-// they pass through its registers, the earlier ones from the cache.  So a
-// chunk's keys are read once and one launch does both.
-// Thread (column c, group g) takes the tokens with p % G == g of the block,
-// ascending, whatever their source: a pooled key does not depend on how the
-// appends were cut.  Sums are compensated (Kahan), as in the key pooling
-// kernel.  Bound: HBM.
+// they pass through its registers, the earlier ones from the cache.  So a chunk's
+// keys are read once and one launch does both.
+// Thread (column, group g of 64 in the cluster) takes the tokens with p % 64 == g
+// of the block, ascending, whatever their source: a pooled key does not depend on
+// how the appends were cut.  Sums are compensated (Kahan), as in the key pooling
+// kernel; the first CTA reads the others' through distributed shared memory.
+// Bound: HBM for chunks, latency for a step: the step that completes a block
+// reads all of its keys, which four CTAs do in two rounds of loads (one CTA's
+// rounds took twice the time of the whole call now).
 constexpr int kAppendThreads = 256;
+constexpr int kAppendCtas = 4;      // of a cluster
+constexpr int kAppendPages = 512;
 
 struct AppendArgs {
     Cache c;
@@ -63,16 +68,42 @@ struct AppendArgs {
     __nv_bfloat16 *kp, *vp;
     float *kbar;
     int cand;  // blocks that a sequence's new tokens touch, at most
+    int psh;   // log2(page size)
     int *status;
 };
 
+// the address of the same shared variable in CTA `rank` of the cluster
+__device__ __forceinline__ float peer_load(const float *p, int rank) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(at)
+        : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// (s, c) += x, compensated
+__device__ __forceinline__ void kahan(float &s, float &c, float x) {
+    const float y = x - c, t = s + y;
+    c = (t - s) - y;
+    s = t;
+}
+
 template <int D, bool MAX>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
-    constexpr int CW = D / 8;                     // threads across a token
-    constexpr int G = kAppendThreads / CW;        // tokens in flight
+    constexpr int CW = D / 8;                        // threads across a token
+    constexpr int GC = kAppendThreads / CW;          // groups of a CTA
+    constexpr int G = GC * kAppendCtas;
+    constexpr int U = 4;
     __shared__ float red[kAppendThreads][9];
-    const int b = blockIdx.x / a.cand, hk = blockIdx.y;
-    const bool is_k = blockIdx.z == 0;
+    __shared__ float s_sum[D], s_bad;
+    __shared__ int s_page[kAppendPages];
+    const int rank = blockIdx.x % kAppendCtas, bj = blockIdx.x / kAppendCtas;
+    const int b = bj / a.cand, hk = blockIdx.y;
     Seq s;
     const int state = a.c.seq(b, s);
     if (state != kSeqOk) {
@@ -81,15 +112,21 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     }
     const int bs = a.c.bs, ps = a.c.ps;
     const int first = s.len - s.n;  // position of the first new token
-    const int p0 = (first / bs + (int)(blockIdx.x % a.cand)) * bs;
+    const int p0 = (first / bs + bj % a.cand) * bs;
     if (p0 >= s.len) return;
-    const bool pool = is_k && a.kbar && p0 + bs <= s.len;
-    const int col = threadIdx.x % CW, g = threadIdx.x / CW;
+    const bool pool = a.kbar && p0 + bs <= s.len;
     const int c1 = min(p0 + bs, s.len);
     const int t0 = pool ? p0 : max(p0, first);  // first token that is read
-    const __nv_bfloat16 *src = is_k ? a.k : a.v;
-    __nv_bfloat16 *pages = is_k ? a.kp : a.vp;
+    const int col = threadIdx.x % CW, g = rank * GC + threadIdx.x / CW;
     const int *table = a.c.table + (size_t)b * a.c.max_pages;
+    // the block's pages, looked up once (a block of more pages than the array
+    // holds looks them up as it goes)
+    const int g0 = t0 >> a.psh, gn = ((c1 - 1) >> a.psh) + 1 - g0;
+    const bool held = gn <= kAppendPages;
+    if (held) {
+        for (int i = threadIdx.x; i < gn; i += kAppendThreads) s_page[i] = __ldg(table + g0 + i);
+        __syncthreads();
+    }
     float acc[8], comp[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -97,79 +134,85 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
         comp[e] = 0.f;
     }
     bool bad = false;
-    constexpr int U = 8;
     for (int pb = t0 - (t0 - p0) % G + g; pb < c1; pb += U * G) {
-        uint4 x[U];
-        __nv_bfloat16 *dst[U];
+        uint4 x[U], y[U];
+        size_t at[U];
         bool live[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const int p = pb + j * G;
             live[j] = p >= t0 && p < c1;
             if (live[j]) {
-                const int page = __ldg(table + p / ps);
+                const int page = held ? s_page[(p >> a.psh) - g0] : __ldg(table + (p >> a.psh));
                 live[j] = (unsigned)page < (unsigned)a.c.num_pages;
                 bad |= !live[j];
-                dst[j] = pages + (((size_t)page * a.c.Hkv + hk) * ps + p % ps) * D + col * 8;
+                at[j] = ((((size_t)page * a.c.Hkv + hk) << a.psh) + (p & (ps - 1))) * D + col * 8;
             }
-            if (live[j])
-                x[j] = p >= first
-                           ? __ldcs(reinterpret_cast<const uint4 *>(
-                                 src + ((size_t)(s.row0 + p - first) * a.c.Hkv + hk) * D + col * 8))
-                           : *reinterpret_cast<const uint4 *>(dst[j]);
+            if (live[j] && p >= first) {
+                const size_t src = ((size_t)(s.row0 + p - first) * a.c.Hkv + hk) * D + col * 8;
+                x[j] = __ldcs(reinterpret_cast<const uint4 *>(a.k + src));
+                y[j] = __ldcs(reinterpret_cast<const uint4 *>(a.v + src));
+            } else if (live[j]) {
+                x[j] = *reinterpret_cast<const uint4 *>(a.kp + at[j]);
+            }
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (!live[j]) continue;
-            if (pb + j * G >= first) *reinterpret_cast<uint4 *>(dst[j]) = x[j];
+            if (pb + j * G >= first) {
+                *reinterpret_cast<uint4 *>(a.kp + at[j]) = x[j];
+                *reinterpret_cast<uint4 *>(a.vp + at[j]) = y[j];
+            }
             if (pool) {
                 const __nv_bfloat162 *p2 = reinterpret_cast<const __nv_bfloat162 *>(&x[j]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float f = e & 1 ? __high2float(p2[e >> 1]) : __low2float(p2[e >> 1]);
-                    if (MAX) {
-                        acc[e] = fmaxf(acc[e], f);
-                    } else {
-                        const float y = f - comp[e];
-                        const float t = acc[e] + y;
-                        comp[e] = (t - acc[e]) - y;
-                        acc[e] = t;
-                    }
+                    if (MAX) acc[e] = fmaxf(acc[e], f);
+                    else kahan(acc[e], comp[e], f);
                 }
             }
         }
     }
     bad = __syncthreads_or(bad);
     if (bad && threadIdx.x == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-    if (!pool || bad) return;
+    if (!pool) return;
+    // (all four CTAs of the cluster alike from here on)
 #pragma unroll
     for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = acc[e];
+    if (threadIdx.x == 0) s_bad = bad ? 1.f : 0.f;
     __syncthreads();
     if (threadIdx.x < D) {
         const int c8 = threadIdx.x / 8, e = threadIdx.x % 8;
-        float sum = red[c8][e];
-        if (MAX) {
-            for (int x = 1; x < G; ++x) sum = fmaxf(sum, red[x * CW + c8][e]);
-        } else {
-            float cp = 0.f;
-            for (int x = 1; x < G; ++x) {
-                const float y = red[x * CW + c8][e] - cp;
-                const float t = sum + y;
-                cp = (t - sum) - y;
-                sum = t;
-            }
-            sum /= (float)bs;
+        float sum = red[c8][e], cp = 0.f;
+        for (int x = 1; x < GC; ++x) {
+            if (MAX) sum = fmaxf(sum, red[x * CW + c8][e]);
+            else kahan(sum, cp, red[x * CW + c8][e]);
         }
-        const int page = __ldg(table + (p0 + bs) / ps - 1);
-        a.kbar[((size_t)page * a.c.Hkv + hk) * D + threadIdx.x] = sum;
+        s_sum[threadIdx.x] = sum;
     }
+    cluster_barrier();
+    if (rank == 0 && threadIdx.x < D) {
+        float sum = s_sum[threadIdx.x], cp = 0.f, any = s_bad;
+#pragma unroll
+        for (int r = 1; r < kAppendCtas; ++r) {
+            const float x = peer_load(s_sum + threadIdx.x, r);
+            if (MAX) sum = fmaxf(sum, x);
+            else kahan(sum, cp, x);
+            any += peer_load(&s_bad, r);
+        }
+        if (!MAX) sum /= (float)bs;
+        const int page = __ldg(table + ((p0 + bs) >> a.psh) - 1);
+        if (any == 0.f) a.kbar[((size_t)page * a.c.Hkv + hk) * D + threadIdx.x] = sum;
+    }
+    cluster_barrier();  // the others' shared memory has been read
 }
 
 // ----------------------------------------------------------------------------
 // page copy
 // ----------------------------------------------------------------------------
-// CTA (i, part) copies its part of pair i in every layer, 16 bytes a lane with
-// several loads in flight.  Each CTA first looks its pair up in the whole
+// A CTA copies a part of one pair in one layer, 16 bytes a lane with several
+// loads in flight.  Each CTA first looks its pair up in the whole
 // destination list: a destination given twice, or a source that some pair
 // overwrites, would make the result depend on the order.
 constexpr int kCopyThreads = 256;
@@ -177,7 +220,7 @@ constexpr int kCopyThreads = 256;
 struct CopyArgs {
     uint4 *k, *v, *kbar;  // kbar may be null
     const int *src, *dst;
-    int n, layers, num_pages, parts;
+    int n, num_pages, parts;
     long long page16, bar16;  // 16-byte units of a page of k (or v), of a pooled key slot
     int *status;
 };
@@ -199,7 +242,7 @@ __device__ __forceinline__ void copy_run(const uint4 *__restrict__ s, uint4 *__r
 }
 
 __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(CopyArgs a) {
-    const int i = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+    const int i = blockIdx.x / a.parts, part = blockIdx.x % a.parts, l = blockIdx.y;
     const int src = __ldg(a.src + i), dst = __ldg(a.dst + i);
     bool bad = (unsigned)src >= (unsigned)a.num_pages || (unsigned)dst >= (unsigned)a.num_pages;
     for (int j = threadIdx.x; j < a.n; j += kCopyThreads) {
@@ -210,21 +253,27 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(CopyArgs a) {
         if (threadIdx.x == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
         return;
     }
-    for (int l = 0; l < a.layers; ++l) {
-        const long long s = (long long)l * a.num_pages + src, d = (long long)l * a.num_pages + dst;
-        copy_run(a.k + s * a.page16, a.k + d * a.page16, a.page16, part, a.parts);
-        copy_run(a.v + s * a.page16, a.v + d * a.page16, a.page16, part, a.parts);
-        if (a.kbar) copy_run(a.kbar + s * a.bar16, a.kbar + d * a.bar16, a.bar16, part, a.parts);
-    }
+    const long long s = (long long)l * a.num_pages + src, d = (long long)l * a.num_pages + dst;
+    copy_run(a.k + s * a.page16, a.k + d * a.page16, a.page16, part, a.parts);
+    copy_run(a.v + s * a.page16, a.v + d * a.page16, a.page16, part, a.parts);
+    if (a.kbar) copy_run(a.kbar + s * a.bar16, a.kbar + d * a.bar16, a.bar16, part, a.parts);
 }
 
 template <int D>
 static cudaError_t launch_append(const AppendArgs &a, bool max, cudaStream_t st) {
-    const dim3 grid(a.c.num_seqs * a.cand, a.c.Hkv, 2);
-    if (max) append_kernel<D, true><<<grid, kAppendThreads, 0, st>>>(a);
-    else append_kernel<D, false><<<grid, kAppendThreads, 0, st>>>(a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.c.num_seqs * a.cand * kAppendCtas, a.c.Hkv);
+    cfg.blockDim = kAppendThreads;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = kAppendCtas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
     note_launches(1);
-    return cudaGetLastError();
+    return max ? cudaLaunchKernelEx(&cfg, append_kernel<D, true>, a)
+               : cudaLaunchKernelEx(&cfg, append_kernel<D, false>, a);
 }
 
 }  // namespace paged
@@ -257,8 +306,9 @@ MOBA_EXPORT int moba_paged_append(const void *k, const void *v, void *k_pages, v
     a.kp = static_cast<__nv_bfloat16 *>(k_pages);
     a.vp = static_cast<__nv_bfloat16 *>(v_pages);
     a.kbar = kbar_pages;
+    a.psh = __builtin_ctz((unsigned)page_size);
     a.cand = (int)(((long long)a.c.max_new + block_size - 2) / block_size + 1);
-    if ((long long)num_seqs * a.cand >= (1ll << 31)) return MOBA_ERR_UNSUPPORTED;
+    if ((long long)num_seqs * a.cand >= (1ll << 31) / kAppendCtas) return MOBA_ERR_UNSUPPORTED;
     a.status = status_word();
     if (!a.status) return cuda_result(cudaErrorInvalidDevice);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -277,7 +327,7 @@ MOBA_EXPORT int moba_page_copy(void *k_pages, void *v_pages, float *kbar_pages, 
     if ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 3)
         return MOBA_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return MOBA_ERR_UNSUPPORTED;
-    if (Hkv > 65535 || page_size > (1 << 20) ||
+    if (Hkv > 65535 || layers > 65535 || page_size > (1 << 20) ||
         (long long)Hkv * page_size * D > (1ll << 40) / num_pages / layers)
         return MOBA_ERR_UNSUPPORTED;
     CopyArgs a;
@@ -287,7 +337,6 @@ MOBA_EXPORT int moba_page_copy(void *k_pages, void *v_pages, float *kbar_pages, 
     a.src = src;
     a.dst = dst;
     a.n = n;
-    a.layers = layers;
     a.num_pages = num_pages;
     a.page16 = (long long)Hkv * page_size * D / 8;
     a.bar16 = (long long)Hkv * D / 4;
@@ -295,12 +344,13 @@ MOBA_EXPORT int moba_page_copy(void *k_pages, void *v_pages, float *kbar_pages, 
     if (!a.status) return cuda_result(cudaErrorInvalidDevice);
     // enough CTAs to fill the GPU; a part is at least 16 KB of a page
     const long long fill = (long long)sm_count() * 8;
-    long long parts = (fill + n - 1) / n;
+    long long parts = (fill + (long long)n * layers - 1) / ((long long)n * layers);
     const long long most = (a.page16 + 1023) / 1024;
     if (parts > most) parts = most;
     a.parts = (int)parts;
     if ((long long)n * parts >= (1ll << 31)) return MOBA_ERR_UNSUPPORTED;
-    page_copy_kernel<<<(unsigned)(n * parts), kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    page_copy_kernel<<<dim3((unsigned)(n * parts), layers), kCopyThreads, 0,
+                       static_cast<cudaStream_t>(stream)>>>(a);
     note_launches(1);
     return cuda_result(cudaGetLastError());
 }

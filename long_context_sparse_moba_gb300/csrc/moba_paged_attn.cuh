@@ -49,10 +49,9 @@ struct Attn {
     int *own_off;               // [num_seqs + 1] 256-row tiles before each sequence
     long long *unit_off;        // [w_cap + 1] key tiles before each row tile (all blocks)
     int *counts;                // [num_seqs][n_max][Hkv] rows that selected the block
-    int *next_job;              // [1] behind them: jobs handed out
     int *list_off;              // [num_seqs * n_max * Hkv + 1]
-    int2 *jobs;                 // [job_cap] list, first entry
-    int *n_jobs;                // [1]
+    int2 *jobs, *halves;        // [job_cap] list, first entry: of up to 256 rows, of up to 128
+    int *n_jobs;                // [3] how many of each, and how many jobs are handed out
     int *list;                  // rows of each list: (token * G + head) << 5 | slot
     int2 *sel;                  // [Hkv][total * G][km1] a row's past blocks, ascending (-1: none, and
                                 // kSelBad: a page outside the pool), and its place in the block's list

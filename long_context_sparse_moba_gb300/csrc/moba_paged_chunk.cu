@@ -11,8 +11,10 @@
 // head are numbered token * G + head, so that a job's 256 rows share its keys
 // whatever the group size.  Jobs:
 //   with selection: (1) up to 256 rows that selected one past block of one kv
-//     head, from its list; (2) up to 256 consecutive rows with the keys of
-//     their own blocks.  Each writes, for a row and slot, a normalised partial
+//     head, from its list; the last rows of a list, where they are 128 at most,
+//     share a job with another list's, each with its own keys, so that one Q
+//     tile's MMAs still run under the other's softmax; (2) up to 256 consecutive
+//     rows with the keys of their own blocks.  Each writes, for a row and slot, a normalised partial
 //     output and its log2-sum-exp; the merge kernel joins a row's slots.
 //     Partials are fp16 with a power-of-two scale per row and 64 columns: half
 //     the bytes of fp32, and 2^-11 of a value is a fraction of the rounding of
@@ -55,18 +57,23 @@ constexpr int kTmemCols = 512;
 constexpr int kJobs = 3;         // descriptors in flight
 constexpr int kBadSlots = 8;
 
-struct Job {
-    int valid;
-    int own;         // consecutive rows (else a list)
+// One Q tile's share of a job.
+struct Half {
     int b, hk;
-    int nrows;
-    int rbase;       // first row, or first entry of the list
-    int key0;        // position of key tile 0
-    int key_end;     // keys from here on are seen by no row
-    int lo, nt;      // first key tile of this job's part, and how many
-    int te[kG];      // tiles of the part that Q tile g visits
-    int pdelta;      // own: position of a row = its token + pdelta
+    int rbase;       // own: first row; list: first entry
+    int nrows;       // of its 128
+    int key0;        // position of the keys' first tile
+    int te;          // tiles that it visits
     int rlo, rn;     // list: the sequence's rows [rlo, rlo + rn)
+};
+struct Job {
+    Half h[kG];
+    int valid;
+    int own;         // consecutive rows (else lists)
+    int pair;        // the Q tiles have rows of two lists, and their own keys each
+    int key_end;     // own: keys from here on are seen by no row
+    int lo, nt;      // first key tile of this job's part, and how many
+    int pdelta;      // own: position of a row = its token + pdelta
     int whole;       // all blocks: the part is the whole job
     int slot;        // all blocks: partial slot
     int pad[3];
@@ -104,41 +111,57 @@ struct Smem {
     static constexpr uint32_t kRequest = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
 };
 
-// The part [lo, lo + nt) of the key tiles of 256-row tile x of sequence b on kv head hk.
+// The job of the 256-row tile x of sequence b on kv head hk, all its key tiles.
 template <int N>
 __device__ __forceinline__ void own_job(const Attn &a, const Seq &s, int b, int hk, int x, Job &J) {
-    const int r0 = x * kJobRows;
+    const int r0 = x * kJobRows, nrows = min(kJobRows, s.n * a.G - r0);
     J.valid = 1;
     J.own = 1;
-    J.b = b;
-    J.hk = hk;
-    J.nrows = min(kJobRows, s.n * a.G - r0);
-    J.rbase = s.row0 * a.G + r0;
+    J.pair = 0;
     J.pdelta = s.len - s.n - s.row0;
-    const int pf = s.len - s.n + r0 / a.G, pl = s.len - s.n + (r0 + J.nrows - 1) / a.G;
-    J.key0 = a.dense ? 0 : pf / a.c.bs * a.c.bs;
+    const int pf = s.len - s.n + r0 / a.G, pl = s.len - s.n + (r0 + nrows - 1) / a.G;
+    const int key0 = a.dense ? 0 : pf / a.c.bs * a.c.bs;
     J.key_end = pl + 1;
     J.lo = 0;
-    J.nt = (pl - J.key0) / N + 1;
+    J.nt = (pl - key0) / N + 1;
     J.whole = 1;
     J.slot = 0;
-    J.rlo = J.rn = 0;
-}
-
-// Q tile g's share of the part's tiles: those up to its last row.
-template <int N>
-__device__ __forceinline__ void job_ends(const Attn &a, Job &J) {
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-        if (J.nrows <= g * kM) {
-            J.te[g] = 0;
-        } else if (!J.own) {
-            J.te[g] = J.nt;
-        } else {
-            const int last = (J.rbase + min(J.nrows, (g + 1) * kM) - 1) / a.G + J.pdelta;
-            J.te[g] = min(max((last - J.key0) / N + 1 - J.lo, 0), J.nt);
-        }
+        J.h[g].b = b;
+        J.h[g].hk = hk;
+        J.h[g].rbase = s.row0 * a.G + r0 + g * kM;
+        J.h[g].nrows = min(max(nrows - g * kM, 0), kM);
+        J.h[g].key0 = key0;
+        J.h[g].rlo = J.h[g].rn = 0;
     }
+}
+
+// A Q tile's share of the part's tiles: those up to its last row.
+template <int N>
+__device__ __forceinline__ void own_ends(const Attn &a, Job &J) {
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+        const int last = (J.h[g].rbase + J.h[g].nrows - 1) / a.G + J.pdelta;
+        J.h[g].te = J.h[g].nrows > 0 ? min(max((last - J.h[g].key0) / N + 1 - J.lo, 0), J.nt) : 0;
+    }
+}
+
+// Up to 128 rows of a list, from entry `start` on, as a Q tile's share.
+template <int N>
+__device__ __forceinline__ void list_half(const Attn &a, int l, int start, Half &h) {
+    const int lb = a.list_off[l];
+    h.hk = l % a.c.Hkv;
+    const int bc = l / a.c.Hkv;
+    h.b = bc / a.n_max;
+    h.rbase = lb + start;
+    h.nrows = min(max(a.list_off[l + 1] - lb - start, 0), kM);
+    h.key0 = (bc - h.b * a.n_max) * a.c.bs;
+    h.te = h.nrows > 0 ? a.c.bs / N : 0;
+    Seq s;
+    a.c.seq(h.b, s);
+    h.rlo = s.row0 * a.G;
+    h.rn = s.n * a.G;
 }
 
 template <int D, int N, bool DENSE>
@@ -161,8 +184,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *bad_job = reinterpret_cast<volatile int *>(gmisc + L::kBad);
     Job *ring = reinterpret_cast<Job *>(gmisc + L::kJob);
     Ctl ctl{abort_flag, a.status, ca.wait_limit};
-    after_previous();
-    let_next();
 
     if (tid == 0) {
         for (int g = 0; g < kG; ++g) {
@@ -198,6 +219,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (tid == 0)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
+    if (tid == 320)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
+    after_previous();
+    let_next();
 
     if (warp == 11) {
         // ================= job descriptors =================
@@ -234,13 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int T = J.nt;
                         for (; go && u < u1 && u < a.unit_off[w + 1];) {
                             const long long in = u - a.unit_off[w];
-                            J.hk = (int)(in / T);
-                            J.lo = (int)(in - (long long)J.hk * T);
+                            const int hk = (int)(in / T);
+                            J.h[0].hk = J.h[1].hk = hk;
+                            J.lo = (int)(in - (long long)hk * T);
                             J.nt = (int)min((long long)(T - J.lo), u1 - u);
                             J.whole = J.nt == T;
                             J.slot = blockIdx.x * 2 + (J.lo == 0 ? 1 : 0);
-                            job_ends<N>(a, J);
-                            const int e = w * a.c.Hkv + J.hk;
+                            own_ends<N>(a, J);
+                            const int e = w * a.c.Hkv + hk;
                             if (J.lo + J.nt == T) a.c_last[e] = blockIdx.x;
                             else if (J.lo == 0) open = e;
                             go = hand(J);
@@ -251,39 +279,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 a.c_open[blockIdx.x] = open;
             } else {
-                const int listed = a.km1 > 0 ? *a.n_jobs : 0;
+                // jobs: 256 rows of a list; pairs of lists' last rows, up to 128
+                // each; own blocks
+                const int full = a.km1 > 0 ? a.n_jobs[0] : 0, halves = a.km1 > 0 ? a.n_jobs[1] : 0;
+                const int listed = full + (halves + 1) / 2;
                 const long long all = listed + (long long)tiles * a.c.Hkv;
                 // jobs differ in length: taken as CTAs become free (the next one's
                 // number is fetched while this one is looked up)
-                long long q = (long long)atomicAdd(a.next_job, 1);
+                long long q = atomicAdd(a.n_jobs + 2, 1);
                 while (go && q < all) {
-                    const long long after = (long long)atomicAdd(a.next_job, 1);
+                    const long long after = atomicAdd(a.n_jobs + 2, 1);
                     if (q < listed) {
-                        const int2 d = a.jobs[q];
-                        const int lb = a.list_off[d.x];
                         J.valid = 1;
                         J.own = 0;
-                        J.hk = d.x % a.c.Hkv;
-                        J.b = d.x / a.c.Hkv / a.n_max;
-                        J.nrows = min(kJobRows, a.list_off[d.x + 1] - lb - d.y);
-                        J.rbase = lb + d.y;
-                        J.key0 = (d.x / a.c.Hkv % a.n_max) * a.c.bs;
-                        J.key_end = J.key0 + a.c.bs;
+                        J.key_end = 0x7fffffff;
                         J.lo = 0;
                         J.nt = a.c.bs / N;
                         J.pdelta = 0;
                         J.whole = 1;
                         J.slot = 0;
-                        a.c.seq(J.b, sq);
-                        J.rlo = sq.row0 * a.G;
-                        J.rn = sq.n * a.G;
+                        if (q < full) {
+                            const int2 d = a.jobs[q];
+                            list_half<N>(a, d.x, d.y, J.h[0]);
+                            list_half<N>(a, d.x, d.y + kM, J.h[1]);
+                            J.pair = 0;
+                        } else {
+                            const int h = 2 * (int)(q - full);
+                            const int2 d = a.halves[h];
+                            list_half<N>(a, d.x, d.y, J.h[0]);
+                            J.pair = h + 1 < halves;
+                            if (J.pair) {
+                                const int2 f = a.halves[h + 1];
+                                list_half<N>(a, f.x, f.y, J.h[1]);
+                                // (an empty one: only where refused sequences spoilt the counts)
+                                if (J.h[0].te == 0) J.h[0] = J.h[1], J.pair = 0;
+                                else if (J.h[1].te == 0) J.pair = 0;
+                            }
+                            if (!J.pair) {
+                                J.h[1] = J.h[0];
+                                J.h[1].nrows = J.h[1].te = 0;
+                            }
+                        }
                     } else {
                         const int w = (int)((q - listed) / a.c.Hkv);
                         const int b = upper_index(a.own_off, a.c.num_seqs, w);
                         a.c.seq(b, sq);
                         own_job<N>(a, sq, b, (int)((q - listed) % a.c.Hkv), w - __ldg(a.own_off + b), J);
+                        own_ends<N>(a, J);
                     }
-                    job_ends<N>(a, J);
                     go = hand(J);
                     q = after;
                 }
@@ -309,30 +352,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Job J = ring[js];
                 mbar_arrive(bar(L::kBarJE + js));
                 if (!J.valid) break;
-                const int *table = a.c.table + (size_t)J.b * a.c.max_pages;
                 bool ok = true;
-                for (int j = 0; j < J.nt; ++j, ++t) {
+                const int tiles_of_job = J.pair ? 2 * J.nt : J.nt;
+                for (int j = 0; j < tiles_of_job; ++j, ++t) {
                     const int s = t % ST;
+                    // (a pair's Q tiles take their tiles in turn)
+                    const int g = J.pair ? j & 1 : 0, i0 = J.pair ? j >> 1 : j;
+                    const int hb = g ? J.h[1].b : J.h[0].b, hk = g ? J.h[1].hk : J.h[0].hk;
+                    const int p0 = (g ? J.h[1].key0 : J.h[0].key0) + (J.lo + i0) * N;
+                    const int *table = a.c.table + (size_t)hb * a.c.max_pages;
+                    const int nv = min(N, J.key_end - p0);  // keys that some row sees
+                    const int boxes = (nv + box - 1) / box;
+                    int page[N / 16];
+#pragma unroll
+                    for (int i = 0; i < N / 16; ++i)
+                        if (i < boxes) page[i] = __ldg(table + ((p0 + i * box) >> ca.psh));
                     if (t >= ST && !wait_bar(bar(bempty + s), (t / ST - 1) & 1, ctl)) {
                         ok = false;
                         break;
                     }
                     pend[s] = -1;
-                    const int p0 = J.key0 + (J.lo + j) * N;
-                    const int nv = min(N, J.key_end - p0);  // keys that some row sees
-                    const int boxes = (nv + box - 1) / box;
                     mbar_expect_tx(bar(bfull + s), (uint32_t)(boxes * box) * 128u * L::NB);
-                    for (int i = 0; i < boxes; ++i) {
-                        const int p = p0 + i * box;
-                        int page = __ldg(table + (p >> ca.psh));
-                        if ((unsigned)page >= (unsigned)a.c.num_pages) {
-                            page = 0;  // some memory of the pool; the job's results are dropped
+#pragma unroll
+                    for (int i = 0; i < N / 16; ++i) {
+                        if (i >= boxes) continue;
+                        if ((unsigned)page[i] >= (unsigned)a.c.num_pages) {
+                            page[i] = 0;  // some memory of the pool; the job's results are dropped
                             if (is_k) {
                                 bad_job[n % kBadSlots] = n + 1;
                                 __threadfence_block();
                             }
                         }
-                        const int row = (page * a.c.Hkv + J.hk) * ps + (p & (ps - 1));
+                        const int row = (page[i] * a.c.Hkv + hk) * ps + ((p0 + i * box) & (ps - 1));
 #pragma unroll
                         for (int x = 0; x < L::NB; ++x)
                             asm volatile(
@@ -360,77 +411,98 @@ __global__ void __launch_bounds__(kThreads, 1)
             int t = 0;
             int gt[kG] = {0, 0};  // S tiles of each Q tile so far
             bool ok = true;
+            // descriptors of the first tiles; the address field counts 16 bytes
+            const uint64_t qd0 = sdesc(sQ, 16, 1024), kd0 = sdesc(sK, 16, 1024),
+                           vd0 = sdesc(sV, L::kKVBox, 1024);
+            // O_g += P_g V of tile i of Q tile g, V described by vd; P_g is in the first
+            // columns of S_g (a job's first P is made after the last job's O was read)
+            auto pv = [&](int g, int i, int te, uint64_t vd) -> bool {
+                if (!wait_poll(bar(L::kBarP + g), (gt[g] + i) & 1, ctl)) return false;
+                tc_fence_after();
+                const uint32_t tS = tmem + g * 256, tO = tS + 128;
+                const uint32_t more = i > 0;
+                tc_mma_ta(tO, tS, vd, idesc_o, more);
+#pragma unroll
+                for (int k = 1; k < N / 16; ++k) tc_mma_ta(tO, tS + k * 8, vd + k * 128, idesc_o, 1u);
+                if (i == te - 1) tc_commit(bar(L::kBarPV + g));
+                return true;
+            };
+            // S_g = Q_g K^T of tile i of Q tile g, K described by kd
+            auto qk = [&](int g, int i, int te, uint64_t kd, int n) -> bool {
+                if (i == 0) {
+                    if (!wait_poll(bar(L::kBarQ + g), n & 1, ctl)) return false;
+                    fence_proxy_async();
+                    tc_fence_after();
+                }
+                const uint32_t tS = tmem + g * 256;
+                const uint64_t qd = qd0 + g * (L::NB * L::kQBox / 16);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tc_mma(tS, qd + (k / 4) * (L::kQBox / 16) + (k % 4) * 2,
+                           kd + (k / 4) * (L::kKVBox / 16) + (k % 4) * 2, idesc_s, k > 0);
+                tc_commit(bar(L::kBarS + g));
+                if (i == te - 1) tc_commit(bar(L::kBarQE + g));
+                return true;
+            };
+            auto kd = [&](int s) { return kd0 + (uint64_t)(s * (L::kTileBytes / 16)); };
+            auto vd = [&](int s) { return vd0 + (uint64_t)(s * (L::kTileBytes / 16)); };
+            auto ready = [&](int full, int s, int tile) {
+                return wait_poll(bar(full + s), (tile / ST) & 1, ctl);
+            };
             for (int n = 0; ok; ++n) {
                 const int js = n % kJobs;
                 if (!wait_poll(bar(L::kBarJF + js), (n / kJobs) & 1, ctl)) break;
-                const Job J = ring[js];
+                const Job *R = ring + js;
+                const int te[kG] = {R->h[0].te, R->h[1].te}, nt = R->nt;
+                const bool valid = R->valid, pair = R->pair;
                 mbar_arrive(bar(L::kBarJE + js));
-                if (!J.valid) break;
+                if (!valid) break;
                 // a Q tile without tiles in this job is released at once
 #pragma unroll
                 for (int g = 0; g < kG; ++g)
-                    if (ok && J.te[g] == 0) {
+                    if (ok && te[g] == 0) {
                         ok = wait_poll(bar(L::kBarQ + g), n & 1, ctl);
                         if (ok) mbar_arrive(bar(L::kBarQE + g));
                     }
-                for (int j = 0; ok && j <= J.nt; ++j) {
-                    const int tk = t + j, s = tk % ST, tp = tk - 1, sp = (tp + ST) % ST, jp = j - 1;
-                    if (j < J.nt) {
-                        if (!wait_poll(bar(L::kBarKF + s), (tk / ST) & 1, ctl)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                    }
-                    if (jp >= 0 && !wait_poll(bar(L::kBarVF + sp), (tp / ST) & 1, ctl)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t kb = sK + s * L::kTileBytes, vb = sV + sp * L::kTileBytes;
+                if (pair) {  // each Q tile has its own keys
+                    for (int i = 0; ok && i <= nt; ++i) {
 #pragma unroll
-                    for (int g = 0; g < kG; ++g) {
-                        const uint32_t tS = tmem + g * 256, tO = tS + 128;
-                        if (ok && jp >= 0 && jp < J.te[g]) {
-                            // O_g += P_g V, P_g in the first columns of S_g (the warps
-                            // make a job's first P after they have read the last job's O)
-                            if (!wait_poll(bar(L::kBarP + g), (gt[g] + jp) & 1, ctl)) {
-                                ok = false;
-                                break;
+                        for (int g = 0; g < kG; ++g) {
+                            const int tk = t + 2 * i + g, tv = tk - 2, sk = tk % ST, sv = (tv + 2 * ST) % ST;
+                            if (ok && i > 0) {
+                                ok = ready(L::kBarVF, sv, tv) && pv(g, i - 1, nt, vd(sv));
+                                if (ok) tc_commit(bar(L::kBarVE + sv));
                             }
-                            tc_fence_after();
-#pragma unroll
-                            for (int k = 0; k < N / 16; ++k)
-                                tc_mma_ta(tO, tS + k * 8, sdesc(vb + k * 2048, L::kKVBox, 1024), idesc_o,
-                                          (jp > 0 || k > 0) ? 1u : 0u);
-                            if (jp == J.te[g] - 1) tc_commit(bar(L::kBarPV + g));
-                        }
-                        if (ok && j < J.nt && j < J.te[g]) {
-                            if (j == 0) {
-                                if (!wait_poll(bar(L::kBarQ + g), n & 1, ctl)) {
-                                    ok = false;
-                                    break;
-                                }
-                                fence_proxy_async();
+                            if (ok && i < nt) {
+                                ok = ready(L::kBarKF, sk, tk);
                                 tc_fence_after();
+                                if (ok) ok = qk(g, i, nt, kd(sk), n);
+                                if (ok) tc_commit(bar(L::kBarKE + sk));
                             }
-                            const uint32_t qb = sQ + g * L::NB * L::kQBox;
-#pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint32_t off = (uint32_t)(k % 4) * 32;
-                                tc_mma(tS, sdesc(qb + (k / 4) * L::kQBox + off, 16, 1024),
-                                       sdesc(kb + (k / 4) * L::kKVBox + off, 16, 1024), idesc_s, k > 0);
-                            }
-                            tc_commit(bar(L::kBarS + g));
-                            if (j == J.te[g] - 1) tc_commit(bar(L::kBarQE + g));
                         }
                     }
-                    if (!ok) break;
-                    if (j < J.nt) tc_commit(bar(L::kBarKE + s));
-                    if (jp >= 0) tc_commit(bar(L::kBarVE + sp));
-                }
-                t += J.nt;
+                } else {
+                    for (int i = 0; ok && i <= nt; ++i) {
+                        const int tk = t + i, sk = tk % ST, sv = (sk + ST - 1) % ST;
+                        const uint64_t kdi = kd(sk), vdi = vd(sv);
+                        if (i < nt) {
+                            ok = ready(L::kBarKF, sk, tk);
+                            tc_fence_after();
+                        }
+                        if (ok && i > 0) ok = ready(L::kBarVF, sv, tk - 1);
 #pragma unroll
-                for (int g = 0; g < kG; ++g) gt[g] += J.te[g];
+                        for (int g = 0; g < kG; ++g) {
+                            if (ok && i > 0 && i <= te[g]) ok = pv(g, i - 1, te[g], vdi);
+                            if (ok && i < nt && i < te[g]) ok = qk(g, i, te[g], kdi, n);
+                        }
+                        if (!ok) break;
+                        if (i < nt) tc_commit(bar(L::kBarKE + sk));
+                        if (i > 0) tc_commit(bar(L::kBarVE + sv));
+                    }
+                }
+                t += pair ? 2 * nt : nt;
+#pragma unroll
+                for (int g = 0; g < kG; ++g) gt[g] += te[g];
             }
             tc_commit(bar(L::kBarDrain));
             drain_bar(bar(L::kBarDrain), 0, ca.wait_limit);
@@ -439,20 +511,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ================= softmax (warps 2..9) =================
         const int g = (warp - 2) >> 2, quarter = warp & 3;
-        const int jrow = g * kM + quarter * 32 + lane;  // row inside the job
+        const int trow = quarter * 32 + lane;  // row inside the Q tile
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_off + g * 256, tO = tS + 128;
         const uint32_t sQg = sQ + g * L::NB * L::kQBox;
         const uint32_t stg = base + L::kStage + (uint32_t)(warp - 2) * 4096u;
         const int S = a.km1 + 1;
+        // what the Q tile's warps need of a job
+        struct Mine {
+            Half h;
+            int valid, own, key_end, lo, pdelta, whole, slot, tiles;
+        };
         // this thread's row of a job: row << 5 | slot
-        auto entry_of = [&](const Job &J) -> int {
-            if (jrow >= J.nrows) return -1;
-            if (J.own) return (J.rbase + jrow) << 5 | a.km1;
+        auto entry_of = [&](const Mine &J) -> int {
+            if (trow >= J.h.nrows) return -1;
+            if (J.own) return (J.h.rbase + trow) << 5 | a.km1;
             // (two sequences that claim the same rows, from offsets that decrease,
             // spoil one another's lists: such an entry is no row)
-            const int e = __ldg(a.list + J.rbase + jrow);
-            return (unsigned)((e >> 5) - J.rlo) < (unsigned)J.rn && (e & 31) < a.km1 ? e : -1;
+            const int e = __ldg(a.list + J.h.rbase + trow);
+            return (unsigned)((e >> 5) - J.h.rlo) < (unsigned)J.h.rn && (e & 31) < a.km1 ? e : -1;
         };
         auto q_row = [&](int hk, int entry) -> size_t {
             const int row = entry >> 5;
@@ -477,36 +554,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             cp_async_arrive_noinc(bar(L::kBarQ + g));
         };
-        auto take = [&](int n, Job &J) -> bool {
+        auto take = [&](int n, Mine &J) -> bool {
             const int js = n % kJobs;
             if (!__all_sync(0xffffffffu, wait_bar(bar(L::kBarJF + js), (n / kJobs) & 1, ctl))) return false;
-            J = ring[js];
+            const Job &R = ring[js];
+            J.h = R.h[g];
+            J.valid = R.valid;
+            J.own = R.own;
+            J.key_end = R.key_end;
+            J.lo = R.lo;
+            J.pdelta = R.pdelta;
+            J.whole = R.whole;
+            J.slot = R.slot;
+            J.tiles = R.pair ? 2 * R.nt : R.nt;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::kBarJE + js));
             return true;
         };
         int gt = 0, gj = 0, t = 0, n = 0;
-        Job J;
+        Mine J;
         bool ok = take(0, J);
         int entry = -1;
         if (ok && J.valid) {
             entry = entry_of(J);
-            gather(J.hk, entry);
+            gather(J.h.hk, entry);
         }
         while (ok && J.valid) {
-            const int ntile = g == 0 ? J.te[0] : J.te[1];
-            // positions that this row sees: [lo, hi]
-            int lo = 0, hi = J.key_end - 1;
+            const int ntile = J.h.te;
+            // own blocks: positions that this row sees, [lo, hi]; a list's rows see
+            // their block whole
+            int lo = 0, hi = 0x7fffffff, lo_max = 0, hi_min = 0x7fffffff;
             if (J.own) {
                 hi = (entry >> 5) / a.G + J.pdelta;
                 if (!DENSE) lo = hi / a.c.bs * a.c.bs;
-            }
-            int lo_max = lo, hi_min = hi;
-            if (J.own) {  // over the Q tile's rows: consecutive, so the last and the first one
-                const int first = (J.rbase + g * kM) / a.G + J.pdelta;
-                const int last = (J.rbase + min(J.nrows, (g + 1) * kM) - 1) / a.G + J.pdelta;
-                hi_min = first;
-                lo_max = DENSE ? 0 : last / a.c.bs * a.c.bs;
+                // over the Q tile's rows: consecutive, so the first's and the last's
+                hi_min = J.h.rbase / a.G + J.pdelta;
+                if (!DENSE)
+                    lo_max = ((J.h.rbase + J.h.nrows - 1) / a.G + J.pdelta) / a.c.bs * a.c.bs;
             }
             float m_run = -INFINITY, l_run = 0.f;
             const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
@@ -516,20 +600,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const int key0 = J.key0 + (J.lo + j) * N;
-                const bool mask = key0 + N - 1 > hi_min || key0 < lo_max || key0 + N > J.key_end;
+                const int key0 = J.h.key0 + (J.lo + j) * N;
+                const bool mask_hi = key0 + N - 1 > hi_min, mask_lo = key0 < lo_max;
 #pragma unroll 1
                 for (int h2 = 0; h2 < N / 64; ++h2) {
                     uint32_t sr[2][32];
                     tc_ld32(tS + 64 * h2, sr[0]);
                     tc_ld32(tS + 64 * h2 + 32, sr[1]);
                     tc_wait_ld();
-                    if (mask) {
+                    if (mask_hi) {
+                        const int top = hi - key0 - 64 * h2;  // last column that the row sees
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) {
-                            const int p = key0 + 64 * h2 + c;
-                            if (p > hi || p < lo) sr[c >> 5][c & 31] = 0xff800000u;
-                        }
+                        for (int c = 0; c < 64; ++c)
+                            if (c > top) sr[c >> 5][c & 31] = 0xff800000u;
+                    }
+                    if (!DENSE && mask_lo) {
+                        const int bottom = lo - key0 - 64 * h2;
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (c < bottom) sr[c >> 5][c & 31] = 0xff800000u;
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -592,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_st32(tS + 32 * h2, pk);
                     l_run += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
                 }
-                if (key0 + N > J.key_end) {
+                if (J.own && key0 + N > J.key_end) {
                     // keys that no row sees: zeros in V (both Q tiles' warps write
                     // the same zeros, each before its own product)
                     const int tv = t + j;
@@ -615,9 +704,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             gt += ntile;
-            t += J.nt;
+            t += J.tiles;
             // the next job's rows, as soon as this job's S MMAs have read Q
-            Job NJ;
+            Mine NJ;
             if (!take(n + 1, NJ)) {
                 ok = false;
                 break;
@@ -629,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                gather(NJ.hk, next_entry);
+                gather(NJ.h.hk, next_entry);
             }
             // ---------------- results ----------------
             const bool bad = bad_job[n % kBadSlots] == n + 1;
@@ -645,8 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float lse2 = m_run + __log2f(l_run);
                 if (!DENSE || J.whole) {
                     // 64 columns a pass, 128 bytes of each row: fp16 with a scale, or the bf16 result
-                    const size_t at = DENSE ? q_row(J.hk, max(entry, 0))
-                                            : ((size_t)J.hk * a.c.total * a.G + (max(entry, 0) >> 5)) * S +
+                    const size_t at = DENSE ? q_row(J.h.hk, max(entry, 0))
+                                            : ((size_t)J.h.hk * a.c.total * a.G + (max(entry, 0) >> 5)) * S +
                                                   (max(entry, 0) & 31);
                     uint16_t *dst0 = DENSE ? reinterpret_cast<uint16_t *>(a.out) : reinterpret_cast<uint16_t *>(a.part_h);
                     const unsigned long long mine =
@@ -720,19 +809,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int it = 0; it < 8; ++it) {
                             const int r = it * 4 + (lane >> 3), ch = lane & 7;
                             const uint4 val = ld_shared_v4(stg + r * 128 + ((uint32_t)(ch ^ (r & 7)) << 4));
-                            if (g * kM + quarter * 32 + r < J.nrows)
+                            if (quarter * 32 + r < J.h.nrows)
                                 *reinterpret_cast<uint4 *>(prow + (size_t)r * D + c0 + ch * 4) = val;
                         }
                         __syncwarp();
                     }
                     if (entry >= 0)
-                        a.part_ml[(size_t)J.slot * kJobRows + jrow] = make_float2(m_run, bad ? -1.f : l_run);
+                        a.part_ml[(size_t)J.slot * kJobRows + g * kM + trow] = make_float2(m_run, bad ? -1.f : l_run);
                 }
                 // O may be overwritten
                 tc_fence_before();
             } else if (DENSE && entry >= 0) {
                 // rows that see nothing of this part
-                a.part_ml[(size_t)J.slot * kJobRows + jrow] = make_float2(-INFINITY, bad ? -1.f : 0.f);
+                a.part_ml[(size_t)J.slot * kJobRows + g * kM + trow] = make_float2(-INFINITY, bad ? -1.f : 0.f);
             }
             ++n;
             J = NJ;
@@ -804,7 +893,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
         if (b < a.c.num_seqs) a.own_off[b + 1] = (int)min(run + inc, (long long)a.w_cap);
         run += total;
     }
-    if (tid == 0) a.own_off[0] = 0;
+    if (tid == 0) {
+        a.own_off[0] = 0;
+        if (!a.dense) a.n_jobs[2] = 0;
+    }
     __threadfence_block();
     __syncthreads();
     const int tiles = (int)min(run, (long long)a.w_cap);
@@ -833,30 +925,40 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
         return;
     }
     if (a.km1 == 0) return;
-    // offsets of the lists, and a job for every 256 rows of one
+    // offsets of the lists, a job for every 256 rows of one, and the last rows: a
+    // job where they are more than 128, else half of one
     const long long lists = (long long)a.c.num_seqs * a.n_max * a.c.Hkv;
     const long long per = (lists + kPlanThreads - 1) / kPlanThreads;
     const long long l0 = min(per * tid, lists), l1 = min(l0 + per, lists);
-    long long rows = 0, jobs = 0;
+    long long rows = 0, jobs = 0, halves = 0;
     for (long long l = l0; l < l1; ++l) {
-        const int n = a.counts[l];
+        const int n = a.counts[l], rest = n % kJobRows;
         rows += n;
-        jobs += (n + kJobRows - 1) / kJobRows;
+        jobs += n / kJobRows + (rest > kM);
+        halves += rest > 0 && rest <= kM;
     }
     long long row = block_scan(rows, warps, total) - rows;
     const long long all_rows = total;
-    long long job = block_scan(jobs, warps, total) - jobs;
+    // (jobs and halves in one scan: both stay below 2^31)
+    const long long inc = block_scan(jobs << 32 | halves, warps, total) - (jobs << 32 | halves);
+    long long job = inc >> 32, half = inc & 0xffffffffll;
     for (long long l = l0; l < l1; ++l) {
         const int n = a.counts[l];
         a.list_off[l] = (int)min(row, a.list_cap);
-        for (int s = 0; s < n; s += kJobRows, ++job)
+        int s = 0;
+        for (; n - s > kM; s += kJobRows, ++job)
             if (job < a.job_cap) a.jobs[job] = make_int2((int)l, s);
+        if (s < n) {
+            if (half < a.job_cap) a.halves[half] = make_int2((int)l, s);
+            ++half;
+        }
         row += n;
     }
     // (more rows than the tensors hold: only from offsets that overlap, refused ones among them)
     if (tid == 0) {
         a.list_off[lists] = (int)min(all_rows, a.list_cap);
-        *a.n_jobs = (int)min(total, a.job_cap);
+        a.n_jobs[0] = (int)min(total >> 32, a.job_cap);
+        a.n_jobs[1] = (int)min(total & 0xffffffffll, a.job_cap);
     }
 }
 

@@ -698,11 +698,11 @@ size_t scratch(Attn *a, void *base) {
     if (a->chunk && !a->dense) {
         const size_t lists = (size_t)a->c.num_seqs * a->n_max * a->c.Hkv;
         const size_t slots = (size_t)a->c.total * a->Hq * (a->km1 + 1);
-        a->counts = static_cast<int *>(take(4 * (lists + 1)));
-        a->next_job = a->counts + lists;
+        a->counts = static_cast<int *>(take(4 * lists));
         a->list_off = static_cast<int *>(take(4 * (lists + 1)));
         a->jobs = static_cast<int2 *>(take(8 * (size_t)a->job_cap));
-        a->n_jobs = static_cast<int *>(take(4));
+        a->halves = static_cast<int2 *>(take(8 * (size_t)a->job_cap));
+        a->n_jobs = static_cast<int *>(take(12));
         a->list = static_cast<int *>(take(4 * (size_t)a->list_cap));
         a->sel = static_cast<int2 *>(take(8 * (size_t)a->c.total * a->Hq * a->km1));
         a->part_h = static_cast<__half *>(take(sizeof(__half) * slots * a->D));
@@ -815,7 +815,7 @@ MOBA_EXPORT int moba_paged_attn(const void *q, const void *k_pages, const void *
     scratch(&a, workspace);
     cudaError_t e = cudaSuccess;
     if (a.chunk && !a.dense)
-        e = cudaMemsetAsync(a.counts, 0, 4 * ((size_t)num_seqs * a.n_max * Hkv + 1), st);
+        e = cudaMemsetAsync(a.counts, 0, 4 * (size_t)num_seqs * a.n_max * Hkv, st);
     if (e == cudaSuccess) e = a.chunk && !a.dense ? launch_chunk_gate(a, st) : launch_gate(a, st);
     const bool gated = !a.dense || a.idx;
     if (e == cudaSuccess && a.chunk) e = launch_plan(a, gated, st);

@@ -1,9 +1,9 @@
 """Appending to a paged cache and copying its pages.
 
 Stored keys and values and copied pages are exact.  A pooled key is a
-compensated fp32 sum of bf16 values in two levels and one division: each level
+compensated fp32 sum of bf16 values in three levels and one division: each level
 errs by at most 2 u of the sum of magnitudes (u = 2^-24), the division by u, so
-|error| <= 6 u mean|k|."""
+|error| <= 8 u mean|k|."""
 import pytest
 import torch
 
@@ -92,7 +92,7 @@ def test_append_in_uneven_chunks(hkv, d, page, block, pooling):
                 assert torch.equal(c.kbar[slot].double(), x.amax(0))
             else:
                 err = (c.kbar[slot].double() - x.mean(0)).abs()
-                assert (err <= 6 * 2.0 ** -24 * x.abs().mean(0)).all()
+                assert (err <= 8 * 2.0 ** -24 * x.abs().mean(0)).all()
     # nothing else was written, and the cuts made no difference
     for pool in (c.k, c.v):
         assert pool.transpose(1, 2)[~written].isnan().all()
