@@ -13,9 +13,10 @@
 // score's place (another 2^-16 |q||k|), and each round of a maximum over the
 // lanes yields the next best; the topk + 1 best of the tiles before compete again.
 // (A list kept by insertion costs several times the instructions.)
-// Where the last kept and the first dropped score are more than 2 E apart, E =
-// 2^-13 |q| max|k| (plus a term for pooled keys so small that lo underflows), the
-// selection is settled; the other rows (two in a hundred on random keys, all of
+// The three errors add up to 2^-14 |q||k|.  Where the last kept and the first
+// dropped score are more than 2 E apart, E = 1.1 2^-14 |q| max|k| (plus a term for
+// pooled keys so small that lo underflows), the selection is settled; the other
+// rows (one or two in a hundred on random keys, all of
 // them when keys tie) are decided by a warp with 64-bit scores, so that the
 // selection is the one of 64-bit arithmetic: scores of the topk best by fp32 where
 // the next one lies 2 E below the boundary, else of all blocks within 3 E of it.
@@ -107,34 +108,58 @@ __device__ __noinline__ int pick64(const Attn &a, int hk, const int *table, cons
     return who;
 }
 
-// The same among n given blocks, in any order.
+// The same among n given blocks, in any order; four at a time, their loads and
+// sums side by side (one after the other they took a fifth of the kernel).
 template <int D>
 __device__ __noinline__ int pick64_of(const Attn &a, int hk, const int *table, const __nv_bfloat16 *qr,
                                       const int *ids, int n) {
+    constexpr int U = 4, DL = D / 32;
     const int lane = threadIdx.x & 31, ppb = a.c.bs / a.c.ps;
+    double q[DL];
+#pragma unroll
+    for (int d = 0; d < DL; ++d) q[d] = (double)__bfloat162float(qr[32 * d + lane]);
     double best = -INFINITY;
     int who = sel::kEmpty;
-    for (int i = 0; i < n; ++i) {
-        const int c = ids[i], page = __ldg(table + (c + 1) * ppb - 1);
-        if ((unsigned)page >= (unsigned)a.c.num_pages) continue;
-        const float *kb = a.kbar + ((size_t)page * a.c.Hkv + hk) * D;
-        double s = 0.0;
+    for (int i0 = 0; i0 < n; i0 += U) {
+        int c[U];
+        float k[U][DL];
+        double s[U];
 #pragma unroll
-        for (int d = 0; d < D; d += 32)
-            s = fma((double)__bfloat162float(qr[d + lane]), (double)__ldg(kb + d + lane), s);
+        for (int u = 0; u < U; ++u) {
+            c[u] = i0 + u < n ? ids[i0 + u] : sel::kEmpty;
+            const int page = i0 + u < n ? __ldg(table + (c[u] + 1) * ppb - 1) : -1;
+            if ((unsigned)page >= (unsigned)a.c.num_pages) c[u] = sel::kEmpty;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (s != s) s = -INFINITY;
-        const int at = __popc(__ballot_sync(
-            0xffffffffu, who != sel::kEmpty && (best > s || (best == s && who < c))));
-        const double pb = __shfl_up_sync(0xffffffffu, best, 1);
-        const int pw = __shfl_up_sync(0xffffffffu, who, 1);
-        if (lane > at) {
-            best = pb;
-            who = pw;
-        } else if (lane == at) {
-            best = s;
-            who = c;
+            for (int d = 0; d < DL; ++d)
+                k[u][d] = c[u] == sel::kEmpty
+                              ? 0.f
+                              : __ldg(a.kbar + ((size_t)page * a.c.Hkv + hk) * D + 32 * d + lane);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            s[u] = 0.0;
+#pragma unroll
+            for (int d = 0; d < DL; ++d) s[u] = fma(q[d], (double)k[u][d], s[u]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (c[u] == sel::kEmpty) continue;  // (every lane alike)
+            if (s[u] != s[u]) s[u] = -INFINITY;
+            const int at = __popc(__ballot_sync(
+                0xffffffffu, who != sel::kEmpty && (best > s[u] || (best == s[u] && who < c[u]))));
+            const double pb = __shfl_up_sync(0xffffffffu, best, 1);
+            const int pw = __shfl_up_sync(0xffffffffu, who, 1);
+            if (lane > at) {
+                best = pb;
+                who = pw;
+            } else if (lane == at) {
+                best = s[u];
+                who = c[u];
+            }
         }
     }
     return who;
@@ -248,7 +273,7 @@ __device__ __forceinline__ void decide(const Best<NS> &best, int r, int own, int
 #pragma unroll
     for (int i = 0; i < NS; ++i)
         if (4 * i + (lane & 3) <= km1) sel[r * (km1 + 1) + 4 * i + (lane & 3)] = best.blk[i];
-    const float err = sqrtf(q2) * fmaf(knmax, 1.220703125e-4f, 1e-34f);
+    const float err = sqrtf(q2) * fmaf(knmax, 6.72e-5f, 1e-34f);
     if ((lane & 3) == 0 && !(kept - dropped > 2.f * err)) {
         const int u = atomicAdd(&un.n, 1);
         un.row[u] = r;
