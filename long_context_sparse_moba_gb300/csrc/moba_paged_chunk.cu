@@ -732,14 +732,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const float inv = 1.f / l_run;
                 const float lse2 = m_run + __log2f(l_run);
-                if (!DENSE || J.whole) {
-                    // 64 columns a pass, 128 bytes of each row: fp16 with a scale, or the bf16 result
-                    const size_t at = DENSE ? q_row(J.h.hk, max(entry, 0))
-                                            : ((size_t)J.h.hk * a.c.total * a.G + (max(entry, 0) >> 5)) * S +
-                                                  (max(entry, 0) & 31);
-                    uint16_t *dst0 = DENSE ? reinterpret_cast<uint16_t *>(a.out) : reinterpret_cast<uint16_t *>(a.part_h);
-                    const unsigned long long mine =
-                        entry >= 0 ? reinterpret_cast<unsigned long long>(dst0 + at * D) : 0ull;
+                if constexpr (!DENSE) {
+                    // fp16 with a scale, 64 columns a pass, straight from the row's
+                    // thread in whole 32-byte sectors (through shared memory, for whole
+                    // lines, this took three times the instructions, and a tenth of the
+                    // kernel)
+                    const size_t at = ((size_t)J.h.hk * a.c.total * a.G + (max(entry, 0) >> 5)) * S +
+                                      (max(entry, 0) & 31);
+                    __half *dst = a.part_h + at * D;
                     float back[2] = {0.f, 0.f};
 #pragma unroll
                     for (int c0 = 0; c0 < D; c0 += 64) {
@@ -747,32 +747,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_ld32(tO + c0, o[0]);
                         tc_ld32(tO + c0 + 32, o[1]);
                         tc_wait_ld();
-                        float f = inv;
-                        if (!DENSE) {
-                            float mx = 0.f;
+                        float mx[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int c = 0; c < 64; ++c)
-                                mx = fmaxf(mx, fabsf(__uint_as_float(o[c >> 5][c & 31]) * inv));
-                            // the largest value into [2^14, 2^15)
-                            const int ex = min(max((__float_as_int(mx) >> 23) & 255, 15), 254);
-                            f = inv * __int_as_float((268 - ex) << 23);
-                            back[c0 / 64] = __int_as_float((ex - 14) << 23);
+                        for (int c = 0; c < 64; ++c)
+                            mx[c & 3] = fmaxf(mx[c & 3], fabsf(__uint_as_float(o[c >> 5][c & 31])));
+                        // the largest value into [2^14, 2^15)
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * inv;
+                        const int ex = min(max((__float_as_int(top) >> 23) & 255, 15), 254);
+                        const float f = inv * __int_as_float((268 - ex) << 23);
+                        back[c0 / 64] = __int_as_float((ex - 14) << 23);
+                        const float2 f2 = make_float2(f, f), zero = make_float2(0.f, 0.f);
+                        uint32_t w[32];
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float2 x = ffma2(
+                                make_float2(__uint_as_float(o[(2 * c) >> 5][(2 * c) & 31]),
+                                            __uint_as_float(o[(2 * c + 1) >> 5][(2 * c + 1) & 31])),
+                                f2, zero);
+                            __half2 hh = __floats2half2_rn(x.x, x.y);
+                            w[c] = *reinterpret_cast<uint32_t *>(&hh);
                         }
+                        if (entry >= 0) {
+#pragma unroll
+                            for (int c = 0; c < 32; c += 8)
+                                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(
+                                                 dst + c0 + 2 * c),
+                                             "r"(w[c]), "r"(w[c + 1]), "r"(w[c + 2]), "r"(w[c + 3]),
+                                             "r"(w[c + 4]), "r"(w[c + 5]), "r"(w[c + 6]), "r"(w[c + 7])
+                                             : "memory");
+                        }
+                    }
+                    if (entry >= 0)
+                        a.part_s[at] = make_float4(lse2, back[0], back[1], bad ? 0.f : 1.f);
+                } else if (J.whole) {
+                    // the bf16 result, 64 columns a pass, 128 bytes of each row
+                    const size_t at = q_row(J.h.hk, max(entry, 0));
+                    const unsigned long long mine =
+                        entry >= 0 ? reinterpret_cast<unsigned long long>(a.out + at * D) : 0ull;
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 64) {
+                        uint32_t o[2][32];
+                        tc_ld32(tO + c0, o[0]);
+                        tc_ld32(tO + c0 + 32, o[1]);
+                        tc_wait_ld();
 #pragma unroll
                         for (int ch = 0; ch < 8; ++ch) {
                             uint32_t w[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const int c = ch * 8 + 2 * e;
-                                const float x = __uint_as_float(o[c >> 5][c & 31]);
-                                const float y = __uint_as_float(o[(c + 1) >> 5][(c + 1) & 31]);
-                                if (DENSE) {
-                                    __nv_bfloat162 bb = __floats2bfloat162_rn(x * f, y * f);
-                                    w[e] = bad ? 0u : *reinterpret_cast<uint32_t *>(&bb);
-                                } else {
-                                    __half2 hh = __floats2half2_rn(x * f, y * f);
-                                    w[e] = *reinterpret_cast<uint32_t *>(&hh);
-                                }
+                                __nv_bfloat162 bb = __floats2bfloat162_rn(
+                                    __uint_as_float(o[c >> 5][c & 31]) * inv,
+                                    __uint_as_float(o[(c + 1) >> 5][(c + 1) & 31]) * inv);
+                                w[e] = bad ? 0u : *reinterpret_cast<uint32_t *>(&bb);
                             }
                             st_shared_v4(stg + lane * 128 + ((uint32_t)(ch ^ (lane & 7)) << 4), w[0], w[1],
                                          w[2], w[3]);
@@ -784,14 +811,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const unsigned long long d = __shfl_sync(0xffffffffu, mine, r);
                             const uint4 val = ld_shared_v4(stg + r * 128 + ((uint32_t)(ch ^ (r & 7)) << 4));
                             if (d)
-                                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(d) + c0 + ch * 8) = val;
+                                *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(d) + c0 + ch * 8) = val;
                         }
                         __syncwarp();
                     }
-                    if (entry >= 0) {
-                        if (DENSE) a.lse[at] = bad ? -INFINITY : lse2 * 0.69314718055994530942f;
-                        else a.part_s[at] = make_float4(lse2, back[0], back[1], bad ? 0.f : 1.f);
-                    }
+                    if (entry >= 0) a.lse[at] = bad ? -INFINITY : lse2 * 0.69314718055994530942f;
                 } else {
                     // fp32 partial sums, 32 columns a pass
                     float *prow = a.part_o + ((size_t)J.slot * kJobRows + g * kM + quarter * 32) * D;
