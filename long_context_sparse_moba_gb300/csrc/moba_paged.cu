@@ -5,6 +5,7 @@
 // (hncyxsy.com/news/197418) section 3 (mean-pooled block keys) and section 4
 // (the cache's memory); the pages describe no paged cache.
 #include "moba_paged.cuh"
+#include "moba_ptx.cuh"
 
 namespace moba {
 namespace paged {
@@ -54,7 +55,7 @@ int make_cache(Cache *c, const void *k_pages, const void *v_pages, const float *
 // Thread (column, group g of 64 in the cluster) takes the tokens with p % 64 == g
 // of the block, ascending, whatever their source: a pooled key does not depend on
 // how the appends were cut.  Sums are compensated (Kahan), as in the key pooling
-// kernel; the first CTA reads the others' through distributed shared memory.
+// kernel; the others send theirs to the first CTA's shared memory.
 // Bound: HBM for chunks, latency for a step: the step that completes a block
 // reads all of its keys, which four CTAs do in two rounds of loads (one CTA's
 // rounds took twice the time of the whole call now).
@@ -72,18 +73,17 @@ struct AppendArgs {
     int *status;
 };
 
-// the address of the same shared variable in CTA `rank` of the cluster
-__device__ __forceinline__ float peer_load(const float *p, int rank) {
+// the address of a shared variable's counterpart in CTA 0 of the cluster
+__device__ __forceinline__ uint32_t in_first(const void *p) {
     uint32_t at;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;"
-        : "=r"(at)
-        : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::saddr(p)), "r"(0));
+    return at;
 }
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+// v to *at of CTA 0, counted by its barrier
+__device__ __forceinline__ void send(uint32_t at, float v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(at),
+                 "r"(__float_as_uint(v)), "r"(bar)
+                 : "memory");
 }
 
 // (s, c) += x, compensated
@@ -100,8 +100,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     constexpr int G = GC * kAppendCtas;
     constexpr int U = 4;
     __shared__ float red[kAppendThreads][9];
-    __shared__ float s_sum[D], s_bad;
-    __shared__ int s_page[kAppendPages];
+    __shared__ float s_sum[kAppendCtas][D], s_bad[kAppendCtas];  // of CTA 0: what the CTAs sent
+    __shared__ int s_page[kAppendPages], s_abort;
+    __shared__ __align__(8) unsigned long long s_bar;
     const int rank = blockIdx.x % kAppendCtas, bj = blockIdx.x / kAppendCtas;
     const int b = bj / a.cand, hk = blockIdx.y;
     Seq s;
@@ -119,6 +120,18 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     const int t0 = pool ? p0 : max(p0, first);  // first token that is read
     const int col = threadIdx.x % CW, g = rank * GC + threadIdx.x / CW;
     const int *table = a.c.table + (size_t)b * a.c.max_pages;
+    const uint32_t bar = ptx::saddr(&s_bar);
+    if (pool) {
+        // CTA 0's barrier stands before any CTA sends to it (all four alike; nothing
+        // is in flight yet, so the barrier costs little)
+        if (rank == 0 && threadIdx.x == 0) {
+            s_abort = 0;
+            ptx::mbar_init(bar, 1);
+            ptx::fence_mbar_init();
+            ptx::mbar_expect_tx(bar, (kAppendCtas - 1) * (D + 1) * 4);
+        }
+        asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+    }
     // the block's pages, looked up once (a block of more pages than the array
     // holds looks them up as it goes)
     const int g0 = t0 >> a.psh, gn = ((c1 - 1) >> a.psh) + 1 - g0;
@@ -177,35 +190,43 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     bad = __syncthreads_or(bad);
     if (bad && threadIdx.x == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
     if (!pool) return;
-    // (all four CTAs of the cluster alike from here on)
 #pragma unroll
     for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = acc[e];
-    if (threadIdx.x == 0) s_bad = bad ? 1.f : 0.f;
     __syncthreads();
+    float sum = 0.f;
     if (threadIdx.x < D) {
         const int c8 = threadIdx.x / 8, e = threadIdx.x % 8;
-        float sum = red[c8][e], cp = 0.f;
+        float cp = 0.f;
+        sum = red[c8][e];
         for (int x = 1; x < GC; ++x) {
             if (MAX) sum = fmaxf(sum, red[x * CW + c8][e]);
             else kahan(sum, cp, red[x * CW + c8][e]);
         }
-        s_sum[threadIdx.x] = sum;
     }
-    cluster_barrier();
-    if (rank == 0 && threadIdx.x < D) {
-        float sum = s_sum[threadIdx.x], cp = 0.f, any = s_bad;
+    if (rank != 0) {
+        // (sent and counted, no barrier: that would wait for the stores to the pages)
+        const uint32_t to = in_first(&s_bar);
+        if (threadIdx.x < D) send(in_first(&s_sum[rank][threadIdx.x]), sum, to);
+        if (threadIdx.x == 0) send(in_first(&s_bad[rank]), bad ? 1.f : 0.f, to);
+        return;
+    }
+    ptx::Ctl ctl{&s_abort, a.status, kDefaultWaitLimit};
+    if (!ptx::wait_bar(bar, 0, ctl)) {  // recorded as a timeout; the slot stays as it was
+        ptx::drain_bar(bar, 0, kDefaultWaitLimit);
+        return;
+    }
+    if (threadIdx.x < D) {
+        float cp = 0.f, any = bad ? 1.f : 0.f;
 #pragma unroll
         for (int r = 1; r < kAppendCtas; ++r) {
-            const float x = peer_load(s_sum + threadIdx.x, r);
-            if (MAX) sum = fmaxf(sum, x);
-            else kahan(sum, cp, x);
-            any += peer_load(&s_bad, r);
+            if (MAX) sum = fmaxf(sum, s_sum[r][threadIdx.x]);
+            else kahan(sum, cp, s_sum[r][threadIdx.x]);
+            any += s_bad[r];
         }
         if (!MAX) sum /= (float)bs;
         const int page = __ldg(table + ((p0 + bs) >> a.psh) - 1);
         if (any == 0.f) a.kbar[((size_t)page * a.c.Hkv + hk) * D + threadIdx.x] = sum;
     }
-    cluster_barrier();  // the others' shared memory has been read
 }
 
 // ----------------------------------------------------------------------------
