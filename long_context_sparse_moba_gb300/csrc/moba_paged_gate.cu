@@ -282,14 +282,10 @@ __device__ __forceinline__ void decide(const Best<NS> &best, int r, int own, int
     }
 }
 
-// Pooled keys [cb, cb + 64) of a sequence, split into bf16 hi + lo tiles (zeros
-// from c_end on), and their largest norm into s_knmax.  Between two barriers.
-template <int D, int T>
-__device__ __forceinline__ void load_pooled(const Attn &a, int hk, const int *table, int cb, int c_end,
-                                            int *s_page, int *s_bad, int *s_knmax, uint8_t *hi,
-                                            uint8_t *lo) {
-    constexpr int LR = D / 4;  // lanes per pooled key, four values each
-    constexpr int NR = kTile / (T / LR);
+// The pages that hold the pooled keys of blocks [cb, cb + 64): -1 from c_end on,
+// and for a page outside the pool.
+__device__ __forceinline__ void load_pages(const Attn &a, const int *table, int cb, int c_end,
+                                           int *s_page, int *s_bad) {
     const int tid = threadIdx.x, ppb = a.c.bs / a.c.ps;
     if (tid < kTile) {
         const int page = cb + tid < c_end ? __ldg(table + (cb + tid + 1) * ppb - 1) : -1;
@@ -297,8 +293,18 @@ __device__ __forceinline__ void load_pooled(const Attn &a, int hk, const int *ta
         s_page[tid] = ok ? page : -1;
         if (cb + tid < c_end && !ok) *s_bad = 1;
     }
-    __syncthreads();
-    constexpr int HALF = NR > 4 ? NR / 2 : NR;  // loads in flight
+}
+
+// Those pooled keys, split into bf16 hi + lo tiles (zeros where there is no page),
+// and their largest norm into s_knmax.  T threads, FLY loads of a thread in flight.
+// Between two barriers.
+template <int D, int T, int FLY>
+__device__ __forceinline__ void load_pooled(const Attn &a, int hk, const int *s_page, int *s_knmax,
+                                            uint8_t *hi, uint8_t *lo) {
+    constexpr int LR = D / 4;  // lanes per pooled key, four values each
+    constexpr int NR = kTile / (T / LR);
+    const int tid = threadIdx.x;
+    constexpr int HALF = NR > FLY ? FLY : NR;
     float kn = 0.f;
 #pragma unroll
     for (int i0 = 0; i0 < NR; i0 += HALF) {
@@ -438,6 +444,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
     };
     auto own_of = [&](int r) -> int { return (x.pos0 + r / G) / bs; };
     if (scored) {
+        load_pages(a, table, 0, c_own, s_page, &s_bad);  // (in flight with q)
         // this warp's 16 rows of q as MMA operands, and each row's norm
         uint32_t qa[KS][4];
         float q2[2];
@@ -449,15 +456,19 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
         best[1].clear();
         const uint32_t s_hi = smem_u32(smem + L.hi), s_lo = smem_u32(smem + L.lo);
         for (int cb = 0; cb < c_own; cb += kTile) {
-            __syncthreads();  // (the tile before has been read)
-            load_pooled<D, kThreads>(a, x.hk, table, cb, c_own, s_page, &s_bad, &s_knmax, smem + L.hi,
-                                     smem + L.lo);
+            if (cb > 0) {
+                __syncthreads();  // (the tile before has been read)
+                load_pages(a, table, cb, c_own, s_page, &s_bad);
+            }
+            __syncthreads();
+            load_pooled<D, kThreads, 16>(a, x.hk, s_page, &s_knmax, smem + L.hi, smem + L.lo);
             __syncthreads();
             if (warp * 16 < nrows) {
                 float acc[8][4];
                 score_tile<D>(qa, s_hi, s_lo, acc);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) best[h].rank(acc, h, cb, ci[h], km1 + 2);
+                for (int h = 0; h < 2; ++h)
+                    if (warp * 16 + 8 * h < nrows) best[h].rank(acc, h, cb, ci[h], km1 + 2);
             }
         }
         if (warp * 16 < nrows)
@@ -613,7 +624,9 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kern
         const uint32_t s_hi = smem_u32(hi), s_lo = smem_u32(lo);
         for (int cb = 0; cb < c_own; cb += kTile) {
             __syncthreads();  // (the tile before has been read)
-            load_pooled<D, kChunkThreads>(a, hk, table, cb, c_own, s_page, &s_bad, &s_knmax, hi, lo);
+            load_pages(a, table, cb, c_own, s_page, &s_bad);
+            __syncthreads();
+            load_pooled<D, kChunkThreads, 4>(a, hk, s_page, &s_knmax, hi, lo);
             __syncthreads();
             if (warp * 16 < nrows) {
                 float acc[8][4];
