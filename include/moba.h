@@ -499,8 +499,9 @@ int moba_rope_frequencies(double *freqs, int rot_dim, double base, int scaling, 
  * rows outside [0, total), more tokens than max_pages hold) or that needs a
  * page outside [0, num_pages) records MOBA_ERR_INVALID_ARG in the device
  * status word; nothing outside the given arrays is read or written, and the
- * other sequences are computed (rows that two sequences claim, where offsets
- * decrease, hold either one's results or neither's).
+ * other sequences are computed (where offsets decrease, rows of the others may
+ * stay unwritten, and rows that two sequences claim hold either one's results or
+ * neither's).
  *
  * moba_paged_append writes the new tokens' k and v ([total][Hkv][D] bf16) to
  * their pages and pools every block that they complete (options: pooling)
@@ -553,7 +554,7 @@ size_t moba_paged_attn_workspace_size(int num_seqs, int total, int max_new, int 
  * Copies whole pages, page src[i] to page dst[i] (DEVICE int32 [n]), in every
  * one of `layers` layers (pools [layers][num_pages]...): the last, partly
  * filled page of a forked sequence, or a pool's live pages when it is
- * compacted.  kbar_pages may be NULL.  A pair whose source or destination lies
+ * compacted.  At most 65536 pairs a call.  kbar_pages may be NULL.  A pair whose source or destination lies
  * outside [0, num_pages), whose destination is another pair's destination too,
  * or whose source is a pair's destination, copies nothing and records
  * MOBA_ERR_INVALID_ARG in the device status word; the other pairs are copied.

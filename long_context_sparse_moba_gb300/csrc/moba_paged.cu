@@ -348,6 +348,8 @@ MOBA_EXPORT int moba_page_copy(void *k_pages, void *v_pages, float *kbar_pages, 
     if ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 3)
         return MOBA_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return MOBA_ERR_UNSUPPORTED;
+    // (every CTA looks its pair up among all)
+    if (n > 65536) return MOBA_ERR_UNSUPPORTED;
     if (Hkv > 65535 || layers > 65535 || page_size > (1 << 20) ||
         (long long)Hkv * page_size * D > (1ll << 40) / num_pages / layers)
         return MOBA_ERR_UNSUPPORTED;

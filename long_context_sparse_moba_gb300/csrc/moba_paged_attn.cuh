@@ -53,8 +53,10 @@ struct Attn {
     int2 *jobs, *halves;        // [job_cap] list, first entry: of up to 256 rows, of up to 128
     int *n_jobs;                // [3] how many of each, and how many jobs are handed out
     int *list;                  // rows of each list: (token * G + head) << 5 | slot
-    int2 *sel;                  // [Hkv][total * G][km1] a row's past blocks, ascending (-1: none, and
-                                // kSelBad: a page outside the pool), and its place in the block's list
+    int *tok;                   // [total] behind counts: a token's position + 1 (0: of no sequence, or of
+                                // a refused one)
+    int2 *sel;                  // [Hkv][total * G][km1] a row's past blocks, ascending, as list numbers
+                                // (-1: none, kSelBad: a page outside the pool), and its place in each list
     __half *part_h;             // [Hkv][total * G][km1 + 1][D] normalised partial outputs
     float4 *part_s;             // [Hkv][total * G][km1 + 1] log2-sum-exp, scale of each 64 columns,
                                 // and 1 (0: a page outside the pool)

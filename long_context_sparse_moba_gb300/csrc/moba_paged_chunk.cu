@@ -993,17 +993,14 @@ constexpr int kScatterThreads = 256;
 __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(Attn a) {
     after_previous();
     let_next();
-    const int b = blockIdx.y;
-    Seq s;
-    if (a.c.seq(b, s) != kSeqOk) return;
-    const long long per = (long long)s.n * a.G * a.km1, all = per * a.c.Hkv;
-    for (long long i = (long long)blockIdx.x * kScatterThreads + threadIdx.x; i < all;
+    const int hk = blockIdx.y;
+    const long long n = (long long)a.c.total * a.G * a.km1;
+    for (long long i = (long long)blockIdx.x * kScatterThreads + threadIdx.x; i < n;
          i += (long long)gridDim.x * kScatterThreads) {
-        const int hk = (int)(i / per), x = (int)(i - hk * per);
-        const int row = s.row0 * a.G + x / a.km1, slot = x % a.km1;
-        const int2 c = a.sel[((size_t)hk * a.c.total * a.G + row) * a.km1 + slot];
-        if (c.x < 0) continue;
-        const long long at = (long long)a.list_off[((size_t)b * a.n_max + c.x) * a.c.Hkv + hk] + c.y;
+        const int row = (int)(i / a.km1), slot = (int)(i - (long long)row * a.km1);
+        const int2 c = a.sel[hk * n + i];
+        if (a.tok[row / a.G] == 0 || c.x < 0) continue;
+        const long long at = (long long)a.list_off[c.x] + c.y;
         if (at < a.list_cap) a.list[at] = row << 5 | slot;
     }
 }
@@ -1022,18 +1019,15 @@ template <int D>
 __global__ void __launch_bounds__(kSlotThreads, 3) merge_slots_kernel(Attn a) {
     constexpr int GL = D / 16, U = 4, ROWS = kSlotThreads / GL;
     after_previous();
-    const int hk = blockIdx.y, b = blockIdx.z, gl = threadIdx.x % GL, S = a.km1 + 1, G = a.G;
-    Seq s;
-    if (a.c.seq(b, s) != kSeqOk) return;  // (refused ones are cleared by the plan)
-    const int nrows = s.n * G, first = s.len - s.n, c_first = first / a.c.bs;
-    const size_t base = ((size_t)hk * a.c.total + s.row0) * G;
-    for (int r = blockIdx.x * ROWS + threadIdx.x / GL; r < nrows; r += gridDim.x * ROWS) {
-        const int t = r / G;
-        const size_t lin = base + r, p0 = lin * S;
-        // slots, the own block's last (past blocks are counted from the first token's)
-        int n = a.km1;
-        if (c_first < a.km1) n = min(a.km1, (first + t) / a.c.bs);
-        ++n;
+    const int hk = blockIdx.y, gl = threadIdx.x % GL, S = a.km1 + 1, G = a.G;
+    const int nrows = a.c.total * G;
+    const size_t base = (size_t)hk * nrows;
+    for (int row = blockIdx.x * ROWS + threadIdx.x / GL; row < nrows; row += gridDim.x * ROWS) {
+        const int t = row / G, pos1 = __ldg(a.tok + t);
+        if (pos1 == 0) continue;  // (refused ones are cleared by the plan)
+        const size_t lin = base + row, p0 = lin * S;
+        // slots, the own block's last
+        const int n = min(a.km1, (pos1 - 1) / a.c.bs) + 1;
         bool bad = a.km1 > 0 && __ldg(&a.sel[lin * a.km1].x) == kSelBad;
         float M = -INFINITY, W = 0.f, acc[16];
 #pragma unroll
@@ -1084,7 +1078,7 @@ __global__ void __launch_bounds__(kSlotThreads, 3) merge_slots_kernel(Attn a) {
         for (int k = 0; k < 8; ++k)
             o2[k] = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
         if (bad) o[0] = o[1] = make_uint4(0, 0, 0, 0);
-        const size_t at = (size_t)(s.row0 + t) * a.Hq + hk * G + (r - t * G);
+        const size_t at = (size_t)t * a.Hq + hk * G + (row - t * G);
         uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D) + 2 * gl;
         dst[0] = o[0];
         dst[1] = o[1];
@@ -1124,9 +1118,9 @@ cudaError_t launch(const Attn &a, cudaStream_t st) {
     if (DENSE) return launch_merge_runs(a, st);
     note_launches(1);
     constexpr int ROWS = kSlotThreads / (D / 16);
-    const long long tiles = ((long long)a.c.max_new * a.G + ROWS - 1) / ROWS;
+    const long long tiles = ((long long)a.c.total * a.G + ROWS - 1) / ROWS;
     const long long fill = (3 * a.ctas + a.c.Hkv - 1) / a.c.Hkv;
-    const dim3 grid((unsigned)(tiles < fill ? tiles : fill), a.c.Hkv, a.c.num_seqs);
+    const dim3 grid((unsigned)(tiles < fill ? tiles : fill), a.c.Hkv);
     return launch_after(merge_slots_kernel<D>, grid, kSlotThreads, 0, st, a);
 }
 
@@ -1147,9 +1141,9 @@ cudaError_t launch_plan(const Attn &a, bool after_gate, cudaStream_t st) {
     note_launches(1);
     if (rc != cudaSuccess || a.km1 == 0) return rc;
     note_launches(1);
-    const long long most = (long long)a.c.max_new * a.G * a.km1 * a.c.Hkv;
+    const long long most = (long long)a.c.total * a.G * a.km1;
     const long long ctas = (most + 4 * kScatterThreads - 1) / (4 * kScatterThreads);
-    const dim3 grid((unsigned)(ctas < 4096 ? ctas : 4096), a.c.num_seqs);
+    const dim3 grid((unsigned)(ctas < 4096 ? ctas : 4096), a.c.Hkv);
     return launch_after(scatter_kernel, grid, kScatterThreads, 0, st, a);
 }
 

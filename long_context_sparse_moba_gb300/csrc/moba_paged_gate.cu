@@ -574,7 +574,7 @@ __host__ __device__ constexpr int chunk_gate_smem(int D, int km1) {
 }
 
 template <int D, int NS>
-__global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kernel(Attn a, int tps) {
+__global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kernel(Attn a) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_bad, s_knmax, s_page[kTile], s_place[kPlaces];
     __shared__ Unsure<kChunkRows> s_un;
@@ -582,13 +582,13 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kern
     int *sel = reinterpret_cast<int *>(smem + 2 * kTile * D * 2);  // [row][km1 + 1]
     let_next();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hk = blockIdx.x % a.c.Hkv, bt = blockIdx.x / a.c.Hkv;
-    const int b = bt / tps, r0 = (bt - b * tps) * kChunkRows;
+    int tile;
+    const int hk = blockIdx.x % a.c.Hkv, b = a.c.tile_of(blockIdx.x / a.c.Hkv, a.G, kChunkRows, tile);
     const int bs = a.c.bs, km1 = a.km1, G = a.G, ss = km1 + 1;
     Seq s;
     const int state = a.c.seq(b, s);
-    const int nrows = min(kChunkRows, s.n * G - r0);
-    if (nrows <= 0 || state == kSeqEmpty) return;
+    if (state == kSeqEmpty || tile < 0 || (long long)tile * kChunkRows >= (long long)s.n * G) return;
+    const int r0 = tile * kChunkRows, nrows = min(kChunkRows, s.n * G - r0);
     const int row0 = s.row0 * G + r0;  // row = row0 + r: token row / G, head row % G
     if (state == kSeqBad) {
         if (a.idx)
@@ -689,10 +689,12 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kern
         __syncthreads();
     }
     if (tid >= nrows) return;
+    if (hk == 0 && row % G == 0) a.tok[row / G] = row / G + pdelta + 1;
+    const int list0 = b * a.n_max * a.c.Hkv + hk;
     for (int i = 0; i < km1; ++i) {
         const int c = bad ? kSelBad : i < n ? mine[i] : -1;
         const int place = c < 0 ? 0 : counted ? s_place[c] + at[i] : atomicAdd(counts + (size_t)c * a.c.Hkv, 1);
-        out[i] = make_int2(c, place);
+        out[i] = make_int2(c < 0 ? c : list0 + c * a.c.Hkv, place);
     }
 }
 
@@ -736,9 +738,8 @@ template <int D, int NS>
 cudaError_t launch_c(const Attn &a, cudaStream_t st) {
     const cudaError_t rc = allow_smem<chunk_gate_kernel<D, NS>>(chunk_gate_smem(D, kMaxPastSlots));
     if (rc != cudaSuccess) return rc;
-    const int tps = (int)(((long long)a.c.max_new * a.G + kChunkRows - 1) / kChunkRows);
-    chunk_gate_kernel<D, NS><<<a.c.num_seqs * tps * a.c.Hkv, kChunkThreads, chunk_gate_smem(D, a.km1),
-                               st>>>(a, tps);
+    chunk_gate_kernel<D, NS><<<(unsigned)(a.c.tile_slots(a.G, kChunkRows) * a.c.Hkv), kChunkThreads,
+                               chunk_gate_smem(D, a.km1), st>>>(a);
     note_launches(1);
     return cudaGetLastError();
 }

@@ -698,7 +698,8 @@ size_t scratch(Attn *a, void *base) {
     if (a->chunk && !a->dense) {
         const size_t lists = (size_t)a->c.num_seqs * a->n_max * a->c.Hkv;
         const size_t slots = (size_t)a->c.total * a->Hq * (a->km1 + 1);
-        a->counts = static_cast<int *>(take(4 * lists));
+        a->counts = static_cast<int *>(take(4 * (lists + a->c.total)));
+        a->tok = a->counts + lists;
         a->list_off = static_cast<int *>(take(4 * (lists + 1)));
         a->jobs = static_cast<int2 *>(take(8 * (size_t)a->job_cap));
         a->halves = static_cast<int2 *>(take(8 * (size_t)a->job_cap));
@@ -746,7 +747,7 @@ int make_attn(Attn *a, int Hq, int D, int topk) {
         a->w_cap = (int)(w0 < w1 ? w0 : w1);
         a->job_cap = a->list_cap / kJobRows + (lists < a->list_cap ? lists : a->list_cap) + 1;
         if ((long long)a->w_cap * a->c.Hkv >= (1ll << 30) ||
-            (long long)a->c.num_seqs * (rows / 128 + 1) * a->c.Hkv >= (1ll << 31))
+            a->c.tile_slots(a->G, 128) * a->c.Hkv >= (1ll << 31))
             return MOBA_ERR_UNSUPPORTED;
     }
     const long long ucap = (long long)a->rows * (a->km1 + 1);
@@ -815,7 +816,7 @@ MOBA_EXPORT int moba_paged_attn(const void *q, const void *k_pages, const void *
     scratch(&a, workspace);
     cudaError_t e = cudaSuccess;
     if (a.chunk && !a.dense)
-        e = cudaMemsetAsync(a.counts, 0, 4 * (size_t)num_seqs * a.n_max * Hkv, st);
+        e = cudaMemsetAsync(a.counts, 0, 4 * ((size_t)num_seqs * a.n_max * Hkv + total), st);
     if (e == cudaSuccess) e = a.chunk && !a.dense ? launch_chunk_gate(a, st) : launch_gate(a, st);
     const bool gated = !a.dense || a.idx;
     if (e == cudaSuccess && a.chunk) e = launch_plan(a, gated, st);

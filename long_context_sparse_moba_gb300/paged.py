@@ -177,8 +177,8 @@ class PagedCache:
         return torch.tensor(x, dtype=torch.int32).to(self.device)
 
     def _move(self, pairs):
-        if pairs:
-            src, dst = zip(*pairs)
+        for i in range(0, len(pairs), 65536):  # (what one call takes)
+            src, dst = zip(*pairs[i:i + 65536])
             ops.page_copy(self.k_pages, self.v_pages, self.kbar_pages, self._ints(src), self._ints(dst))
 
     def new(self) -> int:

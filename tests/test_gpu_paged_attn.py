@@ -142,6 +142,14 @@ def test_prefill_and_decode_steps_in_one_call():
     case([1, 600, 1, 1, 3, 1], [900, 2000, 17, 2300, 1200, 1], 8, 2, 128, 32, 128, 4, seed=8)
 
 
+@pytest.mark.parametrize("topk", [3, 1000])
+def test_many_steps_beside_one_long_chunk(topk):
+    lens = [700 + 13 * i for i in range(40)] + [1500]
+    nq = [1 + i % 3 for i in range(40)] + [900]
+    order = [40] + list(range(40)) if topk == 3 else list(range(41))
+    case([nq[i] for i in order], [lens[i] for i in order], 8, 2, 64, 16, 64, topk, seed=9, with_idx=topk < 100)
+
+
 def test_ties_go_to_the_lower_block():
     # equal keys in every block, and queries of zeros: every score ties
     c, ks, vs = filled([1024, 900], 2, 64, 16, 64, seed=4)

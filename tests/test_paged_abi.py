@@ -126,7 +126,7 @@ def test_append_refuses(lib, want, kw):
     (INV, dict(k=0)), (INV, dict(v=0)), (INV, dict(src=0)), (INV, dict(dst=0)), (INV, dict(n=0)), (INV, dict(layers=0)),
     (INV, dict(pages=0)), (INV, dict(hkv=0)), (INV, dict(page=8)), (INV, dict(page=20)), (INV, dict(k=2 * MB + 8)),
     (INV, dict(kbar=4 * MB + 8)), (INV, dict(src=5 * MB + 2)), (INV, dict(dst=6 * MB + 1)), (UNS, dict(d=96)),
-    (UNS, dict(page=1 << 21)), (UNS, dict(pages=1 << 30, layers=100))])
+    (UNS, dict(page=1 << 21)), (UNS, dict(pages=1 << 30, layers=100)), (UNS, dict(n=65537)), (UNS, dict(layers=70000))])
 def test_page_copy_refuses(lib, want, kw):
     a = dict(k=2 * MB, v=3 * MB, kbar=4 * MB, src=5 * MB, dst=6 * MB, n=3, layers=1, pages=100, hkv=2, d=64, page=16)
     a.update(kw)
