@@ -68,8 +68,9 @@ struct AppendArgs {
     const __nv_bfloat16 *k, *v;  // [total][Hkv][D]
     __nv_bfloat16 *kp, *vp;
     float *kbar;
-    int cand;  // blocks that a sequence's new tokens touch, at most
+    int cand;  // blocks that a sequence's new tokens touch, at most; 0: clusters by packed tokens
     int psh;   // log2(page size)
+    long long clusters;
     int *status;
 };
 
@@ -103,9 +104,18 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     __shared__ float s_sum[kAppendCtas][D], s_bad[kAppendCtas];  // of CTA 0: what the CTAs sent
     __shared__ int s_page[kAppendPages], s_abort;
     __shared__ __align__(8) unsigned long long s_bar;
-    const int rank = blockIdx.x % kAppendCtas, bj = blockIdx.x / kAppendCtas;
-    const int b = bj / a.cand, hk = blockIdx.y;
+    const int rank = blockIdx.x % kAppendCtas, bj = blockIdx.x / kAppendCtas, hk = blockIdx.y;
+    int b, j;  // the sequence, and which of the blocks that its new tokens touch
     Seq s;
+    if (a.cand > 0) {
+        b = bj / a.cand;
+        j = bj % a.cand;
+    } else {
+        b = a.c.tile_of(bj, 1, a.c.bs, 2, j);
+        // (no slot need lead to a sequence whose offsets are wrong)
+        if (bj < a.c.num_seqs && threadIdx.x == 0 && a.c.seq(bj, s) == kSeqBad)
+            atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+    }
     const int state = a.c.seq(b, s);
     if (state != kSeqOk) {
         if (state == kSeqBad && threadIdx.x == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
@@ -113,7 +123,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     }
     const int bs = a.c.bs, ps = a.c.ps;
     const int first = s.len - s.n;  // position of the first new token
-    const int p0 = (first / bs + bj % a.cand) * bs;
+    if (j < 0 || j > s.n / bs + 1) return;
+    const int p0 = (first / bs + j) * bs;
     if (p0 >= s.len) return;
     const bool pool = a.kbar && p0 + bs <= s.len;
     const int c1 = min(p0 + bs, s.len);
@@ -283,7 +294,7 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(CopyArgs a) {
 template <int D>
 static cudaError_t launch_append(const AppendArgs &a, bool max, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.c.num_seqs * a.cand * kAppendCtas, a.c.Hkv);
+    cfg.gridDim = dim3((unsigned)(a.clusters * kAppendCtas), a.c.Hkv);
     cfg.blockDim = kAppendThreads;
     cfg.stream = st;
     cudaLaunchAttribute at;
@@ -329,7 +340,16 @@ MOBA_EXPORT int moba_paged_append(const void *k, const void *v, void *k_pages, v
     a.kbar = kbar_pages;
     a.psh = __builtin_ctz((unsigned)page_size);
     a.cand = (int)(((long long)a.c.max_new + block_size - 2) / block_size + 1);
-    if ((long long)num_seqs * a.cand >= (1ll << 31) / kAppendCtas) return MOBA_ERR_UNSUPPORTED;
+    // clusters for the longest chunk of every sequence, or, where chunks are uneven
+    // and that is more of them, by packed tokens (n tokens touch n / block_size + 2
+    // blocks at most), which costs a search for the sequence
+    a.clusters = (long long)num_seqs * a.cand;
+    const long long packed = a.c.tile_slots(1, block_size, 2);
+    if (packed < a.clusters) {
+        a.clusters = packed;
+        a.cand = 0;
+    }
+    if (a.clusters >= (1ll << 31) / kAppendCtas) return MOBA_ERR_UNSUPPORTED;
     a.status = status_word();
     if (!a.status) return cuda_result(cudaErrorInvalidDevice);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);

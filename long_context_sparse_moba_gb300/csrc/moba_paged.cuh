@@ -44,20 +44,22 @@ struct Cache {
     }
 
     // Tiles of `rows` rows (head rows of a group of G, numbered token * G + head)
-    // without a table: sequence b's begin at slot cu[b] * G / rows + b, which
-    // leaves room for every sequence's last, partly filled one.  There are
-    // tile_slots of them; a slot's sequence, and its tile (any number: it may lie
-    // behind the sequence's end).
-    __device__ __forceinline__ int tile_of(int slot, int G, int rows, int &tile) const {
+    // without a table: sequence b's begin at slot cu[b] * G / rows + spare * b,
+    // which leaves room for `spare` tiles of every sequence that are not full.
+    // There are tile_slots of them; a slot's sequence, and its tile (any number: it
+    // may lie behind the sequence's end).
+    __device__ __forceinline__ int tile_of(int slot, int G, int rows, int spare, int &tile) const {
         int lo = 0, hi = num_seqs - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if ((long long)__ldg(cu + mid) * G / rows + mid <= slot) lo = mid; else hi = mid - 1;
+            if ((long long)__ldg(cu + mid) * G / rows + (long long)spare * mid <= slot) lo = mid; else hi = mid - 1;
         }
-        tile = (int)(slot - ((long long)__ldg(cu + lo) * G / rows + lo));
+        tile = (int)(slot - ((long long)__ldg(cu + lo) * G / rows + (long long)spare * lo));
         return lo;
     }
-    long long tile_slots(int G, int rows) const { return (long long)total * G / rows + num_seqs; }
+    long long tile_slots(int G, int rows, int spare) const {
+        return (long long)total * G / rows + (long long)spare * num_seqs;
+    }
 };
 
 // A kernel that follows another one of the same call: its CTAs may start while

@@ -730,7 +730,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++gj;
                 tc_fence_after();
-                const float inv = 1.f / l_run;
+                // (a block whose scores are all -inf has weight 0 beside others)
+                const float inv = !DENSE && l_run == 0.f ? 0.f : 1.f / l_run;
                 const float lse2 = m_run + __log2f(l_run);
                 if constexpr (!DENSE) {
                     // fp16 with a scale, 64 columns a pass, straight from the row's
@@ -906,12 +907,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
         const int state = b < a.c.num_seqs ? a.c.seq(b, s) : (int)kSeqEmpty;
         if (state == kSeqBad) {
             atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-            for (size_t i = (size_t)s.row0 * a.Hq; i < (size_t)(s.row0 + s.n) * a.Hq; ++i) {
-                a.lse[i] = -INFINITY;
-                for (int d = 0; d < a.D; d += 8)
-                    *reinterpret_cast<uint4 *>(a.out + i * a.D + d) = make_uint4(0, 0, 0, 0);
-            }
         }
+        if (__syncthreads_or(state == kSeqBad))
+            for (int r = b0; r < min(b0 + kPlanThreads, a.c.num_seqs); ++r) {
+                Seq x;
+                if (a.c.seq(r, x) != kSeqBad) continue;
+                const size_t first = (size_t)x.row0 * a.Hq, n = (size_t)x.n * a.Hq;
+                for (size_t i = tid; i < n; i += kPlanThreads) a.lse[first + i] = -INFINITY;
+                uint4 *out = reinterpret_cast<uint4 *>(a.out + first * a.D);
+                for (size_t i = tid; i < n * a.D / 8; i += kPlanThreads) out[i] = make_uint4(0, 0, 0, 0);
+            }
         const long long mine = state == kSeqOk ? ((long long)s.n * a.G + kJobRows - 1) / kJobRows : 0;
         const long long inc = block_scan(mine, warps, total);
         if (b < a.c.num_seqs) a.own_off[b + 1] = (int)min(run + inc, (long long)a.w_cap);
@@ -1055,11 +1060,12 @@ __global__ void __launch_bounds__(kSlotThreads, 3) merge_slots_kernel(Attn a) {
                 for (int k = 0; k < 16; ++k) acc[k] *= f;
             }
             M = mx;
+            const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 if (s0 + j < n) {
                     bad |= ps[j].w == 0.f;
-                    const float w = fast_exp2(ps[j].x - M);
+                    const float w = fast_exp2(ps[j].x - ref);
                     W += w;
                     const float f = w * (gl < 4 ? ps[j].y : ps[j].z);
                     const __half2 *h2 = reinterpret_cast<const __half2 *>(h[j]);

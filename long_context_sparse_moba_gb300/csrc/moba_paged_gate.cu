@@ -14,8 +14,8 @@
 // lanes yields the next best; the topk + 1 best of the tiles before compete again.
 // (A list kept by insertion costs several times the instructions.)
 // The three errors add up to 2^-14 |q||k|.  Where the last kept and the first
-// dropped score are more than 2 E apart, E = 1.1 2^-14 |q| max|k| (plus a term for
-// pooled keys so small that lo underflows), the selection is settled; the other
+// dropped score are more than 2 E apart, E = 1.1 2^-14 |q| max|k| (plus terms for
+// values so small that they underflow), the selection is settled; the other
 // rows (one or two in a hundred on random keys, all of
 // them when keys tie) are decided by a warp with 64-bit scores, so that the
 // selection is the one of 64-bit arithmetic: scores of the topk best by fp32 where
@@ -273,7 +273,9 @@ __device__ __forceinline__ void decide(const Best<NS> &best, int r, int own, int
 #pragma unroll
     for (int i = 0; i < NS; ++i)
         if (4 * i + (lane & 3) <= km1) sel[r * (km1 + 1) + 4 * i + (lane & 3)] = best.blk[i];
-    const float err = sqrtf(q2) * fmaf(knmax, 6.72e-5f, 1e-34f);
+    // (the squares of values below 1e-22 vanish in fp32, products below 1e-38 in the
+    // scores: far below any real score, the additions keep the bound a bound)
+    const float err = fmaf(sqrtf(q2 + 1e-36f), knmax * 6.72e-5f, 1e-35f);
     if ((lane & 3) == 0 && !(kept - dropped > 2.f * err)) {
         const int u = atomicAdd(&un.n, 1);
         un.row[u] = r;
@@ -337,7 +339,7 @@ __device__ __forceinline__ void load_pooled(const Attn &a, int hk, const int *s_
         }
     }
     // a NaN norm has the largest bits of all
-    if (tid % LR == 0) atomicMax(s_knmax, __float_as_int(fabsf(sqrtf(kn))));
+    if (tid % LR == 0) atomicMax(s_knmax, __float_as_int(fabsf(sqrtf(kn + 1e-36f))));
 }
 
 // Scores of this warp's 16 rows with the 64 pooled keys.
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kern
     let_next();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int tile;
-    const int hk = blockIdx.x % a.c.Hkv, b = a.c.tile_of(blockIdx.x / a.c.Hkv, a.G, kChunkRows, tile);
+    const int hk = blockIdx.x % a.c.Hkv, b = a.c.tile_of(blockIdx.x / a.c.Hkv, a.G, kChunkRows, 1, tile);
     const int bs = a.c.bs, km1 = a.km1, G = a.G, ss = km1 + 1;
     Seq s;
     const int state = a.c.seq(b, s);
@@ -699,16 +701,21 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kern
 }
 
 // The selection where topk covers every block: all of them.
+constexpr int kFillTokens = 16;  // of a CTA
+
 __global__ void __launch_bounds__(kThreads) fill_kernel(Attn a) {
     let_next();
-    const Entry x = get_entry(a, blockIdx.x);
-    if (x.state == kSeqEmpty) return;
-    const long long n = (long long)x.nt * a.G * a.topk;
-    for (long long i = threadIdx.x; i < n; i += kThreads) {
-        const int r = (int)(i / a.topk), j = (int)(i % a.topk);
-        const int ci = (x.pos0 + r / a.G) / a.c.bs;
-        a.idx[((size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G) * a.topk + j] =
-            x.state == kSeqOk && j <= ci ? j : -1;
+    int tile;
+    const int b = a.c.tile_of(blockIdx.x, 1, kFillTokens, 1, tile);
+    Seq s;
+    const int state = a.c.seq(b, s);
+    if (state == kSeqEmpty || tile < 0 || (long long)tile * kFillTokens >= s.n) return;
+    const int t0 = tile * kFillTokens, nt = min(kFillTokens, s.n - t0);
+    const long long per = (long long)a.Hq * a.topk;  // of a token
+    for (long long i = threadIdx.x; i < nt * per; i += kThreads) {
+        const int t = t0 + (int)(i / per), j = (int)(i % a.topk);
+        const int own = (s.len - s.n + t) / a.c.bs;
+        a.idx[(s.row0 + t0) * per + i] = state == kSeqOk && j <= own ? j : -1;
     }
 }
 
@@ -738,7 +745,7 @@ template <int D, int NS>
 cudaError_t launch_c(const Attn &a, cudaStream_t st) {
     const cudaError_t rc = allow_smem<chunk_gate_kernel<D, NS>>(chunk_gate_smem(D, kMaxPastSlots));
     if (rc != cudaSuccess) return rc;
-    chunk_gate_kernel<D, NS><<<(unsigned)(a.c.tile_slots(a.G, kChunkRows) * a.c.Hkv), kChunkThreads,
+    chunk_gate_kernel<D, NS><<<(unsigned)(a.c.tile_slots(a.G, kChunkRows, 1) * a.c.Hkv), kChunkThreads,
                                chunk_gate_smem(D, a.km1), st>>>(a);
     note_launches(1);
     return cudaGetLastError();
@@ -757,7 +764,7 @@ cudaError_t launch_cd(const Attn &a, cudaStream_t st) {
 cudaError_t launch_gate(const Attn &a, cudaStream_t st) {
     if (a.dense) {
         if (!a.idx) return cudaSuccess;
-        fill_kernel<<<a.n_ent, kThreads, 0, st>>>(a);
+        fill_kernel<<<(unsigned)a.c.tile_slots(1, kFillTokens, 1), kThreads, 0, st>>>(a);
         note_launches(1);
         return cudaGetLastError();
     }

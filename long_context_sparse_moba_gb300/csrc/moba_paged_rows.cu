@@ -747,7 +747,7 @@ int make_attn(Attn *a, int Hq, int D, int topk) {
         a->w_cap = (int)(w0 < w1 ? w0 : w1);
         a->job_cap = a->list_cap / kJobRows + (lists < a->list_cap ? lists : a->list_cap) + 1;
         if ((long long)a->w_cap * a->c.Hkv >= (1ll << 30) ||
-            a->c.tile_slots(a->G, 128) * a->c.Hkv >= (1ll << 31))
+            a->c.tile_slots(a->G, 128, 1) * a->c.Hkv >= (1ll << 31))
             return MOBA_ERR_UNSUPPORTED;
     }
     const long long ucap = (long long)a->rows * (a->km1 + 1);

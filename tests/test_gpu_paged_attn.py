@@ -75,7 +75,9 @@ def expect(q, ks, vs, c, nq, lens, block, topk):
         z = torch.logsumexp(logit, -1)
         w = torch.exp(logit - z[..., None])
         o = w @ v
-        err = d * 2.0 ** -23 * d ** -0.5 * (x.abs() @ k.abs().transpose(1, 2)).masked_fill(~seen, 0).amax(-1)
+        # (a key whose logit is -inf has weight 0 with or without errors)
+        size = (x.abs() @ k.abs().transpose(1, 2)).masked_fill(~seen | logit.isneginf(), 0)
+        err = d * 2.0 ** -23 * d ** -0.5 * size.amax(-1)
         A = w @ v.abs()
         out[row:row + n], lse[row:row + n] = o.transpose(0, 1), z.T
         tol[row:row + n] = (2.0 ** -8 * o.abs() + A * (2.0 ** -8 + 2.0 ** -18 + 2 * err[..., None])).transpose(0, 1)
@@ -142,6 +144,12 @@ def test_prefill_and_decode_steps_in_one_call():
     case([1, 600, 1, 1, 3, 1], [900, 2000, 17, 2300, 1200, 1], 8, 2, 128, 32, 128, 4, seed=8)
 
 
+@pytest.mark.parametrize("topk", [50, 64])
+def test_selection_of_every_block(topk):
+    nq, lens = [3, 70, 0, 1, 33], [2500, 90, 5, 64, 1000]
+    case(nq, lens, 8, 2, 64, 16, 64, topk, seed=31, slack=100)
+
+
 @pytest.mark.parametrize("topk", [3, 1000])
 def test_many_steps_beside_one_long_chunk(topk):
     lens = [700 + 13 * i for i in range(40)] + [1500]
@@ -192,6 +200,40 @@ def test_odd_values_in_pooled_keys():
     got = attend(c, q, [9], lens, 64, 4, with_idx=True)
     assert ops.get_status() == ops.MOBA_OK
     compare(got, expect(q, ks, vs, c, [9], lens, 64, 4))
+
+
+@pytest.mark.parametrize("n", [4, 300])
+@pytest.mark.parametrize("qexp,kexp", [(-80, 0), (0, -80), (-40, -62)])
+def test_scores_whose_squares_vanish_in_fp32(n, qexp, kexp):
+    length = 64 * 48 + 7
+    c, ks, vs = filled([length], 2, 64, 64, 64, seed=21)
+    slots = c.table[0, :48].long()
+    c.kbar[slots] *= 2.0 ** kexp
+    q = normal(22, n, 8, 64) * 2.0 ** qexp
+    got = attend(c, q, [n], [length], 64, 4, with_idx=True)
+    assert ops.get_status() == ops.MOBA_OK
+    compare(got, expect(q, ks, vs, c, [n], [length], 64, 4))
+
+
+@pytest.mark.parametrize("n", [1, 80])
+@pytest.mark.parametrize("topk", [3, 100])
+def test_a_block_of_scores_of_minus_infinity(n, topk):
+    """A block whose keys are out of range, for rows that score -inf with all of them, has no weight."""
+    lens = [64 * 6 + 30]
+    c, ks, vs = filled(lens, 1, 64, 16, 64, seed=23)
+    q = normal(24, n, 4, 64)
+    q[..., 0] = q[..., 0].abs() + 0.1
+    ks[0][64:128, :, 0] = -float("inf")
+    pages = c.table[0, 4:8].long()
+    c.k[pages, :, :, 0] = -float("inf")
+    blocks = torch.arange(6, device="cuda")
+    slots = c.table[0, blocks * 4 + 3].long()
+    c.kbar[slots[1]] = 100.0 * q.double().mean((0, 1)).float()  # chosen by many rows all the same
+    got = attend(c, q, [n], lens, 64, topk, with_idx=True)
+    assert ops.get_status() == ops.MOBA_OK
+    want = expect(q, ks, vs, c, [n], lens, 64, topk)
+    assert all(x.isfinite().all() for x in want) and (topk == 100 or (got[2] == 1).any())
+    compare(got, want)
 
 
 def test_padding_rows_and_unwritten_memory_stay_out():

@@ -102,6 +102,47 @@ def test_append_in_uneven_chunks(hkv, d, page, block, pooling):
     assert torch.equal(c.kbar.view(torch.int32), one.kbar.view(torch.int32))
 
 
+@pytest.mark.parametrize("where", [0, 17, 39])
+def test_append_of_steps_beside_a_long_chunk(where):
+    n, block = 40, 64
+    lens = [63 + 7 * b for b in range(n)]
+    nq = [1 + b % 2 for b in range(n)]
+    lens[where], nq[where] = 1500, 1401
+    c, page = Cache(n, 1536, 2, 64, 16, block), 16
+    cu = [0]
+    for m in nq:
+        cu.append(cu[-1] + m)
+    old = [normal(b, L, 2, 64) for b, L in enumerate(lens)]
+    start = [0]
+    for L, m in zip(lens, nq):
+        start.append(start[-1] + L - m)
+    before = torch.cat([k[:L - m] for k, L, m in zip(old, lens, nq)])
+    c.append(before, before, start, [L - m for L, m in zip(lens, nq)])
+    new = torch.cat([k[L - m:] for k, L, m in zip(old, lens, nq)])
+    c.append(new, -new, cu, lens)
+    assert ops.get_status() == ops.MOBA_OK
+    one = Cache(n, 1536, 2, 64, page, block)
+    full = [0]
+    for L in lens:
+        full.append(full[-1] + L)
+    one.append(torch.cat(old), torch.cat(old), full, lens)
+    assert torch.equal(c.k.view(torch.int16), one.k.view(torch.int16))
+    assert torch.equal(c.kbar.view(torch.int32), one.kbar.view(torch.int32))
+    for b, (L, m) in enumerate(zip(lens, nq)):
+        assert torch.equal(c.read(c.v, b, L)[L - m:], -old[b][L - m:])
+    # a refused sequence beside them is recorded, the others stand
+    wrong = list(lens)
+    wrong[3 if where else 4] = 0
+    c.append(new, new, cu, wrong)
+    assert ops.get_status() == ops.MOBA_ERR_INVALID_ARG
+    for b, (L, m) in enumerate(zip(wrong, nq)):
+        if L:
+            assert torch.equal(c.read(c.v, b, L)[L - m:], old[b][L - m:])
+    # offsets that decrease are recorded too
+    c.append(new, new, [0] * 5 + [-1] * (n - 4), [9] * n)
+    assert ops.get_status() == ops.MOBA_ERR_INVALID_ARG
+
+
 def test_append_without_pooled_keys_and_padding_rows():
     c = Cache(2, 128, 2, 64, 16, 64)
     k, v = normal(1, 200, 2, 64), normal(2, 200, 2, 64)
