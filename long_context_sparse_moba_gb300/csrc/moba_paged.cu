@@ -47,20 +47,21 @@ int make_cache(Cache *c, const void *k_pages, const void *v_pages, const float *
 // ----------------------------------------------------------------------------
 // append
 // ----------------------------------------------------------------------------
-// A cluster of four CTAs per (block of a sequence that the new tokens touch, kv
-// head): it copies the block's new tokens to their pages (16 bytes a lane) and,
+// A cluster of up to eight CTAs per (block of a sequence that the new tokens touch,
+// kv head): it copies the block's new tokens to their pages (16 bytes a lane) and,
 // when the block is complete with them, sums the block's keys: the new ones as
 // they pass through its registers, the earlier ones from the cache.  So a chunk's
 // keys are read once and one launch does both.
-// Thread (column, group g of 64 in the cluster) takes the tokens with p % 64 == g
-// of the block, ascending, whatever their source: a pooled key does not depend on
-// how the appends were cut.  Sums are compensated (Kahan), as in the key pooling
+// The block's tokens fall into 64 groups (p % 64; 128 where D is 64), eight parts of
+// them, a CTA one or more parts.  A thread (column, group) takes its tokens in
+// ascending order, whatever their source: a pooled key depends neither on how the
+// appends were cut nor on the size of the cluster.  Sums are compensated (Kahan), as in the key pooling
 // kernel; the others send theirs to the first CTA's shared memory.
-// Bound: HBM for chunks, latency for a step: the step that completes a block
-// reads all of its keys, which four CTAs do in two rounds of loads (one CTA's
-// rounds took twice the time of the whole call now).
-constexpr int kAppendThreads = 256;
-constexpr int kAppendCtas = 4;      // of a cluster
+// Bound: HBM for long chunks (6.5 TB/s at 65536 tokens of 8 heads of 128, blocks of
+// 512), latency for a step: the one that completes a block reads all of its keys,
+// which eight CTAs do in two rounds of loads.
+constexpr int kAppendThreads = 128;
+constexpr int kAppendParts = 8;     // of a block's tokens; the 1, 2, 4 or 8 CTAs of a cluster take them
 constexpr int kAppendPages = 512;
 
 struct AppendArgs {
@@ -71,6 +72,7 @@ struct AppendArgs {
     int cand;  // blocks that a sequence's new tokens touch, at most; 0: clusters by packed tokens
     int psh;   // log2(page size)
     long long clusters;
+    int ctas;  // of a cluster
     int *status;
 };
 
@@ -98,20 +100,20 @@ template <int D, bool MAX>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     constexpr int CW = D / 8;                        // threads across a token
     constexpr int GC = kAppendThreads / CW;          // groups of a CTA
-    constexpr int G = GC * kAppendCtas;
+    constexpr int G = GC * kAppendParts;
     constexpr int U = 4;
     __shared__ float red[kAppendThreads][9];
-    __shared__ float s_sum[kAppendCtas][D], s_bad[kAppendCtas];  // of CTA 0: what the CTAs sent
+    __shared__ float s_sum[kAppendParts][D], s_bad[kAppendParts];  // of CTA 0: the parts' sums
     __shared__ int s_page[kAppendPages], s_abort;
     __shared__ __align__(8) unsigned long long s_bar;
-    const int rank = blockIdx.x % kAppendCtas, bj = blockIdx.x / kAppendCtas, hk = blockIdx.y;
-    int b, j;  // the sequence, and which of the blocks that its new tokens touch
+    const int rank = blockIdx.x & (a.ctas - 1), bj = (int)blockIdx.x / a.ctas, hk = blockIdx.y;
+    int b, nth;  // the sequence, and which of the blocks that its new tokens touch
     Seq s;
     if (a.cand > 0) {
         b = bj / a.cand;
-        j = bj % a.cand;
+        nth = bj % a.cand;
     } else {
-        b = a.c.tile_of(bj, 1, a.c.bs, 2, j);
+        b = a.c.tile_of(bj, 1, a.c.bs, 2, nth);
         // (no slot need lead to a sequence whose offsets are wrong)
         if (bj < a.c.num_seqs && threadIdx.x == 0 && a.c.seq(bj, s) == kSeqBad)
             atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
@@ -123,23 +125,25 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     }
     const int bs = a.c.bs, ps = a.c.ps;
     const int first = s.len - s.n;  // position of the first new token
-    if (j < 0 || j > s.n / bs + 1) return;
-    const int p0 = (first / bs + j) * bs;
+    if (nth < 0 || nth > s.n / bs + 1) return;
+    const int p0 = (first / bs + nth) * bs;
     if (p0 >= s.len) return;
     const bool pool = a.kbar && p0 + bs <= s.len;
     const int c1 = min(p0 + bs, s.len);
     const int t0 = pool ? p0 : max(p0, first);  // first token that is read
-    const int col = threadIdx.x % CW, g = rank * GC + threadIdx.x / CW;
+    if (!pool && c1 - t0 == 1 && (((t0 - p0) % G / GC) & (a.ctas - 1)) != rank)
+        return;  // a step: the CTAs without the token leave
+    const int col = threadIdx.x % CW;
     const int *table = a.c.table + (size_t)b * a.c.max_pages;
     const uint32_t bar = ptx::saddr(&s_bar);
-    if (pool) {
-        // CTA 0's barrier stands before any CTA sends to it (all four alike; nothing
+    if (pool && a.ctas > 1) {
+        // CTA 0's barrier stands before any CTA sends to it (all of them alike; nothing
         // is in flight yet, so the barrier costs little)
         if (rank == 0 && threadIdx.x == 0) {
             s_abort = 0;
             ptx::mbar_init(bar, 1);
             ptx::fence_mbar_init();
-            ptx::mbar_expect_tx(bar, (kAppendCtas - 1) * (D + 1) * 4);
+            ptx::mbar_expect_tx(bar, (kAppendParts - kAppendParts / a.ctas) * (D + 1) * 4);
         }
         asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
     }
@@ -151,85 +155,88 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
         for (int i = threadIdx.x; i < gn; i += kAppendThreads) s_page[i] = __ldg(table + g0 + i);
         __syncthreads();
     }
-    float acc[8], comp[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        acc[e] = MAX ? -INFINITY : 0.f;
-        comp[e] = 0.f;
-    }
     bool bad = false;
-    for (int pb = t0 - (t0 - p0) % G + g; pb < c1; pb += U * G) {
-        uint4 x[U], y[U];
-        size_t at[U];
-        bool live[U];
+    for (int part = rank; part < kAppendParts; part += a.ctas) {
+        float acc[8], comp[8];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int p = pb + j * G;
-            live[j] = p >= t0 && p < c1;
-            if (live[j]) {
-                const int page = held ? s_page[(p >> a.psh) - g0] : __ldg(table + (p >> a.psh));
-                live[j] = (unsigned)page < (unsigned)a.c.num_pages;
-                bad |= !live[j];
-                at[j] = ((((size_t)page * a.c.Hkv + hk) << a.psh) + (p & (ps - 1))) * D + col * 8;
-            }
-            if (live[j] && p >= first) {
-                const size_t src = ((size_t)(s.row0 + p - first) * a.c.Hkv + hk) * D + col * 8;
-                x[j] = __ldcs(reinterpret_cast<const uint4 *>(a.k + src));
-                y[j] = __ldcs(reinterpret_cast<const uint4 *>(a.v + src));
-            } else if (live[j]) {
-                x[j] = *reinterpret_cast<const uint4 *>(a.kp + at[j]);
-            }
+        for (int e = 0; e < 8; ++e) {
+            acc[e] = MAX ? -INFINITY : 0.f;
+            comp[e] = 0.f;
         }
+        for (int pb = t0 - (t0 - p0) % G + part * GC + (int)threadIdx.x / CW; pb < c1; pb += U * G) {
+            uint4 x[U], y[U];
+            size_t at[U];
+            bool live[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (!live[j]) continue;
-            if (pb + j * G >= first) {
-                *reinterpret_cast<uint4 *>(a.kp + at[j]) = x[j];
-                *reinterpret_cast<uint4 *>(a.vp + at[j]) = y[j];
+            for (int j = 0; j < U; ++j) {
+                const int p = pb + j * G;
+                live[j] = p >= t0 && p < c1;
+                if (live[j]) {
+                    const int page = held ? s_page[(p >> a.psh) - g0] : __ldg(table + (p >> a.psh));
+                    live[j] = (unsigned)page < (unsigned)a.c.num_pages;
+                    bad |= !live[j];
+                    at[j] = ((((size_t)page * a.c.Hkv + hk) << a.psh) + (p & (ps - 1))) * D + col * 8;
+                }
+                if (live[j] && p >= first) {
+                    const size_t src = ((size_t)(s.row0 + p - first) * a.c.Hkv + hk) * D + col * 8;
+                    x[j] = __ldcs(reinterpret_cast<const uint4 *>(a.k + src));
+                    y[j] = __ldcs(reinterpret_cast<const uint4 *>(a.v + src));
+                } else if (live[j]) {
+                    x[j] = *reinterpret_cast<const uint4 *>(a.kp + at[j]);
+                }
             }
-            if (pool) {
-                const __nv_bfloat162 *p2 = reinterpret_cast<const __nv_bfloat162 *>(&x[j]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float f = e & 1 ? __high2float(p2[e >> 1]) : __low2float(p2[e >> 1]);
-                    if (MAX) acc[e] = fmaxf(acc[e], f);
-                    else kahan(acc[e], comp[e], f);
+            for (int j = 0; j < U; ++j) {
+                if (!live[j]) continue;
+                if (pb + j * G >= first) {
+                    *reinterpret_cast<uint4 *>(a.kp + at[j]) = x[j];
+                    *reinterpret_cast<uint4 *>(a.vp + at[j]) = y[j];
+                }
+                if (pool) {
+                    const __nv_bfloat162 *p2 = reinterpret_cast<const __nv_bfloat162 *>(&x[j]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float f = e & 1 ? __high2float(p2[e >> 1]) : __low2float(p2[e >> 1]);
+                        if (MAX) acc[e] = fmaxf(acc[e], f);
+                        else kahan(acc[e], comp[e], f);
+                    }
                 }
             }
         }
-    }
-    bad = __syncthreads_or(bad);
-    if (bad && threadIdx.x == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-    if (!pool) return;
+        if (!pool) continue;
+        if (part != rank) __syncthreads();  // (the part before has been summed)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = acc[e];
-    __syncthreads();
-    float sum = 0.f;
-    if (threadIdx.x < D) {
-        const int c8 = threadIdx.x / 8, e = threadIdx.x % 8;
-        float cp = 0.f;
-        sum = red[c8][e];
-        for (int x = 1; x < GC; ++x) {
-            if (MAX) sum = fmaxf(sum, red[x * CW + c8][e]);
-            else kahan(sum, cp, red[x * CW + c8][e]);
+        for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = acc[e];
+        const bool some = __syncthreads_or(bad);
+        if (threadIdx.x < D) {
+            const int c8 = threadIdx.x / 8, e = threadIdx.x % 8;
+            float cp = 0.f, sum = red[c8][e];
+            for (int x = 1; x < GC; ++x) {
+                if (MAX) sum = fmaxf(sum, red[x * CW + c8][e]);
+                else kahan(sum, cp, red[x * CW + c8][e]);
+            }
+            // (sent and counted, no barrier: that would wait for the stores to the pages)
+            if (rank == 0) s_sum[part][threadIdx.x] = sum;
+            else send(in_first(&s_sum[part][threadIdx.x]), sum, in_first(&s_bar));
+        }
+        if (threadIdx.x == 0) {
+            if (rank == 0) s_bad[part] = some ? 1.f : 0.f;
+            else send(in_first(&s_bad[part]), some ? 1.f : 0.f, in_first(&s_bar));
         }
     }
-    if (rank != 0) {
-        // (sent and counted, no barrier: that would wait for the stores to the pages)
-        const uint32_t to = in_first(&s_bar);
-        if (threadIdx.x < D) send(in_first(&s_sum[rank][threadIdx.x]), sum, to);
-        if (threadIdx.x == 0) send(in_first(&s_bad[rank]), bad ? 1.f : 0.f, to);
-        return;
-    }
-    ptx::Ctl ctl{&s_abort, a.status, kDefaultWaitLimit};
-    if (!ptx::wait_bar(bar, 0, ctl)) {  // recorded as a timeout; the slot stays as it was
-        ptx::drain_bar(bar, 0, kDefaultWaitLimit);
-        return;
+    if (__syncthreads_or(bad) && threadIdx.x == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+    if (!pool || rank != 0) return;
+    if (a.ctas > 1) {
+        ptx::Ctl ctl{&s_abort, a.status, kDefaultWaitLimit};
+        if (!ptx::wait_bar(bar, 0, ctl)) {  // recorded as a timeout; the slot stays as it was
+            ptx::drain_bar(bar, 0, kDefaultWaitLimit);
+            return;
+        }
     }
     if (threadIdx.x < D) {
-        float cp = 0.f, any = bad ? 1.f : 0.f;
+        float sum = s_sum[0][threadIdx.x], cp = 0.f, any = s_bad[0];
 #pragma unroll
-        for (int r = 1; r < kAppendCtas; ++r) {
+        for (int r = 1; r < kAppendParts; ++r) {
             if (MAX) sum = fmaxf(sum, s_sum[r][threadIdx.x]);
             else kahan(sum, cp, s_sum[r][threadIdx.x]);
             any += s_bad[r];
@@ -294,12 +301,12 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(CopyArgs a) {
 template <int D>
 static cudaError_t launch_append(const AppendArgs &a, bool max, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.clusters * kAppendCtas), a.c.Hkv);
+    cfg.gridDim = dim3((unsigned)(a.clusters * a.ctas), a.c.Hkv);
     cfg.blockDim = kAppendThreads;
     cfg.stream = st;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = kAppendCtas;
+    at.val.clusterDim.x = a.ctas;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
@@ -349,7 +356,15 @@ MOBA_EXPORT int moba_paged_append(const void *k, const void *v, void *k_pages, v
         a.clusters = packed;
         a.cand = 0;
     }
-    if (a.clusters >= (1ll << 31) / kAppendCtas) return MOBA_ERR_UNSUPPORTED;
+    if (a.clusters >= (1ll << 31) / kAppendParts) return MOBA_ERR_UNSUPPORTED;
+    // CTAs to a block.  More of them shorten the step that completes one, fewer
+    // leave the GPU to more blocks at once (six CTAs an SM side by side).  us with 8,
+    // 4, 2, 1 (D 128, 8 kv heads, blocks of 512): a step of one sequence that
+    // completes its block 4.8, 6.6, 10.4, 17.1; of 64 of which few do 12.3, 11.7, 14.0,
+    // 19.0; of 256 that do not 26.6, 19.2, 18.3, 14.9; a chunk of 65536 tokens 91, 85,
+    // 81, 89, and 312, 216, 167, 136 with blocks of 64
+    const double waves = (double)((long long)total / block_size + num_seqs) * Hkv / (6.0 * sm_count());
+    a.ctas = waves * 8 <= 1 ? 8 : waves * 4 <= 2.5 ? 4 : block_size >= 512 ? 2 : 1;
     a.status = status_word();
     if (!a.status) return cuda_result(cudaErrorInvalidDevice);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
