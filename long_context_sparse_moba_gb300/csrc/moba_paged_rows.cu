@@ -23,6 +23,9 @@
 // bf16 for the second product, as the prefill kernels do.
 // Waits on mbarriers are bounded as in the other kernels; a warp that gives up
 // still joins the barrier of the part, where all warps agree to leave.
+// Measured (heads of 128): 16 sequences of up to 49152 tokens, 32 / 8 heads, all blocks
+// 312 us, 6.5 TB/s, 0.96 of the copy rate; 8 sequences, 32 heads, three blocks of
+// 512 each 41 us, 5.1 TB/s.
 #include "moba_mma.cuh"
 #include "moba_paged_attn.cuh"
 #include "moba_ptx.cuh"
@@ -736,7 +739,10 @@ int make_attn(Attn *a, int Hq, int D, int topk) {
     a->ctas = sm_count();
     a->n_max = (int)(n_max < (1 << 30) ? n_max : 1 << 30);
     // more rows than an entry holds go to the tcgen05 kernel, where row numbers
-    // (token, head of the group) and lists are 32-bit
+    // (token, head of the group) and lists are 32-bit.  (us at 64 rows here and 68
+    // there, 32 / 8 heads of 128, caches of 32768: one sequence 66 and 67 with
+    // selection, 44 and 70 over all blocks; 8 sequences 218 and 207, 214 and 198; 32
+    // sequences 732 and 723, 780 and 718)
     const long long lists = a->dense ? 0 : (long long)a->c.num_seqs * n_max * a->c.Hkv;
     a->list_cap = (long long)a->c.total * Hq * a->km1;
     a->chunk = rows > kMaxRows && (long long)a->c.total * a->G < (1ll << 26) &&
