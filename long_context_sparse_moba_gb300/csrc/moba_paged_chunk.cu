@@ -37,7 +37,7 @@
 // Keys that no row of a job sees (behind its last row, possibly never written)
 // are zeroed in the V tile before its product; in K their scores are masked.
 // Bound: tensor and softmax in turn where jobs are long: 2048 rows x 32 heads over
-// 32768 keys of 128 take 850 us in this kernel, 1240 TFLOP/s, 0.66 of the burst peak.
+// 32768 keys of 128 take 850 us in this kernel, 1260 TFLOP/s, 0.67 of the burst peak.
 // Job boundaries where they are short: 4096 tokens x 32 heads, three blocks of 512
 // (four tiles a job) 132 us, tensor pipe active 0.38; blocks of 128 are one tile a job.
 // (Leaving out the loads of K and V, or the exponentials, changes neither.)
@@ -1023,7 +1023,7 @@ __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(Attn a) {
 // each slot a lane, up to four slots in flight.  Bound: HBM and L2 (the partials),
 // then the issue of instructions, so a lane does much per row and index
 // arithmetic is kept to one division.  131072 rows of three slots of 128: 27 us,
-// 5.4 TB/s of partials and results.
+// 5 TB/s of partials and results.
 constexpr int kSlotThreads = 256;
 
 template <int D>
