@@ -57,7 +57,7 @@ struct Cache {
         tile = (int)(slot - ((long long)__ldg(cu + lo) * G / rows + (long long)spare * lo));
         return lo;
     }
-    long long tile_slots(int G, int rows, int spare) const {
+    __host__ __device__ long long tile_slots(int G, int rows, int spare) const {
         return (long long)total * G / rows + (long long)spare * num_seqs;
     }
 };

@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
     if (tid == 320)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
-    after_previous();
+    if (DENSE) after_previous();
     let_next();
 
     if (warp == 11) {
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool go = true;
             Job J;
             Seq sq;
-            const int tiles = __ldg(a.own_off + a.c.num_seqs);
             if (DENSE) {
+                const int tiles = __ldg(a.own_off + a.c.num_seqs);
                 int open = -1;
                 const long long total = a.unit_off[tiles];
                 const long long runs = total < (long long)gridDim.x ? total : (long long)gridDim.x;
@@ -284,11 +284,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 a.c_open[blockIdx.x] = open;
             } else {
+                // own blocks need none of the lists: equal shares of them are worked off
+                // while the kernels before make those
+                const long long owns = a.c.tile_slots(a.G, kJobRows, 1) * a.c.Hkv;
+                const long long shared = owns - owns % gridDim.x;
+                auto own = [&](long long u) -> bool {
+                    int x;
+                    const int b = a.c.tile_of((int)(u / a.c.Hkv), a.G, kJobRows, 1, x);
+                    if (a.c.seq(b, sq) != kSeqOk || x < 0 || (long long)x * kJobRows >= (long long)sq.n * a.G)
+                        return true;
+                    own_job<N>(a, sq, b, (int)(u % a.c.Hkv), x, J);
+                    own_ends<N>(a, J);
+                    return hand(J);
+                };
+                for (long long u = blockIdx.x; go && u < shared; u += gridDim.x) go = own(u);
+                after_previous();
                 // jobs: 256 rows of a list; pairs of lists' last rows, up to 128
-                // each; own blocks
+                // each; the own blocks that are left
                 const int full = a.km1 > 0 ? a.n_jobs[0] : 0, halves = a.km1 > 0 ? a.n_jobs[1] : 0;
                 const int listed = full + (halves + 1) / 2;
-                const long long all = listed + (long long)tiles * a.c.Hkv;
+                const long long all = listed + owns - shared;
                 // jobs differ in length: taken as CTAs become free (the next one's
                 // number is fetched while this one is looked up)
                 long long q = atomicAdd(a.n_jobs + 2, 1);
@@ -326,13 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     } else {
-                        const int w = (int)((q - listed) / a.c.Hkv);
-                        const int b = upper_index(a.own_off, a.c.num_seqs, w);
-                        a.c.seq(b, sq);
-                        own_job<N>(a, sq, b, (int)((q - listed) % a.c.Hkv), w - __ldg(a.own_off + b), J);
-                        own_ends<N>(a, J);
+                        go = own(shared + q - listed);
                     }
-                    go = hand(J);
+                    if (q < listed) go = hand(J);
                     q = after;
                 }
             }
@@ -527,8 +538,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             Half h;
             int valid, own, key_end, lo, pdelta, whole, slot, tiles;
         };
+        // one inline look first: the bounded wait is a call
+        auto wait = [&](int b, int parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_poll(bar(b), parity) || wait_bar(bar(b), parity, ctl));
+        };
         // this thread's row of a job: row << 5 | slot
+        bool lists = false;  // the kernels that make the lists have ended
         auto entry_of = [&](const Mine &J) -> int {
+            if (!J.own && !lists) {
+                after_previous();
+                lists = true;
+            }
             if (trow >= J.h.nrows) return -1;
             if (J.own) return (J.h.rbase + trow) << 5 | a.km1;
             // (two sequences that claim the same rows, from offsets that decrease,
@@ -561,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto take = [&](int n, Mine &J) -> bool {
             const int js = n % kJobs;
-            if (!__all_sync(0xffffffffu, wait_bar(bar(L::kBarJF + js), (n / kJobs) & 1, ctl))) return false;
+            if (!wait(L::kBarJF + js, (n / kJobs) & 1)) return false;
             const Job &R = ring[js];
             J.h = R.h[g];
             J.valid = R.valid;
@@ -600,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_run = -INFINITY, l_run = 0.f;
             const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
             for (int j = 0; j < ntile; ++j) {
-                if (!__all_sync(0xffffffffu, wait_bar(bar(L::kBarS + g), (gt + j) & 1, ctl))) {
+                if (!wait(L::kBarS + g, (gt + j) & 1)) {
                     ok = false;
                     break;
                 }
@@ -719,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int next_entry = -1;
             if (NJ.valid) {
                 next_entry = entry_of(NJ);
-                if (!__all_sync(0xffffffffu, wait_bar(bar(L::kBarQE + g), n & 1, ctl))) {
+                if (!wait(L::kBarQE + g, n & 1)) {
                     ok = false;
                     break;
                 }
@@ -729,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool bad = bad_job[n % kBadSlots] == n + 1;
             if (bad && lane == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
             if (ntile > 0) {
-                if (!__all_sync(0xffffffffu, wait_bar(bar(L::kBarPV + g), gj & 1, ctl))) {
+                if (!wait(L::kBarPV + g, gj & 1)) {
                     ok = false;
                     break;
                 }
@@ -900,11 +920,12 @@ __device__ __forceinline__ long long block_scan(long long v, long long *warps, l
 template <int N>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
     __shared__ long long warps[kPlanThreads / 32];
-    after_previous();
     let_next();
+    after_previous();
     const int tid = threadIdx.x;
     long long total;
-    // 256-row tiles of each sequence; refused ones have none, and clear rows
+    // 256-row tiles of each sequence (all blocks); refused ones have none, and clear
+    // rows
     long long run = 0;
     for (int b0 = 0; b0 < a.c.num_seqs; b0 += kPlanThreads) {
         const int b = b0 + tid;
@@ -922,19 +943,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
                 uint4 *out = reinterpret_cast<uint4 *>(a.out + first * a.D);
                 for (size_t i = tid; i < n * a.D / 8; i += kPlanThreads) out[i] = make_uint4(0, 0, 0, 0);
             }
+        if (!a.dense) continue;
         const long long mine = state == kSeqOk ? ((long long)s.n * a.G + kJobRows - 1) / kJobRows : 0;
         const long long inc = block_scan(mine, warps, total);
         if (b < a.c.num_seqs) a.own_off[b + 1] = (int)min(run + inc, (long long)a.w_cap);
         run += total;
     }
-    if (tid == 0) {
-        a.own_off[0] = 0;
-        if (!a.dense) a.n_jobs[2] = 0;
-    }
-    __threadfence_block();
-    __syncthreads();
-    const int tiles = (int)min(run, (long long)a.w_cap);
     if (a.dense) {
+        if (tid == 0) a.own_off[0] = 0;
+        __threadfence_block();
+        __syncthreads();
+        const int tiles = (int)min(run, (long long)a.w_cap);
         run = 0;
         for (int w0 = 0; w0 < tiles; w0 += kPlanThreads) {
             const int w = w0 + tid;
@@ -958,6 +977,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
         if (tid == 0) a.unit_off[0] = 0;
         return;
     }
+    if (tid == 0) a.n_jobs[2] = 0;
     if (a.km1 == 0) return;
     // offsets of the lists, a job for every 256 rows of one, and the last rows: a
     // job where they are more than 128, else half of one
@@ -998,11 +1018,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
 
 // The rows into the lists of the blocks that they selected; a row's slots are
 // its past blocks in ascending order.  Latency: 7 us for 262144 entries (the plan 6 us).
-constexpr int kScatterThreads = 256;
+constexpr int kScatterThreads = 1024;
 
 __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(Attn a) {
-    after_previous();
     let_next();
+    after_previous();
     const int hk = blockIdx.y;
     const long long n = (long long)a.c.total * a.G * a.km1;
     for (long long i = (long long)blockIdx.x * kScatterThreads + threadIdx.x; i < n;
@@ -1154,8 +1174,10 @@ cudaError_t launch_plan(const Attn &a, bool after_gate, cudaStream_t st) {
     if (rc != cudaSuccess || a.km1 == 0) return rc;
     note_launches(1);
     const long long most = (long long)a.c.total * a.G * a.km1;
+    // few and large CTAs: the other SMs begin with their own blocks meanwhile
     const long long ctas = (most + 4 * kScatterThreads - 1) / (4 * kScatterThreads);
-    const dim3 grid((unsigned)(ctas < 4096 ? ctas : 4096), a.c.Hkv);
+    const long long cap = (a.ctas / 3 + a.c.Hkv - 1) / a.c.Hkv;
+    const dim3 grid((unsigned)(ctas < cap ? ctas : cap), a.c.Hkv);
     return launch_after(scatter_kernel, grid, kScatterThreads, 0, st, a);
 }
 

@@ -694,7 +694,7 @@ size_t scratch(Attn *a, void *base) {
         a->ublk = static_cast<int *>(take(4 * n * a->ucap));
         a->umask = static_cast<unsigned long long *>(take(8 * n * a->ucap));
     }
-    if (a->chunk) {
+    if (a->chunk && a->dense) {
         a->own_off = static_cast<int *>(take(4 * ((size_t)a->c.num_seqs + 1)));
         a->unit_off = static_cast<long long *>(take(8 * ((size_t)a->w_cap + 1)));
     }
