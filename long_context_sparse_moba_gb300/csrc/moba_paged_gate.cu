@@ -580,6 +580,15 @@ __host__ __device__ constexpr int chunk_gate_smem(int D, int km1) {
     return 2 * kTile * D * 2 + 4 * kChunkRows * (2 * km1 + 1);
 }
 
+// Zeros where the gate counts: the gate runs beside it up to its first count (a
+// memset before the gate cost the chunk 2 us).
+__global__ void __launch_bounds__(kChunkThreads) zero_kernel(int *p, long long n) {
+    let_next();
+    for (long long i = (long long)blockIdx.x * kChunkThreads + threadIdx.x; i < n;
+         i += (long long)gridDim.x * kChunkThreads)
+        p[i] = 0;
+}
+
 template <int D, int NS>
 __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kernel(Attn a) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -594,7 +603,10 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kern
     const int bs = a.c.bs, km1 = a.km1, G = a.G, ss = km1 + 1;
     Seq s;
     const int state = a.c.seq(b, s);
-    if (state == kSeqEmpty || tile < 0 || (long long)tile * kChunkRows >= (long long)s.n * G) return;
+    if (state == kSeqEmpty || tile < 0 || (long long)tile * kChunkRows >= (long long)s.n * G) {
+        after_previous();
+        return;
+    }
     const int r0 = tile * kChunkRows, nrows = min(kChunkRows, s.n * G - r0);
     const int row0 = s.row0 * G + r0;  // row = row0 + r: token row / G, head row % G
     if (state == kSeqBad) {
@@ -603,6 +615,7 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kern
                 const int row = row0 + i / a.topk;
                 a.idx[((size_t)(row / G) * a.Hq + hk * G + row % G) * a.topk + i % a.topk] = -1;
             }
+        after_previous();
         return;
     }
     const int pdelta = s.len - s.n - s.row0;  // position of a row = its token + pdelta
@@ -678,6 +691,7 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kern
         int32_t *dst = a.idx + ((size_t)(row / G) * a.Hq + hk * G + row % G) * a.topk;
         for (int i = 0; i < a.topk; ++i) dst[i] = bad || i > n ? -1 : i < n ? mine[i] : own;
     }
+    after_previous();
     // its places in the blocks' lists: counted in shared memory first, then one
     // global addition per block and CTA (an addition per row and block waits a
     // third of the kernel for the few hundred counters that all rows share)
@@ -750,10 +764,9 @@ template <int D, int NS>
 cudaError_t launch_c(const Attn &a, cudaStream_t st) {
     const cudaError_t rc = allow_smem<chunk_gate_kernel<D, NS>>(chunk_gate_smem(D, kMaxPastSlots));
     if (rc != cudaSuccess) return rc;
-    chunk_gate_kernel<D, NS><<<(unsigned)(a.c.tile_slots(a.G, kChunkRows, 1) * a.c.Hkv), kChunkThreads,
-                               chunk_gate_smem(D, a.km1), st>>>(a);
     note_launches(1);
-    return cudaGetLastError();
+    return launch_after(chunk_gate_kernel<D, NS>, (unsigned)(a.c.tile_slots(a.G, kChunkRows, 1) * a.c.Hkv),
+                        kChunkThreads, chunk_gate_smem(D, a.km1), st, a);
 }
 
 template <int D>
@@ -777,6 +790,12 @@ cudaError_t launch_gate(const Attn &a, cudaStream_t st) {
 }
 
 cudaError_t launch_chunk_gate(const Attn &a, cudaStream_t st) {
+    const long long n = (long long)a.c.num_seqs * a.n_max * a.c.Hkv + a.c.total;  // counts and tok
+    const long long ctas = (n + 4 * kChunkThreads - 1) / (4 * kChunkThreads);
+    zero_kernel<<<(unsigned)(ctas < 4 * a.ctas ? ctas : 4 * a.ctas), kChunkThreads, 0, st>>>(a.counts, n);
+    note_launches(1);
+    const cudaError_t rc = cudaGetLastError();
+    if (rc != cudaSuccess) return rc;
     return a.D == 64 ? launch_cd<64>(a, st) : launch_cd<128>(a, st);
 }
 

@@ -820,10 +820,7 @@ MOBA_EXPORT int moba_paged_attn(const void *q, const void *k_pages, const void *
         workspace = own;
     }
     scratch(&a, workspace);
-    cudaError_t e = cudaSuccess;
-    if (a.chunk && !a.dense)
-        e = cudaMemsetAsync(a.counts, 0, 4 * ((size_t)num_seqs * a.n_max * Hkv + total), st);
-    if (e == cudaSuccess) e = a.chunk && !a.dense ? launch_chunk_gate(a, st) : launch_gate(a, st);
+    cudaError_t e = a.chunk && !a.dense ? launch_chunk_gate(a, st) : launch_gate(a, st);
     const bool gated = !a.dense || a.idx;
     if (e == cudaSuccess && a.chunk) e = launch_plan(a, gated, st);
     if (e == cudaSuccess) e = a.chunk ? launch_chunk(a, st) : launch_rows(a, gated, st);
