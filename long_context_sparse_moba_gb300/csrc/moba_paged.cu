@@ -57,8 +57,8 @@ int make_cache(Cache *c, const void *k_pages, const void *v_pages, const float *
 // ascending order, whatever their source: a pooled key depends neither on how the
 // appends were cut nor on the size of the cluster.  Sums are compensated (Kahan), as in the key pooling
 // kernel; the others send theirs to the first CTA's shared memory.
-// Bound: HBM for long chunks (6.5 TB/s at 65536 tokens of 8 heads of 128, blocks of
-// 512), latency for a step: the one that completes a block reads all of its keys,
+// Bound: HBM for long chunks (79 us, 6.8 TB/s at 65536 tokens of 8 heads of 128,
+// blocks of 512), latency for a step: the one that completes a block reads all of its keys,
 // which eight CTAs do in two rounds of loads.
 constexpr int kAppendThreads = 128;
 constexpr int kAppendParts = 8;     // of a block's tokens; the 1, 2, 4 or 8 CTAs of a cluster take them
@@ -360,13 +360,13 @@ MOBA_EXPORT int moba_paged_append(const void *k, const void *v, void *k_pages, v
     }
     if (a.clusters >= (1ll << 31) / kAppendParts) return MOBA_ERR_UNSUPPORTED;
     // CTAs to a block.  More of them shorten the step that completes one, fewer
-    // leave the GPU to more blocks at once (six CTAs an SM side by side).  us with 8,
+    // leave the GPU to more blocks at once (five CTAs fit an SM).  us with 8,
     // 4, 2, 1 (D 128, 8 kv heads, blocks of 512): a step of one sequence that
     // completes its block 4.8, 6.6, 10.4, 17.1; of 64 of which few do 12.3, 11.7, 14.0,
     // 19.0; of 256 that do not 26.6, 19.2, 18.3, 14.9; a chunk of 65536 tokens 91, 85,
     // 81, 89, and 312, 216, 167, 136 with blocks of 64
-    const double waves = (double)((long long)total / block_size + num_seqs) * Hkv / (6.0 * sm_count());
-    a.ctas = waves * 8 <= 1 ? 8 : waves * 4 <= 2.5 ? 4 : block_size >= 512 ? 2 : 1;
+    const double per_sm = (double)((long long)total / block_size + num_seqs) * Hkv / sm_count();
+    a.ctas = per_sm * 8 <= 6 ? 8 : per_sm * 4 <= 15 ? 4 : block_size >= 512 ? 2 : 1;
     a.status = status_word();
     if (!a.status) return cuda_result(cudaErrorInvalidDevice);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
