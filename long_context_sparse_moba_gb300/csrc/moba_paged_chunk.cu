@@ -67,6 +67,35 @@ constexpr int kTmemCols = 512;
 constexpr int kJobs = 3;         // descriptors in flight
 constexpr int kBadSlots = 8;
 
+// tcgen05.mma, its commit and an arrival by one elected lane of a warp that runs
+// them as one; A from shared or (ta) tensor memory.
+__device__ __forceinline__ void one_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t more) {
+    asm volatile(
+        "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(more)
+        : "memory");
+}
+__device__ __forceinline__ void one_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t more) {
+    asm volatile(
+        "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(more)
+        : "memory");
+}
+__device__ __forceinline__ void one_commit(uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void one_arrive(uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar)
+        : "memory");
+}
+
 // One Q tile's share of a job.
 struct Half {
     int b, hk;
@@ -186,7 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t misc = base - raw >= L::kMisc ? raw : base + L::kEnd;
     uint8_t *gmisc = smem_raw + (misc - raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be uniform)
     const uint32_t sQ = base + L::kQ, sK = base + L::kK, sV = base + L::kV;
     auto bar = [&](int i) -> uint32_t { return misc + 8u * (uint32_t)i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gmisc + L::kSlot);
@@ -228,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     if (tid == 0)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
     if (tid == 320)
@@ -426,108 +456,113 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ================= MMA issuer =================
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc_bf16(kM, N, 0);
-            constexpr uint32_t idesc_o = idesc_bf16(kM, D, 1);
-            int t = 0;
-            int gt[kG] = {0, 0};  // S tiles of each Q tile so far
-            bool ok = true;
-            // descriptors of the first tiles; the address field counts 16 bytes
-            const uint64_t qd0 = sdesc(sQ, 16, 1024), kd0 = sdesc(sK, 16, 1024),
-                           vd0 = sdesc(sV, L::kKVBox, 1024);
-            // O_g += P_g V of tile i of Q tile g, V described by vd; P_g is in the first
-            // columns of S_g (a job's first P is made after the last job's O was read)
-            auto pv = [&](int g, int i, int te, uint64_t vd) -> bool {
-                if (!wait_poll(bar(L::kBarP + g), (gt[g] + i) & 1, ctl)) return false;
+        // The whole warp runs the loops, an elected lane issues: descriptors of a
+        // warp-uniform flow stay in uniform registers.  (One lane running alone took 92
+        // cycles an MMA, 65 being the tensor core's.)
+        auto poll = [&](int b, int parity) -> bool {
+            return __all_sync(0xffffffffu, wait_poll(bar(b), parity, ctl));
+        };
+        auto all = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+        constexpr uint32_t idesc_s = idesc_bf16(kM, N, 0);
+        constexpr uint32_t idesc_o = idesc_bf16(kM, D, 1);
+        int t = 0;
+        int gt[kG] = {0, 0};  // S tiles of each Q tile so far
+        bool ok = true;
+        // descriptors of the first tiles; the address field counts 16 bytes
+        const uint64_t qd0 = sdesc(sQ, 16, 1024), kd0 = sdesc(sK, 16, 1024),
+                       vd0 = sdesc(sV, L::kKVBox, 1024);
+        // O_g += P_g V of tile i of Q tile g, V described by vd; P_g is in the first
+        // columns of S_g (a job's first P is made after the last job's O was read)
+        auto pv = [&](int g, int i, int te, uint64_t vd) -> bool {
+            if (!poll(L::kBarP + g, (gt[g] + i) & 1)) return false;
+            tc_fence_after();
+            const uint32_t tS = tmem + g * 256, tO = tS + 128;
+            const uint32_t more = i > 0;
+            one_mma_ta(tO, tS, vd, idesc_o, more);
+#pragma unroll
+            for (int k = 1; k < N / 16; ++k) one_mma_ta(tO, tS + k * 8, vd + k * 128, idesc_o, 1u);
+            if (i == te - 1) one_commit(bar(L::kBarPV + g));
+            return true;
+        };
+        // S_g = Q_g K^T of tile i of Q tile g, K described by kd
+        auto qk = [&](int g, int i, int te, uint64_t kd, int n) -> bool {
+            if (i == 0) {
+                if (!poll(L::kBarQ + g, n & 1)) return false;
+                fence_proxy_async();
                 tc_fence_after();
-                const uint32_t tS = tmem + g * 256, tO = tS + 128;
-                const uint32_t more = i > 0;
-                tc_mma_ta(tO, tS, vd, idesc_o, more);
+            }
+            const uint32_t tS = tmem + g * 256;
+            const uint64_t qd = qd0 + g * (L::NB * L::kQBox / 16);
 #pragma unroll
-                for (int k = 1; k < N / 16; ++k) tc_mma_ta(tO, tS + k * 8, vd + k * 128, idesc_o, 1u);
-                if (i == te - 1) tc_commit(bar(L::kBarPV + g));
-                return true;
-            };
-            // S_g = Q_g K^T of tile i of Q tile g, K described by kd
-            auto qk = [&](int g, int i, int te, uint64_t kd, int n) -> bool {
-                if (i == 0) {
-                    if (!wait_poll(bar(L::kBarQ + g), n & 1, ctl)) return false;
-                    fence_proxy_async();
-                    tc_fence_after();
+            for (int k = 0; k < D / 16; ++k)
+                one_mma(tS, qd + (k / 4) * (L::kQBox / 16) + (k % 4) * 2,
+                       kd + (k / 4) * (L::kKVBox / 16) + (k % 4) * 2, idesc_s, k > 0);
+            one_commit(bar(L::kBarS + g));
+            if (i == te - 1) one_commit(bar(L::kBarQE + g));
+            return true;
+        };
+        auto kd = [&](int s) { return kd0 + (uint64_t)(s * (L::kTileBytes / 16)); };
+        auto vd = [&](int s) { return vd0 + (uint64_t)(s * (L::kTileBytes / 16)); };
+        auto ready = [&](int full, int s, int tile) {
+            return poll(full + s, (tile / ST) & 1);
+        };
+        for (int n = 0; ok; ++n) {
+            const int js = n % kJobs;
+            if (!poll(L::kBarJF + js, (n / kJobs) & 1)) break;
+            const Job *R = ring + js;
+            const int te[kG] = {all(R->h[0].te), all(R->h[1].te)}, nt = all(R->nt);
+            const bool valid = all(R->valid), pair = all(R->pair);
+            one_arrive(bar(L::kBarJE + js));
+            if (!valid) break;
+            // a Q tile without tiles in this job is released at once
+#pragma unroll
+            for (int g = 0; g < kG; ++g)
+                if (ok && te[g] == 0) {
+                    ok = poll(L::kBarQ + g, n & 1);
+                    if (ok) one_arrive(bar(L::kBarQE + g));
                 }
-                const uint32_t tS = tmem + g * 256;
-                const uint64_t qd = qd0 + g * (L::NB * L::kQBox / 16);
+            if (pair) {  // each Q tile has its own keys
+                for (int i = 0; ok && i <= nt; ++i) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc_mma(tS, qd + (k / 4) * (L::kQBox / 16) + (k % 4) * 2,
-                           kd + (k / 4) * (L::kKVBox / 16) + (k % 4) * 2, idesc_s, k > 0);
-                tc_commit(bar(L::kBarS + g));
-                if (i == te - 1) tc_commit(bar(L::kBarQE + g));
-                return true;
-            };
-            auto kd = [&](int s) { return kd0 + (uint64_t)(s * (L::kTileBytes / 16)); };
-            auto vd = [&](int s) { return vd0 + (uint64_t)(s * (L::kTileBytes / 16)); };
-            auto ready = [&](int full, int s, int tile) {
-                return wait_poll(bar(full + s), (tile / ST) & 1, ctl);
-            };
-            for (int n = 0; ok; ++n) {
-                const int js = n % kJobs;
-                if (!wait_poll(bar(L::kBarJF + js), (n / kJobs) & 1, ctl)) break;
-                const Job *R = ring + js;
-                const int te[kG] = {R->h[0].te, R->h[1].te}, nt = R->nt;
-                const bool valid = R->valid, pair = R->pair;
-                mbar_arrive(bar(L::kBarJE + js));
-                if (!valid) break;
-                // a Q tile without tiles in this job is released at once
-#pragma unroll
-                for (int g = 0; g < kG; ++g)
-                    if (ok && te[g] == 0) {
-                        ok = wait_poll(bar(L::kBarQ + g), n & 1, ctl);
-                        if (ok) mbar_arrive(bar(L::kBarQE + g));
-                    }
-                if (pair) {  // each Q tile has its own keys
-                    for (int i = 0; ok && i <= nt; ++i) {
-#pragma unroll
-                        for (int g = 0; g < kG; ++g) {
-                            const int tk = t + 2 * i + g, tv = tk - 2, sk = tk % ST, sv = (tv + 2 * ST) % ST;
-                            if (ok && i > 0) {
-                                ok = ready(L::kBarVF, sv, tv) && pv(g, i - 1, nt, vd(sv));
-                                if (ok) tc_commit(bar(L::kBarVE + sv));
-                            }
-                            if (ok && i < nt) {
-                                ok = ready(L::kBarKF, sk, tk);
-                                tc_fence_after();
-                                if (ok) ok = qk(g, i, nt, kd(sk), n);
-                                if (ok) tc_commit(bar(L::kBarKE + sk));
-                            }
+                    for (int g = 0; g < kG; ++g) {
+                        const int tk = t + 2 * i + g, tv = tk - 2, sk = tk % ST, sv = (tv + 2 * ST) % ST;
+                        if (ok && i > 0) {
+                            ok = ready(L::kBarVF, sv, tv) && pv(g, i - 1, nt, vd(sv));
+                            if (ok) one_commit(bar(L::kBarVE + sv));
                         }
-                    }
-                } else {
-                    for (int i = 0; ok && i <= nt; ++i) {
-                        const int tk = t + i, sk = tk % ST, sv = (sk + ST - 1) % ST;
-                        const uint64_t kdi = kd(sk), vdi = vd(sv);
-                        if (i < nt) {
+                        if (ok && i < nt) {
                             ok = ready(L::kBarKF, sk, tk);
                             tc_fence_after();
+                            if (ok) ok = qk(g, i, nt, kd(sk), n);
+                            if (ok) one_commit(bar(L::kBarKE + sk));
                         }
-                        if (ok && i > 0) ok = ready(L::kBarVF, sv, tk - 1);
-#pragma unroll
-                        for (int g = 0; g < kG; ++g) {
-                            if (ok && i > 0 && i <= te[g]) ok = pv(g, i - 1, te[g], vdi);
-                            if (ok && i < nt && i < te[g]) ok = qk(g, i, te[g], kdi, n);
-                        }
-                        if (!ok) break;
-                        if (i < nt) tc_commit(bar(L::kBarKE + sk));
-                        if (i > 0) tc_commit(bar(L::kBarVE + sv));
                     }
                 }
-                t += pair ? 2 * nt : nt;
+            } else {
+                for (int i = 0; ok && i <= nt; ++i) {
+                    const int tk = t + i, sk = tk % ST, sv = (sk + ST - 1) % ST;
+                    const uint64_t kdi = kd(sk), vdi = vd(sv);
+                    if (i < nt) {
+                        ok = ready(L::kBarKF, sk, tk);
+                        tc_fence_after();
+                    }
+                    if (ok && i > 0) ok = ready(L::kBarVF, sv, tk - 1);
 #pragma unroll
-                for (int g = 0; g < kG; ++g) gt[g] += te[g];
+                    for (int g = 0; g < kG; ++g) {
+                        if (ok && i > 0 && i <= te[g]) ok = pv(g, i - 1, te[g], vdi);
+                        if (ok && i < nt && i < te[g]) ok = qk(g, i, te[g], kdi, n);
+                    }
+                    if (!ok) break;
+                    if (i < nt) one_commit(bar(L::kBarKE + sk));
+                    if (i > 0) one_commit(bar(L::kBarVE + sv));
+                }
             }
-            tc_commit(bar(L::kBarDrain));
-            drain_bar(bar(L::kBarDrain), 0, ca.wait_limit);
+            t += pair ? 2 * nt : nt;
+#pragma unroll
+            for (int g = 0; g < kG; ++g) gt[g] += te[g];
         }
+        one_commit(bar(L::kBarDrain));
+        drain_bar(bar(L::kBarDrain), 0, ca.wait_limit);
         __syncwarp();
     } else {
         // ================= softmax (warps 2..9) =================
