@@ -67,22 +67,12 @@ constexpr int kTmemCols = 512;
 constexpr int kJobs = 3;         // descriptors in flight
 constexpr int kBadSlots = 8;
 
-// tcgen05.mma, its commit and an arrival by one elected lane of a warp that runs
-// them as one; A from shared or (ta) tensor memory.
-__device__ __forceinline__ void one_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t more) {
-    asm volatile(
-        "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(more)
-        : "memory");
+__device__ __forceinline__ bool elected() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+    return e != 0;
 }
-__device__ __forceinline__ void one_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t more) {
-    asm volatile(
-        "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(more)
-        : "memory");
-}
+// A commit and an arrival by one elected lane of a warp that runs them as one.
 __device__ __forceinline__ void one_commit(uint32_t bar) {
     asm volatile(
         "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
@@ -478,10 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t tS = tmem + g * 256, tO = tS + 128;
             const uint32_t more = i > 0;
-            one_mma_ta(tO, tS, vd, idesc_o, more);
+            if (elected()) {
+                tc_mma_ta(tO, tS, vd, idesc_o, more);
 #pragma unroll
-            for (int k = 1; k < N / 16; ++k) one_mma_ta(tO, tS + k * 8, vd + k * 128, idesc_o, 1u);
-            if (i == te - 1) one_commit(bar(L::kBarPV + g));
+                for (int k = 1; k < N / 16; ++k) tc_mma_ta(tO, tS + k * 8, vd + k * 128, idesc_o, 1u);
+                if (i == te - 1) tc_commit(bar(L::kBarPV + g));
+            }
+            __syncwarp();
             return true;
         };
         // S_g = Q_g K^T of tile i of Q tile g, K described by kd
@@ -493,12 +486,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t tS = tmem + g * 256;
             const uint64_t qd = qd0 + g * (L::NB * L::kQBox / 16);
+            if (elected()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                one_mma(tS, qd + (k / 4) * (L::kQBox / 16) + (k % 4) * 2,
-                       kd + (k / 4) * (L::kKVBox / 16) + (k % 4) * 2, idesc_s, k > 0);
-            one_commit(bar(L::kBarS + g));
-            if (i == te - 1) one_commit(bar(L::kBarQE + g));
+                for (int k = 0; k < D / 16; ++k)
+                    tc_mma(tS, qd + (k / 4) * (L::kQBox / 16) + (k % 4) * 2,
+                           kd + (k / 4) * (L::kKVBox / 16) + (k % 4) * 2, idesc_s, k > 0);
+                tc_commit(bar(L::kBarS + g));
+                if (i == te - 1) tc_commit(bar(L::kBarQE + g));
+            }
+            __syncwarp();
             return true;
         };
         auto kd = [&](int s) { return kd0 + (uint64_t)(s * (L::kTileBytes / 16)); };
