@@ -6,20 +6,21 @@
 // (hncyxsy.com/news/197418) section 3 (the own block forced).
 //
 // 64 pooled keys at a time are split into two bf16 terms (hi + lo) and scored on
-// the tensor cores, q being bf16 already.  A score errs by at most 2^-16 |q||k|
-// for the split and 256 roundings of at most 2^-23 |q||k| for the sums.  The
-// accumulators go straight into the selection: the four lanes of a row hold 16
-// scores each as integers in the scores' order, their low 7 bits replaced by the
-// score's place (another 2^-16 |q||k|), and each round of a maximum over the
+// the tensor cores, q being bf16 already.  A score errs by at most 2^-18 |q||k|
+// for the split (two roundings of 2^-9) and 2 D roundings of at most 2^-23 |q||k| for
+// the sums.  The accumulators go straight into the selection: the four lanes of a
+// row hold 16 scores each as integers in the scores' order, their low 7 bits replaced
+// by the score's place (2^-16 of the score), and each round of a maximum over the
 // lanes yields the next best; the topk + 1 best of the tiles before compete again.
 // (A list kept by insertion costs several times the instructions.)
-// The three errors add up to 2^-14 |q||k|.  Where the last kept and the first
-// dropped score are more than 2 E apart, E = 1.1 2^-14 |q| max|k| (plus terms for
-// values so small that they underflow), the selection is settled; the other
-// rows (one or two in a hundred on random keys, all of
-// them when keys tie) are decided by a warp with 64-bit scores, so that the
-// selection is the one of 64-bit arithmetic: scores of the topk best by fp32 where
-// the next one lies 2 E below the boundary, else of all blocks within 3 E of it.
+// A score is off by E = 1.1 (2^-18 + D 2^-22) |q| max|k| at most (plus terms for values
+// so small that they underflow) and by 2^-16 of itself.  Where the last kept and the
+// first dropped score are more than twice that apart, the selection is settled (a
+// lower score's upper end is lower too); the other rows (one in a hundred on random
+// keys, all of them when keys tie) are decided by a warp with 64-bit scores, so that
+// the selection is the one of 64-bit arithmetic: scores of the topk best by fp32 where
+// the next one lies as far below the boundary, else of all blocks within three times
+// that of it.
 //
 // gate_kernel: one CTA per entry (up to 64 query rows that share a kv head); then
 // the blocks that any row selected are listed, each with the rows that did: the
@@ -267,7 +268,7 @@ struct Unsure {
 
 // A row's ranks into sel[0 .. km1], and whether its selection is settled.  All
 // four lanes of a row (r < 0: of no row).
-template <int NS, int ROWS>
+template <int D, int NS, int ROWS>
 __device__ __forceinline__ void decide(const Best<NS> &best, int r, int own, int km1, float q2,
                                        float knmax, int *sel, Unsure<ROWS> &un) {
     const int lane = threadIdx.x & 31;
@@ -280,12 +281,15 @@ __device__ __forceinline__ void decide(const Best<NS> &best, int r, int own, int
         if (4 * i + (lane & 3) <= km1) sel[r * (km1 + 1) + 4 * i + (lane & 3)] = best.blk[i];
     // (the squares of values below 1e-22 vanish in fp32, products below 1e-38 in the
     // scores: far below any real score, the additions keep the bound a bound)
-    const float err = fmaf(sqrtf(q2 + 1e-36f), knmax * 6.72e-5f, 1e-35f);
+    constexpr float kBound = 1.1f * (0x1p-18f + D * 0x1p-22f), kPlace = 0x1p-16f;
+    const float base = fmaf(sqrtf(q2 + 1e-36f), knmax * kBound, 1e-35f);
+    const float err = fmaf(fmaxf(fabsf(kept), fabsf(dropped)), kPlace, base);
     if ((lane & 3) == 0 && !(kept - dropped > 2.f * err)) {
         const int u = atomicAdd(&un.n, 1);
         un.row[u] = r;
         un.from[u] = kept - 3.f * err;
-        un.few[u] = b == sel::kEmpty || next < kept - 2.f * err;  // (b: there is no next one)
+        un.few[u] = b == sel::kEmpty ||  // (there is no next one)
+                    next < kept - 2.f * fmaf(fmaxf(fabsf(kept), fabsf(next)), kPlace, base);
     }
 }
 
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
         if (warp * 16 < nrows)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                decide(best[h], rq + 8 * h < nrows ? rq + 8 * h : -1, ci[h], km1, q2[h],
+                decide<D>(best[h], rq + 8 * h < nrows ? rq + 8 * h : -1, ci[h], km1, q2[h],
                        __int_as_float(s_knmax), sel, s_un);
         __syncthreads();
         // rows that the error bound leaves open: a warp each
@@ -662,7 +666,7 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kern
         if (warp * 16 < nrows)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                decide(best[h], rq + 8 * h < nrows ? rq + 8 * h : -1, ci[h], km1, q2[h],
+                decide<D>(best[h], rq + 8 * h < nrows ? rq + 8 * h : -1, ci[h], km1, q2[h],
                        __int_as_float(s_knmax), sel, s_un);
         __syncthreads();
         for (int u = warp; u < s_un.n; u += kChunkThreads / 32) {

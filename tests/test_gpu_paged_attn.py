@@ -202,6 +202,21 @@ def test_odd_values_in_pooled_keys():
     compare(got, expect(q, ks, vs, c, [9], lens, 64, 4))
 
 
+@pytest.mark.parametrize("n", [3, 400])
+@pytest.mark.parametrize("d,noise,topk", [(64, 1e-2, 6), (128, 1e-4, 3), (128, 1e-6, 9)])
+def test_scores_that_differ_little(n, d, noise, topk):
+    """Pooled keys around a common one: the scores' differences reach down into fp32's last bits."""
+    length = 64 * 70 + 11
+    c, ks, vs = filled([length], 2, d, 64, 64, seed=25)
+    g = torch.Generator("cuda").manual_seed(26)
+    common = 3 * torch.randn(2, d, generator=g, device="cuda")
+    c.kbar[c.table[0, :70].long()] = common * (1 + noise * torch.randn(70, 2, d, generator=g, device="cuda"))
+    q = normal(27, n, 8, d)
+    got = attend(c, q, [n], [length], 64, topk, with_idx=True)
+    assert ops.get_status() == ops.MOBA_OK
+    compare(got, expect(q, ks, vs, c, [n], [length], 64, topk))
+
+
 @pytest.mark.parametrize("n", [4, 300])
 @pytest.mark.parametrize("qexp,kexp", [(-80, 0), (0, -80), (-40, -62)])
 def test_scores_whose_squares_vanish_in_fp32(n, qexp, kexp):
