@@ -24,12 +24,12 @@
 //     job that falls into several runs leaves fp32 partial sums.
 //
 // With selection, the CTAs start as the gate's leave and work off equal shares of
-// (2), which need no list, while the plan and scatter kernels make the lists (218 us
-// a call instead of 232 at 4096 tokens x 32 heads of 128 over 32768 keys).
+// (2), which need no list, while the plan and scatter kernels make the lists (14 us of
+// a call of 232 at 4096 tokens x 32 heads of 128 over 32768 keys).
 //
 // Persistent, one CTA per SM, 12 warps:
 //   warp 0   K pages by TMA (one lane), warp 10 V pages, into rings of tiles;
-//   warp 1   allocates TMEM; one lane issues, for the two 128-row tiles g of a
+//   warp 1   allocates TMEM; an elected lane issues, for the two 128-row tiles g of a
 //            job, PV_0(j-1), S_0(j), PV_1(j-1), S_1(j): one tile's MMAs run
 //            while the other tile's softmax works;
 //   warps 2..9  softmax: thread r owns row r of its tile.  The offset mu is
@@ -41,9 +41,9 @@
 // Keys that no row of a job sees (behind its last row, possibly never written)
 // are zeroed in the V tile before its product; in K their scores are masked.
 // Bound: tensor and softmax in turn where jobs are long: 2048 rows x 32 heads over
-// 32768 keys of 128 take 850 us in this kernel, 1260 TFLOP/s, 0.67 of the burst peak.
+// 32768 keys of 128 take 800 us, 1340 TFLOP/s, 0.71 of the burst peak.
 // Job boundaries where they are short: 4096 tokens x 32 heads, three blocks of 512
-// (four tiles a job) 124 us, tensor pipe active 0.36; blocks of 128 are one tile a job.
+// (four tiles a job) 100 us behind the lists; blocks of 128 are one tile a job.
 // (Leaving out the loads of K and V, or the exponentials, changes neither; nor does
 // looking the next job's rows up a tile earlier.)
 // Every mbarrier wait is bounded: one that runs out sets MOBA_ERR_TIMEOUT in the
@@ -446,9 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ================= MMA issuer =================
-        // The whole warp runs the loops, an elected lane issues: descriptors of a
-        // warp-uniform flow stay in uniform registers.  (One lane running alone took 92
-        // cycles an MMA, 65 being the tensor core's.)
+        // The whole warp runs the loops, with the job and the waits' results broadcast so
+        // that the flow is uniform, and an elected lane issues a product's MMAs.  (One
+        // lane that ran all of it took 92 cycles an MMA, 65 being the tensor core's: 895
+        // us instead of 800 over all blocks.)
         auto poll = [&](int b, int parity) -> bool {
             return __all_sync(0xffffffffu, wait_poll(bar(b), parity, ctl));
         };

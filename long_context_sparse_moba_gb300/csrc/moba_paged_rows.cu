@@ -1,5 +1,6 @@
 // moba_paged_rows.cu -- attention of a few query rows (up to 64 that share a kv
-// head: the heads of a decode step, or of a few new tokens) over a paged cache.
+// head: the heads of a decode step, or of a few new tokens) over a paged cache, and
+// the host side of the call.
 //
 // Pages: "When a MoBA reproduction will not run" (mhpq.cn/news/582794) section
 // 3.3 (softmax attention over the selected blocks) and "MOBA mixture of block
@@ -739,13 +740,22 @@ int make_attn(Attn *a, int Hq, int D, int topk) {
     a->ctas = sm_count();
     a->n_max = (int)(n_max < (1 << 30) ? n_max : 1 << 30);
     // more rows than an entry holds go to the tcgen05 kernel, where row numbers
-    // (token, head of the group) and lists are 32-bit.  (us at 64 rows here and 68
-    // there, 32 / 8 heads of 128, caches of 32768: one sequence 66 and 67 with
-    // selection, 44 and 70 over all blocks; 8 sequences 218 and 207, 214 and 198; 32
-    // sequences 732 and 723, 780 and 718)
+    // (token, head of the group) and lists are 32-bit.  (us at 64 rows in this file's
+    // kernel and 68 in the other, 32 / 8 heads of 128, caches of 32768: one sequence 59
+    // and 60 with selection, 44 and 70 over all blocks; 8 sequences 217 and 192, 214 and
+    // 193; 32 sequences 732 and 612, 777 and 698)
     const long long lists = a->dense ? 0 : (long long)a->c.num_seqs * n_max * a->c.Hkv;
     a->list_cap = (long long)a->c.total * Hq * a->km1;
-    a->chunk = rows > kMaxRows && (long long)a->c.total * a->G < (1ll << 26) &&
+    // From 33 rows on an entry's warps have four times 16 rows to multiply for every
+    // key, which by then bounds them; so do many entries there, but for short blocks
+    // (jobs of few tiles) and, over all blocks, heads of 64.  (us here and there, 36 to
+    // 64 rows, caches of 16384, blocks of 512: 8 sequences of 8 kv heads 132 to 147 and
+    // 124 to 127 with selection, 118 to 122 and 108 to 112 over all blocks, 99 to 109
+    // and 89 to 92 with selection and heads of 64; 32 sequences 408 to 446 and 337 to
+    // 363.  Against it: blocks of 128 137 and 152, heads of 64 over all blocks 89 and 95)
+    const bool many = rows > 32 && (long long)a->c.num_seqs * a->c.Hkv >= 64 &&
+                      (a->dense ? D == 128 : bs >= 512);
+    a->chunk = (rows > kMaxRows || many) && (long long)a->c.total * a->G < (1ll << 26) &&
                lists < (1ll << 30) && a->list_cap < (1ll << 31);
     if (a->chunk) {
         const long long w0 = (long long)a->c.num_seqs * ((rows + kJobRows - 1) / kJobRows);

@@ -158,6 +158,15 @@ def test_many_steps_beside_one_long_chunk(topk):
     case([nq[i] for i in order], [lens[i] for i in order], 8, 2, 64, 16, 64, topk, seed=9, with_idx=topk < 100)
 
 
+@pytest.mark.parametrize("hq,hkv,d,block,topk", [(16, 4, 128, 512, 3), (16, 4, 64, 512, 2), (16, 4, 128, 64, 200),
+                                                 (12, 4, 128, 128, 3), (16, 4, 64, 64, 200)])
+def test_several_new_tokens_of_many_sequences(hq, hkv, d, block, topk):
+    nq = [9 + 3 * (i % 2) for i in range(16)]
+    nq[5] = 0
+    lens = [400 + 97 * i for i in range(16)]
+    case(nq, lens, hq, hkv, d, 32, block, topk, seed=41, with_idx=topk < 100)
+
+
 def test_ties_go_to_the_lower_block():
     # equal keys in every block, and queries of zeros: every score ties
     c, ks, vs = filled([1024, 900], 2, 64, 16, 64, seed=4)
