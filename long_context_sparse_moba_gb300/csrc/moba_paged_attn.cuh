@@ -33,7 +33,8 @@ struct Attn {
     int ucap;       // union blocks of an entry at most
     float scale_log2;
     int *status;
-    // scratch
+    // scratch (a kernel may start while the one that writes it still runs, so it is read
+    // with plain loads behind after_previous(), never as constant data: no __ldg)
     int *tiles;                 // [n_ent] key tiles of an entry (selection only)
     int *ublk;                  // [n_ent][ucap] blocks that some row of the entry selected, ascending
     unsigned long long *umask;  // [n_ent][ucap] which rows did
@@ -84,6 +85,16 @@ __device__ __forceinline__ Entry get_entry(const Attn &a, int e) {
     // a refused sequence is recorded by its first entry, with rows or without
     if (x.nt == 0 && !(x.state == kSeqBad && x.t0 == 0)) x.state = kSeqEmpty;
     return x;
+}
+
+// the sequence of 256-row tile w (all blocks)
+__device__ __forceinline__ int seq_of_tile(const Attn &a, int w) {
+    int lo = 0, hi = a.c.num_seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.own_off[mid] <= w) lo = mid; else hi = mid - 1;
+    }
+    return lo;
 }
 
 // key tiles that an entry visits

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Job J;
             Seq sq;
             if (DENSE) {
-                const int tiles = __ldg(a.own_off + a.c.num_seqs);
+                const int tiles = a.own_off[a.c.num_seqs];
                 int open = -1;
                 const long long total = a.unit_off[tiles];
                 const long long runs = total < (long long)gridDim.x ? total : (long long)gridDim.x;
@@ -284,9 +284,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (a.unit_off[mid] <= u) w = mid; else hi = mid - 1;
                     }
                     while (go && u < u1) {
-                        const int b = upper_index(a.own_off, a.c.num_seqs, w);
+                        const int b = seq_of_tile(a, w);
                         a.c.seq(b, sq);
-                        own_job<N>(a, sq, b, 0, w - __ldg(a.own_off + b), J);
+                        own_job<N>(a, sq, b, 0, w - a.own_off[b], J);
                         const int T = J.nt;
                         for (; go && u < u1 && u < a.unit_off[w + 1];) {
                             const long long in = u - a.unit_off[w];
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (J.own) return (J.h.rbase + trow) << 5 | a.km1;
             // (two sequences that claim the same rows, from offsets that decrease,
             // spoil one another's lists: such an entry is no row)
-            const int e = __ldg(a.list + J.h.rbase + trow);
+            const int e = a.list[J.h.rbase + trow];
             return (unsigned)((e >> 5) - J.h.rlo) < (unsigned)J.h.rn && (e & 31) < a.km1 ? e : -1;
         };
         auto q_row = [&](int hk, int entry) -> size_t {
@@ -995,11 +995,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
             const int w = w0 + tid;
             long long mine = 0;
             if (w < tiles) {
-                int b = 0, hi = a.c.num_seqs - 1;
-                while (b < hi) {
-                    const int mid = (b + hi + 1) >> 1;
-                    if (a.own_off[mid] <= w) b = mid; else hi = mid - 1;
-                }
+                const int b = seq_of_tile(a, w);
                 Seq s;
                 a.c.seq(b, s);
                 Job J;
@@ -1090,12 +1086,12 @@ __global__ void __launch_bounds__(kSlotThreads, 3) merge_slots_kernel(Attn a) {
     const int nrows = a.c.total * G;
     const size_t base = (size_t)hk * nrows;
     for (int row = blockIdx.x * ROWS + threadIdx.x / GL; row < nrows; row += gridDim.x * ROWS) {
-        const int t = row / G, pos1 = __ldg(a.tok + t);
+        const int t = row / G, pos1 = a.tok[t];
         if (pos1 == 0) continue;  // (refused ones are cleared by the plan)
         const size_t lin = base + row, p0 = lin * S;
         // slots, the own block's last
         const int n = min(a.km1, (pos1 - 1) / a.c.bs) + 1;
-        bool bad = a.km1 > 0 && __ldg(&a.sel[lin * a.km1].x) == kSelBad;
+        bool bad = a.km1 > 0 && a.sel[lin * a.km1].x == kSelBad;
         float M = -INFINITY, W = 0.f, acc[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) acc[k] = 0.f;
@@ -1106,7 +1102,7 @@ __global__ void __launch_bounds__(kSlotThreads, 3) merge_slots_kernel(Attn a) {
             for (int j = 0; j < U; ++j)
                 if (s0 + j < n) {
                     const size_t p = p0 + (s0 + j < n - 1 ? s0 + j : a.km1);
-                    ps[j] = __ldg(a.part_s + p);
+                    ps[j] = a.part_s[p];
                     const uint4 *src = reinterpret_cast<const uint4 *>(a.part_h + p * D) + 2 * gl;
                     h[j][0] = __ldcs(src);
                     h[j][1] = __ldcs(src + 1);

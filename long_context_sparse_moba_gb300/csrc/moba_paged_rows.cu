@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(Attn a) {
     Entry x;
     int row0 = 0, nrows, hk;
     if (CHUNK) {
-        const int w = e / a.c.Hkv, b = upper_index(a.own_off, a.c.num_seqs, w);
+        const int w = e / a.c.Hkv, b = seq_of_tile(a, w);
         Seq s;
         a.c.seq(b, s);
         const int r0 = (w - a.own_off[b]) * kJobRows;
