@@ -24,8 +24,8 @@ struct Cache {
     int num_seqs, total, max_new, Hkv, num_pages, ps, max_pages, bs;
 
     // Reads and checks sequence b's offsets and length.  kSeqBad: its rows, if
-    // any, are [s.row0, s.row0 + s.n) after clamping into [0, total) and to
-    // max_new rows, and nothing else of it may be used.
+    // any, are [s.row0, s.row0 + s.n) after clamping into [0, total), which may be
+    // more than max_new, and nothing else of it may be used.
     __device__ __forceinline__ int seq(int b, Seq &s) const {
         const int lo = __ldg(cu + b), hi = __ldg(cu + b + 1);
         s.row0 = lo;
@@ -38,8 +38,7 @@ struct Cache {
             return kSeqBad;
         }
         s.row0 = min(max(lo, 0), total);
-        const int end = min(max(hi, s.row0), total);
-        s.n = min(end - s.row0, max_new);
+        s.n = min(max(hi, s.row0), total) - s.row0;
         return kSeqBad;
     }
 

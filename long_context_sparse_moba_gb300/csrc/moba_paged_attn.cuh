@@ -68,7 +68,7 @@ struct Entry {
     int t0, nt;    // tokens [t0, t0 + nt) of the sequence's new ones
     int row0;      // packed row of token t0
     int pos0;      // position of token t0
-    int state;     // kSeqOk (then nt > 0), kSeqBad (rows to clear, if any), or kSeqEmpty
+    int state;     // kSeqOk (then nt > 0), kSeqEmpty, or kSeqBad: the first entry of a refused sequence
 };
 
 __device__ __forceinline__ Entry get_entry(const Attn &a, int e) {
@@ -82,9 +82,23 @@ __device__ __forceinline__ Entry get_entry(const Attn &a, int e) {
     x.nt = max(0, min(a.tt, s.n - x.t0));
     x.row0 = s.row0 + x.t0;
     x.pos0 = s.len - s.n + x.t0;
-    // a refused sequence is recorded by its first entry, with rows or without
-    if (x.nt == 0 && !(x.state == kSeqBad && x.t0 == 0)) x.state = kSeqEmpty;
+    if (x.state == kSeqBad ? x.t0 > 0 : x.nt == 0) x.state = kSeqEmpty;
     return x;
+}
+
+// The rows of refused sequence s, heads [h0, h0 + nh): thread `at` of `threads`
+// that clear them together.  By sequence, not by tile: its rows may be more than
+// max_new, and lie where no tile begins.
+__device__ __forceinline__ void clear_refused(const Attn &a, const Seq &s, int h0, int nh, int at, int threads) {
+    const long long n = (long long)s.n * nh, per = a.D / 8;
+    const size_t row0 = s.row0;
+    for (long long i = at; i < n; i += threads) a.lse[(row0 + i / nh) * a.Hq + h0 + i % nh] = -INFINITY;
+    for (long long i = at; i < n * per; i += threads)
+        *reinterpret_cast<uint4 *>(a.out + ((row0 + i / per / nh) * a.Hq + h0 + i / per % nh) * a.D + i % per * 8) =
+            make_uint4(0, 0, 0, 0);
+    if (a.idx)
+        for (long long i = at; i < n * a.topk; i += threads)
+            a.idx[((row0 + i / a.topk / nh) * a.Hq + h0 + i / a.topk % nh) * a.topk + i % a.topk] = -1;
 }
 
 // the sequence of 256-row tile w (all blocks)

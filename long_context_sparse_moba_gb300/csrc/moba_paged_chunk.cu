@@ -967,17 +967,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
         const int b = b0 + tid;
         Seq s;
         const int state = b < a.c.num_seqs ? a.c.seq(b, s) : (int)kSeqEmpty;
-        if (state == kSeqBad) {
-            atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-        }
+        if (state == kSeqBad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
         if (__syncthreads_or(state == kSeqBad))
             for (int r = b0; r < min(b0 + kPlanThreads, a.c.num_seqs); ++r) {
                 Seq x;
-                if (a.c.seq(r, x) != kSeqBad) continue;
-                const size_t first = (size_t)x.row0 * a.Hq, n = (size_t)x.n * a.Hq;
-                for (size_t i = tid; i < n; i += kPlanThreads) a.lse[first + i] = -INFINITY;
-                uint4 *out = reinterpret_cast<uint4 *>(a.out + first * a.D);
-                for (size_t i = tid; i < n * a.D / 8; i += kPlanThreads) out[i] = make_uint4(0, 0, 0, 0);
+                if (a.c.seq(r, x) == kSeqBad) clear_refused(a, x, 0, a.Hq, tid, kPlanThreads);
             }
         if (!a.dense) continue;
         const long long mine = state == kSeqOk ? ((long long)s.n * a.G + kJobRows - 1) / kJobRows : 0;

@@ -430,13 +430,8 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
     const Entry x = get_entry(a, e);
     const int bs = a.c.bs, km1 = a.km1, G = a.G;
     const int nrows = x.nt * G;
-    if (x.state != kSeqOk) {
+    if (x.state != kSeqOk) {  // (refused rows are cleared by the attention kernel)
         if (tid == 0) a.tiles[e] = 0;
-        if (x.state == kSeqBad && a.idx)
-            for (int i = tid; i < nrows * a.topk; i += kThreads) {
-                const int r = i / a.topk;
-                a.idx[((size_t)(x.row0 + r / G) * a.Hq + x.hk * G + r % G) * a.topk + i % a.topk] = -1;
-            }
         return;
     }
     const int pos_last = x.pos0 + x.nt - 1, c_own = pos_last / bs;
@@ -607,21 +602,12 @@ __global__ void __launch_bounds__(kChunkThreads, NS > 2 ? 1 : 3) chunk_gate_kern
     const int bs = a.c.bs, km1 = a.km1, G = a.G, ss = km1 + 1;
     Seq s;
     const int state = a.c.seq(b, s);
-    if (state == kSeqEmpty || tile < 0 || (long long)tile * kChunkRows >= (long long)s.n * G) {
-        after_previous();
+    if (state != kSeqOk || tile < 0 || (long long)tile * kChunkRows >= (long long)s.n * G) {
+        after_previous();  // (refused rows are cleared by the plan)
         return;
     }
     const int r0 = tile * kChunkRows, nrows = min(kChunkRows, s.n * G - r0);
     const int row0 = s.row0 * G + r0;  // row = row0 + r: token row / G, head row % G
-    if (state == kSeqBad) {
-        if (a.idx)
-            for (int i = tid; i < nrows * a.topk; i += kChunkThreads) {
-                const int row = row0 + i / a.topk;
-                a.idx[((size_t)(row / G) * a.Hq + hk * G + row % G) * a.topk + i % a.topk] = -1;
-            }
-        after_previous();
-        return;
-    }
     const int pdelta = s.len - s.n - s.row0;  // position of a row = its token + pdelta
     const int c_own = ((row0 + nrows - 1) / G + pdelta) / bs;
     const int *table = a.c.table + (size_t)b * a.c.max_pages;
@@ -731,14 +717,14 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(Attn a) {
     int tile;
     const int b = a.c.tile_of(blockIdx.x, 1, kFillTokens, 1, tile);
     Seq s;
-    const int state = a.c.seq(b, s);
-    if (state == kSeqEmpty || tile < 0 || (long long)tile * kFillTokens >= s.n) return;
+    // (refused rows are cleared by the kernels that follow)
+    if (a.c.seq(b, s) != kSeqOk || tile < 0 || (long long)tile * kFillTokens >= s.n) return;
     const int t0 = tile * kFillTokens, nt = min(kFillTokens, s.n - t0);
     const long long per = (long long)a.Hq * a.topk;  // of a token
     for (long long i = threadIdx.x; i < nt * per; i += kThreads) {
         const int t = t0 + (int)(i / per), j = (int)(i % a.topk);
         const int own = (s.len - s.n + t) / a.c.bs;
-        a.idx[(s.row0 + t0) * per + i] = state == kSeqOk && j <= own ? j : -1;
+        a.idx[(s.row0 + t0) * per + i] = j <= own ? j : -1;
     }
 }
 

@@ -71,18 +71,29 @@ struct RowsArgs {
     long long wait_limit;
 };
 
-// The rows of an entry without tiles: of a refused sequence, or one whose
-// selection met a page outside the pool.
+// The rows of an entry without tiles, whose selection met a page outside the
+// pool.  True: the entry is a refused sequence's.
 template <int D>
-__device__ __noinline__ void clear_entry(const Attn &a, int e) {
+__device__ __noinline__ bool clear_entry(const Attn &a, int e) {
     const Entry x = get_entry(a, e);
-    if (x.state == kSeqEmpty) return;
-    if (x.state == kSeqBad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+    if (x.state != kSeqOk) return x.state == kSeqBad;
     for (int r = 0; r < x.nt * a.G; ++r) {
         const size_t at = (size_t)(x.row0 + r / a.G) * a.Hq + x.hk * a.G + r % a.G;
         a.lse[at] = -INFINITY;
         for (int d = 0; d < D; d += 8)
             *reinterpret_cast<uint4 *>(a.out + at * D + d) = make_uint4(0, 0, 0, 0);
+    }
+    return false;
+}
+// The refused sequences among this CTA's entries, one kv head's rows at a time.
+__device__ __noinline__ void clear_sequences(const Attn &a) {
+    for (int e = blockIdx.x; e < a.n_ent; e += gridDim.x) {
+        const Entry x = get_entry(a, e);
+        if (x.state != kSeqBad) continue;
+        if (threadIdx.x == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+        Seq s;
+        a.c.seq(x.b, s);
+        clear_refused(a, s, x.hk * a.G, a.G, threadIdx.x, blockDim.x);
     }
 }
 
@@ -122,12 +133,13 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
     const int per = (a.n_ent + kThreads - 1) / kThreads;
     const int lo = min(tid * per, a.n_ent), hi = min(lo + per, a.n_ent);
     long long sum = 0;
+    bool refused = false;
     after_previous();
     let_next();
     for (int e = lo; e < hi; ++e) {
         const int T = get_tiles(a, e);
         sum += T;
-        if (T == 0 && e % (int)gridDim.x == cta) clear_entry<D>(a, e);
+        if (T == 0 && e % (int)gridDim.x == cta) refused |= clear_entry<D>(a, e);
     }
     long long inc = sum;
 #pragma unroll
@@ -148,7 +160,7 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
         s_abort = 0;
         ptx::fence_mbar_init();
     }
-    __syncthreads();
+    if (__syncthreads_or(refused)) clear_sequences(a);
     long long before = inc - sum, total = 0;
 #pragma unroll
     for (int w = 0; w <= CW; ++w) {
