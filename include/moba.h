@@ -506,9 +506,11 @@ int moba_rope_frequencies(double *freqs, int rot_dim, double base, int scaling, 
  * moba_paged_append writes the new tokens' k and v ([total][Hkv][D] bf16) to
  * their pages and pools every block that they complete (options: pooling)
  * from the keys as stored.  A pooled key depends on the block's keys alone,
- * not on how the appends were cut.  Tokens of a refused sequence, and tokens on
- * pages outside the pool, are not written.  Pages that are written must not be
- * shared with another sequence of the call.
+ * not on how the appends were cut.  A mean is a compensated fp32 sum, or a
+ * 64-bit one where that is not finite: infinite where the keys' mean is
+ * (moba_kpool may give NaN there).  A maximum leaves NaN keys out.  Tokens of a
+ * refused sequence, and tokens on pages outside the pool, are not written.
+ * Pages that are written must not be shared with another sequence of the call.
  */
 int moba_paged_append(const void *k, const void *v, void *k_pages, void *v_pages,
                       float *kbar_pages, const int32_t *page_table, const int32_t *cu_new,

@@ -96,6 +96,21 @@ __device__ __forceinline__ void kahan(float &s, float &c, float x) {
     s = t;
 }
 
+// One dimension of the mean key of positions [p0, p0 + bs) of a sequence, in 64 bits,
+// `first` and the later ones from the new tokens' rows (at k, dimension d of the first).
+template <int D>
+__device__ __noinline__ float mean64(const __nv_bfloat16 *kp, int Hkv, int psh, const int *table, int hk, int d,
+                                     int p0, int bs, int first, const __nv_bfloat16 *k) {
+    double sum = 0.0;
+    for (int p = p0; p < p0 + bs; ++p) {
+        const __nv_bfloat16 *x = p < first ? kp + ((((size_t)__ldg(table + (p >> psh)) * Hkv + hk) << psh) +
+                                                   (p & ((1 << psh) - 1))) * D + d
+                                           : k + (size_t)(p - first) * Hkv * D;
+        sum += (double)__bfloat162float(*x);
+    }
+    return (float)(sum / bs);
+}
+
 template <int D, bool MAX>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     constexpr int CW = D / 8;                        // threads across a token
@@ -241,9 +256,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
             else kahan(sum, cp, s_sum[r][threadIdx.x]);
             any += s_bad[r];
         }
+        if (any != 0.f) return;
         if (!MAX) sum /= (float)bs;
+        // infinite keys, or a sum out of fp32's range: the compensation makes a NaN of either
+        // (asking at every addition took 3 to 6 % of the call)
+        if (!MAX && !(fabsf(sum) < INFINITY))
+            sum = mean64<D>(a.kp, a.c.Hkv, a.psh, table, hk, threadIdx.x, p0, bs, first,
+                            a.k + ((size_t)s.row0 * a.c.Hkv + hk) * D + threadIdx.x);
         const int page = __ldg(table + ((p0 + bs) >> a.psh) - 1);
-        if (any == 0.f) a.kbar[((size_t)page * a.c.Hkv + hk) * D + threadIdx.x] = sum;
+        a.kbar[((size_t)page * a.c.Hkv + hk) * D + threadIdx.x] = sum;
     }
 }
 
