@@ -50,7 +50,8 @@ struct Attn {
     int *own_off;               // [num_seqs + 1] 256-row tiles before each sequence
     long long *unit_off;        // [w_cap + 1] key tiles before each row tile (all blocks)
     int *counts;                // [num_seqs][n_max][Hkv] rows that selected the block
-    int *list_off;              // [num_seqs * n_max * Hkv + 1]
+    int *list_off;              // [num_seqs * n_max * Hkv], of the lists in use
+    int *used_off;              // [num_seqs + 1] lists in use before each sequence: of the blocks before its last
     int2 *jobs, *halves;        // [job_cap] list, first entry: of up to 256 rows, of up to 128
     int *n_jobs;                // [3] how many of each, and how many jobs are handed out
     int *list;                  // rows of each list: (token * G + head) << 5 | slot

@@ -183,7 +183,7 @@ __device__ __forceinline__ void list_half(const Attn &a, int l, int start, Half 
     const int bc = l / a.c.Hkv;
     h.b = bc / a.n_max;
     h.rbase = lb + start;
-    h.nrows = min(max(a.list_off[l + 1] - lb - start, 0), kM);
+    h.nrows = min(max(min(a.counts[l], (int)a.list_cap - lb) - start, 0), kM);
     h.key0 = (bc - h.b * a.n_max) * a.c.bs;
     h.te = h.nrows > 0 ? a.c.bs / N : 0;
     Seq s;
@@ -928,41 +928,57 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ----------------------------------------------------------------------------
 // row tiles, list offsets and jobs (one CTA), and the lists
 // ----------------------------------------------------------------------------
-constexpr int kPlanThreads = 1024;
+// The plan goes by the lists in use, not by the page table's width: a chunk of 600 beside
+// 64 steps takes 73 us in tables of 256 to 8192 blocks (192 to 7700 when every list of
+// the table was walked).  1 ns for a list in use where they are many (16.8 M of 512
+// sequences that share a long cache: 15.8 ms for the whole call).
+constexpr int kPlanThreads = 1024, kPlanLists = 4;
 
-// inclusive sum over the CTA's threads
-__device__ __forceinline__ long long block_scan(long long v, long long *warps, long long &total) {
+// inclusive sums over the CTA's threads, N at a time
+template <int N>
+__device__ __forceinline__ void block_scan(long long (&v)[N], long long (*warps)[kPlanThreads / 32],
+                                           long long (&total)[N]) {
     static_assert(kPlanThreads == 1024, "a warp scans the warps' sums");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-    }
-    __syncthreads();
-    if (lane == 31) warps[warp] = v;
-    __syncthreads();
-    long long s = warps[lane];
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v[i], o);
+            if (lane >= o) v[i] += y;
+        }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (lane == 31) warps[i][warp] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        long long s = warps[i][lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        total[i] = __shfl_sync(0xffffffffu, s, 31);
+        const long long before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+        v[i] += warp > 0 ? before : 0;
     }
-    total = __shfl_sync(0xffffffffu, s, 31);
-    const long long before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
-    return v + (warp > 0 ? before : 0);
 }
 
 template <int N>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
-    __shared__ long long warps[kPlanThreads / 32];
+    __shared__ long long warps[2][kPlanThreads / 32];
+    __shared__ int s_off[kPlanThreads + 1];  // `off`, where that is no longer
     let_next();
     after_previous();
     const int tid = threadIdx.x;
-    long long total;
-    // 256-row tiles of each sequence (all blocks); refused ones have none, and clear
-    // rows
+    // 256-row tiles of each sequence (all blocks), or its lists in use: those of the
+    // blocks before its last, whatever the page table's width; refused ones have none,
+    // and clear rows
     long long run = 0;
+    int *off = a.dense ? a.own_off : a.used_off;
+    const long long most = a.dense ? a.w_cap : (long long)a.c.num_seqs * a.n_max * a.c.Hkv;
     for (int b0 = 0; b0 < a.c.num_seqs; b0 += kPlanThreads) {
         const int b = b0 + tid;
         Seq s;
@@ -973,32 +989,37 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
                 Seq x;
                 if (a.c.seq(r, x) == kSeqBad) clear_refused(a, x, 0, a.Hq, tid, kPlanThreads);
             }
-        if (!a.dense) continue;
-        const long long mine = state == kSeqOk ? ((long long)s.n * a.G + kJobRows - 1) / kJobRows : 0;
-        const long long inc = block_scan(mine, warps, total);
-        if (b < a.c.num_seqs) a.own_off[b + 1] = (int)min(run + inc, (long long)a.w_cap);
-        run += total;
+        long long inc[1] = {0}, total[1];
+        if (state == kSeqOk)
+            inc[0] = a.dense ? ((long long)s.n * a.G + kJobRows - 1) / kJobRows
+                             : (long long)((s.len - 1) / a.c.bs) * a.c.Hkv;
+        block_scan(inc, warps, total);
+        if (b < a.c.num_seqs) {
+            off[b + 1] = (int)min(run + inc[0], most);
+            if (b < kPlanThreads) s_off[b + 1] = off[b + 1];
+        }
+        run += total[0];
     }
+    if (tid == 0) off[0] = s_off[0] = 0;
+    __threadfence_block();
+    __syncthreads();
     if (a.dense) {
-        if (tid == 0) a.own_off[0] = 0;
-        __threadfence_block();
-        __syncthreads();
-        const int tiles = (int)min(run, (long long)a.w_cap);
+        const int tiles = (int)min(run, most);
         run = 0;
         for (int w0 = 0; w0 < tiles; w0 += kPlanThreads) {
             const int w = w0 + tid;
-            long long mine = 0;
+            long long inc[1] = {0}, total[1];
             if (w < tiles) {
                 const int b = seq_of_tile(a, w);
                 Seq s;
                 a.c.seq(b, s);
                 Job J;
                 own_job<N>(a, s, b, 0, w - a.own_off[b], J);
-                mine = (long long)J.nt * a.c.Hkv;
+                inc[0] = (long long)J.nt * a.c.Hkv;
             }
-            const long long inc = block_scan(mine, warps, total);
-            if (w < tiles) a.unit_off[w + 1] = run + inc;
-            run += total;
+            block_scan(inc, warps, total);
+            if (w < tiles) a.unit_off[w + 1] = run + inc[0];
+            run += total[0];
         }
         if (tid == 0) a.unit_off[0] = 0;
         return;
@@ -1007,38 +1028,62 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
     if (a.km1 == 0) return;
     // offsets of the lists, a job for every 256 rows of one, and the last rows: a
     // job where they are more than 128, else half of one
-    const long long lists = (long long)a.c.num_seqs * a.n_max * a.c.Hkv;
-    const long long per = (lists + kPlanThreads - 1) / kPlanThreads;
-    const long long l0 = min(per * tid, lists), l1 = min(l0 + per, lists);
-    long long rows = 0, jobs = 0, halves = 0;
-    for (long long l = l0; l < l1; ++l) {
-        const int n = a.counts[l], rest = n % kJobRows;
-        rows += n;
-        jobs += n / kJobRows + (rest > kM);
-        halves += rest > 0 && rest <= kM;
-    }
-    long long row = block_scan(rows, warps, total) - rows;
-    const long long all_rows = total;
-    // (jobs and halves in one scan: both stay below 2^31)
-    const long long inc = block_scan(jobs << 32 | halves, warps, total) - (jobs << 32 | halves);
-    long long job = inc >> 32, half = inc & 0xffffffffll;
-    for (long long l = l0; l < l1; ++l) {
-        const int n = a.counts[l];
-        a.list_off[l] = (int)min(row, a.list_cap);
-        int s = 0;
-        for (; n - s > kM; s += kJobRows, ++job)
-            if (job < a.job_cap) a.jobs[job] = make_int2((int)l, s);
-        if (s < n) {
-            if (half < a.job_cap) a.halves[half] = make_int2((int)l, s);
-            ++half;
+    const int lists = (int)run;
+    const int *before = a.c.num_seqs <= kPlanThreads ? s_off : off;
+    long long row = 0, job = 0, half = 0;
+    for (int i0 = 0; i0 < lists;) {
+        // consecutive lists a thread, consecutive threads: loads and stores of whole lines
+        const int per = min(kPlanLists, (lists - i0 + kPlanThreads - 1) / kPlanThreads);
+        const int i = i0 + tid * per, end = min(i + per, lists);
+        i0 += kPlanThreads * per;
+        int at[kPlanLists], n[kPlanLists];
+        long long inc[2] = {0, 0}, total[2];  // rows; jobs << 32 | halves (both stay below 2^31)
+        if (i < lists) {
+            int b = 0, hi = a.c.num_seqs - 1;
+            while (b < hi) {
+                const int mid = (b + hi + 1) >> 1;
+                if (before[mid] <= i) b = mid; else hi = mid - 1;
+            }
+#pragma unroll
+            for (int k = 0; k < kPlanLists; ++k)
+                if (i + k < end) {
+                    while (before[b + 1] <= i + k) ++b;
+                    at[k] = b * a.n_max * a.c.Hkv + i + k - before[b];
+                    n[k] = a.counts[at[k]];
+                }
+#pragma unroll
+            for (int k = 0; k < kPlanLists; ++k)
+                if (i + k < end) {
+                    const int rest = n[k] % kJobRows;
+                    inc[0] += n[k];
+                    inc[1] += (long long)(n[k] / kJobRows + (rest > kM)) << 32 | (rest > 0 && rest <= kM);
+                }
         }
-        row += n;
+        const long long mine[2] = {inc[0], inc[1]};
+        block_scan(inc, warps, total);
+        long long r = row + inc[0] - mine[0];
+        long long j = job + ((inc[1] - mine[1]) >> 32), h = half + ((inc[1] - mine[1]) & 0xffffffffll);
+#pragma unroll
+        for (int k = 0; k < kPlanLists; ++k)
+            if (i + k < end) {
+                a.list_off[at[k]] = (int)min(r, a.list_cap);
+                int s = 0;
+                for (; n[k] - s > kM; s += kJobRows, ++j)
+                    if (j < a.job_cap) a.jobs[j] = make_int2(at[k], s);
+                if (s < n[k]) {
+                    if (h < a.job_cap) a.halves[h] = make_int2(at[k], s);
+                    ++h;
+                }
+                r += n[k];
+            }
+        row += total[0];
+        job += total[1] >> 32;
+        half += total[1] & 0xffffffffll;
     }
     // (more rows than the tensors hold: only from offsets that overlap, refused ones among them)
     if (tid == 0) {
-        a.list_off[lists] = (int)min(all_rows, a.list_cap);
-        a.n_jobs[0] = (int)min(total >> 32, a.job_cap);
-        a.n_jobs[1] = (int)min(total & 0xffffffffll, a.job_cap);
+        a.n_jobs[0] = (int)min(job, a.job_cap);
+        a.n_jobs[1] = (int)min(half, a.job_cap);
     }
 }
 
