@@ -639,6 +639,8 @@ def _rope(fn, what, q, k, positions, freqs, interleaved, magnitude, q_out, k_out
             else:
                 kos = _heads(ko, device, "k_out")[3]
             pk, pko = k.data_ptr(), ko.data_ptr()
+        if T == 0:
+            return qo, ko
         rc = fn(q.data_ptr(), pk, qo.data_ptr(), pko, positions.data_ptr(), freqs.data_ptr(), T, Hq,
                 Hk, D, 2 * freqs.numel(), 1 if interleaved else 0, magnitude, qs, ks, qos, kos, st)
         if rc:
@@ -655,7 +657,8 @@ def rope(q, k, positions, freqs, interleaved: bool = False, magnitude: float = 1
     ``positions[t] * freqs`` -> (q_out, k_out).  positions int32, one per token;
     freqs float64 (:func:`rope_frequencies`).  Pairs are (i, i + half), or
     (2i, 2i + 1) when ``interleaved``.  The tokens of an operand may be a stride
-    apart (slices of one projection); q_out / k_out may be q / k (in place)."""
+    apart (slices of one projection); q_out / k_out may be q / k (in place).
+    No tokens: empty results, as of the other calls here."""
     return _rope(lib().moba_rope, "moba_rope", q, k, positions, freqs, interleaved, magnitude,
                  q_out, k_out, stream)
 
@@ -707,6 +710,8 @@ def paged_append(k, v, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_l
     shape = k.shape
     if len(shape) != 3 or shape[1] != Hkv or shape[2] != D or v.shape != shape:
         raise ValueError("k and v must be [total, Hkv, D] of the pages")
+    if shape[0] == 0:
+        return
     opt = ctypes.byref(_options(pooling=pooling)[0]) if pooling != POOL_MEAN else None
     rc = _call(device, stream, lambda st: lib().moba_paged_append(
         k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), bar,
@@ -754,6 +759,8 @@ def paged_attn(q, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens, 
         sel = None
         if with_idx or idx is not None:
             sel = _result(idx, (total, Hq, topk), torch.int32, q, device, "idx")
+        if total == 0:
+            return o, z, sel
         rc = lib().moba_paged_attn(
             q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), bar, page_table.data_ptr(),
             cu_new.data_ptr(), cache_lens.data_ptr(), o.data_ptr(), z.data_ptr(),
@@ -788,6 +795,8 @@ def page_copy(k_pages, v_pages, kbar_pages, src, dst, stream=None):
     n = src.numel()
     if n != dst.numel():
         raise ValueError("src and dst must have the same length")
+    if n == 0:
+        return
     layers = shape[0] if len(shape) == 5 else 1
     rc = _call(device, stream, lambda st: lib().moba_page_copy(
         k_pages.data_ptr(), v_pages.data_ptr(), bar, src.data_ptr(), dst.data_ptr(), n, layers, P,
