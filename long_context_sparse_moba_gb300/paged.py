@@ -99,6 +99,24 @@ class Pages:
                 self._pages[seq].append(self._take())
         return copies
 
+    def undo_extend(self, counts: dict, copies: list):
+        """Takes back the last :meth:`extend`, which returned ``copies``."""
+        for seq in reversed(counts):
+            pages = self._pages[seq]
+            self._length[seq] -= counts[seq]
+            while len(pages) * self.page_size >= self._length[seq] + self.page_size:
+                self._drop(pages.pop())
+        where = {}  # of each copy, whose it is
+        for seq in counts:
+            at = self._length[seq] // self.page_size
+            if at < len(self._pages[seq]):
+                where[self._pages[seq][at]] = seq, at
+        for old, page in reversed(copies):
+            seq, at = where[page]
+            self._pages[seq][at] = old
+            self._owners[old] += 1
+            self._drop(page)
+
     def fork(self, seq: int) -> int:
         """Another sequence with the same tokens, sharing every page; the first of
         them to write the last, partly filled one gets a copy then."""
@@ -122,13 +140,18 @@ class Pages:
         self.truncate(seq, 0)
         del self._pages[seq], self._length[seq]
 
+    def compaction(self) -> list:
+        """What :meth:`compact` will move, into pages that are free until then."""
+        live = self.num_pages - len(self._free)
+        holes = sorted(p for p in self._free if p < live)
+        high = sorted(p for p in range(live, self.num_pages) if self._owners[p])
+        return list(zip(high, holes))
+
     def compact(self) -> list:
         """Moves live pages to the lowest numbers; afterwards the live pages are
         0 .. live - 1."""
         live = self.num_pages - len(self._free)
-        holes = sorted(p for p in self._free if p < live)
-        high = sorted(p for p in range(live, self.num_pages) if self._owners[p])
-        where = dict(zip(high, holes))
+        where = dict(self.compaction())
         for pages in self._pages.values():
             pages[:] = [where.get(p, p) for p in pages]
         for src, dst in where.items():
@@ -194,17 +217,28 @@ class PagedCache:
         self.books.free(seq)
 
     def compact(self) -> int:
-        """Moves the live pages to the front of the pools; how many moved."""
-        pairs = self.books.compact()
+        """Moves the live pages to the front of the pools; how many moved.  A
+        batch made before names the old pages: finish its step first."""
+        pairs = self.books.compaction()
         self._move(pairs)
+        self.books.compact()  # (a copy that fails changes nothing)
         return len(pairs)
 
     def extend(self, counts: dict) -> Batch:
         """Room for ``counts[seq]`` new tokens of each sequence, and the tables of the
-        step that writes and attends them.  :class:`OutOfPages` changes nothing."""
+        step that writes and attends them.  A call that fails changes nothing
+        (:class:`OutOfPages`, or what copying shared pages or making the tables raises)."""
         if not counts:
             raise ValueError("a step needs a sequence")
-        self._move(self.books.extend(counts))
+        copies = self.books.extend(counts)
+        try:
+            self._move(copies)
+            return self._batch(counts)
+        except BaseException:  # (pages that were copied to are free again)
+            self.books.undo_extend(counts, copies)
+            raise
+
+    def _batch(self, counts: dict) -> Batch:
         seqs = tuple(counts)
         cu, positions, lens, rows = [0], [], [], []
         for seq in seqs:
