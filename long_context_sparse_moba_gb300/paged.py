@@ -253,14 +253,15 @@ class PagedCache:
                      max(1, max(counts.values())), cu[-1])
 
     def attend(self, layer: int, batch: Batch, q, k, v, topk: int, freqs=None,
-               interleaved: bool = False, magnitude: float = 1.0, **kw):
+               interleaved: bool = False, magnitude: float = 1.0, stream=None, **kw):
         """One layer of a step: q and k rotated to the tokens' positions (with
         ``freqs``, see ``ops.rope_frequencies``), k and v appended, and the attention
-        -> (out, lse, idx) of ``ops.paged_attn`` (further arguments go to it)."""
+        -> (out, lse, idx) of ``ops.paged_attn`` (further arguments go to it), all on
+        ``stream`` (None: the current one)."""
         if freqs is not None:
-            q, k = ops.rope(q, k, batch.positions, freqs, interleaved, magnitude)
+            q, k = ops.rope(q, k, batch.positions, freqs, interleaved, magnitude, stream=stream)
         pools = self.k_pages[layer], self.v_pages[layer], self.kbar_pages[layer]
         ops.paged_append(k, v, *pools, batch.page_table, batch.cu_new, batch.cache_lens,
-                         batch.max_new, self.block_size, pooling=self.pooling)
+                         batch.max_new, self.block_size, pooling=self.pooling, stream=stream)
         return ops.paged_attn(q, *pools, batch.page_table, batch.cu_new, batch.cache_lens,
-                              batch.max_new, self.block_size, topk, **kw)
+                              batch.max_new, self.block_size, topk, stream=stream, **kw)
