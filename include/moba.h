@@ -542,9 +542,10 @@ int moba_paged_append(const void *k, const void *v, void *k_pages, void *v_pages
  * ones that do not see it too.  What pages hold behind a sequence's last token
  * reaches none.
  * workspace: device scratch, 256-byte aligned, at least
- * moba_paged_attn_workspace_size bytes, used by nothing else until the call's
- * work has finished; NULL: stream-ordered scratch of the call's own.  It needs
- * no initialisation.
+ * moba_paged_attn_workspace_size bytes (asked with the same device current: it
+ * goes by the number of SMs), used by nothing else until the call's work has
+ * finished; NULL: stream-ordered scratch of the call's own.  It needs no
+ * initialisation.
  */
 int moba_paged_attn(const void *q, const void *k_pages, const void *v_pages,
                     const float *kbar_pages, const int32_t *page_table, const int32_t *cu_new,

@@ -723,7 +723,7 @@ def paged_append(k, v, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_l
 
 def paged_attn_workspace_size(num_seqs, total, max_new, Hq, Hkv, D, page_size, max_pages,
                               block_size, topk) -> int:
-    """Bytes of device scratch :func:`paged_attn` needs (0: sizes it refuses)."""
+    """Bytes of scratch :func:`paged_attn` needs on the current device (0: sizes it refuses)."""
     return int(lib().moba_paged_attn_workspace_size(num_seqs, total, max_new, Hq, Hkv, D, page_size,
                                                     max_pages, block_size, topk))
 
@@ -748,12 +748,13 @@ def paged_attn(q, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens, 
     total, Hq = shape[0], shape[1]
     if workspace is not None:
         _tensor(workspace, torch.uint8, device, "workspace")
-    size = 0 if workspace is not None else lib().moba_paged_attn_workspace_size(
-        n, total, max_new, Hq, Hkv, D, ps, mp, block_size, topk)
 
     def run(st):
-        ws = workspace if workspace is not None else torch.empty(size, dtype=torch.uint8,
-                                                                 device=q.device)
+        ws = workspace
+        if ws is None:
+            size = lib().moba_paged_attn_workspace_size(n, total, max_new, Hq, Hkv, D, ps, mp,
+                                                        block_size, topk)
+            ws = torch.empty(size, dtype=torch.uint8, device=q.device)
         o = _result(out, shape, torch.bfloat16, q, device, "out")
         z = _result(lse, (total, Hq), torch.float32, q, device, "lse")
         sel = None
