@@ -94,9 +94,10 @@ struct Half {
     int te;          // tiles that it visits
     int rlo, rn;     // list: the sequence's rows [rlo, rlo + rn)
 };
+enum { kNoJob = 0, kAJob = 1, kLists = 2 };
 struct Job {
     Half h[kG];
-    int valid;
+    int valid;       // kNoJob: leave; kLists: no job, the kernels before have to end first
     int own;         // consecutive rows (else lists)
     int pair;        // the Q tiles have rows of two lists, and their own keys each
     int key_end;     // own: keys from here on are seen by no row
@@ -143,7 +144,7 @@ struct Smem {
 template <int N>
 __device__ __forceinline__ void own_job(const Attn &a, const Seq &s, int b, int hk, int x, Job &J) {
     const int r0 = x * kJobRows, nrows = min(kJobRows, s.n * a.G - r0);
-    J.valid = 1;
+    J.valid = kAJob;
     J.own = 1;
     J.pair = 0;
     J.pdelta = s.len - s.n - s.row0;
@@ -322,6 +323,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return hand(J);
                 };
                 for (long long u = blockIdx.x; go && u < shared; u += gridDim.x) go = own(u);
+                // every role waits for those kernels itself, however long they take: a
+                // bounded wait for the next job would run while they work
+                J.valid = kLists;
+                if (go) go = hand(J);
                 after_previous();
                 // jobs: 256 rows of a list; pairs of lists' last rows, up to 128
                 // each; the own blocks that are left
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 while (go && q < all) {
                     const long long after = atomicAdd(a.n_jobs + 2, 1);
                     if (q < listed) {
-                        J.valid = 1;
+                        J.valid = kAJob;
                         J.own = 0;
                         J.key_end = 0x7fffffff;
                         J.lo = 0;
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     q = after;
                 }
             }
-            J.valid = 0;
+            J.valid = kNoJob;
             if (go) hand(J);
         }
         __syncwarp();
@@ -385,13 +390,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ps = a.c.ps, box = min(ps, N);
             int pend[ST];
             for (int s = 0; s < ST; ++s) pend[s] = -1;
-            int t = 0;
-            for (int n = 0;; ++n) {
-                const int js = n % kJobs;
-                if (!wait_bar(bar(L::kBarJF + js), (n / kJobs) & 1, ctl)) break;
+            int t = 0, n = -1;  // tiles so far, the job's number
+            for (int r = 0;; ++r) {
+                const int js = r % kJobs;
+                if (!wait_bar(bar(L::kBarJF + js), (r / kJobs) & 1, ctl)) break;
                 const Job J = ring[js];
                 mbar_arrive(bar(L::kBarJE + js));
-                if (!J.valid) break;
+                if (J.valid == kNoJob) break;
+                if (J.valid == kLists) {
+                    after_previous();
+                    continue;
+                }
+                ++n;
                 bool ok = true;
                 const int tiles_of_job = J.pair ? 2 * J.nt : J.nt;
                 for (int j = 0; j < tiles_of_job; ++j, ++t) {
@@ -502,14 +512,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto ready = [&](int full, int s, int tile) {
             return poll(full + s, (tile / ST) & 1);
         };
-        for (int n = 0; ok; ++n) {
-            const int js = n % kJobs;
-            if (!poll(L::kBarJF + js, (n / kJobs) & 1)) break;
+        int n = -1;  // the job's number
+        for (int r = 0; ok; ++r) {
+            const int js = r % kJobs;
+            if (!poll(L::kBarJF + js, (r / kJobs) & 1)) break;
             const Job *R = ring + js;
-            const int te[kG] = {all(R->h[0].te), all(R->h[1].te)}, nt = all(R->nt);
-            const bool valid = all(R->valid), pair = all(R->pair);
+            const int te[kG] = {all(R->h[0].te), all(R->h[1].te)}, nt = all(R->nt), valid = all(R->valid);
+            const bool pair = all(R->pair);
             one_arrive(bar(L::kBarJE + js));
-            if (!valid) break;
+            if (valid == kNoJob) break;
+            if (valid == kLists) {
+                after_previous();
+                continue;
+            }
+            ++n;
             // a Q tile without tiles in this job is released at once
 #pragma unroll
             for (int g = 0; g < kG; ++g)
@@ -579,12 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return __all_sync(0xffffffffu, mbar_poll(bar(b), parity) || wait_bar(bar(b), parity, ctl));
         };
         // this thread's row of a job: row << 5 | slot
-        bool lists = false;  // the kernels that make the lists have ended
         auto entry_of = [&](const Mine &J) -> int {
-            if (!J.own && !lists) {
-                after_previous();
-                lists = true;
-            }
             if (trow >= J.h.nrows) return -1;
             if (J.own) return (J.h.rbase + trow) << 5 | a.km1;
             // (two sequences that claim the same rows, from offsets that decrease,
@@ -615,26 +626,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             cp_async_arrive_noinc(bar(L::kBarQ + g));
         };
-        auto take = [&](int n, Mine &J) -> bool {
-            const int js = n % kJobs;
-            if (!wait(L::kBarJF + js, (n / kJobs) & 1)) return false;
-            const Job &R = ring[js];
-            J.h = R.h[g];
-            J.valid = R.valid;
-            J.own = R.own;
-            J.key_end = R.key_end;
-            J.lo = R.lo;
-            J.pdelta = R.pdelta;
-            J.whole = R.whole;
-            J.slot = R.slot;
-            J.tiles = R.pair ? 2 * R.nt : R.nt;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::kBarJE + js));
-            return true;
+        int r = 0;  // descriptors so far
+        auto take = [&](Mine &J) -> bool {
+            for (;;) {
+                const int js = r % kJobs;
+                if (!wait(L::kBarJF + js, (r / kJobs) & 1)) return false;
+                const Job &R = ring[js];
+                J.h = R.h[g];
+                J.valid = R.valid;
+                J.own = R.own;
+                J.key_end = R.key_end;
+                J.lo = R.lo;
+                J.pdelta = R.pdelta;
+                J.whole = R.whole;
+                J.slot = R.slot;
+                J.tiles = R.pair ? 2 * R.nt : R.nt;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::kBarJE + js));
+                ++r;
+                if (DENSE || J.valid != kLists) return true;
+                after_previous();
+            }
         };
         int gt = 0, gj = 0, t = 0, n = 0;
         Mine J;
-        bool ok = take(0, J);
+        bool ok = take(J);
         int entry = -1;
         if (ok && J.valid) {
             entry = entry_of(J);
@@ -768,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             t += J.tiles;
             // the next job's rows, as soon as this job's S MMAs have read Q
             Mine NJ;
-            if (!take(n + 1, NJ)) {
+            if (!take(NJ)) {
                 ok = false;
                 break;
             }

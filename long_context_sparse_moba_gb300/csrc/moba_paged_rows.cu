@@ -768,9 +768,8 @@ int make_attn(Attn *a, int Hq, int D, int topk) {
     // 363.  Against it: blocks of 128 137 and 152, heads of 64 over all blocks 89 and 95)
     const bool many = rows > 32 && (long long)a->c.num_seqs * a->c.Hkv >= 64 &&
                       (a->dense ? D == 128 : bs >= 512);
-    // (the plan takes 1 ns for a list in use, while the tcgen05 kernel's waits of two seconds run)
     a->chunk = (rows > kMaxRows || many) && (long long)a->c.total * a->G < (1ll << 26) &&
-               lists < (1ll << 28) && a->list_cap < (1ll << 31);
+               lists < (1ll << 30) && a->list_cap < (1ll << 31);
     if (a->chunk) {
         const long long w0 = (long long)a->c.num_seqs * ((rows + kJobRows - 1) / kJobRows);
         const long long w1 = (long long)a->c.total * a->G / kJobRows + a->c.num_seqs;
