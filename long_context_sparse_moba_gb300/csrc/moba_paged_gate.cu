@@ -414,8 +414,11 @@ __device__ __forceinline__ void settle(const Attn &a, int hk, const int *table, 
     if (lane < km1) sel[lane] = who;
 }
 
+// (four CTAs an SM where 128 registers hold the ranks: the compiler's own choice of 168
+// left three; 32 and 64 sequences of 32 kv heads over 64 blocks of 128, k 6, 108 and
+// 196 us, against 116 and 205)
 template <int D, int NS>
-__global__ void __launch_bounds__(kThreads) gate_kernel(Attn a, int words) {
+__global__ void __launch_bounds__(kThreads, NS > 2 ? 0 : 4) gate_kernel(Attn a, int words) {
     constexpr int KS = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_bad, s_knmax, s_count, s_page[kTile];
