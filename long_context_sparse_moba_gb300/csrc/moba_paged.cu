@@ -57,9 +57,10 @@ int make_cache(Cache *c, const void *k_pages, const void *v_pages, const float *
 // ascending order, whatever their source: a pooled key depends neither on how the
 // appends were cut nor on the size of the cluster.  Sums are compensated (Kahan), as in the key pooling
 // kernel; the others send theirs to the first CTA's shared memory.
-// Bound: HBM for long chunks (79 us, 6.8 TB/s at 65536 tokens of 8 heads of 128,
-// blocks of 512), latency for a step: the one that completes a block reads all of its keys,
-// which eight CTAs do in two rounds of loads.
+// Bound: HBM for long chunks (76 us at 65536 tokens of 8 heads of 128, blocks of 512:
+// the copy rate), latency for a step (2.5 us in a graph; 9 by a call, which is the host):
+// the one that completes a block reads all of its keys, which eight CTAs do in two rounds
+// of loads.
 constexpr int kAppendThreads = 128;
 constexpr int kAppendParts = 8;     // of a block's tokens; the 1, 2, 4 or 8 CTAs of a cluster take them
 constexpr int kAppendPages = 512;
@@ -276,7 +277,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 // destination list: a destination given twice, or a source that some pair
 // overwrites, would make the result depend on the order.
 // Bound: HBM; 203 us for 2500 pages of 8 x 64 x 128 (6.6 TB/s, 0.97 of the copy
-// rate), 16 us for 16 pages in 8 layers, which is one wave's loads and stores.
+// rate); 16 us for 16 pages in 8 layers, latency: 1024 CTAs of which 73 registers let 456
+// in at once.  Many small pages are bound by the look at the list, n entries a CTA: 65536
+// pages of 16 tokens of one head of 64 take 1.4 ms where their bytes take 84 us, 16384
+// of them 137 us.
 constexpr int kCopyThreads = 256;
 
 struct CopyArgs {
@@ -381,11 +385,11 @@ MOBA_EXPORT int moba_paged_append(const void *k, const void *v, void *k_pages, v
     }
     if (a.clusters >= (1ll << 31) / kAppendParts) return MOBA_ERR_UNSUPPORTED;
     // CTAs to a block.  More of them shorten the step that completes one, fewer
-    // leave the GPU to more blocks at once (five CTAs fit an SM).  us with 8,
-    // 4, 2, 1 (D 128, 8 kv heads, blocks of 512): a step of one sequence that
-    // completes its block 4.8, 6.6, 10.4, 17.1; of 64 of which few do 12.3, 11.7, 14.0,
-    // 19.0; of 256 that do not 26.6, 19.2, 18.3, 14.9; a chunk of 65536 tokens 91, 85,
-    // 81, 89, and 312, 216, 167, 136 with blocks of 64
+    // leave the GPU to more blocks at once (six CTAs fit an SM).  us with 8,
+    // 4, 2, 1 (D 128, 8 kv heads, blocks of 512, in a graph): a step of one sequence that
+    // completes its block 4.8, 6.7, 10.4, 17.2; of 64 of which one does 9.3, 9.0, 11.1,
+    // 17.9; of 256 of which three do 25.1, 18.8, 18.7, 24.1; a chunk of 65536 tokens 78,
+    // 73, 75, 84, and 267, 185, 144, 117 with blocks of 64
     const double per_sm = (double)((long long)total / block_size + num_seqs) * Hkv / sm_count();
     a.ctas = per_sm * 8 <= 6 ? 8 : per_sm * 4 <= 15 ? 4 : block_size >= 512 ? 2 : 1;
     a.status = status_word();
@@ -423,7 +427,7 @@ MOBA_EXPORT int moba_page_copy(void *k_pages, void *v_pages, float *kbar_pages, 
     a.bar16 = (long long)Hkv * D / 4;
     a.status = status_word();
     if (!a.status) return cuda_result(cudaErrorInvalidDevice);
-    // enough CTAs to fill the GPU; a part is at least 16 KB of a page
+    // eight CTAs an SM (three fit at once); a part is at least 16 KB of a page
     const long long fill = (long long)sm_count() * 8;
     long long parts = (fill + (long long)n * layers - 1) / ((long long)n * layers);
     const long long most = (a.page16 + 1023) / 1024;

@@ -24,8 +24,9 @@
 //     job that falls into several runs leaves fp32 partial sums.
 //
 // With selection, the CTAs start as the gate's leave and work off equal shares of
-// (2), which need no list, while the plan and scatter kernels make the lists (14 us of
-// a call of 232 at 4096 tokens x 32 heads of 128 over 32768 keys).
+// (2), which need no list, while the plan and scatter kernels make the lists (15 us of
+// a call of 200 at 4096 tokens x 32 heads of 128 over 32768 keys).  A mark in the ring of
+// job descriptors then has every role wait for those kernels.
 //
 // Persistent, one CTA per SM, 12 warps:
 //   warp 0   K pages by TMA (one lane), warp 10 V pages, into rings of tiles;
@@ -42,7 +43,8 @@
 // are zeroed in the V tile before its product; in K their scores are masked.
 // Bound: tensor and softmax in turn where jobs are long: 2048 rows x 32 heads over
 // 32768 keys of 128 take 719 us in this kernel alone, 800 us in a row of
-// calls, 1340 TFLOP/s, 0.71 of the burst peak.
+// calls, 1340 TFLOP/s, 0.70 of the burst peak.  168 registers a thread is all that 384
+// threads leave: over all blocks the softmax spills 40 to 52 bytes, with lists nothing.
 // Job boundaries where they are short: 4096 tokens x 32 heads, three blocks of 512
 // (four tiles a job) 100 us behind the lists; blocks of 128 are one tile a job.
 // Every mbarrier wait is bounded: one that runs out sets MOBA_ERR_TIMEOUT in the
@@ -719,7 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tc_st16(tO + c0, o);
                             }
                         }
-                        if (h2 > 0) {  // the first half's P was made with the old offset
+                        if (h2 > 0) {
+                            // the first half's P was made with the old offset: rounded again,
+                            // but by a power of two, so exact unless it underflows
                             tc_wait_st();
 #pragma unroll
                             for (int c0 = 0; c0 < 32; c0 += 16) {
@@ -1104,7 +1108,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
 }
 
 // The rows into the lists of the blocks that they selected; a row's slots are
-// its past blocks in ascending order.  Latency: 7 us for 262144 entries (the plan 6 us).
+// its past blocks in ascending order.  Latency: 8 us for 262144 entries (the plan 6 us).
 constexpr int kScatterThreads = 1024;
 
 __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(Attn a) {

@@ -31,7 +31,10 @@
 // blocks takes 10 to 17 us, a chunk of 4096 tokens x 32 heads of 128 over 64 blocks
 // 54 us: of a CTA's 38 K cycles, three CTAs side by side on an SM, 6 K bring the
 // pooled keys in, 12 K score (8 cycles an MMA on each of the SM's four parts), 5 K
-// rank, 8 K go to near ties and 6 K to the lists.
+// rank, 8 K go to near ties and 6 K to the lists.  (2.5 rows a ns; the prefill gate's
+// tcgen05 scores reach 6.)  Three CTAs an SM leave chunk_gate_kernel 80 registers: with
+// heads of 128 it spills 96 bytes up to top-k 3 and 156 up to 7, and its 1032 CTAs are
+// two waves and a quarter.  From top-k 8 on the ranks take up to 236 registers, one CTA.
 #include "moba_mma.cuh"
 #include "moba_paged_attn.cuh"
 #include "moba_select.cuh"

@@ -21,7 +21,9 @@
 // phases of a stage's barrier could take an old phase for its own); they join
 // through shared memory at the end of an entry's part.  Scores and outputs on
 // mma.sync; one pass with running maximum and sum in 32 bits; P is rounded to
-// bf16 for the second product, as the prefill kernels do.
+// bf16 for the second product, as the prefill kernels do: relative to 64 bits outputs
+// err by 0.0022, of which the result's own rounding is 0.0016.  (A second bf16 term of P
+// brings that back to 0.0016 and costs 3 % over all blocks, about 5 % with selection.)
 // Waits on mbarriers are bounded as in the other kernels; a warp that gives up
 // still joins the barrier of the part, where all warps agree to leave.
 // Measured (heads of 128): 16 sequences of up to 49152 tokens, 32 / 8 heads, all blocks
@@ -765,7 +767,8 @@ int make_attn(Attn *a, int Hq, int D, int topk) {
     // 64 rows, caches of 16384, blocks of 512: 8 sequences of 8 kv heads 132 to 147 and
     // 124 to 127 with selection, 118 to 122 and 108 to 112 over all blocks, 99 to 109
     // and 89 to 92 with selection and heads of 64; 32 sequences 408 to 446 and 337 to
-    // 363.  Against it: blocks of 128 137 and 152, heads of 64 over all blocks 89 and 95)
+    // 363.  Against it: blocks of 128 137 and 152, heads of 64 over all blocks 89 and 95.
+    // Blocks of 256 were not measured)
     const bool many = rows > 32 && (long long)a->c.num_seqs * a->c.Hkv >= 64 &&
                       (a->dense ? D == 128 : bs >= 512);
     a->chunk = (rows > kMaxRows || many) && (long long)a->c.total * a->G < (1ll << 26) &&

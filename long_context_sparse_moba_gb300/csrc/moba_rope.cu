@@ -16,7 +16,9 @@
 // token and a run of its heads; a lane keeps the cos and sin of its eight
 // pairs in registers for all of them, so the phases cost little.  Measured: 165 us
 // for 32768 tokens of 64 heads of 128, 6.5 TB/s, 0.97 of the copy rate; 85 us, 0.93,
-// for the gradient of 32764 tokens of 32 heads, half of each rotated.
+// for the gradient of 32764 tokens of 32 heads, half of each rotated.  A decode step's
+// tokens are bound by latency and the call: 1, 64, 256 tokens of 40 heads 2.9, 3.4, 3.3 us
+// in a graph, 10.6 by a call from Python.
 #include <cmath>
 
 #include "moba.h"
