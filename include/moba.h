@@ -475,6 +475,42 @@ int moba_rope_frequencies(double *freqs, int rot_dim, double base, int scaling, 
                           double original_length, double slow_turns, double fast_turns);
 
 /*
+ * Norms of queries and keys for each head, with the rotation of moba_rope in the same
+ * pass, for models that normalise q and k:  y = R(x r w),  r = 1 / sqrt(mean x^2 + eps)
+ * over the D values of a head, all in fp32 and rounded once, to bf16.
+ *   q, k, q_out, k_out, strides, positions, freqs, rot_dim, interleaved, magnitude:
+ *     as for moba_rope (k and k_out NULL with Hk = 0); the magnitude scales the rotated
+ *     values only
+ *   q_weight, k_weight : [D] bf16 or fp32 (weight_bits 16 or 32; device)
+ *   eps : finite, at least 1e-12
+ * An output may be its own input; any other overlap is MOBA_ERR_INVALID_ARG.
+ *
+ * moba_qk_norm_rope_bwd is the gradient, from that of the outputs (dq_out, dk_out) and
+ * the forward's inputs q, k: with g = R^T dy and n = x r,
+ *   dx = r (g w - n mean(g w n)),  dw = sum over tokens and heads of g n (fp32 [D]).
+ * dq may be dq_out and dk dk_out, in place; any other overlap is an error.  The order of
+ * dw's sums goes by the sizes and the GPU alone: equal calls give equal bits.
+ * workspace: device scratch, 256-byte aligned, at least
+ * moba_qk_norm_rope_bwd_workspace_size bytes (asked with the same device current), used
+ * by nothing else until the call's work has finished; NULL: stream-ordered scratch of the
+ * call's own.  It needs no initialisation.
+ */
+int moba_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const void *q_weight,
+                      const void *k_weight, int weight_bits, float eps, const int32_t *positions,
+                      const double *freqs, int tokens, int Hq, int Hk, int D, int rot_dim,
+                      int interleaved, float magnitude, long long q_stride, long long k_stride,
+                      long long q_out_stride, long long k_out_stride, void *stream);
+int moba_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                          const void *q_weight, const void *k_weight, void *dq, void *dk,
+                          float *dq_weight, float *dk_weight, int weight_bits, float eps,
+                          const int32_t *positions, const double *freqs, int tokens, int Hq, int Hk,
+                          int D, int rot_dim, int interleaved, float magnitude,
+                          long long dq_out_stride, long long dk_out_stride, long long q_stride,
+                          long long k_stride, long long dq_stride, long long dk_stride,
+                          void *workspace, size_t workspace_bytes, void *stream);
+size_t moba_qk_norm_rope_bwd_workspace_size(int tokens, int Hq, int Hk, int D);
+
+/*
  * Paged cache.  One layer's cache is three pools of pages of page_size tokens:
  *   k_pages, v_pages : [num_pages][Hkv][page_size][D] bf16 (device); a page's
  *                      tokens of one head are one dense run, since heads
@@ -517,6 +553,31 @@ int moba_paged_append(const void *k, const void *v, void *k_pages, void *v_pages
                       const int32_t *cache_lens, int num_seqs, int total, int max_new, int Hkv,
                       int D, int num_pages, int page_size, int max_pages, int block_size,
                       const moba_options_t *options, void *stream);
+
+/*
+ * moba_paged_append with the norms and the rotation applied on the way: the new tokens'
+ * q, normalised and rotated, go to q_out, k the same to the pages, v as it is, and the
+ * completed blocks are pooled from the keys as stored, to the same bits as by
+ * moba_paged_append.  q, k and v are read once, from slices of one projection as they are.
+ *   q, q_out [total][Hq][D], k, v [total][Hkv][D] bf16 (device): a token's heads dense,
+ *     tokens *_stride elements apart (0: dense); 16-byte aligned, strides multiples of 8
+ *   positions : [total] int32 (device), or NULL: a token's place in its sequence
+ *   q_weight, k_weight : [D] bf16 or fp32 (weight_bits 16 or 32), or NULL: that operand
+ *     is rotated only; weight_bits and eps count where one is given
+ *   freqs, rot_dim, interleaved, magnitude, eps: as for moba_qk_norm_rope
+ * q_out may be q; an overlap with anything else is MOBA_ERR_INVALID_ARG.  Rows of q_out
+ * of refused sequences, and behind the last one, are left as they were.
+ */
+int moba_paged_append_rope(const void *q, const void *k, const void *v, void *q_out, void *k_pages,
+                           void *v_pages, float *kbar_pages, const int32_t *page_table,
+                           const int32_t *cu_new, const int32_t *cache_lens,
+                           const int32_t *positions, const double *freqs, const void *q_weight,
+                           const void *k_weight, int weight_bits, float eps, int num_seqs, int total,
+                           int max_new, int Hq, int Hkv, int D, int rot_dim, int interleaved,
+                           float magnitude, long long q_stride, long long k_stride,
+                           long long v_stride, long long q_out_stride, int num_pages, int page_size,
+                           int max_pages, int block_size, const moba_options_t *options,
+                           void *stream);
 
 /*
  * Attention of the new tokens over the paged cache (their own k, v appended

@@ -65,18 +65,6 @@ constexpr int kAppendThreads = 128;
 constexpr int kAppendParts = 8;     // of a block's tokens; the 1, 2, 4 or 8 CTAs of a cluster take them
 constexpr int kAppendPages = 512;
 
-struct AppendArgs {
-    Cache c;
-    const __nv_bfloat16 *k, *v;  // [total][Hkv][D]
-    __nv_bfloat16 *kp, *vp;
-    float *kbar;
-    int cand;  // blocks that a sequence's new tokens touch, at most; 0: clusters by packed tokens
-    int psh;   // log2(page size)
-    long long clusters;
-    int ctas;  // of a cluster
-    int *status;
-};
-
 // the address of a shared variable's counterpart in CTA 0 of the cluster
 __device__ __forceinline__ uint32_t in_first(const void *p) {
     uint32_t at;
@@ -112,7 +100,9 @@ __device__ __noinline__ float mean64(const __nv_bfloat16 *kp, int Hkv, int psh, 
     return (float)(sum / bs);
 }
 
-template <int D, bool MAX>
+// POOL: the new tokens are in their pages already, from the kernel before this one, and
+// the CTAs only sum what is complete: the same sums in the same order.
+template <int D, bool MAX, bool POOL>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     constexpr int CW = D / 8;                        // threads across a token
     constexpr int GC = kAppendThreads / CW;          // groups of a CTA
@@ -122,6 +112,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     __shared__ float s_sum[kAppendParts][D], s_bad[kAppendParts];  // of CTA 0: the parts' sums
     __shared__ int s_page[kAppendPages], s_abort;
     __shared__ __align__(8) unsigned long long s_bar;
+    if (POOL) after_previous();
     const int rank = blockIdx.x & (a.ctas - 1), bj = (int)blockIdx.x / a.ctas, hk = blockIdx.y;
     int b, nth;  // the sequence, and which of the blocks that its new tokens touch
     Seq s;
@@ -140,11 +131,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
         return;
     }
     const int bs = a.c.bs, ps = a.c.ps;
-    const int first = s.len - s.n;  // position of the first new token
     if (nth < 0 || nth > s.n / bs + 1) return;
-    const int p0 = (first / bs + nth) * bs;
+    const int p0 = ((s.len - s.n) / bs + nth) * bs;
+    const int first = POOL ? s.len : s.len - s.n;  // position of the first token from k and v
     if (p0 >= s.len) return;
     const bool pool = a.kbar && p0 + bs <= s.len;
+    if (POOL && !pool) return;
     const int c1 = min(p0 + bs, s.len);
     const int t0 = pool ? p0 : max(p0, first);  // first token that is read
     if (!pool && c1 - t0 == 1 && (((t0 - p0) % G / GC) & (a.ctas - 1)) != rank)
@@ -325,21 +317,63 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(CopyArgs a) {
     if (a.kbar) copy_run(a.kbar + s * a.bar16, a.kbar + d * a.bar16, a.bar16, part, a.parts);
 }
 
-template <int D>
+template <int D, bool POOL>
 static cudaError_t launch_append(const AppendArgs &a, bool max, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.clusters * a.ctas), a.c.Hkv);
     cfg.blockDim = kAppendThreads;
     cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = a.ctas;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = a.ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = POOL ? 2 : 1;
     note_launches(1);
-    return max ? cudaLaunchKernelEx(&cfg, append_kernel<D, true>, a)
-               : cudaLaunchKernelEx(&cfg, append_kernel<D, false>, a);
+    return max ? cudaLaunchKernelEx(&cfg, append_kernel<D, true, POOL>, a)
+               : cudaLaunchKernelEx(&cfg, append_kernel<D, false, POOL>, a);
+}
+
+// The grid of an append whose cache and pools are set.
+static int plan_append(AppendArgs *a) {
+    const int bs = a->c.bs;
+    a->psh = __builtin_ctz((unsigned)a->c.ps);
+    a->cand = (int)(((long long)a->c.max_new + bs - 2) / bs + 1);
+    // clusters for the longest chunk of every sequence, or, where chunks are uneven
+    // and that is more of them, by packed tokens (n tokens touch n / block_size + 2
+    // blocks at most), which costs a search for the sequence
+    a->clusters = (long long)a->c.num_seqs * a->cand;
+    const long long packed = a->c.tile_slots(1, bs, 2);
+    if (packed < a->clusters) {
+        a->clusters = packed;
+        a->cand = 0;
+    }
+    if (a->clusters >= (1ll << 31) / kAppendParts) return MOBA_ERR_UNSUPPORTED;
+    // CTAs to a block.  More of them shorten the step that completes one, fewer
+    // leave the GPU to more blocks at once (six CTAs fit an SM).  us with 8,
+    // 4, 2, 1 (D 128, 8 kv heads, blocks of 512, in a graph): a step of one sequence that
+    // completes its block 4.8, 6.7, 10.4, 17.2; of 64 of which one does 9.3, 9.0, 11.1,
+    // 17.9; of 256 of which three do 25.1, 18.8, 18.7, 24.1; a chunk of 65536 tokens 78,
+    // 73, 75, 84, and 267, 185, 144, 117 with blocks of 64
+    const double per_sm = (double)((long long)a->c.total / bs + a->c.num_seqs) * a->c.Hkv / sm_count();
+    a->ctas = per_sm * 8 <= 6 ? 8 : per_sm * 4 <= 15 ? 4 : bs >= 512 ? 2 : 1;
+    return MOBA_OK;
+}
+
+int make_pool(AppendArgs *a, const Cache &c, void *k_pages, float *kbar_pages, int *status) {
+    a->c = c;
+    a->k = a->v = nullptr;
+    a->kp = static_cast<__nv_bfloat16 *>(k_pages);
+    a->vp = nullptr;
+    a->kbar = kbar_pages;
+    a->status = status;
+    return plan_append(a);
+}
+
+cudaError_t launch_pool(const AppendArgs &a, int D, bool max, cudaStream_t st) {
+    return D == 64 ? launch_append<64, true>(a, max, st) : launch_append<128, true>(a, max, st);
 }
 
 }  // namespace paged
@@ -372,31 +406,13 @@ MOBA_EXPORT int moba_paged_append(const void *k, const void *v, void *k_pages, v
     a.kp = static_cast<__nv_bfloat16 *>(k_pages);
     a.vp = static_cast<__nv_bfloat16 *>(v_pages);
     a.kbar = kbar_pages;
-    a.psh = __builtin_ctz((unsigned)page_size);
-    a.cand = (int)(((long long)a.c.max_new + block_size - 2) / block_size + 1);
-    // clusters for the longest chunk of every sequence, or, where chunks are uneven
-    // and that is more of them, by packed tokens (n tokens touch n / block_size + 2
-    // blocks at most), which costs a search for the sequence
-    a.clusters = (long long)num_seqs * a.cand;
-    const long long packed = a.c.tile_slots(1, block_size, 2);
-    if (packed < a.clusters) {
-        a.clusters = packed;
-        a.cand = 0;
-    }
-    if (a.clusters >= (1ll << 31) / kAppendParts) return MOBA_ERR_UNSUPPORTED;
-    // CTAs to a block.  More of them shorten the step that completes one, fewer
-    // leave the GPU to more blocks at once (six CTAs fit an SM).  us with 8,
-    // 4, 2, 1 (D 128, 8 kv heads, blocks of 512, in a graph): a step of one sequence that
-    // completes its block 4.8, 6.7, 10.4, 17.2; of 64 of which one does 9.3, 9.0, 11.1,
-    // 17.9; of 256 of which three do 25.1, 18.8, 18.7, 24.1; a chunk of 65536 tokens 78,
-    // 73, 75, 84, and 267, 185, 144, 117 with blocks of 64
-    const double per_sm = (double)((long long)total / block_size + num_seqs) * Hkv / sm_count();
-    a.ctas = per_sm * 8 <= 6 ? 8 : per_sm * 4 <= 15 ? 4 : block_size >= 512 ? 2 : 1;
+    const int planned = plan_append(&a);
+    if (planned != MOBA_OK) return planned;
     a.status = status_word();
     if (!a.status) return cuda_result(cudaErrorInvalidDevice);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool max = pool == MOBA_POOL_MAX;
-    return cuda_result(D == 64 ? launch_append<64>(a, max, st) : launch_append<128>(a, max, st));
+    return cuda_result(D == 64 ? launch_append<64, false>(a, max, st) : launch_append<128, false>(a, max, st));
 }
 
 MOBA_EXPORT int moba_page_copy(void *k_pages, void *v_pages, float *kbar_pages, const int32_t *src,

@@ -102,6 +102,23 @@ cudaError_t allow_smem(int bytes) {
     return rc;
 }
 
+// Appending (moba_paged.cu), or pooling what has been appended.
+struct AppendArgs {
+    Cache c;
+    const __nv_bfloat16 *k, *v;  // [total][Hkv][D]
+    __nv_bfloat16 *kp, *vp;
+    float *kbar;
+    int cand;  // blocks that a sequence's new tokens touch, at most; 0: clusters by packed tokens
+    int psh;   // log2(page size)
+    long long clusters;
+    int ctas;  // of a cluster
+    int *status;
+};
+// Pooling alone, behind a kernel of the same call that wrote the pages: its arguments
+// (MOBA_OK, or why not), and the launch.
+int make_pool(AppendArgs *a, const Cache &c, void *k_pages, float *kbar_pages, int *status);
+cudaError_t launch_pool(const AppendArgs &a, int D, bool max, cudaStream_t st);
+
 // Host checks shared by the entry points; fills c.
 int make_cache(Cache *c, const void *k_pages, const void *v_pages, const float *kbar_pages,
                const int32_t *table, const int32_t *cu, const int32_t *lens, int num_seqs,

@@ -1,0 +1,416 @@
+// moba_qk_norm.cu -- norms of queries and keys for each head with the position
+// rotation in the same pass, and their gradient.
+//
+// Pages: "When a MoBA reproduction will not run" (mhpq.cn/news/582794) section
+// 3.3 asks where positions enter MoBA; here they enter before the gate, and so do the
+// norms of models that bound their logits by normalising q and k.
+//
+// For a head x of D values with weights w:  r = 1 / sqrt(mean x^2 + eps),
+//   y = R (x r w), R the rotation of moba_rope.
+// Gradient, with g = R^T dy and n = x r:
+//   dx = r (g w - n mean(g w n)),  dw = sum over tokens and heads of g n.
+// Everything between the loads and the one rounding of the result is fp32; r and n are
+// made again from x in the gradient, which costs nothing where x has to be read anyway.
+//
+// Bound: HBM (4 bytes a value, 6 in the gradient).
+#include <cmath>
+
+#include "moba.h"
+#include "moba_paged.cuh"
+#include "moba_rope.cuh"
+
+namespace moba {
+namespace qk_norm {
+
+using namespace rope;
+
+constexpr int kWarps = 8;
+constexpr int kUnroll = 4;      // heads whose loads a lane has in flight
+constexpr int kBwdUnroll = 2;
+constexpr int kFwdCtas = 8, kBwdCtas = 2;  // of an SM at most
+
+struct Side {                   // q or k
+    const __nv_bfloat16 *x, *dy;  // dy: gradient only
+    __nv_bfloat16 *out;
+    const void *w;
+    long long xs, ds, os;       // elements between tokens
+    int heads;
+    int chunk, splits;          // gradient: heads per unit, units per token
+};
+struct Args {
+    Side q, k;
+    const int32_t *pos;
+    const double *freqs;
+    float *part;                // gradient: [CTAs][D] sums of the weights'
+    int q_ctas;                 // gradient: CTAs of q, before those of k
+    int tokens, rot;
+    int chunk, splits;          // heads per unit, units per token
+    int w32;                    // weights are fp32 (else bf16)
+    float eps, mag;
+};
+
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(32 * kWarps) fwd_kernel(Args a) {
+    constexpr int LH = D / 16;   // lanes per head: 16 values (8 pairs) each
+    constexpr int HW = 32 / LH;  // heads per warp and step
+    __shared__ unsigned long long s_turn[D / 2];
+    __shared__ __align__(16) float s_w[2][D];
+    load_turns(s_turn, a.freqs, a.rot / 2, threadIdx.x, 32 * kWarps);
+    for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps)
+        if (i < D || a.k.heads) s_w[i / D][i % D] = weight(i < D ? a.q.w : a.k.w, a.w32, i % D);
+    __syncthreads();
+    const int lane = threadIdx.x & 31, item = lane % LH, hsub = lane / LH;
+    const bool turns = item < a.rot / 16;  // the other items are not rotated
+    int va, vb;
+    vectors<D, INTERLEAVED>(item, a.rot / 2, va, vb);
+    const long long units = (long long)a.tokens * a.splits;
+    for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units;
+         u += (long long)gridDim.x * kWarps) {
+        const int t = (int)(u / a.splits);
+        const int h0 = (int)(u % a.splits) * a.chunk, h1 = min(h0 + a.chunk, a.q.heads + a.k.heads);
+        float c[8], s[8];
+        if (turns) cos_sin(s_turn + item * 8, __ldg(a.pos + t), a.mag, 1.f, c, s);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+            const Side &x = kv ? a.k : a.q;
+            const int base = kv ? a.q.heads : 0, lo = max(h0 - base, 0), hi = min(h1 - base, x.heads);
+            if (lo >= hi) continue;
+            float wa[8], wb[8];
+            load_weights(s_w[kv], va, vb, wa, wb);
+            const __nv_bfloat16 *src = x.x + t * x.xs;
+            __nv_bfloat16 *dst = x.out + t * x.os;
+            for (int hb = lo; hb < hi; hb += HW * kUnroll) {
+                uint4 xa[kUnroll], xb[kUnroll];
+#pragma unroll
+                for (int j = 0; j < kUnroll; ++j) {
+                    const int h = hb + j * HW + hsub;
+                    xa[j] = xb[j] = make_uint4(0, 0, 0, 0);
+                    if (h < hi) {
+                        xa[j] = *reinterpret_cast<const uint4 *>(src + (size_t)h * D + va);
+                        xb[j] = *reinterpret_cast<const uint4 *>(src + (size_t)h * D + vb);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kUnroll; ++j) {
+                    const int h = hb + j * HW + hsub;
+                    float fa[8], fb[8];
+                    unpack(xa[j], fa);
+                    unpack(xb[j], fb);
+                    normalise<D>(fa, fb, wa, wb, a.eps);
+                    if (turns) turn_pairs<INTERLEAVED>(fa, fb, c, s);
+                    if (h < hi) {
+                        *reinterpret_cast<uint4 *>(dst + (size_t)h * D + va) = pack(fa);
+                        *reinterpret_cast<uint4 *>(dst + (size_t)h * D + vb) = pack(fb);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// The first q_ctas CTAs take q, the others k, so that a thread sums one weight's
+// gradient (both cost it 16 more registers, and the second CTA of an SM).
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
+    constexpr int LH = D / 16, HW = 32 / LH;
+    __shared__ unsigned long long s_turn[D / 2];
+    __shared__ __align__(16) float s_w[D];
+    __shared__ float s_sum[kWarps][D];
+    const bool is_k = (int)blockIdx.x >= a.q_ctas;
+    const Side x = is_k ? a.k : a.q;
+    load_turns(s_turn, a.freqs, a.rot / 2, threadIdx.x, 32 * kWarps);
+    for (int i = threadIdx.x; i < D; i += 32 * kWarps) s_w[i] = weight(x.w, a.w32, i);
+    __syncthreads();
+    paged::let_next();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, item = lane % LH, hsub = lane / LH;
+    const bool turns = item < a.rot / 16;
+    int va, vb;
+    vectors<D, INTERLEAVED>(item, a.rot / 2, va, vb);
+    float wa[8], wb[8], da[8], db[8];  // weights, and the sums of their gradients
+    load_weights(s_w, va, vb, wa, wb);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) da[i] = db[i] = 0.f;
+    const int cta = is_k ? blockIdx.x - a.q_ctas : blockIdx.x, ctas = is_k ? gridDim.x - a.q_ctas : a.q_ctas;
+    const long long units = (long long)a.tokens * x.splits;
+    for (long long u = (long long)cta * kWarps + warp; u < units; u += (long long)ctas * kWarps) {
+        const int t = (int)(u / x.splits);
+        const int lo = (int)(u % x.splits) * x.chunk, hi = min(lo + x.chunk, x.heads);
+        float c[8], s[8];
+        if (turns) cos_sin(s_turn + item * 8, __ldg(a.pos + t), a.mag, -1.f, c, s);
+        const __nv_bfloat16 *src = x.x + t * x.xs, *up = x.dy + t * x.ds;
+        __nv_bfloat16 *dst = x.out + t * x.os;
+        for (int hb = lo; hb < hi; hb += HW * kBwdUnroll) {
+            uint4 xa[kBwdUnroll], xb[kBwdUnroll], ya[kBwdUnroll], yb[kBwdUnroll];
+#pragma unroll
+            for (int j = 0; j < kBwdUnroll; ++j) {
+                const int h = hb + j * HW + hsub;
+                xa[j] = xb[j] = ya[j] = yb[j] = make_uint4(0, 0, 0, 0);
+                if (h < hi) {
+                    xa[j] = *reinterpret_cast<const uint4 *>(src + (size_t)h * D + va);
+                    xb[j] = *reinterpret_cast<const uint4 *>(src + (size_t)h * D + vb);
+                    ya[j] = *reinterpret_cast<const uint4 *>(up + (size_t)h * D + va);
+                    yb[j] = *reinterpret_cast<const uint4 *>(up + (size_t)h * D + vb);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kBwdUnroll; ++j) {
+                const int h = hb + j * HW + hsub;
+                float fa[8], fb[8], ga[8], gb[8];
+                unpack(xa[j], fa);
+                unpack(xb[j], fb);
+                unpack(ya[j], ga);
+                unpack(yb[j], gb);
+                const float r = inverse_rms<D>(fa, fb, a.eps);
+                if (turns) turn_pairs<INTERLEAVED>(ga, gb, c, s);
+                float dot = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    fa[i] *= r;
+                    fb[i] *= r;
+                    da[i] = fmaf(ga[i], fa[i], da[i]);
+                    db[i] = fmaf(gb[i], fb[i], db[i]);
+                    ga[i] *= wa[i];
+                    gb[i] *= wb[i];
+                    dot = fmaf(ga[i], fa[i], dot);
+                    dot = fmaf(gb[i], fb[i], dot);
+                }
+#pragma unroll
+                for (int o = 1; o < LH; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                dot *= -1.f / D;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    ga[i] = r * fmaf(fa[i], dot, ga[i]);
+                    gb[i] = r * fmaf(fb[i], dot, gb[i]);
+                }
+                if (h < hi) {
+                    *reinterpret_cast<uint4 *>(dst + (size_t)h * D + va) = pack(ga);
+                    *reinterpret_cast<uint4 *>(dst + (size_t)h * D + vb) = pack(gb);
+                }
+            }
+        }
+    }
+    // the weight's gradient of this CTA, in an order fixed by the grid alone
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int o = LH; o < 32; o <<= 1) {
+            da[i] += __shfl_xor_sync(0xffffffffu, da[i], o);
+            db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
+        }
+        if (hsub == 0) {
+            s_sum[warp][va + i] = da[i];
+            s_sum[warp][vb + i] = db[i];
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += 32 * kWarps) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += s_sum[w][i];
+        a.part[(size_t)blockIdx.x * D + i] = sum;
+    }
+}
+
+// The CTAs' sums of a weight's gradient: a warp 32 columns of every 32nd CTA, the
+// warps joined in shared memory; in 64 bits, which costs nothing here.
+constexpr int kSumWarps = 32;
+
+__global__ void __launch_bounds__(32 * kSumWarps) weights_kernel(const float *part, int q_ctas, int ctas, int D,
+                                                                 float *dwq, float *dwk) {
+    __shared__ double s[kSumWarps][32];
+    paged::after_previous();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = blockIdx.x * 32 + lane;
+    const int c0 = blockIdx.y ? q_ctas : 0, c1 = blockIdx.y ? ctas : q_ctas;
+    double sum = 0.0;
+    for (int c = c0 + warp; c < c1; c += kSumWarps) sum += part[(size_t)c * D + col];
+    s[warp][lane] = sum;
+    __syncthreads();
+    if (warp) return;
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kSumWarps; ++w) sum += s[w][lane];
+    (blockIdx.y ? dwk : dwq)[col] = (float)sum;
+}
+
+// The gradient's CTAs, which leave a row of partial sums each: for q and k by their
+// heads where the GPU is full, one for every kWarps units where not.
+int bwd_grid(Args *a, int D) {
+    long long want[2], cap = (long long)sm_count() * kBwdCtas;
+    Side *sides[2] = {&a->q, &a->k};
+    for (int i = 0; i < 2; ++i) {
+        Side &s = *sides[i];
+        want[i] = 0;
+        if (s.heads == 0) continue;
+        split_heads(s.heads, a->tokens, D, kBwdUnroll, &s.chunk, &s.splits);
+        want[i] = ((long long)a->tokens * s.splits + kWarps - 1) / kWarps;
+    }
+    if (want[0] + want[1] > cap) {
+        long long nk = a->k.heads ? cap * a->k.heads / (a->q.heads + a->k.heads) : 0;
+        if (a->k.heads && nk < 1) nk = 1;
+        if (nk > want[1]) nk = want[1];
+        want[1] = nk;
+        if (want[0] > cap - nk) want[0] = cap - nk;
+    }
+    a->q_ctas = (int)want[0];
+    return (int)(want[0] + want[1]);
+}
+
+int check(const Args &a, int D, int interleaved, int weight_bits) {
+    if (!a.pos || !a.freqs || a.tokens < 1 || a.q.heads < 1 || a.k.heads < 0) return MOBA_ERR_INVALID_ARG;
+    if (!a.q.w || (a.k.heads && !a.k.w)) return MOBA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return MOBA_ERR_UNSUPPORTED;
+    if (a.rot < 16 || a.rot > D || a.rot % 16 != 0) return MOBA_ERR_INVALID_ARG;
+    if (interleaved != 0 && interleaved != 1) return MOBA_ERR_INVALID_ARG;
+    if (weight_bits != 16 && weight_bits != 32) return MOBA_ERR_INVALID_ARG;
+    if (!std::isfinite(a.mag) || !(a.eps >= 1e-12f) || !std::isfinite(a.eps)) return MOBA_ERR_INVALID_ARG;
+    if (a.q.heads > 65535 || a.k.heads > 65535) return MOBA_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(a.pos) & 3 || reinterpret_cast<uintptr_t>(a.freqs) & 7)
+        return MOBA_ERR_INVALID_ARG;
+    const uintptr_t w = reinterpret_cast<uintptr_t>(a.q.w) | (a.k.heads ? reinterpret_cast<uintptr_t>(a.k.w) : 0);
+    if (w & (weight_bits / 8 - 1)) return MOBA_ERR_INVALID_ARG;
+    return MOBA_OK;
+}
+
+struct Area {
+    const void *p;
+    long long stride, width;  // bytes
+};
+Area area(const void *p, long long stride, int heads, int D) { return {p, 2 * stride, 2ll * heads * D}; }
+
+// an output against what else the call reads and writes; it may be `same`, in place
+bool collides(const Area &out, const Area &in, bool same, long long tokens) {
+    if (!in.p || !out.p) return false;
+    if (same && out.p == in.p && out.stride == in.stride) return false;
+    return overlaps(out.p, out.stride, out.width, in.p, in.stride, in.width, tokens);
+}
+
+template <int D>
+cudaError_t launch_fwd(const Args &a, bool interleaved, cudaStream_t st) {
+    const long long units = (long long)a.tokens * a.splits;
+    const long long want = (units + kWarps - 1) / kWarps, cap = (long long)sm_count() * kFwdCtas;
+    const int grid = (int)(want < cap ? want : cap);
+    if (interleaved) fwd_kernel<D, true><<<grid, 32 * kWarps, 0, st>>>(a);
+    else fwd_kernel<D, false><<<grid, 32 * kWarps, 0, st>>>(a);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_bwd(const Args &a, int grid, bool interleaved, float *dwq, float *dwk, cudaStream_t st) {
+    if (interleaved) bwd_kernel<D, true><<<grid, 32 * kWarps, 0, st>>>(a);
+    else bwd_kernel<D, false><<<grid, 32 * kWarps, 0, st>>>(a);
+    note_launches(2);
+    const cudaError_t rc = cudaGetLastError();
+    if (rc != cudaSuccess) return rc;
+    return paged::launch_after(weights_kernel, dim3(D / 32, dwk ? 2 : 1), dim3(32 * kSumWarps), 0, st,
+                               (const float *)a.part, a.q_ctas, grid, D, dwq, dwk);
+}
+
+}  // namespace qk_norm
+}  // namespace moba
+
+using namespace moba;
+using namespace moba::qk_norm;
+
+MOBA_EXPORT int moba_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const void *q_weight,
+                                  const void *k_weight, int weight_bits, float eps, const int32_t *positions,
+                                  const double *freqs, int tokens, int Hq, int Hk, int D, int rot_dim,
+                                  int interleaved, float magnitude, long long q_stride, long long k_stride,
+                                  long long q_out_stride, long long k_out_stride, void *stream) {
+    Args a = {};
+    a.q = {static_cast<const __nv_bfloat16 *>(q), nullptr, static_cast<__nv_bfloat16 *>(q_out), q_weight, q_stride, 0,
+           q_out_stride, Hq};
+    a.k = {static_cast<const __nv_bfloat16 *>(k), nullptr, static_cast<__nv_bfloat16 *>(k_out), k_weight, k_stride, 0,
+           k_out_stride, Hk};
+    a.pos = positions;
+    a.freqs = freqs;
+    a.tokens = tokens;
+    a.rot = rot_dim;
+    a.w32 = weight_bits == 32;
+    a.eps = eps;
+    a.mag = magnitude;
+    int rc = check(a, D, interleaved, weight_bits);
+    for (Side *s : {&a.q, &a.k}) {
+        if (s == &a.k && Hk == 0) break;
+        if (rc == MOBA_OK) rc = check_rows(s->x, s->heads, D, tokens, &s->xs);
+        if (rc == MOBA_OK) rc = check_rows(s->out, s->heads, D, tokens, &s->os);
+    }
+    if (rc != MOBA_OK) return rc;
+    const Area qi = area(q, a.q.xs, Hq, D), qo = area(q_out, a.q.os, Hq, D);
+    const Area ki = Hk ? area(k, a.k.xs, Hk, D) : Area{}, ko = Hk ? area(k_out, a.k.os, Hk, D) : Area{};
+    if (collides(qo, qi, true, tokens) || collides(qo, ki, false, tokens) || collides(ko, qi, false, tokens) ||
+        collides(ko, ki, true, tokens) || collides(ko, qo, false, tokens))
+        return MOBA_ERR_INVALID_ARG;
+    split_heads(Hq + Hk, tokens, D, kUnroll, &a.chunk, &a.splits);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_result(D == 64 ? launch_fwd<64>(a, interleaved != 0, st) : launch_fwd<128>(a, interleaved != 0, st));
+}
+
+MOBA_EXPORT size_t moba_qk_norm_rope_bwd_workspace_size(int tokens, int Hq, int Hk, int D) {
+    if (tokens < 1 || Hq < 1 || Hk < 0 || (D != 64 && D != 128) || Hq > 65535 || Hk > 65535) return 0;
+    Args a = {};
+    a.tokens = tokens;
+    a.q.heads = Hq;
+    a.k.heads = Hk;
+    return sizeof(float) * D * (size_t)bwd_grid(&a, D);
+}
+
+MOBA_EXPORT int moba_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                                      const void *q_weight, const void *k_weight, void *dq, void *dk,
+                                      float *dq_weight, float *dk_weight, int weight_bits, float eps,
+                                      const int32_t *positions, const double *freqs, int tokens, int Hq, int Hk,
+                                      int D, int rot_dim, int interleaved, float magnitude, long long dq_out_stride,
+                                      long long dk_out_stride, long long q_stride, long long k_stride,
+                                      long long dq_stride, long long dk_stride, void *workspace,
+                                      size_t workspace_bytes, void *stream) {
+    Args a = {};
+    a.q = {static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(dq_out),
+           static_cast<__nv_bfloat16 *>(dq), q_weight, q_stride, dq_out_stride, dq_stride, Hq};
+    a.k = {static_cast<const __nv_bfloat16 *>(k), static_cast<const __nv_bfloat16 *>(dk_out),
+           static_cast<__nv_bfloat16 *>(dk), k_weight, k_stride, dk_out_stride, dk_stride, Hk};
+    a.pos = positions;
+    a.freqs = freqs;
+    a.tokens = tokens;
+    a.rot = rot_dim;
+    a.w32 = weight_bits == 32;
+    a.eps = eps;
+    a.mag = magnitude;
+    int rc = check(a, D, interleaved, weight_bits);
+    for (Side *s : {&a.q, &a.k}) {
+        if (s == &a.k && Hk == 0) break;
+        if (rc == MOBA_OK) rc = check_rows(s->x, s->heads, D, tokens, &s->xs);
+        if (rc == MOBA_OK) rc = check_rows(s->dy, s->heads, D, tokens, &s->ds);
+        if (rc == MOBA_OK) rc = check_rows(s->out, s->heads, D, tokens, &s->os);
+    }
+    if (rc != MOBA_OK) return rc;
+    if (!dq_weight || (Hk && !dk_weight) ||
+        ((reinterpret_cast<uintptr_t>(dq_weight) | (Hk ? reinterpret_cast<uintptr_t>(dk_weight) : 0)) & 3))
+        return MOBA_ERR_INVALID_ARG;
+    const Area qx = area(q, a.q.xs, Hq, D), qy = area(dq_out, a.q.ds, Hq, D), qo = area(dq, a.q.os, Hq, D);
+    const Area kx = Hk ? area(k, a.k.xs, Hk, D) : Area{}, ky = Hk ? area(dk_out, a.k.ds, Hk, D) : Area{};
+    const Area ko = Hk ? area(dk, a.k.os, Hk, D) : Area{};
+    for (const Area &in : {qx, kx, qy, ky})
+        if (collides(qo, in, in.p == dq_out && in.width == qo.width, tokens) ||
+            collides(ko, in, in.p == dk_out && in.width == ko.width, tokens))
+            return MOBA_ERR_INVALID_ARG;
+    if (collides(ko, qo, false, tokens)) return MOBA_ERR_INVALID_ARG;
+    const int grid = bwd_grid(&a, D);
+    const size_t need = sizeof(float) * D * (size_t)grid;
+    if (workspace && (workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+        return MOBA_ERR_WORKSPACE;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void *own = nullptr;
+    if (!workspace) {
+        const cudaError_t e = cudaMallocAsync(&own, need, st);
+        if (e != cudaSuccess) return cuda_result(e);
+        workspace = own;
+    }
+    a.part = static_cast<float *>(workspace);
+    cudaError_t e = D == 64 ? launch_bwd<64>(a, grid, interleaved != 0, dq_weight, Hk ? dk_weight : nullptr, st)
+                            : launch_bwd<128>(a, grid, interleaved != 0, dq_weight, Hk ? dk_weight : nullptr, st);
+    if (own) {
+        const cudaError_t f = cudaFreeAsync(own, st);
+        if (e == cudaSuccess) e = f;
+    }
+    return cuda_result(e);
+}

@@ -22,7 +22,7 @@
 #include <cmath>
 
 #include "moba.h"
-#include "moba_internal.cuh"
+#include "moba_rope.cuh"
 
 namespace moba {
 namespace rope {
@@ -47,40 +47,19 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(Args a) {
     constexpr int HW = 32 / LH;  // heads per warp and step
     __shared__ unsigned long long s_turn[D / 2];
     const int half = a.rot / 2;
-    for (int i = threadIdx.x; i < half; i += 32 * kWarps) {
-        const double t = __ldg(a.freqs + i) * 0.15915494309189533577;  // turns per position
-        s_turn[i] = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
-    }
+    load_turns(s_turn, a.freqs, half, threadIdx.x, 32 * kWarps);
     __syncthreads();
     const int lane = threadIdx.x & 31, item = lane % LH, hsub = lane / LH;
     const bool turns = item < a.rot / 16;  // the other items copy the unrotated rest
-    // where the item's two 16-byte vectors start inside the head
-    int va, vb;
-    if (!turns || INTERLEAVED) {
-        va = item * 16;
-        vb = va + 8;
-    } else {
-        va = item * 8;
-        vb = va + half;
-    }
+    int va, vb;  // where the item's two 16-byte vectors start inside the head
+    vectors<D, INTERLEAVED>(item, half, va, vb);
     const long long units = (long long)a.tokens * a.splits;
     for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units;
          u += (long long)gridDim.x * kWarps) {
         const int t = (int)(u / a.splits);
         const int h0 = (int)(u % a.splits) * a.chunk, h1 = min(h0 + a.chunk, a.Hq + a.Hk);
         float c[8], s[8];
-        if (turns) {
-            const long long p = __ldg(a.pos + t);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const unsigned long long phase = s_turn[item * 8 + i] * (unsigned long long)p;
-                // the upper 32 bits as a signed fraction of half a turn
-                const float x = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;
-                sincospif(x, &s[i], &c[i]);
-                s[i] *= a.mag * a.sin_sign;
-                c[i] *= a.mag;
-            }
-        }
+        if (turns) cos_sin(s_turn + item * 8, __ldg(a.pos + t), a.mag, a.sin_sign, c, s);
         for (int hb = h0; hb < h1; hb += HW * kUnroll) {
             uint4 xa[kUnroll], xb[kUnroll];
 #pragma unroll
@@ -135,20 +114,6 @@ static cudaError_t launch(const Args &a, bool interleaved, cudaStream_t st) {
     else rope_kernel<D, false><<<grid, 32 * kWarps, 0, st>>>(a);
     note_launches(1);
     return cudaGetLastError();
-}
-
-// Whether two areas of `rows` rows overlap in memory: wx bytes every sx bytes
-// from x, wy bytes every sy from y.
-static bool overlaps(const void *x, long long sx, long long wx, const void *y, long long sy,
-                     long long wy, long long rows) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-    const uintptr_t a1 = a + (uintptr_t)((rows - 1) * sx + wx);
-    const uintptr_t b1 = b + (uintptr_t)((rows - 1) * sy + wy);
-    if (a1 <= b || b1 <= a) return false;
-    if (sx != sy) return true;
-    // equal strides: rows may lie between one another (slices of one projection)
-    const uintptr_t s = (uintptr_t)sx, d = b >= a ? (b - a) % s : (s - (a - b) % s) % s;
-    return d < (uintptr_t)wx || s - d < (uintptr_t)wy;
 }
 
 static int run(const void *q, const void *k, void *qo, void *ko, const int32_t *pos,

@@ -74,6 +74,14 @@ _SIGNATURES = {
     "moba_rope_bwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _LL, _LL, _LL, _LL,
                            _P]),
     "moba_rope_frequencies": (_I, [_P, _I, _DB, _I, _DB, _DB, _DB, _DB]),
+    "moba_qk_norm_rope": (_I, [_P, _P, _P, _P, _P, _P, _I, _F, _P, _P, _I, _I, _I, _I, _I, _I, _F, _LL,
+                               _LL, _LL, _LL, _P]),
+    "moba_qk_norm_rope_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _F, _P, _P, _I, _I, _I,
+                                   _I, _I, _I, _F, _LL, _LL, _LL, _LL, _LL, _LL, _P, _SZ, _P]),
+    "moba_qk_norm_rope_bwd_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "moba_paged_append_rope": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _F, _I,
+                                    _I, _I, _I, _I, _I, _I, _I, _F, _LL, _LL, _LL, _LL, _I, _I, _I, _I,
+                                    _P, _P]),
     "moba_paged_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                _P, _P]),
     "moba_paged_attn": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
@@ -670,6 +678,132 @@ def rope_bwd(dq_out, dk_out, positions, freqs, interleaved: bool = False, magnit
                  interleaved, magnitude, dq, dk, stream)
 
 
+def _weights(device, D, q_weight, k_weight):
+    """Checks norm weights ([D], both bf16 or both fp32, or None); their bits."""
+    bits = 0
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            continue
+        mine = {torch.bfloat16: 16, torch.float32: 32}.get(w.dtype, 0)
+        if not mine or (bits and mine != bits):
+            raise ValueError("norm weights must be both torch.bfloat16 or both torch.float32")
+        bits = mine
+        _tensor(w, w.dtype, device, name)
+        if w.shape != (D,):
+            raise ValueError(f"{name} must have shape ({D},)")
+    return bits
+
+
+def _norm_operands(q, k, q_weight, k_weight, positions, freqs):
+    """Checks what the norms' calls share: device, tokens, heads, D and strides of q and
+    k, and the weights' bits."""
+    device = _device(q, "q")
+    T, Hq, D, qs = _heads(q, device, "q")
+    Hk = ks = 0
+    if k is not None:
+        Tk, Hk, Dk, ks = _heads(k, device, "k")
+        if Tk != T or Dk != D:
+            raise ValueError("k must have the tokens and the head dimension of q")
+    if q_weight is None or (k is None) != (k_weight is None):
+        raise ValueError("q needs q_weight, and k k_weight")
+    _tensor(positions, torch.int32, device, "positions")
+    _tensor(freqs, torch.float64, device, "freqs")
+    if positions.numel() != T:
+        raise ValueError(f"positions must hold one position for each of the {T} tokens")
+    return device, T, Hq, Hk, D, qs, ks, _weights(device, D, q_weight, k_weight)
+
+
+def _rows_like(out, x, device, name):
+    """A result [..., H, D] beside x, or the caller's one, and its token stride."""
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device), 0
+    if out.shape != x.shape:
+        raise ValueError(f"{name} must have shape {tuple(x.shape)}")
+    return out, _heads(out, device, name)[3]
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, eps: float = 1e-6,
+                 interleaved: bool = False, magnitude: float = 1.0, q_out=None, k_out=None,
+                 stream=None):
+    """Norms of queries and keys with :func:`rope` in the same pass: each head of q [...,
+    Hq, D] and k [..., Hk, D] bf16 (k and k_weight may be None) over its root mean square,
+    times the weights [D] (bf16 or fp32), rotated -> (q_out, k_out).  Operands, positions
+    and freqs are those of :func:`rope`; q_out / k_out may be q / k (in place)."""
+    device, T, Hq, Hk, D, qs, ks, bits = _norm_operands(q, k, q_weight, k_weight, positions, freqs)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+
+    def run(st):
+        qo, qos = _rows_like(q_out, q, device, "q_out")
+        ko, kos = _rows_like(k_out, k, device, "k_out") if k is not None else (None, 0)
+        if T == 0:
+            return qo, ko
+        rc = lib().moba_qk_norm_rope(
+            q.data_ptr(), k.data_ptr() if Hk else None, qo.data_ptr(), ko.data_ptr() if Hk else None,
+            q_weight.data_ptr(), k_weight.data_ptr() if Hk else None, bits, eps, positions.data_ptr(),
+            freqs.data_ptr(), T, Hq, Hk, D, 2 * freqs.numel(), 1 if interleaved else 0, magnitude,
+            qs, ks, qos, kos, st)
+        if rc:
+            _check(rc, "moba_qk_norm_rope")
+        return qo, ko
+
+    return _call(device, stream, run)
+
+
+def qk_norm_rope_bwd_workspace_size(tokens: int, Hq: int, Hk: int, D: int) -> int:
+    """Bytes of scratch :func:`qk_norm_rope_bwd` needs on the current device (0: sizes it refuses)."""
+    return int(lib().moba_qk_norm_rope_bwd_workspace_size(tokens, Hq, Hk, D))
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, freqs, eps: float = 1e-6,
+                     interleaved: bool = False, magnitude: float = 1.0, dq=None, dk=None,
+                     dq_weight=None, dk_weight=None, workspace=None, stream=None):
+    """The gradient of :func:`qk_norm_rope`: gradients of its outputs and its inputs ->
+    (dq, dk, dq_weight, dk_weight), the weights' in fp32 [D], summed over all tokens and
+    heads.  dq / dk may be dq_out / dk_out (in place).  ``workspace`` is a uint8 CUDA tensor
+    of at least :func:`qk_norm_rope_bwd_workspace_size` bytes, or None (scratch from torch's
+    allocator, on the call's stream).  No tokens: weight gradients of zero."""
+    device, T, Hq, Hk, D, qs, ks, bits = _norm_operands(q, k, q_weight, k_weight, positions, freqs)
+    if dq_out.shape != q.shape or (k is None) != (dk_out is None) or \
+            (k is not None and dk_out.shape != k.shape):
+        raise ValueError("dq_out and dk_out must have the shapes of q and k")
+    if k is None and (dk is not None or dk_weight is not None):
+        raise ValueError("dk and dk_weight without k")
+    ys = _heads(dq_out, device, "dq_out")[3]
+    zs = _heads(dk_out, device, "dk_out")[3] if Hk else 0
+    if workspace is not None:
+        _tensor(workspace, torch.uint8, device, "workspace")
+
+    def run(st):
+        qo, qos = _rows_like(dq, q, device, "dq")
+        ko, kos = _rows_like(dk, k, device, "dk") if k is not None else (None, 0)
+        wq = _result(dq_weight, (D,), torch.float32, q, device, "dq_weight")
+        wk = _result(dk_weight, (D,), torch.float32, q, device, "dk_weight") if k is not None else None
+        if wk is not None and Hk == 0:
+            wk.zero_()
+        if T == 0:
+            for w in (wq, wk):
+                if w is not None:
+                    w.zero_()
+            return qo, ko, wq, wk
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(lib().moba_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D),
+                             dtype=torch.uint8, device=q.device)
+        rc = lib().moba_qk_norm_rope_bwd(
+            dq_out.data_ptr(), dk_out.data_ptr() if Hk else None, q.data_ptr(),
+            k.data_ptr() if Hk else None, q_weight.data_ptr(), k_weight.data_ptr() if Hk else None,
+            qo.data_ptr(), ko.data_ptr() if Hk else None, wq.data_ptr(),
+            wk.data_ptr() if Hk else None, bits, eps, positions.data_ptr(), freqs.data_ptr(), T, Hq,
+            Hk, D, 2 * freqs.numel(), 1 if interleaved else 0, magnitude, ys, zs, qs, ks, qos, kos,
+            ws.data_ptr(), ws.numel(), st)
+        if rc:
+            _check(rc, "moba_qk_norm_rope_bwd")
+        return qo, ko, wq, wk
+
+    return _call(device, stream, run)
+
+
 def _paged(device, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens):
     """Checks one layer's pools and the sequences' tables; the sizes a call passes on."""
     bf16, i32 = torch.bfloat16, torch.int32
@@ -719,6 +853,51 @@ def paged_append(k, v, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_l
         D, P, ps, mp, block_size, opt, st))
     if rc:
         _check(rc, "moba_paged_append")
+
+
+def paged_append_rope(q, k, v, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens,
+                      max_new: int, block_size: int, freqs, positions=None, q_weight=None,
+                      k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                      magnitude: float = 1.0, pooling=POOL_MEAN, q_out=None, stream=None):
+    """:func:`paged_append` with :func:`qk_norm_rope` on the way: q [total, Hq, D] and k
+    [total, Hkv, D] bf16 normalised (where their weight is given), rotated to ``positions``
+    (int32 [total]; None: each token's place in its sequence), k and v written to their
+    pages -> q_out (q itself for in place).  The tokens of q, k and v may be a stride apart
+    (slices of one projection).  Rows of q_out behind the last sequence, and of refused
+    ones, are left as they were."""
+    device = _device(k_pages, "k_pages")
+    P, Hkv, ps, D, n, mp, bar = _paged(device, k_pages, v_pages, kbar_pages, page_table, cu_new,
+                                       cache_lens)
+    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != D or k.shape != (q.shape[0], Hkv, D) or \
+            v.shape != k.shape:
+        raise ValueError("q must be [total, Hq, D], k and v [total, Hkv, D] of the pages")
+    total, Hq = q.shape[0], q.shape[1]
+    qs, ks, vs = (_heads(x, device, name)[3] for x, name in ((q, "q"), (k, "k"), (v, "v")))
+    _tensor(freqs, torch.float64, device, "freqs")
+    if positions is not None:
+        _tensor(positions, torch.int32, device, "positions")
+        if positions.numel() != total:
+            raise ValueError(f"positions must hold one position for each of the {total} tokens")
+    bits = _weights(device, D, q_weight, k_weight)
+    opt = ctypes.byref(_options(pooling=pooling)[0]) if pooling != POOL_MEAN else None
+
+    def run(st):
+        qo, qos = _rows_like(q_out, q, device, "q_out")
+        if total == 0:
+            return qo
+        rc = lib().moba_paged_append_rope(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), qo.data_ptr(), k_pages.data_ptr(),
+            v_pages.data_ptr(), bar, page_table.data_ptr(), cu_new.data_ptr(), cache_lens.data_ptr(),
+            positions.data_ptr() if positions is not None else None, freqs.data_ptr(),
+            q_weight.data_ptr() if q_weight is not None else None,
+            k_weight.data_ptr() if k_weight is not None else None, bits, eps, n, total, max_new, Hq,
+            Hkv, D, 2 * freqs.numel(), 1 if interleaved else 0, magnitude, qs, ks, vs, qos, P, ps, mp,
+            block_size, opt, st)
+        if rc:
+            _check(rc, "moba_paged_append_rope")
+        return qo
+
+    return _call(device, stream, run)
 
 
 def paged_attn_workspace_size(num_seqs, total, max_new, Hq, Hkv, D, page_size, max_pages,
