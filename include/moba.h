@@ -619,6 +619,36 @@ size_t moba_paged_attn_workspace_size(int num_seqs, int total, int max_new, int 
                                       int topk);
 
 /*
+ * Attention of the new tokens over every key up to each of them, as moba_paged_attn's
+ * with a topk that covers every block, for sequences that share long prefixes: a prefix is
+ * read and multiplied once for all the rows of its group.
+ *   cu_groups   : [n_groups + 1] int32 (device): group g is the sequences [cu_groups[g],
+ *                 cu_groups[g + 1]), in the order of the page table; sequences of no group
+ *                 (before the first, behind the last) share nothing
+ *   prefix_lens : [n_groups] int32 (device): the first tokens that a group's sequences have
+ *                 in common, whole pages of them (0: none), all before their new tokens
+ * The page table's rows of a group name the same pages for the prefix; those of its first
+ * sequence with new tokens are read.  Groups whose offsets decrease or leave [0, num_seqs]
+ * (no group counts then), a prefix that is negative, no multiple of page_size, wider than
+ * the table or longer than what a member has before its new tokens, and a refused member
+ * (the group counts for nothing then) record MOBA_ERR_INVALID_ARG in the device status
+ * word; the sequences are attended by their own pages all the same.
+ *   n_groups 0 (cu_groups and prefix_lens may be NULL): no sequence shares
+ * q, out, lse, the cache, refused sequences, pages outside the pool, values that are not
+ * finite (rows of a group are computed together) and workspace: as for moba_paged_attn, the
+ * workspace with moba_paged_attn_shared_workspace_size.  total * (Hq / Hkv) is below 2^26.
+ */
+int moba_paged_attn_shared(const void *q, const void *k_pages, const void *v_pages,
+                           const int32_t *page_table, const int32_t *cu_new,
+                           const int32_t *cache_lens, const int32_t *cu_groups,
+                           const int32_t *prefix_lens, void *out, float *lse, int num_seqs,
+                           int n_groups, int total, int max_new, int Hq, int Hkv, int D,
+                           int num_pages, int page_size, int max_pages, void *workspace,
+                           size_t workspace_bytes, void *stream);
+size_t moba_paged_attn_shared_workspace_size(int num_seqs, int n_groups, int total, int max_new,
+                                             int Hq, int Hkv, int D, int page_size, int max_pages);
+
+/*
  * Copies whole pages, page src[i] to page dst[i] (DEVICE int32 [n]), in every
  * one of `layers` layers (pools [layers][num_pages]...): the last, partly
  * filled page of a forked sequence, or a pool's live pages when it is

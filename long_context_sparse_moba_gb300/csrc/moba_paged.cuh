@@ -42,6 +42,21 @@ struct Cache {
         return kSeqBad;
     }
 
+    // The sequence that may hold packed row t: the last one that starts at or before it, 32
+    // places a look.  All lanes of a warp call it, with the same t.
+    __device__ __forceinline__ int seq_of_row(int t, int lane) const {
+        int lo = 0, n = num_seqs;  // the answer is in [lo, lo + n)
+        while (n > 1) {
+            const int step = (n + 31) / 32;
+            const bool below = lane * step < n && __ldg(cu + lo + lane * step) <= t;
+            const unsigned some = __ballot_sync(0xffffffffu, below);
+            const int last = some ? 31 - __clz(some) : 0;
+            n = min(step, n - last * step);
+            lo += last * step;
+        }
+        return lo;
+    }
+
     // Tiles of `rows` rows (head rows of a group of G, numbered token * G + head)
     // without a table: sequence b's begin at slot cu[b] * G / rows + spare * b,
     // which leaves room for `spare` tiles of every sequence that are not full.

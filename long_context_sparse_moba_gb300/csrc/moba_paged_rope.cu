@@ -46,21 +46,6 @@ struct WriteArgs {
     int *status;
 };
 
-// The sequence with packed row t: the last one that starts at or before it, 32 places a
-// look.  All lanes call it, with the same t.
-__device__ __forceinline__ int seq_of_row(const Cache &c, int t, int lane) {
-    int lo = 0, n = c.num_seqs;  // the answer is in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 31) / 32, at = lo + lane * step;
-        const bool below = lane * step < n && __ldg(c.cu + at) <= t;
-        const unsigned some = __ballot_sync(0xffffffffu, below);
-        const int last = some ? 31 - __clz(some) : 0;
-        n = min(step, n - last * step);
-        lo += last * step;
-    }
-    return lo;
-}
-
 template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kWarps) write_kernel(WriteArgs a) {
     constexpr int LH = D / 16;   // lanes per head: 16 values (8 pairs) each
@@ -89,7 +74,7 @@ __global__ void __launch_bounds__(32 * kWarps) write_kernel(WriteArgs a) {
          u += (long long)gridDim.x * kWarps) {
         const int t = (int)(u / a.splits);
         const int h0 = (int)(u % a.splits) * a.chunk, h1 = min(h0 + a.chunk, heads);
-        const int b = seq_of_row(a.c, t, lane);
+        const int b = a.c.seq_of_row(t, lane);
         Seq s;
         // (rows of no sequence, or of a refused one, are left as they were)
         if (a.c.seq(b, s) != kSeqOk || t < s.row0 || t >= s.row0 + s.n) continue;

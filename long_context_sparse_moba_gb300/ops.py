@@ -87,6 +87,9 @@ _SIGNATURES = {
     "moba_paged_attn": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                              _I, _I, _I, _P, _SZ, _P]),
     "moba_paged_attn_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I]),
+    "moba_paged_attn_shared": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                                    _I, _I, _I, _P, _SZ, _P]),
+    "moba_paged_attn_shared_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
     "moba_page_copy": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "moba_attn_bwd_varlen_ex": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I,
                                      _I, _I, _I, _P, _P, _SZ, _P]),
@@ -949,6 +952,59 @@ def paged_attn(q, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens, 
         if rc:
             _check(rc, "moba_paged_attn")
         return o, z, sel
+
+    return _call(device, stream, run)
+
+
+def paged_attn_shared_workspace_size(num_seqs, n_groups, total, max_new, Hq, Hkv, D, page_size,
+                                     max_pages) -> int:
+    """Bytes of scratch :func:`paged_attn_shared` needs on the current device (0: sizes it refuses)."""
+    return int(lib().moba_paged_attn_shared_workspace_size(num_seqs, n_groups, total, max_new, Hq, Hkv,
+                                                           D, page_size, max_pages))
+
+
+def paged_attn_shared(q, k_pages, v_pages, page_table, cu_new, cache_lens, max_new: int, cu_groups,
+                      prefix_lens, out=None, lse=None, workspace=None, stream=None):
+    """:func:`paged_attn` over all blocks for sequences that share prefixes -> (out [total,
+    Hq, D] bf16, lse [total, Hq] fp32).  Sequences ``cu_groups[g]`` to ``cu_groups[g + 1]`` -
+    1 (int32 [groups + 1]) have their first ``prefix_lens[g]`` tokens (int32 [groups], whole
+    pages, before the new tokens) on the same pages, which are read once for all of them;
+    sequences of no group share nothing.  ``workspace`` is a uint8 CUDA tensor of at least
+    :func:`paged_attn_shared_workspace_size` bytes, or None (scratch from torch's allocator,
+    on the call's stream)."""
+    device = _device(k_pages, "k_pages")
+    P, Hkv, ps, D, n, mp, _ = _paged(device, k_pages, v_pages, None, page_table, cu_new, cache_lens)
+    _tensor(q, torch.bfloat16, device, "q")
+    _tensor(cu_groups, torch.int32, device, "cu_groups")
+    _tensor(prefix_lens, torch.int32, device, "prefix_lens")
+    groups = prefix_lens.numel()
+    if cu_groups.numel() != groups + 1:
+        raise ValueError("cu_groups must be [groups + 1] and prefix_lens [groups]")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D:
+        raise ValueError("q must be [total, Hq, D] with the pages' head dimension")
+    total, Hq = shape[0], shape[1]
+    if workspace is not None:
+        _tensor(workspace, torch.uint8, device, "workspace")
+
+    def run(st):
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(lib().moba_paged_attn_shared_workspace_size(n, groups, total, max_new, Hq,
+                                                                         Hkv, D, ps, mp),
+                             dtype=torch.uint8, device=q.device)
+        o = _result(out, shape, torch.bfloat16, q, device, "out")
+        z = _result(lse, (total, Hq), torch.float32, q, device, "lse")
+        if total == 0:
+            return o, z
+        rc = lib().moba_paged_attn_shared(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+            cu_new.data_ptr(), cache_lens.data_ptr(), cu_groups.data_ptr(), prefix_lens.data_ptr(),
+            o.data_ptr(), z.data_ptr(), n, groups, total, max_new, Hq, Hkv, D, P, ps, mp,
+            ws.data_ptr(), ws.numel(), st)
+        if rc:
+            _check(rc, "moba_paged_attn_shared")
+        return o, z
 
     return _call(device, stream, run)
 
