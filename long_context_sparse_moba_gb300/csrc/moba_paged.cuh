@@ -27,9 +27,11 @@ struct Cache {
     // any, are [s.row0, s.row0 + s.n) after clamping into [0, total), which may be
     // more than max_new, and nothing else of it may be used.
     __device__ __forceinline__ int seq(int b, Seq &s) const {
-        const int lo = __ldg(cu + b), hi = __ldg(cu + b + 1);
+        return check(__ldg(cu + b), __ldg(cu + b + 1), __ldg(lens + b), s);
+    }
+    __device__ __forceinline__ int check(int lo, int hi, int len, Seq &s) const {
         s.row0 = lo;
-        s.len = __ldg(lens + b);
+        s.len = len;
         const bool rows_ok = lo >= 0 && hi >= lo && hi <= total && hi - lo <= max_new;
         if (rows_ok) {
             s.n = hi - lo;

@@ -16,6 +16,15 @@ constexpr int kJobRows = 256;    // query rows of a job of the tcgen05 kernel
 constexpr int kSelBad = -2;
 constexpr int kMaxBlocks = 65536;  // blocks of a sequence where blocks are selected
 
+// A tile of rows (numbered token * G + head) with the keys [key0, key_end) of sequence b's
+// pages, those of a prefix whole, else each row's up to its position, its token + pdelta.
+struct Span {
+    int row0, nrows;
+    int b, full;
+    int key0, key_end;
+    int pdelta, pad;
+};
+
 struct Attn {
     Cache c;
     const __nv_bfloat16 *q, *k, *v;
@@ -33,12 +42,6 @@ struct Attn {
     int ucap;       // union blocks of an entry at most
     float scale_log2;
     int *status;
-    // sequences that share prefixes (all blocks): groups of consecutive sequences
-    bool shared;
-    const int *cu_groups;       // [n_groups + 1]
-    const int *prefix_lens;     // [n_groups] tokens that a group's sequences share
-    int n_groups;
-    int pre_cap;                // tiles of the groups on one kv head, at most
     // scratch (a kernel may start while the one that writes it still runs, so it is read
     // with plain loads behind after_previous(), never as constant data: no __ldg)
     int *tiles;                 // [n_ent] key tiles of an entry (selection only)
@@ -48,17 +51,10 @@ struct Attn {
     int *c_last;                // [n_ent] the CTA in whose run the entry ends
     float *part_o;              // [ctas][2][rows][D] partial sums of exp2(s - m) v
     float2 *part_ml;            // [ctas][2][rows] their m and sum of exp2(s - m); a sum below 0: bad page
-    // ---- shared prefixes.  A task is a 256-row tile of a group's rows with the prefix on
-    // one kv head, or (chunks of many rows) such a tile of a sequence with what is behind
-    // it: e = tile * Hkv + kv head.  Every part of one leaves partial sums in slot e + CTA,
-    // of its own since the next part has another task or another CTA.
-    int *first;                 // [num_seqs] tokens of the sequence that its group shares (0: none)
-    int *pre_row;               // [num_seqs] its first row, numbered by the tiles of the groups' rows
-    int *rep;                   // [n_groups] the sequence whose pages are read (num_seqs: no prefix is shared)
-    int *pre_off;               // [n_groups + 1] tiles before each group
-    int *c_first;               // [n_ent] the CTA in whose run the entry starts
-    float *own_o;               // [n_ent + ctas][rows][D] partial sums of entries, as part_o
-    float2 *own_ml;             // [n_ent + ctas][rows]
+    // ---- shared prefixes: jobs that are tiles of rows with a range of keys ----
+    Span *tiles_big;            // [...] 256 rows at most, for the tcgen05 kernel
+    long long *off_big;         // [... + 1] key tiles before each, times the kv heads
+    int *n_spans;               // [2] how many of them, and of the streamed ones
     // ---- chunks of many rows (the tcgen05 kernel): jobs of up to 256 rows ----
     bool chunk;
     int n_max;                  // blocks of a sequence at most
@@ -129,12 +125,11 @@ __device__ __forceinline__ int seq_of_tile(const Attn &a, int w) {
     return lo;
 }
 
-// key tiles that an entry visits (SHARED: behind its group's prefix)
-template <bool SHARED = false>
+// key tiles that an entry visits
 __device__ __forceinline__ int get_tiles(const Attn &a, int e) {
-    if (!SHARED && !a.dense) return a.tiles[e];
+    if (!a.dense) return a.tiles[e];
     const Entry x = get_entry(a, e);
-    return x.state == kSeqOk ? (x.pos0 + x.nt - 1 - (SHARED ? a.first[x.b] : 0)) / kTile + 1 : 0;
+    return x.state == kSeqOk ? (x.pos0 + x.nt - 1) / kTile + 1 : 0;
 }
 
 // Sizes of a call whose cache has been checked (a->c is filled): MOBA_OK, or why not.
@@ -147,10 +142,9 @@ cudaError_t launch_rows(const Attn &a, bool after_gate, cudaStream_t st);
 // chunks of many rows: row tiles, lists and jobs; then the attention and the merge
 cudaError_t launch_plan(const Attn &a, bool after_gate, cudaStream_t st);
 cudaError_t launch_chunk(const Attn &a, cudaStream_t st);
-// shared prefixes: the groups and their tiles; then the tiles on the tcgen05 kernel (that
-// plan before it)
-cudaError_t launch_plan_shared(const Attn &a, cudaStream_t st);
-cudaError_t launch_chunk_shared(const Attn &a, cudaStream_t st);
+// shared prefixes: the big spans on the tcgen05 kernel, whose parts leave partial sums in
+// slot span * Hkv + kv head + CTA (the next part has another span, head or CTA)
+cudaError_t launch_chunk_spans(const Attn &a, cudaStream_t st);
 // joins the partial sums of entries (row tiles of chunks) that fell into several runs
 cudaError_t launch_merge_runs(const Attn &a, cudaStream_t st);
 

@@ -101,7 +101,7 @@ enum { kCausal = 1, kFull = 2 };
 struct Job {
     Half h[kG];
     int valid;       // kNoJob: leave; kLists: no job, the kernels before have to end first
-    int own;         // consecutive rows (else lists): kCausal, or kFull (a shared prefix)
+    int own;         // consecutive rows (else lists): kCausal, or kFull (keys whole)
     int pair;        // the Q tiles have rows of two lists, and their own keys each
     int key_end;     // own: keys from here on are seen by no row
     int lo, nt;      // first key tile of this job's part, and how many
@@ -143,9 +143,8 @@ struct Smem {
     static constexpr uint32_t kRequest = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
 };
 
-// The job of the 256-row tile x of sequence b on kv head hk, all its key tiles (SHARED:
-// those behind its group's prefix).
-template <int N, bool SHARED = false>
+// The job of the 256-row tile x of sequence b on kv head hk, all its key tiles.
+template <int N>
 __device__ __forceinline__ void own_job(const Attn &a, const Seq &s, int b, int hk, int x, Job &J) {
     const int r0 = x * kJobRows, nrows = min(kJobRows, s.n * a.G - r0);
     J.valid = kAJob;
@@ -153,7 +152,7 @@ __device__ __forceinline__ void own_job(const Attn &a, const Seq &s, int b, int 
     J.pair = 0;
     J.pdelta = s.len - s.n - s.row0;
     const int pf = s.len - s.n + r0 / a.G, pl = s.len - s.n + (r0 + nrows - 1) / a.G;
-    const int key0 = SHARED ? a.first[b] : a.dense ? 0 : pf / a.c.bs * a.c.bs;
+    const int key0 = a.dense ? 0 : pf / a.c.bs * a.c.bs;
     J.key_end = pl + 1;
     J.lo = 0;
     J.nt = (pl - key0) / N + 1;
@@ -170,43 +169,26 @@ __device__ __forceinline__ void own_job(const Attn &a, const Seq &s, int b, int 
     }
 }
 
-// The job of tile w where prefixes are shared: a group's rows with its prefix, which all
-// of them see whole, or (behind those) a sequence's rows with its own keys.
+// A span as a job, all its key tiles.
 template <int N>
-__device__ __forceinline__ void shared_job(const Attn &a, int w, Job &J) {
-    const int pre = a.pre_off[a.n_groups];
-    if (w >= pre) {
-        const int b = seq_of_tile(a, w - pre);
-        Seq s;
-        a.c.seq(b, s);
-        own_job<N, true>(a, s, b, 0, w - pre - a.own_off[b], J);
-        J.whole = 0;
-        return;
-    }
-    int g = 0, hi = a.n_groups - 1;
-    while (g < hi) {
-        const int mid = (g + hi + 1) >> 1;
-        if (a.pre_off[mid] <= w) g = mid; else hi = mid - 1;
-    }
-    const int row0 = __ldg(a.c.cu + __ldg(a.cu_groups + g)), row1 = __ldg(a.c.cu + __ldg(a.cu_groups + g + 1));
-    const int r0 = (w - a.pre_off[g]) * kJobRows, nrows = min(kJobRows, (row1 - row0) * a.G - r0);
+__device__ __forceinline__ void span_job(const Span &s, Job &J) {
     J.valid = kAJob;
-    J.own = kFull;
+    J.own = s.full ? kFull : kCausal;
     J.pair = 0;
-    J.pdelta = 0;
-    J.key_end = __ldg(a.prefix_lens + g);
+    J.pdelta = s.pdelta;
+    J.key_end = s.key_end;
     J.lo = 0;
-    J.nt = (J.key_end + N - 1) / N;
+    J.nt = (s.key_end - s.key0 + N - 1) / N;
     J.whole = 0;
     J.slot = 0;
 #pragma unroll
-    for (int i = 0; i < kG; ++i) {
-        J.h[i].b = a.rep[g];
-        J.h[i].hk = 0;
-        J.h[i].rbase = row0 * a.G + r0 + i * kM;
-        J.h[i].nrows = min(max(nrows - i * kM, 0), kM);
-        J.h[i].key0 = 0;
-        J.h[i].rlo = J.h[i].rn = 0;
+    for (int g = 0; g < kG; ++g) {
+        J.h[g].b = s.b;
+        J.h[g].hk = 0;
+        J.h[g].rbase = s.row0 + g * kM;
+        J.h[g].nrows = min(max(s.nrows - g * kM, 0), kM);
+        J.h[g].key0 = s.key0;
+        J.h[g].rlo = J.h[g].rn = 0;
     }
 }
 
@@ -237,9 +219,8 @@ __device__ __forceinline__ void list_half(const Attn &a, int l, int start, Half 
     h.rn = s.n * a.G;
 }
 
-// SHARED (with DENSE): tiles of groups and of sequences; every part of a job leaves
-// partial sums.
-template <int D, int N, bool DENSE, bool SHARED>
+// SPANS (with DENSE): jobs from spans; every part of one leaves partial sums.
+template <int D, int N, bool DENSE, bool SPANS>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap tmap_k,
                  const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ ChunkArgs ca) {
@@ -318,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             Job J;
             Seq sq;
             if (DENSE) {
-                const int tiles = SHARED ? a.pre_off[a.n_groups] + (a.chunk ? a.own_off[a.c.num_seqs] : 0)
-                                         : a.own_off[a.c.num_seqs];
+                const int tiles = SPANS ? a.n_spans[0] : a.own_off[a.c.num_seqs];
+                const long long *off = SPANS ? a.off_big : a.unit_off;
                 int open = -1;
-                const long long total = a.unit_off[tiles];
+                const long long total = off[tiles];
                 const long long runs = total < (long long)gridDim.x ? total : (long long)gridDim.x;
                 if ((long long)blockIdx.x < runs) {
                     long long u = total * blockIdx.x / runs;
@@ -329,28 +310,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     int w = 0, hi = tiles - 1;  // largest row tile that starts at or before u
                     while (w < hi) {
                         const int mid = (w + hi + 1) >> 1;
-                        if (a.unit_off[mid] <= u) w = mid; else hi = mid - 1;
+                        if (off[mid] <= u) w = mid; else hi = mid - 1;
                     }
                     while (go && u < u1) {
-                        if constexpr (SHARED) {
-                            shared_job<N>(a, w, J);
+                        if constexpr (SPANS) {
+                            const Span s = a.tiles_big[w];
+                            span_job<N>(s, J);
                         } else {
                             const int b = seq_of_tile(a, w);
                             a.c.seq(b, sq);
                             own_job<N>(a, sq, b, 0, w - a.own_off[b], J);
                         }
                         const int T = J.nt;
-                        for (; go && u < u1 && u < a.unit_off[w + 1];) {
-                            const long long in = u - a.unit_off[w];
+                        for (; go && u < u1 && u < off[w + 1];) {
+                            const long long in = u - off[w];
                             const int hk = (int)(in / T);
                             J.h[0].hk = J.h[1].hk = hk;
                             J.lo = (int)(in - (long long)hk * T);
                             J.nt = (int)min((long long)(T - J.lo), u1 - u);
                             const int e = w * a.c.Hkv + hk;
-                            J.whole = !SHARED && J.nt == T;
-                            J.slot = SHARED ? e + blockIdx.x : blockIdx.x * 2 + (J.lo == 0 ? 1 : 0);
+                            J.whole = !SPANS && J.nt == T;
+                            J.slot = SPANS ? e + blockIdx.x : blockIdx.x * 2 + (J.lo == 0 ? 1 : 0);
                             own_ends<N>(a, J);
-                            if (SHARED) {
+                            if (SPANS) {
                             } else if (J.lo + J.nt == T) a.c_last[e] = blockIdx.x;
                             else if (J.lo == 0) open = e;
                             go = hand(J);
@@ -359,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ++w;
                     }
                 }
-                if (!SHARED) a.c_open[blockIdx.x] = open;
+                if (!SPANS) a.c_open[blockIdx.x] = open;
             } else {
                 // own blocks need none of the lists: equal shares of them are worked off
                 // while the kernels before make those
@@ -714,10 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // their block whole
             int lo = 0, hi = 0x7fffffff, lo_max = 0, hi_min = 0x7fffffff;
             if (J.own) {
-                hi = SHARED && J.own == kFull ? J.key_end - 1 : (entry >> 5) / a.G + J.pdelta;
+                hi = SPANS && J.own == kFull ? J.key_end - 1 : (entry >> 5) / a.G + J.pdelta;
                 if (!DENSE) lo = hi / a.c.bs * a.c.bs;
                 // over the Q tile's rows: consecutive, so the first's and the last's
-                hi_min = SHARED && J.own == kFull ? hi : J.h.rbase / a.G + J.pdelta;
+                hi_min = SPANS && J.own == kFull ? hi : J.h.rbase / a.G + J.pdelta;
                 if (!DENSE)
                     lo_max = ((J.h.rbase + J.h.nrows - 1) / a.G + J.pdelta) / a.c.bs * a.c.bs;
             }
@@ -911,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (entry >= 0)
                         a.part_s[at] = make_float4(lse2, back[0], back[1], bad ? 0.f : 1.f);
-                } else if (!SHARED && J.whole) {
+                } else if (!SPANS && J.whole) {
                     // the bf16 result, 64 columns a pass, 128 bytes of each row
                     const size_t at = q_row(J.h.hk, max(entry, 0));
                     const unsigned long long mine =
@@ -1157,120 +1139,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Attn a) {
     }
 }
 
-// Where sequences share prefixes: which groups do, their 256-row tiles, where each sequence
-// stands in them, and (chunks of many rows) the sequences' own tiles.  A group whose
-// members or prefix are inconsistent shares nothing, and is reported: its sequences
-// attend to their own pages from the first token on.
-template <int N>
-__global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(Attn a) {
-    __shared__ long long warps[1][kPlanThreads / 32];
-    let_next();
-    after_previous();
-    const int tid = threadIdx.x, ns = a.c.num_seqs, ng = a.n_groups;
-    // the group of sequence b, or -1
-    auto group_of = [&](int b) {
-        int g = 0, hi = ng - 1;
-        while (g < hi) {
-            const int mid = (g + hi + 1) >> 1;
-            if (__ldg(a.cu_groups + mid) <= b) g = mid; else hi = mid - 1;
-        }
-        return ng > 0 && __ldg(a.cu_groups + g) <= b && b < __ldg(a.cu_groups + g + 1) ? g : -1;
-    };
-    bool wrong = false;
-    for (int g = tid; ng > 0 && g <= ng; g += kPlanThreads) {
-        const int at = __ldg(a.cu_groups + g);
-        wrong |= at < 0 || at > ns || (g > 0 && __ldg(a.cu_groups + g - 1) > at);
-    }
-    const bool none = __syncthreads_or(wrong);  // offsets that lead nowhere: no group
-    for (int g = tid; g < ng; g += kPlanThreads) {
-        const int p = __ldg(a.prefix_lens + g);
-        const bool ok = !none && p >= 0 && p % a.c.ps == 0 && p <= (long long)a.c.max_pages * a.c.ps;
-        a.rep[g] = ok ? ns : -1;
-    }
-    __threadfence_block();
-    __syncthreads();
-    // every sequence's say: the first with new tokens lends its pages; one that is refused,
-    // or new in less than the prefix, voids the group
-    long long run = 0;
-    for (int b0 = 0; b0 < ns; b0 += kPlanThreads) {
-        const int b = b0 + tid;
-        Seq s;
-        const int state = b < ns ? a.c.seq(b, s) : (int)kSeqEmpty;
-        if (state != kSeqEmpty && !none) {
-            const int g = group_of(b);
-            if (g >= 0) {
-                const bool ok = state == kSeqOk && __ldg(a.prefix_lens + g) <= s.len - s.n;
-                atomicMin(a.rep + g, ok ? b : -1);
-            }
-        }
-        if (!a.chunk) continue;  // (the rows kernel clears refused rows itself)
-        if (state == kSeqBad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-        if (__syncthreads_or(state == kSeqBad))
-            for (int r = b0; r < min(b0 + kPlanThreads, ns); ++r) {
-                Seq x;
-                if (a.c.seq(r, x) == kSeqBad) clear_refused(a, x, 0, a.Hq, tid, kPlanThreads);
-            }
-        long long inc[1] = {0}, total[1];
-        if (state == kSeqOk) inc[0] = ((long long)s.n * a.G + kJobRows - 1) / kJobRows;
-        block_scan(inc, warps, total);
-        if (b < ns) a.own_off[b + 1] = (int)min(run + inc[0], (long long)a.w_cap);
-        run += total[0];
-    }
-    if (a.chunk && tid == 0) a.own_off[0] = 0;
-    __threadfence_block();
-    __syncthreads();
-    // tiles of the groups that share something
-    auto rows_of = [&](int g) {
-        return (__ldg(a.c.cu + __ldg(a.cu_groups + g + 1)) - __ldg(a.c.cu + __ldg(a.cu_groups + g))) * a.G;
-    };
-    run = 0;
-    for (int g0 = 0; g0 < ng; g0 += kPlanThreads) {
-        const int g = g0 + tid;
-        long long inc[1] = {0}, total[1];
-        if (g < ng) {
-            const int rep = __ldcg(a.rep + g);  // (where the atomics left it)
-            if (rep < 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-            if (rep >= 0 && rep < ns && __ldg(a.prefix_lens + g) > 0)
-                inc[0] = (rows_of(g) + kJobRows - 1) / kJobRows;
-        }
-        block_scan(inc, warps, total);
-        if (g < ng) a.pre_off[g + 1] = (int)min(run + inc[0], (long long)a.pre_cap);
-        run += total[0];
-    }
-    if (tid == 0) a.pre_off[0] = 0;
-    __threadfence_block();
-    __syncthreads();
-    for (int b = tid; b < ns; b += kPlanThreads) {
-        const int g = none ? -1 : group_of(b);
-        int first = 0, row = 0;
-        // (a group that got fewer tiles than its rows: from offsets that overlap)
-        if (g >= 0 && a.pre_off[g + 1] > a.pre_off[g] &&
-            a.pre_off[g + 1] - a.pre_off[g] == (rows_of(g) + kJobRows - 1) / kJobRows) {
-            first = __ldg(a.prefix_lens + g);
-            row = a.pre_off[g] * kJobRows + (__ldg(a.c.cu + b) - __ldg(a.c.cu + __ldg(a.cu_groups + g))) * a.G;
-        }
-        a.first[b] = first;
-        a.pre_row[b] = row;
-    }
-    __threadfence_block();
-    __syncthreads();
-    const int tiles = a.pre_off[ng] + (a.chunk ? a.own_off[ns] : 0);
-    run = 0;
-    for (int w0 = 0; w0 < tiles; w0 += kPlanThreads) {
-        const int w = w0 + tid;
-        long long inc[1] = {0}, total[1];
-        if (w < tiles) {
-            Job J;
-            shared_job<N>(a, w, J);
-            inc[0] = (long long)J.nt * a.c.Hkv;
-        }
-        block_scan(inc, warps, total);
-        if (w < tiles) a.unit_off[w + 1] = run + inc[0];
-        run += total[0];
-    }
-    if (tid == 0) a.unit_off[0] = 0;
-}
-
 // The rows into the lists of the blocks that they selected; a row's slots are
 // its past blocks in ascending order.  Latency: 8 us for 262144 entries (the plan 6 us).
 constexpr int kScatterThreads = 1024;
@@ -1376,7 +1244,7 @@ __global__ void __launch_bounds__(kSlotThreads, 3) merge_slots_kernel(Attn a) {
 // ----------------------------------------------------------------------------
 // host side
 // ----------------------------------------------------------------------------
-template <int D, int N, bool DENSE, bool SHARED = false>
+template <int D, int N, bool DENSE, bool SPANS = false>
 cudaError_t launch(const Attn &a, cudaStream_t st) {
     CUtensorMap mk, mv;
     const long long rows = (long long)a.c.num_pages * a.c.Hkv * a.c.ps;
@@ -1388,21 +1256,21 @@ cudaError_t launch(const Attn &a, cudaStream_t st) {
     static std::atomic<int> fits{0};
     if (fits.load(std::memory_order_relaxed) == 0) {
         cudaFuncAttributes fa;
-        const cudaError_t e = cudaFuncGetAttributes(&fa, chunk_kernel<D, N, DENSE, SHARED>);
+        const cudaError_t e = cudaFuncGetAttributes(&fa, chunk_kernel<D, N, DENSE, SPANS>);
         if (e != cudaSuccess) return e;
         fits.store(fa.maxThreadsPerBlock >= kThreads ? 1 : -1, std::memory_order_relaxed);
     }
     if (fits.load(std::memory_order_relaxed) < 0) return cudaErrorInvalidConfiguration;
-    cudaError_t rc = allow_smem<chunk_kernel<D, N, DENSE, SHARED>>(bytes);
+    cudaError_t rc = allow_smem<chunk_kernel<D, N, DENSE, SPANS>>(bytes);
     if (rc != cudaSuccess) return rc;
     ChunkArgs ca;
     ca.a = a;
     ca.psh = __builtin_ctz((unsigned)a.c.ps);
     ca.wait_limit = kDefaultWaitLimit;
-    rc = launch_after(chunk_kernel<D, N, DENSE, SHARED>, a.ctas, kThreads, bytes, st, mk, mv, ca);
+    rc = launch_after(chunk_kernel<D, N, DENSE, SPANS>, a.ctas, kThreads, bytes, st, mk, mv, ca);
     note_launches(1);
     if (rc != cudaSuccess) return rc;
-    if (SHARED) return cudaSuccess;
+    if (SPANS) return cudaSuccess;
     if (DENSE) return launch_merge_runs(a, st);
     note_launches(1);
     constexpr int ROWS = kSlotThreads / (D / 16);
@@ -1443,13 +1311,7 @@ cudaError_t launch_chunk(const Attn &a, cudaStream_t st) {
     return a.D == 64 ? launch<64, 64, false>(a, st) : launch<128, 64, false>(a, st);
 }
 
-cudaError_t launch_plan_shared(const Attn &a, cudaStream_t st) {
-    plan_shared_kernel<128><<<1, kPlanThreads, 0, st>>>(a);
-    note_launches(1);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_chunk_shared(const Attn &a, cudaStream_t st) {
+cudaError_t launch_chunk_spans(const Attn &a, cudaStream_t st) {
     return a.D == 64 ? launch<64, 128, true, true>(a, st) : launch<128, 128, true, true>(a, st);
 }
 

@@ -99,9 +99,7 @@ __device__ __noinline__ void clear_sequences(const Attn &a) {
     }
 }
 
-// SHARED: only the keys behind the prefix that an entry's group shares; every part leaves
-// partial sums.
-template <int D, int RW, int CW, bool SHARED>
+template <int D, int RW, int CW>
 __global__ void __launch_bounds__(32 * (CW + 1), 1)
     rows_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                 const __grid_constant__ RowsArgs ra) {
@@ -141,7 +139,7 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
     after_previous();
     let_next();
     for (int e = lo; e < hi; ++e) {
-        const int T = get_tiles<SHARED>(a, e);
+        const int T = get_tiles(a, e);
         sum += T;
         if (T == 0 && e % (int)gridDim.x == cta) refused |= clear_entry<D>(a, e);
     }
@@ -174,14 +172,14 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
     // at least one tile each, so that an entry's runs are those of adjacent CTAs
     const long long runs = total < (long long)gridDim.x ? total : (long long)gridDim.x;
     if (cta >= runs) {
-        if (!SHARED && tid == 0) a.c_open[cta] = -1;
+        if (tid == 0) a.c_open[cta] = -1;
         return;
     }
     const long long u0 = total * cta / runs, u1 = total * (cta + 1) / runs;
     if (u0 >= before && u0 < before + sum) {
         int e = lo;
         long long p = before;
-        for (int t; u0 >= p + (t = get_tiles<SHARED>(a, e)); ++e) p += t;
+        for (int t; u0 >= p + (t = get_tiles(a, e)); ++e) p += t;
         s_e0 = e;
         s_base = p;
     }
@@ -198,7 +196,7 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
             const int t = t0 + lane;
             int le = e, li = i + lane, T = 0;
             if (t < n)
-                while (li >= (T = get_tiles<SHARED>(a, le))) {
+                while (li >= (T = get_tiles(a, le))) {
                     li -= T;
                     ++le;
                 }
@@ -211,9 +209,7 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
             f.key0 = f.nv = 0;
             if (t < n) {
                 x = get_entry(a, le);
-                if (SHARED) {
-                    f.key0 = a.first[x.b] + li * kTile;
-                } else if (a.dense) {
+                if (a.dense) {
                     f.key0 = li * kTile;
                 } else {
                     const int u = li / a.tpb;
@@ -476,10 +472,9 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
             bad |= s_badw[w] != 0;
         }
         if (out) break;  // every warp of the attention alike
-        const bool whole = !SHARED && part.start && part.last;
-        const int slot = SHARED ? part.e + cta : cta * 2 + (part.start ? 1 : 0);
+        const bool whole = part.start && part.last;
+        const int slot = cta * 2 + (part.start ? 1 : 0);
         if (tid == 0) {
-            if (SHARED && part.start) a.c_first[part.e] = cta;
             if (part.start && !part.last) open = part.e;
             if (part.last) a.c_last[part.e] = cta;
             if (bad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
@@ -518,16 +513,15 @@ __global__ void __launch_bounds__(32 * (CW + 1), 1)
                 if (d == 0)
                     a.lse[at] = bad ? -INFINITY : (M + log2f(Lsum)) * 0.69314718055994530942f;
             } else {
-                float *dst = (SHARED ? a.own_o : a.part_o) + ((size_t)slot * a.rows + r) * D + d;
+                float *dst = a.part_o + ((size_t)slot * a.rows + r) * D + d;
                 *reinterpret_cast<float4 *>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
                 *reinterpret_cast<float4 *>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
-                if (d == 0)
-                    (SHARED ? a.own_ml : a.part_ml)[(size_t)slot * a.rows + r] = make_float2(M, bad ? -1.f : Lsum);
+                if (d == 0) a.part_ml[(size_t)slot * a.rows + r] = make_float2(M, bad ? -1.f : Lsum);
             }
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * CW) : "memory");  // before the next part's sums
     }
-    if (!SHARED && tid == 0) a.c_open[cta] = open;
+    if (tid == 0) a.c_open[cta] = open;
 }
 
 // Joins the partial sums of an entry (a row tile of a chunk) that starts in one
@@ -643,7 +637,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(Attn a) {
     }
 }
 
-template <int D, int RW, int CW, bool SHARED>
+template <int D, int RW, int CW>
 cudaError_t launch(const Attn &a, bool after_gate, cudaStream_t st) {
     CUtensorMap mk, mv;
     const long long rows = (long long)a.c.num_pages * a.c.Hkv * a.c.ps;
@@ -651,7 +645,7 @@ cudaError_t launch(const Attn &a, bool after_gate, cudaStream_t st) {
     if (!make_tma_rows(&mk, a.k, rows, D, box) || !make_tma_rows(&mv, a.v, rows, D, box))
         return cudaErrorInvalidValue;
     const int bytes = (int)RowsSmem<D, CW>::kBytes;
-    const cudaError_t rc = allow_smem<rows_kernel<D, RW, CW, SHARED>>(bytes);
+    const cudaError_t rc = allow_smem<rows_kernel<D, RW, CW>>(bytes);
     if (rc != cudaSuccess) return rc;
     RowsArgs ra;
     ra.a = a;
@@ -659,23 +653,22 @@ cudaError_t launch(const Attn &a, bool after_gate, cudaStream_t st) {
     ra.wait_limit = kDefaultWaitLimit;
     note_launches(1);
     if (after_gate)
-        return launch_after(rows_kernel<D, RW, CW, SHARED>, a.ctas, 32 * (CW + 1), bytes, st, mk, mv, ra);
-    rows_kernel<D, RW, CW, SHARED><<<a.ctas, 32 * (CW + 1), bytes, st>>>(mk, mv, ra);
+        return launch_after(rows_kernel<D, RW, CW>, a.ctas, 32 * (CW + 1), bytes, st, mk, mv, ra);
+    rows_kernel<D, RW, CW><<<a.ctas, 32 * (CW + 1), bytes, st>>>(mk, mv, ra);
     return cudaGetLastError();
 }
 
-template <int D, bool SHARED>
+template <int D>
 cudaError_t launch_d(const Attn &a, bool after_gate, cudaStream_t st) {
-    return a.rows == 16   ? launch<D, 1, 4, SHARED>(a, after_gate, st)
-           : a.rows == 32 ? launch<D, 2, 4, SHARED>(a, after_gate, st)
-                          : launch<D, 4, 8, SHARED>(a, after_gate, st);
+    return a.rows == 16   ? launch<D, 1, 4>(a, after_gate, st)
+           : a.rows == 32 ? launch<D, 2, 4>(a, after_gate, st)
+                          : launch<D, 4, 8>(a, after_gate, st);
 }
 
 }  // namespace
 
 cudaError_t launch_rows(const Attn &a, bool after_gate, cudaStream_t st) {
-    if (a.shared) return a.D == 64 ? launch_d<64, true>(a, true, st) : launch_d<128, true>(a, true, st);
-    const cudaError_t rc = a.D == 64 ? launch_d<64, false>(a, after_gate, st) : launch_d<128, false>(a, after_gate, st);
+    const cudaError_t rc = a.D == 64 ? launch_d<64>(a, after_gate, st) : launch_d<128>(a, after_gate, st);
     return rc == cudaSuccess ? launch_merge_runs(a, st) : rc;
 }
 

@@ -9,157 +9,659 @@
 // A row's softmax over prefix and own keys is that over each, joined:
 //   M = max(m_i),  L = sum l_i 2^(m_i - M),  out = sum o_i 2^(m_i - M) / L
 // over partial sums o_i of 2^(s - m_i) v, with their l_i, in fp32.
-//   1. The plan (one CTA) checks the groups and cuts their rows into tiles of 256.
-//   2. A group's rows lie one behind the other, whatever sequences they are of, so that a
-//      tile with the prefix of one kv head is a job of the tcgen05 kernel of long chunks,
-//      without a mask; the key tiles of all jobs are cut into equal runs, one per CTA.
-//   3. What is behind the prefix is each sequence's own: few rows (a decode step) go to the
-//      streaming kernel of few rows, chunks of many rows are further tiles of 2.
-//   4. Every part of 2 and 3 leaves partial sums, which the merge joins, a warp a row.
-#include "moba_paged_attn.cuh"
+//   1. The plan (one CTA) checks the groups and makes spans: a tile of rows with a range of
+//      keys.  A group's rows lie one behind the other, whatever sequences they are of, so
+//      that its tiles see the prefix whole, without a mask; what is behind the prefix is
+//      each sequence's own.
+//   2. Big spans, 256 rows, are jobs of the tcgen05 kernel of long chunks: groups of more
+//      rows than a small span holds, and the own keys in calls of many new tokens.
+//   3. Small spans, 16 rows, are streamed on mma.sync: a decode step's own keys, and the
+//      prefixes of groups that fit.
+//   4. Every part of 2 and 3 leaves partial sums, which the merge joins.
 #include "moba_mma.cuh"
+#include "moba_paged_attn.cuh"
 
 namespace moba {
 namespace paged {
 namespace {
 
-constexpr int kMergeWarps = 8;
+constexpr int kSmallRows = 16;   // of a small span
+constexpr int kUnit = 16;        // keys that a warp takes at a time: never more than a page
+constexpr int kBigKeys = 128;    // of a key tile of the tcgen05 kernel
+constexpr int kStreamWarps = 4, kStreamCtas = 3;  // of a CTA, of an SM
+constexpr int kMinUnits = 4;     // units of a warp's run at least, where there are few
 
-// Partial sums of a row joined so far: maximum (log2) and sum, and the lane's columns.
-template <int V>
-struct Joined {
-    float M = -INFINITY, L = 0.f, acc[V] = {};
-    bool bad = false;
-
-    // parts of slots p0, p0 + step, ..., n of them, each row of D values
-    __device__ __forceinline__ void add(const float *o, const float2 *ml, size_t p0, size_t step, int n, int lane) {
-        constexpr int U = 4, D = 32 * V;
-        for (int i = 0; i < n; i += U) {
-            float2 s[U];
-            float v[U][V];
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                s[j] = make_float2(-INFINITY, 0.f);
-                if (i + j < n) {
-                    const size_t p = p0 + (size_t)(i + j) * step;
-                    s[j] = ml[p];
-#pragma unroll
-                    for (int k = 0; k < V; k += 2)
-                        *reinterpret_cast<float2 *>(&v[j][k]) =
-                            *reinterpret_cast<const float2 *>(o + p * D + lane * V + k);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                bad |= s[j].y < 0.f;
-                if (s[j].y == 0.f) continue;  // no part, or one without a key for this row
-                const float mn = fmaxf(M, s[j].x), ref = mn == -INFINITY ? 0.f : mn;
-                const float f = mma::fast_exp2(M - ref), g = mma::fast_exp2(s[j].x - ref);
-                M = mn;
-                L = fmaf(s[j].y, g, L * f);
-#pragma unroll
-                for (int k = 0; k < V; ++k) acc[k] = fmaf(v[j][k], g, acc[k] * f);
-            }
-        }
-    }
+struct SharedArgs {
+    Attn a;
+    const int *cu_groups;        // [n_groups + 1]
+    const int *prefix_lens;      // [n_groups]
+    int n_groups;
+    int small_rows;              // groups of up to that many rows are small spans
+    int cap_big, cap_small;      // spans at most
+    int warps;                   // of the streaming kernel
+    int psh;                     // log2(page size)
+    // scratch
+    Span *tiles_small;           // [cap_small]
+    long long *off_small;        // [cap_small + 1] units before each, times the kv heads
+    int *rep;                    // [n_groups] the sequence whose pages are read (num_seqs: none, -1: a wrong group)
+    int *at;                     // [n_groups] its first span << 1 | big, or -1
+    int4 *info;                  // [num_seqs] tokens shared, rows before it in its group, the group's first span, big
+    int *own;                    // [num_seqs] its own first span, or -1
+    float *small_o;              // [cap_small * Hkv + warps][kSmallRows][D] partial sums, as part_o
+    float2 *small_ml;            // [cap_small * Hkv + warps][kSmallRows]
 };
 
-template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_shared_kernel(Attn a) {
-    constexpr int V = D / 32;
-    after_previous();
-    const int lane = threadIdx.x & 31, G = a.G, Hkv = a.c.Hkv;
-    const long long row = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-    if (row >= (long long)a.c.total * a.Hq) return;
-    const int t = (int)(row / a.Hq), h = (int)(row - (long long)t * a.Hq), hk = h / G, gh = h - hk * G;
-    const int b = a.c.seq_of_row(t, lane);
-    Seq s;
-    if (a.c.seq(b, s) != kSeqOk || t < s.row0 || t >= s.row0 + s.n) return;
-    const int j = t - s.row0;
-    const int pre = a.pre_off[a.n_groups], tiles = pre + (a.chunk ? a.own_off[a.c.num_seqs] : 0);
-    const long long total = a.unit_off[tiles], runs = total < a.ctas ? total : a.ctas;
-    Joined<V> x;
-    // the parts of a tile's row: those of the CTAs whose runs [total c / runs, total (c + 1) /
-    // runs) its key tiles on this kv head lie in
-    auto tile = [&](int r) {
-        const int w = r / kJobRows;
-        const long long u0 = a.unit_off[w], T = (a.unit_off[w + 1] - u0) / Hkv, u = u0 + hk * T;
-        const int c0 = (int)(((u + 1) * runs - 1) / total), c1 = (int)(((u + T) * runs - 1) / total);
-        const size_t slot = (size_t)w * Hkv + hk + c0;
-        x.add(a.part_o, a.part_ml, slot * kJobRows + r % kJobRows, kJobRows, c1 - c0 + 1, lane);
-    };
-    if (a.first[b] > 0) tile(a.pre_row[b] + j * G + gh);
-    if (a.chunk) {
-        // (rows without a tile: from offsets that overlap)
-        const int r = j * G + gh;
-        if (a.own_off[b] + r / kJobRows >= a.own_off[b + 1]) return;
-        tile((pre + a.own_off[b]) * kJobRows + r);
-    } else {
-        const int e = (b * a.tps + j / a.tt) * Hkv + hk;
-        const int c0 = max(a.c_first[e], 0), c1 = min(a.c_last[e], a.ctas - 1);
-        x.add(a.own_o, a.own_ml, (size_t)(e + c0) * a.rows + j % a.tt * G + gh, a.rows, c1 - c0 + 1, lane);
+// ----------------------------------------------------------------------------
+// plan
+// ----------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+constexpr int kHeld = 1024;      // sequences and groups whose tables fit shared memory
+
+// inclusive sums over the CTA's threads, N at a time
+template <int N>
+__device__ __forceinline__ void block_scan(long long (&v)[N], long long (*warps)[32], long long (&total)[N]) {
+    static_assert(kPlanThreads == 1024, "a warp scans the warps' sums");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v[i], o);
+            if (lane >= o) v[i] += y;
+        }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (lane == 31) warps[i][warp] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        long long s = warps[i][lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        total[i] = __shfl_sync(0xffffffffu, s, 31);
+        const long long before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+        v[i] += warp > 0 ? before : 0;
     }
-    const float inv = 1.f / x.L;
+}
+
+// HELD: as many sequences and groups as shared memory has room for, so that the searches
+// cost little.
+template <bool HELD>
+__global__ void __launch_bounds__(kPlanThreads) plan_spans_kernel(SharedArgs x) {
+    __shared__ long long warps[4][32];
+    __shared__ int s_cu[HELD ? kHeld + 1 : 1], s_grp[HELD ? kHeld + 1 : 1], s_pre[HELD ? kHeld : 1];
+    __shared__ int s_rep[HELD ? kHeld : 1], s_at[HELD ? kHeld : 1];
+    const Attn &a = x.a;
+    const Cache &c = a.c;
+    let_next();
+    after_previous();
+    const int tid = threadIdx.x, ns = c.num_seqs, ng = x.n_groups, G = a.G, Hkv = c.Hkv;
+    if (HELD) {
+        for (int i = tid; i <= ns; i += kPlanThreads) s_cu[i] = __ldg(c.cu + i);
+        for (int i = tid; ng > 0 && i <= ng; i += kPlanThreads) s_grp[i] = __ldg(x.cu_groups + i);
+        for (int i = tid; i < ng; i += kPlanThreads) s_pre[i] = __ldg(x.prefix_lens + i);
+        __syncthreads();
+    }
+    auto cu = [&](int i) { return HELD ? s_cu[i] : __ldg(c.cu + i); };
+    auto grp = [&](int i) { return HELD ? s_grp[i] : __ldg(x.cu_groups + i); };
+    auto pre = [&](int i) { return HELD ? s_pre[i] : __ldg(x.prefix_lens + i); };
+    int *rep = HELD ? s_rep : x.rep, *at = HELD ? s_at : x.at;
+    auto sync = [&] {
+        if (!HELD) __threadfence_block();
+        __syncthreads();
+    };
+    auto seq = [&](int b, Seq &s) { return c.check(cu(b), cu(b + 1), __ldg(c.lens + b), s); };
+    // groups: offsets that lead nowhere void all of them
+    bool wrong = false;
+    for (int g = tid; ng > 0 && g <= ng; g += kPlanThreads) {
+        const int p = grp(g);
+        wrong |= p < 0 || p > ns || (g > 0 && grp(g - 1) > p);
+    }
+    const bool none = __syncthreads_or(wrong) || ng == 0;
+    for (int g = tid; g < ng; g += kPlanThreads) {
+        const int p = pre(g);
+        const bool ok = !none && p >= 0 && p % c.ps == 0 && p <= (long long)c.max_pages * c.ps;
+        rep[g] = ok ? ns : -1;
+    }
+    sync();
+    // the group of sequence b, or -1
+    auto group_of = [&](int b) {
+        if (none) return -1;
+        int g = 0, hi = ng - 1;
+        while (g < hi) {
+            const int mid = (g + hi + 1) >> 1;
+            if (grp(mid) <= b) g = mid; else hi = mid - 1;
+        }
+        return grp(g) <= b && b < grp(g + 1) ? g : -1;
+    };
+    // every sequence's say: the first with new tokens lends its pages; one that is refused,
+    // or has new tokens inside the prefix, voids the group
+    for (int b0 = 0; b0 < ns; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        Seq s;
+        const int state = b < ns ? seq(b, s) : (int)kSeqEmpty;
+        if (state != kSeqEmpty) {
+            const int g = group_of(b);
+            if (g >= 0) atomicMin(rep + g, state == kSeqOk && pre(g) <= s.len - s.n ? b : -1);
+        }
+        if (state == kSeqBad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+        if (__syncthreads_or(state == kSeqBad))
+            for (int r = b0; r < min(b0 + kPlanThreads, ns); ++r) {
+                Seq y;
+                if (seq(r, y) == kSeqBad) clear_refused(a, y, 0, a.Hq, tid, kPlanThreads);
+            }
+    }
+    sync();
+    // the groups' spans
+    long long nb = 0, ub = 0, nm = 0, um = 0;  // big and small ones so far, and their units
+    for (int g0 = 0; g0 < ng; g0 += kPlanThreads) {
+        const int g = g0 + tid;
+        long long v[4] = {0, 0, 0, 0}, total[4];
+        int row0 = 0, rows = 0, p = 0, n = 0, lender = -1;
+        bool big = false;
+        if (g < ng) {
+            lender = HELD ? rep[g] : __ldcg(rep + g);  // (where the atomics left it)
+            if (lender < 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+            p = pre(g);
+            if (lender >= 0 && lender < ns && p > 0) {
+                row0 = cu(grp(g)) * G;
+                rows = cu(grp(g + 1)) * G - row0;
+                big = rows > x.small_rows;
+                n = big ? (rows + kJobRows - 1) / kJobRows : 1;
+                v[big ? 0 : 2] = n;
+                v[big ? 1 : 3] = (long long)n * Hkv * ((p + (big ? kBigKeys : kUnit) - 1) / (big ? kBigKeys : kUnit));
+            }
+        }
+        const long long mine_n = v[0] + v[2], mine_u = v[1] + v[3];
+        block_scan(v, warps, total);
+        if (g < ng) {
+            const long long i0 = (big ? nb + v[0] : nm + v[2]) - mine_n, u0 = (big ? ub + v[1] : um + v[3]) - mine_u;
+            const int cap = big ? x.cap_big : x.cap_small;
+            Span *tiles = big ? a.tiles_big : x.tiles_small;
+            long long *off = big ? a.off_big : x.off_small;
+            for (int i = 0; i < n && i0 + i < cap; ++i) {
+                Span t;
+                t.row0 = row0 + i * kJobRows;
+                t.nrows = min(rows - i * kJobRows, kJobRows);
+                t.b = lender;
+                t.full = 1;
+                t.key0 = 0;
+                t.key_end = p;
+                t.pdelta = t.pad = 0;
+                tiles[i0 + i] = t;
+                off[i0 + i + 1] = u0 + mine_u / n * (i + 1);
+            }
+            // (more than there is room for: from offsets that overlap)
+            at[g] = n > 0 && i0 + n <= cap ? (int)i0 << 1 | big : -1;
+        }
+        nb += total[0];
+        ub += total[1];
+        nm += total[2];
+        um += total[3];
+    }
+    sync();
+    // the sequences' own
+    const int cap = a.chunk ? x.cap_big : x.cap_small, tile_rows = a.chunk ? kJobRows : kSmallRows;
+    const int unit = a.chunk ? kBigKeys : kUnit;
+    Span *tiles = a.chunk ? a.tiles_big : x.tiles_small;
+    long long *off = a.chunk ? a.off_big : x.off_small;
+    long long &nt = a.chunk ? nb : nm, &ut = a.chunk ? ub : um;
+    for (int b0 = 0; b0 < ns; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        long long v[2] = {0, 0}, total[2];
+        Seq s;
+        int first = 0, rows = 0, pdelta = 0;
+        int4 info = make_int4(0, 0, 0, 0);
+        if (b < ns && seq(b, s) == kSeqOk) {
+            const int g = group_of(b), t = g >= 0 ? at[g] : -1;
+            if (t >= 0) {
+                first = pre(g);
+                info = make_int4(first, (s.row0 - cu(grp(g))) * G, t >> 1, t & 1);
+            }
+            rows = s.n * G;
+            pdelta = s.len - s.n - s.row0;
+            v[0] = (rows + tile_rows - 1) / tile_rows;
+            for (int r = 0; r < rows; r += tile_rows)
+                v[1] += (s.len - s.n + (min(r + tile_rows, rows) - 1) / G - first) / unit + 1;
+            v[1] *= Hkv;
+        }
+        const long long mine_n = v[0], mine_u = v[1];
+        block_scan(v, warps, total);
+        if (b < ns) {
+            long long i = nt + v[0] - mine_n, u = ut + v[1] - mine_u;
+            x.info[b] = info;
+            x.own[b] = mine_n > 0 && i + mine_n <= cap ? (int)i : -1;
+            for (int r = 0; r < rows && i < cap; r += tile_rows, ++i) {
+                Span t;
+                t.row0 = s.row0 * G + r;
+                t.nrows = min(rows - r, tile_rows);
+                t.b = b;
+                t.full = 0;
+                t.key0 = first;
+                t.key_end = (t.row0 + t.nrows - 1) / G + pdelta + 1;
+                t.pdelta = pdelta;
+                t.pad = 0;
+                tiles[i] = t;
+                u += (long long)Hkv * ((t.key_end - first + unit - 1) / unit);
+                off[i + 1] = u;
+            }
+        }
+        nt += total[0];
+        ut += total[1];
+    }
+    if (tid == 0) {
+        a.n_spans[0] = (int)min(nb, (long long)x.cap_big);
+        a.n_spans[1] = (int)min(nm, (long long)x.cap_small);
+        a.off_big[0] = x.off_small[0] = 0;
+    }
+}
+
+// ----------------------------------------------------------------------------
+// small spans
+// ----------------------------------------------------------------------------
+// The units (16 keys of a span on a kv head) of all spans form one sequence that is cut
+// into equal runs, one per warp.  A warp works alone: K and V go from memory straight into
+// the registers of its fragments, 16 bytes a lane, with nothing shared and no barrier, so
+// that a span that ends costs its partial sums and no more.  For that the products take
+// their dimensions in an order of their own: of 32 dimensions, a lane's 16 bytes (8 of
+// them) are its two pairs of two steps of q k; of 64, they are one column of each of
+// eight steps of p v, whose pairs are two keys' values.
+// Bound: HBM.  K of the next unit and V of this one are in flight while the scores are
+// made; 12 warps an SM keep about 60 KB on the way.
+__device__ __forceinline__ uint4 load_once(const __nv_bfloat16 *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas) stream_kernel(SharedArgs x) {
+    using mma::fast_exp2;
+    using mma::mma16816;
+    using mma::pack_bf16;
+    constexpr int C = D / 32, O = D / 64;
+    __shared__ uint4 s_q[kStreamWarps][2 * C][32];
+    const Attn &a = x.a;
+    const Cache &c = a.c;
+    after_previous();
+    let_next();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n8 = lane >> 2, c4 = lane & 3;
+    const int gw = blockIdx.x * kStreamWarps + warp, G = a.G, Hkv = c.Hkv, ps = c.ps;
+    const int spans = a.n_spans[1];
+    const long long total = x.off_small[spans];
+    const long long most = (total + kMinUnits - 1) / kMinUnits, runs = most < x.warps ? most : x.warps;
+    if (gw >= runs) return;
+    long long u = total * gw / runs;
+    const long long u1 = total * (gw + 1) / runs;
+    int w = 0;  // the span with unit u: the last that starts at or before it
+    for (int n = spans; n > 1;) {
+        const int step = (n + 31) / 32;
+        const bool below = lane * step < n && x.off_small[w + lane * step] <= u;
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
+        n = min(step, n - last * step);
+        w += last * step;
+    }
+    uint4 (*sq)[32] = s_q[warp];
+    while (u < u1) {
+        const Span s = x.tiles_small[w];
+        const long long o0 = x.off_small[w], T = (x.off_small[w + 1] - o0) / Hkv;
+        const int hk = (int)((u - o0) / T), i0 = (int)(u - o0 - hk * T), n = (int)min(T - i0, u1 - u);
+        // ---- this lane's rows, n8 and n8 + 8 ----
+        int see[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = n8 + 8 * h, row = s.row0 + r, t = row / G;
+            const bool live = r < s.nrows;
+            // last key that the row sees (no row: whatever, its scores do not matter)
+            see[h] = live && !s.full ? t + s.pdelta : 0x7fffffff;
+            const __nv_bfloat16 *src = a.q + ((size_t)t * a.Hq + hk * G + (row - t * G)) * D + 8 * c4;
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                sq[2 * i + h][lane] = live ? *reinterpret_cast<const uint4 *>(src + 32 * i) : make_uint4(0, 0, 0, 0);
+        }
+        float o[O][8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < O; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[i][j][k] = 0.f;
+        const int *table = c.table + (size_t)s.b * c.max_pages;
+        const int kfirst = s.key0 + i0 * kUnit;  // of the part
+        bool bad = false;
+        int place = 0;   // lane: the first row of unit `lane` of the 32 at hand, among all rows of the pools
+        auto look_up = [&](int i) {
+            const int key = kfirst + (i + lane) * kUnit;
+            place = 0;
+            if (i + lane < n) {
+                const int page = __ldg(table + (key >> x.psh));
+                const bool ok = (unsigned)page < (unsigned)c.num_pages;
+                bad |= !ok;
+                // (some memory of the pool for a page outside it: its rows are dropped)
+                place = (((ok ? page : 0) * Hkv + hk) << x.psh) + (key & (ps - 1));
+            }
+        };
+        uint4 kr[C][2];
+        auto load_k = [&](int i, int at) {
+            const int nv = s.key_end - (kfirst + i * kUnit);  // keys that some row sees, if below 16
+            const __nv_bfloat16 *src = a.k + ((size_t)at + n8) * D + 8 * c4;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < C; ++q)
+                    kr[q][j] = n8 + 8 * j < nv ? load_once(src + 8 * j * D + 32 * q) : make_uint4(0, 0, 0, 0);
+        };
+        look_up(0);
+        int at = __shfl_sync(0xffffffffu, place, 0);
+        load_k(0, at);
+        for (int i = 0; i < n; ++i) {
+            const int key0 = kfirst + i * kUnit, nv = s.key_end - key0;
+            uint4 vr[O][4];  // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
+            {
+                const __nv_bfloat16 *src = a.v + ((size_t)at + 2 * c4) * D + 8 * n8;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int key = (k & 1) + 8 * (k >> 1);
+#pragma unroll
+                    for (int q = 0; q < O; ++q)
+                        // (keys that no row sees may never have been written: zeros)
+                        vr[q][k] = 2 * c4 + key < nv ? load_once(src + key * D + 64 * q) : make_uint4(0, 0, 0, 0);
+                }
+            }
+            float sc[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sc[j][k] = 0.f;
+#pragma unroll
+            for (int q = 0; q < C; ++q) {
+                const uint4 q0 = sq[2 * q][lane], q8 = sq[2 * q + 1][lane];
+                const uint32_t lo[4] = {q0.x, q8.x, q0.y, q8.y}, hi[4] = {q0.z, q8.z, q0.w, q8.w};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    mma16816(sc[j], lo, kr[q][j].x, kr[q][j].y);
+                    mma16816(sc[j], hi, kr[q][j].z, kr[q][j].w);
+                }
+            }
+            if (i + 1 < n) {
+                if (((i + 1) & 31) == 0) look_up(i + 1);
+                at = __shfl_sync(0xffffffffu, place, (i + 1) & 31);
+                load_k(i + 1, at);
+            }
+            float mx[2] = {-INFINITY, -INFINITY}, mu[2];
+            const bool open = key0 + kUnit - 1 <= min(see[0], see[1]) && nv >= kUnit;
+            if (__all_sync(0xffffffffu, open)) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mx[k >> 1] = fmaxf(mx[k >> 1], sc[j][k]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int key = j * 8 + 2 * c4 + (k & 1);
+                        if (key >= nv || key0 + key > see[k >> 1]) sc[j][k] = -INFINITY;
+                        mx[k >> 1] = fmaxf(mx[k >> 1], sc[j][k]);
+                    }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * a.scale_log2;
+            }
+            if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float mn = fmaxf(m[h], mx[h]);
+                    const float r = fast_exp2(m[h] - (mn == -INFINITY ? 0.f : mn));
+                    m[h] = mn;
+                    l[h] *= r;
+#pragma unroll
+                    for (int q = 0; q < O; ++q)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            o[q][j][2 * h] *= r;
+                            o[q][j][2 * h + 1] *= r;
+                        }
+                }
+            }
+            mu[0] = m[0] == -INFINITY ? 0.f : m[0];
+            mu[1] = m[1] == -INFINITY ? 0.f : m[1];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    sc[j][k] = fast_exp2(fmaf(sc[j][k], a.scale_log2, -mu[k >> 1]));
+                    l[k >> 1] += sc[j][k];
+                }
+            const uint32_t pa[4] = {pack_bf16(sc[0][0], sc[0][1]), pack_bf16(sc[0][2], sc[0][3]),
+                                    pack_bf16(sc[1][0], sc[1][1]), pack_bf16(sc[1][2], sc[1][3])};
+#pragma unroll
+            for (int q = 0; q < O; ++q) {
+                const uint32_t *v0 = &vr[q][0].x, *v1 = &vr[q][1].x, *v8 = &vr[q][2].x, *v9 = &vr[q][3].x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    mma16816(o[q][2 * j], pa, __byte_perm(v0[j], v1[j], 0x5410), __byte_perm(v8[j], v9[j], 0x5410));
+                    mma16816(o[q][2 * j + 1], pa, __byte_perm(v0[j], v1[j], 0x7632), __byte_perm(v8[j], v9[j], 0x7632));
+                }
+            }
+        }
+        // ---- the part's sums ----
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad && lane == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+        const size_t slot = ((size_t)w * Hkv + hk + gw) * kSmallRows;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            const int r = n8 + 8 * h;
+            if (r >= s.nrows) continue;
+            float *dst = x.small_o + (slot + r) * D + 16 * c4;
+#pragma unroll
+            for (int q = 0; q < O; ++q)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4)
+                        *reinterpret_cast<float4 *>(dst + 64 * q + 8 * k + j) =
+                            make_float4(o[q][j][2 * h + k], o[q][j + 1][2 * h + k], o[q][j + 2][2 * h + k],
+                                        o[q][j + 3][2 * h + k]);
+            if (c4 == 0) x.small_ml[slot + r] = make_float2(m[h], bad ? -1.f : l[h]);
+        }
+        u += n;
+        if (hk == Hkv - 1 && i0 + n == T) ++w;
+    }
+}
+
+// ----------------------------------------------------------------------------
+// merge
+// ----------------------------------------------------------------------------
+// W warps to a row, every W-th part each: one where there are rows enough, more where few
+// rows have many parts.
+constexpr int kMergeWarps = 16;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_spans_kernel(SharedArgs x, int W) {
+    constexpr int V = D / 32, U = 4;
+    __shared__ float s_acc[kMergeWarps][D], s_m[kMergeWarps], s_l[kMergeWarps];
+    const Attn &a = x.a;
+    after_previous();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W, G = a.G, Hkv = a.c.Hkv;
+    const long long row = (long long)blockIdx.x * (kMergeWarps / W) + warp / W;
+    float M = -INFINITY, L = 0.f, acc[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+    bool bad = false, live = row < (long long)a.c.total * a.Hq;
+    if (live) {
+        const int t = (int)(row / a.Hq), h = (int)(row - (long long)t * a.Hq), hk = h / G, gh = h - hk * G;
+        const int b = a.c.seq_of_row(t, lane);
+        Seq s;
+        const int own = x.own[b];
+        const int4 info = x.info[b];
+        live = a.c.seq(b, s) == kSeqOk && t >= s.row0 && t < s.row0 + s.n && own >= 0;
+        if (live) {
+            const int r = (t - s.row0) * G + gh;
+            // the parts of row `at` of the spans from `first` on: those of the runs [total c /
+            // runs, total (c + 1) / runs) that the span's units on this kv head lie in
+            auto add = [&](bool big, int first, int at) {
+                const int rows = big ? kJobRows : kSmallRows, w = first + at / rows;
+                const long long *off = big ? a.off_big : x.off_small;
+                const long long total = off[a.n_spans[big ? 0 : 1]], u0 = off[w], T = (off[w + 1] - u0) / Hkv;
+                const long long most = big ? total : (total + kMinUnits - 1) / kMinUnits;
+                const long long runs = min(most, (long long)(big ? a.ctas : x.warps)), u = u0 + hk * T;
+                const int c0 = (int)(((u + 1) * runs - 1) / total), c1 = (int)(((u + T) * runs - 1) / total);
+                const float *o = big ? a.part_o : x.small_o;
+                const float2 *ml = big ? a.part_ml : x.small_ml;
+                const size_t p0 = ((size_t)w * Hkv + hk) * rows + at % rows;
+                for (int c = c0 + part; c <= c1; c += W * U) {
+                    float2 z[U];
+                    float v[U][V];
+#pragma unroll
+                    for (int j = 0; j < U; ++j) {
+                        z[j] = make_float2(-INFINITY, 0.f);
+                        if (c + W * j <= c1) {
+                            const size_t p = p0 + (size_t)(c + W * j) * rows;
+                            z[j] = ml[p];
+#pragma unroll
+                            for (int k = 0; k < V; k += 2)
+                                *reinterpret_cast<float2 *>(&v[j][k]) =
+                                    *reinterpret_cast<const float2 *>(o + p * D + lane * V + k);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < U; ++j) {
+                        bad |= z[j].y < 0.f;
+                        if (z[j].y == 0.f) continue;  // no part, or one without a key for this row
+                        const float mn = fmaxf(M, z[j].x), ref = mn == -INFINITY ? 0.f : mn;
+                        const float f = mma::fast_exp2(M - ref), g = mma::fast_exp2(z[j].x - ref);
+                        M = mn;
+                        L = fmaf(z[j].y, g, L * f);
+#pragma unroll
+                        for (int k = 0; k < V; ++k) acc[k] = fmaf(v[j][k], g, acc[k] * f);
+                    }
+                }
+            };
+            if (info.x > 0) add(info.w != 0, info.z, info.y + r);
+            add(a.chunk, own, r);
+        }
+    }
+    if (W > 1) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_l[warp] = bad ? -1.f : L;
+        }
+        __syncthreads();
+        if (!live || part) return;
+        M = -INFINITY;
+        L = 0.f;
+        bad = false;
+        for (int w = warp; w < warp + W; ++w) {
+            M = fmaxf(M, s_m[w]);
+            bad |= s_l[w] < 0.f;
+        }
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        for (int w = warp; w < warp + W; ++w) {
+            const float f = mma::fast_exp2(s_m[w] - ref);
+            L = fmaf(s_l[w], f, L);
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] = fmaf(s_acc[w][lane * V + k], f, acc[k]);
+        }
+    }
+    if (!live) return;
+    const float inv = 1.f / L;
 #pragma unroll
     for (int k = 0; k < V; k += 2)
         *reinterpret_cast<uint32_t *>(a.out + (size_t)row * D + lane * V + k) =
-            x.bad ? 0u : mma::pack_bf16(x.acc[k] * inv, x.acc[k + 1] * inv);
-    if (lane == 0) a.lse[row] = x.bad ? -INFINITY : (x.M + log2f(x.L)) * 0.69314718055994530942f;
+            bad ? 0u : mma::pack_bf16(acc[k] * inv, acc[k + 1] * inv);
+    if (lane == 0) a.lse[row] = bad ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
 }
 
-size_t scratch(Attn *a, void *base) {
+// ----------------------------------------------------------------------------
+// host side
+// ----------------------------------------------------------------------------
+size_t scratch(SharedArgs *x, void *base) {
     size_t off = 0;
     auto take = [&](size_t bytes) -> void * {
         void *p = base ? static_cast<char *>(base) + off : nullptr;
         off = (off + bytes + 255) & ~size_t(255);
         return p;
     };
-    const size_t ns = a->c.num_seqs, ng = a->n_groups, tiles = (size_t)a->pre_cap + (a->chunk ? a->w_cap : 0);
-    a->first = static_cast<int *>(take(4 * ns));
-    a->pre_row = static_cast<int *>(take(4 * ns));
-    a->rep = static_cast<int *>(take(4 * (ng + 1)));
-    a->pre_off = static_cast<int *>(take(4 * (ng + 1)));
-    a->unit_off = static_cast<long long *>(take(8 * (tiles + 1)));
-    const size_t parts = tiles ? (tiles * a->c.Hkv + a->ctas) * kJobRows : 0;
-    a->part_ml = static_cast<float2 *>(take(sizeof(float2) * parts));
-    a->part_o = static_cast<float *>(take(sizeof(float) * parts * a->D));
-    if (a->chunk) {
-        a->own_off = static_cast<int *>(take(4 * (ns + 1)));
-    } else {
-        const size_t own = ((size_t)a->n_ent + a->ctas) * a->rows;
-        a->c_first = static_cast<int *>(take(4 * (size_t)a->n_ent));
-        a->c_last = static_cast<int *>(take(4 * (size_t)a->n_ent));
-        a->own_ml = static_cast<float2 *>(take(sizeof(float2) * own));
-        a->own_o = static_cast<float *>(take(sizeof(float) * own * a->D));
-    }
+    Attn &a = x->a;
+    const size_t ns = a.c.num_seqs, ng = x->n_groups, nb = x->cap_big, nm = x->cap_small;
+    a.n_spans = static_cast<int *>(take(8));
+    a.tiles_big = static_cast<Span *>(take(sizeof(Span) * nb));
+    a.off_big = static_cast<long long *>(take(8 * (nb + 1)));
+    x->tiles_small = static_cast<Span *>(take(sizeof(Span) * nm));
+    x->off_small = static_cast<long long *>(take(8 * (nm + 1)));
+    x->rep = static_cast<int *>(take(4 * ng));
+    x->at = static_cast<int *>(take(4 * ng));
+    x->info = static_cast<int4 *>(take(sizeof(int4) * ns));
+    x->own = static_cast<int *>(take(4 * ns));
+    const size_t big = nb ? (nb * a.c.Hkv + a.ctas) * kJobRows : 0;
+    a.part_ml = static_cast<float2 *>(take(sizeof(float2) * big));
+    a.part_o = static_cast<float *>(take(sizeof(float) * big * a.D));
+    const size_t small = nm ? (nm * a.c.Hkv + x->warps) * kSmallRows : 0;
+    x->small_ml = static_cast<float2 *>(take(sizeof(float2) * small));
+    x->small_o = static_cast<float *>(take(sizeof(float) * small * a.D));
     return off;
 }
 
-// Sizes of a call whose cache has been checked.
-int make_shared(Attn *a, int Hq, int D, int n_groups) {
+// Sizes of a call whose cache has been checked (x->a.c is filled).
+int make_shared(SharedArgs *x, int Hq, int D, int n_groups) {
+    Attn &a = x->a;
     if (n_groups < 0) return MOBA_ERR_INVALID_ARG;
     if (n_groups > 65535) return MOBA_ERR_UNSUPPORTED;
-    const int rc = make_attn(a, Hq, D, 1 << 30);
+    const int rc = make_attn(&a, Hq, D, 1 << 30);
     if (rc != MOBA_OK) return rc;
-    a->shared = true;
-    a->n_groups = n_groups;
-    const long long rows = (long long)a->c.total * a->G;
+    const long long rows = (long long)a.c.total * a.G;
     if (rows >= (1ll << 26)) return MOBA_ERR_UNSUPPORTED;
-    // a tile that is not full for every group with rows
-    long long some = n_groups < a->c.num_seqs ? n_groups : a->c.num_seqs;
-    if (some > a->c.total) some = a->c.total;
-    a->pre_cap = n_groups ? (int)(rows / kJobRows + some) : 0;
-    const long long tiles = a->pre_cap + (a->chunk ? (long long)a->w_cap : 0);
-    if (tiles * a->c.Hkv >= (1ll << 30) || a->n_ent >= (1 << 30)) return MOBA_ERR_UNSUPPORTED;
+    x->n_groups = n_groups;
+    x->warps = sm_count() * kStreamCtas * kStreamWarps;
+    x->psh = __builtin_ctz((unsigned)a.c.ps);
+    x->small_rows = a.chunk ? 0 : kSmallRows;
+    // sequences and groups with rows: each may leave a tile that is not full
+    const long long seqs = a.c.num_seqs < a.c.total ? a.c.num_seqs : a.c.total;
+    const long long groups = n_groups < seqs ? n_groups : seqs;
+    const long long own = rows / (a.chunk ? kJobRows : kSmallRows) + seqs;
+    const long long big = groups && rows > x->small_rows ? rows / kJobRows + groups : 0;
+    const long long nb = big + (a.chunk ? own : 0), nm = a.chunk ? 0 : own + groups;
+    if (nb * a.c.Hkv >= (1ll << 30) || nm * a.c.Hkv >= (1ll << 30)) return MOBA_ERR_UNSUPPORTED;
+    x->cap_big = (int)nb;
+    x->cap_small = (int)nm;
     return MOBA_OK;
 }
 
-template <int D>
-cudaError_t launch_merge(const Attn &a, cudaStream_t st) {
-    const long long rows = (long long)a.c.total * a.Hq;
+cudaError_t launch_plan(const SharedArgs &x, cudaStream_t st) {
     note_launches(1);
-    return launch_after(merge_shared_kernel<D>, dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)),
-                        dim3(32 * kMergeWarps), 0, st, a);
+    if (x.a.c.num_seqs <= kHeld && x.n_groups <= kHeld) plan_spans_kernel<true><<<1, kPlanThreads, 0, st>>>(x);
+    else plan_spans_kernel<false><<<1, kPlanThreads, 0, st>>>(x);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_small(const SharedArgs &x, cudaStream_t st) {
+    note_launches(1);
+    return launch_after(stream_kernel<D>, dim3(x.warps / kStreamWarps), dim3(32 * kStreamWarps), 0, st, x);
+}
+
+template <int D>
+cudaError_t launch_merge(const SharedArgs &x, cudaStream_t st) {
+    const long long rows = (long long)x.a.c.total * x.a.Hq;
+    const int W = rows <= 2 * x.a.ctas ? 16 : rows <= 32 * x.a.ctas ? 4 : 1;
+    const long long ctas = (rows * W + kMergeWarps - 1) / kMergeWarps;
+    note_launches(1);
+    return launch_after(merge_spans_kernel<D>, dim3((unsigned)ctas), dim3(32 * kMergeWarps), 0, st, x, W);
 }
 
 }  // namespace
@@ -174,15 +676,15 @@ static int any_block(int page_size) { return page_size < 64 ? 64 : page_size; }
 
 MOBA_EXPORT size_t moba_paged_attn_shared_workspace_size(int num_seqs, int n_groups, int total, int max_new, int Hq,
                                                          int Hkv, int D, int page_size, int max_pages) {
-    Attn a = {};
+    SharedArgs x = {};
     // any non-null, aligned addresses: only the sizes matter here
     const void *some = reinterpret_cast<const void *>(256);
     const int32_t *ints = static_cast<const int32_t *>(some);
-    if (make_cache(&a.c, some, some, nullptr, ints, ints, ints, num_seqs, total, max_new, Hkv, D, 1, page_size,
+    if (make_cache(&x.a.c, some, some, nullptr, ints, ints, ints, num_seqs, total, max_new, Hkv, D, 1, page_size,
                    max_pages, any_block(page_size)) != MOBA_OK ||
-        make_shared(&a, Hq, D, n_groups) != MOBA_OK)
+        make_shared(&x, Hq, D, n_groups) != MOBA_OK)
         return 0;
-    return scratch(&a, nullptr);
+    return scratch(&x, nullptr);
 }
 
 MOBA_EXPORT int moba_paged_attn_shared(const void *q, const void *k_pages, const void *v_pages,
@@ -192,10 +694,11 @@ MOBA_EXPORT int moba_paged_attn_shared(const void *q, const void *k_pages, const
                                        int num_pages, int page_size, int max_pages, void *workspace,
                                        size_t workspace_bytes, void *stream) {
     if (!q || !out || !lse || (n_groups > 0 && (!cu_groups || !prefix_lens))) return MOBA_ERR_INVALID_ARG;
-    Attn a = {};
+    SharedArgs x = {};
+    Attn &a = x.a;
     int rc = make_cache(&a.c, k_pages, v_pages, nullptr, page_table, cu_new, cache_lens, num_seqs, total, max_new,
                         Hkv, D, num_pages, page_size, max_pages, any_block(page_size));
-    if (rc == MOBA_OK) rc = make_shared(&a, Hq, D, n_groups);
+    if (rc == MOBA_OK) rc = make_shared(&x, Hq, D, n_groups);
     if (rc != MOBA_OK) return rc;
     if (misaligned16(q) || misaligned16(out) ||
         ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_groups) |
@@ -206,10 +709,10 @@ MOBA_EXPORT int moba_paged_attn_shared(const void *q, const void *k_pages, const
     a.v = static_cast<const __nv_bfloat16 *>(v_pages);
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
-    a.cu_groups = cu_groups;
-    a.prefix_lens = prefix_lens;
+    x.cu_groups = cu_groups;
+    x.prefix_lens = prefix_lens;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const size_t need = scratch(&a, nullptr);
+    const size_t need = scratch(&x, nullptr);
     if (workspace && (workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
         return MOBA_ERR_WORKSPACE;
     a.status = status_word();
@@ -220,11 +723,11 @@ MOBA_EXPORT int moba_paged_attn_shared(const void *q, const void *k_pages, const
         if (e != cudaSuccess) return cuda_result(e);
         workspace = own;
     }
-    scratch(&a, workspace);
-    cudaError_t e = launch_plan_shared(a, st);
-    if (e == cudaSuccess && (a.n_groups || a.chunk)) e = launch_chunk_shared(a, st);
-    if (e == cudaSuccess && !a.chunk) e = launch_rows(a, true, st);
-    if (e == cudaSuccess) e = D == 64 ? launch_merge<64>(a, st) : launch_merge<128>(a, st);
+    scratch(&x, workspace);
+    cudaError_t e = launch_plan(x, st);
+    if (e == cudaSuccess && x.cap_big) e = launch_chunk_spans(a, st);
+    if (e == cudaSuccess && x.cap_small) e = D == 64 ? launch_small<64>(x, st) : launch_small<128>(x, st);
+    if (e == cudaSuccess) e = D == 64 ? launch_merge<64>(x, st) : launch_merge<128>(x, st);
     if (own) {
         const cudaError_t f = cudaFreeAsync(own, st);
         if (e == cudaSuccess) e = f;
