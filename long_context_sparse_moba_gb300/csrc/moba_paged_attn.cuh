@@ -13,6 +13,7 @@ namespace paged {
 constexpr int kTile = 64;        // keys per tile
 constexpr int kMaxRows = 64;     // query rows of an entry at most
 constexpr int kJobRows = 256;    // query rows of a job of the tcgen05 kernel
+constexpr int kBigStart = 3;     // key tiles that the start of a span's job counts as
 constexpr int kSelBad = -2;
 constexpr int kMaxBlocks = 65536;  // blocks of a sequence where blocks are selected
 
@@ -53,8 +54,9 @@ struct Attn {
     float2 *part_ml;            // [ctas][2][rows] their m and sum of exp2(s - m); a sum below 0: bad page
     // ---- shared prefixes: jobs that are tiles of rows with a range of keys ----
     Span *tiles_big;            // [...] 256 rows at most, for the tcgen05 kernel
-    long long *off_big;         // [... + 1] key tiles before each, times the kv heads
-    int *n_spans;               // [2] how many of them, and of the streamed ones
+    long long *off_big;         // [... + 1] key tiles before each (and kBigStart), times the kv heads
+    int *n_spans;               // [4] how many of them, and of the streamed ones; of groups among each
+    int *c_first;               // [... * Hkv] the CTAs in whose runs the span on the kv head lies, to c_last
     // ---- chunks of many rows (the tcgen05 kernel): jobs of up to 256 rows ----
     bool chunk;
     int n_max;                  // blocks of a sequence at most

@@ -324,19 +324,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int T = J.nt;
                         for (; go && u < u1 && u < off[w + 1];) {
                             const long long in = u - off[w];
-                            const int hk = (int)(in / T);
-                            J.h[0].hk = J.h[1].hk = hk;
-                            J.lo = (int)(in - (long long)hk * T);
-                            J.nt = (int)min((long long)(T - J.lo), u1 - u);
-                            const int e = w * a.c.Hkv + hk;
-                            J.whole = !SPANS && J.nt == T;
-                            J.slot = SPANS ? e + blockIdx.x : blockIdx.x * 2 + (J.lo == 0 ? 1 : 0);
-                            own_ends<N>(a, J);
-                            if (SPANS) {
-                            } else if (J.lo + J.nt == T) a.c_last[e] = blockIdx.x;
-                            else if (J.lo == 0) open = e;
-                            go = hand(J);
-                            u += J.nt;
+                            if constexpr (SPANS) {
+                                // (the first units of a span on a kv head stand for its start)
+                                const int V = T + kBigStart, hk = (int)(in / V), v0 = (int)(in - (long long)hk * V);
+                                const int take = (int)min((long long)(V - v0), u1 - u), e = w * a.c.Hkv + hk;
+                                J.h[0].hk = J.h[1].hk = hk;
+                                J.lo = max(v0 - kBigStart, 0);
+                                J.nt = v0 + take - kBigStart - J.lo;
+                                J.slot = e + blockIdx.x;
+                                u += take;
+                                if (J.nt <= 0) continue;
+                                if (J.lo == 0) a.c_first[e] = blockIdx.x;
+                                if (J.lo + J.nt == T) a.c_last[e] = blockIdx.x;
+                                own_ends<N>(a, J);
+                                go = hand(J);
+                            } else {
+                                const int hk = (int)(in / T);
+                                J.h[0].hk = J.h[1].hk = hk;
+                                J.lo = (int)(in - (long long)hk * T);
+                                J.nt = (int)min((long long)(T - J.lo), u1 - u);
+                                J.whole = J.nt == T;
+                                J.slot = blockIdx.x * 2 + (J.lo == 0 ? 1 : 0);
+                                own_ends<N>(a, J);
+                                const int e = w * a.c.Hkv + hk;
+                                if (J.lo + J.nt == T) a.c_last[e] = blockIdx.x;
+                                else if (J.lo == 0) open = e;
+                                go = hand(J);
+                                u += J.nt;
+                            }
                         }
                         ++w;
                     }

@@ -20,6 +20,7 @@
 //   4. Every part of 2 and 3 leaves partial sums, which the merge joins.
 #include "moba_mma.cuh"
 #include "moba_paged_attn.cuh"
+#include "moba_ptx.cuh"
 
 namespace moba {
 namespace paged {
@@ -28,8 +29,11 @@ namespace {
 constexpr int kSmallRows = 16;   // of a small span
 constexpr int kUnit = 16;        // keys that a warp takes at a time: never more than a page
 constexpr int kBigKeys = 128;    // of a key tile of the tcgen05 kernel
-constexpr int kStreamWarps = 4, kStreamCtas = 3;  // of a CTA, of an SM
-constexpr int kMinUnits = 4;     // units of a warp's run at least, where there are few
+constexpr int kStreamWarps = 4, kStreamCtas = 2;  // of a CTA, of an SM
+constexpr int kMinUnits = 6;     // units of a warp's run at least, where there are few
+// The start of a span on a kv head counts as that many units, its rows and sums being
+// what they cost: runs of equal units then take equal time.
+constexpr int kSmallStart = 2;
 
 struct SharedArgs {
     Attn a;
@@ -38,6 +42,7 @@ struct SharedArgs {
     int n_groups;
     int small_rows;              // groups of up to that many rows are small spans
     int cap_big, cap_small;      // spans at most
+    int own_cap;                 // of them sequences' own
     int warps;                   // of the streaming kernel
     int psh;                     // log2(page size)
     // scratch
@@ -45,8 +50,8 @@ struct SharedArgs {
     long long *off_small;        // [cap_small + 1] units before each, times the kv heads
     int *rep;                    // [n_groups] the sequence whose pages are read (num_seqs: none, -1: a wrong group)
     int *at;                     // [n_groups] its first span << 1 | big, or -1
-    int4 *info;                  // [num_seqs] tokens shared, rows before it in its group, the group's first span, big
-    int *own;                    // [num_seqs] its own first span, or -1
+    int4 *info;                  // [num_seqs] tokens shared, the group's first row, its first span, big
+    int *small_first, *small_last;  // [cap_small * Hkv] the warps in whose runs the span on the kv head lies
     float *small_o;              // [cap_small * Hkv + warps][kSmallRows][D] partial sums, as part_o
     float2 *small_ml;            // [cap_small * Hkv + warps][kSmallRows]
 };
@@ -54,13 +59,12 @@ struct SharedArgs {
 // ----------------------------------------------------------------------------
 // plan
 // ----------------------------------------------------------------------------
-constexpr int kPlanThreads = 1024;
 constexpr int kHeld = 1024;      // sequences and groups whose tables fit shared memory
 
-// inclusive sums over the CTA's threads, N at a time
-template <int N>
+// inclusive sums over the CTA's T threads, N at a time
+template <int T, int N>
 __device__ __forceinline__ void block_scan(long long (&v)[N], long long (*warps)[32], long long (&total)[N]) {
-    static_assert(kPlanThreads == 1024, "a warp scans the warps' sums");
+    constexpr int W = T / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -76,34 +80,39 @@ __device__ __forceinline__ void block_scan(long long (&v)[N], long long (*warps)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        long long s = warps[i][lane];
+        long long s = lane < W ? warps[i][lane] : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
+        for (int o = 1; o < W; o <<= 1) {
             const long long y = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += y;
         }
-        total[i] = __shfl_sync(0xffffffffu, s, 31);
+        total[i] = __shfl_sync(0xffffffffu, s, W - 1);
         const long long before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
         v[i] += warp > 0 ? before : 0;
     }
 }
 
-// HELD: as many sequences and groups as shared memory has room for, so that the searches
-// cost little.
-template <bool HELD>
-__global__ void __launch_bounds__(kPlanThreads) plan_spans_kernel(SharedArgs x) {
+// T threads.  HELD: as many sequences and groups as shared memory has room for, so that
+// the searches cost little.
+template <int T, bool HELD>
+__global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
     __shared__ long long warps[4][32];
-    __shared__ int s_cu[HELD ? kHeld + 1 : 1], s_grp[HELD ? kHeld + 1 : 1], s_pre[HELD ? kHeld : 1];
-    __shared__ int s_rep[HELD ? kHeld : 1], s_at[HELD ? kHeld : 1];
+    __shared__ int s_cu[HELD ? kHeld + 1 : 1], s_len[HELD ? kHeld : 1], s_grp[HELD ? kHeld + 1 : 1];
+    __shared__ int s_pre[HELD ? kHeld : 1], s_rep[HELD ? kHeld : 1], s_at[HELD ? kHeld : 1];
     const Attn &a = x.a;
     const Cache &c = a.c;
     let_next();
     after_previous();
     const int tid = threadIdx.x, ns = c.num_seqs, ng = x.n_groups, G = a.G, Hkv = c.Hkv;
     if (HELD) {
-        for (int i = tid; i <= ns; i += kPlanThreads) s_cu[i] = __ldg(c.cu + i);
-        for (int i = tid; ng > 0 && i <= ng; i += kPlanThreads) s_grp[i] = __ldg(x.cu_groups + i);
-        for (int i = tid; i < ng; i += kPlanThreads) s_pre[i] = __ldg(x.prefix_lens + i);
+        for (int i = tid; i <= ns; i += T) {
+            s_cu[i] = __ldg(c.cu + i);
+            if (i < ns) s_len[i] = __ldg(c.lens + i);
+        }
+        for (int i = tid; ng > 0 && i <= ng; i += T) {
+            s_grp[i] = __ldg(x.cu_groups + i);
+            if (i < ng) s_pre[i] = __ldg(x.prefix_lens + i);
+        }
         __syncthreads();
     }
     auto cu = [&](int i) { return HELD ? s_cu[i] : __ldg(c.cu + i); };
@@ -114,15 +123,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_spans_kernel(SharedArgs x) 
         if (!HELD) __threadfence_block();
         __syncthreads();
     };
-    auto seq = [&](int b, Seq &s) { return c.check(cu(b), cu(b + 1), __ldg(c.lens + b), s); };
+    auto seq = [&](int b, Seq &s) { return c.check(cu(b), cu(b + 1), HELD ? s_len[b] : __ldg(c.lens + b), s); };
     // groups: offsets that lead nowhere void all of them
     bool wrong = false;
-    for (int g = tid; ng > 0 && g <= ng; g += kPlanThreads) {
+    for (int g = tid; ng > 0 && g <= ng; g += T) {
         const int p = grp(g);
         wrong |= p < 0 || p > ns || (g > 0 && grp(g - 1) > p);
     }
     const bool none = __syncthreads_or(wrong) || ng == 0;
-    for (int g = tid; g < ng; g += kPlanThreads) {
+    for (int g = tid; g < ng; g += T) {
         const int p = pre(g);
         const bool ok = !none && p >= 0 && p % c.ps == 0 && p <= (long long)c.max_pages * c.ps;
         rep[g] = ok ? ns : -1;
@@ -140,7 +149,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_spans_kernel(SharedArgs x) 
     };
     // every sequence's say: the first with new tokens lends its pages; one that is refused,
     // or has new tokens inside the prefix, voids the group
-    for (int b0 = 0; b0 < ns; b0 += kPlanThreads) {
+    for (int b0 = 0; b0 < ns; b0 += T) {
         const int b = b0 + tid;
         Seq s;
         const int state = b < ns ? seq(b, s) : (int)kSeqEmpty;
@@ -150,15 +159,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_spans_kernel(SharedArgs x) 
         }
         if (state == kSeqBad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
         if (__syncthreads_or(state == kSeqBad))
-            for (int r = b0; r < min(b0 + kPlanThreads, ns); ++r) {
+            for (int r = b0; r < min(b0 + T, ns); ++r) {
                 Seq y;
-                if (seq(r, y) == kSeqBad) clear_refused(a, y, 0, a.Hq, tid, kPlanThreads);
+                if (seq(r, y) == kSeqBad) clear_refused(a, y, 0, a.Hq, tid, T);
             }
     }
     sync();
     // the groups' spans
     long long nb = 0, ub = 0, nm = 0, um = 0;  // big and small ones so far, and their units
-    for (int g0 = 0; g0 < ng; g0 += kPlanThreads) {
+    for (int g0 = 0; g0 < ng; g0 += T) {
         const int g = g0 + tid;
         long long v[4] = {0, 0, 0, 0}, total[4];
         int row0 = 0, rows = 0, p = 0, n = 0, lender = -1;
@@ -173,11 +182,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_spans_kernel(SharedArgs x) 
                 big = rows > x.small_rows;
                 n = big ? (rows + kJobRows - 1) / kJobRows : 1;
                 v[big ? 0 : 2] = n;
-                v[big ? 1 : 3] = (long long)n * Hkv * ((p + (big ? kBigKeys : kUnit) - 1) / (big ? kBigKeys : kUnit));
+                v[big ? 1 : 3] = (long long)n * Hkv * (big ? (p + kBigKeys - 1) / kBigKeys + kBigStart
+                                                           : (p + kUnit - 1) / kUnit + kSmallStart);
             }
         }
         const long long mine_n = v[0] + v[2], mine_u = v[1] + v[3];
-        block_scan(v, warps, total);
+        block_scan<T>(v, warps, total);
         if (g < ng) {
             const long long i0 = (big ? nb + v[0] : nm + v[2]) - mine_n, u0 = (big ? ub + v[1] : um + v[3]) - mine_u;
             const int cap = big ? x.cap_big : x.cap_small;
@@ -204,13 +214,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_spans_kernel(SharedArgs x) 
         um += total[3];
     }
     sync();
+    const int groups_spans[2] = {(int)min(nb, (long long)x.cap_big), (int)min(nm, (long long)x.cap_small)};
     // the sequences' own
     const int cap = a.chunk ? x.cap_big : x.cap_small, tile_rows = a.chunk ? kJobRows : kSmallRows;
-    const int unit = a.chunk ? kBigKeys : kUnit;
+    const int unit = a.chunk ? kBigKeys : kUnit, start = a.chunk ? kBigStart : kSmallStart;
     Span *tiles = a.chunk ? a.tiles_big : x.tiles_small;
     long long *off = a.chunk ? a.off_big : x.off_small;
     long long &nt = a.chunk ? nb : nm, &ut = a.chunk ? ub : um;
-    for (int b0 = 0; b0 < ns; b0 += kPlanThreads) {
+    for (int b0 = 0; b0 < ns; b0 += T) {
         const int b = b0 + tid;
         long long v[2] = {0, 0}, total[2];
         Seq s;
@@ -220,21 +231,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_spans_kernel(SharedArgs x) 
             const int g = group_of(b), t = g >= 0 ? at[g] : -1;
             if (t >= 0) {
                 first = pre(g);
-                info = make_int4(first, (s.row0 - cu(grp(g))) * G, t >> 1, t & 1);
+                info = make_int4(first, cu(grp(g)) * G, t >> 1, t & 1);
             }
             rows = s.n * G;
             pdelta = s.len - s.n - s.row0;
             v[0] = (rows + tile_rows - 1) / tile_rows;
             for (int r = 0; r < rows; r += tile_rows)
-                v[1] += (s.len - s.n + (min(r + tile_rows, rows) - 1) / G - first) / unit + 1;
+                v[1] += (s.len - s.n + (min(r + tile_rows, rows) - 1) / G - first) / unit + 1 + start;
             v[1] *= Hkv;
         }
         const long long mine_n = v[0], mine_u = v[1];
-        block_scan(v, warps, total);
+        block_scan<T>(v, warps, total);
         if (b < ns) {
             long long i = nt + v[0] - mine_n, u = ut + v[1] - mine_u;
             x.info[b] = info;
-            x.own[b] = mine_n > 0 && i + mine_n <= cap ? (int)i : -1;
             for (int r = 0; r < rows && i < cap; r += tile_rows, ++i) {
                 Span t;
                 t.row0 = s.row0 * G + r;
@@ -246,7 +256,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_spans_kernel(SharedArgs x) 
                 t.pdelta = pdelta;
                 t.pad = 0;
                 tiles[i] = t;
-                u += (long long)Hkv * ((t.key_end - first + unit - 1) / unit);
+                u += (long long)Hkv * ((t.key_end - first + unit - 1) / unit + start);
                 off[i + 1] = u;
             }
         }
@@ -254,8 +264,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_spans_kernel(SharedArgs x) 
         ut += total[1];
     }
     if (tid == 0) {
-        a.n_spans[0] = (int)min(nb, (long long)x.cap_big);
-        a.n_spans[1] = (int)min(nm, (long long)x.cap_small);
+        // spans, and those of groups among them
+        *reinterpret_cast<int4 *>(a.n_spans) = make_int4((int)min(nb, (long long)x.cap_big), (int)min(nm, (long long)x.cap_small),
+                                                         groups_spans[0], groups_spans[1]);
         a.off_big[0] = x.off_small[0] = 0;
     }
 }
@@ -264,20 +275,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_spans_kernel(SharedArgs x) 
 // small spans
 // ----------------------------------------------------------------------------
 // The units (16 keys of a span on a kv head) of all spans form one sequence that is cut
-// into equal runs, one per warp.  A warp works alone: K and V go from memory straight into
-// the registers of its fragments, 16 bytes a lane, with nothing shared and no barrier, so
-// that a span that ends costs its partial sums and no more.  For that the products take
+// into equal runs, one per warp.  A warp works alone: it copies K and V by 16 bytes a lane
+// into a ring of stages that no other warp sees, and a lane reads back only what it copied
+// itself, so that nothing is shared and there is no barrier; a span that ends costs its
+// partial sums and no more, and the copies run ahead over it.  For that the products take
 // their dimensions in an order of their own: of 32 dimensions, a lane's 16 bytes (8 of
 // them) are its two pairs of two steps of q k; of 64, they are one column of each of
 // eight steps of p v, whose pairs are two keys' values.
-// Bound: HBM.  K of the next unit and V of this one are in flight while the scores are
-// made; 12 warps an SM keep about 60 KB on the way.
-__device__ __forceinline__ uint4 load_once(const __nv_bfloat16 *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+// Bound: HBM.
+template <int D>
+struct Ring {
+    static constexpr int C = D / 32, O = D / 64;
+    static constexpr int kPieces = 2 * C + 4 * O;  // 16 bytes a lane: K, then V
+    static constexpr int kStages = 3 * 128 / D;
+    static constexpr int kWarpBytes = kStages * kPieces * 512;
+    static constexpr int kBytes = kStreamWarps * kWarpBytes;
+};
+
+template <int N>
+__device__ __forceinline__ void copies_left() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int D>
@@ -285,8 +302,9 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas) stream_kernel(
     using mma::fast_exp2;
     using mma::mma16816;
     using mma::pack_bf16;
-    constexpr int C = D / 32, O = D / 64;
-    __shared__ uint4 s_q[kStreamWarps][2 * C][32];
+    using R = Ring<D>;
+    constexpr int C = R::C, O = R::O, ST = R::kStages;
+    extern __shared__ __align__(128) uint8_t s_ring[];
     const Attn &a = x.a;
     const Cache &c = a.c;
     after_previous();
@@ -297,23 +315,84 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas) stream_kernel(
     const long long total = x.off_small[spans];
     const long long most = (total + kMinUnits - 1) / kMinUnits, runs = most < x.warps ? most : x.warps;
     if (gw >= runs) return;
-    long long u = total * gw / runs;
-    const long long u1 = total * (gw + 1) / runs;
-    int w = 0;  // the span with unit u: the last that starts at or before it
-    for (int n = spans; n > 1;) {
-        const int step = (n + 31) / 32;
-        const bool below = lane * step < n && x.off_small[w + lane * step] <= u;
+    const long long u0 = total * gw / runs;
+    const int n = (int)(total * (gw + 1) / runs - u0);
+    int w = 0;  // the span with unit u0: the last that starts at or before it
+    for (int k = spans; k > 1;) {
+        const int step = (k + 31) / 32;
+        const bool below = lane * step < k && x.off_small[w + lane * step] <= u0;
         const int last = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
-        n = min(step, n - last * step);
+        k = min(step, k - last * step);
         w += last * step;
     }
-    uint4 (*sq)[32] = s_q[warp];
-    while (u < u1) {
+    uint8_t *mine = s_ring + warp * R::kWarpBytes + lane * 16;  // the lane's place of piece 0 of stage 0
+    const uint32_t ring = ptx::saddr(mine);
+    // ---- copies ----
+    int ahead = 0, wa = w;              // units of the run that have been issued; a span at or before the next
+    int place = 0, keys = 0;            // lane: its unit of the 32 at hand: first row of the pools, keys (0: none)
+    unsigned long long bad_units = 0;   // of the last 64 units
+    auto look_up = [&] {
+        int wl = wa;
+        bool bad = false;
+        keys = 0;
+        if (ahead + lane < n) {
+            const long long u = u0 + ahead + lane;
+            while (x.off_small[wl + 1] <= u) ++wl;
+            const Span s = x.tiles_small[wl];
+            const long long o = x.off_small[wl], T = (x.off_small[wl + 1] - o) / Hkv;
+            const int hk = (int)((u - o) / T), i = (int)(u - o - hk * T) - kSmallStart;
+            if (i >= 0) {
+                const int key = s.key0 + i * kUnit;
+                const int page = __ldg(c.table + (size_t)s.b * c.max_pages + (key >> x.psh));
+                bad = (unsigned)page >= (unsigned)c.num_pages;
+                // (some memory of the pool for a page outside it: its rows are dropped)
+                place = (((bad ? 0 : page) * Hkv + hk) << x.psh) + (key & (ps - 1));
+                keys = min(s.key_end - key, kUnit);
+            }
+        }
+        const unsigned long long ballot = __ballot_sync(0xffffffffu, bad);
+        const int at = ahead & 63;
+        bad_units = (bad_units & ~(0xffffffffull << at)) | ballot << at;
+        wa = __shfl_sync(0xffffffffu, wl, min(31, n - 1 - ahead));
+    };
+    auto issue = [&] {
+        if (ahead < n) {
+            if ((ahead & 31) == 0) look_up();
+            const int at = __shfl_sync(0xffffffffu, place, ahead & 31), nv = __shfl_sync(0xffffffffu, keys, ahead & 31);
+            if (nv > 0) {
+                // (keys that no row sees may never have been written: zeros)
+                const uint32_t dst = ring + (ahead % ST) * R::kPieces * 512;
+                const __nv_bfloat16 *k = a.k + ((size_t)at + n8) * D + 8 * c4;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < C; ++q)
+                        ptx::cp_async16(dst + (2 * q + j) * 512, k + 8 * j * D + 32 * q, n8 + 8 * j < nv);
+                const __nv_bfloat16 *v = a.v + ((size_t)at + 2 * c4) * D + 8 * n8;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int q = 0; q < O; ++q) {
+                        const int key = (j & 1) + 8 * (j >> 1);
+                        ptx::cp_async16(dst + (2 * C + 4 * q + j) * 512, v + key * D + 64 * q, 2 * c4 + key < nv);
+                    }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++ahead;
+    };
+#pragma unroll 1
+    for (int i = 0; i < ST - 1; ++i) issue();
+    // ---- parts: the run's units of one span on one kv head ----
+    for (int j = 0; j < n;) {
+        while (x.off_small[w + 1] <= u0 + j) ++w;
         const Span s = x.tiles_small[w];
-        const long long o0 = x.off_small[w], T = (x.off_small[w + 1] - o0) / Hkv;
-        const int hk = (int)((u - o0) / T), i0 = (int)(u - o0 - hk * T), n = (int)min(T - i0, u1 - u);
-        // ---- this lane's rows, n8 and n8 + 8 ----
+        const long long in = u0 + j - x.off_small[w], T = (x.off_small[w + 1] - x.off_small[w]) / Hkv;
+        const int hk = (int)(in / T), v0 = (int)(in - hk * T), cnt = (int)min(T - v0, (long long)(n - j));
+        const int e = w * Hkv + hk;
+        // this lane's rows, n8 and n8 + 8
         int see[2];
+        uint4 qr[C][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = n8 + 8 * h, row = s.row0 + r, t = row / G;
@@ -323,92 +402,55 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas) stream_kernel(
             const __nv_bfloat16 *src = a.q + ((size_t)t * a.Hq + hk * G + (row - t * G)) * D + 8 * c4;
 #pragma unroll
             for (int i = 0; i < C; ++i)
-                sq[2 * i + h][lane] = live ? *reinterpret_cast<const uint4 *>(src + 32 * i) : make_uint4(0, 0, 0, 0);
+                qr[i][h] = live ? __ldg(reinterpret_cast<const uint4 *>(src + 32 * i)) : make_uint4(0, 0, 0, 0);
         }
         float o[O][8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < O; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int k = 0; k < 8; ++k)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[i][j][k] = 0.f;
-        const int *table = c.table + (size_t)s.b * c.max_pages;
-        const int kfirst = s.key0 + i0 * kUnit;  // of the part
+                for (int z = 0; z < 4; ++z) o[i][k][z] = 0.f;
         bool bad = false;
-        int place = 0;   // lane: the first row of unit `lane` of the 32 at hand, among all rows of the pools
-        auto look_up = [&](int i) {
-            const int key = kfirst + (i + lane) * kUnit;
-            place = 0;
-            if (i + lane < n) {
-                const int page = __ldg(table + (key >> x.psh));
-                const bool ok = (unsigned)page < (unsigned)c.num_pages;
-                bad |= !ok;
-                // (some memory of the pool for a page outside it: its rows are dropped)
-                place = (((ok ? page : 0) * Hkv + hk) << x.psh) + (key & (ps - 1));
-            }
-        };
-        uint4 kr[C][2];
-        auto load_k = [&](int i, int at) {
-            const int nv = s.key_end - (kfirst + i * kUnit);  // keys that some row sees, if below 16
-            const __nv_bfloat16 *src = a.k + ((size_t)at + n8) * D + 8 * c4;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int q = 0; q < C; ++q)
-                    kr[q][j] = n8 + 8 * j < nv ? load_once(src + 8 * j * D + 32 * q) : make_uint4(0, 0, 0, 0);
-        };
-        look_up(0);
-        int at = __shfl_sync(0xffffffffu, place, 0);
-        load_k(0, at);
-        for (int i = 0; i < n; ++i) {
-            const int key0 = kfirst + i * kUnit, nv = s.key_end - key0;
-            uint4 vr[O][4];  // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
-            {
-                const __nv_bfloat16 *src = a.v + ((size_t)at + 2 * c4) * D + 8 * n8;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int key = (k & 1) + 8 * (k >> 1);
-#pragma unroll
-                    for (int q = 0; q < O; ++q)
-                        // (keys that no row sees may never have been written: zeros)
-                        vr[q][k] = 2 * c4 + key < nv ? load_once(src + key * D + 64 * q) : make_uint4(0, 0, 0, 0);
-                }
-            }
+        for (int v = v0; v < v0 + cnt; ++v, ++j) {
+            issue();
+            copies_left<ST - 1>();
+            if (v < kSmallStart) continue;  // (units that stand for the span's start)
+            bad |= bad_units >> (j & 63) & 1;
+            const int key0 = s.key0 + (v - kSmallStart) * kUnit, nv = s.key_end - key0;
+            const uint8_t *stage = mine + (j % ST) * R::kPieces * 512;
+            auto piece = [&](int i) { return *reinterpret_cast<const uint4 *>(stage + i * 512); };
             float sc[2][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int z = 0; z < 2; ++z)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) sc[j][k] = 0.f;
+                for (int k = 0; k < 4; ++k) sc[z][k] = 0.f;
 #pragma unroll
             for (int q = 0; q < C; ++q) {
-                const uint4 q0 = sq[2 * q][lane], q8 = sq[2 * q + 1][lane];
-                const uint32_t lo[4] = {q0.x, q8.x, q0.y, q8.y}, hi[4] = {q0.z, q8.z, q0.w, q8.w};
+                const uint32_t lo[4] = {qr[q][0].x, qr[q][1].x, qr[q][0].y, qr[q][1].y};
+                const uint32_t hi[4] = {qr[q][0].z, qr[q][1].z, qr[q][0].w, qr[q][1].w};
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    mma16816(sc[j], lo, kr[q][j].x, kr[q][j].y);
-                    mma16816(sc[j], hi, kr[q][j].z, kr[q][j].w);
+                for (int z = 0; z < 2; ++z) {
+                    const uint4 k = piece(2 * q + z);
+                    mma16816(sc[z], lo, k.x, k.y);
+                    mma16816(sc[z], hi, k.z, k.w);
                 }
-            }
-            if (i + 1 < n) {
-                if (((i + 1) & 31) == 0) look_up(i + 1);
-                at = __shfl_sync(0xffffffffu, place, (i + 1) & 31);
-                load_k(i + 1, at);
             }
             float mx[2] = {-INFINITY, -INFINITY}, mu[2];
             const bool open = key0 + kUnit - 1 <= min(see[0], see[1]) && nv >= kUnit;
             if (__all_sync(0xffffffffu, open)) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int z = 0; z < 2; ++z)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mx[k >> 1] = fmaxf(mx[k >> 1], sc[j][k]);
+                    for (int k = 0; k < 4; ++k) mx[k >> 1] = fmaxf(mx[k >> 1], sc[z][k]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int z = 0; z < 2; ++z)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int key = j * 8 + 2 * c4 + (k & 1);
-                        if (key >= nv || key0 + key > see[k >> 1]) sc[j][k] = -INFINITY;
-                        mx[k >> 1] = fmaxf(mx[k >> 1], sc[j][k]);
+                        const int key = z * 8 + 2 * c4 + (k & 1);
+                        if (key >= nv || key0 + key > see[k >> 1]) sc[z][k] = -INFINITY;
+                        mx[k >> 1] = fmaxf(mx[k >> 1], sc[z][k]);
                     }
             }
 #pragma unroll
@@ -426,37 +468,44 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas) stream_kernel(
 #pragma unroll
                     for (int q = 0; q < O; ++q)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            o[q][j][2 * h] *= r;
-                            o[q][j][2 * h + 1] *= r;
+                        for (int k = 0; k < 8; ++k) {
+                            o[q][k][2 * h] *= r;
+                            o[q][k][2 * h + 1] *= r;
                         }
                 }
             }
             mu[0] = m[0] == -INFINITY ? 0.f : m[0];
             mu[1] = m[1] == -INFINITY ? 0.f : m[1];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int z = 0; z < 2; ++z)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    sc[j][k] = fast_exp2(fmaf(sc[j][k], a.scale_log2, -mu[k >> 1]));
-                    l[k >> 1] += sc[j][k];
+                    sc[z][k] = fast_exp2(fmaf(sc[z][k], a.scale_log2, -mu[k >> 1]));
+                    l[k >> 1] += sc[z][k];
                 }
             const uint32_t pa[4] = {pack_bf16(sc[0][0], sc[0][1]), pack_bf16(sc[0][2], sc[0][3]),
                                     pack_bf16(sc[1][0], sc[1][1]), pack_bf16(sc[1][2], sc[1][3])};
 #pragma unroll
             for (int q = 0; q < O; ++q) {
-                const uint32_t *v0 = &vr[q][0].x, *v1 = &vr[q][1].x, *v8 = &vr[q][2].x, *v9 = &vr[q][3].x;
+                const uint4 p0 = piece(2 * C + 4 * q), p1 = piece(2 * C + 4 * q + 1), p8 = piece(2 * C + 4 * q + 2),
+                            p9 = piece(2 * C + 4 * q + 3);
+                const uint32_t x0[4] = {p0.x, p0.y, p0.z, p0.w}, x1[4] = {p1.x, p1.y, p1.z, p1.w},
+                               x8[4] = {p8.x, p8.y, p8.z, p8.w}, x9[4] = {p9.x, p9.y, p9.z, p9.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    mma16816(o[q][2 * j], pa, __byte_perm(v0[j], v1[j], 0x5410), __byte_perm(v8[j], v9[j], 0x5410));
-                    mma16816(o[q][2 * j + 1], pa, __byte_perm(v0[j], v1[j], 0x7632), __byte_perm(v8[j], v9[j], 0x7632));
+                for (int k = 0; k < 4; ++k) {
+                    mma16816(o[q][2 * k], pa, __byte_perm(x0[k], x1[k], 0x5410), __byte_perm(x8[k], x9[k], 0x5410));
+                    mma16816(o[q][2 * k + 1], pa, __byte_perm(x0[k], x1[k], 0x7632), __byte_perm(x8[k], x9[k], 0x7632));
                 }
             }
         }
         // ---- the part's sums ----
-        bad = __any_sync(0xffffffffu, bad);
+        if (v0 + cnt <= kSmallStart) continue;  // (it had no keys)
         if (bad && lane == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-        const size_t slot = ((size_t)w * Hkv + hk + gw) * kSmallRows;
+        if (lane == 0) {
+            if (v0 <= kSmallStart) x.small_first[e] = gw;
+            if (v0 + cnt == T) x.small_last[e] = gw;
+        }
+        const size_t slot = ((size_t)e + gw) * kSmallRows;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -469,122 +518,124 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas) stream_kernel(
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int j = 0; j < 8; j += 4)
-                        *reinterpret_cast<float4 *>(dst + 64 * q + 8 * k + j) =
-                            make_float4(o[q][j][2 * h + k], o[q][j + 1][2 * h + k], o[q][j + 2][2 * h + k],
-                                        o[q][j + 3][2 * h + k]);
+                    for (int z = 0; z < 8; z += 4)
+                        *reinterpret_cast<float4 *>(dst + 64 * q + 8 * k + z) =
+                            make_float4(o[q][z][2 * h + k], o[q][z + 1][2 * h + k], o[q][z + 2][2 * h + k],
+                                        o[q][z + 3][2 * h + k]);
             if (c4 == 0) x.small_ml[slot + r] = make_float2(m[h], bad ? -1.f : l[h]);
         }
-        u += n;
-        if (hk == Hkv - 1 && i0 + n == T) ++w;
     }
+    copies_left<0>();
 }
 
 // ----------------------------------------------------------------------------
 // merge
 // ----------------------------------------------------------------------------
-// W warps to a row, every W-th part each: one where there are rows enough, more where few
-// rows have many parts.
-constexpr int kMergeWarps = 16;
+// A CTA takes up to kMergeRows rows of a sequence's own span on a kv head, whose parts and
+// whose group's it looks up once; W warps to a row, every W-th part each, where rows are
+// few (they have many parts then).
+constexpr int kMergeWarps = 8, kMergeRows = 32;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_spans_kernel(SharedArgs x, int W) {
+__global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_spans_kernel(SharedArgs x) {
     constexpr int V = D / 32, U = 4;
     __shared__ float s_acc[kMergeWarps][D], s_m[kMergeWarps], s_l[kMergeWarps];
     const Attn &a = x.a;
     after_previous();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W, G = a.G, Hkv = a.c.Hkv;
-    const long long row = (long long)blockIdx.x * (kMergeWarps / W) + warp / W;
-    float M = -INFINITY, L = 0.f, acc[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.f;
-    bool bad = false, live = row < (long long)a.c.total * a.Hq;
-    if (live) {
-        const int t = (int)(row / a.Hq), h = (int)(row - (long long)t * a.Hq), hk = h / G, gh = h - hk * G;
-        const int b = a.c.seq_of_row(t, lane);
-        Seq s;
-        const int own = x.own[b];
-        const int4 info = x.info[b];
-        live = a.c.seq(b, s) == kSeqOk && t >= s.row0 && t < s.row0 + s.n && own >= 0;
-        if (live) {
-            const int r = (t - s.row0) * G + gh;
-            // the parts of row `at` of the spans from `first` on: those of the runs [total c /
-            // runs, total (c + 1) / runs) that the span's units on this kv head lie in
-            auto add = [&](bool big, int first, int at) {
-                const int rows = big ? kJobRows : kSmallRows, w = first + at / rows;
-                const long long *off = big ? a.off_big : x.off_small;
-                const long long total = off[a.n_spans[big ? 0 : 1]], u0 = off[w], T = (off[w + 1] - u0) / Hkv;
-                const long long most = big ? total : (total + kMinUnits - 1) / kMinUnits;
-                const long long runs = min(most, (long long)(big ? a.ctas : x.warps)), u = u0 + hk * T;
-                const int c0 = (int)(((u + 1) * runs - 1) / total), c1 = (int)(((u + T) * runs - 1) / total);
-                const float *o = big ? a.part_o : x.small_o;
-                const float2 *ml = big ? a.part_ml : x.small_ml;
-                const size_t p0 = ((size_t)w * Hkv + hk) * rows + at % rows;
-                for (int c = c0 + part; c <= c1; c += W * U) {
-                    float2 z[U];
-                    float v[U][V];
-#pragma unroll
-                    for (int j = 0; j < U; ++j) {
-                        z[j] = make_float2(-INFINITY, 0.f);
-                        if (c + W * j <= c1) {
-                            const size_t p = p0 + (size_t)(c + W * j) * rows;
-                            z[j] = ml[p];
-#pragma unroll
-                            for (int k = 0; k < V; k += 2)
-                                *reinterpret_cast<float2 *>(&v[j][k]) =
-                                    *reinterpret_cast<const float2 *>(o + p * D + lane * V + k);
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < U; ++j) {
-                        bad |= z[j].y < 0.f;
-                        if (z[j].y == 0.f) continue;  // no part, or one without a key for this row
-                        const float mn = fmaxf(M, z[j].x), ref = mn == -INFINITY ? 0.f : mn;
-                        const float f = mma::fast_exp2(M - ref), g = mma::fast_exp2(z[j].x - ref);
-                        M = mn;
-                        L = fmaf(z[j].y, g, L * f);
-#pragma unroll
-                        for (int k = 0; k < V; ++k) acc[k] = fmaf(v[j][k], g, acc[k] * f);
-                    }
-                }
-            };
-            if (info.x > 0) add(info.w != 0, info.z, info.y + r);
-            add(a.chunk, own, r);
-        }
-    }
-    if (W > 1) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
-        if (lane == 0) {
-            s_m[warp] = M;
-            s_l[warp] = bad ? -1.f : L;
-        }
-        __syncthreads();
-        if (!live || part) return;
-        M = -INFINITY;
-        L = 0.f;
-        bad = false;
-        for (int w = warp; w < warp + W; ++w) {
-            M = fmaxf(M, s_m[w]);
-            bad |= s_l[w] < 0.f;
-        }
-        const float ref = M == -INFINITY ? 0.f : M;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.G, Hkv = a.c.Hkv;
+    const bool chunk = a.chunk;
+    const int4 n = *reinterpret_cast<const int4 *>(a.n_spans);
+    const int w = (int)blockIdx.x / Hkv + (chunk ? n.z : n.w), hk = blockIdx.x % Hkv;
+    if (w >= (chunk ? n.x : n.y)) return;
+    const Span s = (chunk ? a.tiles_big : x.tiles_small)[w];
+    const int r0 = blockIdx.y * kMergeRows, rows = min(s.nrows - r0, kMergeRows);
+    if (rows <= 0) return;
+    const int4 info = x.info[s.b];
+    const int W = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8, part = warp % W;
+    for (int ri = warp / W; ri < (W > 1 ? kMergeWarps / W : rows); ri += kMergeWarps / W) {
+        const bool live = ri < rows;
+        const int row = s.row0 + r0 + ri;
+        float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[k] = 0.f;
-        for (int w = warp; w < warp + W; ++w) {
-            const float f = mma::fast_exp2(s_m[w] - ref);
-            L = fmaf(s_l[w], f, L);
+        bool bad = false;
+        // the parts of row r of span e / Hkv on kv head e % Hkv
+        auto add = [&](bool big, int e, int r) {
+            const int slots = big ? kJobRows : kSmallRows;
+            const int c0 = max((big ? a.c_first : x.small_first)[e], 0);
+            const int c1 = min((big ? a.c_last : x.small_last)[e], (big ? a.ctas : x.warps) - 1);
+            const float *o = big ? a.part_o : x.small_o;
+            const float2 *ml = big ? a.part_ml : x.small_ml;
+            for (int c = c0 + part; c <= c1; c += W * U) {
+                float2 z[U];
+                float v[U][V];
 #pragma unroll
-            for (int k = 0; k < V; ++k) acc[k] = fmaf(s_acc[w][lane * V + k], f, acc[k]);
+                for (int j = 0; j < U; ++j) {
+                    z[j] = make_float2(-INFINITY, 0.f);
+                    if (c + W * j <= c1) {
+                        const size_t p = ((size_t)e + c + W * j) * slots + r;
+                        z[j] = ml[p];
+#pragma unroll
+                        for (int k = 0; k < V; k += 2)
+                            *reinterpret_cast<float2 *>(&v[j][k]) =
+                                *reinterpret_cast<const float2 *>(o + p * D + lane * V + k);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    bad |= z[j].y < 0.f;
+                    if (z[j].y == 0.f) continue;  // no part, or one without a key for this row
+                    const float mn = fmaxf(M, z[j].x), ref = mn == -INFINITY ? 0.f : mn;
+                    const float f = mma::fast_exp2(M - ref), g = mma::fast_exp2(z[j].x - ref);
+                    M = mn;
+                    L = fmaf(z[j].y, g, L * f);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[k] = fmaf(v[j][k], g, acc[k] * f);
+                }
+            }
+        };
+        if (live) {
+            if (info.x > 0) {
+                const int at = row - info.y, tile = info.w ? kJobRows : kSmallRows;
+                add(info.w != 0, (info.z + at / tile) * Hkv + hk, at % tile);
+            }
+            add(chunk, w * Hkv + hk, r0 + ri);
         }
-    }
-    if (!live) return;
-    const float inv = 1.f / L;
+        if (W > 1) {  // (one round: every warp is here)
 #pragma unroll
-    for (int k = 0; k < V; k += 2)
-        *reinterpret_cast<uint32_t *>(a.out + (size_t)row * D + lane * V + k) =
-            bad ? 0u : mma::pack_bf16(acc[k] * inv, acc[k + 1] * inv);
-    if (lane == 0) a.lse[row] = bad ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+            for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
+            if (lane == 0) {
+                s_m[warp] = M;
+                s_l[warp] = bad ? -1.f : L;
+            }
+            __syncthreads();
+            if (!live || part) return;
+            M = -INFINITY;
+            L = 0.f;
+            bad = false;
+            for (int i = warp; i < warp + W; ++i) {
+                M = fmaxf(M, s_m[i]);
+                bad |= s_l[i] < 0.f;
+            }
+            const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] = 0.f;
+            for (int i = warp; i < warp + W; ++i) {
+                const float f = mma::fast_exp2(s_m[i] - ref);
+                L = fmaf(s_l[i], f, L);
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[k] = fmaf(s_acc[i][lane * V + k], f, acc[k]);
+            }
+        }
+        const int t = row / G;
+        const size_t at = (size_t)t * a.Hq + hk * G + (row - t * G);
+        const float inv = 1.f / L;
+#pragma unroll
+        for (int k = 0; k < V; k += 2)
+            *reinterpret_cast<uint32_t *>(a.out + at * D + lane * V + k) =
+                bad ? 0u : mma::pack_bf16(acc[k] * inv, acc[k + 1] * inv);
+        if (lane == 0) a.lse[at] = bad ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+    }
 }
 
 // ----------------------------------------------------------------------------
@@ -599,7 +650,7 @@ size_t scratch(SharedArgs *x, void *base) {
     };
     Attn &a = x->a;
     const size_t ns = a.c.num_seqs, ng = x->n_groups, nb = x->cap_big, nm = x->cap_small;
-    a.n_spans = static_cast<int *>(take(8));
+    a.n_spans = static_cast<int *>(take(16));
     a.tiles_big = static_cast<Span *>(take(sizeof(Span) * nb));
     a.off_big = static_cast<long long *>(take(8 * (nb + 1)));
     x->tiles_small = static_cast<Span *>(take(sizeof(Span) * nm));
@@ -607,7 +658,10 @@ size_t scratch(SharedArgs *x, void *base) {
     x->rep = static_cast<int *>(take(4 * ng));
     x->at = static_cast<int *>(take(4 * ng));
     x->info = static_cast<int4 *>(take(sizeof(int4) * ns));
-    x->own = static_cast<int *>(take(4 * ns));
+    a.c_first = static_cast<int *>(take(4 * nb * a.c.Hkv));
+    a.c_last = static_cast<int *>(take(4 * nb * a.c.Hkv));
+    x->small_first = static_cast<int *>(take(4 * nm * a.c.Hkv));
+    x->small_last = static_cast<int *>(take(4 * nm * a.c.Hkv));
     const size_t big = nb ? (nb * a.c.Hkv + a.ctas) * kJobRows : 0;
     a.part_ml = static_cast<float2 *>(take(sizeof(float2) * big));
     a.part_o = static_cast<float *>(take(sizeof(float) * big * a.D));
@@ -637,6 +691,7 @@ int make_shared(SharedArgs *x, int Hq, int D, int n_groups) {
     const long long big = groups && rows > x->small_rows ? rows / kJobRows + groups : 0;
     const long long nb = big + (a.chunk ? own : 0), nm = a.chunk ? 0 : own + groups;
     if (nb * a.c.Hkv >= (1ll << 30) || nm * a.c.Hkv >= (1ll << 30)) return MOBA_ERR_UNSUPPORTED;
+    x->own_cap = (int)own;
     x->cap_big = (int)nb;
     x->cap_small = (int)nm;
     return MOBA_OK;
@@ -644,24 +699,26 @@ int make_shared(SharedArgs *x, int Hq, int D, int n_groups) {
 
 cudaError_t launch_plan(const SharedArgs &x, cudaStream_t st) {
     note_launches(1);
-    if (x.a.c.num_seqs <= kHeld && x.n_groups <= kHeld) plan_spans_kernel<true><<<1, kPlanThreads, 0, st>>>(x);
-    else plan_spans_kernel<false><<<1, kPlanThreads, 0, st>>>(x);
+    const int most = x.a.c.num_seqs > x.n_groups ? x.a.c.num_seqs : x.n_groups;
+    if (most <= 128) plan_spans_kernel<128, true><<<1, 128, 0, st>>>(x);
+    else if (most <= kHeld) plan_spans_kernel<1024, true><<<1, 1024, 0, st>>>(x);
+    else plan_spans_kernel<1024, false><<<1, 1024, 0, st>>>(x);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_small(const SharedArgs &x, cudaStream_t st) {
+    const cudaError_t rc = allow_smem<stream_kernel<D>>(Ring<D>::kBytes);
+    if (rc != cudaSuccess) return rc;
     note_launches(1);
-    return launch_after(stream_kernel<D>, dim3(x.warps / kStreamWarps), dim3(32 * kStreamWarps), 0, st, x);
+    return launch_after(stream_kernel<D>, dim3(x.warps / kStreamWarps), dim3(32 * kStreamWarps), Ring<D>::kBytes, st, x);
 }
 
 template <int D>
 cudaError_t launch_merge(const SharedArgs &x, cudaStream_t st) {
-    const long long rows = (long long)x.a.c.total * x.a.Hq;
-    const int W = rows <= 2 * x.a.ctas ? 16 : rows <= 32 * x.a.ctas ? 4 : 1;
-    const long long ctas = (rows * W + kMergeWarps - 1) / kMergeWarps;
     note_launches(1);
-    return launch_after(merge_spans_kernel<D>, dim3((unsigned)ctas), dim3(32 * kMergeWarps), 0, st, x, W);
+    return launch_after(merge_spans_kernel<D>, dim3((unsigned)(x.own_cap * x.a.c.Hkv), x.a.chunk ? kJobRows / kMergeRows : 1),
+                        dim3(32 * kMergeWarps), 0, st, x);
 }
 
 }  // namespace
