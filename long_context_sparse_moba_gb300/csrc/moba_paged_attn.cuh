@@ -55,7 +55,7 @@ struct Attn {
     // ---- shared prefixes: jobs that are tiles of rows with a range of keys ----
     Span *tiles_big;            // [...] 256 rows at most, for the tcgen05 kernel
     long long *off_big;         // [... + 1] key tiles before each (and kBigStart), times the kv heads
-    int *n_spans;               // [4] how many of them, and of the streamed ones; of groups among each
+    int *n_spans;               // [5] how many of them, and of the streamed ones; of groups among each; runs taken
     int *c_first;               // [... * Hkv] the CTAs in whose runs the span on the kv head lies, to c_last
     // ---- chunks of many rows (the tcgen05 kernel): jobs of up to 256 rows ----
     bool chunk;

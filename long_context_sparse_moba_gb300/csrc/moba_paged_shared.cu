@@ -29,11 +29,15 @@ namespace {
 constexpr int kSmallRows = 16;   // of a small span
 constexpr int kUnit = 16;        // keys that a warp takes at a time: never more than a page
 constexpr int kBigKeys = 128;    // of a key tile of the tcgen05 kernel
-constexpr int kStreamWarps = 4, kStreamCtas = 2;  // of a CTA, of an SM
+constexpr int kStreamWarps = 4, kStreamCtas = 3;  // of a CTA, of an SM
 constexpr int kMinUnits = 6;     // units of a warp's run at least, where there are few
 // The start of a span on a kv head counts as that many units, its rows and sums being
 // what they cost: runs of equal units then take equal time.
 constexpr int kSmallStart = 2;
+// From kDynamic units a warp on, a quarter of them is cut into runs (kShort a warp) that the
+// warps take as they become free: SMs differ, by their distance from the memory, in what
+// they get through (160 K to 210 K cycles of equal runs).
+constexpr int kDynamic = 24, kShort = 2;
 
 struct SharedArgs {
     Attn a;
@@ -51,9 +55,9 @@ struct SharedArgs {
     int *rep;                    // [n_groups] the sequence whose pages are read (num_seqs: none, -1: a wrong group)
     int *at;                     // [n_groups] its first span << 1 | big, or -1
     int4 *info;                  // [num_seqs] tokens shared, the group's first row, its first span, big
-    int *small_first, *small_last;  // [cap_small * Hkv] the warps in whose runs the span on the kv head lies
-    float *small_o;              // [cap_small * Hkv + warps][kSmallRows][D] partial sums, as part_o
-    float2 *small_ml;            // [cap_small * Hkv + warps][kSmallRows]
+    int *small_first, *small_last;  // [cap_small * Hkv] the runs that the span on the kv head lies in
+    float *small_o;              // [cap_small * Hkv + runs][kSmallRows][D] partial sums, as part_o
+    float2 *small_ml;            // [cap_small * Hkv + runs][kSmallRows]
 };
 
 // ----------------------------------------------------------------------------
@@ -267,6 +271,7 @@ __global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
         // spans, and those of groups among them
         *reinterpret_cast<int4 *>(a.n_spans) = make_int4((int)min(nb, (long long)x.cap_big), (int)min(nm, (long long)x.cap_small),
                                                          groups_spans[0], groups_spans[1]);
+        a.n_spans[4] = 0;
         a.off_big[0] = x.off_small[0] = 0;
     }
 }
@@ -275,257 +280,289 @@ __global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
 // small spans
 // ----------------------------------------------------------------------------
 // The units (16 keys of a span on a kv head) of all spans form one sequence that is cut
-// into equal runs, one per warp.  A warp works alone: it copies K and V by 16 bytes a lane
-// into a ring of stages that no other warp sees, and a lane reads back only what it copied
-// itself, so that nothing is shared and there is no barrier; a span that ends costs its
-// partial sums and no more, and the copies run ahead over it.  For that the products take
-// their dimensions in an order of their own: of 32 dimensions, a lane's 16 bytes (8 of
-// them) are its two pairs of two steps of q k; of 64, they are one column of each of
+// into runs, one per warp.  A warp works alone: it brings K and V (boxes of 16 keys) into
+// a ring of its own and there is no barrier among warps; a span that ends costs its
+// partial sums and no more, and the copies run ahead over it.  A lane takes K and V from
+// the ring 16 bytes at a time, straight into the registers of its fragments.  For that
+// the products take their dimensions in an order of their own: of 64 dimensions, a lane's
+// 16 neighbours are its pairs of four steps of q k, and 8 neighbours one column of each of
 // eight steps of p v, whose pairs are two keys' values.
-// Bound: HBM.
+// Bound: HBM.  16 rows with 16384 keys on 32 kv heads and 16 times up to 2000 more, 541 MB:
+// 88 us, 6.15 TB/s, 0.91 of the copy rate.  (By cp.async, 16 bytes a lane in requests of 64
+// bytes, it took 105 us, whatever the warps and stages.)
 template <int D>
 struct Ring {
     static constexpr int C = D / 32, O = D / 64;
-    static constexpr int kPieces = 2 * C + 4 * O;  // 16 bytes a lane: K, then V
-    static constexpr int kStages = 3 * 128 / D;
-    static constexpr int kWarpBytes = kStages * kPieces * 512;
-    static constexpr int kBytes = kStreamWarps * kWarpBytes;
+    static constexpr int kBox = kUnit * 128;       // 64 dimensions of the keys, 128-byte swizzle
+    static constexpr int kStage = 2 * O * kBox;    // K, then V
+    static constexpr int kStages = 2 * 128 / D;
+    static constexpr int kBytes = kStreamWarps * kStages * kStage + 1024;
 };
 
-template <int N>
-__device__ __forceinline__ void copies_left() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <int D>
-__global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas) stream_kernel(SharedArgs x) {
+__global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
+    stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                  const __grid_constant__ SharedArgs x) {
     using mma::fast_exp2;
     using mma::mma16816;
     using mma::pack_bf16;
     using R = Ring<D>;
     constexpr int C = R::C, O = R::O, ST = R::kStages;
-    extern __shared__ __align__(128) uint8_t s_ring[];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) unsigned long long s_bar[kStreamWarps][ST];
+    __shared__ int s_abort;
     const Attn &a = x.a;
     const Cache &c = a.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n8 = lane >> 2, c4 = lane & 3;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStreamWarps; ++i)
+            for (int s = 0; s < ST; ++s) ptx::mbar_init(ptx::saddr(&s_bar[i][s]), 1);
+        s_abort = 0;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
     after_previous();
     let_next();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n8 = lane >> 2, c4 = lane & 3;
+    ptx::Ctl ctl{&s_abort, a.status, kDefaultWaitLimit};
+    const uint32_t raw = ptx::saddr(smem_raw), base = (raw + 1023u) & ~1023u;
+    const uint32_t ring = base + warp * ST * R::kStage, bars = ptx::saddr(&s_bar[warp][0]);
+    const uint8_t *mine = smem_raw + (ring - raw);
     const int gw = blockIdx.x * kStreamWarps + warp, G = a.G, Hkv = c.Hkv, ps = c.ps;
     const int spans = a.n_spans[1];
-    const long long total = x.off_small[spans];
-    const long long most = (total + kMinUnits - 1) / kMinUnits, runs = most < x.warps ? most : x.warps;
-    if (gw >= runs) return;
-    const long long u0 = total * gw / runs;
-    const int n = (int)(total * (gw + 1) / runs - u0);
-    int w = 0;  // the span with unit u0: the last that starts at or before it
-    for (int k = spans; k > 1;) {
-        const int step = (k + 31) / 32;
-        const bool below = lane * step < k && x.off_small[w + lane * step] <= u0;
-        const int last = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
-        k = min(step, k - last * step);
-        w += last * step;
-    }
-    uint8_t *mine = s_ring + warp * R::kWarpBytes + lane * 16;  // the lane's place of piece 0 of stage 0
-    const uint32_t ring = ptx::saddr(mine);
-    // ---- copies ----
-    int ahead = 0, wa = w;              // units of the run that have been issued; a span at or before the next
-    int place = 0, keys = 0;            // lane: its unit of the 32 at hand: first row of the pools, keys (0: none)
-    unsigned long long bad_units = 0;   // of the last 64 units
-    auto look_up = [&] {
-        int wl = wa;
-        bool bad = false;
-        keys = 0;
-        if (ahead + lane < n) {
-            const long long u = u0 + ahead + lane;
-            while (x.off_small[wl + 1] <= u) ++wl;
-            const Span s = x.tiles_small[wl];
-            const long long o = x.off_small[wl], T = (x.off_small[wl + 1] - o) / Hkv;
-            const int hk = (int)((u - o) / T), i = (int)(u - o - hk * T) - kSmallStart;
-            if (i >= 0) {
-                const int key = s.key0 + i * kUnit;
-                const int page = __ldg(c.table + (size_t)s.b * c.max_pages + (key >> x.psh));
-                bad = (unsigned)page >= (unsigned)c.num_pages;
-                // (some memory of the pool for a page outside it: its rows are dropped)
-                place = (((bad ? 0 : page) * Hkv + hk) << x.psh) + (key & (ps - 1));
-                keys = min(s.key_end - key, kUnit);
-            }
+    const long long total = x.off_small[spans], most = (total + kMinUnits - 1) / kMinUnits;
+    const bool dynamic = total > (long long)x.warps * kDynamic;
+    const long long even = dynamic ? total - total / 4 : total;  // units of the runs that are one for each warp
+    const int runs = dynamic ? x.warps * (1 + kShort) : (int)(most < x.warps ? most : x.warps);
+    int issued = 0, used = 0;  // stages so far
+    for (int run = gw, next = 0; run < runs; run = next) {
+        if (dynamic && lane == 0) next = atomicAdd(a.n_spans + 4, 1);
+        const long long firsts = dynamic ? x.warps : runs;
+        auto begin = [&](int r) {
+            return r <= firsts ? even * r / firsts : even + (total - even) * (r - firsts) / (x.warps * kShort);
+        };
+        const long long u0 = begin(run);
+        const int n = (int)(begin(run + 1) - u0);
+        int w = 0;  // the span with unit u0: the last that starts at or before it
+        for (int k = spans; k > 1;) {
+            const int step = (k + 31) / 32;
+            const bool below = lane * step < k && x.off_small[w + lane * step] <= u0;
+            const int last = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
+            k = min(step, k - last * step);
+            w += last * step;
         }
-        const unsigned long long ballot = __ballot_sync(0xffffffffu, bad);
-        const int at = ahead & 63;
-        bad_units = (bad_units & ~(0xffffffffull << at)) | ballot << at;
-        wa = __shfl_sync(0xffffffffu, wl, min(31, n - 1 - ahead));
-    };
-    auto issue = [&] {
-        if (ahead < n) {
-            if ((ahead & 31) == 0) look_up();
-            const int at = __shfl_sync(0xffffffffu, place, ahead & 31), nv = __shfl_sync(0xffffffffu, keys, ahead & 31);
-            if (nv > 0) {
-                // (keys that no row sees may never have been written: zeros)
-                const uint32_t dst = ring + (ahead % ST) * R::kPieces * 512;
-                const __nv_bfloat16 *k = a.k + ((size_t)at + n8) * D + 8 * c4;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int q = 0; q < C; ++q)
-                        ptx::cp_async16(dst + (2 * q + j) * 512, k + 8 * j * D + 32 * q, n8 + 8 * j < nv);
-                const __nv_bfloat16 *v = a.v + ((size_t)at + 2 * c4) * D + 8 * n8;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int q = 0; q < O; ++q) {
-                        const int key = (j & 1) + 8 * (j >> 1);
-                        ptx::cp_async16(dst + (2 * C + 4 * q + j) * 512, v + key * D + 64 * q, 2 * c4 + key < nv);
-                    }
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        ++ahead;
-    };
-#pragma unroll 1
-    for (int i = 0; i < ST - 1; ++i) issue();
-    // ---- parts: the run's units of one span on one kv head ----
-    for (int j = 0; j < n;) {
-        while (x.off_small[w + 1] <= u0 + j) ++w;
-        const Span s = x.tiles_small[w];
-        const long long in = u0 + j - x.off_small[w], T = (x.off_small[w + 1] - x.off_small[w]) / Hkv;
-        const int hk = (int)(in / T), v0 = (int)(in - hk * T), cnt = (int)min(T - v0, (long long)(n - j));
-        const int e = w * Hkv + hk;
-        // this lane's rows, n8 and n8 + 8
-        int see[2];
-        uint4 qr[C][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = n8 + 8 * h, row = s.row0 + r, t = row / G;
-            const bool live = r < s.nrows;
-            // last key that the row sees (no row: whatever, its scores do not matter)
-            see[h] = live && !s.full ? t + s.pdelta : 0x7fffffff;
-            const __nv_bfloat16 *src = a.q + ((size_t)t * a.Hq + hk * G + (row - t * G)) * D + 8 * c4;
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-                qr[i][h] = live ? __ldg(reinterpret_cast<const uint4 *>(src + 32 * i)) : make_uint4(0, 0, 0, 0);
-        }
-        float o[O][8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < O; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) o[i][k][z] = 0.f;
-        bool bad = false;
-        for (int v = v0; v < v0 + cnt; ++v, ++j) {
-            issue();
-            copies_left<ST - 1>();
-            if (v < kSmallStart) continue;  // (units that stand for the span's start)
-            bad |= bad_units >> (j & 63) & 1;
-            const int key0 = s.key0 + (v - kSmallStart) * kUnit, nv = s.key_end - key0;
-            const uint8_t *stage = mine + (j % ST) * R::kPieces * 512;
-            auto piece = [&](int i) { return *reinterpret_cast<const uint4 *>(stage + i * 512); };
-            float sc[2][4];
-#pragma unroll
-            for (int z = 0; z < 2; ++z)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sc[z][k] = 0.f;
-#pragma unroll
-            for (int q = 0; q < C; ++q) {
-                const uint32_t lo[4] = {qr[q][0].x, qr[q][1].x, qr[q][0].y, qr[q][1].y};
-                const uint32_t hi[4] = {qr[q][0].z, qr[q][1].z, qr[q][0].w, qr[q][1].w};
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const uint4 k = piece(2 * q + z);
-                    mma16816(sc[z], lo, k.x, k.y);
-                    mma16816(sc[z], hi, k.z, k.w);
+        // ---- copies ----
+        int ahead = 0, wa = w;              // units of the run that have been issued; a span at or before the next
+        int place = 0;                      // lane: its unit of the 32 at hand: first row of the pools (-1: no keys)
+        unsigned long long bad_units = 0;   // of the last 64 units
+        auto look_up = [&] {
+            int wl = wa;
+            bool bad = false;
+            place = -1;
+            if (ahead + lane < n) {
+                const long long u = u0 + ahead + lane;
+                while (x.off_small[wl + 1] <= u) ++wl;
+                const Span s = x.tiles_small[wl];
+                const long long o = x.off_small[wl], T = (x.off_small[wl + 1] - o) / Hkv;
+                const int hk = (int)((u - o) / T), i = (int)(u - o - hk * T) - kSmallStart;
+                if (i >= 0) {
+                    const int key = s.key0 + i * kUnit;
+                    const int page = __ldg(c.table + (size_t)s.b * c.max_pages + (key >> x.psh));
+                    bad = (unsigned)page >= (unsigned)c.num_pages;
+                    // (some memory of the pool for a page outside it: its rows are dropped)
+                    place = (((bad ? 0 : page) * Hkv + hk) << x.psh) + (key & (ps - 1));
                 }
             }
-            float mx[2] = {-INFINITY, -INFINITY}, mu[2];
-            const bool open = key0 + kUnit - 1 <= min(see[0], see[1]) && nv >= kUnit;
-            if (__all_sync(0xffffffffu, open)) {
+            const unsigned long long ballot = __ballot_sync(0xffffffffu, bad);
+            const int at = ahead & 63;
+            bad_units = (bad_units & ~(0xffffffffull << at)) | ballot << at;
+            wa = __shfl_sync(0xffffffffu, wl, min(31, n - 1 - ahead));
+        };
+        auto issue = [&] {
+            if (ahead >= n) return;
+            if ((ahead & 31) == 0) look_up();
+            const int at = __shfl_sync(0xffffffffu, place, ahead & 31);
+            ++ahead;
+            if (at < 0) return;
+            if (lane == 0) {
+                const uint32_t bar = bars + 8 * (issued % ST), dst = ring + (issued % ST) * R::kStage;
+                ptx::mbar_expect_tx(bar, R::kStage);
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+#pragma unroll
+                    for (int q = 0; q < O; ++q)
+                        asm volatile(
+                            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                            "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst + (v * O + q) * R::kBox),
+                            "l"(reinterpret_cast<uint64_t>(v ? &tmap_v : &tmap_k)), "r"(bar), "r"(q * 64), "r"(at)
+                            : "memory");
+            }
+            ++issued;
+        };
+#pragma unroll 1
+        for (int i = 0; i < ST - 1; ++i) issue();
+        bool ok = true;
+        // ---- parts: the run's units of one span on one kv head ----
+        for (int j = 0; ok && j < n;) {
+            while (x.off_small[w + 1] <= u0 + j) ++w;
+            const Span s = x.tiles_small[w];
+            const long long in = u0 + j - x.off_small[w], T = (x.off_small[w + 1] - x.off_small[w]) / Hkv;
+            const int hk = (int)(in / T), v0 = (int)(in - hk * T), cnt = (int)min(T - v0, (long long)(n - j));
+            const int e = w * Hkv + hk;
+            // this lane's rows, n8 and n8 + 8
+            int see[2];
+            uint4 qr[C][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = n8 + 8 * h, row = s.row0 + r, t = row / G;
+                const bool live = r < s.nrows;
+                // last key that the row sees (no row: whatever, its scores do not matter)
+                see[h] = live && !s.full ? t + s.pdelta : 0x7fffffff;
+                const __nv_bfloat16 *src = a.q + ((size_t)t * a.Hq + hk * G + (row - t * G)) * D + 16 * c4;
+#pragma unroll
+                for (int i = 0; i < C; ++i)
+                    qr[i][h] = live ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * (i >> 1) + 8 * (i & 1)))
+                                    : make_uint4(0, 0, 0, 0);
+            }
+            float o[O][8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < O; ++i)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) o[i][k][z] = 0.f;
+            bool bad = false;
+            for (int v = v0; v < v0 + cnt; ++v, ++j) {
+                issue();
+                if (v < kSmallStart) continue;  // (units that stand for the span's start)
+                ok = __all_sync(0xffffffffu, ptx::wait_fast(bars + 8 * (used % ST), (used / ST) & 1, ctl));
+                if (!ok) break;
+                bad |= bad_units >> (j & 63) & 1;
+                const int key0 = s.key0 + (v - kSmallStart) * kUnit, nv = s.key_end - key0;
+                const uint8_t *stage = mine + (used % ST) * R::kStage;
+                ++used;
+                // 16 bytes of row r of a box (r & 7 as in the address of its swizzle)
+                auto piece = [&](int box, int r, int p) {
+                    return *reinterpret_cast<const uint4 *>(stage + box * R::kBox + r * 128 + ((p ^ (r & 7)) << 4));
+                };
+                float sc[2][4];
 #pragma unroll
                 for (int z = 0; z < 2; ++z)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mx[k >> 1] = fmaxf(mx[k >> 1], sc[z][k]);
-            } else {
+                    for (int k = 0; k < 4; ++k) sc[z][k] = 0.f;
+#pragma unroll
+                for (int q = 0; q < C; ++q) {
+                    const uint32_t lo[4] = {qr[q][0].x, qr[q][1].x, qr[q][0].y, qr[q][1].y};
+                    const uint32_t hi[4] = {qr[q][0].z, qr[q][1].z, qr[q][0].w, qr[q][1].w};
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const uint4 k = piece(q >> 1, n8 + 8 * z, 2 * c4 + (q & 1));
+                        mma16816(sc[z], lo, k.x, k.y);
+                        mma16816(sc[z], hi, k.z, k.w);
+                    }
+                }
+                float mx[2] = {-INFINITY, -INFINITY}, mu[2];
+                const bool open = key0 + kUnit - 1 <= min(see[0], see[1]) && nv >= kUnit;
+                if (__all_sync(0xffffffffu, open)) {
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mx[k >> 1] = fmaxf(mx[k >> 1], sc[z][k]);
+                } else {
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int key = z * 8 + 2 * c4 + (k & 1);
+                            if (key >= nv || key0 + key > see[k >> 1]) sc[z][k] = -INFINITY;
+                            mx[k >> 1] = fmaxf(mx[k >> 1], sc[z][k]);
+                        }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * a.scale_log2;
+                }
+                if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float mn = fmaxf(m[h], mx[h]);
+                        const float r = fast_exp2(m[h] - (mn == -INFINITY ? 0.f : mn));
+                        m[h] = mn;
+                        l[h] *= r;
+#pragma unroll
+                        for (int q = 0; q < O; ++q)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                o[q][k][2 * h] *= r;
+                                o[q][k][2 * h + 1] *= r;
+                            }
+                    }
+                }
+                mu[0] = m[0] == -INFINITY ? 0.f : m[0];
+                mu[1] = m[1] == -INFINITY ? 0.f : m[1];
 #pragma unroll
                 for (int z = 0; z < 2; ++z)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int key = z * 8 + 2 * c4 + (k & 1);
-                        if (key >= nv || key0 + key > see[k >> 1]) sc[z][k] = -INFINITY;
-                        mx[k >> 1] = fmaxf(mx[k >> 1], sc[z][k]);
+                        sc[z][k] = fast_exp2(fmaf(sc[z][k], a.scale_log2, -mu[k >> 1]));
+                        l[k >> 1] += sc[z][k];
                     }
+                const uint32_t pa[4] = {pack_bf16(sc[0][0], sc[0][1]), pack_bf16(sc[0][2], sc[0][3]),
+                                        pack_bf16(sc[1][0], sc[1][1]), pack_bf16(sc[1][2], sc[1][3])};
+#pragma unroll
+                for (int q = 0; q < O; ++q) {
+                    uint4 p[4];  // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = 2 * c4 + (k & 1) + 8 * (k >> 1);
+                        p[k] = piece(O + q, r, n8);
+                        // (keys that no row sees may never have been written: zeros)
+                        if (r >= nv) p[k] = make_uint4(0, 0, 0, 0);
+                    }
+                    const uint32_t x0[4] = {p[0].x, p[0].y, p[0].z, p[0].w}, x1[4] = {p[1].x, p[1].y, p[1].z, p[1].w},
+                                   x8[4] = {p[2].x, p[2].y, p[2].z, p[2].w}, x9[4] = {p[3].x, p[3].y, p[3].z, p[3].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        mma16816(o[q][2 * k], pa, __byte_perm(x0[k], x1[k], 0x5410), __byte_perm(x8[k], x9[k], 0x5410));
+                        mma16816(o[q][2 * k + 1], pa, __byte_perm(x0[k], x1[k], 0x7632), __byte_perm(x8[k], x9[k], 0x7632));
+                    }
+                }
+                __syncwarp();  // (the stage has been read: the next copy may go there)
             }
+            // ---- the part's sums ----
+            if (!ok) break;
+            if (v0 + cnt <= kSmallStart) continue;  // (it had no keys)
+            if (bad && lane == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+            if (lane == 0) {
+                if (v0 <= kSmallStart) x.small_first[e] = run;
+                if (v0 + cnt == T) x.small_last[e] = run;
+            }
+            const size_t slot = ((size_t)e + run) * kSmallRows;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * a.scale_log2;
-            }
-            if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+                const int r = n8 + 8 * h;
+                if (r >= s.nrows) continue;
+                float *dst = x.small_o + (slot + r) * D + 16 * c4;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float mn = fmaxf(m[h], mx[h]);
-                    const float r = fast_exp2(m[h] - (mn == -INFINITY ? 0.f : mn));
-                    m[h] = mn;
-                    l[h] *= r;
+                for (int q = 0; q < O; ++q)
 #pragma unroll
-                    for (int q = 0; q < O; ++q)
+                    for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            o[q][k][2 * h] *= r;
-                            o[q][k][2 * h + 1] *= r;
-                        }
-                }
-            }
-            mu[0] = m[0] == -INFINITY ? 0.f : m[0];
-            mu[1] = m[1] == -INFINITY ? 0.f : m[1];
-#pragma unroll
-            for (int z = 0; z < 2; ++z)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    sc[z][k] = fast_exp2(fmaf(sc[z][k], a.scale_log2, -mu[k >> 1]));
-                    l[k >> 1] += sc[z][k];
-                }
-            const uint32_t pa[4] = {pack_bf16(sc[0][0], sc[0][1]), pack_bf16(sc[0][2], sc[0][3]),
-                                    pack_bf16(sc[1][0], sc[1][1]), pack_bf16(sc[1][2], sc[1][3])};
-#pragma unroll
-            for (int q = 0; q < O; ++q) {
-                const uint4 p0 = piece(2 * C + 4 * q), p1 = piece(2 * C + 4 * q + 1), p8 = piece(2 * C + 4 * q + 2),
-                            p9 = piece(2 * C + 4 * q + 3);
-                const uint32_t x0[4] = {p0.x, p0.y, p0.z, p0.w}, x1[4] = {p1.x, p1.y, p1.z, p1.w},
-                               x8[4] = {p8.x, p8.y, p8.z, p8.w}, x9[4] = {p9.x, p9.y, p9.z, p9.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    mma16816(o[q][2 * k], pa, __byte_perm(x0[k], x1[k], 0x5410), __byte_perm(x8[k], x9[k], 0x5410));
-                    mma16816(o[q][2 * k + 1], pa, __byte_perm(x0[k], x1[k], 0x7632), __byte_perm(x8[k], x9[k], 0x7632));
-                }
+                        for (int z = 0; z < 8; z += 4)
+                            *reinterpret_cast<float4 *>(dst + 64 * q + 8 * k + z) =
+                                make_float4(o[q][z][2 * h + k], o[q][z + 1][2 * h + k], o[q][z + 2][2 * h + k],
+                                            o[q][z + 3][2 * h + k]);
+                if (c4 == 0) x.small_ml[slot + r] = make_float2(m[h], bad ? -1.f : l[h]);
             }
         }
-        // ---- the part's sums ----
-        if (v0 + cnt <= kSmallStart) continue;  // (it had no keys)
-        if (bad && lane == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-        if (lane == 0) {
-            if (v0 <= kSmallStart) x.small_first[e] = gw;
-            if (v0 + cnt == T) x.small_last[e] = gw;
+        if (!ok) {  // copies in flight land before the CTA ends
+            for (; used < issued; ++used) ptx::drain_bar(bars + 8 * (used % ST), (used / ST) & 1, kDefaultWaitLimit);
+            return;
         }
-        const size_t slot = ((size_t)e + gw) * kSmallRows;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            const int r = n8 + 8 * h;
-            if (r >= s.nrows) continue;
-            float *dst = x.small_o + (slot + r) * D + 16 * c4;
-#pragma unroll
-            for (int q = 0; q < O; ++q)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int z = 0; z < 8; z += 4)
-                        *reinterpret_cast<float4 *>(dst + 64 * q + 8 * k + z) =
-                            make_float4(o[q][z][2 * h + k], o[q][z + 1][2 * h + k], o[q][z + 2][2 * h + k],
-                                        o[q][z + 3][2 * h + k]);
-            if (c4 == 0) x.small_ml[slot + r] = make_float2(m[h], bad ? -1.f : l[h]);
-        }
+        next = dynamic ? x.warps + __shfl_sync(0xffffffffu, next, 0) : runs;
     }
-    copies_left<0>();
 }
 
 // ----------------------------------------------------------------------------
@@ -563,7 +600,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_spans_kernel(Shared
         auto add = [&](bool big, int e, int r) {
             const int slots = big ? kJobRows : kSmallRows;
             const int c0 = max((big ? a.c_first : x.small_first)[e], 0);
-            const int c1 = min((big ? a.c_last : x.small_last)[e], (big ? a.ctas : x.warps) - 1);
+            const int c1 = min((big ? a.c_last : x.small_last)[e], (big ? a.ctas : x.warps * (1 + kShort)) - 1);
             const float *o = big ? a.part_o : x.small_o;
             const float2 *ml = big ? a.part_ml : x.small_ml;
             for (int c = c0 + part; c <= c1; c += W * U) {
@@ -650,7 +687,7 @@ size_t scratch(SharedArgs *x, void *base) {
     };
     Attn &a = x->a;
     const size_t ns = a.c.num_seqs, ng = x->n_groups, nb = x->cap_big, nm = x->cap_small;
-    a.n_spans = static_cast<int *>(take(16));
+    a.n_spans = static_cast<int *>(take(32));
     a.tiles_big = static_cast<Span *>(take(sizeof(Span) * nb));
     a.off_big = static_cast<long long *>(take(8 * (nb + 1)));
     x->tiles_small = static_cast<Span *>(take(sizeof(Span) * nm));
@@ -665,7 +702,7 @@ size_t scratch(SharedArgs *x, void *base) {
     const size_t big = nb ? (nb * a.c.Hkv + a.ctas) * kJobRows : 0;
     a.part_ml = static_cast<float2 *>(take(sizeof(float2) * big));
     a.part_o = static_cast<float *>(take(sizeof(float) * big * a.D));
-    const size_t small = nm ? (nm * a.c.Hkv + x->warps) * kSmallRows : 0;
+    const size_t small = nm ? (nm * a.c.Hkv + (size_t)x->warps * (1 + kShort)) * kSmallRows : 0;
     x->small_ml = static_cast<float2 *>(take(sizeof(float2) * small));
     x->small_o = static_cast<float *>(take(sizeof(float) * small * a.D));
     return off;
@@ -708,10 +745,15 @@ cudaError_t launch_plan(const SharedArgs &x, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_small(const SharedArgs &x, cudaStream_t st) {
+    CUtensorMap mk, mv;
+    const long long rows = (long long)x.a.c.num_pages * x.a.c.Hkv * x.a.c.ps;
+    if (!make_tma_rows(&mk, x.a.k, rows, D, kUnit) || !make_tma_rows(&mv, x.a.v, rows, D, kUnit))
+        return cudaErrorInvalidValue;
     const cudaError_t rc = allow_smem<stream_kernel<D>>(Ring<D>::kBytes);
     if (rc != cudaSuccess) return rc;
     note_launches(1);
-    return launch_after(stream_kernel<D>, dim3(x.warps / kStreamWarps), dim3(32 * kStreamWarps), Ring<D>::kBytes, st, x);
+    return launch_after(stream_kernel<D>, dim3(x.warps / kStreamWarps), dim3(32 * kStreamWarps), Ring<D>::kBytes, st, mk,
+                        mv, x);
 }
 
 template <int D>
