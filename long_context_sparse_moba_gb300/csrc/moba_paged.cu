@@ -336,8 +336,8 @@ static cudaError_t launch_append(const AppendArgs &a, bool max, cudaStream_t st)
                : cudaLaunchKernelEx(&cfg, append_kernel<D, false, POOL>, a);
 }
 
-// The grid of an append whose cache and pools are set.
-static int plan_append(AppendArgs *a) {
+// The grid of an append (or of its pooling alone) whose cache and pools are set.
+static int plan_append(AppendArgs *a, bool pool) {
     const int bs = a->c.bs;
     a->psh = __builtin_ctz((unsigned)a->c.ps);
     a->cand = (int)(((long long)a->c.max_new + bs - 2) / bs + 1);
@@ -358,7 +358,7 @@ static int plan_append(AppendArgs *a) {
     // 17.9; of 256 of which three do 25.1, 18.8, 18.7, 24.1; a chunk of 65536 tokens 78,
     // 73, 75, 84, and 267, 185, 144, 117 with blocks of 64
     const double per_sm = (double)((long long)a->c.total / bs + a->c.num_seqs) * a->c.Hkv / sm_count();
-    a->ctas = per_sm * 8 <= 6 ? 8 : per_sm * 4 <= 15 ? 4 : bs >= 512 ? 2 : 1;
+    a->ctas = per_sm * 8 <= 6 ? 8 : per_sm * 4 <= (pool ? 6 : 15) ? 4 : bs >= 512 ? 2 : 1;
     return MOBA_OK;
 }
 
@@ -369,7 +369,7 @@ int make_pool(AppendArgs *a, const Cache &c, void *k_pages, float *kbar_pages, i
     a->vp = nullptr;
     a->kbar = kbar_pages;
     a->status = status;
-    return plan_append(a);
+    return plan_append(a, true);
 }
 
 cudaError_t launch_pool(const AppendArgs &a, int D, bool max, cudaStream_t st) {
@@ -406,7 +406,7 @@ MOBA_EXPORT int moba_paged_append(const void *k, const void *v, void *k_pages, v
     a.kp = static_cast<__nv_bfloat16 *>(k_pages);
     a.vp = static_cast<__nv_bfloat16 *>(v_pages);
     a.kbar = kbar_pages;
-    const int planned = plan_append(&a);
+    const int planned = plan_append(&a, false);
     if (planned != MOBA_OK) return planned;
     a.status = status_word();
     if (!a.status) return cuda_result(cudaErrorInvalidDevice);

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(32 * kWarps) write_kernel(WriteArgs a) {
     constexpr int LH = D / 16;   // lanes per head: 16 values (8 pairs) each
     constexpr int HW = 32 / LH;  // heads per warp and step
     __shared__ unsigned long long s_turn[D / 2];
-    __shared__ __align__(16) float s_w[2][D];
+    __shared__ __align__(16) float s_w[2][D], s_c[kWarps][D / 2], s_s[kWarps][D / 2];
     let_next();
     load_turns(s_turn, a.freqs, a.rot / 2, threadIdx.x, 32 * kWarps);
     for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps) {
@@ -69,15 +69,16 @@ __global__ void __launch_bounds__(32 * kWarps) write_kernel(WriteArgs a) {
     const bool turns = item < a.rot / 16;  // the other items are not rotated
     int va, vb;
     vectors<D, INTERLEAVED>(item, a.rot / 2, va, vb);
-    const long long units = (long long)a.c.total * a.splits;
-    for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units;
-         u += (long long)gridDim.x * kWarps) {
-        const int t = (int)(u / a.splits);
-        const int h0 = (int)(u % a.splits) * a.chunk, h1 = min(h0 + a.chunk, heads);
+    const int warp = threadIdx.x >> 5;
+    const unsigned units = (unsigned)a.c.total * a.splits, stride = gridDim.x * kWarps;
+    for (unsigned u = blockIdx.x * kWarps + warp; u < units; u += stride) {
+        const int t = a.splits == 1 ? u : u / a.splits, part = a.splits == 1 ? 0 : u % a.splits;
+        const int h0 = part * a.chunk, h1 = min(h0 + a.chunk, heads);
         const int b = a.c.seq_of_row(t, lane);
         Seq s;
+        const int state = a.c.seq(b, s);
         // (rows of no sequence, or of a refused one, are left as they were)
-        if (a.c.seq(b, s) != kSeqOk || t < s.row0 || t >= s.row0 + s.n) continue;
+        if (state != kSeqOk || t < s.row0 || t >= s.row0 + s.n) continue;
         const int p = s.len - s.n + t - s.row0;  // the token's place
         __nv_bfloat16 *page_k = nullptr, *page_v = nullptr;
         if (h1 > a.Hq) {
@@ -90,8 +91,14 @@ __global__ void __launch_bounds__(32 * kWarps) write_kernel(WriteArgs a) {
                 atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
             }
         }
-        float c[8], sn[8];
-        if (turns && h0 < a.Hq + Hkv) cos_sin(s_turn + item * 8, a.pos ? __ldg(a.pos + t) : p, a.mag, 1.f, c, sn);
+        float2 c[4], sn[4];
+        if (h0 < a.Hq + Hkv) {
+            warp_cos_sin(s_turn, a.rot / 2, lane, a.pos ? __ldg(a.pos + t) : p, a.mag, 1.f, s_c[warp], s_s[warp]);
+            if (turns) {
+                load_eight(s_c[warp] + item * 8, c);
+                load_eight(s_s[warp] + item * 8, sn);
+            }
+        }
 #pragma unroll 1
         for (int kind = 0; kind < 3; ++kind) {  // q, k, v
             const int base = kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + Hkv;
@@ -102,8 +109,11 @@ __global__ void __launch_bounds__(32 * kWarps) write_kernel(WriteArgs a) {
             if (!dst) continue;
             const size_t step = kind == 0 ? (size_t)D : (size_t)D << a.psh;  // between heads of dst
             const bool norm = kind == 0 ? a.wq != nullptr : kind == 1 && a.wk != nullptr;
-            float wa[8], wb[8];
-            if (norm) load_weights(s_w[kind], va, vb, wa, wb);
+            float2 wa[4], wb[4];
+            if (norm) {
+                load_eight(s_w[kind] + va, wa);
+                load_eight(s_w[kind] + vb, wb);
+            }
             for (int hb = lo; hb < hi; hb += HW * kUnroll) {
                 uint4 xa[kUnroll], xb[kUnroll];
 #pragma unroll
@@ -119,7 +129,7 @@ __global__ void __launch_bounds__(32 * kWarps) write_kernel(WriteArgs a) {
                 for (int j = 0; j < kUnroll; ++j) {
                     const int h = hb + j * HW + hsub;
                     if (kind < 2) {
-                        float fa[8], fb[8];
+                        float2 fa[4], fb[4];
                         unpack(xa[j], fa);
                         unpack(xb[j], fb);
                         if (norm) normalise<D>(fa, fb, wa, wb, a.eps);

@@ -29,6 +29,7 @@ constexpr int kUnroll = 4;      // heads whose loads a lane has in flight
 constexpr int kBwdUnroll = 2;
 constexpr int kFwdCtas = 8, kBwdCtas = 2;  // of an SM at most
 
+
 struct Side {                   // q or k
     const __nv_bfloat16 *x, *dy;  // dy: gradient only
     __nv_bfloat16 *out;
@@ -46,6 +47,7 @@ struct Args {
     int tokens, rot;
     int chunk, splits;          // heads per unit, units per token
     int w32;                    // weights are fp32 (else bf16)
+    bool wide;                  // gradient: every head of every operand is aligned to 32 bytes
     float eps, mag;
 };
 
@@ -54,7 +56,7 @@ __global__ void __launch_bounds__(32 * kWarps) fwd_kernel(Args a) {
     constexpr int LH = D / 16;   // lanes per head: 16 values (8 pairs) each
     constexpr int HW = 32 / LH;  // heads per warp and step
     __shared__ unsigned long long s_turn[D / 2];
-    __shared__ __align__(16) float s_w[2][D];
+    __shared__ __align__(16) float s_w[2][D], s_c[kWarps][D / 2], s_s[kWarps][D / 2];
     load_turns(s_turn, a.freqs, a.rot / 2, threadIdx.x, 32 * kWarps);
     for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps)
         if (i < D || a.k.heads) s_w[i / D][i % D] = weight(i < D ? a.q.w : a.k.w, a.w32, i % D);
@@ -63,20 +65,25 @@ __global__ void __launch_bounds__(32 * kWarps) fwd_kernel(Args a) {
     const bool turns = item < a.rot / 16;  // the other items are not rotated
     int va, vb;
     vectors<D, INTERLEAVED>(item, a.rot / 2, va, vb);
-    const long long units = (long long)a.tokens * a.splits;
-    for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units;
-         u += (long long)gridDim.x * kWarps) {
-        const int t = (int)(u / a.splits);
-        const int h0 = (int)(u % a.splits) * a.chunk, h1 = min(h0 + a.chunk, a.q.heads + a.k.heads);
-        float c[8], s[8];
-        if (turns) cos_sin(s_turn + item * 8, __ldg(a.pos + t), a.mag, 1.f, c, s);
+    const int warp = threadIdx.x >> 5;
+    const unsigned units = (unsigned)a.tokens * a.splits, stride = gridDim.x * kWarps;
+    for (unsigned u = blockIdx.x * kWarps + warp; u < units; u += stride) {
+        const int t = a.splits == 1 ? u : u / a.splits, part = a.splits == 1 ? 0 : u % a.splits;
+        const int h0 = part * a.chunk, h1 = min(h0 + a.chunk, a.q.heads + a.k.heads);
+        warp_cos_sin(s_turn, a.rot / 2, lane, __ldg(a.pos + t), a.mag, 1.f, s_c[warp], s_s[warp]);
+        float2 c[4], s[4];
+        if (turns) {
+            load_eight(s_c[warp] + item * 8, c);
+            load_eight(s_s[warp] + item * 8, s);
+        }
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
             const Side &x = kv ? a.k : a.q;
             const int base = kv ? a.q.heads : 0, lo = max(h0 - base, 0), hi = min(h1 - base, x.heads);
             if (lo >= hi) continue;
-            float wa[8], wb[8];
-            load_weights(s_w[kv], va, vb, wa, wb);
+            float2 wa[4], wb[4];
+            load_eight(s_w[kv] + va, wa);
+            load_eight(s_w[kv] + vb, wb);
             const __nv_bfloat16 *src = x.x + t * x.xs;
             __nv_bfloat16 *dst = x.out + t * x.os;
             for (int hb = lo; hb < hi; hb += HW * kUnroll) {
@@ -93,7 +100,7 @@ __global__ void __launch_bounds__(32 * kWarps) fwd_kernel(Args a) {
 #pragma unroll
                 for (int j = 0; j < kUnroll; ++j) {
                     const int h = hb + j * HW + hsub;
-                    float fa[8], fb[8];
+                    float2 fa[4], fb[4];
                     unpack(xa[j], fa);
                     unpack(xb[j], fb);
                     normalise<D>(fa, fb, wa, wb, a.eps);
@@ -114,8 +121,7 @@ template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
     constexpr int LH = D / 16, HW = 32 / LH;
     __shared__ unsigned long long s_turn[D / 2];
-    __shared__ __align__(16) float s_w[D];
-    __shared__ float s_sum[kWarps][D];
+    __shared__ __align__(16) float s_w[D], s_c[kWarps][D / 2], s_s[kWarps][D / 2], s_sum[kWarps][D];
     const bool is_k = (int)blockIdx.x >= a.q_ctas;
     const Side x = is_k ? a.k : a.q;
     load_turns(s_turn, a.freqs, a.rot / 2, threadIdx.x, 32 * kWarps);
@@ -126,19 +132,25 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
     const bool turns = item < a.rot / 16;
     int va, vb;
     vectors<D, INTERLEAVED>(item, a.rot / 2, va, vb);
-    float wa[8], wb[8], da[8], db[8];  // weights, and the sums of their gradients
-    load_weights(s_w, va, vb, wa, wb);
+    float2 wa[4], wb[4], da[4], db[4];  // weights, and the sums of their gradients
+    load_eight(s_w + va, wa);
+    load_eight(s_w + vb, wb);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) da[i] = db[i] = 0.f;
+    for (int i = 0; i < 4; ++i) da[i] = db[i] = make_float2(0.f, 0.f);
     const int cta = is_k ? blockIdx.x - a.q_ctas : blockIdx.x, ctas = is_k ? gridDim.x - a.q_ctas : a.q_ctas;
-    const long long units = (long long)a.tokens * x.splits;
-    for (long long u = (long long)cta * kWarps + warp; u < units; u += (long long)ctas * kWarps) {
-        const int t = (int)(u / x.splits);
-        const int lo = (int)(u % x.splits) * x.chunk, hi = min(lo + x.chunk, x.heads);
-        float c[8], s[8];
-        if (turns) cos_sin(s_turn + item * 8, __ldg(a.pos + t), a.mag, -1.f, c, s);
+    const unsigned units = (unsigned)a.tokens * x.splits, stride = ctas * kWarps;
+    for (unsigned u = cta * kWarps + warp; u < units; u += stride) {
+        const int t = x.splits == 1 ? u : u / x.splits;
+        const int lo = x.splits == 1 ? 0 : (int)(u % x.splits) * x.chunk, hi = min(lo + x.chunk, x.heads);
+        warp_cos_sin(s_turn, a.rot / 2, lane, __ldg(a.pos + t), a.mag, -1.f, s_c[warp], s_s[warp]);
+        float2 c[4], s[4];
+        if (turns) {
+            load_eight(s_c[warp] + item * 8, c);
+            load_eight(s_s[warp] + item * 8, s);
+        }
         const __nv_bfloat16 *src = x.x + t * x.xs, *up = x.dy + t * x.ds;
         __nv_bfloat16 *dst = x.out + t * x.os;
+#pragma unroll 1
         for (int hb = lo; hb < hi; hb += HW * kBwdUnroll) {
             uint4 xa[kBwdUnroll], xb[kBwdUnroll], ya[kBwdUnroll], yb[kBwdUnroll];
 #pragma unroll
@@ -146,60 +158,57 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
                 const int h = hb + j * HW + hsub;
                 xa[j] = xb[j] = ya[j] = yb[j] = make_uint4(0, 0, 0, 0);
                 if (h < hi) {
-                    xa[j] = *reinterpret_cast<const uint4 *>(src + (size_t)h * D + va);
-                    xb[j] = *reinterpret_cast<const uint4 *>(src + (size_t)h * D + vb);
-                    ya[j] = *reinterpret_cast<const uint4 *>(up + (size_t)h * D + va);
-                    yb[j] = *reinterpret_cast<const uint4 *>(up + (size_t)h * D + vb);
+                    load_head<INTERLEAVED>(src + (size_t)h * D, va, vb, a.wide, xa[j], xb[j]);
+                    load_head<INTERLEAVED>(up + (size_t)h * D, va, vb, a.wide, ya[j], yb[j]);
                 }
             }
 #pragma unroll
             for (int j = 0; j < kBwdUnroll; ++j) {
                 const int h = hb + j * HW + hsub;
-                float fa[8], fb[8], ga[8], gb[8];
+                float2 fa[4], fb[4], ga[4], gb[4], dot = make_float2(0.f, 0.f);
                 unpack(xa[j], fa);
                 unpack(xb[j], fb);
                 unpack(ya[j], ga);
                 unpack(yb[j], gb);
-                const float r = inverse_rms<D>(fa, fb, a.eps);
+                const float2 r = both(inverse_rms<D>(fa, fb, a.eps));
                 if (turns) turn_pairs<INTERLEAVED>(ga, gb, c, s);
-                float dot = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    fa[i] *= r;
-                    fb[i] *= r;
-                    da[i] = fmaf(ga[i], fa[i], da[i]);
-                    db[i] = fmaf(gb[i], fb[i], db[i]);
-                    ga[i] *= wa[i];
-                    gb[i] *= wb[i];
-                    dot = fmaf(ga[i], fa[i], dot);
-                    dot = fmaf(gb[i], fb[i], dot);
+                for (int i = 0; i < 4; ++i) {
+                    fa[i] = ptx::fmul2(fa[i], r);
+                    fb[i] = ptx::fmul2(fb[i], r);
+                    da[i] = ptx::ffma2(ga[i], fa[i], da[i]);
+                    db[i] = ptx::ffma2(gb[i], fb[i], db[i]);
+                    ga[i] = ptx::fmul2(ga[i], wa[i]);
+                    gb[i] = ptx::fmul2(gb[i], wb[i]);
+                    dot = ptx::ffma2(ga[i], fa[i], dot);
+                    dot = ptx::ffma2(gb[i], fb[i], dot);
                 }
+                float sum = dot.x + dot.y;
 #pragma unroll
-                for (int o = 1; o < LH; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                dot *= -1.f / D;
+                for (int o = 1; o < LH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const float2 mean = both(sum * (-1.f / D));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ga[i] = r * fmaf(fa[i], dot, ga[i]);
-                    gb[i] = r * fmaf(fb[i], dot, gb[i]);
+                for (int i = 0; i < 4; ++i) {
+                    ga[i] = ptx::fmul2(r, ptx::ffma2(fa[i], mean, ga[i]));
+                    gb[i] = ptx::fmul2(r, ptx::ffma2(fb[i], mean, gb[i]));
                 }
-                if (h < hi) {
-                    *reinterpret_cast<uint4 *>(dst + (size_t)h * D + va) = pack(ga);
-                    *reinterpret_cast<uint4 *>(dst + (size_t)h * D + vb) = pack(gb);
-                }
+                if (h < hi) store_head<INTERLEAVED>(dst + (size_t)h * D, va, vb, a.wide, pack(ga), pack(gb));
             }
         }
     }
     // the weight's gradient of this CTA, in an order fixed by the grid alone
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int o = LH; o < 32; o <<= 1) {
-            da[i] += __shfl_xor_sync(0xffffffffu, da[i], o);
-            db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
+            da[i].x += __shfl_xor_sync(0xffffffffu, da[i].x, o);
+            da[i].y += __shfl_xor_sync(0xffffffffu, da[i].y, o);
+            db[i].x += __shfl_xor_sync(0xffffffffu, db[i].x, o);
+            db[i].y += __shfl_xor_sync(0xffffffffu, db[i].y, o);
         }
         if (hsub == 0) {
-            s_sum[warp][va + i] = da[i];
-            s_sum[warp][vb + i] = db[i];
+            *reinterpret_cast<float2 *>(&s_sum[warp][va + 2 * i]) = da[i];
+            *reinterpret_cast<float2 *>(&s_sum[warp][vb + 2 * i]) = db[i];
         }
     }
     __syncthreads();
@@ -394,6 +403,11 @@ MOBA_EXPORT int moba_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, co
             collides(ko, in, in.p == dk_out && in.width == ko.width, tokens))
             return MOBA_ERR_INVALID_ARG;
     if (collides(ko, qo, false, tokens)) return MOBA_ERR_INVALID_ARG;
+    a.wide = true;
+    for (const Side *s : {&a.q, &a.k})
+        if (s->heads)
+            for (const Area &m : {area(s->x, s->xs, 0, 0), area(s->dy, s->ds, 0, 0), area(s->out, s->os, 0, 0)})
+                a.wide = a.wide && ((reinterpret_cast<uintptr_t>(m.p) | (uintptr_t)m.stride) & 31) == 0;
     const int grid = bwd_grid(&a, D);
     const size_t need = sizeof(float) * D * (size_t)grid;
     if (workspace && (workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))

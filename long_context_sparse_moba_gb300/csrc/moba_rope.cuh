@@ -5,6 +5,7 @@
 #include <math_constants.h>
 
 #include "moba_internal.cuh"
+#include "moba_ptx.cuh"
 
 namespace moba {
 namespace rope {
@@ -46,54 +47,112 @@ __device__ __forceinline__ void cos_sin(const unsigned long long *turn, long lon
     }
 }
 
-// The lane's two vectors in 32 bits, a its first eight values, b its last eight.
-__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[8]) {
-    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&v);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 x = __bfloat1622float2(p[e]);
-        f[2 * e] = x.x;
-        f[2 * e + 1] = x.y;
+// The lane's two vectors of a head; neighbours (the pairs interleaved) as one of 32 bytes,
+// in whole sectors, where every head is aligned to that (wide).
+template <bool INTERLEAVED>
+__device__ __forceinline__ void load_head(const __nv_bfloat16 *p, int va, int vb, bool wide, uint4 &a, uint4 &b) {
+    if (INTERLEAVED && wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                     : "l"(p + va));
+    } else {
+        a = *reinterpret_cast<const uint4 *>(p + va);
+        b = *reinterpret_cast<const uint4 *>(p + vb);
     }
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+template <bool INTERLEAVED>
+__device__ __forceinline__ void store_head(__nv_bfloat16 *p, int va, int vb, bool wide, const uint4 &a, const uint4 &b) {
+    if (INTERLEAVED && wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + va), "r"(a.x), "r"(a.y),
+                     "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4 *>(p + va) = a;
+        *reinterpret_cast<uint4 *>(p + vb) = b;
+    }
+}
+
+// The lane's two vectors in 32 bits, a its first eight values, b its last eight, two to a
+// packed operation.
+__device__ __forceinline__ void unpack(const uint4 &v, float2 (&f)[4]) {
+    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = __bfloat1622float2(p[e]);
+}
+__device__ __forceinline__ uint4 pack(const float2 (&f)[4]) {
     uint4 v;
     __nv_bfloat162 *p = reinterpret_cast<__nv_bfloat162 *>(&v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+    for (int e = 0; e < 4; ++e) p[e] = __floats2bfloat162_rn(f[e].x, f[e].y);
     return v;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 minus(float2 x) { return make_float2(-x.x, -x.y); }
+
+// mag * cos and mag * sign * sin of position p for all pairs, by the warp's lanes, left in
+// c and s (of the warp alone); then the lane's eight from there.  (A lane's own pairs are
+// those of every head of the warp: made lane by lane they cost four to eight times as much.)
+__device__ __forceinline__ void warp_cos_sin(const unsigned long long *turn, int half, int lane, long long p,
+                                             float mag, float sign, float *c, float *s) {
+    __syncwarp();  // (the token before has been read)
+    for (int i = lane; i < half; i += 32) {
+        const unsigned long long phase = turn[i] * (unsigned long long)p;
+        // the upper 32 bits as a signed fraction of half a turn
+        const float x = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;
+        float sn, cs;
+        sincospif(x, &sn, &cs);
+        s[i] = sn * (mag * sign);
+        c[i] = cs * mag;
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void load_eight(const float *p, float2 (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const float4 v = *reinterpret_cast<const float4 *>(p + 2 * i);
+        f[i] = make_float2(v.x, v.y);
+        f[i + 1] = make_float2(v.z, v.w);
+    }
 }
 
 // The eight pairs turned: pair i is (a[i], b[i]), or neighbours of a and then of b.
 template <bool INTERLEAVED>
-__device__ __forceinline__ void turn_pairs(float (&a)[8], float (&b)[8], const float (&c)[8],
-                                           const float (&s)[8]) {
+__device__ __forceinline__ void turn_pairs(float2 (&a)[4], float2 (&b)[4], const float2 (&c)[4],
+                                           const float2 (&s)[4]) {
+    if (INTERLEAVED) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float &x = INTERLEAVED ? (i < 4 ? a[2 * i] : b[2 * i - 8]) : a[i];
-        float &y = INTERLEAVED ? (i < 4 ? a[2 * i + 1] : b[2 * i - 7]) : b[i];
-        const float u = fmaf(x, c[i], -y * s[i]), v = fmaf(y, c[i], x * s[i]);
-        x = u;
-        y = v;
+        for (int i = 0; i < 8; ++i) {
+            float2 &x = i < 4 ? a[i] : b[i - 4];
+            const float cc = i & 1 ? c[i / 2].y : c[i / 2].x, ss = i & 1 ? s[i / 2].y : s[i / 2].x;
+            x = make_float2(fmaf(x.x, cc, -x.y * ss), fmaf(x.y, cc, x.x * ss));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 u = ptx::ffma2(a[i], c[i], ptx::fmul2(minus(b[i]), s[i]));
+            b[i] = ptx::ffma2(b[i], c[i], ptx::fmul2(a[i], s[i]));
+            a[i] = u;
+        }
     }
 }
 
-// 1 / sqrt(mean x^2 + eps) of the head whose values are on `lanes` neighbouring
-// lanes.  All lanes of the warp call it.
+// 1 / sqrt(mean x^2 + eps) of the head whose values are on D / 16 neighbouring lanes.
+// All lanes of the warp call it.
 template <int D>
-__device__ __forceinline__ float inverse_rms(const float (&a)[8], const float (&b)[8], float eps) {
+__device__ __forceinline__ float inverse_rms(const float2 (&a)[4], const float2 (&b)[4], float eps) {
     constexpr int LH = D / 16;
     auto squares = [&](float f) {
-        float ss = 0.f;
+        float2 ss = make_float2(0.f, 0.f), tt = ss;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = a[i] * f, y = b[i] * f;
-            ss = fmaf(x, x, ss);
-            ss = fmaf(y, y, ss);
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = f == 1.f ? a[i] : ptx::fmul2(a[i], both(f)), y = f == 1.f ? b[i] : ptx::fmul2(b[i], both(f));
+            ss = ptx::ffma2(x, x, ss);
+            tt = ptx::ffma2(y, y, tt);
         }
+        float sum = (ss.x + ss.y) + (tt.x + tt.y);
 #pragma unroll
-        for (int o = 1; o < LH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        return ss;
+        for (int o = 1; o < LH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        return sum;
     };
     const float ss = squares(1.f);
     float r = rsqrtf(fmaf(ss, 1.f / D, eps));
@@ -111,24 +170,15 @@ __device__ __forceinline__ float weight(const void *w, int w32, int d) {
                : __bfloat162float(__ldg(static_cast<const __nv_bfloat16 *>(w) + d));
 }
 
-// the lane's 16 weights
-__device__ __forceinline__ void load_weights(const float *w, int va, int vb, float (&wa)[8], float (&wb)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-        *reinterpret_cast<float4 *>(wa + i) = *reinterpret_cast<const float4 *>(w + va + i);
-        *reinterpret_cast<float4 *>(wb + i) = *reinterpret_cast<const float4 *>(w + vb + i);
-    }
-}
-
 // a head over its root mean square, times the weights
 template <int D>
-__device__ __forceinline__ void normalise(float (&a)[8], float (&b)[8], const float (&wa)[8], const float (&wb)[8],
-                                          float eps) {
-    const float r = inverse_rms<D>(a, b, eps);
+__device__ __forceinline__ void normalise(float2 (&a)[4], float2 (&b)[4], const float2 (&wa)[4],
+                                          const float2 (&wb)[4], float eps) {
+    const float2 r = both(inverse_rms<D>(a, b, eps));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        a[i] = a[i] * r * wa[i];
-        b[i] = b[i] * r * wb[i];
+    for (int i = 0; i < 4; ++i) {
+        a[i] = ptx::fmul2(ptx::fmul2(a[i], r), wa[i]);
+        b[i] = ptx::fmul2(ptx::fmul2(b[i], r), wb[i]);
     }
 }
 

@@ -161,6 +161,25 @@ def test_slices_of_a_projection_and_in_place():
     check_forward(ops.qk_norm_rope(part, None, w2, None, p2, f2)[0], part, w2, p2, f2, 1e-6, False)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_operands_aligned_to_sixteen_bytes(interleaved):
+    T, hq, d = 33, 3, 64
+    w, pos, freqs = weights(1, d, BF), torch.arange(T, dtype=torch.int32, device="cuda"), ops.rope_frequencies(d)
+    wide, off = hq * d + 8, 8  # rows of 200 values, from the eighth on
+
+    def rows(seed):
+        return normal(seed, T * wide + off)[off:].view(T, wide)[:, :hq * d].view(T, hq, d)
+
+    q, g, out = rows(2), rows(3), rows(4)
+    assert q.data_ptr() % 32 == 16 and q.stride(0) * 2 % 32 == 16
+    for operands in ((q, g, out), (q.contiguous(), g, None), (q, g.contiguous(), None), (q.contiguous(), g.contiguous(), out)):
+        x, dy, dq = operands
+        got, _, dw, _ = ops.qk_norm_rope_bwd(dy, None, x, None, w, None, pos, freqs, interleaved=interleaved, dq=dq)
+        check_gradient(got, dw, dy, x, w, pos, freqs, 1e-6, interleaved)
+        y, _ = ops.qk_norm_rope(x, None, w, None, pos, freqs, interleaved=interleaved, q_out=dq)
+        check_forward(y, x, w, pos, freqs, 1e-6, interleaved)
+
+
 def test_gradient_against_differences():
     """Along a direction in q and one in the weights, against central differences of the
     64-bit formula (step 1e-5, whose own error is far below 1e-6 of the magnitudes here)."""
