@@ -100,9 +100,7 @@ __device__ __noinline__ float mean64(const __nv_bfloat16 *kp, int Hkv, int psh, 
     return (float)(sum / bs);
 }
 
-// POOL: the new tokens are in their pages already, from the kernel before this one, and
-// the CTAs only sum what is complete: the same sums in the same order.
-template <int D, bool MAX, bool POOL>
+template <int D, bool MAX>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     constexpr int CW = D / 8;                        // threads across a token
     constexpr int GC = kAppendThreads / CW;          // groups of a CTA
@@ -112,7 +110,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
     __shared__ float s_sum[kAppendParts][D], s_bad[kAppendParts];  // of CTA 0: the parts' sums
     __shared__ int s_page[kAppendPages], s_abort;
     __shared__ __align__(8) unsigned long long s_bar;
-    if (POOL) after_previous();
     const int rank = blockIdx.x & (a.ctas - 1), bj = (int)blockIdx.x / a.ctas, hk = blockIdx.y;
     int b, nth;  // the sequence, and which of the blocks that its new tokens touch
     Seq s;
@@ -131,12 +128,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
         return;
     }
     const int bs = a.c.bs, ps = a.c.ps;
+    const int first = s.len - s.n;  // position of the first new token
     if (nth < 0 || nth > s.n / bs + 1) return;
-    const int p0 = ((s.len - s.n) / bs + nth) * bs;
-    const int first = POOL ? s.len : s.len - s.n;  // position of the first token from k and v
+    const int p0 = (first / bs + nth) * bs;
     if (p0 >= s.len) return;
     const bool pool = a.kbar && p0 + bs <= s.len;
-    if (POOL && !pool) return;
     const int c1 = min(p0 + bs, s.len);
     const int t0 = pool ? p0 : max(p0, first);  // first token that is read
     if (!pool && c1 - t0 == 1 && (((t0 - p0) % G / GC) & (a.ctas - 1)) != rank)
@@ -262,6 +258,121 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 }
 
 // ----------------------------------------------------------------------------
+// pooling alone
+// ----------------------------------------------------------------------------
+// The pooled keys of blocks whose new tokens a kernel of the same call has just written: the
+// sums of append_kernel in its order, so to the same bits, by one CTA a block and kv
+// head that takes the groups of tokens (p % G) in turn.  A step completes few blocks, so a
+// CTA looks at several and leaves most.  A thread waits for that kernel when it comes to
+// the first new token: until then a block's older keys are on their way.
+constexpr int kPoolThreads = 256, kPoolCtas = 3;  // of an SM
+
+template <int D, bool MAX>
+__global__ void __launch_bounds__(kPoolThreads, kPoolCtas) pool_kernel(AppendArgs a, int candidates) {
+    constexpr int CW = D / 8, GC = kAppendThreads / CW, G = GC * kAppendParts;  // as in append_kernel
+    constexpr int GP = kPoolThreads / CW;                                       // groups at a time
+    constexpr int U = 8;
+    __shared__ float s_red[G][D], s_sum[kAppendParts][D];
+    __shared__ int s_page[kAppendPages];
+    const int tid = threadIdx.x, col = tid % CW, bs = a.c.bs, ps = a.c.ps;
+    bool waited = false;
+    for (int i = blockIdx.x; i < candidates; i += gridDim.x) {
+        const int hk = i % a.c.Hkv, bj = i / a.c.Hkv;
+        int b, nth;
+        if (a.cand > 0) {
+            b = bj / a.cand;
+            nth = bj % a.cand;
+        } else {
+            b = a.c.tile_of(bj, 1, bs, 2, nth);
+        }
+        Seq s;
+        if (a.c.seq(b, s) != kSeqOk || nth < 0 || nth > s.n / bs + 1) continue;
+        const int p0 = ((s.len - s.n) / bs + nth) * bs, fresh = s.len - s.n - p0;  // the first new token's place
+        if (p0 + bs > s.len) continue;
+        const int *table = a.c.table + (size_t)b * a.c.max_pages + (p0 >> a.psh);
+        const int pages = bs >> a.psh;
+        const bool held = pages <= kAppendPages;
+        if (held)
+            for (int k = tid; k < pages; k += kPoolThreads) s_page[k] = __ldg(table + k);
+        __syncthreads();
+        bool bad = false;
+#pragma unroll 1
+        for (int g = tid / CW; g < G; g += GP) {
+            if (!waited && g < bs && g + (bs - 1 - g) / G * G >= fresh) {
+                after_previous();
+                waited = true;
+            }
+            float acc[8], comp[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                acc[e] = MAX ? -INFINITY : 0.f;
+                comp[e] = 0.f;
+            }
+            for (int p = g; p < bs; p += U * G) {
+                uint4 x[U];
+                bool live[U];
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int at = p + j * G;
+                    live[j] = at < bs;
+                    if (live[j]) {
+                        const int page = held ? s_page[at >> a.psh] : __ldg(table + (at >> a.psh));
+                        live[j] = (unsigned)page < (unsigned)a.c.num_pages;
+                        bad |= !live[j];
+                        if (live[j])
+                            x[j] = *reinterpret_cast<const uint4 *>(
+                                a.kp + ((((size_t)page * a.c.Hkv + hk) << a.psh) + (at & (ps - 1))) * D + col * 8);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    if (!live[j]) continue;
+                    const __nv_bfloat162 *p2 = reinterpret_cast<const __nv_bfloat162 *>(&x[j]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float f = e & 1 ? __high2float(p2[e >> 1]) : __low2float(p2[e >> 1]);
+                        if (MAX) acc[e] = fmaxf(acc[e], f);
+                        else kahan(acc[e], comp[e], f);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 4)
+                *reinterpret_cast<float4 *>(&s_red[g][col * 8 + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+        }
+        const bool some = __syncthreads_or(bad);
+        for (int k = tid; k < kAppendParts * D; k += kPoolThreads) {
+            const int part = k / D, d = k % D;
+            float cp = 0.f, sum = s_red[part * GC][d];
+            for (int g = 1; g < GC; ++g) {
+                if (MAX) sum = fmaxf(sum, s_red[part * GC + g][d]);
+                else kahan(sum, cp, s_red[part * GC + g][d]);
+            }
+            s_sum[part][d] = sum;
+        }
+        __syncthreads();
+        if (some) {
+            if (tid == 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+        } else if (tid < D) {
+            float sum = s_sum[0][tid], cp = 0.f;
+#pragma unroll
+            for (int r = 1; r < kAppendParts; ++r) {
+                if (MAX) sum = fmaxf(sum, s_sum[r][tid]);
+                else kahan(sum, cp, s_sum[r][tid]);
+            }
+            if (!MAX) sum /= (float)bs;
+            if (!MAX && !(fabsf(sum) < INFINITY)) {  // (as in append_kernel; every key, new ones too)
+                if (!waited) after_previous();
+                waited = true;
+                sum = mean64<D>(a.kp, a.c.Hkv, a.psh, table - (p0 >> a.psh), hk, tid, p0, bs, p0 + bs, nullptr);
+            }
+            a.kbar[((size_t)__ldg(table + pages - 1) * a.c.Hkv + hk) * D + tid] = sum;
+        }
+    }
+    if (!waited) after_previous();
+}
+
+// ----------------------------------------------------------------------------
 // page copy
 // ----------------------------------------------------------------------------
 // A CTA copies a part of one pair in one layer, 16 bytes a lane with several
@@ -317,49 +428,37 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(CopyArgs a) {
     if (a.kbar) copy_run(a.kbar + s * a.bar16, a.kbar + d * a.bar16, a.bar16, part, a.parts);
 }
 
-template <int D, bool POOL>
+template <int D>
 static cudaError_t launch_append(const AppendArgs &a, bool max, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.clusters * a.ctas), a.c.Hkv);
     cfg.blockDim = kAppendThreads;
     cfg.stream = st;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = a.ctas;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = POOL ? 2 : 1;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = a.ctas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
     note_launches(1);
-    return max ? cudaLaunchKernelEx(&cfg, append_kernel<D, true, POOL>, a)
-               : cudaLaunchKernelEx(&cfg, append_kernel<D, false, POOL>, a);
+    return max ? cudaLaunchKernelEx(&cfg, append_kernel<D, true>, a)
+               : cudaLaunchKernelEx(&cfg, append_kernel<D, false>, a);
 }
 
-// The grid of an append (or of its pooling alone) whose cache and pools are set.
-static int plan_append(AppendArgs *a, bool pool) {
+// The blocks that the new tokens may touch: those of the longest chunk for every
+// sequence, or, where chunks are uneven and that is more of them, by packed tokens (n
+// tokens touch n / block_size + 2 blocks at most), which costs a search for the sequence.
+static int plan_blocks(AppendArgs *a) {
     const int bs = a->c.bs;
     a->psh = __builtin_ctz((unsigned)a->c.ps);
     a->cand = (int)(((long long)a->c.max_new + bs - 2) / bs + 1);
-    // clusters for the longest chunk of every sequence, or, where chunks are uneven
-    // and that is more of them, by packed tokens (n tokens touch n / block_size + 2
-    // blocks at most), which costs a search for the sequence
     a->clusters = (long long)a->c.num_seqs * a->cand;
     const long long packed = a->c.tile_slots(1, bs, 2);
     if (packed < a->clusters) {
         a->clusters = packed;
         a->cand = 0;
     }
-    if (a->clusters >= (1ll << 31) / kAppendParts) return MOBA_ERR_UNSUPPORTED;
-    // CTAs to a block.  More of them shorten the step that completes one, fewer
-    // leave the GPU to more blocks at once (six CTAs fit an SM).  us with 8,
-    // 4, 2, 1 (D 128, 8 kv heads, blocks of 512, in a graph): a step of one sequence that
-    // completes its block 4.8, 6.7, 10.4, 17.2; of 64 of which one does 9.3, 9.0, 11.1,
-    // 17.9; of 256 of which three do 25.1, 18.8, 18.7, 24.1; a chunk of 65536 tokens 78,
-    // 73, 75, 84, and 267, 185, 144, 117 with blocks of 64
-    const double per_sm = (double)((long long)a->c.total / bs + a->c.num_seqs) * a->c.Hkv / sm_count();
-    a->ctas = per_sm * 8 <= 6 ? 8 : per_sm * 4 <= (pool ? 6 : 15) ? 4 : bs >= 512 ? 2 : 1;
-    return MOBA_OK;
+    return a->clusters >= (1ll << 31) / kAppendParts ? MOBA_ERR_UNSUPPORTED : MOBA_OK;
 }
 
 int make_pool(AppendArgs *a, const Cache &c, void *k_pages, float *kbar_pages, int *status) {
@@ -368,12 +467,22 @@ int make_pool(AppendArgs *a, const Cache &c, void *k_pages, float *kbar_pages, i
     a->kp = static_cast<__nv_bfloat16 *>(k_pages);
     a->vp = nullptr;
     a->kbar = kbar_pages;
+    a->ctas = 1;
     a->status = status;
-    return plan_append(a, true);
+    const int rc = plan_blocks(a);
+    if (rc != MOBA_OK) return rc;
+    return a->clusters * c.Hkv >= (1ll << 31) ? MOBA_ERR_UNSUPPORTED : MOBA_OK;
 }
 
 cudaError_t launch_pool(const AppendArgs &a, int D, bool max, cudaStream_t st) {
-    return D == 64 ? launch_append<64, true>(a, max, st) : launch_append<128, true>(a, max, st);
+    const int candidates = (int)(a.clusters * a.c.Hkv), most = sm_count() * kPoolCtas;
+    const dim3 grid(candidates < most ? candidates : most), block(kPoolThreads);
+    note_launches(1);
+    if (D == 64)
+        return max ? launch_after(pool_kernel<64, true>, grid, block, 0, st, a, candidates)
+                   : launch_after(pool_kernel<64, false>, grid, block, 0, st, a, candidates);
+    return max ? launch_after(pool_kernel<128, true>, grid, block, 0, st, a, candidates)
+               : launch_after(pool_kernel<128, false>, grid, block, 0, st, a, candidates);
 }
 
 }  // namespace paged
@@ -406,13 +515,21 @@ MOBA_EXPORT int moba_paged_append(const void *k, const void *v, void *k_pages, v
     a.kp = static_cast<__nv_bfloat16 *>(k_pages);
     a.vp = static_cast<__nv_bfloat16 *>(v_pages);
     a.kbar = kbar_pages;
-    const int planned = plan_append(&a, false);
+    const int planned = plan_blocks(&a);
     if (planned != MOBA_OK) return planned;
+    // CTAs to a block.  More of them shorten the step that completes one, fewer
+    // leave the GPU to more blocks at once (six CTAs fit an SM).  us with 8,
+    // 4, 2, 1 (D 128, 8 kv heads, blocks of 512, in a graph): a step of one sequence that
+    // completes its block 4.8, 6.7, 10.4, 17.2; of 64 of which one does 9.3, 9.0, 11.1,
+    // 17.9; of 256 of which three do 25.1, 18.8, 18.7, 24.1; a chunk of 65536 tokens 78,
+    // 73, 75, 84, and 267, 185, 144, 117 with blocks of 64
+    const double per_sm = (double)((long long)total / block_size + num_seqs) * Hkv / sm_count();
+    a.ctas = per_sm * 8 <= 6 ? 8 : per_sm * 4 <= 15 ? 4 : block_size >= 512 ? 2 : 1;
     a.status = status_word();
     if (!a.status) return cuda_result(cudaErrorInvalidDevice);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool max = pool == MOBA_POOL_MAX;
-    return cuda_result(D == 64 ? launch_append<64, false>(a, max, st) : launch_append<128, false>(a, max, st));
+    return cuda_result(D == 64 ? launch_append<64>(a, max, st) : launch_append<128>(a, max, st));
 }
 
 MOBA_EXPORT int moba_page_copy(void *k_pages, void *v_pages, float *kbar_pages, const int32_t *src,

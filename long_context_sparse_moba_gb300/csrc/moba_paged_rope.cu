@@ -28,8 +28,8 @@ namespace {
 using namespace rope;
 
 constexpr int kWarps = 8;
-constexpr int kUnroll = 4;  // heads whose loads a lane has in flight
-constexpr int kCtas = 8;    // of an SM at most
+constexpr int kUnroll = 4;  // heads of a lane in a step
+constexpr int kCtas = 2;    // of an SM
 
 struct WriteArgs {
     Cache c;
@@ -46,10 +46,17 @@ struct WriteArgs {
     int *status;
 };
 
+// A warp works through its units' steps, kUnroll heads of every lane each, of q, of k or
+// of v, which come by bulk copies two steps ahead.
+using StepRing = WarpRing<3, kUnroll * 1024>;  // 32 lanes * 16 values
+
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(32 * kWarps) write_kernel(WriteArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, kCtas) write_kernel(WriteArgs a) {
     constexpr int LH = D / 16;   // lanes per head: 16 values (8 pairs) each
-    constexpr int HW = 32 / LH;  // heads per warp and step
+    constexpr int HW = 32 / LH, STEP = HW * kUnroll;
+    extern __shared__ __align__(128) uint8_t s_ring[];
+    __shared__ __align__(8) unsigned long long s_bar[kWarps][StepRing::kStages];
+    __shared__ int s_abort;
     __shared__ unsigned long long s_turn[D / 2];
     __shared__ __align__(16) float s_w[2][D], s_c[kWarps][D / 2], s_s[kWarps][D / 2];
     let_next();
@@ -63,6 +70,11 @@ __global__ void __launch_bounds__(32 * kWarps) write_kernel(WriteArgs a) {
         Seq s;
         if (a.c.seq(b, s) == kSeqBad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
     }
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kWarps; ++w) StepRing::init(s_bar[w]);
+        s_abort = 0;
+        ptx::fence_mbar_init();
+    }
     __syncthreads();
     const int lane = threadIdx.x & 31, item = lane % LH, hsub = lane / LH;
     const int Hkv = a.c.Hkv, heads = a.Hq + 2 * Hkv, ps = a.c.ps;
@@ -71,17 +83,40 @@ __global__ void __launch_bounds__(32 * kWarps) write_kernel(WriteArgs a) {
     vectors<D, INTERLEAVED>(item, a.rot / 2, va, vb);
     const int warp = threadIdx.x >> 5;
     const unsigned units = (unsigned)a.c.total * a.splits, stride = gridDim.x * kWarps;
-    for (unsigned u = blockIdx.x * kWarps + warp; u < units; u += stride) {
-        const int t = a.splits == 1 ? u : u / a.splits, part = a.splits == 1 ? 0 : u % a.splits;
-        const int h0 = part * a.chunk, h1 = min(h0 + a.chunk, heads);
+    auto token = [&](unsigned u) { return (int)(a.splits == 1 ? u : u / a.splits); };
+    auto begin = [&](unsigned u) { return a.splits == 1 ? 0 : (int)(u % a.splits) * a.chunk; };
+    // of the kinds q, k, v: their first head among all, and the first behind them
+    auto base = [&](int kind) { return kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + Hkv; };
+    auto limit = [&](int kind, int hi) { return min(hi, kind == 0 ? a.Hq : kind == 1 ? a.Hq + Hkv : heads); };
+    auto kind_of = [&](int h) { return (h >= a.Hq) + (h >= a.Hq + Hkv); };
+    ptx::Ctl ctl{&s_abort, a.status, kDefaultWaitLimit};
+    StepRing ring(s_bar[warp], ptx::saddr(s_ring) + warp * StepRing::kBytes);
+    unsigned u = blockIdx.x * kWarps + warp, nu = u;                      // the unit at hand, the one to be copied next
+    int nh = begin(min(u, units - 1)), nhi = min(nh + a.chunk, heads);    // its heads that are left
+    auto issue = [&] {
+        if (nu >= units) return;
+        const int t = token(nu), kind = kind_of(nh), n = min(STEP, limit(kind, nhi) - nh);
+        const __nv_bfloat16 *row = kind == 0 ? a.q + t * a.qs : kind == 1 ? a.k + t * a.ks : a.v + t * a.vs;
+        const void *const src[1] = {row + (size_t)(nh - base(kind)) * D};
+        ring.fill(lane, src, (uint32_t)n * D * 2);
+        nh += n;
+        if (nh >= nhi && (nu += stride) < units) {
+            nh = begin(nu);
+            nhi = min(nh + a.chunk, heads);
+        }
+    };
+#pragma unroll 1
+    for (int i = 0; i < StepRing::kStages - 1; ++i) issue();
+    bool ok = true;
+    for (; ok && u < units; u += stride) {
+        const int t = token(u), h0 = begin(u), h1 = min(h0 + a.chunk, heads);
         const int b = a.c.seq_of_row(t, lane);
         Seq s;
-        const int state = a.c.seq(b, s);
         // (rows of no sequence, or of a refused one, are left as they were)
-        if (state != kSeqOk || t < s.row0 || t >= s.row0 + s.n) continue;
-        const int p = s.len - s.n + t - s.row0;  // the token's place
+        const bool live = a.c.seq(b, s) == kSeqOk && t >= s.row0 && t < s.row0 + s.n;
+        const int p = live ? s.len - s.n + t - s.row0 : 0;  // the token's place
         __nv_bfloat16 *page_k = nullptr, *page_v = nullptr;
-        if (h1 > a.Hq) {
+        if (live && h1 > a.Hq) {
             const int page = __ldg(a.c.table + (size_t)b * a.c.max_pages + (p >> a.psh));
             if ((unsigned)page < (unsigned)a.c.num_pages) {
                 const size_t at = (((size_t)page * Hkv << a.psh) + (p & (ps - 1))) * D;
@@ -100,53 +135,49 @@ __global__ void __launch_bounds__(32 * kWarps) write_kernel(WriteArgs a) {
             }
         }
 #pragma unroll 1
-        for (int kind = 0; kind < 3; ++kind) {  // q, k, v
-            const int base = kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + Hkv;
-            const int lo = max(h0 - base, 0), hi = min(h1 - base, kind == 0 ? a.Hq : Hkv);
-            if (lo >= hi) continue;
-            const __nv_bfloat16 *src = kind == 0 ? a.q + t * a.qs : kind == 1 ? a.k + t * a.ks : a.v + t * a.vs;
-            __nv_bfloat16 *dst = kind == 0 ? a.qo + t * a.qos : kind == 1 ? page_k : page_v;
-            if (!dst) continue;
+        for (int hb = h0, n; hb < h1; hb += n) {
+            issue();
+            const uint32_t stage = ring.wait(ctl);
+            ok = stage != 0;
+            if (!ok) break;
+            const int kind = kind_of(hb);
+            n = min(STEP, limit(kind, h1) - hb);
+            __nv_bfloat16 *dst = !live ? nullptr : kind == 0 ? a.qo + t * a.qos : kind == 1 ? page_k : page_v;
             const size_t step = kind == 0 ? (size_t)D : (size_t)D << a.psh;  // between heads of dst
             const bool norm = kind == 0 ? a.wq != nullptr : kind == 1 && a.wk != nullptr;
-            float2 wa[4], wb[4];
-            if (norm) {
-                load_eight(s_w[kind] + va, wa);
-                load_eight(s_w[kind] + vb, wb);
-            }
-            for (int hb = lo; hb < hi; hb += HW * kUnroll) {
-                uint4 xa[kUnroll], xb[kUnroll];
+            const float *w = s_w[kind & 1];
 #pragma unroll
-                for (int j = 0; j < kUnroll; ++j) {
-                    const int h = hb + j * HW + hsub;
-                    xa[j] = xb[j] = make_uint4(0, 0, 0, 0);
-                    if (h < hi) {
-                        xa[j] = *reinterpret_cast<const uint4 *>(src + (size_t)h * D + va);
-                        xb[j] = *reinterpret_cast<const uint4 *>(src + (size_t)h * D + vb);
-                    }
+            for (int j = 0; j < kUnroll; ++j) {
+                const int i = j * HW + hsub;
+                if (j * HW >= n) break;  // (the warp alike)
+                uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+                if (i < n) {
+                    xa = ptx::ld_shared_v4(stage + i * D * 2 + 2 * va);
+                    xb = ptx::ld_shared_v4(stage + i * D * 2 + 2 * vb);
                 }
-#pragma unroll
-                for (int j = 0; j < kUnroll; ++j) {
-                    const int h = hb + j * HW + hsub;
-                    if (kind < 2) {
-                        float2 fa[4], fb[4];
-                        unpack(xa[j], fa);
-                        unpack(xb[j], fb);
-                        if (norm) normalise<D>(fa, fb, wa, wb, a.eps);
-                        if (turns) turn_pairs<INTERLEAVED>(fa, fb, c, sn);
-                        if (norm || turns) {  // (else copied as they are, NaN payloads too)
-                            xa[j] = pack(fa);
-                            xb[j] = pack(fb);
-                        }
+                if (kind < 2 && (norm || turns)) {  // (else copied as they are, NaN payloads too)
+                    float2 fa[4], fb[4];
+                    unpack(xa, fa);
+                    unpack(xb, fb);
+                    if (norm) {
+                        float2 wa[4], wb[4];
+                        load_eight(w + va, wa);
+                        load_eight(w + vb, wb);
+                        normalise<D>(fa, fb, wa, wb, a.eps);
                     }
-                    if (h < hi) {
-                        *reinterpret_cast<uint4 *>(dst + h * step + va) = xa[j];
-                        *reinterpret_cast<uint4 *>(dst + h * step + vb) = xb[j];
-                    }
+                    if (turns) turn_pairs<INTERLEAVED>(fa, fb, c, sn);
+                    xa = pack(fa);
+                    xb = pack(fb);
+                }
+                if (dst && i < n) {
+                    *reinterpret_cast<uint4 *>(dst + (hb + i - base(kind)) * step + va) = xa;
+                    *reinterpret_cast<uint4 *>(dst + (hb + i - base(kind)) * step + vb) = xb;
                 }
             }
+            ring.release();
         }
     }
+    ring.drain();
 }
 
 template <int D>
@@ -154,8 +185,11 @@ cudaError_t launch_write(const WriteArgs &a, bool interleaved, cudaStream_t st) 
     const long long units = (long long)a.c.total * a.splits;
     const long long want = (units + kWarps - 1) / kWarps, cap = (long long)sm_count() * kCtas;
     const int grid = (int)(want < cap ? want : cap);
-    if (interleaved) write_kernel<D, true><<<grid, 32 * kWarps, 0, st>>>(a);
-    else write_kernel<D, false><<<grid, 32 * kWarps, 0, st>>>(a);
+    constexpr int bytes = kWarps * StepRing::kBytes;
+    const cudaError_t rc = interleaved ? allow_smem<write_kernel<D, true>>(bytes) : allow_smem<write_kernel<D, false>>(bytes);
+    if (rc != cudaSuccess) return rc;
+    if (interleaved) write_kernel<D, true><<<grid, 32 * kWarps, bytes, st>>>(a);
+    else write_kernel<D, false><<<grid, 32 * kWarps, bytes, st>>>(a);
     note_launches(1);
     return cudaGetLastError();
 }

@@ -47,7 +47,8 @@ struct Args {
     int tokens, rot;
     int chunk, splits;          // heads per unit, units per token
     int w32;                    // weights are fp32 (else bf16)
-    bool wide;                  // gradient: every head of every operand is aligned to 32 bytes
+    int *status;                // gradient
+    bool wide;                  // gradient: every head of the results is aligned to 32 bytes
     float eps, mag;
 };
 
@@ -116,16 +117,30 @@ __global__ void __launch_bounds__(32 * kWarps) fwd_kernel(Args a) {
 }
 
 // The first q_ctas CTAs take q, the others k, so that a thread sums one weight's
-// gradient (both cost it 16 more registers, and the second CTA of an SM).
+// gradient (both cost it 16 more registers, and the second CTA of an SM).  A warp works
+// through its units' steps, kBwdUnroll heads of every lane each, whose x and dy come by
+// bulk copies two steps ahead.
+template <int D>
+using BwdRing = WarpRing<3, 2 * kBwdUnroll * 1024>;  // 32 lanes * 16 values, x and dy
+
 template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
-    constexpr int LH = D / 16, HW = 32 / LH;
+    constexpr int LH = D / 16, HW = 32 / LH, STEP = HW * kBwdUnroll;
+    using R = BwdRing<D>;
+    extern __shared__ __align__(128) uint8_t s_ring[];
     __shared__ unsigned long long s_turn[D / 2];
-    __shared__ __align__(16) float s_w[D], s_c[kWarps][D / 2], s_s[kWarps][D / 2], s_sum[kWarps][D];
+    __shared__ __align__(16) float s_w[D], s_c[kWarps][D / 2], s_s[kWarps][D / 2];
+    __shared__ __align__(8) unsigned long long s_bar[kWarps][R::kStages];
+    __shared__ int s_abort;
     const bool is_k = (int)blockIdx.x >= a.q_ctas;
     const Side x = is_k ? a.k : a.q;
     load_turns(s_turn, a.freqs, a.rot / 2, threadIdx.x, 32 * kWarps);
     for (int i = threadIdx.x; i < D; i += 32 * kWarps) s_w[i] = weight(x.w, a.w32, i);
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kWarps; ++w) R::init(s_bar[w]);
+        s_abort = 0;
+        ptx::fence_mbar_init();
+    }
     __syncthreads();
     paged::let_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, item = lane % LH, hsub = lane / LH;
@@ -139,37 +154,61 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
     for (int i = 0; i < 4; ++i) da[i] = db[i] = make_float2(0.f, 0.f);
     const int cta = is_k ? blockIdx.x - a.q_ctas : blockIdx.x, ctas = is_k ? gridDim.x - a.q_ctas : a.q_ctas;
     const unsigned units = (unsigned)a.tokens * x.splits, stride = ctas * kWarps;
-    for (unsigned u = cta * kWarps + warp; u < units; u += stride) {
-        const int t = x.splits == 1 ? u : u / x.splits;
-        const int lo = x.splits == 1 ? 0 : (int)(u % x.splits) * x.chunk, hi = min(lo + x.chunk, x.heads);
-        warp_cos_sin(s_turn, a.rot / 2, lane, __ldg(a.pos + t), a.mag, -1.f, s_c[warp], s_s[warp]);
+    auto token = [&](unsigned u) { return (int)(x.splits == 1 ? u : u / x.splits); };
+    auto begin = [&](unsigned u) { return x.splits == 1 ? 0 : (int)(u % x.splits) * x.chunk; };
+    auto end = [&](int lo) { return min(lo + x.chunk, x.heads); };
+    ptx::Ctl ctl{&s_abort, a.status, kDefaultWaitLimit};
+    R ring(s_bar[warp], ptx::saddr(s_ring) + warp * R::kBytes);
+    unsigned u = cta * kWarps + warp, nu = u;    // the unit at hand, and the one to be copied next
+    int nh = begin(min(u, units - 1)), nhi = end(nh);  // its heads that are left
+    auto issue = [&] {
+        if (nu >= units) return;
+        const int t = token(nu);
+        const void *const src[2] = {x.x + t * x.xs + (size_t)nh * D, x.dy + t * x.ds + (size_t)nh * D};
+        ring.fill(lane, src, (uint32_t)min(STEP, nhi - nh) * D * 2);
+        nh += STEP;
+        if (nh >= nhi && (nu += stride) < units) {
+            nh = begin(nu);
+            nhi = end(nh);
+        }
+    };
+#pragma unroll 1
+    for (int i = 0; i < R::kStages - 1; ++i) issue();
+    int pos = u < units ? __ldg(a.pos + token(u)) : 0;
+    bool ok = true;
+    for (; ok && u < units; u += stride) {
+        const int t = token(u), lo = begin(u), hi = end(lo);
+        warp_cos_sin(s_turn, a.rot / 2, lane, pos, a.mag, -1.f, s_c[warp], s_s[warp]);
+        if (u + stride < units) pos = __ldg(a.pos + token(u + stride));
         float2 c[4], s[4];
         if (turns) {
             load_eight(s_c[warp] + item * 8, c);
             load_eight(s_s[warp] + item * 8, s);
         }
-        const __nv_bfloat16 *src = x.x + t * x.xs, *up = x.dy + t * x.ds;
         __nv_bfloat16 *dst = x.out + t * x.os;
 #pragma unroll 1
-        for (int hb = lo; hb < hi; hb += HW * kBwdUnroll) {
-            uint4 xa[kBwdUnroll], xb[kBwdUnroll], ya[kBwdUnroll], yb[kBwdUnroll];
+        for (int hb = lo; hb < hi; hb += STEP) {
+            issue();
+            const uint32_t stage = ring.wait(ctl);
+            ok = stage != 0;
+            if (!ok) break;
 #pragma unroll
             for (int j = 0; j < kBwdUnroll; ++j) {
                 const int h = hb + j * HW + hsub;
-                xa[j] = xb[j] = ya[j] = yb[j] = make_uint4(0, 0, 0, 0);
+                const uint32_t xs = stage + (j * HW + hsub) * D * 2, ys = xs + kBwdUnroll * 1024;
+                uint4 v[4];
+                v[0] = v[1] = v[2] = v[3] = make_uint4(0, 0, 0, 0);
                 if (h < hi) {
-                    load_head<INTERLEAVED>(src + (size_t)h * D, va, vb, a.wide, xa[j], xb[j]);
-                    load_head<INTERLEAVED>(up + (size_t)h * D, va, vb, a.wide, ya[j], yb[j]);
+                    v[0] = ptx::ld_shared_v4(xs + 2 * va);
+                    v[1] = ptx::ld_shared_v4(xs + 2 * vb);
+                    v[2] = ptx::ld_shared_v4(ys + 2 * va);
+                    v[3] = ptx::ld_shared_v4(ys + 2 * vb);
                 }
-            }
-#pragma unroll
-            for (int j = 0; j < kBwdUnroll; ++j) {
-                const int h = hb + j * HW + hsub;
                 float2 fa[4], fb[4], ga[4], gb[4], dot = make_float2(0.f, 0.f);
-                unpack(xa[j], fa);
-                unpack(xb[j], fb);
-                unpack(ya[j], ga);
-                unpack(yb[j], gb);
+                unpack(v[0], fa);
+                unpack(v[1], fb);
+                unpack(v[2], ga);
+                unpack(v[3], gb);
                 const float2 r = both(inverse_rms<D>(fa, fb, a.eps));
                 if (turns) turn_pairs<INTERLEAVED>(ga, gb, c, s);
 #pragma unroll
@@ -194,8 +233,12 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
                 }
                 if (h < hi) store_head<INTERLEAVED>(dst + (size_t)h * D, va, vb, a.wide, pack(ga), pack(gb));
             }
+            ring.release();
         }
     }
+    ring.drain();
+    __syncthreads();  // (every warp has read its stages)
+    float (*s_sum)[D] = reinterpret_cast<float (*)[D]>(s_ring);
     // the weight's gradient of this CTA, in an order fixed by the grid alone
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -220,25 +263,32 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
     }
 }
 
-// The CTAs' sums of a weight's gradient: a warp 32 columns of every 32nd CTA, the
-// warps joined in shared memory; in 64 bits, which costs nothing here.
+// The CTAs' sums of a weight's gradient: a warp 32 columns of every 32nd CTA, joined
+// through shared memory by a warp for each column.  (fp32: 64-bit additions are slow
+// enough here to show.)
 constexpr int kSumWarps = 32;
 
 __global__ void __launch_bounds__(32 * kSumWarps) weights_kernel(const float *part, int q_ctas, int ctas, int D,
                                                                  float *dwq, float *dwk) {
-    __shared__ double s[kSumWarps][32];
+    __shared__ float s[kSumWarps][33];
     paged::after_previous();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = blockIdx.x * 32 + lane;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = blockIdx.x * 32;
     const int c0 = blockIdx.y ? q_ctas : 0, c1 = blockIdx.y ? ctas : q_ctas;
-    double sum = 0.0;
-    for (int c = c0 + warp; c < c1; c += kSumWarps) sum += part[(size_t)c * D + col];
+    float sum = 0.f;
+    for (int c = c0 + warp; c < c1; c += 5 * kSumWarps) {
+        float v[5];
+#pragma unroll
+        for (int j = 0; j < 5; ++j)
+            v[j] = c + j * kSumWarps < c1 ? part[(size_t)(c + j * kSumWarps) * D + col + lane] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 5; ++j) sum += v[j];
+    }
     s[warp][lane] = sum;
     __syncthreads();
-    if (warp) return;
-    sum = 0.0;
+    sum = s[lane][warp];
 #pragma unroll
-    for (int w = 0; w < kSumWarps; ++w) sum += s[w][lane];
-    (blockIdx.y ? dwk : dwq)[col] = (float)sum;
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) (blockIdx.y ? dwk : dwq)[col + warp] = sum;
 }
 
 // The gradient's CTAs, which leave a row of partial sums each: for q and k by their
@@ -306,10 +356,13 @@ cudaError_t launch_fwd(const Args &a, bool interleaved, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_bwd(const Args &a, int grid, bool interleaved, float *dwq, float *dwk, cudaStream_t st) {
-    if (interleaved) bwd_kernel<D, true><<<grid, 32 * kWarps, 0, st>>>(a);
-    else bwd_kernel<D, false><<<grid, 32 * kWarps, 0, st>>>(a);
+    constexpr int bytes = kWarps * BwdRing<D>::kBytes;
+    cudaError_t rc = interleaved ? paged::allow_smem<bwd_kernel<D, true>>(bytes) : paged::allow_smem<bwd_kernel<D, false>>(bytes);
+    if (rc != cudaSuccess) return rc;
+    if (interleaved) bwd_kernel<D, true><<<grid, 32 * kWarps, bytes, st>>>(a);
+    else bwd_kernel<D, false><<<grid, 32 * kWarps, bytes, st>>>(a);
     note_launches(2);
-    const cudaError_t rc = cudaGetLastError();
+    rc = cudaGetLastError();
     if (rc != cudaSuccess) return rc;
     return paged::launch_after(weights_kernel, dim3(D / 32, dwk ? 2 : 1), dim3(32 * kSumWarps), 0, st,
                                (const float *)a.part, a.q_ctas, grid, D, dwq, dwk);
@@ -405,13 +458,13 @@ MOBA_EXPORT int moba_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, co
     if (collides(ko, qo, false, tokens)) return MOBA_ERR_INVALID_ARG;
     a.wide = true;
     for (const Side *s : {&a.q, &a.k})
-        if (s->heads)
-            for (const Area &m : {area(s->x, s->xs, 0, 0), area(s->dy, s->ds, 0, 0), area(s->out, s->os, 0, 0)})
-                a.wide = a.wide && ((reinterpret_cast<uintptr_t>(m.p) | (uintptr_t)m.stride) & 31) == 0;
+        if (s->heads) a.wide = a.wide && ((reinterpret_cast<uintptr_t>(s->out) | (uintptr_t)(2 * s->os)) & 31) == 0;
     const int grid = bwd_grid(&a, D);
     const size_t need = sizeof(float) * D * (size_t)grid;
     if (workspace && (workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
         return MOBA_ERR_WORKSPACE;
+    a.status = status_word();
+    if (!a.status) return cuda_result(cudaErrorInvalidDevice);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     void *own = nullptr;
     if (!workspace) {

@@ -47,19 +47,8 @@ __device__ __forceinline__ void cos_sin(const unsigned long long *turn, long lon
     }
 }
 
-// The lane's two vectors of a head; neighbours (the pairs interleaved) as one of 32 bytes,
-// in whole sectors, where every head is aligned to that (wide).
-template <bool INTERLEAVED>
-__device__ __forceinline__ void load_head(const __nv_bfloat16 *p, int va, int vb, bool wide, uint4 &a, uint4 &b) {
-    if (INTERLEAVED && wide) {
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-                     : "l"(p + va));
-    } else {
-        a = *reinterpret_cast<const uint4 *>(p + va);
-        b = *reinterpret_cast<const uint4 *>(p + vb);
-    }
-}
+// The lane's two vectors of a head to memory; neighbours (the pairs interleaved) as one of
+// 32 bytes, a whole sector, where every head is aligned to that (wide).
 template <bool INTERLEAVED>
 __device__ __forceinline__ void store_head(__nv_bfloat16 *p, int va, int vb, bool wide, const uint4 &a, const uint4 &b) {
     if (INTERLEAVED && wide) {
@@ -114,6 +103,52 @@ __device__ __forceinline__ void load_eight(const float *p, float2 (&f)[4]) {
         f[i + 1] = make_float2(v.z, v.w);
     }
 }
+
+// A warp's ring of stages, each filled by bulk copies that its lane 0 starts and its own
+// barrier counts.  Nobody else touches it.
+template <int STAGES, int BYTES>
+struct WarpRing {
+    static constexpr int kStages = STAGES, kBytes = STAGES * BYTES;
+    uint32_t bars, at;                // the barriers, and the stages, in shared memory
+    unsigned issued = 0, used = 0;    // stages so far
+
+    __device__ __forceinline__ WarpRing(const void *b, uint32_t stages) : bars(ptx::saddr(b)), at(stages) {}
+    // by one thread, before the CTA's barrier
+    static __device__ __forceinline__ void init(const void *b) {
+        for (int s = 0; s < STAGES; ++s) ptx::mbar_init(ptx::saddr(b) + 8 * s, 1);
+    }
+    // the next stage: `bytes` of each of n sources (16-byte pieces), one behind the other
+    template <int N>
+    __device__ __forceinline__ void fill(int lane, const void *const (&src)[N], uint32_t bytes) {
+        if (lane == 0) {
+            const uint32_t bar = bars + 8 * (issued % STAGES), dst = at + issued % STAGES * BYTES;
+            ptx::mbar_expect_tx(bar, N * bytes);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                        dst + i * (BYTES / N)),
+                    "l"(src[i]), "r"(bytes), "r"(bar)
+                    : "memory");
+        }
+        ++issued;
+    }
+    // waits for the oldest stage: its address, or 0 where the wait ran out
+    __device__ __forceinline__ uint32_t wait(const ptx::Ctl &ctl) {
+        const bool ok = __all_sync(0xffffffffu, ptx::wait_fast(bars + 8 * (used % STAGES), (used / STAGES) & 1, ctl));
+        return ok ? at + used % STAGES * BYTES : 0;
+    }
+    // the oldest stage has been read by every lane
+    __device__ __forceinline__ void release() {
+        __syncwarp();
+        ++used;
+    }
+    // copies in flight land before the CTA ends
+    __device__ __forceinline__ void drain() {
+        for (; used != issued; ++used)
+            ptx::drain_bar(bars + 8 * (used % STAGES), (used / STAGES) & 1, kDefaultWaitLimit);
+    }
+};
 
 // The eight pairs turned: pair i is (a[i], b[i]), or neighbours of a and then of b.
 template <bool INTERLEAVED>

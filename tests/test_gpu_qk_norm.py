@@ -11,8 +11,8 @@ the rounding to bf16 (half a step, 2^-8):
              by 2^-20 P, the mean by M (2^-20 + 2^-20 + 20 u), dx = r (g w - n mean) has three
              more roundings: 2^-8 |dx| + 2^-17 r (P + |n| M)
   weights    g n errs by 2^-19 of its magnitude A (P without w); a thread sums fewer than 64
-             of them, then the sums of 32 lanes' groups, 8 warps and the CTAs (64 bits):
-             (2^-19 + 80 u) sum A, within 2^-17 sum A."""
+             of them, then the sums of the lanes' groups (3 additions), 8 warps, ten CTAs or
+             fewer and a tree of 32 (5): (2^-19 + 90 u) sum A, within 2^-17 sum A."""
 import pytest
 import torch
 
