@@ -19,11 +19,21 @@ constexpr int kMaxBlocks = 65536;  // blocks of a sequence where blocks are sele
 
 // A tile of rows (numbered token * G + head) with the keys [key0, key_end) of sequence b's
 // pages, those of a prefix whole, else each row's up to its position, its token + pdelta.
-struct Span {
+// A sequence's own span (with the keys from key0 on) names its group's: the group's first
+// row, and where its spans begin among those of groups, << 1 | whether they are big.
+struct alignas(16) Span {
     int row0, nrows;
     int b, full;
     int key0, key_end;
     int pdelta, pad;
+    int group_row, group_span;
+    int pads[2];
+};
+// Of the big spans [0] and the small ones [1], sequences' own before those of groups.
+struct alignas(16) SpanHead {
+    long long units[2];  // of all of them, times the kv heads
+    int spans[2], own[2];
+    int taken, pad[3];   // runs of small spans that have been taken
 };
 
 struct Attn {
@@ -55,7 +65,7 @@ struct Attn {
     // ---- shared prefixes: jobs that are tiles of rows with a range of keys ----
     Span *tiles_big;            // [...] 256 rows at most, for the tcgen05 kernel
     long long *off_big;         // [... + 1] key tiles before each (and kBigStart), times the kv heads
-    int *n_spans;               // [5] how many of them, and of the streamed ones; of groups among each; runs taken
+    SpanHead *head;
     int *c_first;               // [... * Hkv] the CTAs in whose runs the span on the kv head lies, to c_last
     // ---- chunks of many rows (the tcgen05 kernel): jobs of up to 256 rows ----
     bool chunk;

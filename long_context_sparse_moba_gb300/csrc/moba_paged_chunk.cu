@@ -299,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             Job J;
             Seq sq;
             if (DENSE) {
-                const int tiles = SPANS ? a.n_spans[0] : a.own_off[a.c.num_seqs];
+                const int tiles = SPANS ? a.head->spans[0] : a.own_off[a.c.num_seqs];
                 const long long *off = SPANS ? a.off_big : a.unit_off;
                 int open = -1;
-                const long long total = off[tiles];
+                const long long total = SPANS ? a.head->units[0] : off[tiles];
                 const long long runs = total < (long long)gridDim.x ? total : (long long)gridDim.x;
                 if ((long long)blockIdx.x < runs) {
                     long long u = total * blockIdx.x / runs;

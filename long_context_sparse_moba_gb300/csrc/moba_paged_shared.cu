@@ -16,7 +16,7 @@
 //   2. Big spans, 256 rows, are jobs of the tcgen05 kernel of long chunks: groups of more
 //      rows than a small span holds, and the own keys in calls of many new tokens.
 //   3. Small spans, 16 rows, are streamed on mma.sync: a decode step's own keys, and the
-//      prefixes of groups that fit.
+//      prefixes of groups that fit, or of all groups where they are short.
 //   4. Every part of 2 and 3 leaves partial sums, which the merge joins.
 #include "moba_mma.cuh"
 #include "moba_paged_attn.cuh"
@@ -38,6 +38,9 @@ constexpr int kSmallStart = 2;
 // warps take as they become free: SMs differ, by their distance from the memory, in what
 // they get through (160 K to 210 K cycles of equal runs).
 constexpr int kDynamic = 24, kShort = 2;
+// Groups' prefixes are streamed whatever their rows where that is no more than so many
+// units a warp: the tcgen05 kernel takes 20 us to begin with.
+constexpr int kFewUnits = 16;
 
 struct SharedArgs {
     Attn a;
@@ -45,19 +48,19 @@ struct SharedArgs {
     const int *prefix_lens;      // [n_groups]
     int n_groups;
     int small_rows;              // groups of up to that many rows are small spans
-    int cap_big, cap_small;      // spans at most
-    int own_cap;                 // of them sequences' own
+    long long few;               // all groups are, if that is no more units than that
+    int cap_big, cap_small;      // spans of groups at most
+    int own_cap;                 // sequences' own spans, at most
     int warps;                   // of the streaming kernel
     int psh;                     // log2(page size)
     // scratch
-    Span *tiles_small;           // [cap_small]
-    long long *off_small;        // [cap_small + 1] units before each, times the kv heads
+    Span *tiles_small;           // [...]
+    long long *off_small;        // [... + 1] units before each (and kSmallStart), times the kv heads
     int *rep;                    // [n_groups] the sequence whose pages are read (num_seqs: none, -1: a wrong group)
-    int *at;                     // [n_groups] its first span << 1 | big, or -1
-    int4 *info;                  // [num_seqs] tokens shared, the group's first row, its first span, big
-    int *small_first, *small_last;  // [cap_small * Hkv] the runs that the span on the kv head lies in
-    float *small_o;              // [cap_small * Hkv + runs][kSmallRows][D] partial sums, as part_o
-    float2 *small_ml;            // [cap_small * Hkv + runs][kSmallRows]
+    int *at;                     // [n_groups] its first span (among those of groups) << 1 | big, or -1
+    int *small_first, *small_last;  // [... * Hkv] the runs that the span on the kv head lies in
+    float *small_o;              // [... * Hkv + runs][kSmallRows][D] partial sums, as part_o
+    float2 *small_ml;            // [... * Hkv + runs][kSmallRows]
 };
 
 // ----------------------------------------------------------------------------
@@ -100,7 +103,7 @@ __device__ __forceinline__ void block_scan(long long (&v)[N], long long (*warps)
 // the searches cost little.
 template <int T, bool HELD>
 __global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
-    __shared__ long long warps[4][32];
+    __shared__ long long warps[4][32], s_units;
     __shared__ int s_cu[HELD ? kHeld + 1 : 1], s_len[HELD ? kHeld : 1], s_grp[HELD ? kHeld + 1 : 1];
     __shared__ int s_pre[HELD ? kHeld : 1], s_rep[HELD ? kHeld : 1], s_at[HELD ? kHeld : 1];
     const Attn &a = x.a;
@@ -169,110 +172,154 @@ __global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
             }
     }
     sync();
-    // the groups' spans
-    long long nb = 0, ub = 0, nm = 0, um = 0;  // big and small ones so far, and their units
+    // units of all groups, were they streamed
+    auto lent = [&](int g, int &rows) {  // the sequence that lends its pages, and the group's rows; or -1
+        const int l = HELD ? rep[g] : __ldcg(rep + g);  // (where the atomics left it)
+        rows = l >= 0 && l < ns ? (cu(grp(g + 1)) - cu(grp(g))) * G : 0;
+        return l >= 0 && l < ns && pre(g) > 0 ? l : -1;
+    };
+    if (tid == 0) s_units = 0;
+    __syncthreads();
+    {
+        long long units = 0;
+        for (int g = tid; g < ng; g += T) {
+            int rows;
+            if (lent(g, rows) >= 0)
+                units += (long long)((rows + kSmallRows - 1) / kSmallRows) * Hkv * ((pre(g) + kUnit - 1) / kUnit);
+        }
+        if (units) atomicAdd(reinterpret_cast<unsigned long long *>(&s_units), (unsigned long long)units);
+    }
+    __syncthreads();
+    const int small_rows = s_units <= x.few ? 1 << 30 : x.small_rows;
+    // a group's spans: how many, and key tiles or units of each
+    struct Lot {
+        int lender, rows, n, tile, big;
+        long long units;
+    };
+    auto lot_of = [&](int g) {
+        Lot l = {-1, 0, 0, 1, 0, 0};
+        if (g >= ng) return l;
+        l.lender = lent(g, l.rows);
+        if (l.lender < 0) return l;
+        l.big = l.rows > small_rows;
+        l.tile = l.big ? kJobRows : kSmallRows;
+        l.n = (l.rows + l.tile - 1) / l.tile;
+        const int p = pre(g);
+        l.units = (long long)Hkv * (l.big ? (p + kBigKeys - 1) / kBigKeys + kBigStart : (p + kUnit - 1) / kUnit + kSmallStart);
+        return l;
+    };
+    // where they begin (more than there is room for: from offsets that overlap)
+    long long ng_spans[2] = {0, 0};
     for (int g0 = 0; g0 < ng; g0 += T) {
         const int g = g0 + tid;
-        long long v[4] = {0, 0, 0, 0}, total[4];
-        int row0 = 0, rows = 0, p = 0, n = 0, lender = -1;
-        bool big = false;
-        if (g < ng) {
-            lender = HELD ? rep[g] : __ldcg(rep + g);  // (where the atomics left it)
-            if (lender < 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
-            p = pre(g);
-            if (lender >= 0 && lender < ns && p > 0) {
-                row0 = cu(grp(g)) * G;
-                rows = cu(grp(g + 1)) * G - row0;
-                big = rows > x.small_rows;
-                n = big ? (rows + kJobRows - 1) / kJobRows : 1;
-                v[big ? 0 : 2] = n;
-                v[big ? 1 : 3] = (long long)n * Hkv * (big ? (p + kBigKeys - 1) / kBigKeys + kBigStart
-                                                           : (p + kUnit - 1) / kUnit + kSmallStart);
-            }
-        }
-        const long long mine_n = v[0] + v[2], mine_u = v[1] + v[3];
+        const Lot l = lot_of(g);
+        if (g < ng && (HELD ? rep[g] : __ldcg(rep + g)) < 0) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+        long long v[2] = {l.big ? l.n : 0, l.big ? 0 : l.n}, total[2];
         block_scan<T>(v, warps, total);
         if (g < ng) {
-            const long long i0 = (big ? nb + v[0] : nm + v[2]) - mine_n, u0 = (big ? ub + v[1] : um + v[3]) - mine_u;
-            const int cap = big ? x.cap_big : x.cap_small;
-            Span *tiles = big ? a.tiles_big : x.tiles_small;
-            long long *off = big ? a.off_big : x.off_small;
-            for (int i = 0; i < n && i0 + i < cap; ++i) {
-                Span t;
-                t.row0 = row0 + i * kJobRows;
-                t.nrows = min(rows - i * kJobRows, kJobRows);
-                t.b = lender;
-                t.full = 1;
-                t.key0 = 0;
-                t.key_end = p;
-                t.pdelta = t.pad = 0;
-                tiles[i0 + i] = t;
-                off[i0 + i + 1] = u0 + mine_u / n * (i + 1);
-            }
-            // (more than there is room for: from offsets that overlap)
-            at[g] = n > 0 && i0 + n <= cap ? (int)i0 << 1 | big : -1;
+            const long long end = l.big ? ng_spans[0] + v[0] : ng_spans[1] + v[1];
+            at[g] = l.n > 0 && end <= (l.big ? x.cap_big : x.cap_small) ? (int)(end - l.n) << 1 | l.big : -1;
         }
-        nb += total[0];
-        ub += total[1];
-        nm += total[2];
-        um += total[3];
+        ng_spans[0] += total[0];
+        ng_spans[1] += total[1];
     }
     sync();
-    const int groups_spans[2] = {(int)min(nb, (long long)x.cap_big), (int)min(nm, (long long)x.cap_small)};
     // the sequences' own
-    const int cap = a.chunk ? x.cap_big : x.cap_small, tile_rows = a.chunk ? kJobRows : kSmallRows;
+    const int kind = a.chunk ? 0 : 1, tile_rows = a.chunk ? kJobRows : kSmallRows;
     const int unit = a.chunk ? kBigKeys : kUnit, start = a.chunk ? kBigStart : kSmallStart;
     Span *tiles = a.chunk ? a.tiles_big : x.tiles_small;
     long long *off = a.chunk ? a.off_big : x.off_small;
-    long long &nt = a.chunk ? nb : nm, &ut = a.chunk ? ub : um;
+    long long own = 0, units = 0;
     for (int b0 = 0; b0 < ns; b0 += T) {
         const int b = b0 + tid;
         long long v[2] = {0, 0}, total[2];
         Seq s;
-        int first = 0, rows = 0, pdelta = 0;
-        int4 info = make_int4(0, 0, 0, 0);
+        Span t;
+        int rows = 0;
         if (b < ns && seq(b, s) == kSeqOk) {
-            const int g = group_of(b), t = g >= 0 ? at[g] : -1;
-            if (t >= 0) {
-                first = pre(g);
-                info = make_int4(first, cu(grp(g)) * G, t >> 1, t & 1);
-            }
+            const int g = group_of(b), lot = g >= 0 ? at[g] : -1;
+            t.b = b;
+            t.full = 0;
+            t.key0 = lot >= 0 ? pre(g) : 0;
+            t.pdelta = s.len - s.n - s.row0;
+            t.group_row = lot >= 0 ? cu(grp(g)) * G : 0;
+            t.group_span = lot;
+            t.pad = t.pads[0] = t.pads[1] = 0;
             rows = s.n * G;
-            pdelta = s.len - s.n - s.row0;
             v[0] = (rows + tile_rows - 1) / tile_rows;
             for (int r = 0; r < rows; r += tile_rows)
-                v[1] += (s.len - s.n + (min(r + tile_rows, rows) - 1) / G - first) / unit + 1 + start;
+                v[1] += (s.len - s.n + (min(r + tile_rows, rows) - 1) / G - t.key0) / unit + 1 + start;
             v[1] *= Hkv;
         }
         const long long mine_n = v[0], mine_u = v[1];
         block_scan<T>(v, warps, total);
-        if (b < ns) {
-            long long i = nt + v[0] - mine_n, u = ut + v[1] - mine_u;
-            x.info[b] = info;
-            for (int r = 0; r < rows && i < cap; r += tile_rows, ++i) {
-                Span t;
-                t.row0 = s.row0 * G + r;
-                t.nrows = min(rows - r, tile_rows);
-                t.b = b;
-                t.full = 0;
-                t.key0 = first;
-                t.key_end = (t.row0 + t.nrows - 1) / G + pdelta + 1;
-                t.pdelta = pdelta;
-                t.pad = 0;
-                tiles[i] = t;
-                u += (long long)Hkv * ((t.key_end - first + unit - 1) / unit + start);
-                off[i + 1] = u;
-            }
+        long long i = own + v[0] - mine_n, u = units + v[1] - mine_u;
+        for (int r = 0; r < rows && i < x.own_cap; r += tile_rows, ++i) {
+            t.row0 = s.row0 * G + r;
+            t.nrows = min(rows - r, tile_rows);
+            t.key_end = (t.row0 + t.nrows - 1) / G + t.pdelta + 1;
+            tiles[i] = t;
+            u += (long long)Hkv * ((t.key_end - t.key0 + unit - 1) / unit + start);
+            off[i + 1] = u;
         }
-        nt += total[0];
-        ut += total[1];
+        own += total[0];
+        units += total[1];
+    }
+    if (own > x.own_cap) {  // (from offsets that overlap)
+        own = x.own_cap;
+        sync();
+        units = off[own];
+    }
+    // the groups' spans behind them
+    long long n[2] = {kind ? 0 : own, kind ? own : 0}, un[2] = {kind ? 0 : units, kind ? units : 0};
+    const long long own_of[2] = {n[0], n[1]};
+    for (int g0 = 0; g0 < ng; g0 += T) {
+        const int g = g0 + tid;
+        const Lot l = lot_of(g);
+        long long v[4] = {l.big ? l.n : 0, l.big ? 0 : l.n, l.big ? l.n * l.units : 0, l.big ? 0 : l.n * l.units}, total[4];
+        block_scan<T>(v, warps, total);
+        const int k = l.big ? 0 : 1;
+        const long long i0 = n[k] + (l.big ? v[0] : v[1]) - l.n, u0 = un[k] + (l.big ? v[2] : v[3]) - l.n * l.units;
+        const long long room = own_of[k] + (l.big ? x.cap_big : x.cap_small);
+        Span *to = l.big ? a.tiles_big : x.tiles_small;
+        long long *ends = l.big ? a.off_big : x.off_small;
+        for (int i = 0; i < l.n && i0 + i < room; ++i) {
+            Span t;
+            t.row0 = cu(grp(g)) * G + i * l.tile;
+            t.nrows = min(l.rows - i * l.tile, l.tile);
+            t.b = l.lender;
+            t.full = 1;
+            t.key0 = 0;
+            t.key_end = pre(g);
+            t.pdelta = t.group_row = 0;
+            t.group_span = -1;
+            t.pad = t.pads[0] = t.pads[1] = 0;
+            to[i0 + i] = t;
+            ends[i0 + i + 1] = u0 + l.units * (i + 1);
+        }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            n[z] += total[z];
+            un[z] += total[2 + z];
+        }
+    }
+    if (tid == 0) a.off_big[0] = x.off_small[0] = 0;
+    const long long room[2] = {own_of[0] + x.cap_big, own_of[1] + x.cap_small};
+    if (n[0] > room[0] || n[1] > room[1]) {
+        sync();
+        if (n[0] > room[0]) n[0] = room[0], un[0] = a.off_big[room[0]];
+        if (n[1] > room[1]) n[1] = room[1], un[1] = x.off_small[room[1]];
     }
     if (tid == 0) {
-        // spans, and those of groups among them
-        *reinterpret_cast<int4 *>(a.n_spans) = make_int4((int)min(nb, (long long)x.cap_big), (int)min(nm, (long long)x.cap_small),
-                                                         groups_spans[0], groups_spans[1]);
-        a.n_spans[4] = 0;
-        a.off_big[0] = x.off_small[0] = 0;
+        SpanHead h;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            h.units[z] = un[z];
+            h.spans[z] = (int)n[z];
+            h.own[z] = (int)own_of[z];
+        }
+        h.taken = h.pad[0] = h.pad[1] = h.pad[2] = 0;
+        *a.head = h;
     }
 }
 
@@ -328,18 +375,19 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
     const uint32_t ring = base + warp * ST * R::kStage, bars = ptx::saddr(&s_bar[warp][0]);
     const uint8_t *mine = smem_raw + (ring - raw);
     const int gw = blockIdx.x * kStreamWarps + warp, G = a.G, Hkv = c.Hkv, ps = c.ps;
-    const int spans = a.n_spans[1];
-    const long long total = x.off_small[spans], most = (total + kMinUnits - 1) / kMinUnits;
+    const int spans = a.head->spans[1];
+    const long long total = a.head->units[1], most = (total + kMinUnits - 1) / kMinUnits;
+    // the short runs are the first ones, of sequences' own keys: of few parts' rows
     const bool dynamic = total > (long long)x.warps * kDynamic;
-    const long long even = dynamic ? total - total / 4 : total;  // units of the runs that are one for each warp
-    const int runs = dynamic ? x.warps * (1 + kShort) : (int)(most < x.warps ? most : x.warps);
+    const int shorts = dynamic ? x.warps * kShort : 0;
+    const long long cut = dynamic ? total / 4 : 0;  // the units of the short runs
+    const int runs = shorts + (int)(most < x.warps ? most : x.warps);
+    auto begin = [&](int r) {
+        return r < shorts ? cut * r / shorts : cut + (total - cut) * (r - shorts) / (runs - shorts);
+    };
     int issued = 0, used = 0;  // stages so far
-    for (int run = gw, next = 0; run < runs; run = next) {
-        if (dynamic && lane == 0) next = atomicAdd(a.n_spans + 4, 1);
-        const long long firsts = dynamic ? x.warps : runs;
-        auto begin = [&](int r) {
-            return r <= firsts ? even * r / firsts : even + (total - even) * (r - firsts) / (x.warps * kShort);
-        };
+    for (int run = shorts + gw, next = 0; run < runs; run = next) {
+        if (dynamic && lane == 0) next = atomicAdd(&a.head->taken, 1);
         const long long u0 = begin(run);
         const int n = (int)(begin(run + 1) - u0);
         int w = 0;  // the span with unit u0: the last that starts at or before it
@@ -561,33 +609,34 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
             for (; used < issued; ++used) ptx::drain_bar(bars + 8 * (used % ST), (used / ST) & 1, kDefaultWaitLimit);
             return;
         }
-        next = dynamic ? x.warps + __shfl_sync(0xffffffffu, next, 0) : runs;
+        next = __shfl_sync(0xffffffffu, next, 0);
+        if (next >= shorts) break;
     }
 }
 
 // ----------------------------------------------------------------------------
 // merge
 // ----------------------------------------------------------------------------
-// A CTA takes up to kMergeRows rows of a sequence's own span on a kv head, whose parts and
-// whose group's it looks up once; W warps to a row, every W-th part each, where rows are
-// few (they have many parts then).
+// A CTA takes up to `most` rows of a sequence's own span on a kv head, whose parts and whose
+// group's it looks up once; W warps to a row, every W-th part each, where rows are few (they
+// have many parts then).
 constexpr int kMergeWarps = 8, kMergeRows = 32;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_spans_kernel(SharedArgs x) {
+__global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_spans_kernel(SharedArgs x, int most) {
     constexpr int V = D / 32, U = 4;
     __shared__ float s_acc[kMergeWarps][D], s_m[kMergeWarps], s_l[kMergeWarps];
     const Attn &a = x.a;
     after_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.G, Hkv = a.c.Hkv;
     const bool chunk = a.chunk;
-    const int4 n = *reinterpret_cast<const int4 *>(a.n_spans);
-    const int w = (int)blockIdx.x / Hkv + (chunk ? n.z : n.w), hk = blockIdx.x % Hkv;
-    if (w >= (chunk ? n.x : n.y)) return;
+    // (a span behind the last one is some memory of the scratch)
+    const int w = (int)blockIdx.x / Hkv, hk = blockIdx.x % Hkv;
     const Span s = (chunk ? a.tiles_big : x.tiles_small)[w];
-    const int r0 = blockIdx.y * kMergeRows, rows = min(s.nrows - r0, kMergeRows);
+    const int groups = a.head->own[chunk ? 0 : 1], big_groups = chunk ? groups : a.head->own[0], small_groups = a.head->own[1];
+    if (w >= groups) return;
+    const int r0 = blockIdx.y * most, rows = min(s.nrows - r0, most);
     if (rows <= 0) return;
-    const int4 info = x.info[s.b];
     const int W = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8, part = warp % W;
     for (int ri = warp / W; ri < (W > 1 ? kMergeWarps / W : rows); ri += kMergeWarps / W) {
         const bool live = ri < rows;
@@ -596,47 +645,66 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_spans_kernel(Shared
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[k] = 0.f;
         bool bad = false;
-        // the parts of row r of span e / Hkv on kv head e % Hkv
-        auto add = [&](bool big, int e, int r) {
-            const int slots = big ? kJobRows : kSmallRows;
+        // its parts: of its group's span, then of its own one, those of a run (or CTA) each
+        int np = 0, n = 0;
+        const float *o[2] = {nullptr, nullptr};
+        const float2 *ml[2] = {nullptr, nullptr};
+        size_t first[2] = {0, 0};
+        int rows_of[2] = {0, 0};
+        auto parts = [&](int which, bool big, int e, int r) {
             const int c0 = max((big ? a.c_first : x.small_first)[e], 0);
             const int c1 = min((big ? a.c_last : x.small_last)[e], (big ? a.ctas : x.warps * (1 + kShort)) - 1);
-            const float *o = big ? a.part_o : x.small_o;
-            const float2 *ml = big ? a.part_ml : x.small_ml;
-            for (int c = c0 + part; c <= c1; c += W * U) {
-                float2 z[U];
-                float v[U][V];
-#pragma unroll
-                for (int j = 0; j < U; ++j) {
-                    z[j] = make_float2(-INFINITY, 0.f);
-                    if (c + W * j <= c1) {
-                        const size_t p = ((size_t)e + c + W * j) * slots + r;
-                        z[j] = ml[p];
-#pragma unroll
-                        for (int k = 0; k < V; k += 2)
-                            *reinterpret_cast<float2 *>(&v[j][k]) =
-                                *reinterpret_cast<const float2 *>(o + p * D + lane * V + k);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < U; ++j) {
-                    bad |= z[j].y < 0.f;
-                    if (z[j].y == 0.f) continue;  // no part, or one without a key for this row
-                    const float mn = fmaxf(M, z[j].x), ref = mn == -INFINITY ? 0.f : mn;
-                    const float f = mma::fast_exp2(M - ref), g = mma::fast_exp2(z[j].x - ref);
-                    M = mn;
-                    L = fmaf(z[j].y, g, L * f);
-#pragma unroll
-                    for (int k = 0; k < V; ++k) acc[k] = fmaf(v[j][k], g, acc[k] * f);
-                }
-            }
+            o[which] = big ? a.part_o : x.small_o;
+            ml[which] = big ? a.part_ml : x.small_ml;
+            rows_of[which] = big ? kJobRows : kSmallRows;
+            first[which] = ((size_t)e + c0) * rows_of[which] + r;
+            return max(c1 - c0 + 1, 0);
         };
         if (live) {
-            if (info.x > 0) {
-                const int at = row - info.y, tile = info.w ? kJobRows : kSmallRows;
-                add(info.w != 0, (info.z + at / tile) * Hkv + hk, at % tile);
+            if (s.group_span >= 0) {
+                const bool big = s.group_span & 1;
+                const int at = row - s.group_row, tile = big ? kJobRows : kSmallRows;
+                np = parts(0, big, ((big ? big_groups : small_groups) + (s.group_span >> 1) + at / tile) * Hkv + hk, at % tile);
             }
-            add(chunk, w * Hkv + hk, r0 + ri);
+            n = np + parts(1, chunk, w * Hkv + hk, r0 + ri);
+        }
+        for (int i = part; i < n; i += W * U) {
+            float2 z[U];
+            float v[U][V];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                z[j] = make_float2(-INFINITY, 0.f);
+                const int k = i + W * j;
+                const bool of_group = k < np;
+                if (k < n) {
+                    const size_t p = of_group ? first[0] + (size_t)k * rows_of[0] : first[1] + (size_t)(k - np) * rows_of[1];
+                    z[j] = (of_group ? ml[0] : ml[1])[p];
+                    const float *src = (of_group ? o[0] : o[1]) + p * D + lane * V;
+#pragma unroll
+                    for (int d = 0; d < V; d += 2)
+                        *reinterpret_cast<float2 *>(&v[j][d]) = *reinterpret_cast<const float2 *>(src + d);
+                }
+            }
+            float top = M;
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                bad |= z[j].y < 0.f;
+                if (!(z[j].y > 0.f)) z[j].x = -INFINITY;  // no part, or one without a key for this row
+                top = fmaxf(top, z[j].x);
+            }
+            const float ref = top == -INFINITY ? 0.f : top, f = mma::fast_exp2(M - ref);
+            M = top;
+            L *= f;
+#pragma unroll
+            for (int d = 0; d < V; ++d) acc[d] *= f;
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (z[j].x == -INFINITY) continue;
+                const float g = mma::fast_exp2(z[j].x - ref);
+                L = fmaf(z[j].y, g, L);
+#pragma unroll
+                for (int d = 0; d < V; ++d) acc[d] = fmaf(v[j][d], g, acc[d]);
+            }
         }
         if (W > 1) {  // (one round: every warp is here)
 #pragma unroll
@@ -686,15 +754,15 @@ size_t scratch(SharedArgs *x, void *base) {
         return p;
     };
     Attn &a = x->a;
-    const size_t ns = a.c.num_seqs, ng = x->n_groups, nb = x->cap_big, nm = x->cap_small;
-    a.n_spans = static_cast<int *>(take(32));
+    const size_t ng = x->n_groups, nb = (size_t)x->cap_big + (a.chunk ? x->own_cap : 0);
+    const size_t nm = (size_t)x->cap_small + (a.chunk ? 0 : x->own_cap);
+    a.head = static_cast<SpanHead *>(take(sizeof(SpanHead)));
     a.tiles_big = static_cast<Span *>(take(sizeof(Span) * nb));
     a.off_big = static_cast<long long *>(take(8 * (nb + 1)));
     x->tiles_small = static_cast<Span *>(take(sizeof(Span) * nm));
     x->off_small = static_cast<long long *>(take(8 * (nm + 1)));
     x->rep = static_cast<int *>(take(4 * ng));
     x->at = static_cast<int *>(take(4 * ng));
-    x->info = static_cast<int4 *>(take(sizeof(int4) * ns));
     a.c_first = static_cast<int *>(take(4 * nb * a.c.Hkv));
     a.c_last = static_cast<int *>(take(4 * nb * a.c.Hkv));
     x->small_first = static_cast<int *>(take(4 * nm * a.c.Hkv));
@@ -725,12 +793,16 @@ int make_shared(SharedArgs *x, int Hq, int D, int n_groups) {
     const long long seqs = a.c.num_seqs < a.c.total ? a.c.num_seqs : a.c.total;
     const long long groups = n_groups < seqs ? n_groups : seqs;
     const long long own = rows / (a.chunk ? kJobRows : kSmallRows) + seqs;
-    const long long big = groups && rows > x->small_rows ? rows / kJobRows + groups : 0;
-    const long long nb = big + (a.chunk ? own : 0), nm = a.chunk ? 0 : own + groups;
-    if (nb * a.c.Hkv >= (1ll << 30) || nm * a.c.Hkv >= (1ll << 30)) return MOBA_ERR_UNSUPPORTED;
+    const long long lent = groups ? rows / kSmallRows + groups : 0;  // small spans of groups, at most
+    x->few = a.chunk ? -1 : (long long)x->warps * kFewUnits;
+    // no group is big where even a prefix as long as the table is few units, or its rows fit
+    const bool never = !a.chunk && (rows <= kSmallRows || lent * a.c.Hkv * ((long long)a.c.max_pages * a.c.ps / kUnit) <= x->few);
+    const long long big = groups && !never ? rows / kJobRows + groups : 0;
+    const long long small = a.chunk ? 0 : lent;
+    if ((big + own) * a.c.Hkv >= (1ll << 30) || (small + own) * a.c.Hkv >= (1ll << 30)) return MOBA_ERR_UNSUPPORTED;
+    x->cap_big = (int)big;
+    x->cap_small = (int)small;
     x->own_cap = (int)own;
-    x->cap_big = (int)nb;
-    x->cap_small = (int)nm;
     return MOBA_OK;
 }
 
@@ -758,9 +830,14 @@ cudaError_t launch_small(const SharedArgs &x, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_merge(const SharedArgs &x, cudaStream_t st) {
+    const Attn &a = x.a;
+    const long long spans = (long long)x.own_cap * a.c.Hkv, fill = 4 * (long long)a.ctas;
+    const int rows = a.chunk ? kJobRows : a.c.max_new * a.G < kSmallRows ? a.c.max_new * a.G : kSmallRows;
+    int most = a.chunk ? kMergeRows : rows;  // rows of a CTA: fewer where that leaves SMs without one
+    while (!a.chunk && most > 1 && spans * ((rows + most - 1) / most) < fill) most = (most + 1) / 2;
     note_launches(1);
-    return launch_after(merge_spans_kernel<D>, dim3((unsigned)(x.own_cap * x.a.c.Hkv), x.a.chunk ? kJobRows / kMergeRows : 1),
-                        dim3(32 * kMergeWarps), 0, st, x);
+    return launch_after(merge_spans_kernel<D>, dim3((unsigned)spans, (rows + most - 1) / most),
+                        dim3(32 * kMergeWarps), 0, st, x, most);
 }
 
 }  // namespace
@@ -824,8 +901,8 @@ MOBA_EXPORT int moba_paged_attn_shared(const void *q, const void *k_pages, const
     }
     scratch(&x, workspace);
     cudaError_t e = launch_plan(x, st);
-    if (e == cudaSuccess && x.cap_big) e = launch_chunk_spans(a, st);
-    if (e == cudaSuccess && x.cap_small) e = D == 64 ? launch_small<64>(x, st) : launch_small<128>(x, st);
+    if (e == cudaSuccess && (x.cap_big || a.chunk)) e = launch_chunk_spans(a, st);
+    if (e == cudaSuccess && !a.chunk) e = D == 64 ? launch_small<64>(x, st) : launch_small<128>(x, st);
     if (e == cudaSuccess) e = D == 64 ? launch_merge<64>(x, st) : launch_merge<128>(x, st);
     if (own) {
         const cudaError_t f = cudaFreeAsync(own, st);

@@ -120,6 +120,15 @@ def test_a_long_prefix_over_every_cta():
     case([(8192, [(2, 2)]), (4096, [(1, 1), (1, 4096)])], 6, 3, 128, 32, seed=7)
 
 
+@pytest.mark.parametrize("d,page", [(64, 64), (128, 16)])
+def test_groups_of_many_rows_beside_groups_of_few(d, page):
+    """Units enough that groups of more than 16 rows go to the tensor cores, and few rows do
+    not; prefixes that end inside a key tile; a group of more than 256 rows."""
+    groups = [(3328 + page, [(1, 1 + i % 40) for i in range(40)]), (1984, [(2, 50)]), (512, [(1, 3)] * 3),
+              (2560, [(2, 2 + i) for i in range(35)])]
+    case(groups, 32, 8, d, page, seed=17)
+
+
 def test_many_groups():
     """More groups and sequences than the plan's threads."""
     groups = [(16 * (i % 3), [(1, 1 + i % 4)] * (1 + i % 2)) for i in range(1300)]
