@@ -618,17 +618,18 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
 // merge
 // ----------------------------------------------------------------------------
 // A CTA takes up to `most` rows of a sequence's own span on a kv head, whose parts and whose
-// group's it looks up once; W warps to a row, every W-th part each, where rows are few (they
-// have many parts then).
-constexpr int kMergeWarps = 8, kMergeRows = 32;
+// group's it looks up once.  Its threads are teams of 16, a row each; W of them to a row,
+// every W-th part each, where rows are few (they have many parts then).
+constexpr int kMergeThreads = 256, kTeam = 16, kTeams = kMergeThreads / kTeam, kMergeRows = 32;
 
-template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_spans_kernel(SharedArgs x, int most) {
-    constexpr int V = D / 32, U = 4;
-    __shared__ float s_acc[kMergeWarps][D], s_m[kMergeWarps], s_l[kMergeWarps];
+template <int D, int TEAM>
+__global__ void __launch_bounds__(kMergeThreads, TEAM == 16 ? 3 : 4) merge_spans_kernel(SharedArgs x, int most) {
+    constexpr int V = D / TEAM, U = 4, kTeams = kMergeThreads / TEAM;
+    __shared__ __align__(16) float s_acc[kTeams][D];
+    __shared__ float s_m[kTeams], s_l[kTeams];
     const Attn &a = x.a;
     after_previous();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.G, Hkv = a.c.Hkv;
+    const int team = threadIdx.x / TEAM, lane = threadIdx.x % TEAM, G = a.G, Hkv = a.c.Hkv;
     const bool chunk = a.chunk;
     // (a span behind the last one is some memory of the scratch)
     const int w = (int)blockIdx.x / Hkv, hk = blockIdx.x % Hkv;
@@ -637,8 +638,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_spans_kernel(Shared
     if (w >= groups) return;
     const int r0 = blockIdx.y * most, rows = min(s.nrows - r0, most);
     if (rows <= 0) return;
-    const int W = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8, part = warp % W;
-    for (int ri = warp / W; ri < (W > 1 ? kMergeWarps / W : rows); ri += kMergeWarps / W) {
+    const int slots = rows > 4 ? 8 : rows > 2 ? 4 : rows > 1 ? 2 : 1;  // rows at a time
+    const int W = rows > 8 || kTeams == slots ? 1 : kTeams / slots;    // teams to a row
+    const int part = team % W;
+    for (int ri = team / W; ri < (W > 1 ? kTeams / W : rows); ri += kTeams / W) {
         const bool live = ri < rows;
         const int row = s.row0 + r0 + ri;
         float M = -INFINITY, L = 0.f, acc[V];
@@ -706,26 +709,26 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) merge_spans_kernel(Shared
                 for (int d = 0; d < V; ++d) acc[d] = fmaf(v[j][d], g, acc[d]);
             }
         }
-        if (W > 1) {  // (one round: every warp is here)
+        if (W > 1) {  // (one round: every team is here)
 #pragma unroll
-            for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
+            for (int k = 0; k < V; ++k) s_acc[team][lane * V + k] = acc[k];
             if (lane == 0) {
-                s_m[warp] = M;
-                s_l[warp] = bad ? -1.f : L;
+                s_m[team] = M;
+                s_l[team] = bad ? -1.f : L;
             }
             __syncthreads();
             if (!live || part) return;
             M = -INFINITY;
             L = 0.f;
             bad = false;
-            for (int i = warp; i < warp + W; ++i) {
+            for (int i = team; i < team + W; ++i) {
                 M = fmaxf(M, s_m[i]);
                 bad |= s_l[i] < 0.f;
             }
             const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
             for (int k = 0; k < V; ++k) acc[k] = 0.f;
-            for (int i = warp; i < warp + W; ++i) {
+            for (int i = team; i < team + W; ++i) {
                 const float f = mma::fast_exp2(s_m[i] - ref);
                 L = fmaf(s_l[i], f, L);
 #pragma unroll
@@ -835,9 +838,10 @@ cudaError_t launch_merge(const SharedArgs &x, cudaStream_t st) {
     const int rows = a.chunk ? kJobRows : a.c.max_new * a.G < kSmallRows ? a.c.max_new * a.G : kSmallRows;
     int most = a.chunk ? kMergeRows : rows;  // rows of a CTA: fewer where that leaves SMs without one
     while (!a.chunk && most > 1 && spans * ((rows + most - 1) / most) < fill) most = (most + 1) / 2;
+    const dim3 grid((unsigned)spans, (rows + most - 1) / most);
     note_launches(1);
-    return launch_after(merge_spans_kernel<D>, dim3((unsigned)spans, (rows + most - 1) / most),
-                        dim3(32 * kMergeWarps), 0, st, x, most);
+    return a.chunk ? launch_after(merge_spans_kernel<D, 16>, grid, dim3(kMergeThreads), 0, st, x, most)
+                   : launch_after(merge_spans_kernel<D, 32>, grid, dim3(kMergeThreads), 0, st, x, most);
 }
 
 }  // namespace
