@@ -4,7 +4,8 @@ leave, over the paged entry points of ``ops``.
 :class:`Pages` keeps the books (which page holds which tokens of which sequence,
 and who shares it) without touching a device; :class:`PagedCache` owns the pools
 of every layer and carries the books' decisions out with ``ops.page_copy``,
-``ops.rope``, ``ops.paged_append`` and ``ops.paged_attn``.
+``ops.rope``, ``ops.paged_append`` (or ``ops.paged_append_rope``, which does both) and
+``ops.paged_attn`` (or ``ops.paged_attn_shared``, for forks).
 """
 from __future__ import annotations
 
@@ -140,6 +141,37 @@ class Pages:
         self.truncate(seq, 0)
         del self._pages[seq], self._length[seq]
 
+    def shared_pages(self, a: int, b: int) -> int:
+        """How many pages two sequences have in common, from their first one on."""
+        x, y = self._pages[a], self._pages[b]
+        low, high = 0, min(len(x), len(y))  # (what is shared, forks share from the first page on)
+        while low < high:
+            mid = (low + high + 1) // 2
+            if x[mid - 1] == y[mid - 1]:
+                low = mid
+            else:
+                high = mid - 1
+        return low
+
+    def groups(self, counts: dict) -> list:
+        """Runs of neighbours in ``counts`` (new tokens of each sequence, taken as grown by
+        them) that share pages before their new tokens: (first, behind the last, tokens
+        shared) of each run that saves reading, among all of them."""
+        seqs = list(counts)
+        before = [(self._length[s] - counts[s]) // self.page_size for s in seqs]
+        runs, i = [], 0
+        while i < len(seqs):
+            j, common = i + 1, before[i]
+            while j < len(seqs) and common:
+                c = min(common, before[j], self.shared_pages(seqs[i], seqs[j]))
+                if c * (j - i) < common * (j - i - 1) or c == 0:
+                    break  # (less would be saved with it than without)
+                common, j = c, j + 1
+            if j > i + 1:
+                runs.append((i, j, common * self.page_size))
+            i = j
+        return runs
+
     def compaction(self) -> list:
         """What :meth:`compact` will move, into pages that are free until then."""
         live = self.num_pages - len(self._free)
@@ -170,6 +202,18 @@ class Batch:
     positions: torch.Tensor    # [total] int32
     max_new: int
     total: int
+    # sequences that share prefixes, as ops.paged_attn_shared takes them (None: too little
+    # is shared for it to pay)
+    cu_groups: torch.Tensor | None = None     # [groups + 1] int32
+    prefix_lens: torch.Tensor | None = None   # [groups] int32
+
+
+# What has to be saved in reading before sharing pays, and the rows of a sequence on a kv head
+# (new tokens, times query heads to one) up to which it does: us by themselves and shared, 32 / 8
+# heads of 128, sequences of 256 tokens behind 8192 shared ones: 2 of them 27 and 28 (34 MB saved),
+# 4 34 and 30 (101 MB), 16 73 and 40; 16 of 25 rows behind 2048 and 8192 28 and 34 (31 MB), 52 and 44
+# (126 MB); with 256 rows the products bound both, 133 and 151 for 16 of them.
+SHARED_BYTES, SHARED_ROWS = 1 << 26, 64
 
 
 class PagedCache:
@@ -249,19 +293,50 @@ class PagedCache:
             rows.append(list(self.books.pages(seq)))
         width = max(1, max(len(r) for r in rows))
         table = [r + [-1] * (width - len(r)) for r in rows]
+        groups = []
+        hkv, d = self.k_pages.shape[2], self.k_pages.shape[4]
+        runs = self.books.groups(counts)
+        if sum((j - i - 1) * n for i, j, n in runs) * hkv * d * 4 >= SHARED_BYTES:
+            edges, shared = [0], []
+            for i, j, n in runs:
+                if i > edges[-1]:  # (sequences that share nothing, as a group that does not)
+                    edges.append(i)
+                    shared.append(0)
+                edges.append(j)
+                shared.append(n)
+            groups = [self._ints(edges), self._ints(shared)]
         return Batch(seqs, self._ints(table), self._ints(cu), self._ints(lens), self._ints(positions),
-                     max(1, max(counts.values())), cu[-1])
+                     max(1, max(counts.values())), cu[-1], *groups)
 
     def attend(self, layer: int, batch: Batch, q, k, v, topk: int, freqs=None,
-               interleaved: bool = False, magnitude: float = 1.0, stream=None, **kw):
+               interleaved: bool = False, magnitude: float = 1.0, stream=None, norms=None,
+               eps: float = 1e-6, **kw):
         """One layer of a step: q and k rotated to the tokens' positions (with
         ``freqs``, see ``ops.rope_frequencies``), k and v appended, and the attention
         -> (out, lse, idx) of ``ops.paged_attn`` (further arguments go to it), all on
-        ``stream`` (None: the current one)."""
-        if freqs is not None:
-            q, k = ops.rope(q, k, batch.positions, freqs, interleaved, magnitude, stream=stream)
+        ``stream`` (None: the current one).
+
+        With ``norms``, (q_weight, k_weight) of ``ops.qk_norm_rope`` (either may be None: that
+        operand is only rotated), q and k are normalised, rotated and appended in one
+        pass, and q, k and v may be slices of one projection.  Where topk covers every
+        block, sequences that follow one another in the batch and share much of their
+        past (forks) are attended together (``ops.paged_attn_shared``; idx None), unless an
+        argument asks for what only ``ops.paged_attn`` gives."""
         pools = self.k_pages[layer], self.v_pages[layer], self.kbar_pages[layer]
-        ops.paged_append(k, v, *pools, batch.page_table, batch.cu_new, batch.cache_lens,
-                         batch.max_new, self.block_size, pooling=self.pooling, stream=stream)
-        return ops.paged_attn(q, *pools, batch.page_table, batch.cu_new, batch.cache_lens,
-                              batch.max_new, self.block_size, topk, stream=stream, **kw)
+        tables = batch.page_table, batch.cu_new, batch.cache_lens, batch.max_new
+        if norms is not None:
+            if freqs is None:
+                raise ValueError("norms need freqs")
+            q = ops.paged_append_rope(q, k, v, *pools, *tables, self.block_size, freqs, q_weight=norms[0],
+                                      k_weight=norms[1], eps=eps, interleaved=interleaved,
+                                      magnitude=magnitude, pooling=self.pooling, stream=stream)
+        else:
+            if freqs is not None:
+                q, k = ops.rope(q, k, batch.positions, freqs, interleaved, magnitude, stream=stream)
+            ops.paged_append(k, v, *pools, *tables, self.block_size, pooling=self.pooling, stream=stream)
+        if batch.cu_groups is not None and not set(kw) - {"out", "lse"}:
+            every = -(-batch.page_table.shape[1] * self.books.page_size // self.block_size)
+            if topk >= every and batch.max_new * q.shape[1] // k.shape[1] <= SHARED_ROWS:
+                return *ops.paged_attn_shared(q, *pools[:2], *tables, batch.cu_groups, batch.prefix_lens,
+                                              stream=stream, **kw), None
+        return ops.paged_attn(q, *pools, *tables, self.block_size, topk, stream=stream, **kw)
