@@ -112,6 +112,25 @@ __device__ __forceinline__ Entry get_entry(const Attn &a, int e) {
     return x;
 }
 
+// The span that unit u lies in: the last one that starts at or before it, 128 places a
+// look.  All lanes of a warp call it, with the same arguments.
+__device__ __forceinline__ int span_of_unit(const long long *off, int spans, long long u, int lane) {
+    int w = 0;
+    for (int n = spans; n > 1;) {  // the answer is in [w, w + n)
+        const int step = (n + 127) / 128;
+        int last = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int at = (32 * j + lane) * step;
+            last += __popc(__ballot_sync(0xffffffffu, at < n && off[w + at] <= u));
+        }
+        last = max(last - 1, 0);
+        n = min(step, n - last * step);
+        w += last * step;
+    }
+    return w;
+}
+
 // The rows of refused sequence s, heads [h0, h0 + nh): thread `at` of `threads`
 // that clear them together.  By sequence, not by tile: its rows may be more than
 // max_new, and lie where no tile begins.

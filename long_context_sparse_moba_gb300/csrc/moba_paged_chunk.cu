@@ -285,6 +285,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 11) {
         // ================= job descriptors =================
+        // (spans: the run's first one is looked for by the whole warp)
+        int first_span = 0;
+        if constexpr (SPANS) {
+            const long long total = a.head->units[0], runs = total < (long long)gridDim.x ? total : (long long)gridDim.x;
+            if ((long long)blockIdx.x < runs)
+                first_span = span_of_unit(a.off_big, a.head->spans[0], total * blockIdx.x / runs, lane);
+        }
         if (lane == 0) {
             int n = 0;
             auto hand = [&](const Job &J) -> bool {
@@ -307,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((long long)blockIdx.x < runs) {
                     long long u = total * blockIdx.x / runs;
                     const long long u1 = total * (blockIdx.x + 1) / runs;
-                    int w = 0, hi = tiles - 1;  // largest row tile that starts at or before u
+                    int w = first_span, hi = SPANS ? w : tiles - 1;  // largest row tile that starts at or before u
                     while (w < hi) {
                         const int mid = (w + hi + 1) >> 1;
                         if (off[mid] <= u) w = mid; else hi = mid - 1;

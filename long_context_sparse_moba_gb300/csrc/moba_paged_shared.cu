@@ -390,14 +390,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
         if (dynamic && lane == 0) next = atomicAdd(&a.head->taken, 1);
         const long long u0 = begin(run);
         const int n = (int)(begin(run + 1) - u0);
-        int w = 0;  // the span with unit u0: the last that starts at or before it
-        for (int k = spans; k > 1;) {
-            const int step = (k + 31) / 32;
-            const bool below = lane * step < k && x.off_small[w + lane * step] <= u0;
-            const int last = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
-            k = min(step, k - last * step);
-            w += last * step;
-        }
+        int w = span_of_unit(x.off_small, spans, u0, lane);
         // ---- copies ----
         int ahead = 0, wa = w;              // units of the run that have been issued; a span at or before the next
         int place = 0;                      // lane: its unit of the 32 at hand: first row of the pools (-1: no keys)
