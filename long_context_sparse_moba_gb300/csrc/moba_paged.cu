@@ -265,6 +265,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 // head that takes the groups of tokens (p % G) in turn.  A step completes few blocks, so a
 // CTA looks at several and leaves most.  A thread waits for that kernel when it comes to
 // the first new token: until then a block's older keys are on their way.
+// Bound: latency (a block's keys in four rounds of loads).  32 blocks of 512 on 8 kv heads of
+// 128 16 us; one of 64 sequences' 5 beside the kernel before it (9 where every thread waited
+// first; clusters of append_kernel's kind 11 and 19).
 constexpr int kPoolThreads = 256, kPoolCtas = 3;  // of an SM
 
 template <int D, bool MAX>

@@ -12,7 +12,14 @@
 // Everything between the loads and the one rounding of the result is fp32; r and n are
 // made again from x in the gradient, which costs nothing where x has to be read anyway.
 //
-// Bound: HBM (4 bytes a value, 6 in the gradient).
+// Bound: HBM (4 bytes a value, 6 in the gradient).  A lane has 16 values of a head, eight
+// pairs, so that the norm is three shuffles; the phases of a token are made once by the
+// warp's lanes; arithmetic is on pairs.  Measured: 32768 tokens of 64 heads of 128 167 us,
+// 6.4 TB/s, 0.95 of the copy rate, straight from memory to registers; the gradient of 32764
+// tokens of 32 heads, half of each rotated, 128 us in its kernel, 6.3 TB/s, and 3.5 for the
+// weights' sums, 140 by the call.  (The gradient from memory to registers took 144: its 16 warps an
+// SM waited for loads half of the time; with the phases made by every lane for itself
+// and 64-bit unit numbers 170.)
 #include <cmath>
 
 #include "moba.h"
