@@ -565,8 +565,9 @@ int moba_paged_append(const void *k, const void *v, void *k_pages, void *v_pages
  *   q_weight, k_weight : [D] bf16 or fp32 (weight_bits 16 or 32), or NULL: that operand
  *     is rotated only; weight_bits and eps count where one is given
  *   freqs, rot_dim, interleaved, magnitude, eps: as for moba_qk_norm_rope
- * q_out may be q; an overlap with anything else is MOBA_ERR_INVALID_ARG.  Rows of q_out
- * of refused sequences, and behind the last one, are left as they were.
+ * q_out may be q; an overlap with k or v is MOBA_ERR_INVALID_ARG.  Rows of q_out of
+ * refused sequences, and behind the last one, are left as they were (rows of q, k and v
+ * there are read, and come to nothing).
  */
 int moba_paged_append_rope(const void *q, const void *k, const void *v, void *q_out, void *k_pages,
                            void *v_pages, float *kbar_pages, const int32_t *page_table,

@@ -474,7 +474,7 @@ int make_pool(AppendArgs *a, const Cache &c, void *k_pages, float *kbar_pages, i
     a->status = status;
     const int rc = plan_blocks(a);
     if (rc != MOBA_OK) return rc;
-    return a->clusters * c.Hkv >= (1ll << 31) ? MOBA_ERR_UNSUPPORTED : MOBA_OK;
+    return a->clusters * c.Hkv >= (1ll << 30) ? MOBA_ERR_UNSUPPORTED : MOBA_OK;
 }
 
 cudaError_t launch_pool(const AppendArgs &a, int D, bool max, cudaStream_t st) {

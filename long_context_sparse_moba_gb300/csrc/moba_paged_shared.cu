@@ -36,16 +36,21 @@ constexpr int kSmallRows = 16;   // of a small span
 constexpr int kUnit = 16;        // keys that a warp takes at a time: never more than a page
 constexpr int kBigKeys = 128;    // of a key tile of the tcgen05 kernel
 constexpr int kStreamWarps = 4, kStreamCtas = 3;  // of a CTA, of an SM
-constexpr int kMinUnits = 6;     // units of a warp's run at least, where there are few
+// Units of a warp's run at least, where there are few.  (us in a graph with 3, 6 and 12: four forks
+// of 1024 tokens 17, 19, 21; two of 32768 on 8 kv heads, which have many parts then, 51, 51, 47)
+constexpr int kMinUnits = 3;
 // The start of a span on a kv head counts as that many units, its rows and sums being
-// what they cost: runs of equal units then take equal time.
+// what they cost: runs of equal units then take equal time.  (Of small ones 0, 2, 4: three groups
+// 44, 41, 41 us; of big ones, kBigStart, 1, 3, 5: 8 questions on 16384 tokens 243, 182, 186)
 constexpr int kSmallStart = 2;
 // From kDynamic units a warp on, a quarter of them is cut into runs (kShort a warp) that the
 // warps take as they become free: SMs differ, by their distance from the memory, in what
-// they get through (160 K to 210 K cycles of equal runs).
+// they get through.  (16 forks of 16384 tokens on 32 kv heads 109 us without, 107 with; 64 forks of
+// 2048 tokens, at 13 units a warp, 40 without, 51 with)
 constexpr int kDynamic = 24, kShort = 2;
 // Groups' prefixes are streamed whatever their rows where that is no more than so many
-// units a warp: the tcgen05 kernel takes 20 us to begin with.
+// units a warp: the tcgen05 kernel takes 20 us to begin with.  (8, 16 and 32: 64 forks of 2048
+// tokens on 8 kv heads 46, 40, 40 us; three groups of some 170 rows and up to 9000 tokens 41, 41, 69)
 constexpr int kFewUnits = 16;
 
 struct SharedArgs {

@@ -589,8 +589,8 @@ def _heads(t, device, name):
     if t.dim() == 3:  # (the usual cases in few looks: dense, or slices of one projection)
         T, H, D = t.shape
         s, w = t.stride(), H * D
-        if s[2] == 1 and s[1] == D and w > 0 and s[0] >= w:
-            return T, H, D, s[0]
+        if s[2] == 1 and s[1] == D and w > 0 and (T < 2 or s[0] >= w):
+            return T, H, D, s[0] if T > 1 else w
     H, D = t.shape[-2:]
     if t.is_contiguous():
         return t.numel() // max(1, H * D), H, D, H * D

@@ -250,6 +250,17 @@ def test_a_side_stream_and_a_graph():
     assert all(torch.equal(a, b) for a, b in zip(outs, both()))
 
 
+def test_one_token_of_an_odd_stride():
+    """A single token's stride does not matter."""
+    q = normal(1, 203).as_strided((1, 3, 64), (203, 64, 1))
+    assert q.stride(0) % 8
+    w, pos, freqs = weights(2, 64, BF), i32([9]), ops.rope_frequencies(64)
+    check_forward(ops.qk_norm_rope(q, None, w, None, pos, freqs)[0], q, w, pos, freqs, 1e-6, False)
+    assert torch.equal(ops.rope(q, None, pos, freqs)[0], ops.rope(q.contiguous(), None, pos, freqs)[0])
+    dq, _, dw, _ = ops.qk_norm_rope_bwd(q, None, q, None, w, None, pos, freqs)
+    check_gradient(dq, dw, q, q, w, pos, freqs, 1e-6, False)
+
+
 def test_no_tokens():
     q, k = normal(1, 0, 4, 64), normal(2, 0, 2, 64)
     w, pos, freqs = weights(3, 64, BF), i32([]), ops.rope_frequencies(64)
