@@ -631,9 +631,11 @@ size_t moba_paged_attn_workspace_size(int num_seqs, int total, int max_new, int 
  * The page table's rows of a group name the same pages for the prefix; those of its first
  * sequence with new tokens are read.  Groups whose offsets decrease or leave [0, num_seqs]
  * (no group counts then), a prefix that is negative, no multiple of page_size, wider than
- * the table or longer than what a member has before its new tokens, and a refused member
- * (the group counts for nothing then) record MOBA_ERR_INVALID_ARG in the device status
- * word; the sequences are attended by their own pages all the same.
+ * the table or longer than what a member has before its new tokens, a member whose prefix ends
+ * on another page than that sequence's (the pages before it are not compared) and a refused
+ * member (the group counts for nothing then) record MOBA_ERR_INVALID_ARG in the device
+ * status word; the sequences are attended by their own pages all the same.  Members are those
+ * with new tokens.
  *   n_groups 0 (cu_groups and prefix_lens may be NULL): no sequence shares
  * q, out, lse, the cache, refused sequences, pages outside the pool, values that are not
  * finite (rows of a group are computed together) and workspace: as for moba_paged_attn, the

@@ -183,6 +183,18 @@ __global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
             }
     }
     sync();
+    // and one whose prefix ends on another page than the lender's: what the groups were
+    // made of has changed since (a load a member: 0.7 us of the plan's)
+    for (int b = tid; !none && b < ns; b += T) {
+        Seq s;
+        const int g = group_of(b);
+        if (g < 0 || seq(b, s) != kSeqOk) continue;
+        const int l = HELD ? *(volatile const int *)(rep + g) : __ldcg(rep + g), page = pre(g) / c.ps - 1;
+        if (l < 0 || l == b || page < 0) continue;
+        if (__ldg(c.table + (size_t)b * c.max_pages + page) != __ldg(c.table + (size_t)l * c.max_pages + page))
+            atomicMin(rep + g, -1);
+    }
+    sync();
     // units of all groups, were they streamed
     auto lent = [&](int g, int &rows) {  // the sequence that lends its pages, and the group's rows; or -1
         const int l = HELD ? rep[g] : __ldcg(rep + g);  // (where the atomics left it)
@@ -696,7 +708,7 @@ __global__ void __launch_bounds__(kMergeThreads, TEAM == 16 ? 3 : 4) merge_spans
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 bad |= z[j].y < 0.f;
-                if (!(z[j].y > 0.f)) z[j].x = -INFINITY;  // no part, or one without a key for this row
+                if (z[j].y == 0.f) z[j].x = -INFINITY;  // no part, or one without a key for this row
                 top = fmaxf(top, z[j].x);
             }
             const float ref = top == -INFINITY ? 0.f : top, f = mma::fast_exp2(M - ref);
@@ -706,7 +718,7 @@ __global__ void __launch_bounds__(kMergeThreads, TEAM == 16 ? 3 : 4) merge_spans
             for (int d = 0; d < V; ++d) acc[d] *= f;
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                if (z[j].x == -INFINITY) continue;
+                if (z[j].y == 0.f) continue;  // (a sum that is not a number stays in)
                 const float g = mma::fast_exp2(z[j].x - ref);
                 L = fmaf(z[j].y, g, L);
 #pragma unroll

@@ -310,7 +310,7 @@ class PagedCache:
 
     def attend(self, layer: int, batch: Batch, q, k, v, topk: int, freqs=None,
                interleaved: bool = False, magnitude: float = 1.0, stream=None, norms=None,
-               eps: float = 1e-6, **kw):
+               eps: float = 1e-6, shared: bool | None = None, **kw):
         """One layer of a step: q and k rotated to the tokens' positions (with
         ``freqs``, see ``ops.rope_frequencies``), k and v appended, and the attention
         -> (out, lse, idx) of ``ops.paged_attn`` (further arguments go to it), all on
@@ -321,7 +321,9 @@ class PagedCache:
         pass, and q, k and v may be slices of one projection.  Where topk covers every
         block, sequences that follow one another in the batch and share much of their
         past (forks) are attended together (``ops.paged_attn_shared``; idx None), unless an
-        argument asks for what only ``ops.paged_attn`` gives."""
+        argument asks for what only ``ops.paged_attn`` gives, or ``shared`` is False.  A graph
+        that is being captured gets them together only with ``shared`` True: its replays read
+        cu_groups and prefix_lens too, which have to go with the page table that they read."""
         pools = self.k_pages[layer], self.v_pages[layer], self.kbar_pages[layer]
         tables = batch.page_table, batch.cu_new, batch.cache_lens, batch.max_new
         if norms is not None:
@@ -334,7 +336,9 @@ class PagedCache:
             if freqs is not None:
                 q, k = ops.rope(q, k, batch.positions, freqs, interleaved, magnitude, stream=stream)
             ops.paged_append(k, v, *pools, *tables, self.block_size, pooling=self.pooling, stream=stream)
-        if batch.cu_groups is not None and not set(kw) - {"out", "lse"}:
+        if shared is None and batch.cu_groups is not None:
+            shared = not (batch.page_table.is_cuda and torch.cuda.is_current_stream_capturing())
+        if shared and batch.cu_groups is not None and not set(kw) - {"out", "lse"}:
             every = -(-batch.page_table.shape[1] * self.books.page_size // self.block_size)
             if topk >= every and batch.max_new * q.shape[1] // k.shape[1] <= SHARED_ROWS:
                 return *ops.paged_attn_shared(q, *pools[:2], *tables, batch.cu_groups, batch.prefix_lens,

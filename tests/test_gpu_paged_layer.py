@@ -87,3 +87,63 @@ def test_a_server_with_forks(monkeypatch, hq, hkv, d, page, block, interleaved, 
     assert s.c.compact() > 0
     s.step({e: 1, c: 1, f: 1, b: 1})
     assert s.shared >= 4
+
+
+def test_a_captured_step_of_forks(monkeypatch):
+    """Whose page table is rewritten between replays: each by itself, unless the graph is asked to
+    take them together, with groups that are rewritten too."""
+    monkeypatch.setattr(paged, "SHARED_BYTES", 1)
+    c = PagedCache(1, 64, 2, 64, 16, 64)
+    a, b = c.new(), c.new()
+    lens = {a: 128, b: 160}
+    hist = {}
+
+    def step(counts, seed, run):
+        batch = c.extend(counts)
+        q, k, v = (normal(seed + i, batch.total, h, 64) for i, h in ((0, 8), (1, 2), (2, 2)))
+        row = 0
+        for s in batch.seqs:
+            n = counts[s]
+            old = hist.get(s, (k[:0], v[:0]))
+            hist[s] = tuple(torch.cat((o, x[row:row + n])) for o, x in zip(old, (k, v)))
+            row += n
+        got = run(batch, q, k, v)
+        ks, vs = ([hist[s][i] for s in batch.seqs] for i in range(2))
+        compare(got, expect(q, ks, vs, Layer(c, 0, batch), [counts[s] for s in batch.seqs],
+                            [c.books.length(s) for s in batch.seqs], 64, 1000))
+        return batch
+
+    eager = lambda batch, q, k, v: c.attend(0, batch, q, k, v, 1000)
+    step(lens, 1, eager)
+    forks = [c.fork(s) for s in (a, a, b, b)]
+    for f, s in zip(forks, (a, a, b, b)):
+        hist[f] = hist[s]
+    pairs = [forks[:2], forks[2:]]
+    first = step({s: 1 for s in pairs[0]}, 11, eager)
+    assert first.cu_groups is not None
+    for shared in (None, True):
+        batch = c.extend({s: 1 for s in pairs[0]})
+        assert batch.cu_groups is not None
+        batch.page_table = torch.nn.functional.pad(batch.page_table, (0, 4), value=-1).contiguous()
+        q, k, v = (normal(21 + i, 2, h, 64) for i, h in ((0, 8), (1, 2), (2, 2)))
+        for i, s in enumerate(batch.seqs):
+            hist[s] = tuple(torch.cat((o, x[i:i + 1])) for o, x in zip(hist[s], (k, v)))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = c.attend(0, batch, q, k, v, 1000, shared=shared)
+        g.replay()
+
+        def replay(new, q2, k2, v2):
+            for x, y in ((q, q2), (k, k2), (v, v2), (batch.cu_new, new.cu_new), (batch.cache_lens, new.cache_lens)):
+                x.copy_(y)
+            batch.page_table.fill_(-1)
+            batch.page_table[:, :new.page_table.shape[1]] = new.page_table
+            if shared:
+                batch.cu_groups.copy_(new.cu_groups)
+                batch.prefix_lens.copy_(new.prefix_lens)
+            g.replay()
+            return got
+
+        for i, pair in enumerate((pairs[1], pairs[0], pairs[1])):
+            step({s: 1 for s in pair}, 31 + 3 * i, replay)
+        assert ops.get_status() == ops.MOBA_OK

@@ -270,3 +270,45 @@ def test_no_new_tokens():
     out, lse = torch.full_like(q, 7.0), torch.full((3, 4), 7.0, device="cuda")
     f.call(q, out=out, lse=lse)
     assert (out == 7).all() and (lse == 7).all() and ops.get_status() == ops.MOBA_OK
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("new,prefix", [((1, 1, 2), 512), ((2, 3, 13), 40960), ((70, 5, 40), 512)])
+def test_keys_that_are_not_finite_show(value, new, prefix):
+    """A NaN, or infinities that meet, in a key reach the rows that see it (a decode step, a group for
+    the tensor cores, chunks; in the prefix and in the own keys); another group stands."""
+    f = Forks([(prefix, [(n, 90) for n in new]), (512, [(1, 100), (2, 20)])], 2, 64, 32, seed=17)
+    q = normal(1, sum(f.nq), 16, 64)
+    q[..., 5] = q[..., 5].abs() + 0.1
+    want = f.call(q)
+    mine = sum(new)
+    f.k[f.rows[0][3], 1, 4, 5] = value  # kv head 1: query heads 8 to 15
+    out, lse = f.call(q)
+    assert ops.get_status() == ops.MOBA_OK
+    assert out[:mine, 8:].isnan().all() and lse[:mine, 8:].isnan().all()
+    for a, b in ((out, want[0]), (lse, want[1])):
+        assert torch.equal(a[:, :8], b[:, :8]) and torch.equal(a[mine:], b[mine:])
+    f.k[f.rows[0][3], 1, 4, 5] = 0.0
+    f.k[f.rows[1][prefix // 32], 0, 1, 5] = value  # a key of the second sequence alone
+    out, lse = f.call(q)
+    lo, hi = f.cu[1], f.cu[2]
+    assert out[lo:hi, :8].isnan().all() and lse[lo:hi, :8].isnan().all()
+    assert torch.equal(out[mine:], want[0][mine:]) and torch.equal(lse[mine:], want[1][mine:])
+
+
+@pytest.mark.parametrize("count", [4, 1100])
+@pytest.mark.parametrize("scale", [1, 40])
+def test_a_group_whose_tables_have_changed(scale, count):
+    """A row of the page table names another sequence's pages than when the groups were made:
+    by their own pages, and reported."""
+    f = Forks([(96, [(scale, 50 + i % 7) for i in range(count if scale == 1 else 4)]), (96, [(scale, 60), (1, 70)])],
+              1, 64, 32, seed=18)
+    q = normal(1, sum(f.nq), 4, 64)
+    want = f.expect(q)
+    n = len(f.nq)
+    got = f.call(q, cu_groups=[0, n - 1, n], prefixes=[96, 96])  # one of the second group's among the first's
+    assert ops.get_status() == ops.MOBA_ERR_INVALID_ARG
+    compare(got, want)
+    got = f.call(q, cu_groups=[0, n], prefixes=[96])
+    assert ops.get_status() == ops.MOBA_ERR_INVALID_ARG
+    compare(got, want)

@@ -110,7 +110,7 @@ def test_the_calls_of_a_layer(monkeypatch, stream):
     assert f.seen[0][1]["q_weight"] == "wq" and f.seen[0][1]["k_weight"] is None and f.seen[0][1]["eps"] == 1e-5
     assert all(s[1]["stream"] == stream for s in f.seen)
     # selection, an idx asked for, or many rows of a sequence: each by itself
-    for args, more in (((3,), {}), ((99,), {"with_idx": True}), ((99,), {"workspace": "w"})):
+    for args, more in (((3,), {}), ((99,), {"with_idx": True}), ((99,), {"workspace": "w"}), ((99,), {"shared": False})):
         f.seen.clear()
         assert c.attend(0, batch, q, k, "v", *args, **more, **kw) == (1, 2, 3)
         assert [s[0] for s in f.seen] == ["paged_append", "paged_attn"]
