@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
     }
     sync();
     // and one whose prefix ends on another page than the lender's: what the groups were
-    // made of has changed since (a load a member: 0.7 us of the plan's)
+    // made of has changed since (a load a member: 1 us; taken in the loop above, no less)
     for (int b = tid; !none && b < ns; b += T) {
         Seq s;
         const int g = group_of(b);
