@@ -1,7 +1,9 @@
-"""Compile the CUDA sources into ``libmoba_gb300.so`` (sm_103a only).
+"""Compile the CUDA sources into ``libmoba_gb300.so`` (sm_103a only), and the
+binding of the calls whose host time counts into ``moba_calls.so``.
 
 Each ``csrc/*.cu`` is compiled to an object in parallel, then nvcc links the
-shared library in-tree next to this file.  Run ``python -m
+shared library in-tree next to this file; ``csrc/moba_calls.cpp`` (host code on torch's
+headers, linked to that library) is compiled beside them.  Run ``python -m
 long_context_sparse_moba_gb300.build`` or call :func:`build`.
 """
 from __future__ import annotations
@@ -11,12 +13,16 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoba_gb300.so")
+CALLS = os.path.join(HERE, "moba_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "-I", INCLUDE]
@@ -31,6 +37,26 @@ def _nvcc() -> str:
 
 def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+
+
+def _calls_commands(lib: str):
+    """The binding's object, its compile command, and the command that links it.  The
+    object is that of one version of torch."""
+    root = os.path.dirname(torch.__file__)
+    libs = os.path.join(root, "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    obj = os.path.join(BUILD, f"moba_calls-{torch.__version__}.o")
+    cxx = os.environ.get("CXX") or "g++"
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                "-isystem", os.path.join(root, "include"),
+                "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+                "-c", os.path.join(CSRC, "moba_calls.cpp"), "-o", obj]
+    link = lambda to: [cxx, "-shared", "-o", to, obj, "-L", os.path.dirname(lib), "-l:" + os.path.basename(lib),
+                       "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-ltorch",
+                       "-lc10_cuda", "-lc10"]
+    return obj, compile_, link
 
 
 def _stale(target: str, deps) -> bool:
@@ -55,10 +81,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
+    calls_obj, calls_compile, calls_link = _calls_commands(LIB)
+    if force or _stale(calls_obj, [os.path.join(CSRC, "moba_calls.cpp"), os.path.join(INCLUDE, "moba.h")]):
+        jobs.insert(0, calls_compile)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+            raise RuntimeError("compiling failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
         return r.stdout + r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
@@ -69,6 +99,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if force or jobs or _stale(CALLS, [calls_obj]):
+        tmp = CALLS + f".tmp{os.getpid()}"
+        run(calls_link(tmp))
+        os.replace(tmp, CALLS)
     return LIB
 
 

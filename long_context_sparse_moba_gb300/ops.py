@@ -173,6 +173,31 @@ def lib():
     return _lib
 
 
+_calls = None
+
+
+def _native():
+    """The binding that makes the usual call of an operator in one step; None from it: step by
+    step, here."""
+    global _calls
+    if _calls is None:
+        lib()
+        try:
+            from . import moba_calls
+        except ImportError as e:
+            raise RuntimeError(f"moba_calls.so is missing or of another torch ({e}): build it with "
+                               "`python -m long_context_sparse_moba_gb300.build`") from e
+        _calls = moba_calls
+    return _calls
+
+
+def _usual(answer, what: str):
+    """The results of a call by the binding (a CUDA error's code raises)."""
+    if type(answer) is int:
+        _check(answer, what)
+    return answer
+
+
 def status_string(code: int) -> str:
     return lib().moba_status_string(code).decode()
 
@@ -740,6 +765,11 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, eps: float = 1e-6,
     Hq, D] and k [..., Hk, D] bf16 (k and k_weight may be None) over its root mean square,
     times the weights [D] (bf16 or fp32), rotated -> (q_out, k_out).  Operands, positions
     and freqs are those of :func:`rope`; q_out / k_out may be q / k (in place)."""
+    if stream is None:
+        r = _native().qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, eps, interleaved, magnitude,
+                                   q_out, k_out)
+        if r is not None:
+            return _usual(r, "moba_qk_norm_rope")
     device, T, Hq, Hk, D, qs, ks, bits = _norm_operands(q, k, q_weight, k_weight, positions, freqs)
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
@@ -774,6 +804,11 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, freqs,
     heads.  dq / dk may be dq_out / dk_out (in place).  ``workspace`` is a uint8 CUDA tensor
     of at least :func:`qk_norm_rope_bwd_workspace_size` bytes, or None (scratch from torch's
     allocator, on the call's stream).  No tokens: weight gradients of zero."""
+    if stream is None:
+        r = _native().qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, freqs, eps,
+                                       interleaved, magnitude, dq, dk, dq_weight, dk_weight, workspace)
+        if r is not None:
+            return _usual(r, "moba_qk_norm_rope_bwd")
     device, T, Hq, Hk, D, qs, ks, bits = _norm_operands(q, k, q_weight, k_weight, positions, freqs)
     if dq_out.shape != q.shape or (k is None) != (dk_out is None) or \
             (k is not None and dk_out.shape != k.shape):
@@ -876,6 +911,12 @@ def paged_append_rope(q, k, v, k_pages, v_pages, kbar_pages, page_table, cu_new,
     pages -> q_out (q itself for in place).  The tokens of q, k and v may be a stride apart
     (slices of one projection).  Rows of q_out behind the last sequence, and of refused
     ones, are left as they were."""
+    if stream is None and pooling == POOL_MEAN:
+        r = _native().paged_append_rope(q, k, v, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens,
+                                        max_new, block_size, freqs, positions, q_weight, k_weight, eps,
+                                        interleaved, magnitude, q_out)
+        if r is not None:
+            return _usual(r, "moba_paged_append_rope")
     device = _device(k_pages, "k_pages")
     P, Hkv, ps, D, n, mp, bar = _paged(device, k_pages, v_pages, kbar_pages, page_table, cu_new,
                                        cache_lens)
@@ -980,6 +1021,11 @@ def paged_attn_shared(q, k_pages, v_pages, page_table, cu_new, cache_lens, max_n
     sequences of no group share nothing.  ``workspace`` is a uint8 CUDA tensor of at least
     :func:`paged_attn_shared_workspace_size` bytes, or None (scratch from torch's allocator,
     on the call's stream)."""
+    if stream is None:
+        r = _native().paged_attn_shared(q, k_pages, v_pages, page_table, cu_new, cache_lens, max_new, cu_groups,
+                                        prefix_lens, out, lse, workspace)
+        if r is not None:
+            return _usual(r, "moba_paged_attn_shared")
     device = _device(k_pages, "k_pages")
     P, Hkv, ps, D, n, mp, _ = _paged(device, k_pages, v_pages, None, page_table, cu_new, cache_lens)
     _tensor(q, torch.bfloat16, device, "q")
