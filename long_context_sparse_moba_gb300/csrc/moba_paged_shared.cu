@@ -64,6 +64,7 @@ struct SharedArgs {
     int own_cap;                 // sequences' own spans, at most
     int warps;                   // of the streaming kernel
     int psh;                     // log2(page size)
+    bool beside;                 // big spans' kernel runs before the small ones', which begin as its CTAs end
     // scratch
     Span *tiles_small;           // [...]
     long long *off_small;        // [... + 1] units before each (and kSmallStart), times the kv heads
@@ -391,7 +392,11 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
         ptx::fence_mbar_init();
     }
     __syncthreads();
-    after_previous();
+    // Behind the plan.  Where the big spans' kernel lies between them: it lets this one begin once
+    // all its CTAs have waited for the plan, and this one needs nothing of its results, so
+    // that it only has to end behind it (the merge waits for this one's end).
+    if (x.beside) __threadfence();  // (what the plan wrote, not what this SM may still hold)
+    else after_previous();
     let_next();
     ptx::Ctl ctl{&s_abort, a.status, kDefaultWaitLimit};
     const uint32_t raw = ptx::saddr(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -623,11 +628,12 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
         }
         if (!ok) {  // copies in flight land before the CTA ends
             for (; used < issued; ++used) ptx::drain_bar(bars + 8 * (used % ST), (used / ST) & 1, kDefaultWaitLimit);
-            return;
+            break;
         }
         next = __shfl_sync(0xffffffffu, next, 0);
         if (next >= shorts) break;
     }
+    if (x.beside) after_previous();
 }
 
 // ----------------------------------------------------------------------------
@@ -920,6 +926,7 @@ MOBA_EXPORT int moba_paged_attn_shared(const void *q, const void *k_pages, const
         workspace = own;
     }
     scratch(&x, workspace);
+    x.beside = x.cap_big && !a.chunk;
     cudaError_t e = launch_plan(x, st);
     if (e == cudaSuccess && (x.cap_big || a.chunk)) e = launch_chunk_spans(a, st);
     if (e == cudaSuccess && !a.chunk) e = D == 64 ? launch_small<64>(x, st) : launch_small<128>(x, st);
