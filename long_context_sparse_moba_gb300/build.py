@@ -40,12 +40,11 @@ def sources():
 
 
 def _calls_commands(lib: str):
-    """The binding's object, its compile command, and the command that links it.  The
-    object is that of one version of torch."""
+    """The binding's object, its compile command, and the command that links it to ``to``."""
     root = os.path.dirname(torch.__file__)
     libs = os.path.join(root, "lib")
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
-    obj = os.path.join(BUILD, f"moba_calls-{torch.__version__}.o")
+    obj = os.path.join(BUILD, f"moba_calls-{torch.__version__}.o")  # (of one version of torch)
     cxx = os.environ.get("CXX") or "g++"
     compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -99,10 +98,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if force or jobs or _stale(CALLS, [calls_obj]):
+    stamp = os.path.join(BUILD, "moba_calls.torch")  # the version that CALLS is linked to
+    linked = ""
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            linked = f.read()
+    if force or jobs or _stale(CALLS, [calls_obj]) or linked != torch.__version__:
         tmp = CALLS + f".tmp{os.getpid()}"
         run(calls_link(tmp))
         os.replace(tmp, CALLS)
+        with open(stamp + f".tmp{os.getpid()}", "w") as f:
+            f.write(torch.__version__)
+        os.replace(f.name, stamp)
     return LIB
 
 
