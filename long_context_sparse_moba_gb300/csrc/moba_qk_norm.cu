@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(32 * kWarps) fwd_kernel(Args a) {
                 }
 #pragma unroll
                 for (int j = 0; j < kUnroll; ++j) {
+                    if (hb + j * HW >= hi) break;  // (the warp alike)
                     const int h = hb + j * HW + hsub;
                     float2 fa[4], fb[4];
                     unpack(xa[j], fa);
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
             if (!ok) break;
 #pragma unroll
             for (int j = 0; j < kBwdUnroll; ++j) {
+                if (hb + j * HW >= hi) break;  // (the warp alike)
                 const int h = hb + j * HW + hsub;
                 const uint32_t xs = stage + (j * HW + hsub) * D * 2, ys = xs + kBwdUnroll * 1024;
                 uint4 v[4];
@@ -301,17 +303,20 @@ __global__ void __launch_bounds__(32 * kSumWarps) weights_kernel(const float *pa
 // The gradient's CTAs, which leave a row of partial sums each: for q and k by their
 // heads where the GPU is full, one for every kWarps units where not.
 int bwd_grid(Args *a, int D) {
-    long long want[2], cap = (long long)sm_count() * kBwdCtas;
+    long long want[2], cost[2], cap = (long long)sm_count() * kBwdCtas;
+    const int HW = 32 / (D / 16);
     Side *sides[2] = {&a->q, &a->k};
     for (int i = 0; i < 2; ++i) {
         Side &s = *sides[i];
-        want[i] = 0;
+        want[i] = cost[i] = 0;
         if (s.heads == 0) continue;
+        // of a token: steps, and the heads of every lane
+        cost[i] = (s.heads + HW * kBwdUnroll - 1) / (HW * kBwdUnroll) + (s.heads + HW - 1) / HW;
         split_heads(s.heads, a->tokens, D, kBwdUnroll, &s.chunk, &s.splits);
         want[i] = ((long long)a->tokens * s.splits + kWarps - 1) / kWarps;
     }
     if (want[0] + want[1] > cap) {
-        long long nk = a->k.heads ? cap * a->k.heads / (a->q.heads + a->k.heads) : 0;
+        long long nk = cap * cost[1] / (cost[0] + cost[1]);
         if (a->k.heads && nk < 1) nk = 1;
         if (nk > want[1]) nk = want[1];
         want[1] = nk;
