@@ -14,12 +14,14 @@
 //
 // Bound: HBM (4 bytes a value, 6 in the gradient).  A lane has 16 values of a head, eight
 // pairs, so that the norm is three shuffles; the phases of a token are made once by the
-// warp's lanes; arithmetic is on pairs.  Measured: 32768 tokens of 64 heads of 128 167 us,
-// 6.4 TB/s, 0.95 of the copy rate, straight from memory to registers; the gradient of 32764
-// tokens of 32 heads, half of each rotated, 128 us in its kernel, 6.3 TB/s, and 3.5 for the
-// weights' sums, 140 by the call.  (The gradient from memory to registers took 144: its 16 warps an
-// SM waited for loads half of the time; with the phases made by every lane for itself
-// and 64-bit unit numbers 170.)
+// warp's lanes; arithmetic is on pairs; operands come by bulk copies into a ring of stages for
+// each warp, two steps ahead.  Measured: 32768 tokens of 64 heads of 128 162 us, 6.6 TB/s, 0.98 of
+// the copy rate (from memory to registers 170; 15085 of 40 heads of 64 29 and 38); the gradient
+// of 32764 tokens of 32 heads, half of each rotated, 128 us in its kernel, 6.3 TB/s, and 3.5 for
+// the weights' sums, 140 by the call.  (The gradient from memory to registers took 144: its 16
+// warps an SM waited for loads half of the time; with the phases made by every lane for
+// itself and 64-bit unit numbers 170.)
+#include <algorithm>
 #include <cmath>
 
 #include "moba.h"
@@ -34,7 +36,12 @@ using namespace rope;
 constexpr int kWarps = 8;
 constexpr int kUnroll = 4;      // heads whose loads a lane has in flight
 constexpr int kBwdUnroll = 2;
-constexpr int kFwdCtas = 8, kBwdCtas = 2;  // of an SM at most
+constexpr int kFwdCtas = 2, kBwdCtas = 2;  // of an SM at a time
+// CTAs of the forward come in waves, so that SMs which get through more (they differ by their
+// distance from the memory) take more, of at least so many steps a warp: a wave's start costs
+// a microsecond or two.  (One wave, four and eight at most: 32768 tokens of 64 heads of 128 183, 168,
+// 162 us, 59022 of 40 of 64 110, 100, 97; 15085 of these, eight steps, 29 with one and 33 with four.)
+constexpr int kFwdWaves = 8, kWaveSteps = 5;
 
 
 struct Side {                   // q or k
@@ -54,74 +61,109 @@ struct Args {
     int tokens, rot;
     int chunk, splits;          // heads per unit, units per token
     int w32;                    // weights are fp32 (else bf16)
-    int *status;                // gradient
-    bool wide;                  // gradient: every head of the results is aligned to 32 bytes
+    int *status;
+    bool wide;                  // every head of the results is aligned to 32 bytes
     float eps, mag;
 };
 
+// A warp works through its units' steps, kUnroll heads of every lane each, of q or of k,
+// which come by bulk copies two steps ahead.
+using FwdRing = WarpRing<3, kUnroll * 1024>;  // 32 lanes * 16 values
+
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(32 * kWarps) fwd_kernel(Args a) {
+__global__ void __launch_bounds__(32 * kWarps, kFwdCtas) fwd_kernel(Args a) {
     constexpr int LH = D / 16;   // lanes per head: 16 values (8 pairs) each
     constexpr int HW = 32 / LH;  // heads per warp and step
+    constexpr int STEP = HW * kUnroll;
+    extern __shared__ __align__(128) uint8_t s_ring[];
     __shared__ unsigned long long s_turn[D / 2];
     __shared__ __align__(16) float s_w[2][D], s_c[kWarps][D / 2], s_s[kWarps][D / 2];
+    __shared__ __align__(8) unsigned long long s_bar[kWarps][FwdRing::kStages];
+    __shared__ int s_abort;
     load_turns(s_turn, a.freqs, a.rot / 2, threadIdx.x, 32 * kWarps);
     for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps)
         if (i < D || a.k.heads) s_w[i / D][i % D] = weight(i < D ? a.q.w : a.k.w, a.w32, i % D);
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kWarps; ++w) FwdRing::init(s_bar[w]);
+        s_abort = 0;
+        ptx::fence_mbar_init();
+    }
     __syncthreads();
     const int lane = threadIdx.x & 31, item = lane % LH, hsub = lane / LH;
     const bool turns = item < a.rot / 16;  // the other items are not rotated
     int va, vb;
     vectors<D, INTERLEAVED>(item, a.rot / 2, va, vb);
-    const int warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, Hq = a.q.heads, heads = Hq + a.k.heads;
     const unsigned units = (unsigned)a.tokens * a.splits, stride = gridDim.x * kWarps;
-    for (unsigned u = blockIdx.x * kWarps + warp; u < units; u += stride) {
-        const int t = a.splits == 1 ? u : u / a.splits, part = a.splits == 1 ? 0 : u % a.splits;
-        const int h0 = part * a.chunk, h1 = min(h0 + a.chunk, a.q.heads + a.k.heads);
-        warp_cos_sin(s_turn, a.rot / 2, lane, __ldg(a.pos + t), a.mag, 1.f, s_c[warp], s_s[warp]);
+    auto token = [&](unsigned u) { return (int)(a.splits == 1 ? u : u / a.splits); };
+    auto begin = [&](unsigned u) { return a.splits == 1 ? 0 : (int)(u % a.splits) * a.chunk; };
+    // where a step that begins with head h of all ends: at that of q, of k, or of the unit
+    auto length = [&](int h, int end) { return min(STEP, (h < Hq ? min(end, Hq) : end) - h); };
+    ptx::Ctl ctl{&s_abort, a.status, kDefaultWaitLimit};
+    FwdRing ring(s_bar[warp], ptx::saddr(s_ring) + warp * FwdRing::kBytes);
+    unsigned u = blockIdx.x * kWarps + warp, nu = u;                    // the unit at hand, the one to be copied next
+    int nh = begin(min(u, units - 1)), nhi = min(nh + a.chunk, heads);  // its heads that are left
+    auto issue = [&] {
+        if (nu >= units) return;
+        const int t = token(nu), n = length(nh, nhi);
+        const void *const src[1] = {nh < Hq ? a.q.x + t * a.q.xs + (size_t)nh * D : a.k.x + t * a.k.xs + (size_t)(nh - Hq) * D};
+        ring.fill(lane, src, (uint32_t)n * D * 2);
+        nh += n;
+        if (nh >= nhi && (nu += stride) < units) {
+            nh = begin(nu);
+            nhi = min(nh + a.chunk, heads);
+        }
+    };
+#pragma unroll 1
+    for (int i = 0; i < FwdRing::kStages - 1; ++i) issue();
+    int pos = u < units ? __ldg(a.pos + token(u)) : 0;
+    bool ok = true;
+    for (; ok && u < units; u += stride) {
+        const int t = token(u), h0 = begin(u), h1 = min(h0 + a.chunk, heads);
+        warp_cos_sin(s_turn, a.rot / 2, lane, pos, a.mag, 1.f, s_c[warp], s_s[warp]);
+        if (u + stride < units) pos = __ldg(a.pos + token(u + stride));
         float2 c[4], s[4];
         if (turns) {
             load_eight(s_c[warp] + item * 8, c);
             load_eight(s_s[warp] + item * 8, s);
         }
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-            const Side &x = kv ? a.k : a.q;
-            const int base = kv ? a.q.heads : 0, lo = max(h0 - base, 0), hi = min(h1 - base, x.heads);
-            if (lo >= hi) continue;
+        for (int hb = h0, n; hb < h1; hb += n) {
+            issue();
+            const uint32_t stage = ring.wait(ctl);
+            ok = stage != 0;
+            if (!ok) break;
+            n = length(hb, h1);
+            const bool is_k = hb >= Hq;
+            __nv_bfloat16 *dst = (is_k ? a.k.out + t * a.k.os + (size_t)(hb - Hq) * D : a.q.out + t * a.q.os + (size_t)hb * D);
             float2 wa[4], wb[4];
-            load_eight(s_w[kv] + va, wa);
-            load_eight(s_w[kv] + vb, wb);
-            const __nv_bfloat16 *src = x.x + t * x.xs;
-            __nv_bfloat16 *dst = x.out + t * x.os;
-            for (int hb = lo; hb < hi; hb += HW * kUnroll) {
-                uint4 xa[kUnroll], xb[kUnroll];
-#pragma unroll
-                for (int j = 0; j < kUnroll; ++j) {
-                    const int h = hb + j * HW + hsub;
-                    xa[j] = xb[j] = make_uint4(0, 0, 0, 0);
-                    if (h < hi) {
-                        xa[j] = *reinterpret_cast<const uint4 *>(src + (size_t)h * D + va);
-                        xb[j] = *reinterpret_cast<const uint4 *>(src + (size_t)h * D + vb);
-                    }
+            load_eight(s_w[is_k] + va, wa);
+            load_eight(s_w[is_k] + vb, wb);
+            auto group = [&](int j) {
+                const int i = j * HW + hsub;
+                uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+                if (i < n) {
+                    xa = ptx::ld_shared_v4(stage + i * D * 2 + 2 * va);
+                    xb = ptx::ld_shared_v4(stage + i * D * 2 + 2 * vb);
                 }
+                float2 fa[4], fb[4];
+                unpack(xa, fa);
+                unpack(xb, fb);
+                normalise<D>(fa, fb, wa, wb, a.eps);
+                if (turns) turn_pairs<INTERLEAVED>(fa, fb, c, s);
+                if (i < n) store_head<INTERLEAVED>(dst + (size_t)i * D, va, vb, a.wide, pack(fa), pack(fb));
+            };
+            if (n == STEP) {  // (whole: without a branch between them)
 #pragma unroll
-                for (int j = 0; j < kUnroll; ++j) {
-                    if (hb + j * HW >= hi) break;  // (the warp alike)
-                    const int h = hb + j * HW + hsub;
-                    float2 fa[4], fb[4];
-                    unpack(xa[j], fa);
-                    unpack(xb[j], fb);
-                    normalise<D>(fa, fb, wa, wb, a.eps);
-                    if (turns) turn_pairs<INTERLEAVED>(fa, fb, c, s);
-                    if (h < hi) {
-                        *reinterpret_cast<uint4 *>(dst + (size_t)h * D + va) = pack(fa);
-                        *reinterpret_cast<uint4 *>(dst + (size_t)h * D + vb) = pack(fb);
-                    }
-                }
+                for (int j = 0; j < kUnroll; ++j) group(j);
+            } else {
+#pragma unroll 1
+                for (int j = 0; j * HW < n; ++j) group(j);
             }
+            ring.release();
         }
     }
+    ring.drain();
 }
 
 // The first q_ctas CTAs take q, the others k, so that a thread sums one weight's
@@ -342,6 +384,14 @@ int check(const Args &a, int D, int interleaved, int weight_bits) {
     return MOBA_OK;
 }
 
+// whether every head of the results is aligned to 32 bytes
+bool wide(const Args &a) {
+    uintptr_t w = 0;
+    for (const Side *s : {&a.q, &a.k})
+        if (s->heads) w |= reinterpret_cast<uintptr_t>(s->out) | (uintptr_t)(2 * s->os);
+    return (w & 31) == 0;
+}
+
 struct Area {
     const void *p;
     long long stride, width;  // bytes
@@ -358,10 +408,15 @@ bool collides(const Area &out, const Area &in, bool same, long long tokens) {
 template <int D>
 cudaError_t launch_fwd(const Args &a, bool interleaved, cudaStream_t st) {
     const long long units = (long long)a.tokens * a.splits;
-    const long long want = (units + kWarps - 1) / kWarps, cap = (long long)sm_count() * kFwdCtas;
+    const long long want = (units + kWarps - 1) / kWarps, once = (long long)sm_count() * kFwdCtas;
+    const long long steps = (long long)a.tokens * (a.q.heads + a.k.heads) * D / (512 * kUnroll);
+    const long long waves = std::min(std::max(steps / (kWaveSteps * kWarps * once), 1ll), (long long)kFwdWaves), cap = waves * once;
     const int grid = (int)(want < cap ? want : cap);
-    if (interleaved) fwd_kernel<D, true><<<grid, 32 * kWarps, 0, st>>>(a);
-    else fwd_kernel<D, false><<<grid, 32 * kWarps, 0, st>>>(a);
+    constexpr int bytes = kWarps * FwdRing::kBytes;
+    const cudaError_t rc = interleaved ? paged::allow_smem<fwd_kernel<D, true>>(bytes) : paged::allow_smem<fwd_kernel<D, false>>(bytes);
+    if (rc != cudaSuccess) return rc;
+    if (interleaved) fwd_kernel<D, true><<<grid, 32 * kWarps, bytes, st>>>(a);
+    else fwd_kernel<D, false><<<grid, 32 * kWarps, bytes, st>>>(a);
     note_launches(1);
     return cudaGetLastError();
 }
@@ -415,6 +470,9 @@ MOBA_EXPORT int moba_qk_norm_rope(const void *q, const void *k, void *q_out, voi
     if (collides(qo, qi, true, tokens) || collides(qo, ki, false, tokens) || collides(ko, qi, false, tokens) ||
         collides(ko, ki, true, tokens) || collides(ko, qo, false, tokens))
         return MOBA_ERR_INVALID_ARG;
+    a.wide = wide(a);
+    a.status = status_word();
+    if (!a.status) return cuda_result(cudaErrorInvalidDevice);
     split_heads(Hq + Hk, tokens, D, kUnroll, &a.chunk, &a.splits);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_result(D == 64 ? launch_fwd<64>(a, interleaved != 0, st) : launch_fwd<128>(a, interleaved != 0, st));
@@ -468,9 +526,7 @@ MOBA_EXPORT int moba_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, co
             collides(ko, in, in.p == dk_out && in.width == ko.width, tokens))
             return MOBA_ERR_INVALID_ARG;
     if (collides(ko, qo, false, tokens)) return MOBA_ERR_INVALID_ARG;
-    a.wide = true;
-    for (const Side *s : {&a.q, &a.k})
-        if (s->heads) a.wide = a.wide && ((reinterpret_cast<uintptr_t>(s->out) | (uintptr_t)(2 * s->os)) & 31) == 0;
+    a.wide = wide(a);
     const int grid = bwd_grid(&a, D);
     const size_t need = sizeof(float) * D * (size_t)grid;
     if (workspace && (workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
