@@ -37,11 +37,14 @@ constexpr int kWarps = 8;
 constexpr int kUnroll = 4;      // heads whose loads a lane has in flight
 constexpr int kBwdUnroll = 2;
 constexpr int kFwdCtas = 2, kBwdCtas = 2;  // of an SM at a time
-// CTAs of the forward come in waves, so that SMs which get through more (they differ by their
-// distance from the memory) take more, of at least so many steps a warp: a wave's start costs
-// a microsecond or two.  (One wave, four and eight at most: 32768 tokens of 64 heads of 128 183, 168,
-// 162 us, 59022 of 40 of 64 110, 100, 97; 15085 of these, eight steps, 29 with one and 33 with four.)
-constexpr int kFwdWaves = 8, kWaveSteps = 5;
+// CTAs come in waves, so that SMs which get through more (they differ by their distance from
+// the memory) take more: a wave's start costs a microsecond or two, and in the gradient a row
+// of sums for each of its CTAs.  The forward's, of at least so many steps a warp (one wave, four and
+// eight at most: 32768 tokens of 64 heads of 128 183, 168, 162 us, 59022 of 40 of 64 110, 100, 97; 15085
+// of these, eight steps, 29 with one and 33 with four).  The gradient's are four, of as many at least, or
+// one (one, three, four and six: 32764 tokens of 40 heads of 128 182, 171, 167, 167, of 32 140, 132, 133,
+// 137; 15085 of 40 of 64, 15 steps in all, 47 with one and 51 with three).
+constexpr int kFwdWaves = 8, kWaveSteps = 5, kBwdWaves = 4, kBwdWaveSteps = 10;
 
 
 struct Side {                   // q or k
@@ -342,10 +345,12 @@ __global__ void __launch_bounds__(32 * kSumWarps) weights_kernel(const float *pa
     if (lane == 0) (blockIdx.y ? dwk : dwq)[col + warp] = sum;
 }
 
-// The gradient's CTAs, which leave a row of partial sums each: for q and k by their
-// heads where the GPU is full, one for every kWarps units where not.
+// The gradient's CTAs, which leave a row of partial sums each: for q and k by what their
+// tokens take where the GPU is full, one for every kWarps units where not.
 int bwd_grid(Args *a, int D) {
     long long want[2], cost[2], cap = (long long)sm_count() * kBwdCtas;
+    const long long steps = (long long)a->tokens * (a->q.heads + a->k.heads) * D / (512 * kBwdUnroll);
+    if (steps >= kBwdWaves * kBwdWaveSteps * kWarps * cap) cap *= kBwdWaves;
     const int HW = 32 / (D / 16);
     Side *sides[2] = {&a->q, &a->k};
     for (int i = 0; i < 2; ++i) {
