@@ -268,12 +268,17 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 // Bound: latency (a block's keys in four rounds of loads).  32 blocks of 512 on 8 kv heads of
 // 128 16 us; one of 64 sequences' 5 beside the kernel before it (9 where every thread waited
 // first; clusters of append_kernel's kind 11 and 19).
-constexpr int kPoolThreads = 256, kPoolCtas = 3;  // of an SM
+// T threads: 1024, a block's keys in one round, where there are no more candidates than
+// kPoolWide an SM, else 256 and three CTAs an SM.  (us by the call with 256 and 1024: 2048 new tokens
+// that complete a block of 2048 43 and 35, six chunks of up to 2000 with blocks of 512 50 and 45; four
+// of up to 8192 90 and 94, 256 sequences of one token 10 and 21.)
+constexpr int kPoolWide = 2;
+constexpr int pool_ctas(int threads) { return threads == 256 ? 3 : 1; }  // of an SM
 
-template <int D, bool MAX>
-__global__ void __launch_bounds__(kPoolThreads, kPoolCtas) pool_kernel(AppendArgs a, int candidates) {
+template <int D, bool MAX, int T>
+__global__ void __launch_bounds__(T, pool_ctas(T)) pool_kernel(AppendArgs a, int candidates) {
     constexpr int CW = D / 8, GC = kAppendThreads / CW, G = GC * kAppendParts;  // as in append_kernel
-    constexpr int GP = kPoolThreads / CW;                                       // groups at a time
+    constexpr int GP = T / CW;                                       // groups at a time
     constexpr int U = 8;
     __shared__ float s_red[G][D], s_sum[kAppendParts][D];
     __shared__ int s_page[kAppendPages];
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtas) pool_kernel(AppendArg
         const int pages = bs >> a.psh;
         const bool held = pages <= kAppendPages;
         if (held)
-            for (int k = tid; k < pages; k += kPoolThreads) s_page[k] = __ldg(table + k);
+            for (int k = tid; k < pages; k += T) s_page[k] = __ldg(table + k);
         __syncthreads();
         bool bad = false;
 #pragma unroll 1
@@ -344,7 +349,7 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtas) pool_kernel(AppendArg
                 *reinterpret_cast<float4 *>(&s_red[g][col * 8 + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
         }
         const bool some = __syncthreads_or(bad);
-        for (int k = tid; k < kAppendParts * D; k += kPoolThreads) {
+        for (int k = tid; k < kAppendParts * D; k += T) {
             const int part = k / D, d = k % D;
             float cp = 0.f, sum = s_red[part * GC][d];
             for (int g = 1; g < GC; ++g) {
@@ -477,15 +482,20 @@ int make_pool(AppendArgs *a, const Cache &c, void *k_pages, float *kbar_pages, i
     return a->clusters * c.Hkv >= (1ll << 30) ? MOBA_ERR_UNSUPPORTED : MOBA_OK;
 }
 
-cudaError_t launch_pool(const AppendArgs &a, int D, bool max, cudaStream_t st) {
-    const int candidates = (int)(a.clusters * a.c.Hkv), most = sm_count() * kPoolCtas;
-    const dim3 grid(candidates < most ? candidates : most), block(kPoolThreads);
+template <int D, int T>
+static cudaError_t launch_pool(const AppendArgs &a, bool max, int candidates, cudaStream_t st) {
+    const int most = sm_count() * (T == 256 ? pool_ctas(T) : kPoolWide);
+    const dim3 grid(candidates < most ? candidates : most);
     note_launches(1);
-    if (D == 64)
-        return max ? launch_after(pool_kernel<64, true>, grid, block, 0, st, a, candidates)
-                   : launch_after(pool_kernel<64, false>, grid, block, 0, st, a, candidates);
-    return max ? launch_after(pool_kernel<128, true>, grid, block, 0, st, a, candidates)
-               : launch_after(pool_kernel<128, false>, grid, block, 0, st, a, candidates);
+    return max ? launch_after(pool_kernel<D, true, T>, grid, dim3(T), 0, st, a, candidates)
+               : launch_after(pool_kernel<D, false, T>, grid, dim3(T), 0, st, a, candidates);
+}
+
+cudaError_t launch_pool(const AppendArgs &a, int D, bool max, cudaStream_t st) {
+    const int candidates = (int)(a.clusters * a.c.Hkv);
+    if (candidates <= kPoolWide * sm_count())
+        return D == 64 ? launch_pool<64, 1024>(a, max, candidates, st) : launch_pool<128, 1024>(a, max, candidates, st);
+    return D == 64 ? launch_pool<64, 256>(a, max, candidates, st) : launch_pool<128, 256>(a, max, candidates, st);
 }
 
 }  // namespace paged

@@ -220,3 +220,24 @@ def test_no_tokens():
     c = Cache(1, 64, 2, 64, 16, 64)
     out = fused(c, normal(1, 0, 4, 64), normal(2, 0, 2, 64), normal(3, 0, 2, 64), [0, 0], [5], ops.rope_frequencies(64), max_new=1)
     assert out.shape == (0, 4, 64) and c.k.isnan().all()
+
+
+@pytest.mark.parametrize("hkv,d,page,block,pooling", [(8, 64, 16, 64, ops.POOL_MEAN), (8, 128, 32, 128, ops.POOL_MAX),
+                                                      (3, 128, 16, 192, ops.POOL_MEAN)])
+@pytest.mark.parametrize("seqs", [7, 150])
+def test_blocks_completed_by_few_sequences_and_by_many(seqs, hkv, d, page, block, pooling):
+    """Blocks that one new token, several or all of them complete, in calls of few candidates for
+    pooling and in calls of more than the GPU takes at once."""
+    lens = [block * (1 + b % 3) - (b % 5) * (b % 2) for b in range(seqs)]
+    new = [1 + 7 * b % 13 if b % 4 else min(n, block + 5) for b, n in enumerate(lens)]
+    old = [n - m for n, m in zip(lens, new)]
+    one, two = (Cache(seqs, 3 * block, hkv, d, page, block) for _ in range(2))
+    x = normal(1, sum(old), 2 * hkv, d)
+    for c in (one, two):
+        c.append(x[:, :hkv].contiguous(), x[:, hkv:].contiguous(), offsets(old), old, pooling)
+    q, k, v = (normal(s, sum(new), hkv, d) for s in (2, 3, 4))
+    kw = dict(pooling=pooling, k_weight=weights(5, d, BF))
+    freqs = ops.rope_frequencies(d)
+    got = fused(one, q, k, v, offsets(new), lens, freqs, **kw)
+    assert same(got, apart(two, q, k, v, offsets(new), lens, freqs, **kw))
+    assert same(one.k, two.k) and same(one.v, two.v) and same(one.kbar, two.kbar) and ops.get_status() == ops.MOBA_OK
