@@ -53,8 +53,8 @@ def _calls_commands(lib: str):
                 "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
                 "-c", os.path.join(CSRC, "moba_calls.cpp"), "-o", obj]
     link = lambda to: [cxx, "-shared", "-o", to, obj, "-L", os.path.dirname(lib), "-l:" + os.path.basename(lib),
-                       "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-ltorch",
-                       "-lc10_cuda", "-lc10"]
+                       "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda",
+                       "-ltorch", "-lc10_cuda", "-lc10"]
     return obj, compile_, link
 
 

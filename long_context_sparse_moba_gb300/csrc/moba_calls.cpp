@@ -2,16 +2,17 @@
 // looked over, its results and scratch made, and the C entry point called.
 //
 // Bound: the host, where tokens are few: the GPU has 3 to 17 us of work then.  Measured, us from
-// call to call, against the same steps in Python: norms of 3 tokens 7 and 18, the gradient of 517
-// 14 and 32, appending one token 9 and 25, one of each of 64 sequences 12 (the GPU's time) and 26, four
+// call to call, against the same steps in Python: norms of 3 tokens 6 and 18, the gradient of 517
+// 12 and 32, appending one token 9 and 25, one of each of 64 sequences 12 (the GPU's time) and 26, four
 // forks 16 (the GPU's) and 29.
 // Nothing is decided here: whatever is not the plain case (another device than the current
 // one, operands that a check stops at, arguments of another kind, a refusal by the entry point)
 // gives None, and ops.py goes through the same call step by step and says what is wrong.
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -26,6 +27,16 @@ namespace {
 using at::ScalarType;
 using at::Tensor;
 
+// A new tensor straight from the allocator (by the dispatcher 0.4 us more each).
+Tensor make_new(at::IntArrayRef sizes, ScalarType type, int device) {
+    return at::detail::empty_cuda(sizes, type, c10::Device(c10::kCUDA, (c10::DeviceIndex)device), std::nullopt);
+}
+// (which does not fill it, as torch can be told to)
+bool fills() {
+    const at::Context &c = at::globalContext();
+    return c.deterministicAlgorithms() && c.deterministicFillUninitializedMemory();
+}
+
 // The operands of one call.  `ok` turns false at the first that is not the plain case.
 struct Operands {
     bool ok = true;
@@ -36,7 +47,7 @@ struct Operands {
         ok = THPVariable_Check(first);
         if (!ok) return;
         const Tensor t = THPVariable_Unpack(first);
-        ok = t.is_cuda() && t.device().index() == c10::cuda::current_device();
+        ok = t.is_cuda() && t.device().index() == c10::cuda::current_device() && !fills();
         device = t.device().index();
     }
     Tensor any(PyObject *o, ScalarType type) {
@@ -109,7 +120,7 @@ struct Result {
     Result(PyObject *o) : given(o == Py_None ? nullptr : o) {}
     bool made() const { return given == nullptr; }
     void make(at::IntArrayRef sizes, ScalarType type, int device) {
-        if (made()) t = at::empty(sizes, at::TensorOptions().dtype(type).device(at::kCUDA, device));
+        if (made()) t = make_new(sizes, type, device);
     }
     PyObject *object() {
         if (made()) return THPVariable_Wrap(std::move(t));
@@ -121,9 +132,7 @@ struct Result {
 void *stream_of(int device) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream(); }
 void *address(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 
-Tensor scratch(size_t bytes, int device) {
-    return at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, device));
-}
+Tensor scratch(size_t bytes, int device) { return make_new({(int64_t)bytes}, at::kByte, device); }
 
 // What is left of a call: None where the entry point refused it, its code where CUDA failed, or
 // the results.

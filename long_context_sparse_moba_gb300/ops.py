@@ -766,8 +766,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, eps: float = 1e-6,
     times the weights [D] (bf16 or fp32), rotated -> (q_out, k_out).  Operands, positions
     and freqs are those of :func:`rope`; q_out / k_out may be q / k (in place)."""
     if stream is None:
-        r = _native().qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, eps, interleaved, magnitude,
-                                   q_out, k_out)
+        r = (_calls or _native()).qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, eps, interleaved,
+                                                magnitude, q_out, k_out)
         if r is not None:
             return _usual(r, "moba_qk_norm_rope")
     device, T, Hq, Hk, D, qs, ks, bits = _norm_operands(q, k, q_weight, k_weight, positions, freqs)
@@ -805,8 +805,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, freqs,
     of at least :func:`qk_norm_rope_bwd_workspace_size` bytes, or None (scratch from torch's
     allocator, on the call's stream).  No tokens: weight gradients of zero."""
     if stream is None:
-        r = _native().qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, freqs, eps,
-                                       interleaved, magnitude, dq, dk, dq_weight, dk_weight, workspace)
+        r = (_calls or _native()).qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, freqs,
+                                                    eps, interleaved, magnitude, dq, dk, dq_weight,
+                                                    dk_weight, workspace)
         if r is not None:
             return _usual(r, "moba_qk_norm_rope_bwd")
     device, T, Hq, Hk, D, qs, ks, bits = _norm_operands(q, k, q_weight, k_weight, positions, freqs)
@@ -912,9 +913,9 @@ def paged_append_rope(q, k, v, k_pages, v_pages, kbar_pages, page_table, cu_new,
     (slices of one projection).  Rows of q_out behind the last sequence, and of refused
     ones, are left as they were."""
     if stream is None and pooling == POOL_MEAN:
-        r = _native().paged_append_rope(q, k, v, k_pages, v_pages, kbar_pages, page_table, cu_new, cache_lens,
-                                        max_new, block_size, freqs, positions, q_weight, k_weight, eps,
-                                        interleaved, magnitude, q_out)
+        r = (_calls or _native()).paged_append_rope(q, k, v, k_pages, v_pages, kbar_pages, page_table, cu_new,
+                                                    cache_lens, max_new, block_size, freqs, positions,
+                                                    q_weight, k_weight, eps, interleaved, magnitude, q_out)
         if r is not None:
             return _usual(r, "moba_paged_append_rope")
     device = _device(k_pages, "k_pages")
@@ -1022,8 +1023,8 @@ def paged_attn_shared(q, k_pages, v_pages, page_table, cu_new, cache_lens, max_n
     :func:`paged_attn_shared_workspace_size` bytes, or None (scratch from torch's allocator,
     on the call's stream)."""
     if stream is None:
-        r = _native().paged_attn_shared(q, k_pages, v_pages, page_table, cu_new, cache_lens, max_new, cu_groups,
-                                        prefix_lens, out, lse, workspace)
+        r = (_calls or _native()).paged_attn_shared(q, k_pages, v_pages, page_table, cu_new, cache_lens,
+                                                    max_new, cu_groups, prefix_lens, out, lse, workspace)
         if r is not None:
             return _usual(r, "moba_paged_attn_shared")
     device = _device(k_pages, "k_pages")

@@ -199,3 +199,17 @@ def test_threads_and_streams():
     for t in threads:
         t.join()
     assert not wrong and ops.get_status() == ops.MOBA_OK
+
+
+def test_new_tensors_are_filled_where_torch_is_told_to():
+    a = norm_case()
+    assert ops._native().qk_norm_rope(*a, 1e-6, False, 1.0, None, None) is not None
+    torch.use_deterministic_algorithms(True)
+    try:
+        assert ops._native().qk_norm_rope(*a, 1e-6, False, 1.0, None, None) is None
+        x = shared_case()
+        q = torch.cat((x[0], x[0]))  # (rows behind the last sequence)
+        out, lse = ops.paged_attn_shared(q, *x[1:])
+        assert out[4:].isnan().all() and lse[4:].isnan().all()
+    finally:
+        torch.use_deterministic_algorithms(False)
