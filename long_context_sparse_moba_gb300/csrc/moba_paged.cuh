@@ -80,8 +80,8 @@ struct Cache {
 
 // A kernel that follows another one of the same call: its CTAs may start while
 // that one drains, and each begins with after_previous(), which waits for all of
-// its results.  Every CTA of every kernel in such a row has to make that wait, so
-// that a kernel's end implies the end of all before it.
+// its results (or ends with it, where it needs none of them).  Every CTA of every kernel
+// in such a row has to make that wait, so that a kernel's end implies the end of all before it.
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                          const A &...args) {

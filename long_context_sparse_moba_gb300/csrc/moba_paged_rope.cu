@@ -18,9 +18,8 @@
 // heads (q, then k, then v).  Measured (32 + 8 + 8 heads of 128, normalised): 16469 tokens in
 // four chunks 72 us, 5.6 TB/s (the pages' rows of 256 bytes are scattered writes), and 16 for
 // pooling 32 blocks of 512, 91 by the call; a step of 64 sequences of which one completes its
-// block 15 us in a graph, 27 by a call, which is the host.  (Units of a third of a token 102
-// by the call; tokens in consecutive runs a warp 112; k and v first and q beside the pooling,
-// in a launch of its own, 98.)
+// block 12.  (Units of a third of a token 102 by the call; tokens in consecutive runs a warp 112; CTAs
+// in waves 98; k and v first and q beside the pooling, in a launch of its own, 98.)
 #include <cmath>
 
 #include "moba_paged.cuh"

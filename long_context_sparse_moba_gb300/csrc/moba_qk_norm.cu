@@ -17,8 +17,8 @@
 // warp's lanes; arithmetic is on pairs; operands come by bulk copies into a ring of stages for
 // each warp, two steps ahead.  Measured: 32768 tokens of 64 heads of 128 162 us, 6.6 TB/s, 0.98 of
 // the copy rate (from memory to registers 170; 15085 of 40 heads of 64 29 and 38); the gradient
-// of 32764 tokens of 32 heads, half of each rotated, 128 us in its kernel, 6.3 TB/s, and 3.5 for
-// the weights' sums, 140 by the call.  (The gradient from memory to registers took 144: its 16
+// of 32764 tokens of 32 heads, half of each rotated, 125 us in its kernel, 6.4 TB/s, 134 by the
+// call with the weights' sums.  (The gradient from memory to registers took 144: its 16
 // warps an SM waited for loads half of the time; with the phases made by every lane for
 // itself and 64-bit unit numbers 170.)
 #include <algorithm>
@@ -34,9 +34,8 @@ namespace qk_norm {
 using namespace rope;
 
 constexpr int kWarps = 8;
-constexpr int kUnroll = 4;      // heads whose loads a lane has in flight
-constexpr int kBwdUnroll = 2;
-constexpr int kFwdCtas = 2, kBwdCtas = 2;  // of an SM at a time
+constexpr int kUnroll = 4, kBwdUnroll = 2;  // heads of a lane in a step
+constexpr int kFwdCtas = 2, kBwdCtas = 2;   // of an SM at a time
 // CTAs come in waves, so that SMs which get through more (they differ by their distance from
 // the memory) take more: a wave's start costs a microsecond or two, and in the gradient a row
 // of sums for each of its CTAs.  The forward's, of at least so many steps a warp (one wave, four and
@@ -45,7 +44,6 @@ constexpr int kFwdCtas = 2, kBwdCtas = 2;  // of an SM at a time
 // one (one, three, four and six: 32764 tokens of 40 heads of 128 182, 171, 167, 167, of 32 140, 132, 133,
 // 137; 15085 of 40 of 64, 15 steps in all, 47 with one and 51 with three).
 constexpr int kFwdWaves = 8, kWaveSteps = 5, kBwdWaves = 4, kBwdWaveSteps = 10;
-
 
 struct Side {                   // q or k
     const __nv_bfloat16 *x, *dy;  // dy: gradient only
