@@ -213,3 +213,32 @@ def test_new_tensors_are_filled_where_torch_is_told_to():
         assert out[4:].isnan().all() and lse[4:].isnan().all()
     finally:
         torch.use_deterministic_algorithms(False)
+
+
+def test_captured_and_replayed():
+    a, b, c = norm_case(T=40), append_case(), shared_case()
+    g = normal(8, 40, 4, 64), normal(9, 40, 2, 64)
+    call = lambda: (*ops.qk_norm_rope(*a), *ops.qk_norm_rope_bwd(*g, *a), ops.paged_append_rope(*b), *ops.paged_attn_shared(*c))
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for seed in (20, 30):
+        for i, x in enumerate((a[0], a[1], g[0], g[1], b[0], c[0])):
+            x.copy_(normal(seed + i, *x.shape))
+        graph.replay()
+        assert equal(got, call())
+    assert ops.get_status() == ops.MOBA_OK
+
+
+def test_modes_of_autograd():
+    a = norm_case()
+    a[0].requires_grad_(True)
+    a[2] = torch.nn.Parameter(a[2])
+    assert ops._native().qk_norm_rope(*a, 1e-6, False, 1.0, None, None) is not None
+    plain = ops.qk_norm_rope(*a)
+    assert not any(x.requires_grad or x.is_inference() for x in plain)
+    with torch.inference_mode():
+        got = ops.qk_norm_rope(*a)
+        assert all(x.is_inference() for x in got) and equal(got, plain)
