@@ -292,3 +292,20 @@ def test_a_training_step_through_the_attention():
     flat = lambda t: t.reshape(B * S, H, D)
     check_gradient(flat(dq), dwq, flat(gq), flat(q), wq, pos, freqs, 1e-6, False)
     check_gradient(flat(dk), dwk, flat(gk), flat(k), wk, pos, freqs, 1e-6, False)
+
+
+@pytest.mark.parametrize("hq,hk,d,interleaved", [(32, 8, 128, False), (9, 64, 64, True)])
+def test_calls_of_several_waves(hq, hk, d, interleaved):
+    """Tokens enough for CTAs in waves.  A thread of the gradient sums 24 products or fewer here, and
+    40 CTAs or fewer on its way: 2^-19 + (24 + 3 + 8 + 40 + 5) u, within 2^-17 as above."""
+    tokens = 104000000 // ((hq + hk) * d)
+    q, k = normal(1, tokens, hq, d), normal(2, tokens, hk, d)
+    wq, wk, freqs = weights(3, d, BF), weights(4, d, BF), ops.rope_frequencies(d)
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda") * 3
+    a, b = ops.qk_norm_rope(q, k, wq, wk, pos, freqs, interleaved=interleaved)
+    dq, dk = normal(5, tokens, hq, d), normal(6, tokens, hk, d)
+    got = ops.qk_norm_rope_bwd(dq, dk, q, k, wq, wk, pos, freqs, interleaved=interleaved)
+    assert ops.get_status() == ops.MOBA_OK
+    for x, y, dy, w, dx, dw in ((q, a, dq, wq, got[0], got[2]), (k, b, dk, wk, got[1], got[3])):
+        check_forward(y, x, w, pos, freqs, 1e-6, interleaved)
+        check_gradient(dx, dw, dy, x, w, pos, freqs, 1e-6, interleaved)
