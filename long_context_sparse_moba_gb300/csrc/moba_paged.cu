@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(T, pool_ctas(T)) pool_kernel(AppendArgs a, int
     __shared__ float s_red[G][D], s_sum[kAppendParts][D];
     __shared__ int s_page[kAppendPages];
     const int tid = threadIdx.x, col = tid % CW, bs = a.c.bs, ps = a.c.ps;
+    let_next();
     bool waited = false;
     for (int i = blockIdx.x; i < candidates; i += gridDim.x) {
         const int hk = i % a.c.Hkv, bj = i / a.c.Hkv;

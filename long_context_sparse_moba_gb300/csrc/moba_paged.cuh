@@ -82,6 +82,8 @@ struct Cache {
 // that one drains, and each begins with after_previous(), which waits for all of
 // its results (or ends with it, where it needs none of them).  Every CTA of every kernel
 // in such a row has to make that wait, so that a kernel's end implies the end of all before it.
+// (The first kernel of some calls is launched so too: what is before it on the stream has then
+// ended when its wait has; 2 us less from call to call.)
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                          const A &...args) {

@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) write_kernel(WriteArgs a) 
     __shared__ int s_abort;
     __shared__ unsigned long long s_turn[D / 2];
     __shared__ __align__(16) float s_w[2][D], s_c[kWarps][D / 2], s_s[kWarps][D / 2];
+    after_previous();
     let_next();
     load_turns(s_turn, a.freqs, a.rot / 2, threadIdx.x, 32 * kWarps);
     for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps) {
@@ -192,10 +193,9 @@ cudaError_t launch_write(const WriteArgs &a, bool interleaved, cudaStream_t st) 
     constexpr int bytes = kWarps * StepRing::kBytes;
     const cudaError_t rc = interleaved ? allow_smem<write_kernel<D, true>>(bytes) : allow_smem<write_kernel<D, false>>(bytes);
     if (rc != cudaSuccess) return rc;
-    if (interleaved) write_kernel<D, true><<<grid, 32 * kWarps, bytes, st>>>(a);
-    else write_kernel<D, false><<<grid, 32 * kWarps, bytes, st>>>(a);
     note_launches(1);
-    return cudaGetLastError();
+    return interleaved ? launch_after(write_kernel<D, true>, dim3(grid), dim3(32 * kWarps), bytes, st, a)
+                       : launch_after(write_kernel<D, false>, dim3(grid), dim3(32 * kWarps), bytes, st, a);
 }
 
 }  // namespace

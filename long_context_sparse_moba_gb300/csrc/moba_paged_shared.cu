@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
     __shared__ int s_pre[HELD ? kHeld : 1], s_rep[HELD ? kHeld : 1], s_at[HELD ? kHeld : 1];
     const Attn &a = x.a;
     const Cache &c = a.c;
-    let_next();
     after_previous();
+    let_next();  // (not sooner: the next kernels would be brought in while a call before merges, 73 us for 69)
     const int tid = threadIdx.x, ns = c.num_seqs, ng = x.n_groups, G = a.G, Hkv = c.Hkv;
     if (HELD) {
         for (int i = tid; i <= ns; i += T) {
@@ -651,6 +651,7 @@ __global__ void __launch_bounds__(kMergeThreads, TEAM == 16 ? 3 : 4) merge_spans
     __shared__ float s_m[kTeams], s_l[kTeams];
     const Attn &a = x.a;
     after_previous();
+    let_next();
     const int team = threadIdx.x / TEAM, lane = threadIdx.x % TEAM, G = a.G, Hkv = a.c.Hkv;
     const bool chunk = a.chunk;
     // (a span behind the last one is some memory of the scratch)
@@ -834,10 +835,9 @@ int make_shared(SharedArgs *x, int Hq, int D, int n_groups) {
 cudaError_t launch_plan(const SharedArgs &x, cudaStream_t st) {
     note_launches(1);
     const int most = x.a.c.num_seqs > x.n_groups ? x.a.c.num_seqs : x.n_groups;
-    if (most <= 128) plan_spans_kernel<128, true><<<1, 128, 0, st>>>(x);
-    else if (most <= kHeld) plan_spans_kernel<1024, true><<<1, 1024, 0, st>>>(x);
-    else plan_spans_kernel<1024, false><<<1, 1024, 0, st>>>(x);
-    return cudaGetLastError();
+    return most <= 128     ? launch_after(plan_spans_kernel<128, true>, dim3(1), dim3(128), 0, st, x)
+           : most <= kHeld ? launch_after(plan_spans_kernel<1024, true>, dim3(1), dim3(1024), 0, st, x)
+                           : launch_after(plan_spans_kernel<1024, false>, dim3(1), dim3(1024), 0, st, x);
 }
 
 template <int D>

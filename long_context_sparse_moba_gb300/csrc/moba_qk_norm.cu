@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdCtas) fwd_kernel(Args a) {
     __shared__ __align__(16) float s_w[2][D], s_c[kWarps][D / 2], s_s[kWarps][D / 2];
     __shared__ __align__(8) unsigned long long s_bar[kWarps][FwdRing::kStages];
     __shared__ int s_abort;
+    paged::after_previous();
+    paged::let_next();
     load_turns(s_turn, a.freqs, a.rot / 2, threadIdx.x, 32 * kWarps);
     for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps)
         if (i < D || a.k.heads) s_w[i / D][i % D] = weight(i < D ? a.q.w : a.k.w, a.w32, i % D);
@@ -185,6 +187,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
     __shared__ int s_abort;
     const bool is_k = (int)blockIdx.x >= a.q_ctas;
     const Side x = is_k ? a.k : a.q;
+    paged::after_previous();
+    paged::let_next();
     load_turns(s_turn, a.freqs, a.rot / 2, threadIdx.x, 32 * kWarps);
     for (int i = threadIdx.x; i < D; i += 32 * kWarps) s_w[i] = weight(x.w, a.w32, i);
     if (threadIdx.x == 0) {
@@ -193,7 +197,6 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
         ptx::fence_mbar_init();
     }
     __syncthreads();
-    paged::let_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, item = lane % LH, hsub = lane / LH;
     const bool turns = item < a.rot / 16;
     int va, vb;
@@ -324,6 +327,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) weights_kernel(const float *pa
                                                                  float *dwq, float *dwk) {
     __shared__ float s[kSumWarps][33];
     paged::after_previous();
+    paged::let_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = blockIdx.x * 32;
     const int c0 = blockIdx.y ? q_ctas : 0, c1 = blockIdx.y ? ctas : q_ctas;
     float sum = 0.f;
@@ -418,10 +422,9 @@ cudaError_t launch_fwd(const Args &a, bool interleaved, cudaStream_t st) {
     constexpr int bytes = kWarps * FwdRing::kBytes;
     const cudaError_t rc = interleaved ? paged::allow_smem<fwd_kernel<D, true>>(bytes) : paged::allow_smem<fwd_kernel<D, false>>(bytes);
     if (rc != cudaSuccess) return rc;
-    if (interleaved) fwd_kernel<D, true><<<grid, 32 * kWarps, bytes, st>>>(a);
-    else fwd_kernel<D, false><<<grid, 32 * kWarps, bytes, st>>>(a);
     note_launches(1);
-    return cudaGetLastError();
+    return interleaved ? paged::launch_after(fwd_kernel<D, true>, dim3(grid), dim3(32 * kWarps), bytes, st, a)
+                       : paged::launch_after(fwd_kernel<D, false>, dim3(grid), dim3(32 * kWarps), bytes, st, a);
 }
 
 template <int D>
@@ -429,10 +432,9 @@ cudaError_t launch_bwd(const Args &a, int grid, bool interleaved, float *dwq, fl
     constexpr int bytes = kWarps * BwdRing<D>::kBytes;
     cudaError_t rc = interleaved ? paged::allow_smem<bwd_kernel<D, true>>(bytes) : paged::allow_smem<bwd_kernel<D, false>>(bytes);
     if (rc != cudaSuccess) return rc;
-    if (interleaved) bwd_kernel<D, true><<<grid, 32 * kWarps, bytes, st>>>(a);
-    else bwd_kernel<D, false><<<grid, 32 * kWarps, bytes, st>>>(a);
     note_launches(2);
-    rc = cudaGetLastError();
+    rc = interleaved ? paged::launch_after(bwd_kernel<D, true>, dim3(grid), dim3(32 * kWarps), bytes, st, a)
+                     : paged::launch_after(bwd_kernel<D, false>, dim3(grid), dim3(32 * kWarps), bytes, st, a);
     if (rc != cudaSuccess) return rc;
     return paged::launch_after(weights_kernel, dim3(D / 32, dwk ? 2 : 1), dim3(32 * kSumWarps), 0, st,
                                (const float *)a.part, a.q_ctas, grid, D, dwq, dwk);
