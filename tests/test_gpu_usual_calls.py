@@ -242,3 +242,54 @@ def test_modes_of_autograd():
     with torch.inference_mode():
         got = ops.qk_norm_rope(*a)
         assert all(x.is_inference() for x in got) and equal(got, plain)
+
+
+def test_captured_behind_copies_and_a_join():
+    """The first kernel of a call behind a copy, a memset, and the join of two streams."""
+    a, b, c = norm_case(T=40), append_case(), shared_case()
+    g = normal(8, 40, 4, 64), normal(9, 40, 2, 64)
+    calls = [lambda: ops.qk_norm_rope(*a), lambda: ops.qk_norm_rope_bwd(*g, *a), lambda: ops.paged_append_rope(*b),
+             lambda: ops.paged_attn_shared(*c)]
+    inputs = [(a[0], a[1]), g, (b[0], b[1]), (c[0], c[0])]
+    for call, (x, y) in zip(calls, inputs):
+        sx, sy, zero = x.clone(), y.clone(), torch.ones(1 << 20, device="cuda")
+        call()
+        torch.cuda.synchronize()
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                for _ in range(20):
+                    sy.mul_(-1.0)
+                if y is not x:
+                    y.copy_(sy)
+            x.copy_(sx)
+            zero.zero_()
+            torch.cuda.current_stream().wait_stream(side)
+            got = call()
+            again = call()
+        for i in range(3):
+            sx.copy_(normal(60 + i, *x.shape))
+            sy.copy_(normal(70 + i, *y.shape))
+            graph.replay()
+            want = call()
+            assert equal(got, want) and equal(again, want)
+    assert ops.get_status() == ops.MOBA_OK
+
+
+def test_behind_kernels_that_write_their_operands():
+    """Calls one after the other on a stream, each reading what the one before it wrote."""
+    a = norm_case(T=3000, hq=8, hk=8, d=64)
+    q, k = a[0].contiguous(), a[1].contiguous()
+    step = lambda q, k, **kw: ops.qk_norm_rope(q, k, *a[2:], **kw)
+    for _ in range(20):
+        x, y = q, k
+        for _ in range(10):
+            x, y = step(x, y)
+            x = x * 1.0
+        torch.cuda.synchronize()
+        z, w = q, k
+        for _ in range(10):
+            z, w = step(z, w)
+            torch.cuda.synchronize()
+        assert torch.equal(x, z) and torch.equal(y, w)
