@@ -21,9 +21,9 @@
 // P is rounded to bf16 for the second product, as in the other attention kernels: relative
 // to 64 bits outputs err by 0.0020 to 0.0024, of which the result's own rounding is 0.0016.
 // Measured (heads of 128 unless said): 64 forks of 32768 tokens with up to 512 of their own,
-// 32 / 8 heads, 74 us (plan 3, big spans 37, small ones some 15 behind them, merge 12); 16 of 16384
-// with up to 2000, 32 / 32 heads, 101; 3 groups of 11 with up to 5 new tokens, 20 / 4 heads of 64, 40; 8
-// questions of up to 200 tokens on 16384 185, 1135 TFLOP/s of what they cannot do without.
+// 32 / 8 heads, 69 us (plan 3, big spans 37, small ones some 15 behind them, merge 12); 16 of 16384
+// with up to 2000, 32 / 32 heads, 99; 3 groups of 11 with up to 5 new tokens, 20 / 4 heads of 64, 37; 8
+// questions of up to 200 tokens on 16384 181, 1160 TFLOP/s of what they cannot do without.
 #include "moba_mma.cuh"
 #include "moba_paged_attn.cuh"
 #include "moba_ptx.cuh"

@@ -15,9 +15,9 @@
 // Bound: HBM (4 bytes a value, 6 in the gradient).  A lane has 16 values of a head, eight
 // pairs, so that the norm is three shuffles; the phases of a token are made once by the
 // warp's lanes; arithmetic is on pairs; operands come by bulk copies into a ring of stages for
-// each warp, two steps ahead.  Measured: 32768 tokens of 64 heads of 128 162 us, 6.6 TB/s, 0.98 of
+// each warp, two steps ahead.  Measured: 32768 tokens of 64 heads of 128 160 us, 6.7 TB/s, 0.99 of
 // the copy rate (from memory to registers 170; 15085 of 40 heads of 64 29 and 38); the gradient
-// of 32764 tokens of 32 heads, half of each rotated, 125 us in its kernel, 6.4 TB/s, 134 by the
+// of 32764 tokens of 32 heads, half of each rotated, 125 us in its kernel, 6.4 TB/s, 130 by the
 // call with the weights' sums.  (The gradient from memory to registers took 144: its 16
 // warps an SM waited for loads half of the time; with the phases made by every lane for
 // itself and 64-bit unit numbers 170.)
