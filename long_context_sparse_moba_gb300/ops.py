@@ -2,8 +2,9 @@
 
 Every function below calls the C ABI of ``include/moba.h`` with the tensors'
 device pointers and the current CUDA stream; all arithmetic runs in the
-library's kernels.  There is no fallback: if the library is missing or a call
-fails, a ``RuntimeError`` is raised.
+library's kernels.  The usual call of the functions where the host's time counts goes
+through ``moba_calls.so``, which does the same in one step.  There is no fallback: if a
+library is missing or a call fails, a ``RuntimeError`` is raised.
 """
 from __future__ import annotations
 
