@@ -483,13 +483,15 @@ int moba_rope_frequencies(double *freqs, int rot_dim, double base, int scaling, 
  *     values only
  *   q_weight, k_weight : [D] bf16 or fp32 (weight_bits 16 or 32; device)
  *   eps : finite, at least 1e-12
- * An output may be its own input; any other overlap is MOBA_ERR_INVALID_ARG.
+ * An output may be its own input; any other overlap of one with what the call reads or
+ * writes is MOBA_ERR_INVALID_ARG.
  *
  * moba_qk_norm_rope_bwd is the gradient, from that of the outputs (dq_out, dk_out) and
  * the forward's inputs q, k: with g = R^T dy and n = x r,
  *   dx = r (g w - n mean(g w n)),  dw = sum over tokens and heads of g n (fp32 [D]).
- * dq may be dq_out and dk dk_out, in place; any other overlap is an error.  The order of
- * dw's sums goes by the sizes and the GPU alone: equal calls give equal bits.
+ * dq may be dq_out and dk dk_out, in place; any other overlap is an error (dq_out and dk_out
+ * may be one buffer, and then neither dq nor dk may be it).  The order of dw's sums goes by
+ * the sizes and the GPU alone: equal calls give equal bits.
  * workspace: device scratch, 256-byte aligned, at least
  * moba_qk_norm_rope_bwd_workspace_size bytes (asked with the same device current), used
  * by nothing else until the call's work has finished; NULL: stream-ordered scratch of the

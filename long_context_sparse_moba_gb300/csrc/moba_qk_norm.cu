@@ -405,12 +405,42 @@ struct Area {
 };
 Area area(const void *p, long long stride, int heads, int D) { return {p, 2 * stride, 2ll * heads * D}; }
 
-// an output against what else the call reads and writes; it may be `same`, in place
-bool collides(const Area &out, const Area &in, bool same, long long tokens) {
+// an output against what else the call reads and writes; `own`: its own operand, which it may be
+// in place (that goes by the operand, not by its address: another one may have the same)
+bool collides(const Area &out, const Area &in, bool own, long long tokens) {
     if (!in.p || !out.p) return false;
-    if (same && out.p == in.p && out.stride == in.stride) return false;
+    if (own && out.p == in.p && out.stride == in.stride) return false;
     return overlaps(out.p, out.stride, out.width, in.p, in.stride, in.width, tokens);
 }
+
+// `bytes` at p in one piece, and whether an area's rows meet them, or another piece does
+struct Piece {
+    const void *p;
+    long long bytes;
+};
+bool collides(const Area &rows, const Piece &x, long long tokens) {
+    if (!rows.p || !x.p) return false;
+    const intptr_t r = reinterpret_cast<intptr_t>(rows.p), lo = reinterpret_cast<intptr_t>(x.p), hi = lo + x.bytes;
+    const long long first = lo < r + rows.width ? 0 : (lo - r - rows.width) / rows.stride + 1;  // row that ends behind lo
+    return first < tokens && r + first * rows.stride < hi;
+}
+bool collides(const Piece &x, const Piece &y) {
+    const intptr_t a = reinterpret_cast<intptr_t>(x.p), b = reinterpret_cast<intptr_t>(y.p);
+    return x.p && y.p && a < b + y.bytes && b < a + x.bytes;
+}
+
+// What a call reads beside q, k and their gradients.
+struct Small {
+    Piece all[4];
+    Small(const Args &a, int D)
+        : all{{a.q.w, (a.w32 ? 4ll : 2ll) * D}, {a.k.heads ? a.k.w : nullptr, (a.w32 ? 4ll : 2ll) * D}, {a.pos, 4ll * a.tokens},
+              {a.freqs, 4ll * a.rot}} {}
+    bool meet(const Area &out, long long tokens) const {
+        for (const Piece &x : all)
+            if (collides(out, x, tokens)) return true;
+        return false;
+    }
+};
 
 template <int D>
 cudaError_t launch_fwd(const Args &a, bool interleaved, cudaStream_t st) {
@@ -472,8 +502,9 @@ MOBA_EXPORT int moba_qk_norm_rope(const void *q, const void *k, void *q_out, voi
     if (rc != MOBA_OK) return rc;
     const Area qi = area(q, a.q.xs, Hq, D), qo = area(q_out, a.q.os, Hq, D);
     const Area ki = Hk ? area(k, a.k.xs, Hk, D) : Area{}, ko = Hk ? area(k_out, a.k.os, Hk, D) : Area{};
+    const Small small(a, D);
     if (collides(qo, qi, true, tokens) || collides(qo, ki, false, tokens) || collides(ko, qi, false, tokens) ||
-        collides(ko, ki, true, tokens) || collides(ko, qo, false, tokens))
+        collides(ko, ki, true, tokens) || collides(ko, qo, false, tokens) || small.meet(qo, tokens) || small.meet(ko, tokens))
         return MOBA_ERR_INVALID_ARG;
     a.wide = wide(a);
     a.status = status_word();
@@ -526,11 +557,18 @@ MOBA_EXPORT int moba_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, co
     const Area qx = area(q, a.q.xs, Hq, D), qy = area(dq_out, a.q.ds, Hq, D), qo = area(dq, a.q.os, Hq, D);
     const Area kx = Hk ? area(k, a.k.xs, Hk, D) : Area{}, ky = Hk ? area(dk_out, a.k.ds, Hk, D) : Area{};
     const Area ko = Hk ? area(dk, a.k.os, Hk, D) : Area{};
-    for (const Area &in : {qx, kx, qy, ky})
-        if (collides(qo, in, in.p == dq_out && in.width == qo.width, tokens) ||
-            collides(ko, in, in.p == dk_out && in.width == ko.width, tokens))
-            return MOBA_ERR_INVALID_ARG;
-    if (collides(ko, qo, false, tokens)) return MOBA_ERR_INVALID_ARG;
+    if (collides(qo, qy, true, tokens) || collides(qo, ky, false, tokens) || collides(ko, ky, true, tokens) ||
+        collides(ko, qy, false, tokens) || collides(ko, qo, false, tokens))
+        return MOBA_ERR_INVALID_ARG;
+    const Piece wq = {dq_weight, 4ll * D}, wk = {Hk ? dk_weight : nullptr, 4ll * D};
+    for (const Area &in : {qx, kx})
+        if (collides(qo, in, false, tokens) || collides(ko, in, false, tokens)) return MOBA_ERR_INVALID_ARG;
+    for (const Area &rows : {qx, kx, qy, ky, qo, ko})
+        if (collides(rows, wq, tokens) || collides(rows, wk, tokens)) return MOBA_ERR_INVALID_ARG;
+    const Small small(a, D);
+    for (const Piece &x : small.all)
+        if (collides(x, wq) || collides(x, wk)) return MOBA_ERR_INVALID_ARG;
+    if (collides(wq, wk) || small.meet(qo, tokens) || small.meet(ko, tokens)) return MOBA_ERR_INVALID_ARG;
     a.wide = wide(a);
     const int grid = bwd_grid(&a, D);
     const size_t need = sizeof(float) * D * (size_t)grid;
