@@ -29,6 +29,8 @@ struct Cache {
     __device__ __forceinline__ int seq(int b, Seq &s) const {
         return check(__ldg(cu + b), __ldg(cu + b + 1), __ldg(lens + b), s);
     }
+    // (the same by plain loads: see launch_after)
+    __device__ __forceinline__ int seq_now(int b, Seq &s) const { return check(cu[b], cu[b + 1], lens[b], s); }
     __device__ __forceinline__ int check(int lo, int hi, int len, Seq &s) const {
         s.row0 = lo;
         s.len = len;
@@ -45,12 +47,12 @@ struct Cache {
     }
 
     // The sequence that may hold packed row t: the last one that starts at or before it, 32
-    // places a look.  All lanes of a warp call it, with the same t.
+    // places a look, by plain loads.  All lanes of a warp call it, with the same t.
     __device__ __forceinline__ int seq_of_row(int t, int lane) const {
         int lo = 0, n = num_seqs;  // the answer is in [lo, lo + n)
         while (n > 1) {
             const int step = (n + 31) / 32;
-            const bool below = lane * step < n && __ldg(cu + lo + lane * step) <= t;
+            const bool below = lane * step < n && cu[lo + lane * step] <= t;
             const unsigned some = __ballot_sync(0xffffffffu, below);
             const int last = some ? 31 - __clz(some) : 0;
             n = min(step, n - last * step);
@@ -83,7 +85,9 @@ struct Cache {
 // its results (or ends with it, where it needs none of them).  Every CTA of every kernel
 // in such a row has to make that wait, so that a kernel's end implies the end of all before it.
 // (The first kernel of some calls is launched so too: what is before it on the stream has then
-// ended when its wait has; 2 us less from call to call.)
+// ended when its wait has; 2 us less from call to call.  What wrote its operands may run while it
+// is there already, so they are no constant data to it: behind the wait, and by plain loads, which
+// stay behind it.  It lets the next kernel in behind its wait: to that one they are constant.)
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                          const A &...args) {

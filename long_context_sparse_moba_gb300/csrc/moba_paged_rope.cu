@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) write_kernel(WriteArgs a) 
     // refused sequences are reported, rows or not
     for (int b = blockIdx.x * 32 * kWarps + threadIdx.x; b < a.c.num_seqs; b += gridDim.x * 32 * kWarps) {
         Seq s;
-        if (a.c.seq(b, s) == kSeqBad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
+        if (a.c.seq_now(b, s) == kSeqBad) atomicCAS(a.status, 0, (int)MOBA_ERR_INVALID_ARG);
     }
     if (threadIdx.x == 0) {
         for (int w = 0; w < kWarps; ++w) StepRing::init(s_bar[w]);
@@ -118,11 +118,11 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) write_kernel(WriteArgs a) 
         const int b = a.c.seq_of_row(t, lane);
         Seq s;
         // (rows of no sequence, or of a refused one, are left as they were)
-        const bool live = a.c.seq(b, s) == kSeqOk && t >= s.row0 && t < s.row0 + s.n;
+        const bool live = a.c.seq_now(b, s) == kSeqOk && t >= s.row0 && t < s.row0 + s.n;
         const int p = live ? s.len - s.n + t - s.row0 : 0;  // the token's place
         __nv_bfloat16 *page_k = nullptr, *page_v = nullptr;
         if (live && h1 > a.Hq) {
-            const int page = __ldg(a.c.table + (size_t)b * a.c.max_pages + (p >> a.psh));
+            const int page = a.c.table[(size_t)b * a.c.max_pages + (p >> a.psh)];
             if ((unsigned)page < (unsigned)a.c.num_pages) {
                 const size_t at = (((size_t)page * Hkv << a.psh) + (p & (ps - 1))) * D;
                 page_k = a.kp + at;
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) write_kernel(WriteArgs a) 
         }
         float2 c[4], sn[4];
         if (h0 < a.Hq + Hkv) {
-            warp_cos_sin(s_turn, a.rot / 2, lane, a.pos ? __ldg(a.pos + t) : p, a.mag, 1.f, s_c[warp], s_s[warp]);
+            warp_cos_sin(s_turn, a.rot / 2, lane, a.pos ? a.pos[t] : p, a.mag, 1.f, s_c[warp], s_s[warp]);
             if (turns) {
                 load_eight(s_c[warp] + item * 8, c);
                 load_eight(s_s[warp] + item * 8, sn);

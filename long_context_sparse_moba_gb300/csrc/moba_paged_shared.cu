@@ -125,24 +125,24 @@ __global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
     const int tid = threadIdx.x, ns = c.num_seqs, ng = x.n_groups, G = a.G, Hkv = c.Hkv;
     if (HELD) {
         for (int i = tid; i <= ns; i += T) {
-            s_cu[i] = __ldg(c.cu + i);
-            if (i < ns) s_len[i] = __ldg(c.lens + i);
+            s_cu[i] = c.cu[i];
+            if (i < ns) s_len[i] = c.lens[i];
         }
         for (int i = tid; ng > 0 && i <= ng; i += T) {
-            s_grp[i] = __ldg(x.cu_groups + i);
-            if (i < ng) s_pre[i] = __ldg(x.prefix_lens + i);
+            s_grp[i] = x.cu_groups[i];
+            if (i < ng) s_pre[i] = x.prefix_lens[i];
         }
         __syncthreads();
     }
-    auto cu = [&](int i) { return HELD ? s_cu[i] : __ldg(c.cu + i); };
-    auto grp = [&](int i) { return HELD ? s_grp[i] : __ldg(x.cu_groups + i); };
-    auto pre = [&](int i) { return HELD ? s_pre[i] : __ldg(x.prefix_lens + i); };
+    auto cu = [&](int i) { return HELD ? s_cu[i] : c.cu[i]; };
+    auto grp = [&](int i) { return HELD ? s_grp[i] : x.cu_groups[i]; };
+    auto pre = [&](int i) { return HELD ? s_pre[i] : x.prefix_lens[i]; };
     int *rep = HELD ? s_rep : x.rep, *at = HELD ? s_at : x.at;
     auto sync = [&] {
         if (!HELD) __threadfence_block();
         __syncthreads();
     };
-    auto seq = [&](int b, Seq &s) { return c.check(cu(b), cu(b + 1), HELD ? s_len[b] : __ldg(c.lens + b), s); };
+    auto seq = [&](int b, Seq &s) { return c.check(cu(b), cu(b + 1), HELD ? s_len[b] : c.lens[b], s); };
     // groups: offsets that lead nowhere void all of them
     bool wrong = false;
     for (int g = tid; ng > 0 && g <= ng; g += T) {
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
         if (g < 0 || seq(b, s) != kSeqOk) continue;
         const int l = HELD ? *(volatile const int *)(rep + g) : __ldcg(rep + g), page = pre(g) / c.ps - 1;
         if (l < 0 || l == b || page < 0) continue;
-        if (__ldg(c.table + (size_t)b * c.max_pages + page) != __ldg(c.table + (size_t)l * c.max_pages + page))
+        if (c.table[(size_t)b * c.max_pages + page] != c.table[(size_t)l * c.max_pages + page])
             atomicMin(rep + g, -1);
     }
     sync();

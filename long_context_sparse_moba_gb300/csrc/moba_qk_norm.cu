@@ -119,12 +119,12 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdCtas) fwd_kernel(Args a) {
     };
 #pragma unroll 1
     for (int i = 0; i < FwdRing::kStages - 1; ++i) issue();
-    int pos = u < units ? __ldg(a.pos + token(u)) : 0;
+    int pos = u < units ? a.pos[token(u)] : 0;
     bool ok = true;
     for (; ok && u < units; u += stride) {
         const int t = token(u), h0 = begin(u), h1 = min(h0 + a.chunk, heads);
         warp_cos_sin(s_turn, a.rot / 2, lane, pos, a.mag, 1.f, s_c[warp], s_s[warp]);
-        if (u + stride < units) pos = __ldg(a.pos + token(u + stride));
+        if (u + stride < units) pos = a.pos[token(u + stride)];
         float2 c[4], s[4];
         if (turns) {
             load_eight(s_c[warp] + item * 8, c);
@@ -228,12 +228,12 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
     };
 #pragma unroll 1
     for (int i = 0; i < R::kStages - 1; ++i) issue();
-    int pos = u < units ? __ldg(a.pos + token(u)) : 0;
+    int pos = u < units ? a.pos[token(u)] : 0;
     bool ok = true;
     for (; ok && u < units; u += stride) {
         const int t = token(u), lo = begin(u), hi = end(lo);
         warp_cos_sin(s_turn, a.rot / 2, lane, pos, a.mag, -1.f, s_c[warp], s_s[warp]);
-        if (u + stride < units) pos = __ldg(a.pos + token(u + stride));
+        if (u + stride < units) pos = a.pos[token(u + stride)];
         float2 c[4], s[4];
         if (turns) {
             load_eight(s_c[warp] + item * 8, c);

@@ -25,10 +25,11 @@ __device__ __forceinline__ void vectors(int item, int half, int &va, int &vb) {
 }
 
 // frac(freq / 2 pi) * 2^64 of every pair: turns per position in fixed point
+// (Plain loads here and in weight(): see launch_after.)
 __device__ __forceinline__ void load_turns(unsigned long long *turn, const double *freqs, int half,
                                            int thread, int threads) {
     for (int i = thread; i < half; i += threads) {
-        const double t = __ldg(freqs + i) * 0.15915494309189533577;  // turns per position
+        const double t = freqs[i] * 0.15915494309189533577;  // turns per position
         turn[i] = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
     }
 }
@@ -201,8 +202,7 @@ __device__ __forceinline__ float inverse_rms(const float2 (&a)[4], const float2 
 }
 
 __device__ __forceinline__ float weight(const void *w, int w32, int d) {
-    return w32 ? __ldg(static_cast<const float *>(w) + d)
-               : __bfloat162float(__ldg(static_cast<const __nv_bfloat16 *>(w) + d));
+    return w32 ? static_cast<const float *>(w)[d] : __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[d]);
 }
 
 // a head over its root mean square, times the weights

@@ -1,0 +1,43 @@
+"""Kernels that are brought in while the one before them on the stream drains (their source,
+read as text): what they may rely on there is not something that a run shows."""
+import os
+import re
+
+import pytest
+
+from long_context_sparse_moba_gb300 import build
+
+
+def source(name):
+    with open(os.path.join(build.CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def body(text, name):
+    """A function's body, its braces matched."""
+    at = re.search(r"\b%s\([^;{]*\)(?: const)? \{" % re.escape(name), text)
+    assert at, name
+    depth, i = 1, at.end()
+    while depth:
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        i += 1
+    return text[at.end():i]
+
+
+# first kernels of their calls: file, kernel, and what they call that reads operands
+FIRST = [("moba_qk_norm.cu", "fwd_kernel", ["load_turns", "weight"]), ("moba_qk_norm.cu", "bwd_kernel", ["load_turns", "weight"]),
+         ("moba_paged_rope.cu", "write_kernel", ["load_turns", "weight", "seq_now", "seq_of_row"]),
+         ("moba_paged_shared.cu", "plan_spans_kernel", ["clear_refused"])]
+HEADERS = ["moba_rope.cuh", "moba_paged.cuh", "moba_paged_attn.cuh"]
+
+
+@pytest.mark.parametrize("file,kernel,calls", FIRST)
+def test_first_kernels_take_nothing_for_constant(file, kernel, calls):
+    """What wrote their operands may run while they are there: they wait before they read, let the
+    next kernel in behind that, and read by plain loads (constant ones may be moved up)."""
+    text = body(source(file), kernel)
+    assert 0 <= text.find("after_previous()") < text.find("let_next()")
+    headers = "".join(source(h) for h in HEADERS)
+    for part in [text] + [body(headers, c) for c in calls]:
+        assert "__ldg" not in part
+    assert not re.search(r"\bc\.seq\(", text)  # (which reads constants)
