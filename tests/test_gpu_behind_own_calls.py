@@ -7,6 +7,7 @@ import torch
 from long_context_sparse_moba_gb300 import ops
 
 from .test_gpu_paged_cache import BF, Cache, built, i32, normal  # noqa: F401  (built: a fixture)
+from .test_gpu_paged_rope import same
 
 pytestmark = pytest.mark.gpu
 
@@ -19,11 +20,10 @@ def test_weights_that_the_call_before_wrote(captured):
     w = 1 + 0.3 * normal(2, d).float()
     pos, freqs = torch.arange(T, dtype=torch.int32, device="cuda"), ops.rope_frequencies(d)
     dy = [normal(3 + i, T, h, d) for i in range(steps)]
-    wide = [normal(100 + i, d).float() for i in range(3)]
     c = Cache(1, 512, h, d, 32, 64)
     tables = c.k, c.v, c.kbar, c.table, i32([0, T]), i32([T]), T, c.block, freqs
-    dw, dx = wide[0].clone(), torch.empty(T, h, d, dtype=BF, device="cuda")
-    out, want = [[None] * steps for _ in range(2)]
+    dw, dx = torch.empty(d, device="cuda"), torch.empty(T, h, d, dtype=BF, device="cuda")
+    want = []
     ws = torch.empty(ops.qk_norm_rope_bwd_workspace_size(T, h, 0, d), dtype=torch.uint8, device="cuda")
 
     def step(i):
@@ -34,19 +34,17 @@ def test_weights_that_the_call_before_wrote(captured):
         return y, z, c.k.clone(), c.kbar.clone()
 
     for i in range(steps):
-        want[i] = []
+        made = []
         for g in (dy[i], dy[-1 - i]):
             r = ops.qk_norm_rope_bwd(g, None, x[:, :h], None, w, None, pos, freqs)
             torch.cuda.synchronize()
-            a, b = r[0].clone(), r[2].clone()
+            made.append((r[0].clone(), r[2].clone()))
             torch.cuda.synchronize()
-            if g is dy[i] and not want[i]:
-                want[i].append(ops.qk_norm_rope(a, None, b, None, pos, freqs)[0])
-            else:
-                z = ops.paged_append_rope(a, x[:, h:2 * h], x[:, 2 * h:], *tables, q_weight=b, k_weight=b)
-                torch.cuda.synchronize()
-                want[i] += [z, c.k.clone(), c.kbar.clone()]
+        (x1, w1), (x2, w2) = made
+        y = ops.qk_norm_rope(x1, None, w1, None, pos, freqs)[0]
+        z = ops.paged_append_rope(x2, x[:, h:2 * h], x[:, 2 * h:], *tables, q_weight=w2, k_weight=w2)
         torch.cuda.synchronize()
+        want.append((y, z, c.k.clone(), c.kbar.clone()))
     if captured:
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
@@ -56,5 +54,5 @@ def test_weights_that_the_call_before_wrote(captured):
     else:
         out = [step(i) for i in range(steps)]
     for a, b in zip(out, want):
-        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        assert all(same(x, y) for x, y in zip(a, b))
     assert ops.get_status() == ops.MOBA_OK
