@@ -67,12 +67,16 @@ struct Cache {
     // There are tile_slots of them; a slot's sequence, and its tile (any number: it
     // may lie behind the sequence's end).
     __device__ __forceinline__ int tile_of(int slot, int G, int rows, int spare, int &tile) const {
+        return tile_by([](const int *p) { return __ldg(p); }, slot, G, rows, spare, tile);
+    }
+    template <typename Read>
+    __device__ __forceinline__ int tile_by(Read read, int slot, int G, int rows, int spare, int &tile) const {
         int lo = 0, hi = num_seqs - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if ((long long)__ldg(cu + mid) * G / rows + (long long)spare * mid <= slot) lo = mid; else hi = mid - 1;
+            if ((long long)read(cu + mid) * G / rows + (long long)spare * mid <= slot) lo = mid; else hi = mid - 1;
         }
-        tile = (int)(slot - ((long long)__ldg(cu + lo) * G / rows + (long long)spare * lo));
+        tile = (int)(slot - ((long long)read(cu + lo) * G / rows + (long long)spare * lo));
         return lo;
     }
     __host__ __device__ long long tile_slots(int G, int rows, int spare) const {

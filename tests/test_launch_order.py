@@ -41,3 +41,15 @@ def test_first_kernels_take_nothing_for_constant(file, kernel, calls):
     for part in [text] + [body(headers, c) for c in calls]:
         assert "__ldg" not in part
     assert not re.search(r"\bc\.seq\(", text)  # (which reads constants)
+
+
+def test_pooling_reads_nothing_before_its_wait():
+    """The kernel before it is ordered behind what wrote tables and older keys; this one is only
+    by waiting for that one's end.  Before, it may ask for memory, by relaxed loads."""
+    text = body(source("moba_paged.cu"), "pool_kernel")
+    wait = text.find("after_previous()")
+    assert text.count("after_previous()") == 1 and 0 < text.find("prefetch.global.L2") < wait < text.find("__syncthreads")
+    assert "__ldg" not in text and "a.c.seq(" not in text and "tile_of" not in text
+    early = re.sub(r"__shared__[^;]*;", "", text[:wait])
+    assert "s_page[" not in early and "s_red[" not in early
+    assert "__ldg" not in body(source("moba_paged.cu"), "mean64")
