@@ -34,6 +34,7 @@ struct alignas(16) SpanHead {
     long long units[2];  // of all of them, times the kv heads
     int spans[2], own[2];
     int taken, pad[3];   // runs of small spans that have been taken
+    unsigned long long ready, pads;  // the call's token once the plan is made; 0 again when the call ends
 };
 
 struct Attn {

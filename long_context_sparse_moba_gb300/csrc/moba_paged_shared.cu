@@ -24,6 +24,8 @@
 // 32 / 8 heads, 69 us (plan 3, big spans 37, small ones some 15 behind them, merge 12); 16 of 16384
 // with up to 2000, 32 / 32 heads, 99; 3 groups of 11 with up to 5 new tokens, 20 / 4 heads of 64, 37; 8
 // questions of up to 200 tokens on 16384 181, 1160 TFLOP/s of what they cannot do without.
+#include <atomic>
+
 #include "moba_mma.cuh"
 #include "moba_paged_attn.cuh"
 #include "moba_ptx.cuh"
@@ -65,6 +67,7 @@ struct SharedArgs {
     int warps;                   // of the streaming kernel
     int psh;                     // log2(page size)
     bool beside;                 // big spans' kernel runs before the small ones', which begin as its CTAs end
+    unsigned long long token;    // the call's own number, which no memory holds by chance
     // scratch
     Span *tiles_small;           // [...]
     long long *off_small;        // [... + 1] units before each (and kSmallStart), times the kv heads
@@ -343,7 +346,13 @@ __global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
             h.own[z] = (int)own_of[z];
         }
         h.taken = h.pad[0] = h.pad[1] = h.pad[2] = 0;
+        h.ready = h.pads = 0;
         *a.head = h;
+    }
+    if (x.beside) {  // (every thread's part of it, and all that was before it on the stream)
+        __syncthreads();
+        if (tid == 0)
+            asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(&a.head->ready), "l"(x.token) : "memory");
     }
 }
 
@@ -381,7 +390,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
     constexpr int C = R::C, O = R::O, ST = R::kStages;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) unsigned long long s_bar[kStreamWarps][ST];
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_ready;
     const Attn &a = x.a;
     const Cache &c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n8 = lane >> 2, c4 = lane & 3;
@@ -389,13 +398,22 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
         for (int i = 0; i < kStreamWarps; ++i)
             for (int s = 0; s < ST; ++s) ptx::mbar_init(ptx::saddr(&s_bar[i][s]), 1);
         s_abort = 0;
+        s_ready = 0;
+        if (x.beside) {
+            unsigned long long got;
+            asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(got) : "l"(&a.head->ready) : "memory");
+            s_ready = got == x.token;
+        }
         ptx::fence_mbar_init();
     }
     __syncthreads();
-    // Behind the plan.  Where the big spans' kernel lies between them: it lets this one begin once
-    // all its CTAs have waited for the plan, and this one needs nothing of its results, so
-    // that it only has to end behind it (the merge waits for this one's end).
-    if (x.beside) __threadfence();  // (what the plan wrote, not what this SM may still hold)
+    // Behind the plan.  Where the big spans' kernel lies between them, this one needs nothing of
+    // its results, so that it only has to end behind it (the merge waits for this one's end).
+    // It is let in once all CTAs of that one have waited for the plan; but that orders no
+    // memory, so the plan is taken as made where its token says so (in a row of release, acquire
+    // and barrier that what was before the plan is in too), and else by waiting for all.
+    const bool early = s_ready;
+    if (early) asm volatile("fence.proxy.async.global;" ::: "memory");  // (for the bulk copies too)
     else after_previous();
     let_next();
     ptx::Ctl ctl{&s_abort, a.status, kDefaultWaitLimit};
@@ -435,7 +453,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
                 const int hk = (int)((u - o) / T), i = (int)(u - o - hk * T) - kSmallStart;
                 if (i >= 0) {
                     const int key = s.key0 + i * kUnit;
-                    const int page = __ldg(c.table + (size_t)s.b * c.max_pages + (key >> x.psh));
+                    const int page = c.table[(size_t)s.b * c.max_pages + (key >> x.psh)];
                     bad = (unsigned)page >= (unsigned)c.num_pages;
                     // (some memory of the pool for a page outside it: its rows are dropped)
                     place = (((bad ? 0 : page) * Hkv + hk) << x.psh) + (key & (ps - 1));
@@ -489,7 +507,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
                 const __nv_bfloat16 *src = a.q + ((size_t)t * a.Hq + hk * G + (row - t * G)) * D + 16 * c4;
 #pragma unroll
                 for (int i = 0; i < C; ++i)
-                    qr[i][h] = live ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * (i >> 1) + 8 * (i & 1)))
+                    qr[i][h] = live ? *reinterpret_cast<const uint4 *>(src + 64 * (i >> 1) + 8 * (i & 1))
                                     : make_uint4(0, 0, 0, 0);
             }
             float o[O][8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -633,7 +651,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
         next = __shfl_sync(0xffffffffu, next, 0);
         if (next >= shorts) break;
     }
-    if (x.beside) after_previous();
+    if (early) after_previous();
 }
 
 // ----------------------------------------------------------------------------
@@ -652,6 +670,7 @@ __global__ void __launch_bounds__(kMergeThreads, TEAM == 16 ? 3 : 4) merge_spans
     const Attn &a = x.a;
     after_previous();
     let_next();
+    if (x.beside && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) a.head->ready = 0;  // (a replay has the same token)
     const int team = threadIdx.x / TEAM, lane = threadIdx.x % TEAM, G = a.G, Hkv = a.c.Hkv;
     const bool chunk = a.chunk;
     // (a span behind the last one is some memory of the scratch)
@@ -802,6 +821,16 @@ size_t scratch(SharedArgs *x, void *base) {
     return off;
 }
 
+// A call's own number, spread over 64 bits: workspaces come with any contents.
+unsigned long long new_token() {
+    static std::atomic<unsigned long long> calls{0};
+    unsigned long long z = calls.fetch_add(1, std::memory_order_relaxed) + 0x9e3779b97f4a7c15ull;
+    z = (z ^ z >> 30) * 0xbf58476d1ce4e5b9ull;
+    z = (z ^ z >> 27) * 0x94d049bb133111ebull;
+    z ^= z >> 31;
+    return z ? z : 1;
+}
+
 // Sizes of a call whose cache has been checked (x->a.c is filled).
 int make_shared(SharedArgs *x, int Hq, int D, int n_groups) {
     Attn &a = x->a;
@@ -927,6 +956,7 @@ MOBA_EXPORT int moba_paged_attn_shared(const void *q, const void *k_pages, const
     }
     scratch(&x, workspace);
     x.beside = x.cap_big && !a.chunk;
+    x.token = new_token();
     cudaError_t e = launch_plan(x, st);
     if (e == cudaSuccess && (x.cap_big || a.chunk)) e = launch_chunk_spans(a, st);
     if (e == cudaSuccess && !a.chunk) e = D == 64 ? launch_small<64>(x, st) : launch_small<128>(x, st);

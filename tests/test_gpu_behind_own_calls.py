@@ -8,6 +8,7 @@ from long_context_sparse_moba_gb300 import ops
 
 from .test_gpu_paged_cache import BF, Cache, built, i32, normal  # noqa: F401  (built: a fixture)
 from .test_gpu_paged_rope import same
+from .test_gpu_paged_shared import Forks, compare
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,81 @@ def test_weights_that_the_call_before_wrote(captured):
     for a, b in zip(out, want):
         assert all(same(x, y) for x, y in zip(a, b))
     assert ops.get_status() == ops.MOBA_OK
+
+
+@pytest.mark.parametrize("prefix", [512, 8192])
+def test_shared_prefixes_behind_copies_of_their_operands(prefix):
+    """A captured call whose operands are copied in right before it, replayed over workspaces of
+    any contents (prefixes that are streamed, and ones for the tensor cores)."""
+    f = Forks([(prefix, [(1, 1 + i % 40) for i in range(40)]), (64, [(1, 70), (1, 1)])], 8, 64, 16, seed=3)
+    n = len(f.nq)
+    live = [normal(1, n, 32, 64), f.table.clone(), i32(f.lens), i32([0, 40, 42]), i32([prefix, 64])]
+    staged = [x.clone() for x in live]
+    cu, out, lse = i32(f.cu), torch.empty_like(live[0]), torch.empty(n, 32, device="cuda")
+    ws = torch.empty(ops.paged_attn_shared_workspace_size(n, 2, n, 1, 32, 8, 64, 16, f.table.shape[1]), dtype=torch.uint8, device="cuda")
+
+    def call():
+        for x, y in zip(live, staged):
+            x.copy_(y)
+        ops.paged_attn_shared(live[0], f.k, f.v, live[1], cu, live[2], 1, live[3], live[4], out=out, lse=lse, workspace=ws)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for i in range(12):
+        staged[0].copy_(normal(10 + i, n, 32, 64))
+        if i % 3 == 1:  # other pages for everybody: as if the sequences had changed places
+            staged[1].copy_(f.table)
+            staged[2].copy_(i32(f.lens))
+        elif i % 3 == 2:
+            staged[1][:40] = f.table[:40].flip(0)
+            staged[2][:40] = i32(f.lens[:40][::-1])
+        if i % 4 == 0:
+            ws.fill_(i)
+        want = ops.paged_attn_shared(staged[0], f.k, f.v, staged[1], cu, staged[2], 1, staged[3], staged[4])
+        torch.cuda.synchronize()
+        out.fill_(7.0)
+        g.replay()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        call()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    compare(want, f.expect(staged[0]), slice(40, None))
+    assert ops.get_status() == ops.MOBA_OK
+
+
+@pytest.mark.parametrize("seqs", [3, 300])
+def test_pooling_behind_copies_of_the_tables(seqs):
+    """Steps that complete blocks, with page tables and lengths copied in right before them."""
+    hkv, d, page, block = 4, 64, 16, 64
+    freqs = ops.rope_frequencies(d)
+    one, two = (Cache(seqs, 192, hkv, d, page, block, seed=5) for _ in range(2))
+    first = normal(1, seqs * 126, 3 * hkv, d)
+    cu = i32([126 * i for i in range(seqs + 1)])
+    for c in (one, two):
+        ops.paged_append_rope(first[:, :hkv], first[:, hkv:2 * hkv], first[:, 2 * hkv:], c.k, c.v, c.kbar, c.table, cu,
+                              i32([126] * seqs), 126, block, freqs)
+    step = i32(list(range(seqs + 1)))
+    table, lens = one.table.clone(), i32([126] * seqs)
+    x = normal(2, seqs, 3 * hkv, d)
+    staged = [one.table.clone(), i32([126] * seqs), x.clone()]
+    args = x[:, :hkv], x[:, hkv:2 * hkv], x[:, 2 * hkv:], one.k, one.v, one.kbar, table, step, lens, 1, block, freqs
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for a, b in zip((table, lens, x), staged):
+            a.copy_(b)
+        ops.paged_append_rope(*args)
+    for n in range(127, 131):  # the block completed by the second of them
+        order = torch.randperm(seqs, generator=torch.Generator().manual_seed(n)).cuda()
+        staged[0].copy_(one.table[order])
+        staged[1].fill_(n)
+        staged[2].copy_(normal(n, seqs, 3 * hkv, d))
+        torch.cuda.synchronize()
+        g.replay()
+        y = staged[2]
+        torch.cuda.synchronize()
+        ops.paged_append_rope(y[:, :hkv], y[:, hkv:2 * hkv], y[:, 2 * hkv:], two.k, two.v, two.kbar, staged[0], step, staged[1], 1,
+                              block, freqs)
+        torch.cuda.synchronize()
+        for a, b in ((one.k, two.k), (one.v, two.v), (one.kbar, two.kbar)):
+            assert same(a, b)
+    assert not one.kbar[one.table[:, 7].long()].isnan().any() and ops.get_status() == ops.MOBA_OK

@@ -21,7 +21,7 @@ def body(text, name):
     while depth:
         depth += {"{": 1, "}": -1}.get(text[i], 0)
         i += 1
-    return text[at.end():i]
+    return text[at.end():i - 1]
 
 
 # first kernels of their calls: file, kernel, and what they call that reads operands
@@ -53,3 +53,16 @@ def test_pooling_reads_nothing_before_its_wait():
     early = re.sub(r"__shared__[^;]*;", "", text[:wait])
     assert "s_page[" not in early and "s_red[" not in early
     assert "__ldg" not in body(source("moba_paged.cu"), "mean64")
+
+
+def test_streaming_begins_by_the_plans_token_or_waits():
+    """The kernel between it and the plan lets it in without ordering any memory."""
+    text = source("moba_paged_shared.cu")
+    plan, stream, merge = (body(text, n) for n in ("plan_spans_kernel", "stream_kernel", "merge_spans_kernel"))
+    at = plan.find("st.release.gpu")
+    assert plan.rfind("__syncthreads()") < at and plan.rfind("__syncthreads()") > plan.rfind("*a.head = h")
+    begin = stream.find("ld.acquire.gpu")
+    assert 0 < begin < stream.find("__syncthreads()") < stream.find("else after_previous()") < stream.find("a.head->spans")
+    assert stream.rstrip().endswith("if (early) after_previous();")  # it ends behind the kernel before it
+    assert "__ldg" not in stream and "__ldg" not in merge
+    assert merge.find("after_previous()") < merge.find("a.head->ready = 0") < merge.find("return")
