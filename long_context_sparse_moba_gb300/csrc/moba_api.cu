@@ -29,6 +29,34 @@ int *status_word() {
     return a;
 }
 
+// Words in which a kernel leaves its call's token for a later kernel of the call; calls that
+// meet in one find another's token, which says nothing to them.
+constexpr int kReadyWords = 1024;
+__device__ unsigned long long g_moba_ready[kReadyWords];
+
+unsigned long long *ready_word(unsigned long long token) {
+    static std::atomic<unsigned long long *> addr[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    unsigned long long *a = addr[dev].load(std::memory_order_relaxed);
+    if (!a) {
+        void *p = nullptr;
+        if (cudaGetSymbolAddress(&p, g_moba_ready) != cudaSuccess) return nullptr;
+        a = static_cast<unsigned long long *>(p);
+        addr[dev].store(a, std::memory_order_relaxed);
+    }
+    return a + token % kReadyWords;
+}
+
+unsigned long long call_token() {
+    static std::atomic<unsigned long long> calls{0};
+    unsigned long long z = calls.fetch_add(1, std::memory_order_relaxed) + 0x9e3779b97f4a7c15ull;
+    z = (z ^ z >> 30) * 0xbf58476d1ce4e5b9ull;
+    z = (z ^ z >> 27) * 0x94d049bb133111ebull;
+    z ^= z >> 31;
+    return z ? z : 1;
+}
+
 static std::atomic<unsigned long long> g_launches{0};
 
 int past_tile_rows(const Plan &p) { return p.attn_kind == 0 ? tc_tile_rows() : mma_tile_rows(); }

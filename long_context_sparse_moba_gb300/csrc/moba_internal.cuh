@@ -29,6 +29,11 @@ constexpr int kMaxUnion = 8;           // past blocks a fused job may visit
 // with bounded waits record MOBA_ERR_TIMEOUT there.  moba_get_status reads
 // and clears it.
 int *status_word();
+// A call's own number (not 0), spread over 64 bits, which no memory holds by chance: a kernel
+// that releases it where a later one of the call acquires it orders before that one all that
+// was before itself.  And a word of the current device for it, where the call has none.
+unsigned long long call_token();
+unsigned long long *ready_word(unsigned long long token);
 
 struct Geometry {
     const int *cu;        // [num_seqs + 1]

@@ -263,10 +263,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 // The pooled keys of blocks whose new tokens a kernel of the same call has just written: the
 // sums of append_kernel in its order, so to the same bits, by one CTA a block and kv
 // head that takes the groups of tokens (p % G) in turn.  A step completes few blocks, so a
-// CTA looks at several and leaves most.
-// Nothing that is read before that kernel has ended counts: only its end makes what came before
-// it visible here too.  Until then a block's older keys are asked into L2, by tables that are
-// read again behind the wait.
+// CTA looks at several and leaves most.  A thread waits for that kernel when it comes to
+// the first new token: until then a block's older keys are on their way.  What was written
+// before that kernel (tables, older keys) is ordered before this one by the token that it
+// releases, or by its end where that is not seen; nothing is constant data.
 // Bound: latency (a block's keys in four rounds of loads).  32 blocks of 512 on 8 kv heads of
 // 128 16 us; one of 64 sequences' 5 beside the kernel before it (9 where every thread waited
 // first; clusters of append_kernel's kind 11 and 19).
@@ -275,7 +275,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 // that complete a block of 2048 43 and 35, six chunks of up to 2000 with blocks of 512 50 and 45; four
 // of up to 8192 90 and 94, 256 sequences of one token 10 and 21.)
 constexpr int kPoolWide = 2;
-constexpr int kPoolAhead = 8;  // candidates of a CTA whose older keys are asked for
 constexpr int pool_ctas(int threads) { return threads == 256 ? 3 : 1; }  // of an SM
 
 template <int D, bool MAX, int T>
@@ -286,47 +285,25 @@ __global__ void __launch_bounds__(T, pool_ctas(T)) pool_kernel(AppendArgs a, int
     __shared__ float s_red[G][D], s_sum[kAppendParts][D];
     __shared__ int s_page[kAppendPages];
     const int tid = threadIdx.x, col = tid % CW, bs = a.c.bs, ps = a.c.ps;
+    __shared__ int s_early;
+    if (tid == 0) s_early = ptx::ld_acquire(a.ready) == a.token;
+    __syncthreads();
+    bool waited = !s_early;
+    if (waited) after_previous();
     let_next();
-    // the sequence and the first position of a candidate that its new tokens complete (else false)
-    auto look = [&](auto read, int i, int &b, int &p0, Seq &s) {
-        const int bj = i / a.c.Hkv;
-        int nth;
+    for (int i = blockIdx.x; i < candidates; i += gridDim.x) {
+        const int hk = i % a.c.Hkv, bj = i / a.c.Hkv;
+        int b, nth;
         if (a.cand > 0) {
             b = bj / a.cand;
             nth = bj % a.cand;
         } else {
-            b = a.c.tile_by(read, bj, 1, bs, 2, nth);
+            b = a.c.tile_by([](const int *p) { return *p; }, bj, 1, bs, 2, nth);
         }
-        if (a.c.check(read(a.c.cu + b), read(a.c.cu + b + 1), read(a.c.lens + b), s) != kSeqOk || nth < 0 ||
-            nth > s.n / bs + 1)
-            return false;
-        p0 = ((s.len - s.n) / bs + nth) * bs;
-        return p0 + bs <= s.len;
-    };
-    for (int i = blockIdx.x, n = 0; i < candidates && n < kPoolAhead; i += gridDim.x, ++n) {
-        auto peek = [](const int *p) {
-            int v;
-            asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-            return v;
-        };
-        constexpr int L = D / 64;  // lines of 128 bytes to a key
-        int b, p0;
         Seq s;
-        if (!look(peek, i, b, p0, s)) continue;
-        const int older = min(s.len - s.n - p0, bs), hk = i % a.c.Hkv;
-        for (int k = tid; k < older * L; k += T) {
-            const int p = p0 + k / L, page = peek(a.c.table + (size_t)b * a.c.max_pages + (p >> a.psh));
-            if ((unsigned)page < (unsigned)a.c.num_pages)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(
-                    a.kp + ((((size_t)page * a.c.Hkv + hk) << a.psh) + (p & (ps - 1))) * D + k % L * 64));
-        }
-    }
-    after_previous();
-    for (int i = blockIdx.x; i < candidates; i += gridDim.x) {
-        const int hk = i % a.c.Hkv;
-        int b, p0;
-        Seq s;
-        if (!look([](const int *p) { return *p; }, i, b, p0, s)) continue;
+        if (a.c.seq_now(b, s) != kSeqOk || nth < 0 || nth > s.n / bs + 1) continue;
+        const int p0 = ((s.len - s.n) / bs + nth) * bs, fresh = s.len - s.n - p0;  // the first new token's place
+        if (p0 + bs > s.len) continue;
         const int *table = a.c.table + (size_t)b * a.c.max_pages + (p0 >> a.psh);
         const int pages = bs >> a.psh;
         const bool held = pages <= kAppendPages;
@@ -336,6 +313,10 @@ __global__ void __launch_bounds__(T, pool_ctas(T)) pool_kernel(AppendArgs a, int
         bool bad = false;
 #pragma unroll 1
         for (int g = tid / CW; g < G; g += GP) {
+            if (!waited && g < bs && g + (bs - 1 - g) / G * G >= fresh) {
+                after_previous();
+                waited = true;
+            }
             float acc[8], comp[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -395,11 +376,16 @@ __global__ void __launch_bounds__(T, pool_ctas(T)) pool_kernel(AppendArgs a, int
                 else kahan(sum, cp, s_sum[r][tid]);
             }
             if (!MAX) sum /= (float)bs;
-            if (!MAX && !(fabsf(sum) < INFINITY))  // (as in append_kernel)
+            if (!MAX && !(fabsf(sum) < INFINITY)) {  // (as in append_kernel; every key, new ones too)
+                if (!waited) after_previous();
+                waited = true;
                 sum = mean64<D>(a.kp, a.c.Hkv, a.psh, table - (p0 >> a.psh), hk, tid, p0, bs, p0 + bs, nullptr);
+            }
             a.kbar[((size_t)table[pages - 1] * a.c.Hkv + hk) * D + tid] = sum;
         }
     }
+    if (!waited) after_previous();
+    if (blockIdx.x == 0 && tid == 0) *a.ready = 0;  // (a replay of the call has the same token)
 }
 
 // ----------------------------------------------------------------------------
@@ -501,7 +487,10 @@ int make_pool(AppendArgs *a, const Cache &c, void *k_pages, float *kbar_pages, i
     a->status = status;
     const int rc = plan_blocks(a);
     if (rc != MOBA_OK) return rc;
-    return a->clusters * c.Hkv >= (1ll << 30) ? MOBA_ERR_UNSUPPORTED : MOBA_OK;
+    if (a->clusters * c.Hkv >= (1ll << 30)) return MOBA_ERR_UNSUPPORTED;
+    a->token = call_token();
+    a->ready = ready_word(a->token);
+    return a->ready ? MOBA_OK : cuda_result(cudaErrorInvalidDevice);
 }
 
 template <int D, int T>

@@ -140,9 +140,11 @@ struct AppendArgs {
     long long clusters;
     int ctas;  // of a cluster
     int *status;
+    unsigned long long *ready, token;  // pooling alone: where the kernel before it leaves the call's token
 };
-// Pooling alone, behind a kernel of the same call that wrote the pages: its arguments
-// (MOBA_OK, or why not), and the launch.
+// Pooling alone, behind a kernel of the same call that writes the pages and, behind its own wait
+// and before it lets this one in, releases the token: its arguments (MOBA_OK, or why not), and
+// the launch.
 int make_pool(AppendArgs *a, const Cache &c, void *k_pages, float *kbar_pages, int *status);
 cudaError_t launch_pool(const AppendArgs &a, int D, bool max, cudaStream_t st);
 

@@ -48,6 +48,7 @@ struct WriteArgs {
     int w32;                    // weights are fp32 (else bf16)
     float eps, mag;
     int *status;
+    unsigned long long *ready, token;  // for the pooling (nullptr: none)
 };
 
 // A warp works through its units' steps, kUnroll heads of every lane each, of q, of k or
@@ -64,6 +65,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) write_kernel(WriteArgs a) 
     __shared__ unsigned long long s_turn[D / 2];
     __shared__ __align__(16) float s_w[2][D], s_c[kWarps][D / 2], s_s[kWarps][D / 2];
     after_previous();
+    if (a.ready && blockIdx.x == 0 && threadIdx.x == 0) ptx::st_release(a.ready, a.token);
     let_next();
     load_turns(s_turn, a.freqs, a.rot / 2, threadIdx.x, 32 * kWarps);
     for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps) {
@@ -273,6 +275,8 @@ MOBA_EXPORT int moba_paged_append_rope(const void *q, const void *k, const void 
     if (kbar_pages) {
         rc = make_pool(&pool, a.c, k_pages, kbar_pages, a.status);
         if (rc != MOBA_OK) return rc;
+        a.ready = pool.ready;
+        a.token = pool.token;
     }
     split_heads(Hq + 2 * Hkv, total, D, kUnroll, &a.chunk, &a.splits);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);

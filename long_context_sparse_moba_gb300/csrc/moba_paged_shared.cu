@@ -24,8 +24,6 @@
 // 32 / 8 heads, 69 us (plan 3, big spans 37, small ones some 15 behind them, merge 12); 16 of 16384
 // with up to 2000, 32 / 32 heads, 99; 3 groups of 11 with up to 5 new tokens, 20 / 4 heads of 64, 37; 8
 // questions of up to 200 tokens on 16384 181, 1160 TFLOP/s of what they cannot do without.
-#include <atomic>
-
 #include "moba_mma.cuh"
 #include "moba_paged_attn.cuh"
 #include "moba_ptx.cuh"
@@ -351,8 +349,7 @@ __global__ void __launch_bounds__(T) plan_spans_kernel(SharedArgs x) {
     }
     if (x.beside) {  // (every thread's part of it, and all that was before it on the stream)
         __syncthreads();
-        if (tid == 0)
-            asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(&a.head->ready), "l"(x.token) : "memory");
+        if (tid == 0) ptx::st_release(&a.head->ready, x.token);
     }
 }
 
@@ -398,12 +395,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
         for (int i = 0; i < kStreamWarps; ++i)
             for (int s = 0; s < ST; ++s) ptx::mbar_init(ptx::saddr(&s_bar[i][s]), 1);
         s_abort = 0;
-        s_ready = 0;
-        if (x.beside) {
-            unsigned long long got;
-            asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(got) : "l"(&a.head->ready) : "memory");
-            s_ready = got == x.token;
-        }
+        s_ready = x.beside && ptx::ld_acquire(&a.head->ready) == x.token;
         ptx::fence_mbar_init();
     }
     __syncthreads();
@@ -821,16 +813,6 @@ size_t scratch(SharedArgs *x, void *base) {
     return off;
 }
 
-// A call's own number, spread over 64 bits: workspaces come with any contents.
-unsigned long long new_token() {
-    static std::atomic<unsigned long long> calls{0};
-    unsigned long long z = calls.fetch_add(1, std::memory_order_relaxed) + 0x9e3779b97f4a7c15ull;
-    z = (z ^ z >> 30) * 0xbf58476d1ce4e5b9ull;
-    z = (z ^ z >> 27) * 0x94d049bb133111ebull;
-    z ^= z >> 31;
-    return z ? z : 1;
-}
-
 // Sizes of a call whose cache has been checked (x->a.c is filled).
 int make_shared(SharedArgs *x, int Hq, int D, int n_groups) {
     Attn &a = x->a;
@@ -956,7 +938,7 @@ MOBA_EXPORT int moba_paged_attn_shared(const void *q, const void *k_pages, const
     }
     scratch(&x, workspace);
     x.beside = x.cap_big && !a.chunk;
-    x.token = new_token();
+    x.token = call_token();
     cudaError_t e = launch_plan(x, st);
     if (e == cudaSuccess && (x.cap_big || a.chunk)) e = launch_chunk_spans(a, st);
     if (e == cudaSuccess && !a.chunk) e = D == 64 ? launch_small<64>(x, st) : launch_small<128>(x, st);

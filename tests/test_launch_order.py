@@ -43,25 +43,25 @@ def test_first_kernels_take_nothing_for_constant(file, kernel, calls):
     assert not re.search(r"\bc\.seq\(", text)  # (which reads constants)
 
 
-def test_pooling_reads_nothing_before_its_wait():
-    """The kernel before it is ordered behind what wrote tables and older keys; this one is only
-    by waiting for that one's end.  Before, it may ask for memory, by relaxed loads."""
-    text = body(source("moba_paged.cu"), "pool_kernel")
-    wait = text.find("after_previous()")
-    assert text.count("after_previous()") == 1 and 0 < text.find("prefetch.global.L2") < wait < text.find("__syncthreads")
-    assert "__ldg" not in text and "a.c.seq(" not in text and "tile_of" not in text
-    early = re.sub(r"__shared__[^;]*;", "", text[:wait])
-    assert "s_page[" not in early and "s_red[" not in early
+def test_pooling_begins_by_the_writers_token_or_waits():
+    """The kernel before it is ordered behind what wrote tables and older keys; this one is only by
+    the token which that one releases behind its wait, or by waiting for its end."""
+    write, pool = body(source("moba_paged_rope.cu"), "write_kernel"), body(source("moba_paged.cu"), "pool_kernel")
+    assert write.find("after_previous()") < write.find("st_release(a.ready") < write.find("let_next()")
+    begin = pool.find("ld_acquire(a.ready)")
+    assert 0 < begin < pool.find("__syncthreads()") < pool.find("if (waited) after_previous()") < pool.find("seq_now")
+    assert "__ldg" not in pool and "a.c.seq(" not in pool and "tile_of" not in pool
     assert "__ldg" not in body(source("moba_paged.cu"), "mean64")
+    assert pool.rfind("if (!waited) after_previous();") < pool.find("*a.ready = 0")
 
 
 def test_streaming_begins_by_the_plans_token_or_waits():
     """The kernel between it and the plan lets it in without ordering any memory."""
     text = source("moba_paged_shared.cu")
     plan, stream, merge = (body(text, n) for n in ("plan_spans_kernel", "stream_kernel", "merge_spans_kernel"))
-    at = plan.find("st.release.gpu")
+    at = plan.find("st_release")
     assert plan.rfind("__syncthreads()") < at and plan.rfind("__syncthreads()") > plan.rfind("*a.head = h")
-    begin = stream.find("ld.acquire.gpu")
+    begin = stream.find("ld_acquire")
     assert 0 < begin < stream.find("__syncthreads()") < stream.find("else after_previous()") < stream.find("a.head->spans")
     assert stream.rstrip().endswith("if (early) after_previous();")  # it ends behind the kernel before it
     assert "__ldg" not in stream and "__ldg" not in merge
