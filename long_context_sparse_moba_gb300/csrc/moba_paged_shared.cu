@@ -832,9 +832,11 @@ int make_shared(SharedArgs *x, int Hq, int D, int n_groups) {
     const long long own = rows / (a.chunk ? kJobRows : kSmallRows) + seqs;
     const long long lent = groups ? rows / kSmallRows + groups : 0;  // small spans of groups, at most
     x->few = a.chunk ? -1 : (long long)x->warps * kFewUnits;
-    // no group is big where even a prefix as long as the table is few units, or its rows fit
-    const bool never = !a.chunk && (rows <= kSmallRows || lent * a.c.Hkv * ((long long)a.c.max_pages * a.c.ps / kUnit) <= x->few);
-    const long long big = groups && !never ? rows / kJobRows + groups : 0;
+    // no group is big where even a prefix as long as the table is few units
+    const bool never = !a.chunk && lent * a.c.Hkv * ((long long)a.c.max_pages * a.c.ps / kUnit) <= x->few;
+    // (with up to as many groups as have more rows than a small span, where those are streamed)
+    const long long large = a.chunk ? groups : groups < rows / (kSmallRows + 1) ? groups : rows / (kSmallRows + 1);
+    const long long big = large && !never ? rows / kJobRows + large : 0;
     const long long small = a.chunk ? 0 : lent;
     if ((big + own) * a.c.Hkv >= (1ll << 30) || (small + own) * a.c.Hkv >= (1ll << 30)) return MOBA_ERR_UNSUPPORTED;
     x->cap_big = (int)big;
