@@ -156,19 +156,20 @@ class Pages:
     def groups(self, counts: dict) -> list:
         """Runs of neighbours in ``counts`` (new tokens of each sequence, taken as grown by
         them) that share pages before their new tokens: (first, behind the last, tokens
-        shared) of each run that saves reading, among all of them."""
-        seqs = list(counts)
-        before = [(self._length[s] - counts[s]) // self.page_size for s in seqs]
+        shared) of each run that saves reading, among all of them.  Sequences without new
+        tokens read nothing: they may lie inside a run, and count for nothing."""
+        active = [(at, seq) for at, (seq, n) in enumerate(counts.items()) if n]
+        before = [(self._length[s] - counts[s]) // self.page_size for _, s in active]
         runs, i = [], 0
-        while i < len(seqs):
+        while i < len(active):
             j, common = i + 1, before[i]
-            while j < len(seqs) and common:
-                c = min(common, before[j], self.shared_pages(seqs[i], seqs[j]))
+            while j < len(active) and common:
+                c = min(common, before[j], self.shared_pages(active[i][1], active[j][1]))
                 if c * (j - i) < common * (j - i - 1) or c == 0:
                     break  # (less would be saved with it than without)
                 common, j = c, j + 1
             if j > i + 1:
-                runs.append((i, j, common * self.page_size))
+                runs.append((active[i][0], active[j - 1][0] + 1, common * self.page_size))
             i = j
         return runs
 
@@ -295,8 +296,8 @@ class PagedCache:
         table = [r + [-1] * (width - len(r)) for r in rows]
         groups = []
         hkv, d = self.k_pages.shape[2], self.k_pages.shape[4]
-        runs = self.books.groups(counts)
-        if sum((j - i - 1) * n for i, j, n in runs) * hkv * d * 4 >= SHARED_BYTES:
+        runs, reads = self.books.groups(counts), [bool(n) for n in counts.values()]
+        if sum((sum(reads[i:j]) - 1) * n for i, j, n in runs) * hkv * d * 4 >= SHARED_BYTES:
             edges, shared = [0], []
             for i, j, n in runs:
                 if i > edges[-1]:  # (sequences that share nothing, as a group that does not)
