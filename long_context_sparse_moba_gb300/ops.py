@@ -578,6 +578,14 @@ def _call(device: int, stream, fn):
         return fn(torch.cuda.current_stream().cuda_stream)
 
 
+def _capturing(device: int, stream) -> bool:
+    """Whether the stream that a call with ``stream`` works on is being captured."""
+    if stream is None and torch.cuda.current_device() == device:
+        return torch.cuda.is_current_stream_capturing()
+    with _switched(device, stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 # The checks of these calls are on a decode step's latency path: a tensor's
 # device number says in one look that it is a CUDA tensor and on which device.
 def _is(t, dtype, device) -> bool:

@@ -338,7 +338,8 @@ class PagedCache:
                 q, k = ops.rope(q, k, batch.positions, freqs, interleaved, magnitude, stream=stream)
             ops.paged_append(k, v, *pools, *tables, self.block_size, pooling=self.pooling, stream=stream)
         if shared is None and batch.cu_groups is not None:
-            shared = not (batch.page_table.is_cuda and torch.cuda.is_current_stream_capturing())
+            table = batch.page_table
+            shared = not (table.is_cuda and ops._capturing(table.get_device(), stream))
         if shared and batch.cu_groups is not None and not set(kw) - {"out", "lse"}:
             every = -(-batch.page_table.shape[1] * self.books.page_size // self.block_size)
             if topk >= every and batch.max_new * q.shape[1] // k.shape[1] <= SHARED_ROWS:
