@@ -650,9 +650,10 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kStreamCtas)
 // merge
 // ----------------------------------------------------------------------------
 // A CTA takes up to `most` rows of a sequence's own span on a kv head, whose parts and whose
-// group's it looks up once.  Its threads are teams of 16, a row each; W of them to a row,
-// every W-th part each, where rows are few (they have many parts then).
-constexpr int kMergeThreads = 256, kTeam = 16, kTeams = kMergeThreads / kTeam, kMergeRows = 32;
+// group's it looks up once.  Its threads are teams of TEAM, a row each; W of them to a row,
+// every W-th part each, where rows are few (they have many parts then).  Teams of 16 for chunks,
+// of 32 for small spans: there the same rows have more warps, with half the columns a lane.
+constexpr int kMergeThreads = 256, kMergeRows = 32;
 
 template <int D, int TEAM>
 __global__ void __launch_bounds__(kMergeThreads, TEAM == 16 ? 3 : 4) merge_spans_kernel(SharedArgs x, int most) {
