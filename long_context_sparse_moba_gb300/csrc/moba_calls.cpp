@@ -3,7 +3,7 @@
 //
 // Bound: the host, where tokens are few: the GPU has 3 to 17 us of work then.  Measured, us from
 // call to call, against the same steps in Python: norms of 3 tokens 6 and 18, the gradient of 517
-// 12 and 32, appending one token 9 and 25, one of each of 64 sequences 10 (the GPU's time) and 26, four
+// 12 and 32, appending one token 9 and 25, one of each of 64 sequences 11 (the GPU's time) and 26, four
 // forks 15 (the GPU's) and 29.
 // Nothing is decided here: whatever is not the plain case (another device than the current
 // one, operands that a check stops at, arguments of another kind, a refusal by the entry point)

@@ -17,8 +17,8 @@
 // Bound: HBM for chunks, latency for a step.  A warp takes one token and a run of its
 // heads (q, then k, then v).  Measured (32 + 8 + 8 heads of 128, normalised): 16469 tokens in
 // four chunks 72 us, 5.6 TB/s (the pages' rows of 256 bytes are scattered writes), and 16 for
-// pooling 32 blocks of 512, 90 by the call; a step of 64 sequences of which one completes its
-// block 10.  (Units of a third of a token 102 by the call; tokens in consecutive runs a warp 112; CTAs
+// pooling 32 blocks of 512, 91 by the call; a step of 64 sequences of which one completes its
+// block 10.8.  (Units of a third of a token 102 by the call; tokens in consecutive runs a warp 112; CTAs
 // in waves 98; k and v first and q beside the pooling, in a launch of its own, 98.)
 #include <cmath>
 

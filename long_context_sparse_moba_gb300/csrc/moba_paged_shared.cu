@@ -19,10 +19,12 @@
 //      prefixes of groups that fit, or of all groups where they are short.
 //   4. Every part of 2 and 3 leaves partial sums, which the merge joins.
 // P is rounded to bf16 for the second product, as in the other attention kernels: relative
-// to 64 bits outputs err by 0.0020 to 0.0024, of which the result's own rounding is 0.0016.
+// to 64 bits outputs err by 0.0020 to 0.0024, of which the result's own rounding is 0.0016.  (In
+// two bf16 pieces it would need that product twice, which bounds the chunks; a weight errs by 2^-8
+// of itself at most, as does the result.)
 // Measured (heads of 128 unless said): 64 forks of 32768 tokens with up to 512 of their own,
 // 32 / 8 heads, 69 us (plan 3, big spans 37, small ones some 15 behind them, merge 12); 16 of 16384
-// with up to 2000, 32 / 32 heads, 99; 3 groups of 11 with up to 5 new tokens, 20 / 4 heads of 64, 37; 8
+// with up to 2000, 32 / 32 heads, 100; 3 groups of 11 with up to 5 new tokens, 20 / 4 heads of 64, 37; 8
 // questions of up to 200 tokens on 16384 181, 1160 TFLOP/s of what they cannot do without.
 #include "moba_mma.cuh"
 #include "moba_paged_attn.cuh"

@@ -320,11 +320,14 @@ class PagedCache:
         With ``norms``, (q_weight, k_weight) of ``ops.qk_norm_rope`` (either may be None: that
         operand is only rotated), q and k are normalised, rotated and appended in one
         pass, and q, k and v may be slices of one projection.  Where topk covers every
-        block, sequences that follow one another in the batch and share much of their
-        past (forks) are attended together (``ops.paged_attn_shared``; idx None), unless an
-        argument asks for what only ``ops.paged_attn`` gives, or ``shared`` is False.  A graph
-        that is being captured gets them together only with ``shared`` True: its replays read
-        cu_groups and prefix_lens too, which have to go with the page table that they read."""
+        block, sequences that follow one another in the batch and share their past (forks)
+        are attended together (``ops.paged_attn_shared``; idx None) if that saves
+        ``SHARED_BYTES`` of a layer's keys and values (``batch.cu_groups`` is None else) and a
+        sequence has ``SHARED_ROWS`` rows on a kv head at most, new tokens times query heads to
+        one, unless ``shared`` is False or a further argument but out and lse is given.  A graph
+        that is being captured gets them together only with ``shared`` True (which lifts no
+        other condition): its replays read cu_groups and prefix_lens too, which have to go with
+        the page table that they read."""
         pools = self.k_pages[layer], self.v_pages[layer], self.kbar_pages[layer]
         tables = batch.page_table, batch.cu_new, batch.cache_lens, batch.max_new
         if norms is not None:
