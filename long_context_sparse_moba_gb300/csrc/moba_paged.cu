@@ -268,8 +268,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a) {
 // before that kernel (tables, older keys) is ordered before this one by the token that it
 // releases, or by its end where that is not seen; nothing is constant data.
 // Bound: latency (a block's keys in four rounds of loads).  32 blocks of 512 on 8 kv heads of
-// 128 16 us; one of 64 sequences' 6 beside the kernel before it (10 where every thread waited
-// first and keys were only asked into L2 before; clusters of append_kernel's kind 11 and 19).
+// 128 16 us (19 by clusters of append_kernel's kind); a step of 64 sequences of which one completes
+// its block 10.8 by the call, 15.8 where nothing was read before the writing kernel's end but older
+// keys asked into L2.
 // T threads: 1024, a block's keys in one round, where there are no more candidates than
 // kPoolWide an SM, else 256 and three CTAs an SM.  (us by the call with 256 and 1024: 2048 new tokens
 // that complete a block of 2048 43 and 35, six chunks of up to 2000 with blocks of 512 50 and 45; four

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 320)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
     if (DENSE) after_previous();
-    let_next();
+    let_next();  // (SPANS: the small spans' kernel, which goes by the plan's token, not by this)
 
     if (warp == 11) {
         // ================= job descriptors =================

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) bwd_kernel(Args a) {
 // The CTAs' sums of a weight's gradient: a warp 32 columns of every 32nd CTA, joined
 // through shared memory by a warp for each column.  (fp32: 64-bit additions are slow
 // enough here to show.  A thread of bwd_kernel adds tokens * heads / (its side's CTAs * 8 warps * the
-// heads of a warp) terms in turn: 30 at 32764 tokens of 32 heads of 128, 900 at a million, where the sum
+// heads of a warp) terms in turn: some 30 at 32764 tokens of 32 heads of 128, 900 at a million, where the sum
 // errs by 2^-14 of its terms' magnitudes at worst.)
 constexpr int kSumWarps = 32;
 
