@@ -135,3 +135,56 @@ def test_pooling_behind_copies_of_the_tables(seqs):
         for a, b in ((one.k, two.k), (one.v, two.v), (one.kbar, two.kbar)):
             assert same(a, b)
     assert not one.kbar[one.table[:, 7].long()].isnan().any() and ops.get_status() == ops.MOBA_OK
+
+
+def test_two_caches_on_two_streams():
+    """More calls on each than there are words for their tokens, side by side."""
+    hkv, d, page, block, seqs, steps = 2, 64, 16, 64, 5, 1400
+    freqs = ops.rope_frequencies(d)
+    step = i32(list(range(seqs + 1)))
+    lens = [i32([n + 1] * seqs) for n in range(steps)]
+    x = normal(7, steps, seqs, 3 * hkv, d)
+
+    def one(c, n):
+        y = x[n]
+        ops.paged_append_rope(y[:, :hkv], y[:, hkv:2 * hkv], y[:, 2 * hkv:], c.k, c.v, c.kbar, c.table, step, lens[n], 1, block,
+                              freqs)
+
+    caches = [Cache(seqs, steps, hkv, d, page, block, seed=9) for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for n in range(steps):
+        for c, st in zip(caches, streams):
+            with torch.cuda.stream(st):
+                one(c, n)
+    torch.cuda.synchronize()
+    for n in range(steps):
+        one(caches[2], n)
+    for c in caches[:2]:
+        assert same(c.k, caches[2].k) and same(c.v, caches[2].v) and same(c.kbar, caches[2].kbar)
+    assert ops.get_status() == ops.MOBA_OK
+
+
+def test_two_graphs_on_one_workspace():
+    """Replayed in turn: each makes its own plan there."""
+    a = Forks([(8192, [(1, 1 + i) for i in range(40)]), (0, [(1, 50)])], 8, 64, 16, seed=4)
+    b = Forks([(256, [(1, 9)] * 3), (4096, [(2, 20 + i) for i in range(24)])], 8, 64, 16, seed=5)
+    need = max(ops.paged_attn_shared_workspace_size(len(f.nq), 2, sum(f.nq), max(f.nq), 32, 8, 64, 16, f.table.shape[1]) for f in (a, b))
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    calls = []
+    for f in (a, b):
+        n = sum(f.nq)
+        q, out, lse = normal(6, n, 32, 64), torch.empty(n, 32, 64, dtype=BF, device="cuda"), torch.empty(n, 32, device="cuda")
+        args = q, f.k, f.v, f.table, i32(f.cu), i32(f.lens), max(f.nq), i32(f.cu_groups), i32(f.prefixes)
+        want = ops.paged_attn_shared(*args)
+        compare(want, f.expect(q))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ops.paged_attn_shared(*args, out=out, lse=lse, workspace=ws)
+        calls.append((g, q, out, lse, want, args))
+    for i in range(20):
+        g, q, out, lse, want, _ = calls[i * 7 % 3 % 2]
+        out.fill_(7.0)
+        g.replay()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert ops.get_status() == ops.MOBA_OK
